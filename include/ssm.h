@@ -473,6 +473,89 @@ int ssm_ssd_bwd(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim, 
                 void *dB, void *dC, float *dD, void *dz, float *ddelta_bias, float *dh0,
                 int delta_softplus, void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * Linear attention with one decay per head: the recurrence of ssm_ssd_fwd with a step size of
+ * one and a decay that does not depend on the token, for any head sizes.  For every batch
+ * row b and head h, from the state S = h0 (or zeros), token by token:
+ *
+ *     S[i,j]      = exp(log_decay[h]) * S[i,j] + k[b,t,i] * v[b,t,j]
+ *     y[b,t,h,j]  = scale * sum_i q[b,t,i] * S[i,j]
+ *
+ * Sizes and layouts of a call: */
+typedef struct ssm_linattn_shape {
+    int64_t batch, seqlen, nheads;
+    int64_t q_heads, k_heads, v_heads;  /* rows of q, k, v per token: each divides nheads; head h reads row
+                                           h / (nheads / q_heads) of q, and so on */
+    int64_t dk, dv;                     /* columns of q and k, columns of v and y: 1 .. SSM_LINATTN_MAX_DIM */
+    int64_t q_row, k_row, v_row;        /* elements from one token's rows to the next token's (batch rows are
+                                           seqlen such steps apart), e.g. in a joint projection's output;
+                                           0: q_heads * dk, ... (contiguous) */
+    int32_t dtype;                      /* an ssm_dtype: q, k, v, y and their gradients */
+    int32_t reserved;                   /* must be 0 */
+} ssm_linattn_shape;
+
+#define SSM_LINATTN_MAX_DIM 256
+
+/* Host-only: bytes of device workspace of ssm_linattn_fwd (0: none needed, or the shape is
+ * invalid).  Few heads over a long sequence are split into segments that run side by side;
+ * their states pass through the workspace. */
+size_t ssm_linattn_workspace_bytes(const ssm_linattn_shape *shape);
+
+/*
+ *   q         [batch, seqlen, q_heads, dk]  dtype   required (seqlen > 0)
+ *   k         [batch, seqlen, k_heads, dk]  dtype   required
+ *   v         [batch, seqlen, v_heads, dv]  dtype   required
+ *   log_decay [nheads]                      fp32    required; usually <= 0 (-inf: no memory at all)
+ *   lengths   [batch]                       int32   NULL = seqlen for every row; else row b has lengths[b]
+ *             tokens (values are cut to 0 .. seqlen) with padding behind them: y is zero there, h_last is
+ *             the state after lengths[b] tokens, and what the padding holds (NaN, too) is not used
+ *   h0, h_last [batch, nheads, dk, dv]      fp32    NULL = zero start / not stored; must not overlap
+ *   y         [batch, seqlen, nheads, dv]   dtype   output, contiguous; must not overlap an input
+ *   workspace device memory of ssm_linattn_workspace_bytes() bytes (NULL if 0)
+ * batch or nheads == 0 is a no-op; seqlen == 0 stores h0 (or zeros) in h_last.  bf16 runs on the
+ * bf16 matrix cores with every fp32 factor split into two or three bf16 parts, fp32 on the fp32
+ * matrix cores.  A token's NaN or infinity reaches its own and later outputs only (where an
+ * infinity may turn into NaN).  Deterministic.
+ */
+int ssm_linattn_fwd(const ssm_linattn_shape *shape, const void *q, const void *k, const void *v,
+                    const float *log_decay, float scale, const int32_t *lengths, const float *h0,
+                    float *h_last, void *y, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Host-only: bytes of device workspace of ssm_linattn_bwd; with decay_grad != 0, for a call that is
+ * given dlog_decay. */
+size_t ssm_linattn_bwd_workspace_bytes(const ssm_linattn_shape *shape, int decay_grad);
+
+/*
+ * Backward pass of ssm_linattn_fwd: gradients of a loss given dy = dLoss/dy and (optionally)
+ * dh_last = dLoss/dh_last.  With a = log_decay[h] and the state's gradient G:
+ *     dq_t = scale S_t dy_t
+ *     G_t  = exp(a) G_{t+1} + scale q_t dy_t^T  (from dh_last),   dk_t = G_t v_t,   dv_t = G_t^T k_t
+ *     dh0  = exp(a) G_0,   da = sum_t <G_t, exp(a) S_{t-1}>
+ * Inputs as ssm_linattn_fwd, plus
+ *   dy        [batch, seqlen, nheads, dv]   dtype   required, contiguous (padding: not used)
+ *   dh_last   [batch, nheads, dk, dv]       fp32    NULL = zero
+ * Outputs (contiguous, fully overwritten, zero in the padding, none overlapping an input or another output):
+ *   dq, dk, dv  as q, k, v                  dtype   required; summed over the heads that share a row
+ *   dlog_decay [nheads]                     fp32    NULL = not computed (a fixed decay)
+ *   dh0       [batch, nheads, dk, dv]       fp32    NULL = not stored
+ *   workspace device memory of ssm_linattn_bwd_workspace_bytes(shape, dlog_decay != NULL) bytes
+ * nheads == 0 is a no-op; batch == 0 or seqlen == 0 sets dlog_decay to zero (and, with seqlen == 0, dh0 to
+ * dh_last or zeros).  Deterministic.
+ */
+int ssm_linattn_bwd(const ssm_linattn_shape *shape, const void *q, const void *k, const void *v,
+                    const float *log_decay, float scale, const int32_t *lengths, const float *h0,
+                    const void *dy, const float *dh_last, void *dq, void *dk, void *dv, float *dlog_decay,
+                    float *dh0, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One token (generation form): the state h [batch, nheads, dk, dv] fp32 is read and updated in
+ * place; q [batch, q_heads, dk], k, v likewise, y [batch, nheads, dv].  shape->seqlen must be 1; q_row, k_row and
+ * v_row are the elements from one batch row to the next.  L calls give the same y and state as one
+ * ssm_linattn_fwd over those L tokens, up to rounding.
+ */
+int ssm_linattn_update(const ssm_linattn_shape *shape, float *h, const void *q, const void *k, const void *v,
+                       const float *log_decay, float scale, void *y, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

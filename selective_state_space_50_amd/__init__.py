@@ -10,11 +10,13 @@ call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
 __all__ = ["scan_fwd", "scan_fwd_save", "scan_save_sizes", "scan_bwd", "state_update", "scan_plan", "scan_workspace_bytes",
-           "scan_bwd_workspace_bytes", "selective_scan", "conv1d_fwd", "conv1d_update", "lib",
+           "scan_bwd_workspace_bytes", "selective_scan", "conv1d_fwd", "conv1d_update", "linattn_fwd", "linattn_bwd",
+           "linattn_update", "linattn_workspace_bytes", "linattn_bwd_workspace_bytes", "linear_attention", "lib",
            "SSMError", "LIB_PATH",
            "HEADER_PATH", "exported_api"]
 
@@ -53,6 +55,12 @@ class ScanPlan(ctypes.Structure):
                 ("time_block", ctypes.c_int32), ("specialised", ctypes.c_int32),
                 ("workspace_bytes", ctypes.c_uint64), ("blocks", ctypes.c_uint64),
                 ("lds_reserve", ctypes.c_uint64)]
+
+
+class LinAttnShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("batch", "seqlen", "nheads", "q_heads", "k_heads", "v_heads", "dk", "dv",
+                                              "q_row", "k_row", "v_row")] + \
+               [("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -120,6 +128,17 @@ def lib():
     L.ssm_conv1d_bwd_workspace_bytes.argtypes = [I64, I64, I64, I64, I32]
     L.ssm_conv1d_bwd.restype = I32
     L.ssm_conv1d_bwd.argtypes = [I64, I64, I64, I64, I32] + [P] * 9 + [I32, P, SZ, P]
+    S = ctypes.POINTER(LinAttnShape)
+    L.ssm_linattn_workspace_bytes.restype = SZ
+    L.ssm_linattn_workspace_bytes.argtypes = [S]
+    L.ssm_linattn_fwd.restype = I32
+    L.ssm_linattn_fwd.argtypes = [S, P, P, P, P, ctypes.c_float, P, P, P, P, P, SZ, P]
+    L.ssm_linattn_bwd_workspace_bytes.restype = SZ
+    L.ssm_linattn_bwd_workspace_bytes.argtypes = [S, I32]
+    L.ssm_linattn_bwd.restype = I32
+    L.ssm_linattn_bwd.argtypes = [S, P, P, P, P, ctypes.c_float] + [P] * 10 + [SZ, P]
+    L.ssm_linattn_update.restype = I32
+    L.ssm_linattn_update.argtypes = [S, P, P, P, P, P, ctypes.c_float, P, P]
     if L.ssm_abi_version() != ABI_VERSION:
         raise ImportError(f"libssm ABI version {L.ssm_abi_version()} != {ABI_VERSION}")
     _lib = L
@@ -718,3 +737,197 @@ def ssd_bwd(x, delta, A, B, C, D=None, z=None, h0=None, dy=None, dh_last=None, *
                            _ptr(workspace) if ws_bytes else None, ws_bytes, ctypes.c_void_p(s.cuda_stream))
     _check(st, "ssm_ssd_bwd")
     return out
+
+
+def _rows(t, name, tokens, heads, d, dtype, device):
+    """Elements from one token of t [B, L, heads, d] (tokens = (B, L)) or [B, heads, d] (tokens = (B,)) to the
+    next: t may be a part of a wider row (a slice of a joint projection's output) as long as its heads stand side
+    by side and all tokens the same distance apart."""
+    if tuple(t.shape) != (*tokens, heads, d):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(*tokens, heads, d)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.numel() == 0 or t.is_contiguous():
+        return heads * d
+    st = t.stride()
+    sizes = [(n, s) for n, s in zip(tokens, st) if n > 1]
+    row = sizes[-1][1] if sizes else heads * d
+    even = len(sizes) < 2 or sizes[0][1] == row * sizes[1][0]
+    if (d > 1 and st[-1] != 1) or (heads > 1 and st[-2] != d) or not even or row < heads * d:
+        raise ValueError(f"{name} must have its heads contiguous and its tokens evenly spaced (strides {st})")
+    return row
+
+
+def _linattn_shape(q, k, v, log_decay, tokens, what):
+    """The checked ssm_linattn_shape of a call; tokens: 4 for [B, L, heads, d], 3 for [B, heads, d]."""
+    import torch
+    if q.dim() != tokens or k.dim() != tokens or v.dim() != tokens:
+        raise ValueError(f"q, k and v must be [batch, {'seqlen, ' if tokens == 4 else ''}heads, dim]")
+    if log_decay.dim() != 1:
+        raise ValueError("log_decay must be [nheads]")
+    dev, dt, H = q.device, q.dtype, log_decay.shape[0]
+    if dev.type != "cuda":
+        raise ValueError(f"{what} runs on the GPU only; tensors must be on a cuda device")
+    head = tuple(q.shape[:tokens - 2])
+    dk, dv = q.shape[-1], v.shape[-1]
+    rows = [_rows(t, n, head, t.shape[-2], d, dt, dev) for t, n, d in ((q, "q", dk), (k, "k", dk), (v, "v", dv))]
+    _need(log_decay, "log_decay", (H,), torch.float32, dev)
+    return LinAttnShape(head[0], head[1] if tokens == 4 else 1, H, q.shape[-2], k.shape[-2], v.shape[-2], dk, dv, *rows,
+                        _dtype_code(q), 0)
+
+
+def _workspace(given, need, device):
+    import torch
+    if need and (given is None or given.numel() * given.element_size() < need):
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    return given
+
+
+def _on(device, stream):
+    """Context in which a call's tensors are allocated and its kernels launched: the tensors'
+    device, and the stream given (what is allocated belongs to that stream)."""
+    import contextlib
+
+    import torch
+    stack = contextlib.ExitStack()
+    if torch.cuda.current_device() != device.index:
+        stack.enter_context(torch.cuda.device(device))
+    if stream is not None:
+        stack.enter_context(torch.cuda.stream(stream))
+    return stack
+
+
+def linattn_workspace_bytes(batch, seqlen, nheads, dk, dv, dtype="bf16") -> int:
+    """Device workspace bytes of linattn_fwd for this shape (0: none)."""
+    code = DTYPE_BF16 if dtype in ("bf16", "bfloat16") else DTYPE_F32
+    s = LinAttnShape(batch, seqlen, nheads, nheads, nheads, nheads, dk, dv, 0, 0, 0, code, 0)
+    return int(lib().ssm_linattn_workspace_bytes(ctypes.byref(s)))
+
+
+def linattn_bwd_workspace_bytes(batch, seqlen, nheads, dk, dv, dtype="bf16", q_heads=None, k_heads=None,
+                                v_heads=None, decay_grad=True) -> int:
+    """Device workspace bytes of linattn_bwd for this shape; the head counts default to nheads."""
+    code = DTYPE_BF16 if dtype in ("bf16", "bfloat16") else DTYPE_F32
+    s = LinAttnShape(batch, seqlen, nheads, q_heads or nheads, k_heads or nheads, v_heads or nheads, dk, dv, 0, 0, 0, code, 0)
+    return int(lib().ssm_linattn_bwd_workspace_bytes(ctypes.byref(s), int(bool(decay_grad))))
+
+
+def linattn_fwd(q, k, v, log_decay, h0=None, *, scale=None, lengths=None, return_last_state=False, out=None,
+                h_last=None, workspace=None, stream=None):
+    """Linear attention with one decay per head, over a sequence:
+    S_t = exp(log_decay) S_{t-1} + k_t v_t^T,  y_t = scale q_t^T S_t.
+
+    q, k: [B, L, heads, dk];  v: [B, L, heads, dv] (all bf16, or all fp32; dk, dv <= 256);
+    log_decay: [H] fp32, usually <= 0;  h0: [B, H, dk, dv] fp32.  The head counts of q, k and v
+    each divide H: consecutive heads share a row.  q, k, v may be slices of one wider tensor
+    (heads contiguous, tokens evenly spaced).  scale: default dk ** -0.5.  lengths: [B] int32,
+    the tokens of each row, with padding behind them (y is zero there, the last state is the one
+    after lengths[b] tokens).  Returns y [B, L, H, dv], or (y, h_last) when return_last_state.
+    """
+    import torch
+    s = _linattn_shape(q, k, v, log_decay, 4, "linattn_fwd")
+    dev, dt = q.device, q.dtype
+    state = (s.batch, s.nheads, s.dk, s.dv)
+    _need(h0, "h0", state, torch.float32, dev)
+    _need(lengths, "lengths", (s.batch,), torch.int32, dev)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((s.batch, s.seqlen, s.nheads, s.dv), dtype=dt, device=dev)
+        _need(out, "out", (s.batch, s.seqlen, s.nheads, s.dv), dt, dev)
+        if return_last_state and h_last is None:
+            h_last = torch.empty(state, dtype=torch.float32, device=dev)
+        _need(h_last, "h_last", state, torch.float32, dev)
+        need = int(lib().ssm_linattn_workspace_bytes(ctypes.byref(s)))
+        workspace = _workspace(workspace, need, dev)
+        st = lib().ssm_linattn_fwd(ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+                                   s.dk ** -0.5 if scale is None else float(scale), _ptr(lengths), _ptr(h0),
+                                   _ptr(h_last), _ptr(out), _ptr(workspace) if need else None, need,
+                                   ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream))
+    _check(st, "ssm_linattn_fwd")
+    return (out, h_last) if return_last_state else out
+
+
+def linattn_bwd(q, k, v, log_decay, h0=None, dy=None, dh_last=None, *, scale=None, lengths=None,
+                need_dlog_decay=True, need_dh0=True, workspace=None, stream=None):
+    """Gradients of a loss through linattn_fwd, given dy = dLoss/dy [B, L, H, dv] (q's dtype)
+    and optionally dh_last = dLoss/dh_last [B, H, dk, dv] fp32.  Other arguments as linattn_fwd.
+
+    Returns a dict: dq, dk, dv (contiguous, in the shapes and dtype of q, k, v; summed over the
+    heads that share a row, zero in the padding), dlog_decay [H] fp32 (None when not needed: a
+    fixed decay saves a third of the call) and dh0 [B, H, dk, dv] fp32 (None when not needed).
+    """
+    import torch
+    s = _linattn_shape(q, k, v, log_decay, 4, "linattn_bwd")
+    if dy is None:
+        raise ValueError("dy is required")
+    dev, dt = q.device, q.dtype
+    state = (s.batch, s.nheads, s.dk, s.dv)
+    for t, n, shape, d in ((h0, "h0", state, torch.float32), (lengths, "lengths", (s.batch,), torch.int32),
+                           (dy, "dy", (s.batch, s.seqlen, s.nheads, s.dv), dt), (dh_last, "dh_last", state, torch.float32)):
+        _need(t, n, shape, d, dev)
+    with _on(dev, stream):
+        new = lambda shape, d: torch.empty(shape, dtype=d, device=dev)  # noqa: E731
+        out = {"dq": new(q.shape, dt), "dk": new(k.shape, dt), "dv": new(v.shape, dt),
+               "dlog_decay": new((s.nheads,), torch.float32) if need_dlog_decay else None,
+               "dh0": new(state, torch.float32) if need_dh0 else None}
+        need = int(lib().ssm_linattn_bwd_workspace_bytes(ctypes.byref(s), int(bool(need_dlog_decay))))
+        workspace = _workspace(workspace, need, dev)
+        st = lib().ssm_linattn_bwd(ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+                                   s.dk ** -0.5 if scale is None else float(scale), _ptr(lengths), _ptr(h0), _ptr(dy),
+                                   _ptr(dh_last), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
+                                   _ptr(out["dlog_decay"]), _ptr(out["dh0"]), _ptr(workspace) if need else None, need,
+                                   ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream))
+    _check(st, "ssm_linattn_bwd")
+    return out
+
+
+def linattn_update(h, q, k, v, log_decay, *, scale=None, out=None, stream=None):
+    """One token of linattn_fwd: h [B, H, dk, dv] fp32 is updated in place; q, k [B, heads, dk],
+    v [B, heads, dv]; returns y [B, H, dv]."""
+    import torch
+    s = _linattn_shape(q, k, v, log_decay, 3, "linattn_update")
+    dev, dt = q.device, q.dtype
+    _need(h, "h", (s.batch, s.nheads, s.dk, s.dv), torch.float32, dev)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((s.batch, s.nheads, s.dv), dtype=dt, device=dev)
+        _need(out, "out", (s.batch, s.nheads, s.dv), dt, dev)
+        st = lib().ssm_linattn_update(ctypes.byref(s), _ptr(h), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+                                      s.dk ** -0.5 if scale is None else float(scale), _ptr(out),
+                                      ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream))
+    _check(st, "ssm_linattn_update")
+    return out
+
+
+@functools.lru_cache(maxsize=None)
+def _linattn_function():
+    import torch
+
+    class _LinAttn(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, v, log_decay, h0, scale, lengths, last):
+            y, h = linattn_fwd(q, k, v, log_decay, h0, scale=scale, lengths=lengths, return_last_state=True) if last \
+                else (linattn_fwd(q, k, v, log_decay, h0, scale=scale, lengths=lengths), None)
+            ctx.save_for_backward(q, k, v, log_decay, h0, lengths)
+            ctx.scale = scale
+            return (y, h) if last else y
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, gy, gh=None):
+            q, k, v, log_decay, h0, lengths = ctx.saved_tensors
+            need = ctx.needs_input_grad
+            g = linattn_bwd(q, k, v, log_decay, h0, gy.contiguous(), None if gh is None else gh.contiguous(),
+                            scale=ctx.scale, lengths=lengths, need_dlog_decay=need[3], need_dh0=h0 is not None and need[4])
+            return g["dq"], g["dk"], g["dv"], g["dlog_decay"], g["dh0"], None, None, None
+
+    return _LinAttn
+
+
+def linear_attention(q, k, v, log_decay, h0=None, *, scale=None, lengths=None, return_last_state=False):
+    """Differentiable linear attention with one decay per head: linattn_fwd with a torch autograd
+    backward through linattn_bwd (gradients for q, k, v, log_decay and h0).  Arguments as
+    linattn_fwd; with return_last_state both outputs can be differentiated."""
+    return _linattn_function().apply(q, k, v, log_decay, h0, scale, lengths, bool(return_last_state))

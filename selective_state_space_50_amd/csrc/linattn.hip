@@ -1,0 +1,722 @@
+// Linear attention with one decay per head: the sweep over a sequence (prompt, and every
+// gradient of the training pass) and the single-token update.
+//
+// Per batch row b and head h, with lambda = exp(log_decay[h]):
+//     S_t = lambda S_{t-1} + k_t v_t^T,        y_t = scale * q_t^T S_t
+// Over a chunk of m <= Q tokens that starts from the state H (i, j local to the chunk):
+//     y_i = s_in sum_{j<=i} lambda^(i-j) (q_i . k_j) v_j + s_rd lambda^(i+1-sh) q_i^T H
+//     H'  = lambda^m H + s_wr sum_j lambda^(m-1-j+sh) k_j v_j^T
+// with s_in = s_rd = scale, s_wr = 1 and sh = 0.  The decay does not depend on the token, so
+// every power of lambda a chunk needs comes from one table of Q + 1 values per workgroup.
+//
+// The gradients are the same sweep with other operands (dH = dLoss/dS after the last token):
+//     dq = sweep(dy, v, k) from h0^T                        forward in time
+//     dk = sweep(v, dy, q) from dH^T,  dv = sweep(k, q, dy) from dH    backward in time
+// where a backward sweep reads the state before it decays (sh = 1; its end is dh0), and
+// s_wr = scale, s_rd = 1, as dH is a gradient of the state itself.  The gradient of
+// log_decay is sum_i dy_i . dy_i/da: with R = dS/da, R_t = lambda (R_{t-1} + S_{t-1}), the
+// sweep of dq carries R beside S (AGE) and takes its product with q instead of y's with dy.
+#include "ssm_device.h"
+
+namespace ssm {
+namespace {
+
+typedef short s4 __attribute__((ext_vector_type(4)));
+typedef short s8 __attribute__((ext_vector_type(8)));
+typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+
+constexpr int kThreads = 512;   // 8 waves, two per SIMD
+constexpr int kN = 64;          // value columns of one workgroup
+constexpr int kYP = kN + 4;     // padded rows of the fp32 output shares
+
+// Operands of a 16x16 product over K = 32, lane l: row (A) or column (B) l % 16, and eight
+// k in two runs of four: 4 (l / 16) + e and 16 + 4 (l / 16) + e.  That is the order in
+// which two 16x16 results (lane: rows 4 (l / 16) + j, column l % 16) stand side by side, so a
+// result is the next product's operand without any exchange between lanes.
+template <class T>
+struct Op;
+
+template <>
+struct Op<uint16_t> {
+    using V4 = s4;
+    using Frag = s8;
+    static constexpr int kPad = 8;    // LDS row padding (elements): rows 16 bytes apart modulo the banks
+    static constexpr int kWide = 3;   // bf16 parts that carry an fp32 value whole
+    static constexpr int kNarrow = 2; // and to about 16 bits
+    static __device__ __forceinline__ Frag cat(V4 a, V4 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
+    static __device__ __forceinline__ f4 mma(Frag a, Frag b, f4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8, a), __builtin_bit_cast(b8, b), c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ V4 ld4(const uint16_t *p) { return *reinterpret_cast<const s4 *>(p); }
+    static __device__ __forceinline__ Frag ld8(const uint16_t *p) { return *reinterpret_cast<const s8 *>(p); }
+    // column c0 + lr of rows r0 + 4 lg .. + 3, by the LDS transpose read: the sixteen lanes of
+    // group lg address those four rows, four lanes of 8 bytes to a row
+    static __device__ __forceinline__ V4 column4(const uint16_t *base, int row, int r0, int c0, int lr, int lg) {
+        const uint16_t *p = base + (r0 + 4 * lg + (lr >> 2)) * row + c0 + 4 * (lr & 3);
+        return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) s4 *)(const_cast<uint16_t *>(p)));
+    }
+    static __device__ __forceinline__ f4 widen4(V4 v) {
+        const u2 r = __builtin_bit_cast(u2, v);
+        return f4{bf_lo(r.x), bf_hi(r.x), bf_lo(r.y), bf_hi(r.y)};
+    }
+    static __device__ __forceinline__ bool finite4(V4 v) {
+        const u2 r = __builtin_bit_cast(u2, v);
+        return (r.x & 0x7f80u) != 0x7f80u && (r.x & 0x7f800000u) != 0x7f800000u && (r.y & 0x7f80u) != 0x7f80u &&
+               (r.y & 0x7f800000u) != 0x7f800000u;
+    }
+    // v with zeros in place of infinities and NaN
+    static __device__ __forceinline__ V4 only_finite4(V4 v) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = (v[e] & 0x7f80) == 0x7f80 ? 0 : v[e];
+        return v;
+    }
+    // v as a sum of N bf16 values, each the rounding of what the ones before it leave
+    template <int N>
+    static __device__ __forceinline__ void split(f4 v, V4 (&part)[N]) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const u2 r = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+            part[n] = __builtin_bit_cast(s4, r);
+            if (n + 1 < N) v = f4{v[0] - bf_lo(r.x), v[1] - bf_hi(r.x), v[2] - bf_lo(r.y), v[3] - bf_hi(r.y)};
+        }
+    }
+};
+
+template <>
+struct Op<float> {
+    using V4 = f4;
+    struct Frag { f4 a, b; };
+    static constexpr int kPad = 4;
+    static constexpr int kWide = 1;
+    static constexpr int kNarrow = 1;
+    static __device__ __forceinline__ Frag cat(V4 a, V4 b) { return Frag{a, b}; }
+    // K = 32 as eight products over K = 4 (v_mfma_f32_16x16x4_f32): product e takes element e of
+    // every lane, the same k in both operands
+    static __device__ __forceinline__ f4 mma(const Frag &a, const Frag &b, f4 c) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.a[e], b.a[e], c, 0, 0, 0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.b[e], b.b[e], c, 0, 0, 0);
+        return c;
+    }
+    static __device__ __forceinline__ V4 ld4(const float *p) { return *reinterpret_cast<const f4 *>(p); }
+    static __device__ __forceinline__ Frag ld8(const float *p) { return Frag{ld4(p), ld4(p + 4)}; }
+    static __device__ __forceinline__ V4 column4(const float *base, int row, int r0, int c0, int lr, int lg) {
+        const float *p = base + (r0 + 4 * lg) * row + c0 + lr;
+        return f4{p[0], p[row], p[2 * row], p[3 * row]};
+    }
+    static __device__ __forceinline__ f4 widen4(V4 v) { return v; }
+    static __device__ __forceinline__ bool finite1(float v) { return (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u; }
+    static __device__ __forceinline__ bool finite4(V4 v) { return finite1(v[0]) && finite1(v[1]) && finite1(v[2]) && finite1(v[3]); }
+    static __device__ __forceinline__ V4 only_finite4(V4 v) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = finite1(v[e]) ? v[e] : 0.0f;
+        return v;
+    }
+    template <int N>
+    static __device__ __forceinline__ void split(f4 v, V4 (&part)[N]) { part[0] = v; }
+};
+
+// lambda^n = hi + lo to more than 32 bits: near 1 the rounding of lambda^n alone would be
+// the same at every chunk and add up over a long memory
+struct Decay { float hi, lo; };
+__device__ __forceinline__ Decay decay_of(float a, float n) {
+    const float x = a * n;
+    if (n == 0.0f) return Decay{1.0f, 0.0f};
+    if (x > -0.5f && x < 0.5f) return Decay{1.0f, expm1f(x)};
+    return Decay{expf(x), 0.0f};
+}
+
+template <class T, int DK>
+struct Tile {
+    // fp32 at 256 contraction columns: 32 rows to a chunk, so that q and k fit
+    static constexpr int kQ = (sizeof(T) == 4 && DK == 256) ? 32 : 64;
+    static constexpr int kBufs = (sizeof(T) == 2 && DK <= 128) ? 2 : 1;
+    static constexpr int kRow = DK + Op<T>::kPad, kVRow = kN + Op<T>::kPad;
+    static constexpr int kBlocks = kQ / 16;
+    static constexpr int kTiles = kBlocks * (kBlocks + 1) / 2;   // 16x16 tiles on and below the diagonal
+};
+
+template <class T, int DK, bool AGE>
+struct __align__(16) Smem {
+    using G = Tile<T, DK>;
+    using V4 = typename Op<T>::V4;
+    T q[G::kBufs][G::kQ][G::kRow];
+    T k[G::kBufs][G::kQ][G::kRow];
+    T v[G::kBufs][G::kQ][G::kVRow];
+    V4 p[Op<T>::kNarrow][G::kTiles][64];                        // decayed (q k^T)^T, operand-ready
+    V4 pa[AGE ? Op<T>::kWide : 1][AGE ? G::kTiles : 1][64];     // the same times i - j (AGE)
+    float y[2][G::kQ][kYP];                                     // output shares of the two state halves
+    float pw[2 * G::kQ + 4];                                    // lambda^(n - Q), 0 below n = Q
+};
+
+__host__ __device__ constexpr int tile_of(int k, int i) { return i * (i + 1) / 2 + k; }
+
+// One workgroup: the value columns [64 nt, 64 nt + 64) of one (b, h), one segment of the
+// sequence.  Wave w owns value columns 16 (w % 4) .. + 15 and half w / 4 of the contraction
+// columns: its part of the state stays in registers from chunk to chunk.  Per chunk: the
+// tiles of q k^T (shared out over the waves) and each wave's share of the carried state's
+// readout, a barrier, the in-chunk product (output blocks shared out between the halves),
+// the state update and the next chunk's rows into LDS, a barrier, and the sum of the halves'
+// shares to memory.  The rows after those are loaded into registers meanwhile.
+//
+// STATE: only the segment's own contribution to the state (from zero), into the workspace.
+template <class T, int DK, bool AGE, bool STATE>
+__global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
+    using G = Tile<T, DK>;
+    using O = Op<T>;
+    using V4 = typename O::V4;
+    using Frag = typename O::Frag;
+    constexpr int Q = G::kQ, KH = DK / 2, NT = KH / 16, NB = G::kBlocks, NJ = Q / 32;
+    constexpr int NS = AGE ? O::kWide : O::kNarrow;   // parts of the state in its readout
+    constexpr int VE = 16 / sizeof(T);
+    constexpr int NQ = Q * DK / VE / kThreads, NV = Q * kN / VE / kThreads;
+    static_assert(NQ >= 1 && NV >= 1, "a thread loads whole 16-byte pieces");
+    __shared__ Smem<T, DK, AGE> sm;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int nb = w & 3, hf = w >> 2, lr = lane & 15, lg = lane >> 4;
+
+    // workgroup -> (b, h, segment, column tile): the hardware deals workgroups to the 8 XCDs
+    // in turn; the column tiles of one segment read the same q and k and go to one XCD
+    const int64_t per = (a.work + 7) / 8;
+    int64_t id = static_cast<int64_t>(blockIdx.x) % 8 * per + blockIdx.x / 8;
+    if (id >= a.work) return;
+    const int nt = static_cast<int>(id % a.ntiles);
+    id /= a.ntiles;
+    const int64_t segs = STATE ? a.nseg - 1 : a.nseg;
+    const int64_t seg = id % segs;
+    id /= segs;
+    const int64_t h = id % a.H, b = id / a.H;
+    const int n0 = nt * kN;
+
+    int64_t Lb = a.L;
+    if (a.lengths) Lb = min(max(static_cast<int64_t>(a.lengths[b]), int64_t(0)), a.L);
+    const int64_t first = seg * a.seg_len, end = min(first + a.seg_len, Lb);
+    if (STATE && first + a.seg_len >= Lb) return;   // no later segment starts from this one's state
+    const int sh = a.reverse ? 1 : 0;
+    const float la = a.log_decay[h];
+
+    // rows are counted in the sweep's direction: row t is token t, or token Lb - 1 - t
+    const int64_t origin = a.reverse ? Lb - 1 : 0;
+    const int64_t dir = a.reverse ? -1 : 1;
+    const T *qg = static_cast<const T *>(a.q) + (b * a.L + origin) * a.q_row + (h / (a.H / a.q_heads)) * a.dk;
+    const T *kg = static_cast<const T *>(a.k) + (b * a.L + origin) * a.k_row + (h / (a.H / a.k_heads)) * a.dk;
+    const T *vg = static_cast<const T *>(a.v) + (b * a.L + origin) * a.v_row + (h / (a.H / a.v_heads)) * a.dn + n0;
+    const int ncols = min(static_cast<int>(a.dn) - n0, kN);
+
+    // rows past the sequence's end: zeros (a padded batch)
+    if (!STATE && Lb < a.L) {
+        const int64_t from = max(first, Lb), to = min(first + a.seg_len, a.L);
+        for (int64_t e = tid; e < (to - from) * ncols; e += kThreads) {
+            const int64_t at = ((b * a.L + from + e / ncols) * a.H + h) * a.dn + n0 + e % ncols;
+            if (a.out_f32) static_cast<float *>(a.y)[at] = 0.0f;
+            else put(static_cast<T *>(a.y), at, 0.0f);
+        }
+    }
+    if (!STATE && first >= Lb && !(Lb == 0 && seg == 0)) {
+        if (AGE && tid == 0) a.age_part[((b * a.H + h) * a.nseg + seg) * a.ntiles + nt] = 0.0f;
+        return;
+    }
+
+    for (int n = tid; n < 2 * Q + 4; n += kThreads) {
+        const Decay d = decay_of(la, static_cast<float>(n - Q));
+        sm.pw[n] = n < Q ? 0.0f : d.hi + d.lo;
+    }
+    const float *pw = sm.pw + Q;
+
+    // ---- the wave's part of the state: contraction row 16 t + 4 lg + j of its half, column lr
+    f4 S[NT], R[AGE ? NT : 1];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int kk = hf * KH + 16 * t + 4 * lg + j, n = n0 + 16 * nb + lr;
+            const bool in = kk < a.dk && n < a.dn;
+            float s0 = 0.0f, r0 = 0.0f;
+            if (!STATE && in) {
+                if (seg > 0) {
+                    const int64_t at = (((b * a.H + h) * (a.nseg - 1) + seg - 1) * a.dk + kk) * a.dn + n;
+                    s0 = a.ws_S[at];
+                    if constexpr (AGE) r0 = a.ws_R[at];
+                } else if (a.h0) {
+                    s0 = a.h0[(b * a.H + h) * a.dk * a.dn + kk * a.h_sr + n * a.h_sc];
+                }
+            }
+            S[t][j] = s0;
+            if constexpr (AGE) R[t][j] = r0;
+        }
+    }
+
+    // ---- rows to registers (16 bytes each; zeros outside the operand), registers to LDS
+    uint4 rq[STATE ? 1 : NQ], rk[NQ], rv[NV];
+    auto piece = [&](const T *g, int64_t stride, int64_t t, int col, int cols, bool vec) __attribute__((always_inline)) {
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (t >= end) return u;
+        const T *p = g + dir * t * stride + col;
+        if (vec) {
+            if (col < cols) u = *reinterpret_cast<const uint4 *>(p);
+        } else {
+            struct { T e[VE]; } x;
+#pragma unroll
+            for (int i = 0; i < VE; ++i) x.e[i] = col + i < cols ? p[i] : T(0);
+            u = __builtin_bit_cast(uint4, x);
+        }
+        return u;
+    };
+    auto load = [&](int64_t t0) __attribute__((always_inline)) {
+#pragma unroll
+        for (int r = 0; r < NQ; ++r) {
+            const int s = tid + r * kThreads, row = s / (DK / VE), col = s % (DK / VE) * VE;
+            if constexpr (!STATE) rq[r] = piece(qg, a.q_row, t0 + row, col, static_cast<int>(a.dk), a.q_vec);
+            rk[r] = piece(kg, a.k_row, t0 + row, col, static_cast<int>(a.dk), a.k_vec);
+        }
+#pragma unroll
+        for (int r = 0; r < NV; ++r) {
+            const int s = tid + r * kThreads, row = s / (kN / VE), col = s % (kN / VE) * VE;
+            rv[r] = piece(vg, a.v_row, t0 + row, col, ncols, a.v_vec);
+        }
+    };
+    auto stage = [&](int buf) __attribute__((always_inline)) {
+#pragma unroll
+        for (int r = 0; r < NQ; ++r) {
+            const int s = tid + r * kThreads, row = s / (DK / VE), col = s % (DK / VE) * VE;
+            if constexpr (!STATE) *reinterpret_cast<uint4 *>(&sm.q[buf][row][col]) = rq[r];
+            *reinterpret_cast<uint4 *>(&sm.k[buf][row][col]) = rk[r];
+        }
+#pragma unroll
+        for (int r = 0; r < NV; ++r) {
+            const int s = tid + r * kThreads, row = s / (kN / VE), col = s % (kN / VE) * VE;
+            *reinterpret_cast<uint4 *>(&sm.v[buf][row][col]) = rv[r];
+        }
+    };
+
+    const Decay full = decay_of(la, static_cast<float>(Q));
+    const float s_in = a.s_in, s_rd = a.s_rd, s_wr = a.s_wr;
+    float age = 0.0f;
+    int buf = 0;
+    load(first);
+    stage(0);
+    load(first + Q);
+    __syncthreads();
+    for (int64_t t0 = first; t0 < end; t0 += Q) {
+        const int m = static_cast<int>(min(static_cast<int64_t>(Q), end - t0));
+        f4 acc[STATE ? 1 : NB], acca[AGE ? NB : 1];
+        if constexpr (!STATE) {
+            // ---- tiles of (q k^T)^T with their decay: lane s = 16 k + 4 lg + j, t = 16 i + lr
+            for (int idx = w; idx < G::kTiles; idx += 8) {
+                const int i = idx < 1 ? 0 : idx < 3 ? 1 : idx < 6 ? 2 : 3, k = idx - i * (i + 1) / 2;
+                f4 g = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int c = 0; c < DK / 32; ++c)
+                    g = O::mma(O::ld8(&sm.k[buf][16 * k + lr][32 * c + 8 * lg]), O::ld8(&sm.q[buf][16 * i + lr][32 * c + 8 * lg]), g);
+                f4 x;
+                const int d0 = 16 * (i - k) + lr - 4 * lg;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = d0 - j >= 0 ? g[j] * (s_in * pw[d0 - j]) : 0.0f;
+                V4 part[O::kNarrow];
+                O::template split<O::kNarrow>(x, part);
+#pragma unroll
+                for (int n = 0; n < O::kNarrow; ++n) sm.p[n][idx][lane] = part[n];
+                if constexpr (AGE) {
+                    f4 xa;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) xa[j] = d0 - j > 0 ? x[j] * static_cast<float>(d0 - j) : 0.0f;
+                    V4 wide[O::kWide];
+                    O::template split<O::kWide>(xa, wide);
+#pragma unroll
+                    for (int n = 0; n < O::kWide; ++n) sm.pa[n][idx][lane] = wide[n];
+                }
+            }
+            // ---- this half's share of the carried state's readout, y^T: lane n = 4 lg + j, t = lr
+            V4 sp[NT][NS], rp[AGE ? NT : 1][NS];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                O::template split<NS>(S[t], sp[t]);
+                if constexpr (AGE) O::template split<NS>(R[t], rp[t]);
+            }
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                f4 off = {0.0f, 0.0f, 0.0f, 0.0f}, offa = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int c = 0; c < NT / 2; ++c) {
+                    const T *qr = &sm.q[buf][16 * i + lr][hf * KH + 32 * c + 4 * lg];
+                    const Frag qf = O::cat(O::ld4(qr), O::ld4(qr + 16));
+#pragma unroll
+                    for (int n = 0; n < NS; ++n) {
+                        off = O::mma(O::cat(sp[2 * c][n], sp[2 * c + 1][n]), qf, off);
+                        if constexpr (AGE) offa = O::mma(O::cat(rp[2 * c][n], rp[2 * c + 1][n]), qf, offa);
+                    }
+                }
+                const int t = 16 * i + lr;
+                const float e = s_rd * pw[t + 1 - sh];
+                acc[i] = off * e;
+                if constexpr (AGE) acca[i] = offa * e + off * (e * static_cast<float>(t + 1));
+            }
+            __syncthreads();   // tiles built
+        }
+
+        // ---- the value rows as an operand: column 16 nb + lr, rows in the operand order
+        V4 vp[2 * NJ];
+#pragma unroll
+        for (int j = 0; j < 2 * NJ; ++j) vp[j] = O::column4(&sm.v[buf][0][0], G::kVRow, 16 * j, 16 * nb, lr, lg);
+        if constexpr (!STATE) {
+            // ---- in-chunk product; half 0 takes output blocks 0 and 3, half 1 blocks 1 and 2
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const bool mine = NB == 2 ? i == hf : hf == 0 ? (i == 0 || i == 3) : (i == 1 || i == 2);
+                if (mine) {
+                    // the diagonal tile's zeros (rows after the output's) must not meet an infinity
+                    // or NaN: such values are taken out of the product and added to their own and
+                    // later rows only
+                    const bool odd = __ballot(!O::finite4(vp[i])) != 0;
+                    const V4 vd = odd ? O::only_finite4(vp[i]) : vp[i];
+#pragma unroll
+                    for (int k = 0; k <= i; k += 2) {
+                        const bool two = k + 1 <= i;
+                        const V4 zero = {};
+                        const Frag vf = O::cat(k == i ? vd : vp[k], two ? (k + 1 == i ? vd : vp[k + 1]) : zero);
+#pragma unroll
+                        for (int n = 0; n < O::kNarrow; ++n)
+                            acc[i] = O::mma(vf, O::cat(sm.p[n][tile_of(k, i)][lane], two ? sm.p[n][tile_of(k + 1, i)][lane] : zero), acc[i]);
+                        if constexpr (AGE) {
+#pragma unroll
+                            for (int n = 0; n < O::kWide; ++n)
+                                acca[i] = O::mma(vf, O::cat(sm.pa[n][tile_of(k, i)][lane], two ? sm.pa[n][tile_of(k + 1, i)][lane] : zero), acca[i]);
+                        }
+                    }
+                    if (odd) {
+                        for (int r = 0; r <= lr; ++r) {
+                            const int from = (r >> 2) * 16 + lr;   // the lane that holds row r, column lr of the tile
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const float x = widen_v(sm.v[buf][16 * i + r][16 * nb + 4 * lg + j]);
+                                if ((__float_as_uint(x) & 0x7f800000u) != 0x7f800000u) continue;
+                                float p = 0.0f;
+                                for (int n = 0; n < O::kNarrow; ++n) p += O::widen4(sm.p[n][tile_of(i, i)][from])[r & 3];
+                                acc[i][j] = __builtin_fmaf(p, x, acc[i][j]);
+                                if constexpr (AGE) acca[i][j] = __builtin_fmaf(p * static_cast<float>(lr - r), x, acca[i][j]);
+                            }
+                        }
+                    }
+                }
+                *reinterpret_cast<f4 *>(&sm.y[hf][16 * i + lr][16 * nb + 4 * lg]) = acc[i];
+                if constexpr (AGE) {
+                    const int t = 16 * i + lr;
+                    if (t < m) {
+                        const T *wr = static_cast<const T *>(a.age_w) + (b * a.L + t0 + t) * a.age_row + (h / (a.H / a.age_heads)) * a.dn + n0;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int n = 16 * nb + 4 * lg + j;
+                            if (n < ncols) age = __builtin_fmaf(acca[i][j], widen_v(wr[n]), age);
+                        }
+                    }
+                }
+            }
+        }
+
+        // ---- state update with the weighted value rows
+        {
+            const Decay d = m == Q ? full : decay_of(la, static_cast<float>(m));
+            V4 wp[2 * NJ][O::kWide], ap[AGE ? 2 * NJ : 1][O::kWide];
+#pragma unroll
+            for (int j = 0; j < 2 * NJ; ++j) {
+                const f4 x = O::widen4(vp[j]);
+                f4 xw, xa;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int left = m - 1 - (16 * j + 4 * lg + e);   // rows of the chunk after this one
+                    xw[e] = x[e] * (s_wr * pw[left + sh]);
+                    xa[e] = xw[e] * static_cast<float>(left);
+                }
+                O::template split<O::kWide>(xw, wp[j]);
+                if constexpr (AGE) O::template split<O::kWide>(xa, ap[j]);
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                f4 s = S[t];
+                if constexpr (AGE) {
+                    f4 r = R[t] + s * static_cast<float>(m);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) r[j] = __builtin_fmaf(r[j], d.lo, r[j] * d.hi);
+                    R[t] = r;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[j] = __builtin_fmaf(s[j], d.lo, s[j] * d.hi);
+#pragma unroll
+                for (int c = 0; c < NJ; ++c) {
+                    const Frag kf = O::cat(O::column4(&sm.k[buf][0][0], G::kRow, 32 * c, hf * KH + 16 * t, lr, lg),
+                                           O::column4(&sm.k[buf][0][0], G::kRow, 32 * c + 16, hf * KH + 16 * t, lr, lg));
+#pragma unroll
+                    for (int n = 0; n < O::kWide; ++n) {
+                        s = O::mma(kf, O::cat(wp[2 * c][n], wp[2 * c + 1][n]), s);
+                        if constexpr (AGE) R[t] = O::mma(kf, O::cat(ap[2 * c][n], ap[2 * c + 1][n]), R[t]);
+                    }
+                }
+                S[t] = s;
+            }
+        }
+        // ---- the next chunk's rows into LDS, the ones after it into registers
+        if constexpr (G::kBufs == 1) __syncthreads();   // this chunk's rows read
+        const int nbuf = G::kBufs == 1 ? 0 : buf ^ 1;
+        if (t0 + Q < end) {
+            stage(nbuf);
+            load(t0 + 2 * Q);
+        }
+        __syncthreads();   // output shares written, the next chunk staged
+        if constexpr (!STATE) {
+            // ---- the halves' shares added, eight columns of one row per thread
+            const int row = tid >> 3, col = (tid & 7) * 8;
+            if (row < m) {
+                float o[8];
+                const f4 *p0 = reinterpret_cast<const f4 *>(&sm.y[0][row][col]), *p1 = reinterpret_cast<const f4 *>(&sm.y[1][row][col]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[4 * e + j] = p0[e][j] + p1[e][j];
+                const int64_t at = ((b * a.L + origin + dir * (t0 + row)) * a.H + h) * a.dn + n0 + col;
+                if (a.out_f32 || sizeof(T) == 4) {
+                    float *y = static_cast<float *>(a.y) + at;
+                    if (a.y_vec && col + 8 <= ncols) {
+                        *reinterpret_cast<f4 *>(y) = f4{o[0], o[1], o[2], o[3]};
+                        *reinterpret_cast<f4 *>(y + 4) = f4{o[4], o[5], o[6], o[7]};
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (col + j < ncols) y[j] = o[j];
+                    }
+                } else {
+                    uint16_t *y = static_cast<uint16_t *>(a.y) + at;
+                    if (a.y_vec && col + 8 <= ncols) {
+                        *reinterpret_cast<uint4 *>(y) = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]),
+                                                                   pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (col + j < ncols) y[j] = to_bf16(o[j]);
+                    }
+                }
+            }
+        }
+        buf = nbuf;
+    }
+
+    // ---- the state passed on
+    const bool last = !STATE && end == Lb;
+    float *out = STATE ? a.ws_S + ((b * a.H + h) * (a.nseg - 1) + seg) * a.dk * a.dn
+                       : last && a.h_last ? a.h_last + (b * a.H + h) * a.dk * a.dn : nullptr;
+    const int64_t sr = STATE ? a.dn : a.h_sr, sc = STATE ? 1 : a.h_sc;
+    float *outR = STATE && AGE ? a.ws_R + ((b * a.H + h) * (a.nseg - 1) + seg) * a.dk * a.dn : nullptr;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int kk = hf * KH + 16 * t + 4 * lg + j, n = n0 + 16 * nb + lr;
+            if (kk < a.dk && n < a.dn) {
+                if (out) out[kk * sr + n * sc] = S[t][j];
+                if constexpr (AGE) {
+                    if (outR) outR[kk * sr + n * sc] = R[t][j];
+                    // the last state's own gradient sees its age too
+                    if (last && a.age_dh) age = __builtin_fmaf(R[t][j], a.age_dh[(b * a.H + h) * a.dk * a.dn + kk * a.h_sr + n * a.h_sc], age);
+                }
+            }
+        }
+    if constexpr (AGE && !STATE) {
+        // the workgroup's share of dlog_decay, summed in a fixed order
+        __syncthreads();
+        float *red = &sm.y[0][0][0];
+        red[tid] = age;
+        __syncthreads();
+        for (int o = kThreads / 2; o > 0; o >>= 1) {
+            if (tid < o) red[tid] += red[tid + o];
+            __syncthreads();
+        }
+        if (tid == 0) a.age_part[((b * a.H + h) * a.nseg + seg) * a.ntiles + nt] = red[0];
+    }
+}
+
+// Own contributions of the segments -> the states that segments 1, 2, ... start from, one
+// thread per state element: H_{s+1} = lambda^T H_s + own_s (T rows to a segment), and with R
+// its derivative by log_decay.
+__global__ void __launch_bounds__(256) linattn_combine_kernel(LinAttnArgs a) {
+    const int64_t gid = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t sz = a.dk * a.dn;
+    if (gid >= a.B * a.H * sz) return;
+    const int64_t bh = gid / sz, e = gid % sz, kk = e / a.dn, n = e % a.dn;
+    int64_t Lb = a.L;
+    if (a.lengths) Lb = min(max(static_cast<int64_t>(a.lengths[bh / a.H]), int64_t(0)), a.L);
+    const double x = static_cast<double>(a.log_decay[bh % a.H]) * static_cast<double>(a.seg_len);
+    const float d = static_cast<float>(exp(x)), T = static_cast<float>(a.seg_len);
+    float S = a.h0 ? a.h0[bh * sz + kk * a.h_sr + n * a.h_sc] : 0.0f, R = 0.0f;
+    for (int64_t s = 0; s + 1 < a.nseg && (s + 1) * a.seg_len < Lb; ++s) {
+        const int64_t at = (bh * (a.nseg - 1) + s) * sz + e;
+        if (a.ws_R) {
+            R = __builtin_fmaf(d, __builtin_fmaf(T, S, R), a.ws_R[at]);
+            a.ws_R[at] = R;
+        }
+        S = __builtin_fmaf(d, S, a.ws_S[at]);
+        a.ws_S[at] = S;
+    }
+}
+
+// dlog_decay[h] = sum of the workgroups' shares over (b, segment, tile), in a fixed order
+__global__ void __launch_bounds__(64) linattn_age_sum_kernel(const float *part, float *out, int64_t B, int64_t H, int64_t per) {
+    const int64_t h = blockIdx.x;
+    double s = 0.0;
+    for (int64_t i = threadIdx.x; i < B * per; i += 64) s += part[((i / per) * H + h) * per + i % per];
+    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, 64);
+    if (threadIdx.x == 0) out[h] = static_cast<float>(s);
+}
+
+// per-head gradients [rows][H][D] fp32 -> [rows][G][D], summed over the heads of a group in order
+template <class T>
+__global__ void __launch_bounds__(256) linattn_share_kernel(const float *part, T *out, int64_t n, int64_t G, int64_t D, int64_t per) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= n) return;
+    const int64_t d = i % D, g = i / D % G, row = i / (D * G);
+    const float *p = part + (row * G + g) * per * D + d;
+    float s = 0.0f;
+    for (int64_t j = 0; j < per; ++j) s += p[j * D];
+    put(out, i, s);
+}
+
+// One token: every state element is read and written once, so the launch is bound by the
+// state's traffic.  A workgroup takes CW value columns of one (b, h); thread: four columns
+// (16 bytes) of every (1024 / CW)-th contraction row.
+template <class T, int CW>
+__global__ void __launch_bounds__(256) linattn_update_kernel(LinAttnArgs a) {
+    constexpr int C4 = CW / 4, RG = 256 / C4;
+    __shared__ float red[4][CW];
+    __shared__ float qs[256], ks[256];
+    const int tid = threadIdx.x, c4 = tid % C4, rg = tid / C4;
+    const int64_t tiles = (a.dn + CW - 1) / CW;
+    const int64_t bh = blockIdx.x / tiles, h = bh % a.H, b = bh / a.H;
+    const int n = static_cast<int>(blockIdx.x % tiles) * CW + 4 * c4, dk = static_cast<int>(a.dk), dn = static_cast<int>(a.dn);
+    const T *q = static_cast<const T *>(a.q) + b * a.q_row + (h / (a.H / a.q_heads)) * dk;
+    const T *k = static_cast<const T *>(a.k) + b * a.k_row + (h / (a.H / a.k_heads)) * dk;
+    const T *v = static_cast<const T *>(a.v) + b * a.v_row + (h / (a.H / a.v_heads)) * dn;
+    for (int i = tid; i < dk; i += 256) {
+        qs[i] = a.s_rd * widen(q, i);
+        ks[i] = widen(k, i);
+    }
+    f4 vv;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) vv[j] = n + j < dn ? widen(v, n + j) : 0.0f;
+    const Decay d = decay_of(a.log_decay[h], 1.0f);
+    float *S = a.h_last + bh * dk * dn;
+    f4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+    __syncthreads();
+    if (a.y_vec && n < dn) {
+#pragma unroll 8
+        for (int kk = rg; kk < dk; kk += RG) {
+            f4 *p = reinterpret_cast<f4 *>(S + static_cast<int64_t>(kk) * dn + n);
+            f4 s = *p;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[j] = __builtin_fmaf(s[j], d.hi, __builtin_fmaf(s[j], d.lo, ks[kk] * vv[j]));
+                y[j] = __builtin_fmaf(qs[kk], s[j], y[j]);
+            }
+            *p = s;
+        }
+    } else {
+        for (int kk = rg; kk < dk; kk += RG)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (n + j < dn) {
+                    float *p = S + static_cast<int64_t>(kk) * dn + n + j;
+                    const float s = __builtin_fmaf(*p, d.hi, __builtin_fmaf(*p, d.lo, ks[kk] * vv[j]));
+                    y[j] = __builtin_fmaf(qs[kk], s, y[j]);
+                    *p = s;
+                }
+    }
+    // rows of the wave, then of the four waves, in a fixed order
+#pragma unroll
+    for (int o = C4; o < 64; o <<= 1)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] += __shfl_xor(y[j], o, 64);
+    if ((tid & 63) < C4)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) red[tid >> 6][4 * c4 + j] = y[j];
+    __syncthreads();
+    const int nn = static_cast<int>(blockIdx.x % tiles) * CW + tid;
+    if (tid < CW && nn < dn) put(static_cast<T *>(a.y), bh * dn + nn, red[0][tid] + red[1][tid] + red[2][tid] + red[3][tid]);
+}
+
+template <class T, int DK, bool AGE, bool STATE>
+hipError_t launch_one(const LinAttnArgs &a0, hipStream_t s) {
+    LinAttnArgs a = a0;
+    a.work = a.B * a.H * (STATE ? a.nseg - 1 : a.nseg) * a.ntiles;
+    static_assert(sizeof(Smem<T, DK, AGE>) <= kLdsPerCU, "LDS of one CU");
+    hipLaunchKernelGGL((linattn_kernel<T, DK, AGE, STATE>), dim3(static_cast<unsigned>((a.work + 7) / 8 * 8)), dim3(kThreads), 0, s, a);
+    return launch_status(s);
+}
+
+template <class T, int DK, bool AGE>
+hipError_t launch_sweep(const LinAttnArgs &a, hipStream_t s) {
+    if (a.nseg > 1) {
+        hipError_t e = launch_one<T, DK, AGE, true>(a, s);
+        if (e != hipSuccess) return e;
+        const int64_t n = a.B * a.H * a.dk * a.dn;
+        hipLaunchKernelGGL(linattn_combine_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, s, a);
+        e = launch_status(s);
+        if (e != hipSuccess) return e;
+    }
+    return launch_one<T, DK, AGE, false>(a, s);
+}
+
+template <class T>
+hipError_t launch_typed(const LinAttnArgs &a, hipStream_t s) {
+    const bool age = a.age_part != nullptr;
+    if (a.dk <= 64) return age ? launch_sweep<T, 64, true>(a, s) : launch_sweep<T, 64, false>(a, s);
+    if (a.dk <= 128) return age ? launch_sweep<T, 128, true>(a, s) : launch_sweep<T, 128, false>(a, s);
+    return age ? launch_sweep<T, 256, true>(a, s) : launch_sweep<T, 256, false>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_linattn(const LinAttnArgs &a0, bool bf16, hipStream_t s) {
+    LinAttnArgs a = a0;
+    const int64_t ve = bf16 ? 8 : 4;
+    // 16-byte loads where every row and head starts on 16 bytes (the pointers do)
+    a.q_vec = a.q_row % ve == 0 && a.dk % ve == 0;
+    a.k_vec = a.k_row % ve == 0 && a.dk % ve == 0;
+    a.v_vec = a.v_row % ve == 0 && a.dn % ve == 0;
+    a.y_vec = a.dn % 8 == 0;
+    return bf16 ? launch_typed<uint16_t>(a, s) : launch_typed<float>(a, s);
+}
+
+hipError_t launch_linattn_age_sum(const LinAttnArgs &a, float *dlog_decay, hipStream_t s) {
+    hipLaunchKernelGGL(linattn_age_sum_kernel, dim3(static_cast<unsigned>(a.H)), dim3(64), 0, s, a.age_part, dlog_decay, a.B,
+                       a.H, a.nseg * a.ntiles);
+    return launch_status(s);
+}
+
+hipError_t launch_linattn_share(const float *part, void *out, int64_t rows, int64_t H, int64_t G, int64_t D, bool bf16, hipStream_t s) {
+    const int64_t n = rows * G * D;
+    const dim3 grid(static_cast<unsigned>((n + 255) / 256));
+    if (bf16) hipLaunchKernelGGL((linattn_share_kernel<uint16_t>), grid, dim3(256), 0, s, part, static_cast<uint16_t *>(out), n, G, D, H / G);
+    else hipLaunchKernelGGL((linattn_share_kernel<float>), grid, dim3(256), 0, s, part, static_cast<float *>(out), n, G, D, H / G);
+    return launch_status(s);
+}
+
+hipError_t launch_linattn_update(const LinAttnArgs &a0, bool bf16, hipStream_t s) {
+    LinAttnArgs a = a0;
+    a.y_vec = a.dn % 4 == 0;
+    // 16 columns to a workgroup while that leaves CUs without one at 64
+    const bool narrow = a.B * a.H * ((a.dn + 63) / 64) < kCUs;
+    const int64_t cw = narrow ? 16 : 64;
+    const dim3 grid(static_cast<unsigned>(a.B * a.H * ((a.dn + cw - 1) / cw)));
+    if (narrow) {
+        if (bf16) hipLaunchKernelGGL((linattn_update_kernel<uint16_t, 16>), grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((linattn_update_kernel<float, 16>), grid, dim3(256), 0, s, a);
+    } else {
+        if (bf16) hipLaunchKernelGGL((linattn_update_kernel<uint16_t, 64>), grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((linattn_update_kernel<float, 64>), grid, dim3(256), 0, s, a);
+    }
+    return launch_status(s);
+}
+
+}  // namespace ssm

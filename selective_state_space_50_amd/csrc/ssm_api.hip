@@ -1161,3 +1161,146 @@ extern "C" int ssm_ssd_bwd(int64_t batch, int64_t seqlen, int64_t nheads, int64_
     if (e != hipSuccess) return hip_fail("ssd_bwd reduction launch", e);
     return SSM_OK;
 }
+
+namespace ssm {
+namespace {
+LinAttnArgs linattn_args(const ssm_linattn_shape &s, const LinAttnPlan &p, const void *q, const void *k, const void *v,
+                         const float *log_decay, const int32_t *lengths) {
+    LinAttnArgs a{};
+    a.B = s.batch; a.L = s.seqlen; a.H = s.nheads;
+    a.q_heads = s.q_heads; a.k_heads = s.k_heads; a.v_heads = s.v_heads;
+    a.dk = s.dk; a.dn = s.dv;
+    a.q = q; a.k = k; a.v = v;
+    a.q_row = p.q_row; a.k_row = p.k_row; a.v_row = p.v_row;
+    a.log_decay = log_decay; a.lengths = lengths;
+    a.h_sr = s.dv; a.h_sc = 1;
+    return a;
+}
+
+void linattn_split(LinAttnArgs &a, const LinAttnPlan::Sweep &w, void *workspace) {
+    a.nseg = w.nseg; a.seg_len = w.seg_len; a.ntiles = w.ntiles;
+    a.ws_S = w.nseg > 1 ? static_cast<float *>(workspace) : nullptr;
+}
+
+int linattn_fill_state(float *out, const float *from, int64_t n, hipStream_t s) {
+    if (!out || n <= 0) return SSM_OK;
+    hipLaunchKernelGGL(fill_state_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, s, out, from, n);
+    const hipError_t e = launch_status(s);
+    return e == hipSuccess ? SSM_OK : hip_fail("state fill launch", e);
+}
+}  // namespace
+}  // namespace ssm
+
+extern "C" int ssm_linattn_fwd(const ssm_linattn_shape *shape, const void *q, const void *k, const void *v,
+                               const float *log_decay, float scale, const int32_t *lengths, const float *h0,
+                               float *h_last, void *y, void *workspace, size_t workspace_bytes, void *stream) {
+    using namespace ssm;
+    clear_error();
+    LinAttnPlan p;
+    const int st = check_linattn_fwd(shape, q, k, v, log_decay, lengths, h0, h_last, y, workspace, workspace_bytes, &p);
+    if (st != SSM_OK) return st;
+    const ssm_linattn_shape &sh = *shape;
+    if (sh.batch == 0 || sh.nheads == 0) return SSM_OK;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (sh.seqlen == 0) return linattn_fill_state(h_last, h0, sh.batch * sh.nheads * sh.dk * sh.dv, s);
+    log_call("linattn B=%lld L=%lld H=%lld dk=%lld dv=%lld dtype=%d: %lld segments of %lld tokens", (long long)sh.batch,
+             (long long)sh.seqlen, (long long)sh.nheads, (long long)sh.dk, (long long)sh.dv, sh.dtype,
+             (long long)p.fwd.nseg, (long long)p.fwd.seg_len);
+    LinAttnArgs a = linattn_args(sh, p, q, k, v, log_decay, lengths);
+    a.h0 = h0; a.h_last = h_last; a.y = y;
+    a.s_in = scale; a.s_rd = scale;
+    linattn_split(a, p.fwd, workspace);
+    const hipError_t e = launch_linattn(a, sh.dtype == SSM_DTYPE_BF16, s);
+    return e == hipSuccess ? SSM_OK : hip_fail("linattn launch", e);
+}
+
+extern "C" int ssm_linattn_bwd(const ssm_linattn_shape *shape, const void *q, const void *k, const void *v,
+                               const float *log_decay, float scale, const int32_t *lengths, const float *h0,
+                               const void *dy, const float *dh_last, void *dq, void *dk, void *dv, float *dlog_decay,
+                               float *dh0, void *workspace, size_t workspace_bytes, void *stream) {
+    using namespace ssm;
+    clear_error();
+    LinAttnPlan p;
+    const int st = check_linattn_bwd(shape, q, k, v, log_decay, lengths, h0, dy, dh_last, dq, dk, dv, dlog_decay, dh0,
+                                     workspace, workspace_bytes, &p);
+    if (st != SSM_OK) return st;
+    const ssm_linattn_shape &sh = *shape;
+    if (sh.nheads == 0) return SSM_OK;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (sh.batch == 0 || sh.seqlen == 0) {
+        int r = linattn_fill_state(dlog_decay, nullptr, sh.nheads, s);
+        if (r == SSM_OK) r = linattn_fill_state(dh0, dh_last, sh.batch * sh.nheads * sh.dk * sh.dv, s);
+        return r;
+    }
+    const bool bf16 = sh.dtype == SSM_DTYPE_BF16;
+    char *ws = static_cast<char *>(workspace);
+    float *part = reinterpret_cast<float *>(ws + p.part_off);
+    const int64_t rows = sh.batch * sh.seqlen, dy_row = sh.nheads * sh.dv;
+    log_call("linattn backward B=%lld L=%lld H=%lld dk=%lld dv=%lld dtype=%d: %lld and %lld segments", (long long)sh.batch,
+             (long long)sh.seqlen, (long long)sh.nheads, (long long)sh.dk, (long long)sh.dv, sh.dtype,
+             (long long)p.bwd.nseg, (long long)p.fwd.nseg);
+    // one sweep, its output summed over the heads that share a row
+    auto sweep = [&](LinAttnArgs &a, void *out, int64_t heads) {
+        a.out_f32 = heads != sh.nheads;
+        a.y = a.out_f32 ? part : out;
+        hipError_t e = launch_linattn(a, bf16, s);
+        if (e == hipSuccess && a.out_f32) e = launch_linattn_share(part, out, rows, sh.nheads, heads, a.dn, bf16, s);
+        return e;
+    };
+    const LinAttnArgs base = linattn_args(sh, p, q, k, v, log_decay, lengths);
+    // dq = sweep(dy, v, k) from h0^T, with dlog_decay
+    LinAttnArgs a = base;
+    a.q = dy; a.q_heads = sh.nheads; a.q_row = dy_row;
+    a.k = v; a.k_heads = sh.v_heads; a.k_row = p.v_row;
+    a.v = k; a.v_heads = sh.k_heads; a.v_row = p.k_row;
+    a.dk = sh.dv; a.dn = sh.dk;
+    a.h0 = h0; a.h_sr = 1; a.h_sc = sh.dv;
+    a.s_in = scale; a.s_rd = scale;
+    linattn_split(a, p.bwd, workspace);
+    if (dlog_decay) {
+        a.age_w = q; a.age_row = p.q_row; a.age_heads = sh.q_heads;
+        a.age_dh = dh_last;
+        a.age_part = reinterpret_cast<float *>(ws + p.age_off);
+        a.ws_R = p.bwd.nseg > 1 ? reinterpret_cast<float *>(ws + p.ws_R_off) : nullptr;
+    }
+    hipError_t e = sweep(a, dq, sh.q_heads);
+    if (e == hipSuccess && dlog_decay) e = launch_linattn_age_sum(a, dlog_decay, s);
+    // dk = sweep(v, dy, q) from dh_last^T, backward in time
+    if (e == hipSuccess) {
+        a = base;
+        a.q = v; a.q_heads = sh.v_heads; a.q_row = p.v_row;
+        a.k = dy; a.k_heads = sh.nheads; a.k_row = dy_row;
+        a.v = q; a.v_heads = sh.q_heads; a.v_row = p.q_row;
+        a.dk = sh.dv; a.dn = sh.dk;
+        a.h0 = dh_last; a.h_sr = 1; a.h_sc = sh.dv;
+        a.reverse = 1; a.s_in = scale; a.s_wr = scale;
+        linattn_split(a, p.bwd, workspace);
+        e = sweep(a, dk, sh.k_heads);
+    }
+    // dv = sweep(k, q, dy) from dh_last, backward in time; its state ends as dh0
+    if (e == hipSuccess) {
+        a = base;
+        a.q = k; a.q_heads = sh.k_heads; a.q_row = p.k_row;
+        a.k = q; a.k_heads = sh.q_heads; a.k_row = p.q_row;
+        a.v = dy; a.v_heads = sh.nheads; a.v_row = dy_row;
+        a.h0 = dh_last; a.h_last = dh0;
+        a.reverse = 1; a.s_in = scale; a.s_wr = scale;
+        linattn_split(a, p.fwd, workspace);
+        e = sweep(a, dv, sh.v_heads);
+    }
+    return e == hipSuccess ? SSM_OK : hip_fail("linattn backward launch", e);
+}
+
+extern "C" int ssm_linattn_update(const ssm_linattn_shape *shape, float *h, const void *q, const void *k, const void *v,
+                                  const float *log_decay, float scale, void *y, void *stream) {
+    using namespace ssm;
+    clear_error();
+    LinAttnPlan p;
+    const int st = check_linattn_update(shape, h, q, k, v, log_decay, y, &p);
+    if (st != SSM_OK) return st;
+    if (shape->batch == 0 || shape->nheads == 0) return SSM_OK;
+    LinAttnArgs a = linattn_args(*shape, p, q, k, v, log_decay, nullptr);
+    a.h_last = h; a.y = y; a.s_rd = scale;
+    const hipError_t e = launch_linattn_update(a, shape->dtype == SSM_DTYPE_BF16, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? SSM_OK : hip_fail("linattn update launch", e);
+}

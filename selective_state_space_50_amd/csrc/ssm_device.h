@@ -102,6 +102,34 @@ struct SsdArgs {
     int softplus;
 };
 
+struct LinAttnArgs {
+    int64_t B, L, H;                    // batch, tokens, heads
+    int64_t q_heads, k_heads, v_heads;  // head h reads row h / (H / q_heads) of q, ...
+    int64_t dk, dn;                     // columns of q and k, columns of v and y
+    const void *q, *k, *v;              // [B, L, *_heads, .], tokens *_row elements apart
+    int64_t q_row, k_row, v_row;
+    const float *log_decay;             // [H]
+    const int32_t *lengths = nullptr;   // [B] or null: tokens of each row
+    const float *h0 = nullptr;          // [B, H] states or null; element (k, n) at k h_sr + n h_sc
+    float *h_last = nullptr;            // likewise (the update: the state, in place)
+    int64_t h_sr = 0, h_sc = 1;
+    void *y = nullptr;                  // [B, L, H, dn], of the input type or (out_f32) fp32
+    int out_f32 = 0;
+    int reverse = 0;                    // from the last token to the first, the state read before it decays
+    float s_in = 1.0f, s_rd = 1.0f, s_wr = 1.0f;   // factors of the in-chunk product, the readout, the update
+    int64_t nseg = 1, seg_len = 0;      // segments of the sequence that run side by side
+    int64_t ntiles = 1;                 // column tiles of v
+    float *ws_S = nullptr, *ws_R = nullptr;   // [B, H, nseg - 1, dk, dn]
+    // the gradient of log_decay (a sweep of dq): its other factor, q, and the workgroups' shares
+    const void *age_w = nullptr;
+    int64_t age_row = 0, age_heads = 1;
+    const float *age_dh = nullptr;      // gradient of the last state or null, indexed as h0
+    float *age_part = nullptr;          // [B, H, nseg, ntiles], or null: not wanted
+    // set by the launcher
+    int64_t work = 0;
+    int q_vec = 0, k_vec = 0, v_vec = 0, y_vec = 0;
+};
+
 struct ConvArgs {
     int64_t B, L, D;
     int W;                   // filter width (1..4)
@@ -298,6 +326,13 @@ hipError_t launch_conv1d_update(const ConvArgs &a, bool bf16, hipStream_t s);
 hipError_t launch_conv1d_bwd(const ConvArgs &a, bool bf16, hipStream_t s);
 // Multi-head SSD scan (bf16, head dim 64, state size 128): one workgroup per (batch row, head).
 hipError_t launch_ssd(const SsdArgs &a, hipStream_t s);
+// Linear attention: one sweep over a sequence (a prompt, or a gradient), the sum of the shares
+// of dlog_decay, the sum of per-head gradients over the heads that share a row, one token.
+hipError_t launch_linattn(const LinAttnArgs &a, bool bf16, hipStream_t s);
+hipError_t launch_linattn_age_sum(const LinAttnArgs &a, float *dlog_decay, hipStream_t s);
+hipError_t launch_linattn_share(const float *part, void *out, int64_t rows, int64_t H, int64_t G, int64_t D,
+                                bool bf16, hipStream_t s);
+hipError_t launch_linattn_update(const LinAttnArgs &a, bool bf16, hipStream_t s);
 // Backward pass (dstate == 16, dim % 64 == 0).
 hipError_t launch_scan_bwd(const BwdArgs &a, int disc, bool bf16, bool has_z, hipStream_t s);
 

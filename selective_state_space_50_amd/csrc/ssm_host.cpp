@@ -791,6 +791,198 @@ int check_ssd(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim, in
     return check_no_overlap(all + 9, 2, all, n_all);   // h_last, y
 }
 
+// ---------------------------------------------------------------- linear attention
+
+namespace {
+// Segments of one sweep.  A workgroup holds one CU (its LDS tiles), and walks its segment's
+// chunks in order, so a launch takes ceil(workgroups / CUs) rounds of a segment's chunks; more
+// than one segment costs a first pass over k and v for the segments' own states, half
+// of a full pass.  The least of that product is taken.
+void plan_sweep(int64_t batch, int64_t seqlen, int64_t nheads, int64_t contraction, int64_t columns, int dtype,
+                LinAttnPlan::Sweep *p) {
+    const int64_t rows = dtype == SSM_DTYPE_F32 && contraction > 128 ? 32 : 64;
+    const int64_t chunks = ceil_div(seqlen, rows);
+    p->ntiles = ceil_div(columns, 64);
+    const int64_t w = batch * nheads * p->ntiles;
+    int64_t best = 1;
+    double least = 0.0;
+    for (int64_t n = 1; n <= 256 && n <= chunks; ++n) {
+        const int64_t len = ceil_div(chunks, n);
+        if (n > 1 && (len < 4 || ceil_div(chunks, len) != n)) continue;
+        const double cost = static_cast<double>(ceil_div(w * n, kCUs)) * static_cast<double>(len) * (n > 1 ? 1.5 : 1.0);
+        if (n == 1 || cost < 0.95 * least) {
+            least = cost;
+            best = n;
+        }
+        if (w * n >= 4 * kCUs) break;
+    }
+    p->nseg = best;
+    p->seg_len = ceil_div(chunks, best) * rows;
+    p->state_bytes = static_cast<size_t>(batch * nheads * (best - 1) * contraction * columns) * sizeof(float);
+}
+}  // namespace
+
+int plan_linattn(const ssm_linattn_shape *s, bool decay_grad, LinAttnPlan *plan) {
+    if (!s) {
+        set_error("required pointer shape is NULL");
+        return SSM_EINVAL;
+    }
+    if (s->dtype != SSM_DTYPE_F32 && s->dtype != SSM_DTYPE_BF16) {
+        set_error("dtype=%d is neither SSM_DTYPE_F32 nor SSM_DTYPE_BF16", s->dtype);
+        return SSM_EINVAL;
+    }
+    if (s->reserved != 0) {
+        set_error("shape.reserved=%d must be 0", s->reserved);
+        return SSM_EINVAL;
+    }
+    if (s->batch < 0 || s->seqlen < 0 || s->nheads < 0 || s->dk < 1 || s->dv < 1) {
+        set_error("bad size (batch=%lld, seqlen=%lld, nheads=%lld, dk=%lld, dv=%lld)", (long long)s->batch,
+                  (long long)s->seqlen, (long long)s->nheads, (long long)s->dk, (long long)s->dv);
+        return SSM_EINVAL;
+    }
+    const int64_t heads[3] = {s->q_heads, s->k_heads, s->v_heads}, rows[3] = {s->q_row, s->k_row, s->v_row};
+    int64_t *out[3] = {&plan->q_row, &plan->k_row, &plan->v_row};
+    for (int i = 0; i < 3; ++i) {
+        if (heads[i] < 1 || s->nheads % heads[i] != 0) {
+            set_error("%c_heads=%lld must be >= 1 and divide nheads=%lld", "qkv"[i], (long long)heads[i], (long long)s->nheads);
+            return SSM_EINVAL;
+        }
+    }
+    if (s->dk > SSM_LINATTN_MAX_DIM || s->dv > SSM_LINATTN_MAX_DIM) {
+        set_error("dk=%lld, dv=%lld: at most %d is supported", (long long)s->dk, (long long)s->dv, SSM_LINATTN_MAX_DIM);
+        return SSM_EUNSUPPORTED;
+    }
+    // sizes: one launch's workgroups and every index within 64 bits with room to spare
+    if (s->batch > (int64_t(1) << 31) || s->seqlen > (int64_t(1) << 40) || s->nheads > (int64_t(1) << 20) ||
+        (s->nheads > 0 && s->batch > (int64_t(1) << 22) / s->nheads) ||
+        (s->batch > 0 && s->nheads > 0 && s->seqlen > kMaxElems / (s->batch * s->nheads * SSM_LINATTN_MAX_DIM))) {
+        set_error("shape too large for one launch (batch=%lld, seqlen=%lld, nheads=%lld)", (long long)s->batch,
+                  (long long)s->seqlen, (long long)s->nheads);
+        return SSM_EUNSUPPORTED;
+    }
+    for (int i = 0; i < 3; ++i) {
+        const int64_t least = heads[i] * (i < 2 ? s->dk : s->dv);
+        *out[i] = rows[i] ? rows[i] : least;
+        if (*out[i] < least || *out[i] > (int64_t(1) << 31)) {
+            set_error("%c_row=%lld must be 0 or at least the %lld elements of one token", "qkv"[i], (long long)rows[i],
+                      (long long)least);
+            return SSM_EINVAL;
+        }
+    }
+    if (s->batch == 0 || s->nheads == 0 || s->seqlen == 0) return SSM_OK;
+    plan_sweep(s->batch, s->seqlen, s->nheads, s->dk, s->dv, s->dtype, &plan->fwd);
+    plan_sweep(s->batch, s->seqlen, s->nheads, s->dv, s->dk, s->dtype, &plan->bwd);
+    plan->ws_bytes = plan->fwd.state_bytes;
+    size_t at = align_up(plan->fwd.state_bytes > plan->bwd.state_bytes ? plan->fwd.state_bytes : plan->bwd.state_bytes, kWsAlign);
+    plan->ws_R_off = at;
+    if (decay_grad) at = align_up(at + plan->bwd.state_bytes, kWsAlign);
+    plan->age_off = at;
+    if (decay_grad)
+        at = align_up(at + static_cast<size_t>(s->batch * s->nheads * plan->bwd.nseg * plan->bwd.ntiles) * sizeof(float), kWsAlign);
+    plan->part_off = at;
+    int64_t widest = 0;
+    for (int i = 0; i < 3; ++i)
+        if (heads[i] != s->nheads) widest = widest > (i < 2 ? s->dk : s->dv) ? widest : (i < 2 ? s->dk : s->dv);
+    at += static_cast<size_t>(s->batch * s->seqlen * s->nheads * widest) * sizeof(float);
+    plan->ws_bwd_bytes = at;
+    return SSM_OK;
+}
+
+namespace {
+int64_t strided_bytes(const ssm_linattn_shape *s, int64_t row, int64_t heads, int64_t d) {
+    const int64_t tokens = s->batch * s->seqlen;
+    return tokens > 0 ? ((tokens - 1) * row + heads * d) * static_cast<int64_t>(dtype_size(s->dtype)) : 0;
+}
+
+int check_linattn_ranges(const Range *outs, int n_out, const Range *all, int n_all, const void *workspace,
+                         size_t workspace_bytes, size_t need) {
+    int st = check_aligned(all, n_all);
+    if (st != SSM_OK) return st;
+    st = check_no_overlap(outs, n_out, all, n_all);
+    if (st != SSM_OK) return st;
+    if (need > 0 && (!workspace || workspace_bytes < need)) {
+        set_error("workspace of %zu bytes given, %zu needed", workspace ? workspace_bytes : (size_t)0, need);
+        return SSM_EWORKSPACE;
+    }
+    return SSM_OK;
+}
+}  // namespace
+
+int check_linattn_fwd(const ssm_linattn_shape *s, const void *q, const void *k, const void *v, const float *log_decay,
+                      const int32_t *lengths, const float *h0, const float *h_last, const void *y,
+                      const void *workspace, size_t workspace_bytes, LinAttnPlan *plan) {
+    int st = plan_linattn(s, false, plan);
+    if (st != SSM_OK) return st;
+    if (s->batch == 0 || s->nheads == 0) return SSM_OK;
+    const bool rows = s->seqlen > 0;
+    const char *missing = !log_decay ? "log_decay" : rows && !q ? "q" : rows && !k ? "k" : rows && !v ? "v" : rows && !y ? "y" : nullptr;
+    if (missing) {
+        set_error("required pointer %s is NULL", missing);
+        return SSM_EINVAL;
+    }
+    const int64_t es = static_cast<int64_t>(dtype_size(s->dtype)), state = s->batch * s->nheads * s->dk * s->dv * 4;
+    Range all[] = {range("q", q, strided_bytes(s, plan->q_row, s->q_heads, s->dk)),
+                   range("k", k, strided_bytes(s, plan->k_row, s->k_heads, s->dk)),
+                   range("v", v, strided_bytes(s, plan->v_row, s->v_heads, s->dv)),
+                   range("log_decay", log_decay, s->nheads * 4), range("lengths", lengths, s->batch * 4),
+                   range("h0", h0, state),
+                   // outputs from here on
+                   range("h_last", h_last, state), range("y", y, s->batch * s->seqlen * s->nheads * s->dv * es),
+                   range("workspace", workspace, static_cast<int64_t>(plan->ws_bytes))};
+    return check_linattn_ranges(all + 6, 3, all, 9, workspace, workspace_bytes, plan->ws_bytes);
+}
+
+int check_linattn_bwd(const ssm_linattn_shape *s, const void *q, const void *k, const void *v, const float *log_decay,
+                      const int32_t *lengths, const float *h0, const void *dy, const float *dh_last, const void *dq,
+                      const void *dk, const void *dv, const float *dlog_decay, const float *dh0,
+                      const void *workspace, size_t workspace_bytes, LinAttnPlan *plan) {
+    int st = plan_linattn(s, dlog_decay != nullptr, plan);
+    if (st != SSM_OK) return st;
+    if (s->nheads == 0) return SSM_OK;
+    const bool rows = s->seqlen > 0 && s->batch > 0;
+    const char *missing = !log_decay ? "log_decay" : rows && !q ? "q" : rows && !k ? "k" : rows && !v ? "v" : rows && !dy ? "dy"
+                        : rows && !dq ? "dq" : rows && !dk ? "dk" : rows && !dv ? "dv" : nullptr;
+    if (missing) {
+        set_error("required pointer %s is NULL", missing);
+        return SSM_EINVAL;
+    }
+    const int64_t es = static_cast<int64_t>(dtype_size(s->dtype)), state = s->batch * s->nheads * s->dk * s->dv * 4;
+    const int64_t tokens = s->batch * s->seqlen;
+    Range all[] = {range("q", q, strided_bytes(s, plan->q_row, s->q_heads, s->dk)),
+                   range("k", k, strided_bytes(s, plan->k_row, s->k_heads, s->dk)),
+                   range("v", v, strided_bytes(s, plan->v_row, s->v_heads, s->dv)),
+                   range("log_decay", log_decay, s->nheads * 4), range("lengths", lengths, s->batch * 4),
+                   range("h0", h0, state), range("dy", dy, tokens * s->nheads * s->dv * es), range("dh_last", dh_last, state),
+                   // outputs from here on
+                   range("dq", dq, tokens * s->q_heads * s->dk * es), range("dk", dk, tokens * s->k_heads * s->dk * es),
+                   range("dv", dv, tokens * s->v_heads * s->dv * es), range("dlog_decay", dlog_decay, s->nheads * 4),
+                   range("dh0", dh0, state), range("workspace", workspace, static_cast<int64_t>(plan->ws_bwd_bytes))};
+    return check_linattn_ranges(all + 8, 6, all, 14, workspace, workspace_bytes, plan->ws_bwd_bytes);
+}
+
+int check_linattn_update(const ssm_linattn_shape *s, const float *h, const void *q, const void *k, const void *v,
+                         const float *log_decay, const void *y, LinAttnPlan *plan) {
+    int st = plan_linattn(s, false, plan);
+    if (st != SSM_OK) return st;
+    if (s->seqlen != 1) {
+        set_error("shape.seqlen=%lld must be 1 for one token", (long long)s->seqlen);
+        return SSM_EINVAL;
+    }
+    if (s->batch == 0 || s->nheads == 0) return SSM_OK;
+    const char *missing = !h ? "h" : !q ? "q" : !k ? "k" : !v ? "v" : !log_decay ? "log_decay" : !y ? "y" : nullptr;
+    if (missing) {
+        set_error("required pointer %s is NULL", missing);
+        return SSM_EINVAL;
+    }
+    const int64_t es = static_cast<int64_t>(dtype_size(s->dtype));
+    Range all[] = {range("q", q, strided_bytes(s, plan->q_row, s->q_heads, s->dk)),
+                   range("k", k, strided_bytes(s, plan->k_row, s->k_heads, s->dk)),
+                   range("v", v, strided_bytes(s, plan->v_row, s->v_heads, s->dv)),
+                   range("log_decay", log_decay, s->nheads * 4),
+                   range("h", h, s->batch * s->nheads * s->dk * s->dv * 4), range("y", y, s->batch * s->nheads * s->dv * es)};
+    return check_linattn_ranges(all + 4, 2, all, 6, nullptr, 0, 0);
+}
+
 }  // namespace ssm
 
 extern "C" {
@@ -868,6 +1060,18 @@ size_t ssm_scan_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int6
     ssm::ScanPlan p;
     if (ssm::plan_scan(batch, seqlen, dim, dstate, dtype, opts, &p) != SSM_OK) return 0;
     return p.ws_bytes;
+}
+
+size_t ssm_linattn_workspace_bytes(const ssm_linattn_shape *shape) {
+    ssm::clear_error();
+    ssm::LinAttnPlan p;
+    return ssm::plan_linattn(shape, false, &p) == SSM_OK ? p.ws_bytes : 0;
+}
+
+size_t ssm_linattn_bwd_workspace_bytes(const ssm_linattn_shape *shape, int decay_grad) {
+    ssm::clear_error();
+    ssm::LinAttnPlan p;
+    return ssm::plan_linattn(shape, decay_grad != 0, &p) == SSM_OK ? p.ws_bwd_bytes : 0;
 }
 
 }  // extern "C"

@@ -157,6 +157,32 @@ int check_ssd(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim, in
               const float *Dskip, const void *z, const float *delta_bias, const float *h0,
               const float *h_last, const void *y, int delta_softplus);
 
+// Linear attention: how the sequence is split and what the workspace holds.
+struct LinAttnPlan {
+    int64_t q_row = 0, k_row = 0, v_row = 0;   // token strides, with the contiguous default filled in
+    // a sweep with contraction size c and n value columns: segments and their length
+    struct Sweep {
+        int64_t nseg = 1, seg_len = 0, ntiles = 1;
+        size_t state_bytes = 0;   // one array of the segments' states
+    };
+    Sweep fwd;                  // y: contraction over dk, dv columns (dv's sweep, too)
+    Sweep bwd;                  // dq and dk: contraction over dv, dk columns
+    size_t ws_bytes = 0;        // of the forward
+    // backward: states (and their derivatives by log_decay), the shares of dlog_decay, per-head
+    // fp32 gradients of rows that several heads share
+    size_t ws_R_off = 0, age_off = 0, part_off = 0, ws_bwd_bytes = 0;
+};
+int plan_linattn(const ssm_linattn_shape *s, bool decay_grad, LinAttnPlan *plan);
+int check_linattn_fwd(const ssm_linattn_shape *s, const void *q, const void *k, const void *v, const float *log_decay,
+                      const int32_t *lengths, const float *h0, const float *h_last, const void *y,
+                      const void *workspace, size_t workspace_bytes, LinAttnPlan *plan);
+int check_linattn_bwd(const ssm_linattn_shape *s, const void *q, const void *k, const void *v, const float *log_decay,
+                      const int32_t *lengths, const float *h0, const void *dy, const float *dh_last, const void *dq,
+                      const void *dk, const void *dv, const float *dlog_decay, const float *dh0,
+                      const void *workspace, size_t workspace_bytes, LinAttnPlan *plan);
+int check_linattn_update(const ssm_linattn_shape *s, const float *h, const void *q, const void *k, const void *v,
+                         const float *log_decay, const void *y, LinAttnPlan *plan);
+
 inline size_t dtype_size(int dtype) { return dtype == SSM_DTYPE_BF16 ? 2 : 4; }
 
 }  // namespace ssm

@@ -1,0 +1,139 @@
+"""Refusals of the linear attention entry points (no GPU: nothing is launched)."""
+import ctypes
+import os
+
+import pytest
+
+import selective_state_space_50_amd as ssm
+
+A0 = 1 << 40
+STEP = 1 << 32   # fake device addresses 4 GiB apart; never dereferenced
+
+
+def P(i, off=0):
+    return ctypes.c_void_p(A0 + i * STEP + off)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(ssm.LIB_PATH):
+        pytest.skip("libssm.so not built")
+    return ssm.lib()
+
+
+def shape(batch=2, seqlen=100, nheads=4, q_heads=4, k_heads=4, v_heads=4, dk=64, dv=64, q_row=0, k_row=0, v_row=0,
+          dtype=1, reserved=0):
+    return ssm.LinAttnShape(batch, seqlen, nheads, q_heads, k_heads, v_heads, dk, dv, q_row, k_row, v_row, dtype, reserved)
+
+
+def fwd(lib, s, q=P(0), y=P(5), h0=P(6), h_last=P(7), lengths=None, ws=None, ws_bytes=0, log_decay=P(3)):
+    return lib.ssm_linattn_fwd(ctypes.byref(s) if s else None, q, P(1), P(2), log_decay, 1.0, lengths, h0, h_last, y, ws,
+                               ws_bytes, None)
+
+
+@pytest.mark.parametrize("bad,status,text", [
+    (dict(dtype=2), 1, "dtype"), (dict(reserved=1), 1, "reserved"), (dict(batch=-1), 1, "bad size"),
+    (dict(dk=0), 1, "bad size"), (dict(dv=0), 1, "bad size"), (dict(dk=257), 2, "at most 256"),
+    (dict(dv=300), 2, "at most 256"), (dict(q_heads=3), 1, "q_heads"), (dict(k_heads=0), 1, "k_heads"),
+    (dict(v_heads=8), 1, "v_heads"), (dict(q_row=255), 1, "q_row"), (dict(v_row=-1), 1, "v_row"),
+    (dict(batch=1 << 30), 2, "too large"), (dict(seqlen=1 << 50), 2, "too large"),
+])
+def test_shape_refusals(lib, bad, status, text):
+    s = shape(**bad)
+    assert fwd(lib, s) == status
+    assert text in lib.ssm_last_error().decode()
+    assert lib.ssm_linattn_bwd(ctypes.byref(s), *[P(i) for i in range(4)], 1.0, None, *[P(i) for i in range(4, 12)],
+                               P(12), 1 << 40, None) == status
+    assert lib.ssm_linattn_workspace_bytes(ctypes.byref(s)) == 0
+    assert lib.ssm_linattn_bwd_workspace_bytes(ctypes.byref(s), 1) == 0
+
+
+def test_pointer_refusals(lib):
+    assert fwd(lib, None) == 1 and b"shape" in lib.ssm_last_error()
+    assert fwd(lib, shape(), q=None) == 1 and b"q is NULL" in lib.ssm_last_error()
+    assert fwd(lib, shape(), y=None) == 1 and b"y is NULL" in lib.ssm_last_error()
+    assert fwd(lib, shape(), log_decay=None) == 1 and b"log_decay" in lib.ssm_last_error()
+    assert fwd(lib, shape(), q=P(0, 2)) == 1 and b"q is not 16-byte aligned" in lib.ssm_last_error()
+    assert fwd(lib, shape(), lengths=P(8, 4)) == 1 and b"lengths" in lib.ssm_last_error()
+    assert fwd(lib, shape(), y=P(1)) == 1 and b"output y overlaps k" in lib.ssm_last_error()
+    assert fwd(lib, shape(), h_last=P(6)) == 1 and b"output h_last overlaps h0" in lib.ssm_last_error()
+    # y over the last strided token of q
+    wide = shape(q_row=1000)
+    last = (2 * 100 - 1) * 1000 * 2
+    assert fwd(lib, wide, y=P(0, last)) == 1 and b"output y overlaps q" in lib.ssm_last_error()
+
+
+def test_workspace(lib):
+    few = shape(batch=1, seqlen=8192, nheads=2, q_heads=2, k_heads=2, v_heads=2)
+    need = lib.ssm_linattn_workspace_bytes(ctypes.byref(few))
+    assert need > 0 and need % (2 * 64 * 64 * 4) == 0          # whole segment states
+    assert fwd(lib, few) == 3 and b"workspace" in lib.ssm_last_error()
+    assert fwd(lib, few, ws=P(9), ws_bytes=need - 1) == 3
+    assert fwd(lib, few, ws=P(9, 8), ws_bytes=need) == 1        # alignment
+    assert fwd(lib, few, ws=P(5), ws_bytes=need) == 1           # y in the workspace
+    # enough heads to fill the chip: one segment, no workspace
+    assert lib.ssm_linattn_workspace_bytes(ctypes.byref(shape(batch=4, seqlen=4096, nheads=64, q_heads=64, k_heads=64,
+                                                              v_heads=64, dk=128))) == 0
+    # rows shared by heads need their per-head gradients
+    s1, s2 = shape(), shape(k_heads=1, v_heads=1)
+    assert lib.ssm_linattn_bwd_workspace_bytes(ctypes.byref(s2), 0) >= \
+        lib.ssm_linattn_bwd_workspace_bytes(ctypes.byref(s1), 0) + 2 * 100 * 4 * 64 * 4
+    assert ssm.linattn_workspace_bytes(1, 8192, 2, 64, 64) == need
+    assert ssm.linattn_bwd_workspace_bytes(1, 8192, 2, 64, 64) > 2 * need
+
+
+def test_backward_and_update_refusals(lib):
+    def bwd(s, dy=P(5), dq=P(7), dk=P(8), dv=P(9), da=P(10), dh0=P(11), ws=P(12), n=1 << 31):
+        return lib.ssm_linattn_bwd(ctypes.byref(s), P(0), P(1), P(2), P(3), 1.0, None, P(4), dy, P(6), dq, dk, dv, da, dh0,
+                                   ws, n, None)
+    assert bwd(shape(), dy=None) == 1 and b"dy is NULL" in lib.ssm_last_error()
+    assert bwd(shape(), dk=None) == 1 and b"dk is NULL" in lib.ssm_last_error()
+    assert bwd(shape(), dq=P(0)) == 1 and b"output dq overlaps q" in lib.ssm_last_error()
+    assert bwd(shape(), dh0=P(6)) == 1 and b"output dh0 overlaps dh_last" in lib.ssm_last_error()
+    assert bwd(shape(), dv=P(8)) == 1
+    assert bwd(shape(), ws=None, n=0) == 3
+
+    def upd(s, h=P(4), y=P(5)):
+        return lib.ssm_linattn_update(ctypes.byref(s), h, P(0), P(1), P(2), P(3), 1.0, y, None)
+    assert upd(shape()) == 1 and b"seqlen" in lib.ssm_last_error()
+    assert upd(shape(seqlen=1), h=None) == 1 and b"h is NULL" in lib.ssm_last_error()
+    assert upd(shape(seqlen=1), y=P(4)) == 1 and b"overlaps" in lib.ssm_last_error()
+    assert upd(shape(seqlen=1, dk=512)) == 2
+
+
+def test_empty_batches_are_no_ops(lib):
+    assert fwd(lib, shape(batch=0), q=None, y=None) == 0
+    assert upd_empty(lib) == 0
+
+
+def upd_empty(lib):
+    return lib.ssm_linattn_update(ctypes.byref(shape(batch=0, seqlen=1)), None, None, None, None, None, 1.0, None, None)
+
+
+def test_binding_refuses_cpu_and_mismatched_tensors(lib):
+    import torch
+    q = torch.zeros(1, 4, 2, 8)
+    a = torch.zeros(2)
+    for call in (lambda: ssm.linattn_fwd(q, q, q, a), lambda: ssm.linear_attention(q, q, q, a),
+                 lambda: ssm.linattn_bwd(q, q, q, a, dy=q), lambda: ssm.linattn_update(torch.zeros(1, 2, 8, 8), q[:, 0], q[:, 0], q[:, 0], a)):
+        with pytest.raises(ValueError, match="GPU only"):
+            call()
+    with pytest.raises(ValueError, match="must be"):
+        ssm.linattn_fwd(q[0], q, q, a)
+
+
+def test_strided_rows():
+    """The token stride of a slice of a joint projection, and layouts that have none."""
+    import torch
+    wide = torch.zeros(2, 5, 3 * 32)
+    dev = wide.device
+    s = wide[..., 32:64].unflatten(-1, (4, 8))
+    assert ssm._rows(s, "k", (2, 5), 4, 8, torch.float32, dev) == 96
+    assert ssm._rows(s[:, 0], "k", (2,), 4, 8, torch.float32, dev) == 480
+    assert ssm._rows(s[:1, :1], "k", (1, 1), 4, 8, torch.float32, dev) == 32
+    for bad in (s.transpose(2, 3).contiguous().transpose(2, 3), torch.zeros(2, 4, 5, 8).transpose(1, 2),
+                torch.zeros(5, 2, 4, 8).transpose(0, 1), torch.zeros(1, 1, 4, 8).expand(2, 5, 4, 8)):
+        with pytest.raises(ValueError, match="evenly spaced"):
+            ssm._rows(bad, "k", (2, 5), 4, 8, torch.float32, dev)
+    with pytest.raises(TypeError):
+        ssm._rows(s.half(), "k", (2, 5), 4, 8, torch.float32, dev)
