@@ -556,6 +556,48 @@ int ssm_linattn_bwd(const ssm_linattn_shape *shape, const void *q, const void *k
 int ssm_linattn_update(const ssm_linattn_shape *shape, float *h, const void *q, const void *k, const void *v,
                        const float *log_decay, float scale, void *y, void *stream);
 
+/* Host-only: bytes of device workspace of ssm_groupnorm_fwd and (backward != 0) of
+ * ssm_groupnorm_bwd (0: none needed, or the shape is invalid). */
+size_t ssm_groupnorm_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int64_t groups, int dtype, int backward);
+
+/*
+ * Group norm, channels last, with an activation or a gate: the norm after a layer's scan or
+ * linear attention.  The dim channels fall into groups of dim / groups consecutive ones; for every
+ * batch row and group, over its seqlen * dim / groups values,
+ *     u = (x - mean) / sqrt(var + eps) * w[d] + bias[d],   y = act(u) * silu(z)
+ * (var: the mean of squared deviations; act: silu, or nothing when silu == 0).  To norm every
+ * token by itself, as after linear attention with a group per head, pass the tokens as batch rows:
+ * batch * seqlen, 1.
+ *
+ *   x, z      [batch, seqlen, dim]   dtype   z NULL = no gate
+ *   w, bias   [dim]                  fp32    NULL = 1, 0
+ *   y         [batch, seqlen, dim]   dtype   output; must not overlap an input
+ *   mean, rstd [batch, groups]       fp32    what the backward reads; NULL = not stored
+ *   workspace device memory of ssm_groupnorm_workspace_bytes(.., 0) bytes (NULL if 0)
+ * groups must be >= 1 and divide dim, eps >= 0 (else SSM_EINVAL).  batch, seqlen or dim == 0 is a no-op.
+ * Statistics in fp32, from deviations (never a difference of squares).  Deterministic.
+ */
+int ssm_groupnorm_fwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t groups, int dtype, const void *x,
+                      const float *w, const float *bias, const void *z, float eps, int silu, void *y, float *mean,
+                      float *rstd, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Backward pass of ssm_groupnorm_fwd: gradients of a loss given dy = dLoss/dy.  Inputs as the
+ * forward, plus dy [batch, seqlen, dim] and the forward's mean and rstd (required; they already hold
+ * eps).  With xh the normed values, g = dy silu(z) act'(u), e = g w, and means over a group's values:
+ *     dz = dy act(u) silu'(z),  dw = sum g xh,  dbias = sum g,  dx = rstd (e - mean(e) - xh mean(e xh))
+ * Outputs (fully overwritten, none overlapping an input or another output):
+ *   dx        [batch, seqlen, dim]   dtype   required
+ *   dz        [batch, seqlen, dim]   dtype   required when z is given, else ignored
+ *   dw, dbias [dim]                  fp32    NULL = not computed
+ *   workspace device memory of ssm_groupnorm_workspace_bytes(.., 1) bytes
+ * dim == 0 is a no-op; batch or seqlen == 0 sets dw and dbias to zero.  Deterministic.
+ */
+int ssm_groupnorm_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t groups, int dtype, const void *x,
+                      const float *w, const float *bias, const void *z, int silu, const void *dy, const float *mean,
+                      const float *rstd, void *dx, float *dw, float *dbias, void *dz, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -16,7 +16,8 @@ import re
 
 __all__ = ["scan_fwd", "scan_fwd_save", "scan_save_sizes", "scan_bwd", "state_update", "scan_plan", "scan_workspace_bytes",
            "scan_bwd_workspace_bytes", "selective_scan", "conv1d_fwd", "conv1d_update", "linattn_fwd", "linattn_bwd",
-           "linattn_update", "linattn_workspace_bytes", "linattn_bwd_workspace_bytes", "linear_attention", "lib",
+           "linattn_update", "linattn_workspace_bytes", "linattn_bwd_workspace_bytes", "linear_attention",
+           "groupnorm_fwd", "groupnorm_bwd", "groupnorm_workspace_bytes", "group_norm", "lib",
            "SSMError", "LIB_PATH",
            "HEADER_PATH", "exported_api"]
 
@@ -139,6 +140,12 @@ def lib():
     L.ssm_linattn_bwd.argtypes = [S, P, P, P, P, ctypes.c_float] + [P] * 10 + [SZ, P]
     L.ssm_linattn_update.restype = I32
     L.ssm_linattn_update.argtypes = [S, P, P, P, P, P, ctypes.c_float, P, P]
+    L.ssm_groupnorm_workspace_bytes.restype = SZ
+    L.ssm_groupnorm_workspace_bytes.argtypes = [I64, I64, I64, I64, I32, I32]
+    L.ssm_groupnorm_fwd.restype = I32
+    L.ssm_groupnorm_fwd.argtypes = [I64, I64, I64, I64, I32, P, P, P, P, ctypes.c_float, I32, P, P, P, P, SZ, P]
+    L.ssm_groupnorm_bwd.restype = I32
+    L.ssm_groupnorm_bwd.argtypes = [I64, I64, I64, I64, I32, P, P, P, P, I32] + [P] * 8 + [SZ, P]
     if L.ssm_abi_version() != ABI_VERSION:
         raise ImportError(f"libssm ABI version {L.ssm_abi_version()} != {ABI_VERSION}")
     _lib = L
@@ -931,3 +938,121 @@ def linear_attention(q, k, v, log_decay, h0=None, *, scale=None, lengths=None, r
     backward through linattn_bwd (gradients for q, k, v, log_decay and h0).  Arguments as
     linattn_fwd; with return_last_state both outputs can be differentiated."""
     return _linattn_function().apply(q, k, v, log_decay, h0, scale, lengths, bool(return_last_state))
+
+
+def _norm_rows(x, groups, span, activation, what):
+    """(batch, seqlen, dim) as the library takes them, the shape of the statistics, and silu: with span "token" every
+    token is a batch row."""
+    if x.dim() not in (2, 3):
+        raise ValueError("x must be [batch, seqlen, dim] or [batch, dim]")
+    if span not in ("token", "sequence"):
+        raise ValueError(f"span {span!r} is neither 'token' nor 'sequence'")
+    if activation not in ("none", "silu"):
+        raise ValueError(f"activation {activation!r} is neither 'none' nor 'silu'")
+    if x.device.type != "cuda":
+        raise ValueError(f"{what} runs on the GPU only; tensors must be on a cuda device")
+    head, dim = tuple(x.shape[:-1]), x.shape[-1]
+    if span == "token":
+        return (head[0] * (head[1] if len(head) == 2 else 1), 1, dim), (*head, groups), int(activation == "silu")
+    return (head[0], head[1] if len(head) == 2 else 1, dim), (head[0], groups), int(activation == "silu")
+
+
+def groupnorm_workspace_bytes(batch, seqlen, dim, groups, dtype="bf16", span="token", backward=False) -> int:
+    """Device workspace bytes of groupnorm_fwd (or, with backward, groupnorm_bwd) for this shape (0: none)."""
+    code = DTYPE_BF16 if dtype in ("bf16", "bfloat16") else DTYPE_F32
+    n, length = (batch * seqlen, 1) if span == "token" else (batch, seqlen)
+    return int(lib().ssm_groupnorm_workspace_bytes(n, length, dim, groups, code, int(bool(backward))))
+
+
+def groupnorm_fwd(x, groups, w=None, bias=None, z=None, *, span="token", activation="none", eps=1e-5,
+                  return_stats=False, out=None, workspace=None, stream=None):
+    """Group norm, channels last: u = (x - mean) / sqrt(var + eps) * w + bias, y = act(u) * silu(z).
+
+    x, z: [B, L, D] or [B, D] (bf16 or fp32), the D channels in ``groups`` groups of consecutive
+    ones; w, bias: [D] fp32.  span: the values that share a mean and variance, a group's channels
+    of one token ("token": the norm after linear attention, a group per head) or of the whole
+    sequence ("sequence").  activation: "none" or "silu".  Returns y, or (y, mean, rstd) when
+    return_stats: [B, L, groups] (or [B, groups]) fp32, what groupnorm_bwd reads.
+    """
+    import torch
+    size, stats, silu = _norm_rows(x, groups, span, activation, "groupnorm_fwd")
+    dev, dt, shape = x.device, x.dtype, tuple(x.shape)
+    code = _dtype_code(x)
+    for t, n, s, d in ((x, "x", shape, dt), (z, "z", shape, dt), (w, "w", shape[-1:], torch.float32),
+                       (bias, "bias", shape[-1:], torch.float32), (out, "out", shape, dt)):
+        _need(t, n, s, d, dev)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(shape, dtype=dt, device=dev)
+        mean, rstd = (torch.empty(stats, dtype=torch.float32, device=dev) for _ in range(2)) if return_stats else (None, None)
+        need = int(lib().ssm_groupnorm_workspace_bytes(*size, groups, code, 0))
+        workspace = _workspace(workspace, need, dev)
+        st = lib().ssm_groupnorm_fwd(*size, groups, code, _ptr(x), _ptr(w), _ptr(bias), _ptr(z), float(eps), silu, _ptr(out),
+                                     _ptr(mean), _ptr(rstd), _ptr(workspace) if need else None, need,
+                                     ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream))
+    _check(st, "ssm_groupnorm_fwd")
+    return (out, mean, rstd) if return_stats else out
+
+
+def groupnorm_bwd(x, groups, w=None, bias=None, z=None, dy=None, mean=None, rstd=None, *, span="token",
+                  activation="none", need_dw=True, workspace=None, stream=None):
+    """Gradients of a loss through groupnorm_fwd, given dy = dLoss/dy (x's shape and dtype) and
+    the forward's mean and rstd.  Other arguments as groupnorm_fwd.
+
+    Returns a dict: dx and dz (None without z) as x; dw (None without w) and dbias (None without a
+    bias) [D] fp32, both None when need_dw is false.
+    """
+    import torch
+    size, stats, silu = _norm_rows(x, groups, span, activation, "groupnorm_bwd")
+    for t, n in ((dy, "dy"), (mean, "mean"), (rstd, "rstd")):
+        if t is None:
+            raise ValueError(f"{n} is required")
+    dev, dt, shape = x.device, x.dtype, tuple(x.shape)
+    code = _dtype_code(x)
+    for t, n, s, d in ((x, "x", shape, dt), (z, "z", shape, dt), (dy, "dy", shape, dt), (w, "w", shape[-1:], torch.float32),
+                       (bias, "bias", shape[-1:], torch.float32), (mean, "mean", stats, torch.float32),
+                       (rstd, "rstd", stats, torch.float32)):
+        _need(t, n, s, d, dev)
+    with _on(dev, stream):
+        new = lambda s, d: torch.empty(s, dtype=d, device=dev)  # noqa: E731
+        out = {"dx": new(shape, dt), "dz": new(shape, dt) if z is not None else None,
+               "dw": new(shape[-1:], torch.float32) if w is not None and need_dw else None,
+               "dbias": new(shape[-1:], torch.float32) if bias is not None and need_dw else None}
+        need = int(lib().ssm_groupnorm_workspace_bytes(*size, groups, code, 1))
+        workspace = _workspace(workspace, need, dev)
+        st = lib().ssm_groupnorm_bwd(*size, groups, code, _ptr(x), _ptr(w), _ptr(bias), _ptr(z), silu, _ptr(dy), _ptr(mean),
+                                     _ptr(rstd), _ptr(out["dx"]), _ptr(out["dw"]), _ptr(out["dbias"]), _ptr(out["dz"]),
+                                     _ptr(workspace) if need else None, need,
+                                     ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream))
+    _check(st, "ssm_groupnorm_bwd")
+    return out
+
+
+@functools.lru_cache(maxsize=None)
+def _groupnorm_function():
+    import torch
+
+    class _GroupNorm(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, groups, w, bias, z, span, activation, eps):
+            y, mean, rstd = groupnorm_fwd(x, groups, w, bias, z, span=span, activation=activation, eps=eps, return_stats=True)
+            ctx.save_for_backward(x, w, bias, z, mean, rstd)
+            ctx.how = groups, span, activation
+            return y
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, gy):
+            x, w, bias, z, mean, rstd = ctx.saved_tensors
+            groups, span, activation = ctx.how
+            g = groupnorm_bwd(x, groups, w, bias, z, gy.contiguous(), mean, rstd, span=span, activation=activation,
+                              need_dw=ctx.needs_input_grad[2] or ctx.needs_input_grad[3])
+            return g["dx"], None, g["dw"], g["dbias"], g["dz"], None, None, None
+
+    return _GroupNorm
+
+
+def group_norm(x, groups, w=None, bias=None, z=None, *, span="token", activation="none", eps=1e-5):
+    """Differentiable group norm, channels last: groupnorm_fwd with a torch autograd backward
+    through groupnorm_bwd (gradients for x, w, bias and z).  Arguments as groupnorm_fwd."""
+    return _groupnorm_function().apply(x, groups, w, bias, z, span, activation, eps)

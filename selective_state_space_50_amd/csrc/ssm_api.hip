@@ -1182,11 +1182,11 @@ void linattn_split(LinAttnArgs &a, const LinAttnPlan::Sweep &w, void *workspace)
     a.ws_S = w.nseg > 1 ? static_cast<float *>(workspace) : nullptr;
 }
 
-int linattn_fill_state(float *out, const float *from, int64_t n, hipStream_t s) {
+int fill_floats(float *out, const float *from, int64_t n, hipStream_t s) {
     if (!out || n <= 0) return SSM_OK;
     hipLaunchKernelGGL(fill_state_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, s, out, from, n);
     const hipError_t e = launch_status(s);
-    return e == hipSuccess ? SSM_OK : hip_fail("state fill launch", e);
+    return e == hipSuccess ? SSM_OK : hip_fail("fill launch", e);
 }
 }  // namespace
 }  // namespace ssm
@@ -1202,7 +1202,7 @@ extern "C" int ssm_linattn_fwd(const ssm_linattn_shape *shape, const void *q, co
     const ssm_linattn_shape &sh = *shape;
     if (sh.batch == 0 || sh.nheads == 0) return SSM_OK;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if (sh.seqlen == 0) return linattn_fill_state(h_last, h0, sh.batch * sh.nheads * sh.dk * sh.dv, s);
+    if (sh.seqlen == 0) return fill_floats(h_last, h0, sh.batch * sh.nheads * sh.dk * sh.dv, s);
     log_call("linattn B=%lld L=%lld H=%lld dk=%lld dv=%lld dtype=%d: %lld segments of %lld tokens", (long long)sh.batch,
              (long long)sh.seqlen, (long long)sh.nheads, (long long)sh.dk, (long long)sh.dv, sh.dtype,
              (long long)p.fwd.nseg, (long long)p.fwd.seg_len);
@@ -1228,8 +1228,8 @@ extern "C" int ssm_linattn_bwd(const ssm_linattn_shape *shape, const void *q, co
     if (sh.nheads == 0) return SSM_OK;
     hipStream_t s = static_cast<hipStream_t>(stream);
     if (sh.batch == 0 || sh.seqlen == 0) {
-        int r = linattn_fill_state(dlog_decay, nullptr, sh.nheads, s);
-        if (r == SSM_OK) r = linattn_fill_state(dh0, dh_last, sh.batch * sh.nheads * sh.dk * sh.dv, s);
+        int r = fill_floats(dlog_decay, nullptr, sh.nheads, s);
+        if (r == SSM_OK) r = fill_floats(dh0, dh_last, sh.batch * sh.nheads * sh.dk * sh.dv, s);
         return r;
     }
     const bool bf16 = sh.dtype == SSM_DTYPE_BF16;
@@ -1303,4 +1303,63 @@ extern "C" int ssm_linattn_update(const ssm_linattn_shape *shape, float *h, cons
     a.h_last = h; a.y = y; a.s_rd = scale;
     const hipError_t e = launch_linattn_update(a, shape->dtype == SSM_DTYPE_BF16, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? SSM_OK : hip_fail("linattn update launch", e);
+}
+
+extern "C" int ssm_groupnorm_fwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t groups, int dtype, const void *x,
+                                 const float *w, const float *bias, const void *z, float eps, int silu, void *y,
+                                 float *mean, float *rstd, void *workspace, size_t workspace_bytes, void *stream) {
+    using namespace ssm;
+    clear_error();
+    GroupNormPlan p;
+    const int st = check_groupnorm_fwd(batch, seqlen, dim, groups, dtype, x, w, bias, z, eps, silu, y, mean, rstd, workspace,
+                                       workspace_bytes, &p);
+    if (st != SSM_OK) return st;
+    if (batch == 0 || seqlen == 0 || dim == 0) return SSM_OK;
+    char *ws = static_cast<char *>(workspace);
+    GroupNormArgs a{};
+    a.N = batch; a.L = seqlen; a.C = dim; a.G = groups; a.S = dim / groups;
+    a.x = x; a.z = z; a.w = w; a.b = bias; a.eps = eps; a.silu = silu; a.y = y; a.mean = mean; a.rstd = rstd;
+    a.team = p.team; a.nvec = p.nvec; a.nslab = p.nslab; a.slab_rows = p.slab_rows;
+    if (!p.team) {
+        a.part = reinterpret_cast<float *>(ws);
+        if (!mean) a.mean = reinterpret_cast<float *>(ws + p.mean_off);
+        if (!rstd) a.rstd = reinterpret_cast<float *>(ws + p.rstd_off);
+    }
+    log_call("groupnorm N=%lld L=%lld C=%lld G=%lld dtype=%d: team %d, %lld slabs", (long long)batch, (long long)seqlen,
+             (long long)dim, (long long)groups, dtype, p.team, (long long)p.nslab);
+    const hipError_t e = launch_groupnorm_fwd(a, dtype == SSM_DTYPE_BF16, p.vec, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? SSM_OK : hip_fail("groupnorm launch", e);
+}
+
+extern "C" int ssm_groupnorm_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t groups, int dtype, const void *x,
+                                 const float *w, const float *bias, const void *z, int silu, const void *dy,
+                                 const float *mean, const float *rstd, void *dx, float *dw, float *dbias, void *dz,
+                                 void *workspace, size_t workspace_bytes, void *stream) {
+    using namespace ssm;
+    clear_error();
+    GroupNormPlan p;
+    const int st = check_groupnorm_bwd(batch, seqlen, dim, groups, dtype, x, w, bias, z, silu, dy, mean, rstd, dx, dw, dbias, dz,
+                                       workspace, workspace_bytes, &p);
+    if (st != SSM_OK) return st;
+    if (dim == 0) return SSM_OK;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (batch == 0 || seqlen == 0) {
+        const int r = fill_floats(dw, nullptr, dim, s);
+        return r == SSM_OK ? fill_floats(dbias, nullptr, dim, s) : r;
+    }
+    char *ws = static_cast<char *>(workspace);
+    GroupNormArgs a{};
+    a.N = batch; a.L = seqlen; a.C = dim; a.G = groups; a.S = dim / groups;
+    a.x = x; a.z = z; a.dy = dy; a.w = w; a.b = bias; a.silu = silu; a.dx = dx; a.dz = dz; a.dw = dw; a.db = dbias;
+    a.mean = const_cast<float *>(mean); a.rstd = const_cast<float *>(rstd);
+    a.team = p.team; a.nvec = p.nvec; a.nslab = p.nslab; a.slab_rows = p.slab_rows;
+    if (!p.team || dw || dbias) a.part = reinterpret_cast<float *>(ws);
+    if (!p.team) {
+        a.sums = reinterpret_cast<float *>(ws + p.sums_off);
+        a.gsum = reinterpret_cast<float *>(ws + p.gsum_off);
+    }
+    log_call("groupnorm backward N=%lld L=%lld C=%lld G=%lld dtype=%d: team %d, %lld slabs", (long long)batch, (long long)seqlen,
+             (long long)dim, (long long)groups, dtype, p.team, (long long)p.nslab);
+    const hipError_t e = launch_groupnorm_bwd(a, dtype == SSM_DTYPE_BF16, p.vec, s);
+    return e == hipSuccess ? SSM_OK : hip_fail("groupnorm backward launch", e);
 }

@@ -130,6 +130,23 @@ struct LinAttnArgs {
     int q_vec = 0, k_vec = 0, v_vec = 0, y_vec = 0;
 };
 
+struct GroupNormArgs {
+    int64_t N, L, C, G, S;           // rows of statistics, positions, channels, groups, channels of a group
+    const void *x, *z, *dy;          // [N, L, C]; z null = no gate
+    const float *w, *b;              // [C] each, or null
+    float eps;
+    int silu;
+    void *y, *dx, *dz;
+    float *mean, *rstd;              // [N, G]: written by the forward (null: not stored), read by the backward
+    float *dw, *db;                  // [C] or null
+    int team = 0;                    // lanes that hold one group (256: a workgroup); 0: slabs of rows
+    int64_t nvec = 0;                // vectors of one group
+    int64_t nslab = 1, slab_rows = 0;   // slabs (the backward with teams: workgroups along the rows)
+    float *part = nullptr;           // slabs' statistics [N, nslab, G, 2], or channel sums [.., 2 C]
+    float *sums = nullptr;           // backward, slabs: channel sums [N, 2 C]
+    float *gsum = nullptr;           // and the two sums of dx [N, G, 2]
+};
+
 struct ConvArgs {
     int64_t B, L, D;
     int W;                   // filter width (1..4)
@@ -333,6 +350,9 @@ hipError_t launch_linattn_age_sum(const LinAttnArgs &a, float *dlog_decay, hipSt
 hipError_t launch_linattn_share(const float *part, void *out, int64_t rows, int64_t H, int64_t G, int64_t D,
                                 bool bf16, hipStream_t s);
 hipError_t launch_linattn_update(const LinAttnArgs &a, bool bf16, hipStream_t s);
+// Group norm; vec: 16-byte loads (the groups' channels a multiple of 16 bytes).
+hipError_t launch_groupnorm_fwd(const GroupNormArgs &a, bool bf16, bool vec, hipStream_t s);
+hipError_t launch_groupnorm_bwd(const GroupNormArgs &a, bool bf16, bool vec, hipStream_t s);
 // Backward pass (dstate == 16, dim % 64 == 0).
 hipError_t launch_scan_bwd(const BwdArgs &a, int disc, bool bf16, bool has_z, hipStream_t s);
 

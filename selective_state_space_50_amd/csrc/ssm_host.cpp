@@ -894,7 +894,7 @@ int64_t strided_bytes(const ssm_linattn_shape *s, int64_t row, int64_t heads, in
     return tokens > 0 ? ((tokens - 1) * row + heads * d) * static_cast<int64_t>(dtype_size(s->dtype)) : 0;
 }
 
-int check_linattn_ranges(const Range *outs, int n_out, const Range *all, int n_all, const void *workspace,
+int check_ranges(const Range *outs, int n_out, const Range *all, int n_all, const void *workspace,
                          size_t workspace_bytes, size_t need) {
     int st = check_aligned(all, n_all);
     if (st != SSM_OK) return st;
@@ -929,7 +929,7 @@ int check_linattn_fwd(const ssm_linattn_shape *s, const void *q, const void *k, 
                    // outputs from here on
                    range("h_last", h_last, state), range("y", y, s->batch * s->seqlen * s->nheads * s->dv * es),
                    range("workspace", workspace, static_cast<int64_t>(plan->ws_bytes))};
-    return check_linattn_ranges(all + 6, 3, all, 9, workspace, workspace_bytes, plan->ws_bytes);
+    return check_ranges(all + 6, 3, all, 9, workspace, workspace_bytes, plan->ws_bytes);
 }
 
 int check_linattn_bwd(const ssm_linattn_shape *s, const void *q, const void *k, const void *v, const float *log_decay,
@@ -957,7 +957,7 @@ int check_linattn_bwd(const ssm_linattn_shape *s, const void *q, const void *k, 
                    range("dq", dq, tokens * s->q_heads * s->dk * es), range("dk", dk, tokens * s->k_heads * s->dk * es),
                    range("dv", dv, tokens * s->v_heads * s->dv * es), range("dlog_decay", dlog_decay, s->nheads * 4),
                    range("dh0", dh0, state), range("workspace", workspace, static_cast<int64_t>(plan->ws_bwd_bytes))};
-    return check_linattn_ranges(all + 8, 6, all, 14, workspace, workspace_bytes, plan->ws_bwd_bytes);
+    return check_ranges(all + 8, 6, all, 14, workspace, workspace_bytes, plan->ws_bwd_bytes);
 }
 
 int check_linattn_update(const ssm_linattn_shape *s, const float *h, const void *q, const void *k, const void *v,
@@ -980,7 +980,135 @@ int check_linattn_update(const ssm_linattn_shape *s, const float *h, const void 
                    range("v", v, strided_bytes(s, plan->v_row, s->v_heads, s->dv)),
                    range("log_decay", log_decay, s->nheads * 4),
                    range("h", h, s->batch * s->nheads * s->dk * s->dv * 4), range("y", y, s->batch * s->nheads * s->dv * es)};
-    return check_linattn_ranges(all + 4, 2, all, 6, nullptr, 0, 0);
+    return check_ranges(all + 4, 2, all, 6, nullptr, 0, 0);
+}
+
+// ---------------------------------------------------------------- group norm
+
+int plan_groupnorm(int64_t batch, int64_t seqlen, int64_t dim, int64_t groups, int dtype, bool backward, GroupNormPlan *plan) {
+    if (dtype != SSM_DTYPE_F32 && dtype != SSM_DTYPE_BF16) {
+        set_error("dtype=%d is neither SSM_DTYPE_F32 nor SSM_DTYPE_BF16", dtype);
+        return SSM_EINVAL;
+    }
+    if (batch < 0 || seqlen < 0 || dim < 0) {
+        set_error("negative size (batch=%lld, seqlen=%lld, dim=%lld)", (long long)batch, (long long)seqlen, (long long)dim);
+        return SSM_EINVAL;
+    }
+    if (groups < 1 || dim % groups != 0) {
+        set_error("groups=%lld must be >= 1 and divide dim=%lld", (long long)groups, (long long)dim);
+        return SSM_EINVAL;
+    }
+    if (batch == 0 || seqlen == 0 || dim == 0) return SSM_OK;
+    if (dim > (int64_t(1) << 24) || batch > (int64_t(1) << 30) / groups || seqlen > (int64_t(1) << 32) ||
+        seqlen > kMaxElems / (batch * dim)) {
+        set_error("shape too large for one launch (batch=%lld, seqlen=%lld, dim=%lld, groups=%lld)", (long long)batch,
+                  (long long)seqlen, (long long)dim, (long long)groups);
+        return SSM_EUNSUPPORTED;
+    }
+    const int64_t wide = dtype == SSM_DTYPE_BF16 ? 8 : 4, s = dim / groups;
+    plan->vec = s % wide == 0;
+    const int64_t ve = plan->vec ? wide : 1, wg = 256;
+    plan->nvec = seqlen * s / ve;
+    // up to eight vectors a lane; the backward takes single positions (each lane keeps its
+    // channels from row to row) and two vectors a lane (with more its registers spill)
+    if (backward ? seqlen == 1 && plan->nvec <= 2 * wg : plan->nvec <= 8 * wg && seqlen * dim < (int64_t(1) << 31)) {
+        plan->team = static_cast<int>(wg);
+        if (plan->nvec <= (backward ? 64 : 4 * 64)) {
+            plan->team = 1;
+            while (plan->team < 64 && plan->team < plan->nvec) plan->team *= 2;
+        }
+        if (!backward) return SSM_OK;
+        const int64_t teams = wg / plan->team, gb = teams < groups ? teams : groups, side = teams / gb;
+        // four workgroups to a CU, but eight rows at least to each (their sums of dw and db
+        // cost 8 bytes a channel)
+        const int64_t across = ceil_div(groups, gb), most = ceil_div(batch, side * 8);
+        plan->nslab = 4 * kCUs / across;
+        if (plan->nslab > most) plan->nslab = most;
+        if (plan->nslab < 1) plan->nslab = 1;
+        plan->ws_bytes = static_cast<size_t>(plan->nslab * side * 2 * dim) * sizeof(float);
+        return SSM_OK;
+    }
+    if (batch > 65535 || ceil_div(dim, ve) / wg > 65535) {
+        set_error("batch=%lld rows of large groups, or dim=%lld: too many for one launch", (long long)batch, (long long)dim);
+        return SSM_EUNSUPPORTED;
+    }
+    // slabs: eight workgroups to a CU, but four turns of its rows at least to each
+    const int64_t cols = dim / ve < wg ? dim / ve : wg, across = ceil_div(dim / ve, wg), side = wg / cols;
+    int64_t n = 8 * kCUs / (batch * across);
+    const int64_t most = ceil_div(seqlen, 4 * side);
+    if (n > most) n = most;
+    if (n < 1) n = 1;
+    plan->slab_rows = ceil_div(seqlen, n);
+    plan->nslab = ceil_div(seqlen, plan->slab_rows);
+    size_t at = static_cast<size_t>(batch * plan->nslab * 2 * (backward ? dim : groups)) * sizeof(float);
+    auto take = [&](size_t bytes) {
+        const size_t off = align_up(at, kWsAlign);
+        at = off + bytes;
+        return off;
+    };
+    const size_t per_group = static_cast<size_t>(batch * groups) * sizeof(float);
+    if (backward) {
+        plan->sums_off = take(static_cast<size_t>(batch * 2 * dim) * sizeof(float));
+        plan->gsum_off = take(2 * per_group);
+    } else {
+        plan->mean_off = take(per_group);
+        plan->rstd_off = take(per_group);
+    }
+    plan->ws_bytes = at;
+    return SSM_OK;
+}
+
+int check_groupnorm_fwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t groups, int dtype, const void *x,
+                        const float *w, const float *bias, const void *z, float eps, int silu, const void *y,
+                        const float *mean, const float *rstd, const void *workspace, size_t workspace_bytes,
+                        GroupNormPlan *plan) {
+    int st = plan_groupnorm(batch, seqlen, dim, groups, dtype, false, plan);
+    if (st != SSM_OK) return st;
+    if (silu != 0 && silu != 1) {
+        set_error("silu=%d is neither 0 nor 1", silu);
+        return SSM_EINVAL;
+    }
+    if (!(eps >= 0.0f)) {
+        set_error("eps=%g must be >= 0", static_cast<double>(eps));
+        return SSM_EINVAL;
+    }
+    if (batch == 0 || seqlen == 0 || dim == 0) return SSM_OK;
+    if (!x || !y) {
+        set_error("required pointer %s is NULL", !x ? "x" : "y");
+        return SSM_EINVAL;
+    }
+    const int64_t tok = batch * seqlen * dim * static_cast<int64_t>(dtype_size(dtype)), per = batch * groups * 4;
+    Range all[] = {range("x", x, tok), range("w", w, dim * 4), range("bias", bias, dim * 4), range("z", z, tok),
+                   // outputs from here on
+                   range("y", y, tok), range("mean", mean, per), range("rstd", rstd, per),
+                   range("workspace", workspace, static_cast<int64_t>(plan->ws_bytes))};
+    return check_ranges(all + 4, 4, all, 8, workspace, workspace_bytes, plan->ws_bytes);
+}
+
+int check_groupnorm_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t groups, int dtype, const void *x,
+                        const float *w, const float *bias, const void *z, int silu, const void *dy, const float *mean,
+                        const float *rstd, const void *dx, const float *dw, const float *dbias, const void *dz,
+                        const void *workspace, size_t workspace_bytes, GroupNormPlan *plan) {
+    int st = plan_groupnorm(batch, seqlen, dim, groups, dtype, true, plan);
+    if (st != SSM_OK) return st;
+    if (silu != 0 && silu != 1) {
+        set_error("silu=%d is neither 0 nor 1", silu);
+        return SSM_EINVAL;
+    }
+    if (dim == 0) return SSM_OK;
+    const bool rows = batch > 0 && seqlen > 0;
+    const char *missing = !rows ? nullptr : !x ? "x" : !dy ? "dy" : !mean ? "mean" : !rstd ? "rstd" : !dx ? "dx" : z && !dz ? "dz" : nullptr;
+    if (missing) {
+        set_error("required pointer %s is NULL", missing);
+        return SSM_EINVAL;
+    }
+    const int64_t tok = batch * seqlen * dim * static_cast<int64_t>(dtype_size(dtype)), per = batch * groups * 4;
+    Range all[] = {range("x", x, tok), range("w", w, dim * 4), range("bias", bias, dim * 4), range("z", z, tok),
+                   range("dy", dy, tok), range("mean", mean, per), range("rstd", rstd, per),
+                   // outputs from here on
+                   range("dx", dx, tok), range("dw", dw, dim * 4), range("dbias", dbias, dim * 4),
+                   range("dz", z ? dz : nullptr, tok), range("workspace", workspace, static_cast<int64_t>(plan->ws_bytes))};
+    return check_ranges(all + 7, 5, all, 12, workspace, workspace_bytes, plan->ws_bytes);
 }
 
 }  // namespace ssm
@@ -1072,6 +1200,12 @@ size_t ssm_linattn_bwd_workspace_bytes(const ssm_linattn_shape *shape, int decay
     ssm::clear_error();
     ssm::LinAttnPlan p;
     return ssm::plan_linattn(shape, decay_grad != 0, &p) == SSM_OK ? p.ws_bwd_bytes : 0;
+}
+
+size_t ssm_groupnorm_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int64_t groups, int dtype, int backward) {
+    ssm::clear_error();
+    ssm::GroupNormPlan p;
+    return ssm::plan_groupnorm(batch, seqlen, dim, groups, dtype, backward != 0, &p) == SSM_OK ? p.ws_bytes : 0;
 }
 
 }  // extern "C"

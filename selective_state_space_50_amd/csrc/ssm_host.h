@@ -183,6 +183,25 @@ int check_linattn_bwd(const ssm_linattn_shape *s, const void *q, const void *k, 
 int check_linattn_update(const ssm_linattn_shape *s, const float *h, const void *q, const void *k, const void *v,
                          const float *log_decay, const void *y, LinAttnPlan *plan);
 
+// Group norm: how groups are held (see groupnorm.hip) and what the workspace holds.
+struct GroupNormPlan {
+    bool vec = false;        // 16-byte loads
+    int team = 0;            // lanes that hold one group; 0: slabs of rows
+    int64_t nvec = 0;        // vectors (or elements) of one group
+    int64_t nslab = 1, slab_rows = 0;
+    size_t mean_off = 0, rstd_off = 0, sums_off = 0, gsum_off = 0;   // (the slabs' sums come first)
+    size_t ws_bytes = 0;
+};
+int plan_groupnorm(int64_t batch, int64_t seqlen, int64_t dim, int64_t groups, int dtype, bool backward, GroupNormPlan *plan);
+int check_groupnorm_fwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t groups, int dtype, const void *x,
+                        const float *w, const float *bias, const void *z, float eps, int silu, const void *y,
+                        const float *mean, const float *rstd, const void *workspace, size_t workspace_bytes,
+                        GroupNormPlan *plan);
+int check_groupnorm_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t groups, int dtype, const void *x,
+                        const float *w, const float *bias, const void *z, int silu, const void *dy, const float *mean,
+                        const float *rstd, const void *dx, const float *dw, const float *dbias, const void *dz,
+                        const void *workspace, size_t workspace_bytes, GroupNormPlan *plan);
+
 inline size_t dtype_size(int dtype) { return dtype == SSM_DTYPE_BF16 ? 2 : 4; }
 
 }  // namespace ssm
