@@ -224,7 +224,7 @@ def _ptr(t):
 
 
 def _need(t, name, shape, dtype, device):
-    if t is None:
+    if t is None or (t.shape == shape and t.dtype == dtype and t.device == device and t.is_contiguous()):
         return
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
@@ -746,43 +746,81 @@ def ssd_bwd(x, delta, A, B, C, D=None, z=None, h0=None, dy=None, dh_last=None, *
     return out
 
 
-def _rows(t, name, tokens, heads, d, dtype, device):
+def _rows(t, name, tokens, heads, d):
     """Elements from one token of t [B, L, heads, d] (tokens = (B, L)) or [B, heads, d] (tokens = (B,)) to the
-    next: t may be a part of a wider row (a slice of a joint projection's output) as long as its heads stand side
-    by side and all tokens the same distance apart."""
-    if tuple(t.shape) != (*tokens, heads, d):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(*tokens, heads, d)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.numel() == 0 or t.is_contiguous():
+    next, from its (shape, strides): t may be a part of a wider row (a slice of a joint projection's output) as
+    long as its heads stand side by side and all tokens the same distance apart."""
+    shape, st = t
+    if tuple(shape) != (*tokens, heads, d):
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected {(*tokens, heads, d)}")
+    if 0 in shape:
         return heads * d
-    st = t.stride()
     sizes = [(n, s) for n, s in zip(tokens, st) if n > 1]
     row = sizes[-1][1] if sizes else heads * d
     even = len(sizes) < 2 or sizes[0][1] == row * sizes[1][0]
     if (d > 1 and st[-1] != 1) or (heads > 1 and st[-2] != d) or not even or row < heads * d:
-        raise ValueError(f"{name} must have its heads contiguous and its tokens evenly spaced (strides {st})")
+        raise ValueError(f"{name} must have its heads contiguous and its tokens evenly spaced (strides {tuple(st)})")
     return row
 
 
-def _linattn_shape(q, k, v, log_decay, tokens, what):
-    """The checked ssm_linattn_shape of a call; tokens: 4 for [B, L, heads, d], 3 for [B, heads, d]."""
+class _Sizes:
+    """The ssm_linattn_shape of a call, its reference, and the sizes of its state, output and workspaces."""
+
+    def __init__(self, shape):
+        self.c = shape
+        self.ref = ctypes.byref(shape)
+        self.scale = shape.dk ** -0.5
+        self.state = (shape.batch, shape.nheads, shape.dk, shape.dv)
+        self.out = (shape.batch, shape.seqlen, shape.nheads, shape.dv)
+
+    @functools.cached_property
+    def fwd_bytes(self):
+        return int(lib().ssm_linattn_workspace_bytes(self.ref))
+
+    @functools.cached_property
+    def bwd_bytes(self):
+        return [int(lib().ssm_linattn_bwd_workspace_bytes(self.ref, i)) for i in (0, 1)]
+
+
+@functools.lru_cache(maxsize=1024)
+def _linattn_sizes(q, k, v, H, code):
+    """From (shape, strides) of q, k and v, [B, L, heads, d] or [B, heads, d]."""
+    n = len(q[0])
+    if len(k[0]) != n or len(v[0]) != n or n not in (3, 4):
+        raise ValueError(f"q, k and v must be [batch, {'seqlen, ' if n == 4 else ''}heads, dim]")
+    head, dk, dv = tuple(q[0][:-2]), q[0][-1], v[0][-1]
+    rows = [_rows(t, name, head, t[0][-2], d) for t, name, d in ((q, "q", dk), (k, "k", dk), (v, "v", dv))]
+    return _Sizes(LinAttnShape(head[0], head[1] if n == 4 else 1, H, q[0][-2], k[0][-2], v[0][-2], dk, dv, *rows, code, 0))
+
+
+def _linattn_call(q, k, v, log_decay, tokens, what):
+    """Device, dtype and checked sizes of a call; tokens: 4 for [B, L, heads, d], 3 for [B, heads, d]."""
     import torch
-    if q.dim() != tokens or k.dim() != tokens or v.dim() != tokens:
+    dev, dt = q.device, q.dtype
+    if q.dim() != tokens:
         raise ValueError(f"q, k and v must be [batch, {'seqlen, ' if tokens == 4 else ''}heads, dim]")
     if log_decay.dim() != 1:
         raise ValueError("log_decay must be [nheads]")
-    dev, dt, H = q.device, q.dtype, log_decay.shape[0]
     if dev.type != "cuda":
         raise ValueError(f"{what} runs on the GPU only; tensors must be on a cuda device")
-    head = tuple(q.shape[:tokens - 2])
-    dk, dv = q.shape[-1], v.shape[-1]
-    rows = [_rows(t, n, head, t.shape[-2], d, dt, dev) for t, n, d in ((q, "q", dk), (k, "k", dk), (v, "v", dv))]
-    _need(log_decay, "log_decay", (H,), torch.float32, dev)
-    return LinAttnShape(head[0], head[1] if tokens == 4 else 1, H, q.shape[-2], k.shape[-2], v.shape[-2], dk, dv, *rows,
-                        _dtype_code(q), 0)
+    code = _dtype_code(q)
+    for t, name in ((k, "k"), (v, "v")):
+        if t.dtype != dt:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected {dt}")
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    _need(log_decay, "log_decay", log_decay.shape, torch.float32, dev)
+    return dev, dt, _linattn_sizes((q.shape, q.stride()), (k.shape, k.stride()), (v.shape, v.stride()), log_decay.shape[0], code)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream(device):
+    """torch's current HIP stream on the device, as a raw handle."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _workspace(given, need, device):
@@ -792,18 +830,13 @@ def _workspace(given, need, device):
     return given
 
 
-def _on(device, stream):
-    """Context in which a call's tensors are allocated and its kernels launched: the tensors'
-    device, and the stream given (what is allocated belongs to that stream)."""
-    import contextlib
-
+def _elsewhere(device, stream):
+    """None where a call runs as things are; else the context it has to run in: the tensors'
+    device, and the stream given (what the call allocates then belongs to that stream)."""
     import torch
-    stack = contextlib.ExitStack()
-    if torch.cuda.current_device() != device.index:
-        stack.enter_context(torch.cuda.device(device))
-    if stream is not None:
-        stack.enter_context(torch.cuda.stream(stream))
-    return stack
+    if stream is None and torch.cuda.current_device() == device.index:
+        return None
+    return torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
 
 
 def linattn_workspace_bytes(batch, seqlen, nheads, dk, dv, dtype="bf16") -> int:
@@ -834,25 +867,25 @@ def linattn_fwd(q, k, v, log_decay, h0=None, *, scale=None, lengths=None, return
     after lengths[b] tokens).  Returns y [B, L, H, dv], or (y, h_last) when return_last_state.
     """
     import torch
-    s = _linattn_shape(q, k, v, log_decay, 4, "linattn_fwd")
-    dev, dt = q.device, q.dtype
-    state = (s.batch, s.nheads, s.dk, s.dv)
-    _need(h0, "h0", state, torch.float32, dev)
-    _need(lengths, "lengths", (s.batch,), torch.int32, dev)
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty((s.batch, s.seqlen, s.nheads, s.dv), dtype=dt, device=dev)
-        _need(out, "out", (s.batch, s.seqlen, s.nheads, s.dv), dt, dev)
-        if return_last_state and h_last is None:
-            h_last = torch.empty(state, dtype=torch.float32, device=dev)
-        _need(h_last, "h_last", state, torch.float32, dev)
-        need = int(lib().ssm_linattn_workspace_bytes(ctypes.byref(s)))
-        workspace = _workspace(workspace, need, dev)
-        st = lib().ssm_linattn_fwd(ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
-                                   s.dk ** -0.5 if scale is None else float(scale), _ptr(lengths), _ptr(h0),
-                                   _ptr(h_last), _ptr(out), _ptr(workspace) if need else None, need,
-                                   ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream))
-    _check(st, "ssm_linattn_fwd")
+    dev, dt, s = _linattn_call(q, k, v, log_decay, 4, "linattn_fwd")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return linattn_fwd(q, k, v, log_decay, h0, scale=scale, lengths=lengths, return_last_state=return_last_state,
+                               out=out, h_last=h_last, workspace=workspace)
+    _need(h0, "h0", s.state, torch.float32, dev)
+    _need(lengths, "lengths", s.state[:1], torch.int32, dev)
+    _need(out, "out", s.out, dt, dev)
+    _need(h_last, "h_last", s.state, torch.float32, dev)
+    if out is None:
+        out = torch.empty(s.out, dtype=dt, device=dev)
+    if return_last_state and h_last is None:
+        h_last = torch.empty(s.state, dtype=torch.float32, device=dev)
+    need = s.fwd_bytes
+    workspace = _workspace(workspace, need, dev)
+    _check(lib().ssm_linattn_fwd(s.ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                                 s.scale if scale is None else scale, _addr(lengths), _addr(h0), _addr(h_last),
+                                 out.data_ptr(), _addr(workspace) if need else None, need, _stream(dev)), "ssm_linattn_fwd")
     return (out, h_last) if return_last_state else out
 
 
@@ -866,27 +899,28 @@ def linattn_bwd(q, k, v, log_decay, h0=None, dy=None, dh_last=None, *, scale=Non
     fixed decay saves a third of the call) and dh0 [B, H, dk, dv] fp32 (None when not needed).
     """
     import torch
-    s = _linattn_shape(q, k, v, log_decay, 4, "linattn_bwd")
+    dev, dt, s = _linattn_call(q, k, v, log_decay, 4, "linattn_bwd")
     if dy is None:
         raise ValueError("dy is required")
-    dev, dt = q.device, q.dtype
-    state = (s.batch, s.nheads, s.dk, s.dv)
-    for t, n, shape, d in ((h0, "h0", state, torch.float32), (lengths, "lengths", (s.batch,), torch.int32),
-                           (dy, "dy", (s.batch, s.seqlen, s.nheads, s.dv), dt), (dh_last, "dh_last", state, torch.float32)):
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return linattn_bwd(q, k, v, log_decay, h0, dy, dh_last, scale=scale, lengths=lengths,
+                               need_dlog_decay=need_dlog_decay, need_dh0=need_dh0, workspace=workspace)
+    for t, n, shape, d in ((h0, "h0", s.state, torch.float32), (lengths, "lengths", s.state[:1], torch.int32),
+                           (dy, "dy", s.out, dt), (dh_last, "dh_last", s.state, torch.float32)):
         _need(t, n, shape, d, dev)
-    with _on(dev, stream):
-        new = lambda shape, d: torch.empty(shape, dtype=d, device=dev)  # noqa: E731
-        out = {"dq": new(q.shape, dt), "dk": new(k.shape, dt), "dv": new(v.shape, dt),
-               "dlog_decay": new((s.nheads,), torch.float32) if need_dlog_decay else None,
-               "dh0": new(state, torch.float32) if need_dh0 else None}
-        need = int(lib().ssm_linattn_bwd_workspace_bytes(ctypes.byref(s), int(bool(need_dlog_decay))))
-        workspace = _workspace(workspace, need, dev)
-        st = lib().ssm_linattn_bwd(ctypes.byref(s), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
-                                   s.dk ** -0.5 if scale is None else float(scale), _ptr(lengths), _ptr(h0), _ptr(dy),
-                                   _ptr(dh_last), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
-                                   _ptr(out["dlog_decay"]), _ptr(out["dh0"]), _ptr(workspace) if need else None, need,
-                                   ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream))
-    _check(st, "ssm_linattn_bwd")
+    new = lambda shape, d: torch.empty(shape, dtype=d, device=dev)  # noqa: E731
+    out = {"dq": new(q.shape, dt), "dk": new(k.shape, dt), "dv": new(v.shape, dt),
+           "dlog_decay": new(log_decay.shape, torch.float32) if need_dlog_decay else None,
+           "dh0": new(s.state, torch.float32) if need_dh0 else None}
+    need = s.bwd_bytes[bool(need_dlog_decay)]
+    workspace = _workspace(workspace, need, dev)
+    _check(lib().ssm_linattn_bwd(s.ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                                 s.scale if scale is None else scale, _addr(lengths), _addr(h0), dy.data_ptr(),
+                                 _addr(dh_last), out["dq"].data_ptr(), out["dk"].data_ptr(), out["dv"].data_ptr(),
+                                 _addr(out["dlog_decay"]), _addr(out["dh0"]), _addr(workspace) if need else None, need,
+                                 _stream(dev)), "ssm_linattn_bwd")
     return out
 
 
@@ -894,17 +928,18 @@ def linattn_update(h, q, k, v, log_decay, *, scale=None, out=None, stream=None):
     """One token of linattn_fwd: h [B, H, dk, dv] fp32 is updated in place; q, k [B, heads, dk],
     v [B, heads, dv]; returns y [B, H, dv]."""
     import torch
-    s = _linattn_shape(q, k, v, log_decay, 3, "linattn_update")
-    dev, dt = q.device, q.dtype
-    _need(h, "h", (s.batch, s.nheads, s.dk, s.dv), torch.float32, dev)
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty((s.batch, s.nheads, s.dv), dtype=dt, device=dev)
-        _need(out, "out", (s.batch, s.nheads, s.dv), dt, dev)
-        st = lib().ssm_linattn_update(ctypes.byref(s), _ptr(h), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
-                                      s.dk ** -0.5 if scale is None else float(scale), _ptr(out),
-                                      ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream))
-    _check(st, "ssm_linattn_update")
+    dev, dt, s = _linattn_call(q, k, v, log_decay, 3, "linattn_update")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return linattn_update(h, q, k, v, log_decay, scale=scale, out=out)
+    _need(h, "h", s.state, torch.float32, dev)
+    if out is None:
+        out = torch.empty((s.c.batch, s.c.nheads, s.c.dv), dtype=dt, device=dev)
+    else:
+        _need(out, "out", (s.c.batch, s.c.nheads, s.c.dv), dt, dev)
+    _check(lib().ssm_linattn_update(s.ref, h.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                                    s.scale if scale is None else scale, out.data_ptr(), _stream(dev)), "ssm_linattn_update")
     return out
 
 
@@ -961,7 +996,12 @@ def groupnorm_workspace_bytes(batch, seqlen, dim, groups, dtype="bf16", span="to
     """Device workspace bytes of groupnorm_fwd (or, with backward, groupnorm_bwd) for this shape (0: none)."""
     code = DTYPE_BF16 if dtype in ("bf16", "bfloat16") else DTYPE_F32
     n, length = (batch * seqlen, 1) if span == "token" else (batch, seqlen)
-    return int(lib().ssm_groupnorm_workspace_bytes(n, length, dim, groups, code, int(bool(backward))))
+    return _groupnorm_bytes((n, length, dim), groups, code, int(bool(backward)))
+
+
+@functools.lru_cache(maxsize=1024)
+def _groupnorm_bytes(size, groups, code, backward):
+    return int(lib().ssm_groupnorm_workspace_bytes(*size, groups, code, backward))
 
 
 def groupnorm_fwd(x, groups, w=None, bias=None, z=None, *, span="token", activation="none", eps=1e-5,
@@ -976,21 +1016,26 @@ def groupnorm_fwd(x, groups, w=None, bias=None, z=None, *, span="token", activat
     """
     import torch
     size, stats, silu = _norm_rows(x, groups, span, activation, "groupnorm_fwd")
-    dev, dt, shape = x.device, x.dtype, tuple(x.shape)
+    dev, dt, shape = x.device, x.dtype, x.shape
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return groupnorm_fwd(x, groups, w, bias, z, span=span, activation=activation, eps=eps, return_stats=return_stats,
+                                 out=out, workspace=workspace)
     code = _dtype_code(x)
-    for t, n, s, d in ((x, "x", shape, dt), (z, "z", shape, dt), (w, "w", shape[-1:], torch.float32),
-                       (bias, "bias", shape[-1:], torch.float32), (out, "out", shape, dt)):
-        _need(t, n, s, d, dev)
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty(shape, dtype=dt, device=dev)
-        mean, rstd = (torch.empty(stats, dtype=torch.float32, device=dev) for _ in range(2)) if return_stats else (None, None)
-        need = int(lib().ssm_groupnorm_workspace_bytes(*size, groups, code, 0))
-        workspace = _workspace(workspace, need, dev)
-        st = lib().ssm_groupnorm_fwd(*size, groups, code, _ptr(x), _ptr(w), _ptr(bias), _ptr(z), float(eps), silu, _ptr(out),
-                                     _ptr(mean), _ptr(rstd), _ptr(workspace) if need else None, need,
-                                     ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream))
-    _check(st, "ssm_groupnorm_fwd")
+    _need(x, "x", shape, dt, dev)
+    _need(z, "z", shape, dt, dev)
+    _need(w, "w", shape[-1:], torch.float32, dev)
+    _need(bias, "bias", shape[-1:], torch.float32, dev)
+    _need(out, "out", shape, dt, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=dev)
+    mean, rstd = (torch.empty(stats, dtype=torch.float32, device=dev) for _ in range(2)) if return_stats else (None, None)
+    need = _groupnorm_bytes(size, groups, code, 0)
+    workspace = _workspace(workspace, need, dev)
+    _check(lib().ssm_groupnorm_fwd(*size, groups, code, x.data_ptr(), _addr(w), _addr(bias), _addr(z), eps, silu,
+                                   out.data_ptr(), _addr(mean), _addr(rstd), _addr(workspace) if need else None, need,
+                                   _stream(dev)), "ssm_groupnorm_fwd")
     return (out, mean, rstd) if return_stats else out
 
 
@@ -1007,24 +1052,27 @@ def groupnorm_bwd(x, groups, w=None, bias=None, z=None, dy=None, mean=None, rstd
     for t, n in ((dy, "dy"), (mean, "mean"), (rstd, "rstd")):
         if t is None:
             raise ValueError(f"{n} is required")
-    dev, dt, shape = x.device, x.dtype, tuple(x.shape)
+    dev, dt, shape = x.device, x.dtype, x.shape
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return groupnorm_bwd(x, groups, w, bias, z, dy, mean, rstd, span=span, activation=activation, need_dw=need_dw,
+                                 workspace=workspace)
     code = _dtype_code(x)
     for t, n, s, d in ((x, "x", shape, dt), (z, "z", shape, dt), (dy, "dy", shape, dt), (w, "w", shape[-1:], torch.float32),
                        (bias, "bias", shape[-1:], torch.float32), (mean, "mean", stats, torch.float32),
                        (rstd, "rstd", stats, torch.float32)):
         _need(t, n, s, d, dev)
-    with _on(dev, stream):
-        new = lambda s, d: torch.empty(s, dtype=d, device=dev)  # noqa: E731
-        out = {"dx": new(shape, dt), "dz": new(shape, dt) if z is not None else None,
-               "dw": new(shape[-1:], torch.float32) if w is not None and need_dw else None,
-               "dbias": new(shape[-1:], torch.float32) if bias is not None and need_dw else None}
-        need = int(lib().ssm_groupnorm_workspace_bytes(*size, groups, code, 1))
-        workspace = _workspace(workspace, need, dev)
-        st = lib().ssm_groupnorm_bwd(*size, groups, code, _ptr(x), _ptr(w), _ptr(bias), _ptr(z), silu, _ptr(dy), _ptr(mean),
-                                     _ptr(rstd), _ptr(out["dx"]), _ptr(out["dw"]), _ptr(out["dbias"]), _ptr(out["dz"]),
-                                     _ptr(workspace) if need else None, need,
-                                     ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream))
-    _check(st, "ssm_groupnorm_bwd")
+    new = lambda s, d: torch.empty(s, dtype=d, device=dev)  # noqa: E731
+    out = {"dx": new(shape, dt), "dz": new(shape, dt) if z is not None else None,
+           "dw": new(shape[-1:], torch.float32) if w is not None and need_dw else None,
+           "dbias": new(shape[-1:], torch.float32) if bias is not None and need_dw else None}
+    need = _groupnorm_bytes(size, groups, code, 1)
+    workspace = _workspace(workspace, need, dev)
+    _check(lib().ssm_groupnorm_bwd(*size, groups, code, x.data_ptr(), _addr(w), _addr(bias), _addr(z), silu, dy.data_ptr(),
+                                   mean.data_ptr(), rstd.data_ptr(), out["dx"].data_ptr(), _addr(out["dw"]),
+                                   _addr(out["dbias"]), _addr(out["dz"]), _addr(workspace) if need else None, need,
+                                   _stream(dev)), "ssm_groupnorm_bwd")
     return out
 
 

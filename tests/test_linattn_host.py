@@ -126,14 +126,18 @@ def test_strided_rows():
     """The token stride of a slice of a joint projection, and layouts that have none."""
     import torch
     wide = torch.zeros(2, 5, 3 * 32)
-    dev = wide.device
     s = wide[..., 32:64].unflatten(-1, (4, 8))
-    assert ssm._rows(s, "k", (2, 5), 4, 8, torch.float32, dev) == 96
-    assert ssm._rows(s[:, 0], "k", (2,), 4, 8, torch.float32, dev) == 480
-    assert ssm._rows(s[:1, :1], "k", (1, 1), 4, 8, torch.float32, dev) == 32
+
+    def rows(t, *tokens):
+        return ssm._rows((t.shape, t.stride()), "k", tokens, 4, 8)
+    assert rows(s, 2, 5) == 96
+    assert rows(s[:, 0], 2) == 480
+    assert rows(s[:1, :1], 1, 1) == 32
+    assert rows(s[:0], 0, 5) == 32
+    assert rows(s.contiguous(), 2, 5) == 32
     for bad in (s.transpose(2, 3).contiguous().transpose(2, 3), torch.zeros(2, 4, 5, 8).transpose(1, 2),
                 torch.zeros(5, 2, 4, 8).transpose(0, 1), torch.zeros(1, 1, 4, 8).expand(2, 5, 4, 8)):
         with pytest.raises(ValueError, match="evenly spaced"):
-            ssm._rows(bad, "k", (2, 5), 4, 8, torch.float32, dev)
-    with pytest.raises(TypeError):
-        ssm._rows(s.half(), "k", (2, 5), 4, 8, torch.float32, dev)
+            rows(bad, 2, 5)
+    with pytest.raises(ValueError, match="shape"):
+        rows(s, 2, 4)
