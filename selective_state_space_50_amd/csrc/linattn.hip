@@ -164,7 +164,7 @@ __host__ __device__ constexpr int tile_of(int k, int i) { return i * (i + 1) / 2
 // shares to memory.  The rows after those are loaded into registers meanwhile.
 //
 // STATE: only the segment's own contribution to the state (from zero), into the workspace.
-template <class T, int DK, bool AGE, bool STATE>
+template <class T, int DK, bool AGE, bool STATE, bool VEC, int PF>
 __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
     using G = Tile<T, DK>;
     using O = Op<T>;
@@ -251,58 +251,78 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
         }
     }
 
-    // ---- rows to registers (16 bytes each; zeros outside the operand), registers to LDS
-    uint4 rq[STATE ? 1 : NQ], rk[NQ], rv[NV];
-    auto piece = [&](const T *g, int64_t stride, int64_t t, int col, int cols, bool vec) __attribute__((always_inline)) {
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (t >= end) return u;
-        const T *p = g + dir * t * stride + col;
-        if (vec) {
-            if (col < cols) u = *reinterpret_cast<const uint4 *>(p);
-        } else {
-            struct { T e[VE]; } x;
-#pragma unroll
-            for (int i = 0; i < VE; ++i) x.e[i] = col + i < cols ? p[i] : T(0);
-            u = __builtin_bit_cast(uint4, x);
+    // ---- rows to registers (16 bytes each; zeros outside the operand), registers to LDS.  Row
+    // addresses: a wave-uniform base per chunk and a 32-bit offset per lane; backward in time
+    // the base is the chunk's last row, the lowest address
+    uint4 rq[STATE ? 1 : PF][NQ], rk[PF][NQ], rv[PF][NV];
+    // (VEC: the loads carry no branch, so that the wait for one set leaves the later ones in flight:
+    // addresses are clamped into the segment here, and what lies outside is zeroed on its way to LDS)
+    auto piece = [&](const T *g, int64_t stride, int64_t t0, int row, int col, int cols) __attribute__((always_inline)) {
+        if constexpr (VEC) {
+            t0 = min(t0, end - 1);
+            row = min(row, static_cast<int>(min(end - 1 - t0, static_cast<int64_t>(Q - 1))));
+            col = col < cols ? col : 0;
         }
-        return u;
+        const T *base = g + (a.reverse ? -(t0 + Q - 1) : t0) * stride;
+        const uint32_t off = static_cast<uint32_t>(a.reverse ? Q - 1 - row : row) * static_cast<uint32_t>(stride) + col;
+        const T *p = reinterpret_cast<const T *>(reinterpret_cast<const char *>(base) + static_cast<uint64_t>(off) * sizeof(T));
+        if constexpr (VEC) return *reinterpret_cast<const uint4 *>(p);
+        struct { T e[VE]; } x;
+#pragma unroll
+        for (int i = 0; i < VE; ++i) x.e[i] = t0 + row < end && col + i < cols ? p[i] : T(0);
+        return __builtin_bit_cast(uint4, x);
     };
-    auto load = [&](int64_t t0) __attribute__((always_inline)) {
+    auto within = [&](uint4 u, int64_t t0, int row, int col, int cols) __attribute__((always_inline)) {
+        return !VEC || (t0 + row < end && col < cols) ? u : make_uint4(0, 0, 0, 0);
+    };
+    const int dk = static_cast<int>(a.dk);
+    auto load = [&](int64_t t0, int set) __attribute__((always_inline)) {
 #pragma unroll
         for (int r = 0; r < NQ; ++r) {
             const int s = tid + r * kThreads, row = s / (DK / VE), col = s % (DK / VE) * VE;
-            if constexpr (!STATE) rq[r] = piece(qg, a.q_row, t0 + row, col, static_cast<int>(a.dk), a.q_vec);
-            rk[r] = piece(kg, a.k_row, t0 + row, col, static_cast<int>(a.dk), a.k_vec);
+            if constexpr (!STATE) rq[set][r] = piece(qg, a.q_row, t0, row, col, dk);
+            rk[set][r] = piece(kg, a.k_row, t0, row, col, dk);
         }
 #pragma unroll
         for (int r = 0; r < NV; ++r) {
             const int s = tid + r * kThreads, row = s / (kN / VE), col = s % (kN / VE) * VE;
-            rv[r] = piece(vg, a.v_row, t0 + row, col, ncols, a.v_vec);
+            rv[set][r] = piece(vg, a.v_row, t0, row, col, ncols);
         }
     };
-    auto stage = [&](int buf) __attribute__((always_inline)) {
+    auto stage = [&](int64_t t0, int buf, int set) __attribute__((always_inline)) {
 #pragma unroll
         for (int r = 0; r < NQ; ++r) {
             const int s = tid + r * kThreads, row = s / (DK / VE), col = s % (DK / VE) * VE;
-            if constexpr (!STATE) *reinterpret_cast<uint4 *>(&sm.q[buf][row][col]) = rq[r];
-            *reinterpret_cast<uint4 *>(&sm.k[buf][row][col]) = rk[r];
+            if constexpr (!STATE) *reinterpret_cast<uint4 *>(&sm.q[buf][row][col]) = within(rq[set][r], t0, row, col, dk);
+            *reinterpret_cast<uint4 *>(&sm.k[buf][row][col]) = within(rk[set][r], t0, row, col, dk);
         }
 #pragma unroll
         for (int r = 0; r < NV; ++r) {
             const int s = tid + r * kThreads, row = s / (kN / VE), col = s % (kN / VE) * VE;
-            *reinterpret_cast<uint4 *>(&sm.v[buf][row][col]) = rv[r];
+            *reinterpret_cast<uint4 *>(&sm.v[buf][row][col]) = within(rv[set][r], t0, row, col, ncols);
         }
     };
 
     const Decay full = decay_of(la, static_cast<float>(Q));
     const float s_in = a.s_in, s_rd = a.s_rd, s_wr = a.s_wr;
     float age = 0.0f;
-    int buf = 0;
-    load(first);
-    stage(0);
-    load(first + Q);
+#pragma unroll
+    for (int p = 0; p < PF; ++p)
+        if (first < end) load(first + p * Q, p);
+    if (first < end) {
+        stage(first, 0, 0);
+        load(first + PF * Q, 0);
+    }
     __syncthreads();
-    for (int64_t t0 = first; t0 < end; t0 += Q) {
+    for (int64_t t1 = first; t1 < end; t1 += PF * Q)
+#pragma unroll
+    for (int set = 0; set < PF; ++set) {
+        // chunk (t1 - first) / Q + set, staged in LDS; its successor's rows are in register set (set + 1) % PF
+        const int64_t t0 = t1 + set * Q;
+        if (set > 0 && t0 >= end) break;
+        constexpr int kB = G::kBufs;
+        static_assert(kB == 1 || PF % 2 == 0, "a chunk's LDS buffer is known at compile time");
+        const int buf = kB == 1 ? 0 : set & 1, nbuf = kB == 1 ? 0 : buf ^ 1;
         const int m = static_cast<int>(min(static_cast<int64_t>(Q), end - t0));
         f4 acc[STATE ? 1 : NB], acca[AGE ? NB : 1];
         if constexpr (!STATE) {
@@ -461,10 +481,9 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
         }
         // ---- the next chunk's rows into LDS, the ones after it into registers
         if constexpr (G::kBufs == 1) __syncthreads();   // this chunk's rows read
-        const int nbuf = G::kBufs == 1 ? 0 : buf ^ 1;
         if (t0 + Q < end) {
-            stage(nbuf);
-            load(t0 + 2 * Q);
+            stage(t0 + Q, nbuf, (set + 1) % PF);
+            load(t0 + (PF + 1) * Q, (set + 1) % PF);
         }
         __syncthreads();   // output shares written, the next chunk staged
         if constexpr (!STATE) {
@@ -501,7 +520,6 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
                 }
             }
         }
-        buf = nbuf;
     }
 
     // ---- the state passed on
@@ -650,7 +668,11 @@ hipError_t launch_one(const LinAttnArgs &a0, hipStream_t s) {
     LinAttnArgs a = a0;
     a.work = a.B * a.H * (STATE ? a.nseg - 1 : a.nseg) * a.ntiles;
     static_assert(sizeof(Smem<T, DK, AGE>) <= kLdsPerCU, "LDS of one CU");
-    hipLaunchKernelGGL((linattn_kernel<T, DK, AGE, STATE>), dim3(static_cast<unsigned>((a.work + 7) / 8 * 8)), dim3(kThreads), 0, s, a);
+    // chunks whose rows are on their way in registers (an even number with two LDS buffers)
+    constexpr int PF = Tile<T, DK>::kBufs == 2 ? (STATE ? 4 : 2) : (STATE && sizeof(T) == 2 ? 2 : 1);
+    const dim3 grid(static_cast<unsigned>((a.work + 7) / 8 * 8));
+    if (a.vec) hipLaunchKernelGGL((linattn_kernel<T, DK, AGE, STATE, true, PF>), grid, dim3(kThreads), 0, s, a);
+    else hipLaunchKernelGGL((linattn_kernel<T, DK, AGE, STATE, false, Tile<T, DK>::kBufs>), grid, dim3(kThreads), 0, s, a);
     return launch_status(s);
 }
 
@@ -681,9 +703,7 @@ hipError_t launch_linattn(const LinAttnArgs &a0, bool bf16, hipStream_t s) {
     LinAttnArgs a = a0;
     const int64_t ve = bf16 ? 8 : 4;
     // 16-byte loads where every row and head starts on 16 bytes (the pointers do)
-    a.q_vec = a.q_row % ve == 0 && a.dk % ve == 0;
-    a.k_vec = a.k_row % ve == 0 && a.dk % ve == 0;
-    a.v_vec = a.v_row % ve == 0 && a.dn % ve == 0;
+    a.vec = a.q_row % ve == 0 && a.k_row % ve == 0 && a.v_row % ve == 0 && a.dk % ve == 0 && a.dn % ve == 0;
     a.y_vec = a.dn % 8 == 0;
     return bf16 ? launch_typed<uint16_t>(a, s) : launch_typed<float>(a, s);
 }

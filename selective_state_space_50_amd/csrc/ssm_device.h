@@ -127,7 +127,7 @@ struct LinAttnArgs {
     float *age_part = nullptr;          // [B, H, nseg, ntiles], or null: not wanted
     // set by the launcher
     int64_t work = 0;
-    int q_vec = 0, k_vec = 0, v_vec = 0, y_vec = 0;
+    int vec = 0, y_vec = 0;
 };
 
 struct GroupNormArgs {

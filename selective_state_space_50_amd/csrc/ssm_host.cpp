@@ -853,7 +853,7 @@ int plan_linattn(const ssm_linattn_shape *s, bool decay_grad, LinAttnPlan *plan)
         return SSM_EUNSUPPORTED;
     }
     // sizes: one launch's workgroups and every index within 64 bits with room to spare
-    if (s->batch > (int64_t(1) << 31) || s->seqlen > (int64_t(1) << 40) || s->nheads > (int64_t(1) << 20) ||
+    if (s->batch > (int64_t(1) << 31) || s->seqlen > (int64_t(1) << 40) || s->nheads > (int64_t(1) << 16) ||
         (s->nheads > 0 && s->batch > (int64_t(1) << 22) / s->nheads) ||
         (s->batch > 0 && s->nheads > 0 && s->seqlen > kMaxElems / (s->batch * s->nheads * SSM_LINATTN_MAX_DIM))) {
         set_error("shape too large for one launch (batch=%lld, seqlen=%lld, nheads=%lld)", (long long)s->batch,
@@ -863,10 +863,15 @@ int plan_linattn(const ssm_linattn_shape *s, bool decay_grad, LinAttnPlan *plan)
     for (int i = 0; i < 3; ++i) {
         const int64_t least = heads[i] * (i < 2 ? s->dk : s->dv);
         *out[i] = rows[i] ? rows[i] : least;
-        if (*out[i] < least || *out[i] > (int64_t(1) << 31)) {
+        if (*out[i] < least) {
             set_error("%c_row=%lld must be 0 or at least the %lld elements of one token", "qkv"[i], (long long)rows[i],
                       (long long)least);
             return SSM_EINVAL;
+        }
+        // (row offsets within a chunk are 32-bit)
+        if (*out[i] > (int64_t(1) << 24)) {
+            set_error("%c_row=%lld: at most %d elements from token to token are supported", "qkv"[i], (long long)*out[i], 1 << 24);
+            return SSM_EUNSUPPORTED;
         }
     }
     if (s->batch == 0 || s->nheads == 0 || s->seqlen == 0) return SSM_OK;

@@ -37,6 +37,7 @@ def fwd(lib, s, q=P(0), y=P(5), h0=P(6), h_last=P(7), lengths=None, ws=None, ws_
     (dict(dv=300), 2, "at most 256"), (dict(q_heads=3), 1, "q_heads"), (dict(k_heads=0), 1, "k_heads"),
     (dict(v_heads=8), 1, "v_heads"), (dict(q_row=255), 1, "q_row"), (dict(v_row=-1), 1, "v_row"),
     (dict(batch=1 << 30), 2, "too large"), (dict(seqlen=1 << 50), 2, "too large"),
+    (dict(k_row=(1 << 24) + 1), 2, "k_row"), (dict(nheads=1 << 17, q_heads=1, k_heads=1, v_heads=1), 2, "too large"),
 ])
 def test_shape_refusals(lib, bad, status, text):
     s = shape(**bad)
