@@ -18,6 +18,8 @@
 // sweep of dq carries R beside S (AGE) and takes its product with q instead of y's with dy.
 #include "ssm_device.h"
 
+#include <type_traits>
+
 namespace ssm {
 namespace {
 
@@ -62,10 +64,10 @@ struct Op<uint16_t> {
         const u2 r = __builtin_bit_cast(u2, v);
         return f4{bf_lo(r.x), bf_hi(r.x), bf_lo(r.y), bf_hi(r.y)};
     }
-    static __device__ __forceinline__ bool finite4(V4 v) {
-        const u2 r = __builtin_bit_cast(u2, v);
-        return (r.x & 0x7f80u) != 0x7f80u && (r.x & 0x7f800000u) != 0x7f800000u && (r.y & 0x7f80u) != 0x7f80u &&
-               (r.y & 0x7f800000u) != 0x7f800000u;
+    // bits that are set where a piece of eight values holds an infinity or NaN (exponent all ones)
+    static __device__ __forceinline__ uint32_t odd_bits(uint4 u) {
+        auto two = [](uint32_t x) { return (x & 0x7f807f80u) + 0x00800080u; };
+        return (two(u.x) | two(u.y) | two(u.z) | two(u.w)) & 0x80008000u;
     }
     // v with zeros in place of infinities and NaN
     static __device__ __forceinline__ V4 only_finite4(V4 v) {
@@ -110,7 +112,10 @@ struct Op<float> {
     }
     static __device__ __forceinline__ f4 widen4(V4 v) { return v; }
     static __device__ __forceinline__ bool finite1(float v) { return (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u; }
-    static __device__ __forceinline__ bool finite4(V4 v) { return finite1(v[0]) && finite1(v[1]) && finite1(v[2]) && finite1(v[3]); }
+    static __device__ __forceinline__ uint32_t odd_bits(uint4 u) {
+        auto one = [](uint32_t x) { return (x & 0x7f800000u) + 0x00800000u; };
+        return (one(u.x) | one(u.y) | one(u.z) | one(u.w)) & 0x80000000u;
+    }
     static __device__ __forceinline__ V4 only_finite4(V4 v) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = finite1(v[e]) ? v[e] : 0.0f;
@@ -140,17 +145,21 @@ struct Tile {
     static constexpr int kTiles = kBlocks * (kBlocks + 1) / 2;   // 16x16 tiles on and below the diagonal
 };
 
-template <class T, int DK, bool AGE>
+template <class T, int DK, bool AGE, bool STATE>
 struct __align__(16) Smem {
     using G = Tile<T, DK>;
     using V4 = typename Op<T>::V4;
-    T q[G::kBufs][G::kQ][G::kRow];
+    T q[STATE ? 1 : G::kBufs][STATE ? 1 : G::kQ][G::kRow];
     T k[G::kBufs][G::kQ][G::kRow];
     T v[G::kBufs][G::kQ][G::kVRow];
-    V4 p[Op<T>::kNarrow][G::kTiles][64];                        // decayed (q k^T)^T, operand-ready
-    V4 pa[AGE ? Op<T>::kWide : 1][AGE ? G::kTiles : 1][64];     // the same times i - j (AGE)
-    float y[2][G::kQ][kYP];                                     // output shares of the two state halves
-    float pw[2 * G::kQ + 4];                                    // lambda^(n - Q), 0 below n = Q
+    V4 p[Op<T>::kNarrow][STATE ? 1 : G::kTiles][64];                           // decayed (q k^T)^T, operand-ready
+    V4 pa[AGE && !STATE ? Op<T>::kWide : 1][AGE && !STATE ? G::kTiles : 1][64];  // the same times i - j (AGE)
+    float y[STATE ? 1 : 2][STATE ? 1 : G::kQ][kYP];                             // output shares of the two state halves
+    // powers of the decay with the sweep's factors: in-chunk s_in lambda^d (0 for d < 0, offset 16),
+    // readout s_rd lambda^(t + 1 - sh), update s_wr lambda^(m - 1 - j + sh) of a whole chunk and
+    // of the segment's last one (0 past its m rows); AGE: the last two times m - 1 - j
+    float w_in[16 + G::kQ], w_rd[G::kQ], w_up[2][G::kQ], w_age[AGE ? 2 : 1][AGE ? G::kQ : 4];
+    uint32_t odd[2][8];                                         // waves that staged an infinity or NaN of v
 };
 
 __host__ __device__ constexpr int tile_of(int k, int i) { return i * (i + 1) / 2 + k; }
@@ -175,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
     constexpr int VE = 16 / sizeof(T);
     constexpr int NQ = Q * DK / VE / kThreads, NV = Q * kN / VE / kThreads;
     static_assert(NQ >= 1 && NV >= 1, "a thread loads whole 16-byte pieces");
-    __shared__ Smem<T, DK, AGE> sm;
+    __shared__ Smem<T, DK, AGE, STATE> sm;
     const int tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int nb = w & 3, hf = w >> 2, lr = lane & 15, lg = lane >> 4;
@@ -193,10 +202,11 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
     const int64_t h = id % a.H, b = id / a.H;
     const int n0 = nt * kN;
 
-    int64_t Lb = a.L;
-    if (a.lengths) Lb = min(max(static_cast<int64_t>(a.lengths[b]), int64_t(0)), a.L);
-    const int64_t first = seg * a.seg_len, end = min(first + a.seg_len, Lb);
-    if (STATE && first + a.seg_len >= Lb) return;   // no later segment starts from this one's state
+    // (rows are counted in 32 bits, and in scalar registers: the planner's bound on seqlen)
+    const int L = static_cast<int>(a.L), seg_len = static_cast<int>(a.seg_len);
+    const int Lb = a.lengths ? __builtin_amdgcn_readfirstlane(min(max(a.lengths[b], 0), L)) : L;
+    const int first = static_cast<int>(seg) * seg_len, end = min(first + seg_len, Lb);
+    if (STATE && first + seg_len >= Lb) return;   // no later segment starts from this one's state
     const int sh = a.reverse ? 1 : 0;
     const float la = a.log_decay[h];
 
@@ -209,9 +219,9 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
     const int ncols = min(static_cast<int>(a.dn) - n0, kN);
 
     // rows past the sequence's end: zeros (a padded batch)
-    if (!STATE && Lb < a.L) {
-        const int64_t from = max(first, Lb), to = min(first + a.seg_len, a.L);
-        for (int64_t e = tid; e < (to - from) * ncols; e += kThreads) {
+    if (!STATE && Lb < L) {
+        const int from = max(first, Lb), to = min(first + seg_len, L);
+        for (int64_t e = tid; e < static_cast<int64_t>(to - from) * ncols; e += kThreads) {
             const int64_t at = ((b * a.L + from + e / ncols) * a.H + h) * a.dn + n0 + e % ncols;
             if (a.out_f32) static_cast<float *>(a.y)[at] = 0.0f;
             else put(static_cast<T *>(a.y), at, 0.0f);
@@ -222,11 +232,23 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
         return;
     }
 
-    for (int n = tid; n < 2 * Q + 4; n += kThreads) {
-        const Decay d = decay_of(la, static_cast<float>(n - Q));
-        sm.pw[n] = n < Q ? 0.0f : d.hi + d.lo;
+    const float s_in = a.s_in, s_rd = a.s_rd, s_wr = a.s_wr;
+    const int tail = max(end - first, 0) % Q;   // rows of the last chunk, if it is not whole
+    if (tid < 4 * Q) {
+        auto power = [&](int n) { const Decay d = decay_of(la, static_cast<float>(n)); return d.hi + d.lo; };
+        const int t = tid % Q, which = tid / Q;
+        if (which == 0) {
+            sm.w_in[16 + t] = s_in * power(t);
+            if (t < 16) sm.w_in[t] = 0.0f;
+        } else if (which == 1) {
+            sm.w_rd[t] = s_rd * power(t + 1 - sh);
+        } else {
+            const int left = (which == 2 ? Q : tail) - 1 - t;
+            const float x = left >= 0 ? s_wr * power(left + sh) : 0.0f;
+            sm.w_up[which - 2][t] = x;
+            if constexpr (AGE) sm.w_age[which - 2][t] = left >= 0 ? x * static_cast<float>(left) : 0.0f;
+        }
     }
-    const float *pw = sm.pw + Q;
 
     // ---- the wave's part of the state: contraction row 16 t + 4 lg + j of its half, column lr
     f4 S[NT], R[AGE ? NT : 1];
@@ -251,79 +273,105 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
         }
     }
 
-    // ---- rows to registers (16 bytes each; zeros outside the operand), registers to LDS.  Row
-    // addresses: a wave-uniform base per chunk and a 32-bit offset per lane; backward in time
-    // the base is the chunk's last row, the lowest address
+    // ---- rows to registers (16 bytes each), registers to LDS (zeros outside the operand).
+    // VEC: a chunk's loads are the same instructions whatever the chunk, with no branch around
+    // them, so that waiting for one set leaves the later ones in flight.  The last chunk loads
+    // the segment's last Q rows (rows before it among them) and sorts them on the way to LDS; a
+    // sequence shorter than Q rows repeats its last row.  Addresses: a scalar base and a 32-bit
+    // offset per lane; backward in time the base is the last row, the lowest address.
     uint4 rq[STATE ? 1 : PF][NQ], rk[PF][NQ], rv[PF][NV];
-    // (VEC: the loads carry no branch, so that the wait for one set leaves the later ones in flight:
-    // addresses are clamped into the segment here, and what lies outside is zeroed on its way to LDS)
-    auto piece = [&](const T *g, int64_t stride, int64_t t0, int row, int col, int cols) __attribute__((always_inline)) {
-        if constexpr (VEC) {
-            t0 = min(t0, end - 1);
-            row = min(row, static_cast<int>(min(end - 1 - t0, static_cast<int64_t>(Q - 1))));
-            col = col < cols ? col : 0;
-        }
-        const T *base = g + (a.reverse ? -(t0 + Q - 1) : t0) * stride;
-        const uint32_t off = static_cast<uint32_t>(a.reverse ? Q - 1 - row : row) * static_cast<uint32_t>(stride) + col;
-        const T *p = reinterpret_cast<const T *>(reinterpret_cast<const char *>(base) + static_cast<uint64_t>(off) * sizeof(T));
-        if constexpr (VEC) return *reinterpret_cast<const uint4 *>(p);
+    const int dk = static_cast<int>(a.dk);
+    const bool whole_cols = dk == DK && ncols == kN;
+    const int top = min(Q, Lb) - 1, latest = max(end - Q, 0);   // last row of a load, last start of one
+    uint32_t oq[NQ], ok[NQ], ov[NV];
+#pragma unroll
+    for (int r = 0; r < NQ; ++r) {
+        const int s = tid + r * kThreads, row = min(s / (DK / VE), top), c = s % (DK / VE) * VE;
+        const uint32_t at = a.reverse ? top - row : row, col = c < dk ? c : 0;
+        oq[r] = at * static_cast<uint32_t>(a.q_row) + col;
+        ok[r] = at * static_cast<uint32_t>(a.k_row) + col;
+    }
+#pragma unroll
+    for (int r = 0; r < NV; ++r) {
+        const int s = tid + r * kThreads, row = min(s / (kN / VE), top), c = s % (kN / VE) * VE;
+        ov[r] = (a.reverse ? top - row : row) * static_cast<uint32_t>(a.v_row) + (c < ncols ? c : 0);
+    }
+    auto piece = [&](const T *base, uint32_t off) __attribute__((always_inline)) {
+        return *reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(base) + static_cast<uint64_t>(off) * sizeof(T));
+    };
+    // (single elements where rows or heads do not start on 16 bytes)
+    auto piece_of_elements = [&](const T *g, int64_t stride, int t, int col, int cols) __attribute__((always_inline)) {
+        const T *p = g + dir * t * stride + col;
         struct { T e[VE]; } x;
 #pragma unroll
-        for (int i = 0; i < VE; ++i) x.e[i] = t0 + row < end && col + i < cols ? p[i] : T(0);
+        for (int i = 0; i < VE; ++i) x.e[i] = t < end && col + i < cols ? p[i] : T(0);
         return __builtin_bit_cast(uint4, x);
     };
-    auto within = [&](uint4 u, int64_t t0, int row, int col, int cols) __attribute__((always_inline)) {
-        return !VEC || (t0 + row < end && col < cols) ? u : make_uint4(0, 0, 0, 0);
-    };
-    const int dk = static_cast<int>(a.dk);
-    auto load = [&](int64_t t0, int set) __attribute__((always_inline)) {
+    auto load = [&](int t0, int set) __attribute__((always_inline)) {
+        const int64_t at = a.reverse ? -static_cast<int64_t>(min(t0, latest) + top) : min(t0, latest);
 #pragma unroll
         for (int r = 0; r < NQ; ++r) {
             const int s = tid + r * kThreads, row = s / (DK / VE), col = s % (DK / VE) * VE;
-            if constexpr (!STATE) rq[set][r] = piece(qg, a.q_row, t0, row, col, dk);
-            rk[set][r] = piece(kg, a.k_row, t0, row, col, dk);
+            if constexpr (!STATE) rq[set][r] = VEC ? piece(qg + at * a.q_row, oq[r]) : piece_of_elements(qg, a.q_row, t0 + row, col, dk);
+            rk[set][r] = VEC ? piece(kg + at * a.k_row, ok[r]) : piece_of_elements(kg, a.k_row, t0 + row, col, dk);
         }
 #pragma unroll
         for (int r = 0; r < NV; ++r) {
             const int s = tid + r * kThreads, row = s / (kN / VE), col = s % (kN / VE) * VE;
-            rv[set][r] = piece(vg, a.v_row, t0, row, col, ncols);
+            rv[set][r] = VEC ? piece(vg + at * a.v_row, ov[r]) : piece_of_elements(vg, a.v_row, t0 + row, col, ncols);
         }
+        __builtin_amdgcn_sched_barrier(0);   // sets are waited for in the order of their loads
     };
-    auto stage = [&](int64_t t0, int buf, int set) __attribute__((always_inline)) {
+    auto stage_rows = [&](int t0, int buf, int set, auto inside) __attribute__((always_inline)) {
+        constexpr bool IN = decltype(inside)::value || !VEC;
+        // m: the chunk's rows (none past the end: the turn of the last chunk stages zeros); shift: the
+        // loaded rows that come before it, 0 .. Q, whose places the rows behind its end take
+        const int m = max(end - t0, 0), shift = IN || Lb < Q ? 0 : Q - min(m, Q);
+        auto place = [&](int row) { return IN ? row : row >= shift ? row - shift : row - shift + Q; };
+        auto within = [&](uint4 u, int row, int col, int cols) __attribute__((always_inline)) {
+            return IN || (row < m && col < cols) ? u : make_uint4(0, 0, 0, 0);
+        };
 #pragma unroll
         for (int r = 0; r < NQ; ++r) {
-            const int s = tid + r * kThreads, row = s / (DK / VE), col = s % (DK / VE) * VE;
-            if constexpr (!STATE) *reinterpret_cast<uint4 *>(&sm.q[buf][row][col]) = within(rq[set][r], t0, row, col, dk);
-            *reinterpret_cast<uint4 *>(&sm.k[buf][row][col]) = within(rk[set][r], t0, row, col, dk);
+            const int s = tid + r * kThreads, row = place(s / (DK / VE)), col = s % (DK / VE) * VE;
+            if constexpr (!STATE) *reinterpret_cast<uint4 *>(&sm.q[buf][row][col]) = within(rq[set][r], row, col, dk);
+            *reinterpret_cast<uint4 *>(&sm.k[buf][row][col]) = within(rk[set][r], row, col, dk);
         }
+        uint32_t odd = 0;
 #pragma unroll
         for (int r = 0; r < NV; ++r) {
-            const int s = tid + r * kThreads, row = s / (kN / VE), col = s % (kN / VE) * VE;
-            *reinterpret_cast<uint4 *>(&sm.v[buf][row][col]) = within(rv[set][r], t0, row, col, ncols);
+            const int s = tid + r * kThreads, row = place(s / (kN / VE)), col = s % (kN / VE) * VE;
+            const uint4 u = within(rv[set][r], row, col, ncols);
+            *reinterpret_cast<uint4 *>(&sm.v[buf][row][col]) = u;
+            odd |= O::odd_bits(u);
         }
+        if constexpr (!STATE) {
+            const bool any = __ballot(odd != 0) != 0;
+            if (lane == 0) sm.odd[buf][w] = any;
+        }
+    };
+    auto stage = [&](int t0, int buf, int set) __attribute__((always_inline)) {
+        if (t0 + Q <= end && whole_cols) stage_rows(t0, buf, set, std::true_type{});
+        else stage_rows(t0, buf, set, std::false_type{});
     };
 
-    const Decay full = decay_of(la, static_cast<float>(Q));
-    const float s_in = a.s_in, s_rd = a.s_rd, s_wr = a.s_wr;
+    const Decay full = decay_of(la, static_cast<float>(Q)), part = decay_of(la, static_cast<float>(tail));
     float age = 0.0f;
-#pragma unroll
-    for (int p = 0; p < PF; ++p)
-        if (first < end) load(first + p * Q, p);
     if (first < end) {
-        stage(first, 0, 0);
-        load(first + PF * Q, 0);
-    }
-    __syncthreads();
-    for (int64_t t1 = first; t1 < end; t1 += PF * Q)
 #pragma unroll
-    for (int set = 0; set < PF; ++set) {
-        // chunk (t1 - first) / Q + set, staged in LDS; its successor's rows are in register set (set + 1) % PF
-        const int64_t t0 = t1 + set * Q;
-        if (set > 0 && t0 >= end) break;
+    for (int p = 0; p < PF; ++p) load(first + p * Q, p);
+    stage(first, 0, 0);
+    load(first + PF * Q, 0);
+    __syncthreads();
+    // the chunk at row t0, staged in LDS; its successor's rows are in register set (set + 1) % PF
+    auto chunk = [&](int t0, auto which, auto further) __attribute__((always_inline)) {
+        constexpr int set = decltype(which)::value;
+        constexpr bool MORE = decltype(further)::value;   // in the loop: rows are loaded ahead
         constexpr int kB = G::kBufs;
-        static_assert(kB == 1 || PF % 2 == 0, "a chunk's LDS buffer is known at compile time");
+        static_assert(PF == 1 || PF == 2, "one or two sets");
+        static_assert(kB == 1 || PF == 2, "a chunk's LDS buffer is known at compile time");
         const int buf = kB == 1 ? 0 : set & 1, nbuf = kB == 1 ? 0 : buf ^ 1;
-        const int m = static_cast<int>(min(static_cast<int64_t>(Q), end - t0));
+        const int m = min(Q, end - t0);
         f4 acc[STATE ? 1 : NB], acca[AGE ? NB : 1];
         if constexpr (!STATE) {
             // ---- tiles of (q k^T)^T with their decay: lane s = 16 k + 4 lg + j, t = 16 i + lr
@@ -336,7 +384,10 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
                 f4 x;
                 const int d0 = 16 * (i - k) + lr - 4 * lg;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] = d0 - j >= 0 ? g[j] * (s_in * pw[d0 - j]) : 0.0f;
+                for (int j = 0; j < 4; ++j) x[j] = g[j] * sm.w_in[16 + d0 - j];
+                if (i == k)   // rows after the output's: zero whatever q and k hold
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[j] = d0 - j >= 0 ? x[j] : 0.0f;
                 V4 part[O::kNarrow];
                 O::template split<O::kNarrow>(x, part);
 #pragma unroll
@@ -344,7 +395,7 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
                 if constexpr (AGE) {
                     f4 xa;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) xa[j] = d0 - j > 0 ? x[j] * static_cast<float>(d0 - j) : 0.0f;
+                    for (int j = 0; j < 4; ++j) xa[j] = x[j] * static_cast<float>(max(d0 - j, 0));
                     V4 wide[O::kWide];
                     O::template split<O::kWide>(xa, wide);
 #pragma unroll
@@ -372,7 +423,7 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
                     }
                 }
                 const int t = 16 * i + lr;
-                const float e = s_rd * pw[t + 1 - sh];
+                const float e = sm.w_rd[t];
                 acc[i] = off * e;
                 if constexpr (AGE) acca[i] = offa * e + off * (e * static_cast<float>(t + 1));
             }
@@ -384,6 +435,8 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
 #pragma unroll
         for (int j = 0; j < 2 * NJ; ++j) vp[j] = O::column4(&sm.v[buf][0][0], G::kVRow, 16 * j, 16 * nb, lr, lg);
         if constexpr (!STATE) {
+            const uint4 o0 = *reinterpret_cast<const uint4 *>(&sm.odd[buf][0]), o1 = *reinterpret_cast<const uint4 *>(&sm.odd[buf][4]);
+            const bool odd = __builtin_amdgcn_readfirstlane(o0.x | o0.y | o0.z | o0.w | o1.x | o1.y | o1.z | o1.w) != 0;
             // ---- in-chunk product; half 0 takes output blocks 0 and 3, half 1 blocks 1 and 2
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
@@ -392,8 +445,11 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
                     // the diagonal tile's zeros (rows after the output's) must not meet an infinity
                     // or NaN: such values are taken out of the product and added to their own and
                     // later rows only
-                    const bool odd = __ballot(!O::finite4(vp[i])) != 0;
-                    const V4 vd = odd ? O::only_finite4(vp[i]) : vp[i];
+                    V4 vd = vp[i];
+                    if (odd) {
+                        asm volatile("");   // (a branch, not selects: next to no chunk goes here)
+                        vd = O::only_finite4(vd);
+                    }
 #pragma unroll
                     for (int k = 0; k <= i; k += 2) {
                         const bool two = k + 1 <= i;
@@ -440,20 +496,14 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
 
         // ---- state update with the weighted value rows
         {
-            const Decay d = m == Q ? full : decay_of(la, static_cast<float>(m));
+            const Decay d = m == Q ? full : part;
             V4 wp[2 * NJ][O::kWide], ap[AGE ? 2 * NJ : 1][O::kWide];
 #pragma unroll
             for (int j = 0; j < 2 * NJ; ++j) {
                 const f4 x = O::widen4(vp[j]);
-                f4 xw, xa;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int left = m - 1 - (16 * j + 4 * lg + e);   // rows of the chunk after this one
-                    xw[e] = x[e] * (s_wr * pw[left + sh]);
-                    xa[e] = xw[e] * static_cast<float>(left);
-                }
-                O::template split<O::kWide>(xw, wp[j]);
-                if constexpr (AGE) O::template split<O::kWide>(xa, ap[j]);
+                O::template split<O::kWide>(x * *reinterpret_cast<const f4 *>(&sm.w_up[m == Q ? 0 : 1][16 * j + 4 * lg]), wp[j]);
+                if constexpr (AGE)
+                    O::template split<O::kWide>(x * *reinterpret_cast<const f4 *>(&sm.w_age[m == Q ? 0 : 1][16 * j + 4 * lg]), ap[j]);
             }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
@@ -481,10 +531,8 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
         }
         // ---- the next chunk's rows into LDS, the ones after it into registers
         if constexpr (G::kBufs == 1) __syncthreads();   // this chunk's rows read
-        if (t0 + Q < end) {
-            stage(t0 + Q, nbuf, (set + 1) % PF);
-            load(t0 + (PF + 1) * Q, (set + 1) % PF);
-        }
+        stage(t0 + Q, nbuf, (set + 1) % PF);
+        if constexpr (MORE) load(t0 + (PF + 1) * Q, (set + 1) % PF);
         __syncthreads();   // output shares written, the next chunk staged
         if constexpr (!STATE) {
             // ---- the halves' shares added, eight columns of one row per thread
@@ -520,6 +568,16 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
                 }
             }
         }
+    };
+    // whole turns of PF chunks, then the rest (a way out in the middle of a turn would make the
+    // compiler's waits at the top of the loop cover all loads)
+    int t0 = first;
+    for (; t0 + (PF - 1) * Q < end; t0 += PF * Q) {
+        chunk(t0, std::integral_constant<int, 0>{}, std::true_type{});
+        if constexpr (PF > 1) chunk(t0 + Q, std::integral_constant<int, 1 % PF>{}, std::true_type{});
+    }
+    if constexpr (PF > 1)
+        if (t0 < end) chunk(t0, std::integral_constant<int, 0>{}, std::false_type{});
     }
 
     // ---- the state passed on
@@ -667,9 +725,9 @@ template <class T, int DK, bool AGE, bool STATE>
 hipError_t launch_one(const LinAttnArgs &a0, hipStream_t s) {
     LinAttnArgs a = a0;
     a.work = a.B * a.H * (STATE ? a.nseg - 1 : a.nseg) * a.ntiles;
-    static_assert(sizeof(Smem<T, DK, AGE>) <= kLdsPerCU, "LDS of one CU");
-    // chunks whose rows are on their way in registers (an even number with two LDS buffers)
-    constexpr int PF = Tile<T, DK>::kBufs == 2 ? (STATE ? 4 : 2) : (STATE && sizeof(T) == 2 ? 2 : 1);
+    static_assert(sizeof(Smem<T, DK, AGE, STATE>) <= kLdsPerCU, "LDS of one CU");
+    // chunks whose rows are on their way in registers (as many as LDS buffers at least)
+    constexpr int PF = Tile<T, DK>::kBufs == 2 || (STATE && sizeof(T) == 2) ? 2 : 1;
     const dim3 grid(static_cast<unsigned>((a.work + 7) / 8 * 8));
     if (a.vec) hipLaunchKernelGGL((linattn_kernel<T, DK, AGE, STATE, true, PF>), grid, dim3(kThreads), 0, s, a);
     else hipLaunchKernelGGL((linattn_kernel<T, DK, AGE, STATE, false, Tile<T, DK>::kBufs>), grid, dim3(kThreads), 0, s, a);

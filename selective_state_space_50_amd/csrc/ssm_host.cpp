@@ -853,7 +853,7 @@ int plan_linattn(const ssm_linattn_shape *s, bool decay_grad, LinAttnPlan *plan)
         return SSM_EUNSUPPORTED;
     }
     // sizes: one launch's workgroups and every index within 64 bits with room to spare
-    if (s->batch > (int64_t(1) << 31) || s->seqlen > (int64_t(1) << 40) || s->nheads > (int64_t(1) << 16) ||
+    if (s->batch > (int64_t(1) << 31) || s->seqlen > (int64_t(1) << 30) || s->nheads > (int64_t(1) << 16) ||
         (s->nheads > 0 && s->batch > (int64_t(1) << 22) / s->nheads) ||
         (s->batch > 0 && s->nheads > 0 && s->seqlen > kMaxElems / (s->batch * s->nheads * SSM_LINATTN_MAX_DIM))) {
         set_error("shape too large for one launch (batch=%lld, seqlen=%lld, nheads=%lld)", (long long)s->batch,
