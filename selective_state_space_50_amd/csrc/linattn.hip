@@ -31,12 +31,15 @@ typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = 512;   // 8 waves, two per SIMD
 constexpr int kN = 64;          // value columns of one workgroup
-constexpr int kYP = kN + 4;     // padded rows of the fp32 output shares
 
-// Operands of a 16x16 product over K = 32, lane l: row (A) or column (B) l % 16, and eight
-// k in two runs of four: 4 (l / 16) + e and 16 + 4 (l / 16) + e.  That is the order in
-// which two 16x16 results (lane: rows 4 (l / 16) + j, column l % 16) stand side by side, so a
-// result is the next product's operand without any exchange between lanes.
+// Operands of a 16x16 product over K = 32, lane l = 16 lg + lr: row (A) or column (B) lr, and
+// eight k in two runs of four: 4 lg + e and 16 + 4 lg + e.  That is the order in which two
+// 16x16 results (lane: rows 4 lg + j, column lr) stand side by side, so a result is the next
+// product's operand without any exchange between lanes.
+//
+// LDS tiles are unpadded rows of a multiple of 128 bytes; the 16-byte piece c of a row is kept
+// at place c ^ swizzle(row) (within its eight pieces), so that neither reads of one piece of
+// 16 rows nor reads of two pieces of four rows (transposed) meet a bank twice.
 template <class T>
 struct Op;
 
@@ -44,26 +47,51 @@ template <>
 struct Op<uint16_t> {
     using V4 = s4;
     using Frag = s8;
-    static constexpr int kPad = 8;    // LDS row padding (elements): rows 16 bytes apart modulo the banks
     static constexpr int kWide = 3;   // bf16 parts that carry an fp32 value whole
     static constexpr int kNarrow = 2; // and to about 16 bits
+    static constexpr int kRowOffs = 4, kColOffs = 4;
     static __device__ __forceinline__ Frag cat(V4 a, V4 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
     static __device__ __forceinline__ f4 mma(Frag a, Frag b, f4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8, a), __builtin_bit_cast(b8, b), c, 0, 0, 0);
     }
-    static __device__ __forceinline__ V4 ld4(const uint16_t *p) { return *reinterpret_cast<const s4 *>(p); }
-    static __device__ __forceinline__ Frag ld8(const uint16_t *p) { return *reinterpret_cast<const s8 *>(p); }
-    // column c0 + lr of rows r0 + 4 lg .. + 3, by the LDS transpose read: the sixteen lanes of
-    // group lg address those four rows, four lanes of 8 bytes to a row
-    static __device__ __forceinline__ V4 column4(const uint16_t *base, int row, int r0, int c0, int lr, int lg) {
-        const uint16_t *p = base + (r0 + 4 * lg + (lr >> 2)) * row + c0 + 4 * (lr & 3);
-        return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (__attribute__((address_space(3))) s4 *)(const_cast<uint16_t *>(p)));
+    // four rows' places four pieces apart, the next four rows' between them; rows 8 to 15 of
+    // sixteen with their two 8-byte halves of a piece exchanged (reads of 8 bytes take all 16)
+    static __device__ __forceinline__ int swizzle(int row) { return (row & 3) << 1 | (row >> 2 & 1); }
+    static __device__ __forceinline__ void put16(char *tile, int row_bytes, int row, int piece, uint4 u) {
+        char *p = tile + row * row_bytes + ((piece ^ swizzle(row)) << 4);
+        const int flip = row & 8;
+        *reinterpret_cast<u2 *>(p + flip) = u2{u.x, u.y};
+        *reinterpret_cast<u2 *>(p + (8 - flip)) = u2{u.z, u.w};
     }
+    // byte offsets of a lane's operand runs in rows lr (run e of K block c: element c / 2 at [2 (c % 2) + e])
+    static __device__ __forceinline__ int row_off(int i, int lr, int lg, int row_bytes) {
+        return lr * row_bytes + (((2 * i + (lg >> 1)) ^ swizzle(lr)) << 4) + (((lg & 1) ^ (lr >> 3)) << 3);
+    }
+    static __device__ __forceinline__ Frag row(const char *block, const int (&off)[4], int c) {
+        const char *p = block + (c >> 1) * 128;
+        return cat(*reinterpret_cast<const s4 *>(p + off[2 * (c & 1)]), *reinterpret_cast<const s4 *>(p + off[2 * (c & 1) + 1]));
+    }
+    // columns 16 t + lr of rows 4 lg .. + 3 by the LDS transpose read: the sixteen lanes of group lg
+    // address those four rows, four lanes of 8 bytes to a row
+    static __device__ __forceinline__ int col_off(int i, int lr, int lg, int row_bytes) {
+        const int row = 4 * lg + (lr >> 2);
+        return row * row_bytes + (((2 * i + (lr >> 1 & 1)) ^ swizzle(row)) << 4) + (((lr & 1) ^ (lg >> 1)) << 3);
+    }
+    static __device__ __forceinline__ V4 col(const char *block, const int (&off)[4], int t) {
+        return col1(block + (t >> 2) * 128 + off[t & 3]);
+    }
+    static __device__ __forceinline__ V4 col1(const char *p) {
+        return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4 *)(const_cast<char *>(p)));
+    }
+    // one column block of narrow rows (v): its offset is the lane's own
+    static constexpr int kOneCol = 1;
+    static __device__ __forceinline__ int one_off(int, int t, int lr, int lg, int row_bytes) { return col_off(t, lr, lg, row_bytes); }
+    static __device__ __forceinline__ V4 one(const char *block, const int (&off)[1]) { return col1(block + off[0]); }
     static __device__ __forceinline__ f4 widen4(V4 v) {
         const u2 r = __builtin_bit_cast(u2, v);
         return f4{bf_lo(r.x), bf_hi(r.x), bf_lo(r.y), bf_hi(r.y)};
     }
+    static __device__ __forceinline__ float element(V4 v, int j) { return widen_v(static_cast<uint16_t>(v[j])); }
     // bits that are set where a piece of eight values holds an infinity or NaN (exponent all ones)
     static __device__ __forceinline__ uint32_t odd_bits(uint4 u) {
         auto two = [](uint32_t x) { return (x & 0x7f807f80u) + 0x00800080u; };
@@ -91,9 +119,9 @@ template <>
 struct Op<float> {
     using V4 = f4;
     struct Frag { f4 a, b; };
-    static constexpr int kPad = 4;
     static constexpr int kWide = 1;
     static constexpr int kNarrow = 1;
+    static constexpr int kRowOffs = 2, kColOffs = 8;
     static __device__ __forceinline__ Frag cat(V4 a, V4 b) { return Frag{a, b}; }
     // K = 32 as eight products over K = 4 (v_mfma_f32_16x16x4_f32): product e takes element e of
     // every lane, the same k in both operands
@@ -104,13 +132,39 @@ struct Op<float> {
         for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.b[e], b.b[e], c, 0, 0, 0);
         return c;
     }
-    static __device__ __forceinline__ V4 ld4(const float *p) { return *reinterpret_cast<const f4 *>(p); }
-    static __device__ __forceinline__ Frag ld8(const float *p) { return Frag{ld4(p), ld4(p + 4)}; }
-    static __device__ __forceinline__ V4 column4(const float *base, int row, int r0, int c0, int lr, int lg) {
-        const float *p = base + (r0 + 4 * lg) * row + c0 + lr;
-        return f4{p[0], p[row], p[2 * row], p[3 * row]};
+    static __device__ __forceinline__ int swizzle(int row) { return row & 7; }
+    static __device__ __forceinline__ void put16(char *tile, int row_bytes, int row, int piece, uint4 u) {
+        *reinterpret_cast<uint4 *>(tile + row * row_bytes + ((piece ^ swizzle(row)) << 4)) = u;
+    }
+    static __device__ __forceinline__ int row_off(int i, int lr, int lg, int row_bytes) {
+        return lr * row_bytes + (((4 * i + lg) ^ swizzle(lr)) << 4);
+    }
+    static __device__ __forceinline__ Frag row(const char *block, const int (&off)[2], int c) {
+        return Frag{*reinterpret_cast<const f4 *>(block + c * 128 + off[0]), *reinterpret_cast<const f4 *>(block + c * 128 + off[1])};
+    }
+    // (four loads, one per row)
+    static __device__ __forceinline__ int col_off(int i, int lr, int lg, int row_bytes) {
+        const int row = 4 * lg + (i & 3);
+        return row * row_bytes + (((4 * (i >> 2) + (lr >> 2)) ^ swizzle(row)) << 4) + ((lr & 3) << 2);
+    }
+    static __device__ __forceinline__ V4 col(const char *block, const int (&off)[8], int t) {
+        f4 v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const float *>(block + (t >> 1) * 128 + off[4 * (t & 1) + j]);
+        return v;
+    }
+    static constexpr int kOneCol = 4;
+    static __device__ __forceinline__ int one_off(int j, int t, int lr, int lg, int row_bytes) {
+        return col_off(4 * (t & 1) + j, lr, lg, row_bytes) + (t >> 1) * 128;
+    }
+    static __device__ __forceinline__ V4 one(const char *block, const int (&off)[4]) {
+        f4 v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const float *>(block + off[j]);
+        return v;
     }
     static __device__ __forceinline__ f4 widen4(V4 v) { return v; }
+    static __device__ __forceinline__ float element(V4 v, int j) { return v[j]; }
     static __device__ __forceinline__ bool finite1(float v) { return (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u; }
     static __device__ __forceinline__ uint32_t odd_bits(uint4 u) {
         auto one = [](uint32_t x) { return (x & 0x7f800000u) + 0x00800000u; };
@@ -140,478 +194,610 @@ struct Tile {
     // fp32 at 256 contraction columns: 32 rows to a chunk, so that q and k fit
     static constexpr int kQ = (sizeof(T) == 4 && DK == 256) ? 32 : 64;
     static constexpr int kBufs = (sizeof(T) == 2 && DK <= 128) ? 2 : 1;
-    static constexpr int kRow = DK + Op<T>::kPad, kVRow = kN + Op<T>::kPad;
+    static constexpr int kRow = DK * sizeof(T), kVRow = kN * sizeof(T);   // bytes
     static constexpr int kBlocks = kQ / 16;
     static constexpr int kTiles = kBlocks * (kBlocks + 1) / 2;   // 16x16 tiles on and below the diagonal
 };
 
-template <class T, int DK, bool AGE, bool STATE>
-struct __align__(16) Smem {
-    using G = Tile<T, DK>;
-    using V4 = typename Op<T>::V4;
-    T q[STATE ? 1 : G::kBufs][STATE ? 1 : G::kQ][G::kRow];
-    T k[G::kBufs][G::kQ][G::kRow];
-    T v[G::kBufs][G::kQ][G::kVRow];
-    V4 p[Op<T>::kNarrow][STATE ? 1 : G::kTiles][64];                           // decayed (q k^T)^T, operand-ready
-    V4 pa[AGE && !STATE ? Op<T>::kWide : 1][AGE && !STATE ? G::kTiles : 1][64];  // the same times i - j (AGE)
-    float y[STATE ? 1 : 2][STATE ? 1 : G::kQ][kYP];                             // output shares of the two state halves
-    // powers of the decay with the sweep's factors: in-chunk s_in lambda^d (0 for d < 0, offset 16),
-    // readout s_rd lambda^(t + 1 - sh), update s_wr lambda^(m - 1 - j + sh) of a whole chunk and
-    // of the segment's last one (0 past its m rows); AGE: the last two times m - 1 - j
-    float w_in[16 + G::kQ], w_rd[G::kQ], w_up[2][G::kQ], w_age[AGE ? 2 : 1][AGE ? G::kQ : 4];
-    uint32_t odd[2][8];                                         // waves that staged an infinity or NaN of v
-};
-
 __host__ __device__ constexpr int tile_of(int k, int i) { return i * (i + 1) / 2 + k; }
 
-// One workgroup: the value columns [64 nt, 64 nt + 64) of one (b, h), one segment of the
-// sequence.  Wave w owns value columns 16 (w % 4) .. + 15 and half w / 4 of the contraction
-// columns: its part of the state stays in registers from chunk to chunk.  Per chunk: the
-// tiles of q k^T (shared out over the waves) and each wave's share of the carried state's
-// readout, a barrier, the in-chunk product (output blocks shared out between the halves),
-// the state update and the next chunk's rows into LDS, a barrier, and the sum of the halves'
-// shares to memory.  The rows after those are loaded into registers meanwhile.
-//
-// STATE: only the segment's own contribution to the state (from zero), into the workspace.
-template <class T, int DK, bool AGE, bool STATE, bool VEC, int PF>
-__global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
+// What one workgroup works on: value columns n0 .. n0 + ncols of one (b, h), rows [first, end) of
+// the sequence.  Rows are counted in the sweep's direction (row t is token t, or token Lb - 1 - t),
+// in 32 bits (the planner's bound on seqlen) and scalar registers.
+template <class T>
+struct Part {
+    int64_t b, h, seg;
+    int nt, n0, ncols, Lb, first, end, seg_len;
+    int64_t origin, dir;
+    const T *q, *k, *v;   // row 0
+
+    // workgroup -> (b, h, segment, column tile): the hardware deals workgroups to the 8 XCDs in
+    // turn; the column tiles of one segment read the same q and k and go to one XCD
+    __device__ __forceinline__ bool set(const LinAttnArgs &a, int64_t segs) {
+        const int64_t per = (a.work + 7) / 8;
+        int64_t id = static_cast<int64_t>(blockIdx.x) % 8 * per + blockIdx.x / 8;
+        if (id >= a.work) return false;
+        nt = static_cast<int>(id % a.ntiles);
+        id /= a.ntiles;
+        seg = id % segs;
+        id /= segs;
+        h = id % a.H;
+        b = id / a.H;
+        n0 = nt * kN;
+        ncols = min(static_cast<int>(a.dn) - n0, kN);
+        const int L = static_cast<int>(a.L);
+        Lb = a.lengths ? __builtin_amdgcn_readfirstlane(min(max(a.lengths[b], 0), L)) : L;
+        seg_len = static_cast<int>(a.seg_len);
+        first = static_cast<int>(seg) * seg_len;
+        end = min(first + seg_len, Lb);
+        origin = a.reverse ? Lb - 1 : 0;
+        dir = a.reverse ? -1 : 1;
+        q = static_cast<const T *>(a.q) + (b * a.L + origin) * a.q_row + (h / (a.H / a.q_heads)) * a.dk;
+        k = static_cast<const T *>(a.k) + (b * a.L + origin) * a.k_row + (h / (a.H / a.k_heads)) * a.dk;
+        v = static_cast<const T *>(a.v) + (b * a.L + origin) * a.v_row + (h / (a.H / a.v_heads)) * a.dn + n0;
+        return true;
+    }
+};
+
+// Rows to registers (16 bytes each), registers to LDS (zeros outside the operand), by THREADS
+// threads.  VEC: a chunk's loads are the same instructions whatever the chunk, with no branch
+// around them, so that waiting for one set leaves the later ones in flight.  The last chunk loads
+// the segment's last Q rows (rows before it among them) and sorts them on the way to LDS; a
+// sequence shorter than Q rows repeats its last row.  Addresses: a scalar base and a 32-bit
+// offset per lane; backward in time the base is the last row, the lowest address.
+template <class T, int DK, int THREADS, bool WITH_Q, bool VEC>
+struct Rows {
     using G = Tile<T, DK>;
-    using O = Op<T>;
-    using V4 = typename O::V4;
-    using Frag = typename O::Frag;
-    constexpr int Q = G::kQ, KH = DK / 2, NT = KH / 16, NB = G::kBlocks, NJ = Q / 32;
-    constexpr int NS = AGE ? O::kWide : O::kNarrow;   // parts of the state in its readout
-    constexpr int VE = 16 / sizeof(T);
-    constexpr int NQ = Q * DK / VE / kThreads, NV = Q * kN / VE / kThreads;
+    static constexpr int Q = G::kQ, VE = 16 / sizeof(T), PER = DK / VE, VPER = kN / VE;   // pieces of a row
+    static constexpr int NQ = Q * PER / THREADS, NV = Q * VPER / THREADS;
     static_assert(NQ >= 1 && NV >= 1, "a thread loads whole 16-byte pieces");
-    __shared__ Smem<T, DK, AGE, STATE> sm;
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int nb = w & 3, hf = w >> 2, lr = lane & 15, lg = lane >> 4;
-
-    // workgroup -> (b, h, segment, column tile): the hardware deals workgroups to the 8 XCDs
-    // in turn; the column tiles of one segment read the same q and k and go to one XCD
-    const int64_t per = (a.work + 7) / 8;
-    int64_t id = static_cast<int64_t>(blockIdx.x) % 8 * per + blockIdx.x / 8;
-    if (id >= a.work) return;
-    const int nt = static_cast<int>(id % a.ntiles);
-    id /= a.ntiles;
-    const int64_t segs = STATE ? a.nseg - 1 : a.nseg;
-    const int64_t seg = id % segs;
-    id /= segs;
-    const int64_t h = id % a.H, b = id / a.H;
-    const int n0 = nt * kN;
-
-    // (rows are counted in 32 bits, and in scalar registers: the planner's bound on seqlen)
-    const int L = static_cast<int>(a.L), seg_len = static_cast<int>(a.seg_len);
-    const int Lb = a.lengths ? __builtin_amdgcn_readfirstlane(min(max(a.lengths[b], 0), L)) : L;
-    const int first = static_cast<int>(seg) * seg_len, end = min(first + seg_len, Lb);
-    if (STATE && first + seg_len >= Lb) return;   // no later segment starts from this one's state
-    const int sh = a.reverse ? 1 : 0;
-    const float la = a.log_decay[h];
-
-    // rows are counted in the sweep's direction: row t is token t, or token Lb - 1 - t
-    const int64_t origin = a.reverse ? Lb - 1 : 0;
-    const int64_t dir = a.reverse ? -1 : 1;
-    const T *qg = static_cast<const T *>(a.q) + (b * a.L + origin) * a.q_row + (h / (a.H / a.q_heads)) * a.dk;
-    const T *kg = static_cast<const T *>(a.k) + (b * a.L + origin) * a.k_row + (h / (a.H / a.k_heads)) * a.dk;
-    const T *vg = static_cast<const T *>(a.v) + (b * a.L + origin) * a.v_row + (h / (a.H / a.v_heads)) * a.dn + n0;
-    const int ncols = min(static_cast<int>(a.dn) - n0, kN);
-
-    // rows past the sequence's end: zeros (a padded batch)
-    if (!STATE && Lb < L) {
-        const int from = max(first, Lb), to = min(first + seg_len, L);
-        for (int64_t e = tid; e < static_cast<int64_t>(to - from) * ncols; e += kThreads) {
-            const int64_t at = ((b * a.L + from + e / ncols) * a.H + h) * a.dn + n0 + e % ncols;
-            if (a.out_f32) static_cast<float *>(a.y)[at] = 0.0f;
-            else put(static_cast<T *>(a.y), at, 0.0f);
-        }
-    }
-    if (!STATE && first >= Lb && !(Lb == 0 && seg == 0)) {
-        if (AGE && tid == 0) a.age_part[((b * a.H + h) * a.nseg + seg) * a.ntiles + nt] = 0.0f;
-        return;
-    }
-
-    const float s_in = a.s_in, s_rd = a.s_rd, s_wr = a.s_wr;
-    const int tail = max(end - first, 0) % Q;   // rows of the last chunk, if it is not whole
-    if (tid < 4 * Q) {
-        auto power = [&](int n) { const Decay d = decay_of(la, static_cast<float>(n)); return d.hi + d.lo; };
-        const int t = tid % Q, which = tid / Q;
-        if (which == 0) {
-            sm.w_in[16 + t] = s_in * power(t);
-            if (t < 16) sm.w_in[t] = 0.0f;
-        } else if (which == 1) {
-            sm.w_rd[t] = s_rd * power(t + 1 - sh);
-        } else {
-            const int left = (which == 2 ? Q : tail) - 1 - t;
-            const float x = left >= 0 ? s_wr * power(left + sh) : 0.0f;
-            sm.w_up[which - 2][t] = x;
-            if constexpr (AGE) sm.w_age[which - 2][t] = left >= 0 ? x * static_cast<float>(left) : 0.0f;
-        }
-    }
-
-    // ---- the wave's part of the state: contraction row 16 t + 4 lg + j of its half, column lr
-    f4 S[NT], R[AGE ? NT : 1];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int kk = hf * KH + 16 * t + 4 * lg + j, n = n0 + 16 * nb + lr;
-            const bool in = kk < a.dk && n < a.dn;
-            float s0 = 0.0f, r0 = 0.0f;
-            if (!STATE && in) {
-                if (seg > 0) {
-                    const int64_t at = (((b * a.H + h) * (a.nseg - 1) + seg - 1) * a.dk + kk) * a.dn + n;
-                    s0 = a.ws_S[at];
-                    if constexpr (AGE) r0 = a.ws_R[at];
-                } else if (a.h0) {
-                    s0 = a.h0[(b * a.H + h) * a.dk * a.dn + kk * a.h_sr + n * a.h_sc];
-                }
-            }
-            S[t][j] = s0;
-            if constexpr (AGE) R[t][j] = r0;
-        }
-    }
-
-    // ---- rows to registers (16 bytes each), registers to LDS (zeros outside the operand).
-    // VEC: a chunk's loads are the same instructions whatever the chunk, with no branch around
-    // them, so that waiting for one set leaves the later ones in flight.  The last chunk loads
-    // the segment's last Q rows (rows before it among them) and sorts them on the way to LDS; a
-    // sequence shorter than Q rows repeats its last row.  Addresses: a scalar base and a 32-bit
-    // offset per lane; backward in time the base is the last row, the lowest address.
-    uint4 rq[STATE ? 1 : PF][NQ], rk[PF][NQ], rv[PF][NV];
-    const int dk = static_cast<int>(a.dk);
-    const bool whole_cols = dk == DK && ncols == kN;
-    const int top = min(Q, Lb) - 1, latest = max(end - Q, 0);   // last row of a load, last start of one
+    struct Set { uint4 q[WITH_Q ? NQ : 1], k[NQ], v[NV]; };
+    const LinAttnArgs &a;
+    const Part<T> &p;
+    const int tid, dk, top, latest;   // top, latest: last row of a load, last start of one
+    const bool whole_cols;
     uint32_t oq[NQ], ok[NQ], ov[NV];
-#pragma unroll
-    for (int r = 0; r < NQ; ++r) {
-        const int s = tid + r * kThreads, row = min(s / (DK / VE), top), c = s % (DK / VE) * VE;
-        const uint32_t at = a.reverse ? top - row : row, col = c < dk ? c : 0;
-        oq[r] = at * static_cast<uint32_t>(a.q_row) + col;
-        ok[r] = at * static_cast<uint32_t>(a.k_row) + col;
-    }
-#pragma unroll
-    for (int r = 0; r < NV; ++r) {
-        const int s = tid + r * kThreads, row = min(s / (kN / VE), top), c = s % (kN / VE) * VE;
-        ov[r] = (a.reverse ? top - row : row) * static_cast<uint32_t>(a.v_row) + (c < ncols ? c : 0);
-    }
-    auto piece = [&](const T *base, uint32_t off) __attribute__((always_inline)) {
-        return *reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(base) + static_cast<uint64_t>(off) * sizeof(T));
-    };
-    // (single elements where rows or heads do not start on 16 bytes)
-    auto piece_of_elements = [&](const T *g, int64_t stride, int t, int col, int cols) __attribute__((always_inline)) {
-        const T *p = g + dir * t * stride + col;
-        struct { T e[VE]; } x;
-#pragma unroll
-        for (int i = 0; i < VE; ++i) x.e[i] = t < end && col + i < cols ? p[i] : T(0);
-        return __builtin_bit_cast(uint4, x);
-    };
-    auto load = [&](int t0, int set) __attribute__((always_inline)) {
-        const int64_t at = a.reverse ? -static_cast<int64_t>(min(t0, latest) + top) : min(t0, latest);
+
+    __device__ __forceinline__ Rows(const LinAttnArgs &a_, const Part<T> &p_, int tid_)
+        : a(a_), p(p_), tid(tid_), dk(static_cast<int>(a_.dk)), top(min(Q, p_.Lb) - 1), latest(max(p_.end - Q, 0)),
+          whole_cols(a_.dk == DK && p_.ncols == kN) {
 #pragma unroll
         for (int r = 0; r < NQ; ++r) {
-            const int s = tid + r * kThreads, row = s / (DK / VE), col = s % (DK / VE) * VE;
-            if constexpr (!STATE) rq[set][r] = VEC ? piece(qg + at * a.q_row, oq[r]) : piece_of_elements(qg, a.q_row, t0 + row, col, dk);
-            rk[set][r] = VEC ? piece(kg + at * a.k_row, ok[r]) : piece_of_elements(kg, a.k_row, t0 + row, col, dk);
+            const int s = tid + r * THREADS, row = min(s / PER, top), c = s % PER * VE;
+            const uint32_t at = a.reverse ? top - row : row, col = c < dk ? c : 0;
+            oq[r] = at * static_cast<uint32_t>(a.q_row) + col;
+            ok[r] = at * static_cast<uint32_t>(a.k_row) + col;
         }
 #pragma unroll
         for (int r = 0; r < NV; ++r) {
-            const int s = tid + r * kThreads, row = s / (kN / VE), col = s % (kN / VE) * VE;
-            rv[set][r] = VEC ? piece(vg + at * a.v_row, ov[r]) : piece_of_elements(vg, a.v_row, t0 + row, col, ncols);
+            const int s = tid + r * THREADS, row = min(s / VPER, top), c = s % VPER * VE;
+            ov[r] = (a.reverse ? top - row : row) * static_cast<uint32_t>(a.v_row) + (c < p.ncols ? c : 0);
+        }
+    }
+    static __device__ __forceinline__ uint4 piece(const T *base, uint32_t off) {
+        return *reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(base) + static_cast<uint64_t>(off) * sizeof(T));
+    }
+    // (single elements where rows or heads do not start on 16 bytes)
+    __device__ __forceinline__ uint4 elements(const T *g, int64_t stride, int t, int col, int cols) const {
+        const T *at = g + p.dir * t * stride + col;
+        struct { T e[VE]; } x;
+#pragma unroll
+        for (int i = 0; i < VE; ++i) x.e[i] = t < p.end && col + i < cols ? at[i] : T(0);
+        return __builtin_bit_cast(uint4, x);
+    }
+    __device__ __forceinline__ void load(int t0, Set &set) const {
+        const int64_t at = a.reverse ? -static_cast<int64_t>(min(t0, latest) + top) : min(t0, latest);
+#pragma unroll
+        for (int r = 0; r < NQ; ++r) {
+            const int s = tid + r * THREADS, row = s / PER, col = s % PER * VE;
+            if constexpr (WITH_Q) set.q[r] = VEC ? piece(p.q + at * a.q_row, oq[r]) : elements(p.q, a.q_row, t0 + row, col, dk);
+            set.k[r] = VEC ? piece(p.k + at * a.k_row, ok[r]) : elements(p.k, a.k_row, t0 + row, col, dk);
+        }
+#pragma unroll
+        for (int r = 0; r < NV; ++r) {
+            const int s = tid + r * THREADS, row = s / VPER, col = s % VPER * VE;
+            set.v[r] = VEC ? piece(p.v + at * a.v_row, ov[r]) : elements(p.v, a.v_row, t0 + row, col, p.ncols);
         }
         __builtin_amdgcn_sched_barrier(0);   // sets are waited for in the order of their loads
-    };
-    auto stage_rows = [&](int t0, int buf, int set, auto inside) __attribute__((always_inline)) {
-        constexpr bool IN = decltype(inside)::value || !VEC;
+    }
+    // the chunk at row t0 to LDS; whether this thread staged an infinity or NaN of v
+    template <bool INSIDE>
+    __device__ __forceinline__ bool stage_rows(int t0, const Set &set, char *q, char *k, char *v) const {
+        constexpr bool IN = INSIDE || !VEC;
         // m: the chunk's rows (none past the end: the turn of the last chunk stages zeros); shift: the
         // loaded rows that come before it, 0 .. Q, whose places the rows behind its end take
-        const int m = max(end - t0, 0), shift = IN || Lb < Q ? 0 : Q - min(m, Q);
-        auto place = [&](int row) { return IN ? row : row >= shift ? row - shift : row - shift + Q; };
+        const int m = max(p.end - t0, 0), shift = IN || p.Lb < Q ? 0 : Q - min(m, Q);
+        auto place = [&](int row) __attribute__((always_inline)) { return IN ? row : row >= shift ? row - shift : row - shift + Q; };
         auto within = [&](uint4 u, int row, int col, int cols) __attribute__((always_inline)) {
             return IN || (row < m && col < cols) ? u : make_uint4(0, 0, 0, 0);
         };
 #pragma unroll
         for (int r = 0; r < NQ; ++r) {
-            const int s = tid + r * kThreads, row = place(s / (DK / VE)), col = s % (DK / VE) * VE;
-            if constexpr (!STATE) *reinterpret_cast<uint4 *>(&sm.q[buf][row][col]) = within(rq[set][r], row, col, dk);
-            *reinterpret_cast<uint4 *>(&sm.k[buf][row][col]) = within(rk[set][r], row, col, dk);
+            const int s = tid + r * THREADS, row = place(s / PER), c = s % PER;
+            if constexpr (WITH_Q) Op<T>::put16(q, G::kRow, row, c, within(set.q[r], row, c * VE, dk));
+            Op<T>::put16(k, G::kRow, row, c, within(set.k[r], row, c * VE, dk));
         }
         uint32_t odd = 0;
 #pragma unroll
         for (int r = 0; r < NV; ++r) {
-            const int s = tid + r * kThreads, row = place(s / (kN / VE)), col = s % (kN / VE) * VE;
-            const uint4 u = within(rv[set][r], row, col, ncols);
-            *reinterpret_cast<uint4 *>(&sm.v[buf][row][col]) = u;
-            odd |= O::odd_bits(u);
+            const int s = tid + r * THREADS, row = place(s / VPER), c = s % VPER;
+            const uint4 u = within(set.v[r], row, c * VE, p.ncols);
+            Op<T>::put16(v, G::kVRow, row, c, u);
+            odd |= Op<T>::odd_bits(u);
         }
-        if constexpr (!STATE) {
-            const bool any = __ballot(odd != 0) != 0;
-            if (lane == 0) sm.odd[buf][w] = any;
-        }
-    };
-    auto stage = [&](int t0, int buf, int set) __attribute__((always_inline)) {
-        if (t0 + Q <= end && whole_cols) stage_rows(t0, buf, set, std::true_type{});
-        else stage_rows(t0, buf, set, std::false_type{});
-    };
+        return odd != 0;
+    }
+    __device__ __forceinline__ bool stage(int t0, const Set &set, char *q, char *k, char *v) const {
+        return t0 + Q <= p.end && whole_cols ? stage_rows<true>(t0, set, q, k, v) : stage_rows<false>(t0, set, q, k, v);
+    }
+};
 
-    const Decay full = decay_of(la, static_cast<float>(Q)), part = decay_of(la, static_cast<float>(tail));
-    float age = 0.0f;
-    if (first < end) {
+// One chunk's rows take the state of a wave on: S <- lambda^m S + s_wr sum_j lambda^(m-1-j+sh) k_j v_j^T,
+// for contraction rows 16 (TB + t) + 4 lg + j (t < NT) and column lr of its block; AGE: R = dS/da likewise,
+// R <- lambda^m (R + m S) + s_wr sum_j (m-1-j) lambda^(m-1-j) k_j v_j^T.  The row weights go into v, split into
+// as many bf16 parts as carry them whole: a state's error must not grow with the sequence.
+template <class T, int Q, int ROW, int NT, bool AGE, int NR>
+__device__ __forceinline__ void update_state(f4 (&S)[NT], f4 (&R)[NR], int TB, const char *k, const int (&koff)[Op<T>::kColOffs],
+                                             const typename Op<T>::V4 (&vp)[Q / 16], const float *w_up, const float *w_age,
+                                             Decay d, int m, int lg) {
+    using O = Op<T>;
+    constexpr int NJ = Q / 32;
+    typename O::V4 wp[2 * NJ][O::kWide], ap[AGE ? 2 * NJ : 1][O::kWide];
 #pragma unroll
-    for (int p = 0; p < PF; ++p) load(first + p * Q, p);
-    stage(first, 0, 0);
-    load(first + PF * Q, 0);
-    __syncthreads();
-    // the chunk at row t0, staged in LDS; its successor's rows are in register set (set + 1) % PF
-    auto chunk = [&](int t0, auto which, auto further) __attribute__((always_inline)) {
-        constexpr int set = decltype(which)::value;
-        constexpr bool MORE = decltype(further)::value;   // in the loop: rows are loaded ahead
-        constexpr int kB = G::kBufs;
-        static_assert(PF == 1 || PF == 2, "one or two sets");
-        static_assert(kB == 1 || PF == 2, "a chunk's LDS buffer is known at compile time");
-        const int buf = kB == 1 ? 0 : set & 1, nbuf = kB == 1 ? 0 : buf ^ 1;
-        const int m = min(Q, end - t0);
-        f4 acc[STATE ? 1 : NB], acca[AGE ? NB : 1];
-        if constexpr (!STATE) {
-            // ---- tiles of (q k^T)^T with their decay: lane s = 16 k + 4 lg + j, t = 16 i + lr
-            for (int idx = w; idx < G::kTiles; idx += 8) {
-                const int i = idx < 1 ? 0 : idx < 3 ? 1 : idx < 6 ? 2 : 3, k = idx - i * (i + 1) / 2;
-                f4 g = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < 2 * NJ; ++j) {
+        const f4 x = O::widen4(vp[j]);
+        O::template split<O::kWide>(x * *reinterpret_cast<const f4 *>(w_up + 16 * j + 4 * lg), wp[j]);
+        if constexpr (AGE) O::template split<O::kWide>(x * *reinterpret_cast<const f4 *>(w_age + 16 * j + 4 * lg), ap[j]);
+    }
 #pragma unroll
-                for (int c = 0; c < DK / 32; ++c)
-                    g = O::mma(O::ld8(&sm.k[buf][16 * k + lr][32 * c + 8 * lg]), O::ld8(&sm.q[buf][16 * i + lr][32 * c + 8 * lg]), g);
-                f4 x;
-                const int d0 = 16 * (i - k) + lr - 4 * lg;
+    for (int t = 0; t < NT; ++t) {
+        f4 s = S[t];
+        if constexpr (AGE) {
+            f4 r = R[t] + s * static_cast<float>(m);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] = g[j] * sm.w_in[16 + d0 - j];
-                if (i == k)   // rows after the output's: zero whatever q and k hold
+            for (int j = 0; j < 4; ++j) r[j] = __builtin_fmaf(r[j], d.lo, r[j] * d.hi);
+            R[t] = r;
+        }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) x[j] = d0 - j >= 0 ? x[j] : 0.0f;
-                V4 part[O::kNarrow];
-                O::template split<O::kNarrow>(x, part);
+        for (int j = 0; j < 4; ++j) s[j] = __builtin_fmaf(s[j], d.lo, s[j] * d.hi);
 #pragma unroll
-                for (int n = 0; n < O::kNarrow; ++n) sm.p[n][idx][lane] = part[n];
-                if constexpr (AGE) {
-                    f4 xa;
+        for (int c = 0; c < NJ; ++c) {
+            const auto kf = O::cat(O::col(k + 32 * c * ROW, koff, TB + t), O::col(k + (32 * c + 16) * ROW, koff, TB + t));
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) xa[j] = x[j] * static_cast<float>(max(d0 - j, 0));
-                    V4 wide[O::kWide];
-                    O::template split<O::kWide>(xa, wide);
-#pragma unroll
-                    for (int n = 0; n < O::kWide; ++n) sm.pa[n][idx][lane] = wide[n];
-                }
+            for (int n = 0; n < O::kWide; ++n) {
+                s = O::mma(kf, O::cat(wp[2 * c][n], wp[2 * c + 1][n]), s);
+                if constexpr (AGE) R[t] = O::mma(kf, O::cat(ap[2 * c][n], ap[2 * c + 1][n]), R[t]);
             }
-            // ---- this half's share of the carried state's readout, y^T: lane n = 4 lg + j, t = lr
-            V4 sp[NT][NS], rp[AGE ? NT : 1][NS];
+        }
+        S[t] = s;
+    }
+}
+
+// row weights of the update, of a whole chunk and of the segment's last one (0 past its rows)
+template <int Q, bool AGE>
+__device__ __forceinline__ void fill_update_weights(float (&up)[2][Q], float *age, int i, float la, float s_wr, int sh, int tail) {
+    const int t = i % Q, which = i / Q, left = (which == 0 ? Q : tail) - 1 - t;
+    const Decay d = decay_of(la, static_cast<float>(max(left, 0) + sh));
+    const float x = left >= 0 ? s_wr * (d.hi + d.lo) : 0.0f;
+    up[which][t] = x;
+    if constexpr (AGE) age[which * Q + t] = left > 0 ? x * static_cast<float>(left) : 0.0f;
+}
+
+// ---- the sweep.  One workgroup: 64 value columns of one (b, h), one segment of the sequence,
+// chunk by chunk, in two roles of four waves, one of each on every SIMD:
+//  * state waves hold the state in registers (wave w: value columns 16 w .. + 15, all contraction
+//    columns).  They write the carried state's share of the chunk's output to LDS, pass the
+//    barrier and take the state on;
+//  * chunk waves build the chunk's tiles of q k^T, pass the barrier, take them times v, add the
+//    state waves' share, store the output, and bring the next chunk to LDS (its rows were
+//    loaded into registers one or two chunks ahead).
+// Two barriers a chunk.  A state's rows are never read twice and nothing is computed twice: with
+// all eight waves in one role (half a state each) the weights of v and the sum of two output
+// shares cost a third more VALU instructions and LDS traffic.
+template <class T, int DK, bool AGE>
+struct __align__(16) Smem {
+    using G = Tile<T, DK>;
+    using V4 = typename Op<T>::V4;
+    char q[G::kBufs][G::kQ * G::kRow];
+    char k[G::kBufs][G::kQ * G::kRow];
+    char v[G::kBufs][G::kQ * G::kVRow];
+    V4 p[Op<T>::kNarrow][G::kTiles][64];                        // decayed (q k^T)^T, operand-ready
+    V4 pa[AGE ? Op<T>::kWide : 1][AGE ? G::kTiles : 1][64];     // the same times i - j (AGE)
+    f4 y[4][G::kBlocks][64];                                    // the carried state's share of y^T
+    // powers of the decay with the sweep's factors: in-chunk s_in lambda^d (0 for d < 0, offset 16),
+    // readout s_rd lambda^(t + 1 - sh), update; AGE: the update's times the rows behind it
+    float w_in[16 + G::kQ], w_rd[G::kQ], w_up[2][G::kQ], w_age[AGE ? 2 * G::kQ : 4];
+    uint32_t odd[2][4];                                         // chunk waves that staged an infinity or NaN of v
+    float red[kThreads];
+};
+
+template <class T, int DK, bool AGE, bool VEC>
+__global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
+    using G = Tile<T, DK>;
+    using O = Op<T>;
+    using V4 = typename O::V4;
+    using Frag = typename O::Frag;
+    constexpr int Q = G::kQ, NT = DK / 16, NC = DK / 32, NB = G::kBlocks, kB = G::kBufs;
+    constexpr int NS = AGE ? O::kWide : O::kNarrow;   // parts of the state in its readout
+    __shared__ Smem<T, DK, AGE> sm;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), w = wv & 3;
+    const int lr = lane & 15, lg = lane >> 4;
+    Part<T> p;
+    if (!p.set(a, a.nseg)) return;
+    const int first = p.first, end = p.end;
+
+    // rows past the sequence's end: zeros (a padded batch)
+    if (p.Lb < static_cast<int>(a.L)) {
+        const int from = max(first, p.Lb), to = min(first + p.seg_len, static_cast<int>(a.L));
+        for (int64_t e = tid; e < static_cast<int64_t>(to - from) * p.ncols; e += kThreads) {
+            const int64_t at = ((p.b * a.L + from + e / p.ncols) * a.H + p.h) * a.dn + p.n0 + e % p.ncols;
+            if (a.out_f32) static_cast<float *>(a.y)[at] = 0.0f;
+            else put(static_cast<T *>(a.y), at, 0.0f);
+        }
+    }
+    const int64_t share = ((p.b * a.H + p.h) * a.nseg + p.seg) * a.ntiles + p.nt;
+    if (first >= p.Lb && !(p.Lb == 0 && p.seg == 0)) {
+        if (AGE && tid == 0) a.age_part[share] = 0.0f;
+        return;
+    }
+
+    const int sh = a.reverse ? 1 : 0, tail = max(end - first, 0) % Q;   // tail: rows of the last chunk, if not whole
+    const float la = a.log_decay[p.h];
+    if (tid < 2 * Q) {
+        const int t = tid % Q;
+        const Decay d = decay_of(la, static_cast<float>(tid < Q ? t : t + 1 - sh));
+        if (tid < Q) sm.w_in[16 + t] = a.s_in * (d.hi + d.lo);
+        else sm.w_rd[t] = a.s_rd * (d.hi + d.lo);
+        if (tid < 16) sm.w_in[tid] = 0.0f;
+    } else if (tid < 4 * Q) {
+        fill_update_weights<Q, AGE>(sm.w_up, sm.w_age, tid - 2 * Q, la, a.s_wr, sh, tail);
+    }
+    float age = 0.0f;
+    // factor of the age products: row t of the sequence, value columns 16 w + 4 lg .. + 3 of this tile
+    auto age_dot = [&](int t, const f4 &x) __attribute__((always_inline)) {
+        const T *g = static_cast<const T *>(a.age_w) + (p.b * a.L + t) * a.age_row + (p.h / (a.H / a.age_heads)) * a.dn + p.n0;
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                O::template split<NS>(S[t], sp[t]);
-                if constexpr (AGE) O::template split<NS>(R[t], rp[t]);
+        for (int j = 0; j < 4; ++j) {
+            const int n = 16 * w + 4 * lg + j;
+            if (n < p.ncols) age = __builtin_fmaf(x[j], widen_v(g[n]), age);
+        }
+    };
+    int roff[O::kRowOffs];
+#pragma unroll
+    for (int i = 0; i < O::kRowOffs; ++i) roff[i] = O::row_off(i, lr, lg, G::kRow);
+    int voff[O::kOneCol];
+#pragma unroll
+    for (int i = 0; i < O::kOneCol; ++i) voff[i] = O::one_off(i, w, lr, lg, G::kVRow);
+
+    if (wv < 4) {
+        // ================= state waves =================
+        int koff[O::kColOffs];
+#pragma unroll
+        for (int i = 0; i < O::kColOffs; ++i) koff[i] = O::col_off(i, lr, lg, G::kRow);
+        f4 S[NT], R[AGE ? NT : 1];   // contraction row 16 t + 4 lg + j, column 16 w + lr
+        const int n = p.n0 + 16 * w + lr;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int kk = 16 * t + 4 * lg + j;
+                float s0 = 0.0f, r0 = 0.0f;
+                if (kk < a.dk && n < a.dn) {
+                    if (p.seg > 0) {
+                        const int64_t at = (((p.b * a.H + p.h) * (a.nseg - 1) + p.seg - 1) * a.dk + kk) * a.dn + n;
+                        s0 = a.ws_S[at];
+                        if constexpr (AGE) r0 = a.ws_R[at];
+                    } else if (a.h0) {
+                        s0 = a.h0[(p.b * a.H + p.h) * a.dk * a.dn + kk * a.h_sr + n * a.h_sc];
+                    }
+                }
+                S[t][j] = s0;
+                if constexpr (AGE) R[t][j] = r0;
+            }
+        }
+        const Decay full = decay_of(la, static_cast<float>(Q)), part = decay_of(la, static_cast<float>(tail));
+        __syncthreads();   // chunk 0 staged
+        auto chunk = [&](int t0, auto which) __attribute__((always_inline)) {
+            constexpr int buf = decltype(which)::value;
+            const int m = min(Q, end - t0);
+            // ---- the carried state's readout, y^T: lane column n = 4 lg + j, row t = lr
+            f4 acc[NB], acca[AGE ? NB : 1];
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                acc[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+                if constexpr (AGE) acca[i] = acc[i];
+            }
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                V4 s0[NS], s1[NS], r0[NS], r1[NS];
+                O::template split<NS>(S[2 * c], s0);
+                O::template split<NS>(S[2 * c + 1], s1);
+                if constexpr (AGE) {
+                    O::template split<NS>(R[2 * c], r0);
+                    O::template split<NS>(R[2 * c + 1], r1);
+                }
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    const Frag qf = O::row(&sm.q[buf][16 * i * G::kRow], roff, c);
+#pragma unroll
+                    for (int k = 0; k < NS; ++k) {
+                        acc[i] = O::mma(O::cat(s0[k], s1[k]), qf, acc[i]);
+                        if constexpr (AGE) acca[i] = O::mma(O::cat(r0[k], r1[k]), qf, acca[i]);
+                    }
+                }
             }
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
-                f4 off = {0.0f, 0.0f, 0.0f, 0.0f}, offa = {0.0f, 0.0f, 0.0f, 0.0f};
+                const int t = 16 * i + lr;
+                const float e = sm.w_rd[t];
+                sm.y[w][i][lane] = acc[i] * e;
+                if constexpr (AGE)
+                    if (t < m) age_dot(t0 + t, acca[i] * e + acc[i] * (e * static_cast<float>(t + 1)));
+            }
+            __syncthreads();   // tiles built, shares written
+            V4 vp[Q / 16];
 #pragma unroll
-                for (int c = 0; c < NT / 2; ++c) {
-                    const T *qr = &sm.q[buf][16 * i + lr][hf * KH + 32 * c + 4 * lg];
-                    const Frag qf = O::cat(O::ld4(qr), O::ld4(qr + 16));
+            for (int j = 0; j < Q / 16; ++j) vp[j] = O::one(&sm.v[buf][16 * j * G::kVRow], voff);
+            update_state<T, Q, G::kRow, NT, AGE>(S, R, 0, sm.k[buf], koff, vp, sm.w_up[m == Q ? 0 : 1],
+                                                 sm.w_age + (AGE && m != Q ? Q : 0), m == Q ? full : part, m, lg);
+            if constexpr (kB == 1) __syncthreads();   // this chunk's rows read
+            __syncthreads();   // the next chunk staged
+        };
+        for (int t0 = first; t0 < end; t0 += kB * Q) {
+            chunk(t0, std::integral_constant<int, 0>{});
+            if constexpr (kB > 1)
+                if (t0 + Q < end) chunk(t0 + Q, std::integral_constant<int, 1 % kB>{});
+        }
+
+        // ---- the state passed on
+        if (end == p.Lb) {
+            const int64_t at0 = (p.b * a.H + p.h) * a.dk * a.dn;
 #pragma unroll
-                    for (int n = 0; n < NS; ++n) {
-                        off = O::mma(O::cat(sp[2 * c][n], sp[2 * c + 1][n]), qf, off);
-                        if constexpr (AGE) offa = O::mma(O::cat(rp[2 * c][n], rp[2 * c + 1][n]), qf, offa);
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int kk = 16 * t + 4 * lg + j;
+                    if (kk < a.dk && n < a.dn) {
+                        const int64_t at = at0 + kk * a.h_sr + n * a.h_sc;
+                        if (a.h_last) a.h_last[at] = S[t][j];
+                        // the last state's own gradient sees its age too
+                        if constexpr (AGE)
+                            if (a.age_dh) age = __builtin_fmaf(R[t][j], a.age_dh[at], age);
+                    }
+                }
+        }
+    } else {
+        // ================= chunk waves =================
+        constexpr int PF = kB;   // chunks whose rows are on their way in registers
+        using Loader = Rows<T, DK, kThreads / 2, true, VEC>;
+        const Loader rows(a, p, tid - kThreads / 2);
+        typename Loader::Set set[PF];
+        auto stage = [&](int t0, int buf, const typename Loader::Set &from) __attribute__((always_inline)) {
+            const bool odd = rows.stage(t0, from, sm.q[buf], sm.k[buf], sm.v[buf]);
+            const bool any = __ballot(odd) != 0;
+            if (lane == 0) sm.odd[buf][w] = any;
+        };
+        // the wave's tiles: row block ti with column blocks tk, tk + 1, ..; wave 0 the first tile, too
+        const int ti = NB == 2 ? (w == 0 ? 0 : 1) : w == 0 ? 3 : 4 - w, tk = NB == 2 ? (w == 2 ? 1 : 0) : w == 1 ? 2 : 0;
+        const int tn = NB == 2 ? (w < 3 ? 1 : 0) : w == 2 ? 3 : 2;
+        auto build = [&](const Frag (&qf)[NC], int i, int k, const char *kt) __attribute__((always_inline)) {
+            f4 g = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int c = 0; c < NC; ++c) g = O::mma(O::row(kt + 16 * k * G::kRow, roff, c), qf[c], g);
+            // lane: s = 16 k + 4 lg + j, t = 16 i + lr
+            const int idx = tile_of(k, i), d0 = 16 * (i - k) + lr - 4 * lg;
+            f4 x;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = g[j] * sm.w_in[16 + d0 - j];
+            if (i == k)   // rows after the output's: zero whatever q and k hold
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = d0 - j >= 0 ? x[j] : 0.0f;
+            V4 part[O::kNarrow];
+            O::template split<O::kNarrow>(x, part);
+#pragma unroll
+            for (int n = 0; n < O::kNarrow; ++n) sm.p[n][idx][lane] = part[n];
+            if constexpr (AGE) {
+                f4 xa;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) xa[j] = x[j] * static_cast<float>(max(d0 - j, 0));
+                V4 wide[O::kWide];
+                O::template split<O::kWide>(xa, wide);
+#pragma unroll
+                for (int n = 0; n < O::kWide; ++n) sm.pa[n][idx][lane] = wide[n];
+            }
+        };
+        const int col = 16 * w + 4 * lg;
+        const int64_t ystep = p.dir * a.H * a.dn;
+        const int64_t y0 = ((p.b * a.L + p.origin) * a.H + p.h) * a.dn + p.n0 + col;
+        const bool full_cols = a.y_vec && col + 4 <= p.ncols;
+
+        if (first < end) {
+#pragma unroll
+            for (int i = 0; i < PF; ++i) rows.load(first + i * Q, set[i]);
+            stage(first, 0, set[0]);
+            rows.load(first + PF * Q, set[0]);
+        }
+        __syncthreads();   // chunk 0 staged
+        // the chunk at row t0, staged in LDS; its successor's rows are in set (buf + 1) % PF
+        auto chunk = [&](int t0, auto which, auto further) __attribute__((always_inline)) {
+            constexpr int buf = decltype(which)::value, nbuf = (buf + 1) % kB, next = (buf + 1) % PF;
+            constexpr bool MORE = decltype(further)::value;   // in the loop: rows are loaded ahead
+            const int m = min(Q, end - t0);
+            // ---- tiles of (q k^T)^T with their decay
+            {
+                Frag qf[NC];
+#pragma unroll
+                for (int c = 0; c < NC; ++c) qf[c] = O::row(&sm.q[buf][16 * ti * G::kRow], roff, c);
+                for (int k = tk; k < tk + tn; ++k) build(qf, ti, k, sm.k[buf]);
+                if (NB == 4 && w == 0) {
+#pragma unroll
+                    for (int c = 0; c < NC; ++c) qf[c] = O::row(&sm.q[buf][0], roff, c);
+                    build(qf, 0, 0, sm.k[buf]);
+                }
+            }
+            __syncthreads();   // tiles built, shares written
+            const uint4 o = *reinterpret_cast<const uint4 *>(sm.odd[buf]);
+            const bool odd = __builtin_amdgcn_readfirstlane(o.x | o.y | o.z | o.w) != 0;
+            // ---- the tiles times v, on top of the carried state's share
+            V4 vp[Q / 16];
+#pragma unroll
+            for (int j = 0; j < Q / 16; ++j) vp[j] = O::one(&sm.v[buf][16 * j * G::kVRow], voff);
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                f4 acc = sm.y[w][i][lane], acca = {0.0f, 0.0f, 0.0f, 0.0f};
+                // the diagonal tile's zeros (rows after the output's) must not meet an infinity or
+                // NaN: such values are taken out of the product and added to their own and later
+                // rows only
+                V4 vd = vp[i];
+                if (odd) {
+                    asm volatile("");   // (a branch, not selects: next to no chunk goes here)
+                    vd = O::only_finite4(vd);
+                }
+#pragma unroll
+                for (int k = 0; k <= i; k += 2) {
+                    const bool two = k + 1 <= i;
+                    const V4 zero = {};
+                    const Frag vf = O::cat(k == i ? vd : vp[k], two ? (k + 1 == i ? vd : vp[k + 1]) : zero);
+#pragma unroll
+                    for (int n = 0; n < O::kNarrow; ++n)
+                        acc = O::mma(vf, O::cat(sm.p[n][tile_of(k, i)][lane], two ? sm.p[n][tile_of(k + 1, i)][lane] : zero), acc);
+                    if constexpr (AGE) {
+#pragma unroll
+                        for (int n = 0; n < O::kWide; ++n)
+                            acca = O::mma(vf, O::cat(sm.pa[n][tile_of(k, i)][lane], two ? sm.pa[n][tile_of(k + 1, i)][lane] : zero), acca);
+                    }
+                }
+                if (odd) {
+                    for (int r = 0; r <= lr; ++r) {
+                        const int from = (r >> 2) * 16 + lr;   // the lane that holds row r, column lr of the tile
+                        float pr = 0.0f;
+                        for (int n = 0; n < O::kNarrow; ++n) pr += O::element(sm.p[n][tile_of(i, i)][from], r & 3);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int at = 16 * i + r, c = col + j, piece = c / (16 / static_cast<int>(sizeof(T)));
+                            const int in = c % (16 / static_cast<int>(sizeof(T))) * static_cast<int>(sizeof(T)) ^ (sizeof(T) == 2 ? at & 8 : 0);
+                            const float x = widen_v(*reinterpret_cast<const T *>(&sm.v[buf][at * G::kVRow + ((piece ^ O::swizzle(at)) << 4) + in]));
+                            if ((__float_as_uint(x) & 0x7f800000u) != 0x7f800000u) continue;
+                            acc[j] = __builtin_fmaf(pr, x, acc[j]);
+                            if constexpr (AGE) acca[j] = __builtin_fmaf(pr * static_cast<float>(lr - r), x, acca[j]);
+                        }
                     }
                 }
                 const int t = 16 * i + lr;
-                const float e = sm.w_rd[t];
-                acc[i] = off * e;
-                if constexpr (AGE) acca[i] = offa * e + off * (e * static_cast<float>(t + 1));
-            }
-            __syncthreads();   // tiles built
-        }
-
-        // ---- the value rows as an operand: column 16 nb + lr, rows in the operand order
-        V4 vp[2 * NJ];
+                if (t < m) {
+                    if constexpr (AGE) age_dot(t0 + t, acca);
+                    const int64_t at = y0 + (t0 + t) * ystep;
+                    if (sizeof(T) == 4 || a.out_f32) {
+                        float *y = static_cast<float *>(a.y) + at;
+                        if (full_cols) *reinterpret_cast<f4 *>(y) = acc;
+                        else
 #pragma unroll
-        for (int j = 0; j < 2 * NJ; ++j) vp[j] = O::column4(&sm.v[buf][0][0], G::kVRow, 16 * j, 16 * nb, lr, lg);
-        if constexpr (!STATE) {
-            const uint4 o0 = *reinterpret_cast<const uint4 *>(&sm.odd[buf][0]), o1 = *reinterpret_cast<const uint4 *>(&sm.odd[buf][4]);
-            const bool odd = __builtin_amdgcn_readfirstlane(o0.x | o0.y | o0.z | o0.w | o1.x | o1.y | o1.z | o1.w) != 0;
-            // ---- in-chunk product; half 0 takes output blocks 0 and 3, half 1 blocks 1 and 2
-#pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                const bool mine = NB == 2 ? i == hf : hf == 0 ? (i == 0 || i == 3) : (i == 1 || i == 2);
-                if (mine) {
-                    // the diagonal tile's zeros (rows after the output's) must not meet an infinity
-                    // or NaN: such values are taken out of the product and added to their own and
-                    // later rows only
-                    V4 vd = vp[i];
-                    if (odd) {
-                        asm volatile("");   // (a branch, not selects: next to no chunk goes here)
-                        vd = O::only_finite4(vd);
-                    }
-#pragma unroll
-                    for (int k = 0; k <= i; k += 2) {
-                        const bool two = k + 1 <= i;
-                        const V4 zero = {};
-                        const Frag vf = O::cat(k == i ? vd : vp[k], two ? (k + 1 == i ? vd : vp[k + 1]) : zero);
-#pragma unroll
-                        for (int n = 0; n < O::kNarrow; ++n)
-                            acc[i] = O::mma(vf, O::cat(sm.p[n][tile_of(k, i)][lane], two ? sm.p[n][tile_of(k + 1, i)][lane] : zero), acc[i]);
-                        if constexpr (AGE) {
-#pragma unroll
-                            for (int n = 0; n < O::kWide; ++n)
-                                acca[i] = O::mma(vf, O::cat(sm.pa[n][tile_of(k, i)][lane], two ? sm.pa[n][tile_of(k + 1, i)][lane] : zero), acca[i]);
-                        }
-                    }
-                    if (odd) {
-                        for (int r = 0; r <= lr; ++r) {
-                            const int from = (r >> 2) * 16 + lr;   // the lane that holds row r, column lr of the tile
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const float x = widen_v(sm.v[buf][16 * i + r][16 * nb + 4 * lg + j]);
-                                if ((__float_as_uint(x) & 0x7f800000u) != 0x7f800000u) continue;
-                                float p = 0.0f;
-                                for (int n = 0; n < O::kNarrow; ++n) p += O::widen4(sm.p[n][tile_of(i, i)][from])[r & 3];
-                                acc[i][j] = __builtin_fmaf(p, x, acc[i][j]);
-                                if constexpr (AGE) acca[i][j] = __builtin_fmaf(p * static_cast<float>(lr - r), x, acca[i][j]);
-                            }
-                        }
-                    }
-                }
-                *reinterpret_cast<f4 *>(&sm.y[hf][16 * i + lr][16 * nb + 4 * lg]) = acc[i];
-                if constexpr (AGE) {
-                    const int t = 16 * i + lr;
-                    if (t < m) {
-                        const T *wr = static_cast<const T *>(a.age_w) + (b * a.L + t0 + t) * a.age_row + (h / (a.H / a.age_heads)) * a.dn + n0;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int n = 16 * nb + 4 * lg + j;
-                            if (n < ncols) age = __builtin_fmaf(acca[i][j], widen_v(wr[n]), age);
-                        }
-                    }
-                }
-            }
-        }
-
-        // ---- state update with the weighted value rows
-        {
-            const Decay d = m == Q ? full : part;
-            V4 wp[2 * NJ][O::kWide], ap[AGE ? 2 * NJ : 1][O::kWide];
-#pragma unroll
-            for (int j = 0; j < 2 * NJ; ++j) {
-                const f4 x = O::widen4(vp[j]);
-                O::template split<O::kWide>(x * *reinterpret_cast<const f4 *>(&sm.w_up[m == Q ? 0 : 1][16 * j + 4 * lg]), wp[j]);
-                if constexpr (AGE)
-                    O::template split<O::kWide>(x * *reinterpret_cast<const f4 *>(&sm.w_age[m == Q ? 0 : 1][16 * j + 4 * lg]), ap[j]);
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                f4 s = S[t];
-                if constexpr (AGE) {
-                    f4 r = R[t] + s * static_cast<float>(m);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) r[j] = __builtin_fmaf(r[j], d.lo, r[j] * d.hi);
-                    R[t] = r;
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s[j] = __builtin_fmaf(s[j], d.lo, s[j] * d.hi);
-#pragma unroll
-                for (int c = 0; c < NJ; ++c) {
-                    const Frag kf = O::cat(O::column4(&sm.k[buf][0][0], G::kRow, 32 * c, hf * KH + 16 * t, lr, lg),
-                                           O::column4(&sm.k[buf][0][0], G::kRow, 32 * c + 16, hf * KH + 16 * t, lr, lg));
-#pragma unroll
-                    for (int n = 0; n < O::kWide; ++n) {
-                        s = O::mma(kf, O::cat(wp[2 * c][n], wp[2 * c + 1][n]), s);
-                        if constexpr (AGE) R[t] = O::mma(kf, O::cat(ap[2 * c][n], ap[2 * c + 1][n]), R[t]);
-                    }
-                }
-                S[t] = s;
-            }
-        }
-        // ---- the next chunk's rows into LDS, the ones after it into registers
-        if constexpr (G::kBufs == 1) __syncthreads();   // this chunk's rows read
-        stage(t0 + Q, nbuf, (set + 1) % PF);
-        if constexpr (MORE) load(t0 + (PF + 1) * Q, (set + 1) % PF);
-        __syncthreads();   // output shares written, the next chunk staged
-        if constexpr (!STATE) {
-            // ---- the halves' shares added, eight columns of one row per thread
-            const int row = tid >> 3, col = (tid & 7) * 8;
-            if (row < m) {
-                float o[8];
-                const f4 *p0 = reinterpret_cast<const f4 *>(&sm.y[0][row][col]), *p1 = reinterpret_cast<const f4 *>(&sm.y[1][row][col]);
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) o[4 * e + j] = p0[e][j] + p1[e][j];
-                const int64_t at = ((b * a.L + origin + dir * (t0 + row)) * a.H + h) * a.dn + n0 + col;
-                if (a.out_f32 || sizeof(T) == 4) {
-                    float *y = static_cast<float *>(a.y) + at;
-                    if (a.y_vec && col + 8 <= ncols) {
-                        *reinterpret_cast<f4 *>(y) = f4{o[0], o[1], o[2], o[3]};
-                        *reinterpret_cast<f4 *>(y + 4) = f4{o[4], o[5], o[6], o[7]};
+                            for (int j = 0; j < 4; ++j)
+                                if (col + j < p.ncols) y[j] = acc[j];
                     } else {
+                        uint16_t *y = static_cast<uint16_t *>(a.y) + at;
+                        if (full_cols) *reinterpret_cast<u2 *>(y) = u2{pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3])};
+                        else
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (col + j < ncols) y[j] = o[j];
-                    }
-                } else {
-                    uint16_t *y = static_cast<uint16_t *>(a.y) + at;
-                    if (a.y_vec && col + 8 <= ncols) {
-                        *reinterpret_cast<uint4 *>(y) = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]),
-                                                                   pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (col + j < ncols) y[j] = to_bf16(o[j]);
+                            for (int j = 0; j < 4; ++j)
+                                if (col + j < p.ncols) y[j] = to_bf16(acc[j]);
                     }
                 }
             }
+            // ---- the next chunk's rows into LDS, later ones into registers
+            if constexpr (kB == 1) __syncthreads();   // this chunk's rows read
+            stage(t0 + Q, nbuf, set[next]);
+            if constexpr (MORE) rows.load(t0 + (PF + 1) * Q, set[next]);
+            __syncthreads();   // the next chunk staged
+        };
+        // whole turns of PF chunks, then the rest (a way out in the middle of a turn would make the
+        // compiler's waits at the top of the loop cover all loads)
+        int t0 = first;
+        for (; t0 + (PF - 1) * Q < end; t0 += PF * Q) {
+            chunk(t0, std::integral_constant<int, 0>{}, std::true_type{});
+            if constexpr (PF > 1) chunk(t0 + Q, std::integral_constant<int, 1 % PF>{}, std::true_type{});
         }
+        if constexpr (PF > 1)
+            if (t0 < end) chunk(t0, std::integral_constant<int, 0>{}, std::false_type{});
+    }
+    if constexpr (AGE) {
+        // the workgroup's share of dlog_decay, summed in a fixed order
+        sm.red[tid] = age;
+        __syncthreads();
+        for (int o = kThreads / 2; o > 0; o >>= 1) {
+            if (tid < o) sm.red[tid] += sm.red[tid + o];
+            __syncthreads();
+        }
+        if (tid == 0) a.age_part[share] = sm.red[0];
+    }
+}
+
+// ---- the segments' own contributions to the state (from zero), into the workspace: eight waves,
+// wave w value columns 16 (w % 4) .. + 15 and half w / 4 of the contraction columns
+template <class T, int DK, bool AGE, bool VEC>
+__global__ void __launch_bounds__(kThreads) linattn_state_kernel(LinAttnArgs a) {
+    using G = Tile<T, DK>;
+    using O = Op<T>;
+    constexpr int Q = G::kQ, NT = DK / 32;
+    __shared__ __align__(16) char sk[2][Q * G::kRow], sv[2][Q * G::kVRow];
+    __shared__ __align__(16) float w_up[2][Q], w_age[AGE ? 2 * Q : 4];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), w = wv & 3, hf = wv >> 2;
+    const int lr = lane & 15, lg = lane >> 4;
+    Part<T> p;
+    if (!p.set(a, a.nseg - 1)) return;
+    if (p.first + p.seg_len >= p.Lb) return;   // no later segment starts from this one's state
+    const float la = a.log_decay[p.h];
+    if (tid < 2 * Q) fill_update_weights<Q, AGE>(w_up, w_age, tid, la, a.s_wr, a.reverse ? 1 : 0, 0);
+    int koff[O::kColOffs], voff[O::kOneCol];
+#pragma unroll
+    for (int i = 0; i < O::kColOffs; ++i) koff[i] = O::col_off(i, lr, lg, G::kRow);
+#pragma unroll
+    for (int i = 0; i < O::kOneCol; ++i) voff[i] = O::one_off(i, w, lr, lg, G::kVRow);
+    f4 S[NT], R[AGE ? NT : 1];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        S[t] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+        if constexpr (AGE) R[t] = S[t];
+    }
+    const Decay full = decay_of(la, static_cast<float>(Q));
+    using Loader = Rows<T, DK, kThreads, false, VEC>;
+    const Loader rows(a, p, tid);
+    typename Loader::Set set[2];
+    rows.load(p.first, set[0]);
+    rows.load(p.first + Q, set[1]);
+    rows.stage(p.first, set[0], nullptr, sk[0], sv[0]);
+    rows.load(p.first + 2 * Q, set[0]);
+    __syncthreads();
+    // (these segments are whole: seg_len is a multiple of Q)
+    auto chunk = [&](int t0, auto which, auto further) __attribute__((always_inline)) {
+        constexpr int buf = decltype(which)::value;
+        typename O::V4 vp[Q / 16];
+#pragma unroll
+        for (int j = 0; j < Q / 16; ++j) vp[j] = O::one(&sv[buf][16 * j * G::kVRow], voff);
+        update_state<T, Q, G::kRow, NT, AGE>(S, R, hf * NT, sk[buf], koff, vp, w_up[0], w_age, full, Q, lg);
+        rows.stage(t0 + Q, set[buf ^ 1], nullptr, sk[buf ^ 1], sv[buf ^ 1]);
+        if constexpr (decltype(further)::value) rows.load(t0 + 3 * Q, set[buf ^ 1]);
+        __syncthreads();
     };
-    // whole turns of PF chunks, then the rest (a way out in the middle of a turn would make the
-    // compiler's waits at the top of the loop cover all loads)
-    int t0 = first;
-    for (; t0 + (PF - 1) * Q < end; t0 += PF * Q) {
+    int t0 = p.first;
+    for (; t0 + Q < p.end; t0 += 2 * Q) {
         chunk(t0, std::integral_constant<int, 0>{}, std::true_type{});
-        if constexpr (PF > 1) chunk(t0 + Q, std::integral_constant<int, 1 % PF>{}, std::true_type{});
+        chunk(t0 + Q, std::integral_constant<int, 1>{}, std::true_type{});
     }
-    if constexpr (PF > 1)
-        if (t0 < end) chunk(t0, std::integral_constant<int, 0>{}, std::false_type{});
-    }
-
-    // ---- the state passed on
-    const bool last = !STATE && end == Lb;
-    float *out = STATE ? a.ws_S + ((b * a.H + h) * (a.nseg - 1) + seg) * a.dk * a.dn
-                       : last && a.h_last ? a.h_last + (b * a.H + h) * a.dk * a.dn : nullptr;
-    const int64_t sr = STATE ? a.dn : a.h_sr, sc = STATE ? 1 : a.h_sc;
-    float *outR = STATE && AGE ? a.ws_R + ((b * a.H + h) * (a.nseg - 1) + seg) * a.dk * a.dn : nullptr;
+    if (t0 < p.end) chunk(t0, std::integral_constant<int, 0>{}, std::false_type{});
+    const int64_t at0 = ((p.b * a.H + p.h) * (a.nseg - 1) + p.seg) * a.dk * a.dn;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int kk = hf * KH + 16 * t + 4 * lg + j, n = n0 + 16 * nb + lr;
+            const int64_t kk = 16 * (hf * NT + t) + 4 * lg + j, n = p.n0 + 16 * w + lr;
             if (kk < a.dk && n < a.dn) {
-                if (out) out[kk * sr + n * sc] = S[t][j];
-                if constexpr (AGE) {
-                    if (outR) outR[kk * sr + n * sc] = R[t][j];
-                    // the last state's own gradient sees its age too
-                    if (last && a.age_dh) age = __builtin_fmaf(R[t][j], a.age_dh[(b * a.H + h) * a.dk * a.dn + kk * a.h_sr + n * a.h_sc], age);
-                }
+                a.ws_S[at0 + kk * a.dn + n] = S[t][j];
+                if constexpr (AGE) a.ws_R[at0 + kk * a.dn + n] = R[t][j];
             }
         }
-    if constexpr (AGE && !STATE) {
-        // the workgroup's share of dlog_decay, summed in a fixed order
-        __syncthreads();
-        float *red = &sm.y[0][0][0];
-        red[tid] = age;
-        __syncthreads();
-        for (int o = kThreads / 2; o > 0; o >>= 1) {
-            if (tid < o) red[tid] += red[tid + o];
-            __syncthreads();
-        }
-        if (tid == 0) a.age_part[((b * a.H + h) * a.nseg + seg) * a.ntiles + nt] = red[0];
-    }
 }
 
 // Own contributions of the segments -> the states that segments 1, 2, ... start from, one
@@ -721,30 +907,29 @@ __global__ void __launch_bounds__(256) linattn_update_kernel(LinAttnArgs a) {
     if (tid < CW && nn < dn) put(static_cast<T *>(a.y), bh * dn + nn, red[0][tid] + red[1][tid] + red[2][tid] + red[3][tid]);
 }
 
-template <class T, int DK, bool AGE, bool STATE>
-hipError_t launch_one(const LinAttnArgs &a0, hipStream_t s) {
-    LinAttnArgs a = a0;
-    a.work = a.B * a.H * (STATE ? a.nseg - 1 : a.nseg) * a.ntiles;
-    static_assert(sizeof(Smem<T, DK, AGE, STATE>) <= kLdsPerCU, "LDS of one CU");
-    // chunks whose rows are on their way in registers (as many as LDS buffers at least)
-    constexpr int PF = Tile<T, DK>::kBufs == 2 || (STATE && sizeof(T) == 2) ? 2 : 1;
-    const dim3 grid(static_cast<unsigned>((a.work + 7) / 8 * 8));
-    if (a.vec) hipLaunchKernelGGL((linattn_kernel<T, DK, AGE, STATE, true, PF>), grid, dim3(kThreads), 0, s, a);
-    else hipLaunchKernelGGL((linattn_kernel<T, DK, AGE, STATE, false, Tile<T, DK>::kBufs>), grid, dim3(kThreads), 0, s, a);
-    return launch_status(s);
-}
-
 template <class T, int DK, bool AGE>
-hipError_t launch_sweep(const LinAttnArgs &a, hipStream_t s) {
+hipError_t launch_sweep(const LinAttnArgs &a0, hipStream_t s) {
+    LinAttnArgs a = a0;
+    static_assert(sizeof(Smem<T, DK, AGE>) <= kLdsPerCU, "LDS of one CU");
+    auto grid = [&](int64_t segs) {
+        a.work = a.B * a.H * segs * a.ntiles;
+        return dim3(static_cast<unsigned>((a.work + 7) / 8 * 8));
+    };
     if (a.nseg > 1) {
-        hipError_t e = launch_one<T, DK, AGE, true>(a, s);
+        const dim3 g = grid(a.nseg - 1);
+        if (a.vec) hipLaunchKernelGGL((linattn_state_kernel<T, DK, AGE, true>), g, dim3(kThreads), 0, s, a);
+        else hipLaunchKernelGGL((linattn_state_kernel<T, DK, AGE, false>), g, dim3(kThreads), 0, s, a);
+        hipError_t e = launch_status(s);
         if (e != hipSuccess) return e;
         const int64_t n = a.B * a.H * a.dk * a.dn;
         hipLaunchKernelGGL(linattn_combine_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, s, a);
         e = launch_status(s);
         if (e != hipSuccess) return e;
     }
-    return launch_one<T, DK, AGE, false>(a, s);
+    const dim3 g = grid(a.nseg);
+    if (a.vec) hipLaunchKernelGGL((linattn_kernel<T, DK, AGE, true>), g, dim3(kThreads), 0, s, a);
+    else hipLaunchKernelGGL((linattn_kernel<T, DK, AGE, false>), g, dim3(kThreads), 0, s, a);
+    return launch_status(s);
 }
 
 template <class T>
@@ -762,7 +947,7 @@ hipError_t launch_linattn(const LinAttnArgs &a0, bool bf16, hipStream_t s) {
     const int64_t ve = bf16 ? 8 : 4;
     // 16-byte loads where every row and head starts on 16 bytes (the pointers do)
     a.vec = a.q_row % ve == 0 && a.k_row % ve == 0 && a.v_row % ve == 0 && a.dk % ve == 0 && a.dn % ve == 0;
-    a.y_vec = a.dn % 8 == 0;
+    a.y_vec = a.dn % 4 == 0;
     return bf16 ? launch_typed<uint16_t>(a, s) : launch_typed<float>(a, s);
 }
 
