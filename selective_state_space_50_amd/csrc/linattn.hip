@@ -370,6 +370,7 @@ __device__ __forceinline__ void update_state(f4 (&S)[NT], f4 (&R)[NR], int TB, c
             }
         }
         S[t] = s;
+        if (t % 2 == 1) __builtin_amdgcn_sched_barrier(0);
     }
 }
 
@@ -389,9 +390,9 @@ __device__ __forceinline__ void fill_update_weights(float (&up)[2][Q], float *ag
 //    columns).  They write the carried state's share of the chunk's output to LDS, pass the
 //    barrier and take the state on;
 //  * chunk waves build the chunk's tiles of q k^T, pass the barrier, take them times v, add the
-//    state waves' share, store the output, and bring the next chunk to LDS (its rows were
-//    loaded into registers one or two chunks ahead).
-// Two barriers a chunk.  A state's rows are never read twice and nothing is computed twice: with
+//    state waves' share and store the output.
+// All waves bring the next chunk to LDS, whose rows they loaded into registers one or two chunks
+// ahead.  Two barriers a chunk.  A state's rows are never read twice and nothing is computed twice: with
 // all eight waves in one role (half a state each) the weights of v and the sum of two output
 // shares cost a third more VALU instructions and LDS traffic.
 template <class T, int DK, bool AGE>
@@ -407,7 +408,7 @@ struct __align__(16) Smem {
     // powers of the decay with the sweep's factors: in-chunk s_in lambda^d (0 for d < 0, offset 16),
     // readout s_rd lambda^(t + 1 - sh), update; AGE: the update's times the rows behind it
     float w_in[16 + G::kQ], w_rd[G::kQ], w_up[2][G::kQ], w_age[AGE ? 2 * G::kQ : 4];
-    uint32_t odd[2][4];                                         // chunk waves that staged an infinity or NaN of v
+    uint32_t odd[2][8];                                         // waves that staged an infinity or NaN of v
     float red[kThreads];
 };
 
@@ -470,6 +471,42 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
 #pragma unroll
     for (int i = 0; i < O::kOneCol; ++i) voff[i] = O::one_off(i, w, lr, lg, G::kVRow);
 
+    // every wave loads and stages an eighth of the rows, PF chunks ahead
+    constexpr int PF = kB;
+    using Loader = Rows<T, DK, kThreads, true, VEC>;
+    const Loader rows(a, p, tid);
+    typename Loader::Set set[PF];
+    auto stage = [&](int t0, int buf, const typename Loader::Set &from) __attribute__((always_inline)) {
+        const bool odd = rows.stage(t0, from, sm.q[buf], sm.k[buf], sm.v[buf]);
+        const bool any = __ballot(odd) != 0;
+        if (lane == 0) sm.odd[buf][wv] = any;
+    };
+    if (first < end) {
+#pragma unroll
+        for (int i = 0; i < PF; ++i) rows.load(first + i * Q, set[i]);
+        stage(first, 0, set[0]);
+        rows.load(first + PF * Q, set[0]);
+    }
+    // chunk by chunk: whole turns of PF chunks, then the rest (a way out in the middle of a turn would
+    // make the compiler's waits at the top of the loop cover all loads).  The chunk at row t0 is in
+    // LDS buffer `which`, its successor's rows in set (which + 1) % PF; further: rows are loaded ahead
+    auto walk = [&](auto chunk) __attribute__((always_inline)) {
+        __syncthreads();   // chunk 0 staged
+        int t0 = first;
+        for (; t0 + (PF - 1) * Q < end; t0 += PF * Q) {
+            chunk(t0, std::integral_constant<int, 0>{}, std::true_type{});
+            if constexpr (PF > 1) chunk(t0 + Q, std::integral_constant<int, 1 % PF>{}, std::true_type{});
+        }
+        if constexpr (PF > 1)
+            if (t0 < end) chunk(t0, std::integral_constant<int, 0>{}, std::false_type{});
+    };
+    auto next_rows = [&](int t0, auto which, auto further) __attribute__((always_inline)) {
+        constexpr int nbuf = (decltype(which)::value + 1) % kB, next = (decltype(which)::value + 1) % PF;
+        if constexpr (kB == 1) __syncthreads();   // this chunk's rows read
+        stage(t0 + Q, nbuf, set[next]);
+        if constexpr (decltype(further)::value) rows.load(t0 + (PF + 1) * Q, set[next]);
+    };
+
     if (wv < 4) {
         // ================= state waves =================
         int koff[O::kColOffs];
@@ -497,8 +534,7 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
             }
         }
         const Decay full = decay_of(la, static_cast<float>(Q)), part = decay_of(la, static_cast<float>(tail));
-        __syncthreads();   // chunk 0 staged
-        auto chunk = [&](int t0, auto which) __attribute__((always_inline)) {
+        walk([&](int t0, auto which, auto further) __attribute__((always_inline)) {
             constexpr int buf = decltype(which)::value;
             const int m = min(Q, end - t0);
             // ---- the carried state's readout, y^T: lane column n = 4 lg + j, row t = lr
@@ -517,6 +553,7 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
                     O::template split<NS>(R[2 * c], r0);
                     O::template split<NS>(R[2 * c + 1], r1);
                 }
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int i = 0; i < NB; ++i) {
                     const Frag qf = O::row(&sm.q[buf][16 * i * G::kRow], roff, c);
@@ -541,14 +578,9 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
             for (int j = 0; j < Q / 16; ++j) vp[j] = O::one(&sm.v[buf][16 * j * G::kVRow], voff);
             update_state<T, Q, G::kRow, NT, AGE>(S, R, 0, sm.k[buf], koff, vp, sm.w_up[m == Q ? 0 : 1],
                                                  sm.w_age + (AGE && m != Q ? Q : 0), m == Q ? full : part, m, lg);
-            if constexpr (kB == 1) __syncthreads();   // this chunk's rows read
+            next_rows(t0, which, further);
             __syncthreads();   // the next chunk staged
-        };
-        for (int t0 = first; t0 < end; t0 += kB * Q) {
-            chunk(t0, std::integral_constant<int, 0>{});
-            if constexpr (kB > 1)
-                if (t0 + Q < end) chunk(t0 + Q, std::integral_constant<int, 1 % kB>{});
-        }
+        });
 
         // ---- the state passed on
         if (end == p.Lb) {
@@ -569,22 +601,34 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
         }
     } else {
         // ================= chunk waves =================
-        constexpr int PF = kB;   // chunks whose rows are on their way in registers
-        using Loader = Rows<T, DK, kThreads / 2, true, VEC>;
-        const Loader rows(a, p, tid - kThreads / 2);
-        typename Loader::Set set[PF];
-        auto stage = [&](int t0, int buf, const typename Loader::Set &from) __attribute__((always_inline)) {
-            const bool odd = rows.stage(t0, from, sm.q[buf], sm.k[buf], sm.v[buf]);
-            const bool any = __ballot(odd) != 0;
-            if (lane == 0) sm.odd[buf][w] = any;
-        };
-        // the wave's tiles: row block ti with column blocks tk, tk + 1, ..; wave 0 the first tile, too
-        const int ti = NB == 2 ? (w == 0 ? 0 : 1) : w == 0 ? 3 : 4 - w, tk = NB == 2 ? (w == 2 ? 1 : 0) : w == 1 ? 2 : 0;
-        const int tn = NB == 2 ? (w < 3 ? 1 : 0) : w == 2 ? 3 : 2;
-        auto build = [&](const Frag (&qf)[NC], int i, int k, const char *kt) __attribute__((always_inline)) {
-            f4 g = {0.0f, 0.0f, 0.0f, 0.0f};
+        // The wave's tiles (row block i, column block k), whose products run side by side: all of column
+        // block w, where the rows reach it, and wave 3 takes the first tile besides its own
+        //   wave 0: (3,0) (2,0) (1,0)   wave 1: (3,1) (2,1) (1,1)   wave 2: (3,2) (2,2)   wave 3: (3,3) (0,0)
+        // and with two blocks: wave 0 (1,0), wave 1 (1,1), wave 2 (0,0).
+        const int k0 = NB == 2 ? min(w, 1) : w, i1 = NB == 2 || w == 3 ? 0 : 2, k1 = NB == 2 || w == 3 ? 0 : w;
+        const bool has0 = NB == 4 || w < 2, has1 = NB == 4 || w == 2, has2 = NB == 4 && w < 2;
+        auto product = [&](f4 (&g)[3], int buf) __attribute__((always_inline)) {
+            const char *qt = sm.q[buf], *kt = sm.k[buf];
 #pragma unroll
-            for (int c = 0; c < NC; ++c) g = O::mma(O::row(kt + 16 * k * G::kRow, roff, c), qf[c], g);
+            for (int x = 0; x < 3; ++x) g[x] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (NB == 4) {
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    const Frag kf = O::row(kt + 16 * k0 * G::kRow, roff, c), k1f = O::row(kt + 16 * k1 * G::kRow, roff, c);
+                    g[0] = O::mma(kf, O::row(qt + 16 * 3 * G::kRow, roff, c), g[0]);
+                    g[1] = O::mma(k1f, O::row(qt + 16 * i1 * G::kRow, roff, c), g[1]);
+                    g[2] = O::mma(kf, O::row(qt + 16 * G::kRow, roff, c), g[2]);   // (waves 2 and 3: not used)
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    if (has0) g[0] = O::mma(O::row(kt + 16 * k0 * G::kRow, roff, c), O::row(qt + 16 * G::kRow, roff, c), g[0]);
+                    if (has1) g[1] = O::mma(O::row(kt, roff, c), O::row(qt, roff, c), g[1]);
+                }
+            }
+        };
+        auto put_tile = [&](const f4 &g, int i, int k) __attribute__((always_inline)) {
             // lane: s = 16 k + 4 lg + j, t = 16 i + lr
             const int idx = tile_of(k, i), d0 = 16 * (i - k) + lr - 4 * lg;
             f4 x;
@@ -612,33 +656,20 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
         const int64_t y0 = ((p.b * a.L + p.origin) * a.H + p.h) * a.dn + p.n0 + col;
         const bool full_cols = a.y_vec && col + 4 <= p.ncols;
 
-        if (first < end) {
-#pragma unroll
-            for (int i = 0; i < PF; ++i) rows.load(first + i * Q, set[i]);
-            stage(first, 0, set[0]);
-            rows.load(first + PF * Q, set[0]);
-        }
-        __syncthreads();   // chunk 0 staged
-        // the chunk at row t0, staged in LDS; its successor's rows are in set (buf + 1) % PF
-        auto chunk = [&](int t0, auto which, auto further) __attribute__((always_inline)) {
-            constexpr int buf = decltype(which)::value, nbuf = (buf + 1) % kB, next = (buf + 1) % PF;
-            constexpr bool MORE = decltype(further)::value;   // in the loop: rows are loaded ahead
+        walk([&](int t0, auto which, auto further) __attribute__((always_inline)) {
+            constexpr int buf = decltype(which)::value;
             const int m = min(Q, end - t0);
             // ---- tiles of (q k^T)^T with their decay
             {
-                Frag qf[NC];
-#pragma unroll
-                for (int c = 0; c < NC; ++c) qf[c] = O::row(&sm.q[buf][16 * ti * G::kRow], roff, c);
-                for (int k = tk; k < tk + tn; ++k) build(qf, ti, k, sm.k[buf]);
-                if (NB == 4 && w == 0) {
-#pragma unroll
-                    for (int c = 0; c < NC; ++c) qf[c] = O::row(&sm.q[buf][0], roff, c);
-                    build(qf, 0, 0, sm.k[buf]);
-                }
+                f4 g[3];
+                product(g, buf);
+                if (has0) put_tile(g[0], NB - 1, k0);
+                if (has1) put_tile(g[1], i1, k1);
+                if (has2) put_tile(g[2], 1, k0);
             }
             __syncthreads();   // tiles built, shares written
-            const uint4 o = *reinterpret_cast<const uint4 *>(sm.odd[buf]);
-            const bool odd = __builtin_amdgcn_readfirstlane(o.x | o.y | o.z | o.w) != 0;
+            const uint4 o0 = *reinterpret_cast<const uint4 *>(&sm.odd[buf][0]), o1 = *reinterpret_cast<const uint4 *>(&sm.odd[buf][4]);
+            const bool odd = __builtin_amdgcn_readfirstlane(o0.x | o0.y | o0.z | o0.w | o1.x | o1.y | o1.z | o1.w) != 0;
             // ---- the tiles times v, on top of the carried state's share
             V4 vp[Q / 16];
 #pragma unroll
@@ -705,21 +736,9 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
                     }
                 }
             }
-            // ---- the next chunk's rows into LDS, later ones into registers
-            if constexpr (kB == 1) __syncthreads();   // this chunk's rows read
-            stage(t0 + Q, nbuf, set[next]);
-            if constexpr (MORE) rows.load(t0 + (PF + 1) * Q, set[next]);
+            next_rows(t0, which, further);
             __syncthreads();   // the next chunk staged
-        };
-        // whole turns of PF chunks, then the rest (a way out in the middle of a turn would make the
-        // compiler's waits at the top of the loop cover all loads)
-        int t0 = first;
-        for (; t0 + (PF - 1) * Q < end; t0 += PF * Q) {
-            chunk(t0, std::integral_constant<int, 0>{}, std::true_type{});
-            if constexpr (PF > 1) chunk(t0 + Q, std::integral_constant<int, 1 % PF>{}, std::true_type{});
-        }
-        if constexpr (PF > 1)
-            if (t0 < end) chunk(t0, std::integral_constant<int, 0>{}, std::false_type{});
+        });
     }
     if constexpr (AGE) {
         // the workgroup's share of dlog_decay, summed in a fixed order
