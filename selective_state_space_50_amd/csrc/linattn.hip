@@ -32,6 +32,20 @@ typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 constexpr int kThreads = 512;   // 8 waves, two per SIMD
 constexpr int kN = 64;          // value columns of one workgroup
 
+// LDS by 32-bit address.  A lane's base address is kept in a register the compiler cannot see
+// through, and everything else about an access is a constant in the instruction: left to itself
+// it keeps a register for every constant, which the sweep has not got.
+using Lds = uint32_t;
+template <class V>
+__device__ __forceinline__ V lds_get(Lds a) { return *(const __attribute__((address_space(3))) V *)(a); }
+template <class V>
+__device__ __forceinline__ void lds_put(Lds a, V v) { *(__attribute__((address_space(3))) V *)(a) = v; }
+__device__ __forceinline__ Lds lds_of(const void *p) { return (Lds)(uintptr_t)((const __attribute__((address_space(3))) char *)p); }
+__device__ __forceinline__ Lds opaque(Lds a) {
+    asm("" : "+v"(a));
+    return a;
+}
+
 // Operands of a 16x16 product over K = 32, lane l = 16 lg + lr: row (A) or column (B) lr, and
 // eight k in two runs of four: 4 lg + e and 16 + 4 lg + e.  That is the order in which two
 // 16x16 results (lane: rows 4 lg + j, column lr) stand side by side, so a result is the next
@@ -57,19 +71,23 @@ struct Op<uint16_t> {
     // four rows' places four pieces apart, the next four rows' between them; rows 8 to 15 of
     // sixteen with their two 8-byte halves of a piece exchanged (reads of 8 bytes take all 16)
     static __device__ __forceinline__ int swizzle(int row) { return (row & 3) << 1 | (row >> 2 & 1); }
-    static __device__ __forceinline__ void put16(char *tile, int row_bytes, int row, int piece, uint4 u) {
-        char *p = tile + row * row_bytes + ((piece ^ swizzle(row)) << 4);
-        const int flip = row & 8;
-        *reinterpret_cast<u2 *>(p + flip) = u2{u.x, u.y};
-        *reinterpret_cast<u2 *>(p + (8 - flip)) = u2{u.z, u.w};
+    // place of a piece: of its first and second half
+    static __device__ __forceinline__ void place16(int row_bytes, int row, int piece, Lds (&at)[2]) {
+        const Lds p = row * row_bytes + ((piece ^ swizzle(row)) << 4);
+        at[0] = p + (row & 8);
+        at[1] = p + (8 - (row & 8));
+    }
+    static __device__ __forceinline__ void put16(const Lds (&at)[2], Lds more, uint4 u) {
+        lds_put(at[0] + more, u2{u.x, u.y});
+        lds_put(at[1] + more, u2{u.z, u.w});
     }
     // byte offsets of a lane's operand runs in rows lr (run e of K block c: element c / 2 at [2 (c % 2) + e])
     static __device__ __forceinline__ int row_off(int i, int lr, int lg, int row_bytes) {
         return lr * row_bytes + (((2 * i + (lg >> 1)) ^ swizzle(lr)) << 4) + (((lg & 1) ^ (lr >> 3)) << 3);
     }
-    static __device__ __forceinline__ Frag row(const char *block, const int (&off)[4], int c) {
-        const char *p = block + (c >> 1) * 128;
-        return cat(*reinterpret_cast<const s4 *>(p + off[2 * (c & 1)]), *reinterpret_cast<const s4 *>(p + off[2 * (c & 1) + 1]));
+    static __device__ __forceinline__ Frag row(Lds block, const Lds (&off)[4], int c) {
+        const Lds p = block + (c >> 1) * 128;
+        return cat(lds_get<s4>(off[2 * (c & 1)] + p), lds_get<s4>(off[2 * (c & 1) + 1] + p));
     }
     // columns 16 t + lr of rows 4 lg .. + 3 by the LDS transpose read: the sixteen lanes of group lg
     // address those four rows, four lanes of 8 bytes to a row
@@ -77,16 +95,16 @@ struct Op<uint16_t> {
         const int row = 4 * lg + (lr >> 2);
         return row * row_bytes + (((2 * i + (lr >> 1 & 1)) ^ swizzle(row)) << 4) + (((lr & 1) ^ (lg >> 1)) << 3);
     }
-    static __device__ __forceinline__ V4 col(const char *block, const int (&off)[4], int t) {
-        return col1(block + (t >> 2) * 128 + off[t & 3]);
+    static __device__ __forceinline__ V4 col(Lds block, const Lds (&off)[4], int t) {
+        return col1(off[t & 3] + block + (t >> 2) * 128);
     }
-    static __device__ __forceinline__ V4 col1(const char *p) {
-        return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4 *)(const_cast<char *>(p)));
+    static __device__ __forceinline__ V4 col1(Lds p) {
+        return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4 *)(p));
     }
     // one column block of narrow rows (v): its offset is the lane's own
     static constexpr int kOneCol = 1;
     static __device__ __forceinline__ int one_off(int, int t, int lr, int lg, int row_bytes) { return col_off(t, lr, lg, row_bytes); }
-    static __device__ __forceinline__ V4 one(const char *block, const int (&off)[1]) { return col1(block + off[0]); }
+    static __device__ __forceinline__ V4 one(Lds block, const Lds (&off)[1]) { return col1(off[0] + block); }
     static __device__ __forceinline__ f4 widen4(V4 v) {
         const u2 r = __builtin_bit_cast(u2, v);
         return f4{bf_lo(r.x), bf_hi(r.x), bf_lo(r.y), bf_hi(r.y)};
@@ -133,34 +151,38 @@ struct Op<float> {
         return c;
     }
     static __device__ __forceinline__ int swizzle(int row) { return row & 7; }
-    static __device__ __forceinline__ void put16(char *tile, int row_bytes, int row, int piece, uint4 u) {
-        *reinterpret_cast<uint4 *>(tile + row * row_bytes + ((piece ^ swizzle(row)) << 4)) = u;
+    static __device__ __forceinline__ void place16(int row_bytes, int row, int piece, Lds (&at)[2]) {
+        at[0] = row * row_bytes + ((piece ^ swizzle(row)) << 4);
+        at[1] = 0;
+    }
+    static __device__ __forceinline__ void put16(const Lds (&at)[2], Lds more, uint4 u) {
+        lds_put(at[0] + more, __builtin_bit_cast(f4, u));
     }
     static __device__ __forceinline__ int row_off(int i, int lr, int lg, int row_bytes) {
         return lr * row_bytes + (((4 * i + lg) ^ swizzle(lr)) << 4);
     }
-    static __device__ __forceinline__ Frag row(const char *block, const int (&off)[2], int c) {
-        return Frag{*reinterpret_cast<const f4 *>(block + c * 128 + off[0]), *reinterpret_cast<const f4 *>(block + c * 128 + off[1])};
+    static __device__ __forceinline__ Frag row(Lds block, const Lds (&off)[2], int c) {
+        return Frag{lds_get<f4>(off[0] + block + c * 128), lds_get<f4>(off[1] + block + c * 128)};
     }
     // (four loads, one per row)
     static __device__ __forceinline__ int col_off(int i, int lr, int lg, int row_bytes) {
         const int row = 4 * lg + (i & 3);
         return row * row_bytes + (((4 * (i >> 2) + (lr >> 2)) ^ swizzle(row)) << 4) + ((lr & 3) << 2);
     }
-    static __device__ __forceinline__ V4 col(const char *block, const int (&off)[8], int t) {
+    static __device__ __forceinline__ V4 col(Lds block, const Lds (&off)[8], int t) {
         f4 v;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const float *>(block + (t >> 1) * 128 + off[4 * (t & 1) + j]);
+        for (int j = 0; j < 4; ++j) v[j] = lds_get<float>(off[4 * (t & 1) + j] + block + (t >> 1) * 128);
         return v;
     }
     static constexpr int kOneCol = 4;
     static __device__ __forceinline__ int one_off(int j, int t, int lr, int lg, int row_bytes) {
         return col_off(4 * (t & 1) + j, lr, lg, row_bytes) + (t >> 1) * 128;
     }
-    static __device__ __forceinline__ V4 one(const char *block, const int (&off)[4]) {
+    static __device__ __forceinline__ V4 one(Lds block, const Lds (&off)[4]) {
         f4 v;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const float *>(block + off[j]);
+        for (int j = 0; j < 4; ++j) v[j] = lds_get<float>(off[j] + block);
         return v;
     }
     static __device__ __forceinline__ f4 widen4(V4 v) { return v; }
@@ -197,6 +219,8 @@ struct Tile {
     static constexpr int kRow = DK * sizeof(T), kVRow = kN * sizeof(T);   // bytes
     static constexpr int kBlocks = kQ / 16;
     static constexpr int kTiles = kBlocks * (kBlocks + 1) / 2;   // 16x16 tiles on and below the diagonal
+    // operands are read one step ahead of their products where the registers allow it
+    static constexpr bool kAhead = sizeof(T) == 2 ? DK <= 128 : DK <= 64;
 };
 
 __host__ __device__ constexpr int tile_of(int k, int i) { return i * (i + 1) / 2 + k; }
@@ -252,15 +276,28 @@ struct Rows {
     static constexpr int NQ = Q * PER / THREADS, NV = Q * VPER / THREADS;
     static_assert(NQ >= 1 && NV >= 1, "a thread loads whole 16-byte pieces");
     struct Set { uint4 q[WITH_Q ? NQ : 1], k[NQ], v[NV]; };
+    const Lds k_base, v_base;
     const LinAttnArgs &a;
     const Part<T> &p;
     const int tid, dk, top, latest;   // top, latest: last row of a load, last start of one
     const bool whole_cols;
     uint32_t oq[NQ], ok[NQ], ov[NV];
+    // LDS: a thread's pieces stand RS (VRS) rows apart, which a swizzle does not see
+    static constexpr int RS = THREADS / PER, VRS = THREADS / VPER;
+    static_assert(RS % 8 == 0 && VRS % 8 == 0 && (sizeof(T) == 4 || RS % 16 == 0), "pieces in rows of one swizzle");
+    Lds at[2], vat[2];           // its first pieces of k and v in buffer 0
+    const Lds q_from_k, kb, vb;  // bytes from k's to q's place, from buffer 0 to buffer 1
 
-    __device__ __forceinline__ Rows(const LinAttnArgs &a_, const Part<T> &p_, int tid_)
-        : a(a_), p(p_), tid(tid_), dk(static_cast<int>(a_.dk)), top(min(Q, p_.Lb) - 1), latest(max(p_.end - Q, 0)),
-          whole_cols(a_.dk == DK && p_.ncols == kN) {
+    __device__ __forceinline__ Rows(const LinAttnArgs &a_, const Part<T> &p_, int tid_, Lds q0, Lds k0, Lds v0, Lds kb_, Lds vb_)
+        : k_base(k0), v_base(v0), a(a_), p(p_), tid(tid_), dk(static_cast<int>(a_.dk)), top(min(Q, p_.Lb) - 1), latest(max(p_.end - Q, 0)),
+          whole_cols(a_.dk == DK && p_.ncols == kN), q_from_k(q0 - k0), kb(kb_), vb(vb_) {
+        Op<T>::place16(G::kRow, tid / PER, tid % PER, at);
+        Op<T>::place16(G::kVRow, tid / VPER, tid % VPER, vat);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            at[i] = opaque(at[i] + k0);
+            vat[i] = opaque(vat[i] + v0);
+        }
 #pragma unroll
         for (int r = 0; r < NQ; ++r) {
             const int s = tid + r * THREADS, row = min(s / PER, top), c = s % PER * VE;
@@ -300,35 +337,48 @@ struct Rows {
         }
         __builtin_amdgcn_sched_barrier(0);   // sets are waited for in the order of their loads
     }
-    // the chunk at row t0 to LDS; whether this thread staged an infinity or NaN of v
+    // the chunk at row t0 to LDS buffer buf; whether this thread staged an infinity or NaN of v
     template <bool INSIDE>
-    __device__ __forceinline__ bool stage_rows(int t0, const Set &set, char *q, char *k, char *v) const {
+    __device__ __forceinline__ bool stage_rows(int t0, const Set &set, int buf) const {
         constexpr bool IN = INSIDE || !VEC;
         // m: the chunk's rows (none past the end: the turn of the last chunk stages zeros); shift: the
         // loaded rows that come before it, 0 .. Q, whose places the rows behind its end take
         const int m = max(p.end - t0, 0), shift = IN || p.Lb < Q ? 0 : Q - min(m, Q);
-        auto place = [&](int row) __attribute__((always_inline)) { return IN ? row : row >= shift ? row - shift : row - shift + Q; };
+        auto place = [&](int row) __attribute__((always_inline)) { return row >= shift ? row - shift : row - shift + Q; };
         auto within = [&](uint4 u, int row, int col, int cols) __attribute__((always_inline)) {
-            return IN || (row < m && col < cols) ? u : make_uint4(0, 0, 0, 0);
+            return row < m && col < cols ? u : make_uint4(0, 0, 0, 0);
         };
 #pragma unroll
         for (int r = 0; r < NQ; ++r) {
-            const int s = tid + r * THREADS, row = place(s / PER), c = s % PER;
-            if constexpr (WITH_Q) Op<T>::put16(q, G::kRow, row, c, within(set.q[r], row, c * VE, dk));
-            Op<T>::put16(k, G::kRow, row, c, within(set.k[r], row, c * VE, dk));
+            if constexpr (IN) {
+                if constexpr (WITH_Q) Op<T>::put16(at, r * RS * G::kRow + buf * kb + q_from_k, set.q[r]);
+                Op<T>::put16(at, r * RS * G::kRow + buf * kb, set.k[r]);
+            } else {
+                const int row = place(tid / PER + r * RS), c = tid % PER;
+                Lds x[2];
+                Op<T>::place16(G::kRow, row, c, x);
+                if constexpr (WITH_Q) Op<T>::put16(x, k_base + buf * kb + q_from_k, within(set.q[r], row, c * VE, dk));
+                Op<T>::put16(x, k_base + buf * kb, within(set.k[r], row, c * VE, dk));
+            }
         }
         uint32_t odd = 0;
 #pragma unroll
         for (int r = 0; r < NV; ++r) {
-            const int s = tid + r * THREADS, row = place(s / VPER), c = s % VPER;
-            const uint4 u = within(set.v[r], row, c * VE, p.ncols);
-            Op<T>::put16(v, G::kVRow, row, c, u);
+            uint4 u = set.v[r];
+            if constexpr (IN) Op<T>::put16(vat, r * VRS * G::kVRow + buf * vb, u);
+            else {
+                const int row = place(tid / VPER + r * VRS), c = tid % VPER;
+                Lds x[2];
+                Op<T>::place16(G::kVRow, row, c, x);
+                u = within(u, row, c * VE, p.ncols);
+                Op<T>::put16(x, v_base + buf * vb, u);
+            }
             odd |= Op<T>::odd_bits(u);
         }
         return odd != 0;
     }
-    __device__ __forceinline__ bool stage(int t0, const Set &set, char *q, char *k, char *v) const {
-        return t0 + Q <= p.end && whole_cols ? stage_rows<true>(t0, set, q, k, v) : stage_rows<false>(t0, set, q, k, v);
+    __device__ __forceinline__ bool stage(int t0, const Set &set, int buf) const {
+        return t0 + Q <= p.end && whole_cols ? stage_rows<true>(t0, set, buf) : stage_rows<false>(t0, set, buf);
     }
 };
 
@@ -336,41 +386,57 @@ struct Rows {
 // for contraction rows 16 (TB + t) + 4 lg + j (t < NT) and column lr of its block; AGE: R = dS/da likewise,
 // R <- lambda^m (R + m S) + s_wr sum_j (m-1-j) lambda^(m-1-j) k_j v_j^T.  The row weights go into v, split into
 // as many bf16 parts as carry them whole: a state's error must not grow with the sequence.
-template <class T, int Q, int ROW, int NT, bool AGE, int NR>
-__device__ __forceinline__ void update_state(f4 (&S)[NT], f4 (&R)[NR], int TB, const char *k, const int (&koff)[Op<T>::kColOffs],
-                                             const typename Op<T>::V4 (&vp)[Q / 16], const float *w_up, const float *w_age,
-                                             Decay d, int m, int lg) {
+template <class T, int Q, int ROW, int NT, bool AGE, bool AHEAD, int NR>
+__device__ __forceinline__ void update_state(f4 (&S)[NT], f4 (&R)[NR], int TB, Lds k, const Lds (&koff)[Op<T>::kColOffs],
+                                             const typename Op<T>::V4 (&vp)[Q / 16], Lds w_up, Lds w_age,
+                                             Decay d, int m) {
     using O = Op<T>;
     constexpr int NJ = Q / 32;
     typename O::V4 wp[2 * NJ][O::kWide], ap[AGE ? 2 * NJ : 1][O::kWide];
 #pragma unroll
     for (int j = 0; j < 2 * NJ; ++j) {
         const f4 x = O::widen4(vp[j]);
-        O::template split<O::kWide>(x * *reinterpret_cast<const f4 *>(w_up + 16 * j + 4 * lg), wp[j]);
-        if constexpr (AGE) O::template split<O::kWide>(x * *reinterpret_cast<const f4 *>(w_age + 16 * j + 4 * lg), ap[j]);
+        O::template split<O::kWide>(x * lds_get<f4>(w_up + 64 * j), wp[j]);
+        if constexpr (AGE) O::template split<O::kWide>(x * lds_get<f4>(w_age + 64 * j), ap[j]);
     }
+    // AHEAD: two tiles at a time (their products are chains of accumulations), the next two tiles'
+    // columns of k read meanwhile
+    constexpr int STEP = AHEAD && NT > 1 ? 2 : 1;
+    typename O::Frag kf[AHEAD ? 2 : 1][STEP][NJ];
+    auto read = [&](int t, typename O::Frag (&f)[STEP][NJ]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        f4 s = S[t];
-        if constexpr (AGE) {
-            f4 r = R[t] + s * static_cast<float>(m);
+        for (int u = 0; u < STEP; ++u)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) r[j] = __builtin_fmaf(r[j], d.lo, r[j] * d.hi);
-            R[t] = r;
-        }
+            for (int c = 0; c < NJ; ++c)
+                f[u][c] = O::cat(O::col(k + 32 * c * ROW, koff, TB + t + u), O::col(k + (32 * c + 16) * ROW, koff, TB + t + u));
+    };
+    if constexpr (AHEAD) read(0, kf[0]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s[j] = __builtin_fmaf(s[j], d.lo, s[j] * d.hi);
+    for (int t = 0; t < NT; t += STEP) {
+        const int at = AHEAD ? t / STEP & 1 : 0;
+        if constexpr (!AHEAD) read(t, kf[0]);
+        else if (t + STEP < NT) read(t + STEP, kf[at ^ 1]);
 #pragma unroll
-        for (int c = 0; c < NJ; ++c) {
-            const auto kf = O::cat(O::col(k + 32 * c * ROW, koff, TB + t), O::col(k + (32 * c + 16) * ROW, koff, TB + t));
+        for (int u = 0; u < STEP; ++u) {
+            if constexpr (AGE) {
+                f4 r = R[t + u] + S[t + u] * static_cast<float>(m);
 #pragma unroll
-            for (int n = 0; n < O::kWide; ++n) {
-                s = O::mma(kf, O::cat(wp[2 * c][n], wp[2 * c + 1][n]), s);
-                if constexpr (AGE) R[t] = O::mma(kf, O::cat(ap[2 * c][n], ap[2 * c + 1][n]), R[t]);
+                for (int j = 0; j < 4; ++j) r[j] = __builtin_fmaf(r[j], d.lo, r[j] * d.hi);
+                R[t + u] = r;
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) S[t + u][j] = __builtin_fmaf(S[t + u][j], d.lo, S[t + u][j] * d.hi);
         }
-        S[t] = s;
-        if (t % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int c = 0; c < NJ; ++c)
+#pragma unroll
+            for (int n = 0; n < O::kWide; ++n)
+#pragma unroll
+                for (int u = 0; u < STEP; ++u) {
+                    S[t + u] = O::mma(kf[at][u][c], O::cat(wp[2 * c][n], wp[2 * c + 1][n]), S[t + u]);
+                    if constexpr (AGE) R[t + u] = O::mma(kf[at][u][c], O::cat(ap[2 * c][n], ap[2 * c + 1][n]), R[t + u]);
+                }
+        __builtin_amdgcn_sched_barrier(0);   // (no further ahead: the registers are full)
     }
 }
 
@@ -405,9 +471,7 @@ struct __align__(16) Smem {
     V4 p[Op<T>::kNarrow][G::kTiles][64];                        // decayed (q k^T)^T, operand-ready
     V4 pa[AGE ? Op<T>::kWide : 1][AGE ? G::kTiles : 1][64];     // the same times i - j (AGE)
     f4 y[4][G::kBlocks][64];                                    // the carried state's share of y^T
-    // powers of the decay with the sweep's factors: in-chunk s_in lambda^d (0 for d < 0, offset 16),
-    // readout s_rd lambda^(t + 1 - sh), update; AGE: the update's times the rows behind it
-    float w_in[16 + G::kQ], w_rd[G::kQ], w_up[2][G::kQ], w_age[AGE ? 2 * G::kQ : 4];
+    float w_up[2][G::kQ], w_age[AGE ? 2 * G::kQ : 4];           // row weights of the update (AGE: and its derivative)
     uint32_t odd[2][8];                                         // waves that staged an infinity or NaN of v
     float red[kThreads];
 };
@@ -445,15 +509,7 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
 
     const int sh = a.reverse ? 1 : 0, tail = max(end - first, 0) % Q;   // tail: rows of the last chunk, if not whole
     const float la = a.log_decay[p.h];
-    if (tid < 2 * Q) {
-        const int t = tid % Q;
-        const Decay d = decay_of(la, static_cast<float>(tid < Q ? t : t + 1 - sh));
-        if (tid < Q) sm.w_in[16 + t] = a.s_in * (d.hi + d.lo);
-        else sm.w_rd[t] = a.s_rd * (d.hi + d.lo);
-        if (tid < 16) sm.w_in[tid] = 0.0f;
-    } else if (tid < 4 * Q) {
-        fill_update_weights<Q, AGE>(sm.w_up, sm.w_age, tid - 2 * Q, la, a.s_wr, sh, tail);
-    }
+    if (tid < 2 * Q) fill_update_weights<Q, AGE>(sm.w_up, sm.w_age, tid, la, a.s_wr, sh, tail);
     float age = 0.0f;
     // factor of the age products: row t of the sequence, value columns 16 w + 4 lg .. + 3 of this tile
     auto age_dot = [&](int t, const f4 &x) __attribute__((always_inline)) {
@@ -464,20 +520,22 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
             if (n < p.ncols) age = __builtin_fmaf(x[j], widen_v(g[n]), age);
         }
     };
-    int roff[O::kRowOffs];
+    const Lds sq = lds_of(sm.q), sk = lds_of(sm.k), sv = lds_of(sm.v);
+    constexpr Lds KB = G::kQ * G::kRow, VB = G::kQ * G::kVRow;   // bytes of one buffer
+    Lds qoff[O::kRowOffs], voff[O::kOneCol];   // the lane's places in rows of q, in columns of v
 #pragma unroll
-    for (int i = 0; i < O::kRowOffs; ++i) roff[i] = O::row_off(i, lr, lg, G::kRow);
-    int voff[O::kOneCol];
+    for (int i = 0; i < O::kRowOffs; ++i) qoff[i] = opaque(sq + O::row_off(i, lr, lg, G::kRow));
 #pragma unroll
-    for (int i = 0; i < O::kOneCol; ++i) voff[i] = O::one_off(i, w, lr, lg, G::kVRow);
+    for (int i = 0; i < O::kOneCol; ++i) voff[i] = opaque(sv + O::one_off(i, w, lr, lg, G::kVRow));
+    const Lds py = opaque(lds_of(sm.y) + w * sizeof(sm.y[0]) + lane * 16);
 
     // every wave loads and stages an eighth of the rows, PF chunks ahead
     constexpr int PF = kB;
     using Loader = Rows<T, DK, kThreads, true, VEC>;
-    const Loader rows(a, p, tid);
+    const Loader rows(a, p, tid, sq, sk, sv, KB, VB);
     typename Loader::Set set[PF];
     auto stage = [&](int t0, int buf, const typename Loader::Set &from) __attribute__((always_inline)) {
-        const bool odd = rows.stage(t0, from, sm.q[buf], sm.k[buf], sm.v[buf]);
+        const bool odd = rows.stage(t0, from, buf);
         const bool any = __ballot(odd) != 0;
         if (lane == 0) sm.odd[buf][wv] = any;
     };
@@ -509,9 +567,10 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
 
     if (wv < 4) {
         // ================= state waves =================
-        int koff[O::kColOffs];
+        Lds koff[O::kColOffs];
 #pragma unroll
-        for (int i = 0; i < O::kColOffs; ++i) koff[i] = O::col_off(i, lr, lg, G::kRow);
+        for (int i = 0; i < O::kColOffs; ++i) koff[i] = opaque(sk + O::col_off(i, lr, lg, G::kRow));
+        const Lds wup = opaque(lds_of(sm.w_up) + 16 * lg), wage = AGE ? opaque(lds_of(sm.w_age) + 16 * lg) : 0;
         f4 S[NT], R[AGE ? NT : 1];   // contraction row 16 t + 4 lg + j, column 16 w + lr
         const int n = p.n0 + 16 * w + lr;
 #pragma unroll
@@ -534,6 +593,12 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
             }
         }
         const Decay full = decay_of(la, static_cast<float>(Q)), part = decay_of(la, static_cast<float>(tail));
+        float w_rd[NB];   // s_rd lambda^(t + 1 - sh) of the lane's rows
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const Decay d = decay_of(la, static_cast<float>(16 * i + lr + 1 - sh));
+            w_rd[i] = a.s_rd * (d.hi + d.lo);
+        }
         walk([&](int t0, auto which, auto further) __attribute__((always_inline)) {
             constexpr int buf = decltype(which)::value;
             const int m = min(Q, end - t0);
@@ -544,8 +609,17 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
                 acc[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
                 if constexpr (AGE) acca[i] = acc[i];
             }
+            constexpr bool AHEAD = G::kAhead && !AGE;
+            Frag qf[AHEAD ? 2 : 1][NB];
+            if constexpr (AHEAD)
+#pragma unroll
+                for (int i = 0; i < NB; ++i) qf[0][i] = O::row(buf * KB + 16 * i * G::kRow, qoff, 0);
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
+                const int at = AHEAD ? c & 1 : 0, c1 = AHEAD ? c + 1 : c;
+                if (c1 < NC)   // (AHEAD: the next rows' read meanwhile)
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) qf[AHEAD ? at ^ 1 : 0][i] = O::row(buf * KB + 16 * i * G::kRow, qoff, c1);
                 V4 s0[NS], s1[NS], r0[NS], r1[NS];
                 O::template split<NS>(S[2 * c], s0);
                 O::template split<NS>(S[2 * c + 1], s1);
@@ -553,31 +627,29 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
                     O::template split<NS>(R[2 * c], r0);
                     O::template split<NS>(R[2 * c + 1], r1);
                 }
-                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int i = 0; i < NB; ++i) {
-                    const Frag qf = O::row(&sm.q[buf][16 * i * G::kRow], roff, c);
+                for (int k = 0; k < NS; ++k)
 #pragma unroll
-                    for (int k = 0; k < NS; ++k) {
-                        acc[i] = O::mma(O::cat(s0[k], s1[k]), qf, acc[i]);
-                        if constexpr (AGE) acca[i] = O::mma(O::cat(r0[k], r1[k]), qf, acca[i]);
+                    for (int i = 0; i < NB; ++i) {
+                        acc[i] = O::mma(O::cat(s0[k], s1[k]), qf[at][i], acc[i]);
+                        if constexpr (AGE) acca[i] = O::mma(O::cat(r0[k], r1[k]), qf[at][i], acca[i]);
                     }
-                }
+                __builtin_amdgcn_sched_barrier(0);   // (no further ahead: the registers are full)
             }
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
-                const int t = 16 * i + lr;
-                const float e = sm.w_rd[t];
-                sm.y[w][i][lane] = acc[i] * e;
-                if constexpr (AGE)
-                    if (t < m) age_dot(t0 + t, acca[i] * e + acc[i] * (e * static_cast<float>(t + 1)));
+                lds_put(py + i * 1024, acc[i] * w_rd[i]);
+                if constexpr (AGE) {
+                    const int t = 16 * i + lr;
+                    if (t < m) age_dot(t0 + t, acca[i] * w_rd[i] + acc[i] * (w_rd[i] * static_cast<float>(t + 1)));
+                }
             }
             __syncthreads();   // tiles built, shares written
             V4 vp[Q / 16];
 #pragma unroll
-            for (int j = 0; j < Q / 16; ++j) vp[j] = O::one(&sm.v[buf][16 * j * G::kVRow], voff);
-            update_state<T, Q, G::kRow, NT, AGE>(S, R, 0, sm.k[buf], koff, vp, sm.w_up[m == Q ? 0 : 1],
-                                                 sm.w_age + (AGE && m != Q ? Q : 0), m == Q ? full : part, m, lg);
+            for (int j = 0; j < Q / 16; ++j) vp[j] = O::one(buf * VB + 16 * j * G::kVRow, voff);
+            const Lds last = m == Q ? 0 : 4 * Q;
+            update_state<T, Q, G::kRow, NT, AGE, G::kAhead && !AGE>(S, R, 0, buf * KB, koff, vp, wup + last, wage + last, m == Q ? full : part, m);
             next_rows(t0, which, further);
             __syncthreads();   // the next chunk staged
         });
@@ -607,40 +679,59 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
         // and with two blocks: wave 0 (1,0), wave 1 (1,1), wave 2 (0,0).
         const int k0 = NB == 2 ? min(w, 1) : w, i1 = NB == 2 || w == 3 ? 0 : 2, k1 = NB == 2 || w == 3 ? 0 : w;
         const bool has0 = NB == 4 || w < 2, has1 = NB == 4 || w == 2, has2 = NB == 4 && w < 2;
-        auto product = [&](f4 (&g)[3], int buf) __attribute__((always_inline)) {
-            const char *qt = sm.q[buf], *kt = sm.k[buf];
-#pragma unroll
-            for (int x = 0; x < 3; ++x) g[x] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-            if (NB == 4) {
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    const Frag kf = O::row(kt + 16 * k0 * G::kRow, roff, c), k1f = O::row(kt + 16 * k1 * G::kRow, roff, c);
-                    g[0] = O::mma(kf, O::row(qt + 16 * 3 * G::kRow, roff, c), g[0]);
-                    g[1] = O::mma(k1f, O::row(qt + 16 * i1 * G::kRow, roff, c), g[1]);
-                    g[2] = O::mma(kf, O::row(qt + 16 * G::kRow, roff, c), g[2]);   // (waves 2 and 3: not used)
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-            } else {
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    if (has0) g[0] = O::mma(O::row(kt + 16 * k0 * G::kRow, roff, c), O::row(qt + 16 * G::kRow, roff, c), g[0]);
-                    if (has1) g[1] = O::mma(O::row(kt, roff, c), O::row(qt, roff, c), g[1]);
-                }
-            }
-        };
-        auto put_tile = [&](const f4 &g, int i, int k) __attribute__((always_inline)) {
-            // lane: s = 16 k + 4 lg + j, t = 16 i + lr
-            const int idx = tile_of(k, i), d0 = 16 * (i - k) + lr - 4 * lg;
+        auto weights = [&](int i, int k) __attribute__((always_inline)) {   // s_in lambda^(t - s) of tile (i, k)
             f4 x;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[j] = g[j] * sm.w_in[16 + d0 - j];
+            for (int j = 0; j < 4; ++j) {
+                const int d = 16 * (i - k) + lr - 4 * lg - j;
+                const Decay p = decay_of(la, static_cast<float>(max(d, 0)));
+                x[j] = d >= 0 ? a.s_in * (p.hi + p.lo) : 0.0f;
+            }
+            return x;
+        };
+        const f4 wt[3] = {weights(NB - 1, k0), weights(i1, k1), weights(1, k0)};
+        Lds k0off[O::kRowOffs];   // the lane's places in rows of k, column block k0
+#pragma unroll
+        for (int i = 0; i < O::kRowOffs; ++i) k0off[i] = opaque(qoff[i] + (sk - sq) + 16 * k0 * G::kRow);
+        const Lds k1_from_k0 = 16 * (k1 - k0) * G::kRow;   // (negative as it may be: addresses wrap)
+        const Lds pp = opaque(lds_of(sm.p) + lane * sizeof(V4)), ppa = AGE ? opaque(lds_of(sm.pa) + lane * sizeof(V4)) : 0;
+        constexpr Lds TB = 64 * sizeof(V4), PB = G::kTiles * TB;   // bytes of a tile, of a part
+        auto product = [&](f4 (&g)[3], int buf) __attribute__((always_inline)) {
+            constexpr bool AHEAD = G::kAhead;
+            Frag f[AHEAD ? 2 : 1][5];
+            auto read = [&](int c, Frag (&x)[5]) __attribute__((always_inline)) {
+                if (NB == 2 && w == 3) return;
+                x[0] = O::row(buf * KB, k0off, c);
+                x[1] = O::row(buf * KB + k1_from_k0, k0off, c);
+                x[2] = O::row(buf * KB + 16 * (NB - 1) * G::kRow, qoff, c);
+                x[3] = O::row(buf * KB + 16 * i1 * G::kRow, qoff, c);
+                if (NB == 4) x[4] = O::row(buf * KB + 16 * G::kRow, qoff, c);
+            };
+#pragma unroll
+            for (int x = 0; x < 3; ++x) g[x] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+            if constexpr (AHEAD) read(0, f[0]);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const int at = AHEAD ? c & 1 : 0;
+                if constexpr (!AHEAD) read(c, f[0]);
+                else if (c + 1 < NC) read(c + 1, f[at ^ 1]);   // the next rows' read meanwhile
+                g[0] = O::mma(f[at][0], f[at][2], g[0]);   // (a wave without a tile: not used)
+                g[1] = O::mma(f[at][1], f[at][3], g[1]);
+                if (NB == 4) g[2] = O::mma(f[at][0], f[at][4], g[2]);
+                __builtin_amdgcn_sched_barrier(0);   // (no further ahead: the registers are full)
+            }
+        };
+        auto put_tile = [&](const f4 &g, const f4 &wt, int i, int k) __attribute__((always_inline)) {
+            // lane: s = 16 k + 4 lg + j, t = 16 i + lr
+            const int idx = tile_of(k, i), d0 = 16 * (i - k) + lr - 4 * lg;
+            f4 x = g * wt;
             if (i == k)   // rows after the output's: zero whatever q and k hold
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[j] = d0 - j >= 0 ? x[j] : 0.0f;
             V4 part[O::kNarrow];
             O::template split<O::kNarrow>(x, part);
 #pragma unroll
-            for (int n = 0; n < O::kNarrow; ++n) sm.p[n][idx][lane] = part[n];
+            for (int n = 0; n < O::kNarrow; ++n) lds_put(pp + idx * TB + n * PB, part[n]);
             if constexpr (AGE) {
                 f4 xa;
 #pragma unroll
@@ -648,7 +739,7 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
                 V4 wide[O::kWide];
                 O::template split<O::kWide>(xa, wide);
 #pragma unroll
-                for (int n = 0; n < O::kWide; ++n) sm.pa[n][idx][lane] = wide[n];
+                for (int n = 0; n < O::kWide; ++n) lds_put(ppa + idx * TB + n * PB, wide[n]);
             }
         };
         const int col = 16 * w + 4 * lg;
@@ -663,79 +754,99 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
             {
                 f4 g[3];
                 product(g, buf);
-                if (has0) put_tile(g[0], NB - 1, k0);
-                if (has1) put_tile(g[1], i1, k1);
-                if (has2) put_tile(g[2], 1, k0);
+                if (has0) put_tile(g[0], wt[0], NB - 1, k0);
+                if (has1) put_tile(g[1], wt[1], i1, k1);
+                if (has2) put_tile(g[2], wt[2], 1, k0);
             }
             __syncthreads();   // tiles built, shares written
             const uint4 o0 = *reinterpret_cast<const uint4 *>(&sm.odd[buf][0]), o1 = *reinterpret_cast<const uint4 *>(&sm.odd[buf][4]);
             const bool odd = __builtin_amdgcn_readfirstlane(o0.x | o0.y | o0.z | o0.w | o1.x | o1.y | o1.z | o1.w) != 0;
-            // ---- the tiles times v, on top of the carried state's share
-            V4 vp[Q / 16];
-#pragma unroll
-            for (int j = 0; j < Q / 16; ++j) vp[j] = O::one(&sm.v[buf][16 * j * G::kVRow], voff);
-#pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                f4 acc = sm.y[w][i][lane], acca = {0.0f, 0.0f, 0.0f, 0.0f};
-                // the diagonal tile's zeros (rows after the output's) must not meet an infinity or
-                // NaN: such values are taken out of the product and added to their own and later
-                // rows only
-                V4 vd = vp[i];
-                if (odd) {
-                    asm volatile("");   // (a branch, not selects: next to no chunk goes here)
-                    vd = O::only_finite4(vd);
-                }
-#pragma unroll
-                for (int k = 0; k <= i; k += 2) {
-                    const bool two = k + 1 <= i;
-                    const V4 zero = {};
-                    const Frag vf = O::cat(k == i ? vd : vp[k], two ? (k + 1 == i ? vd : vp[k + 1]) : zero);
-#pragma unroll
-                    for (int n = 0; n < O::kNarrow; ++n)
-                        acc = O::mma(vf, O::cat(sm.p[n][tile_of(k, i)][lane], two ? sm.p[n][tile_of(k + 1, i)][lane] : zero), acc);
-                    if constexpr (AGE) {
-#pragma unroll
-                        for (int n = 0; n < O::kWide; ++n)
-                            acca = O::mma(vf, O::cat(sm.pa[n][tile_of(k, i)][lane], two ? sm.pa[n][tile_of(k + 1, i)][lane] : zero), acca);
-                    }
-                }
-                if (odd) {
+            // The diagonal tiles' zeros (rows after the output's) must not meet an infinity or NaN: where
+            // a chunk has one (next to none does), such values are taken out of the products, and added
+            // to the shares of their own and later rows here, one by one
+            if (odd) {
+#pragma unroll 1
+                for (int i = 0; i < NB; ++i) {
+                    f4 y = lds_get<f4>(py + i * 1024), ya = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
                     for (int r = 0; r <= lr; ++r) {
-                        const int from = (r >> 2) * 16 + lr;   // the lane that holds row r, column lr of the tile
+                        const Lds from = ((r >> 2) * 16 + lr - lane) * sizeof(V4);   // the lane that holds row r, column lr of the tile
                         float pr = 0.0f;
-                        for (int n = 0; n < O::kNarrow; ++n) pr += O::element(sm.p[n][tile_of(i, i)][from], r & 3);
+                        for (int n = 0; n < O::kNarrow; ++n) pr += O::element(lds_get<V4>(pp + tile_of(i, i) * TB + n * PB + from), r & 3);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const int at = 16 * i + r, c = col + j, piece = c / (16 / static_cast<int>(sizeof(T)));
                             const int in = c % (16 / static_cast<int>(sizeof(T))) * static_cast<int>(sizeof(T)) ^ (sizeof(T) == 2 ? at & 8 : 0);
-                            const float x = widen_v(*reinterpret_cast<const T *>(&sm.v[buf][at * G::kVRow + ((piece ^ O::swizzle(at)) << 4) + in]));
+                            const float x = widen_v(lds_get<T>(sv + buf * VB + at * G::kVRow + ((piece ^ O::swizzle(at)) << 4) + in));
                             if ((__float_as_uint(x) & 0x7f800000u) != 0x7f800000u) continue;
-                            acc[j] = __builtin_fmaf(pr, x, acc[j]);
-                            if constexpr (AGE) acca[j] = __builtin_fmaf(pr * static_cast<float>(lr - r), x, acca[j]);
+                            y[j] = __builtin_fmaf(pr, x, y[j]);
+                            ya[j] = __builtin_fmaf(pr * static_cast<float>(lr - r), x, ya[j]);
                         }
                     }
+                    lds_put(py + i * 1024, y);
+                    if constexpr (AGE)
+                        if (16 * i + lr < m) age_dot(t0 + 16 * i + lr, ya);
                 }
-                const int t = 16 * i + lr;
-                if (t < m) {
-                    if constexpr (AGE) age_dot(t0 + t, acca);
-                    const int64_t at = y0 + (t0 + t) * ystep;
-                    if (sizeof(T) == 4 || a.out_f32) {
-                        float *y = static_cast<float *>(a.y) + at;
-                        if (full_cols) *reinterpret_cast<f4 *>(y) = acc;
-                        else
+            }
+            // ---- the tiles times v, on top of the carried state's share
+            f4 acc[NB], acca[AGE ? NB : 1];
+            V4 vp[NB], vd[NB];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                if (col + j < p.ncols) y[j] = acc[j];
+            for (int i = 0; i < NB; ++i) {
+                vp[i] = vd[i] = O::one(buf * VB + 16 * i * G::kVRow, voff);
+                acc[i] = lds_get<f4>(py + i * 1024);
+                if constexpr (AGE) acca[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+            }
+            if (odd) {
+                asm volatile("");   // (a branch, not selects)
+#pragma unroll
+                for (int i = 0; i < NB; ++i) vd[i] = O::only_finite4(vp[i]);
+            }
+#pragma unroll
+            for (int k = 0; k < NB; k += 2)
+#pragma unroll
+                for (int i = k; i < NB; ++i) {
+                    const bool two = k + 1 <= i;
+                    const V4 zero = {};
+                    const Frag vf = O::cat(k == i ? vd[k] : vp[k], two ? (k + 1 == i ? vd[k + 1] : vp[k + 1]) : zero);
+#pragma unroll
+                    for (int n = 0; n < O::kNarrow; ++n)
+                        acc[i] = O::mma(vf, O::cat(lds_get<V4>(pp + tile_of(k, i) * TB + n * PB), two ? lds_get<V4>(pp + tile_of(k + 1, i) * TB + n * PB) : zero), acc[i]);
+                    if constexpr (AGE) {
+#pragma unroll
+                        for (int n = 0; n < O::kWide; ++n)
+                            acca[i] = O::mma(vf, O::cat(lds_get<V4>(ppa + tile_of(k, i) * TB + n * PB), two ? lds_get<V4>(ppa + tile_of(k + 1, i) * TB + n * PB) : zero), acca[i]);
+                    }
+                }
+            const int64_t yt = y0 + (t0 + lr) * ystep;
+            if (sizeof(T) == 2 && !a.out_f32 && full_cols) {
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+                    if (16 * i + lr < m)
+                        *reinterpret_cast<u2 *>(static_cast<uint16_t *>(a.y) + yt + 16 * i * ystep) =
+                            u2{pack_bf16(acc[i][0], acc[i][1]), pack_bf16(acc[i][2], acc[i][3])};
+            } else {
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    if (16 * i + lr >= m) continue;
+                    const int64_t at = yt + 16 * i * ystep;
+                    if (sizeof(T) == 2 && !a.out_f32) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (col + j < p.ncols) put(static_cast<uint16_t *>(a.y), at + j, acc[i][j]);
+                    } else if (full_cols) {
+                        *reinterpret_cast<f4 *>(static_cast<float *>(a.y) + at) = acc[i];
                     } else {
-                        uint16_t *y = static_cast<uint16_t *>(a.y) + at;
-                        if (full_cols) *reinterpret_cast<u2 *>(y) = u2{pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3])};
-                        else
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                if (col + j < p.ncols) y[j] = to_bf16(acc[j]);
+                        for (int j = 0; j < 4; ++j)
+                            if (col + j < p.ncols) static_cast<float *>(a.y)[at + j] = acc[i][j];
                     }
                 }
             }
+            if constexpr (AGE)
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+                    if (16 * i + lr < m) age_dot(t0 + 16 * i + lr, acca[i]);
             next_rows(t0, which, further);
             __syncthreads();   // the next chunk staged
         });
@@ -759,7 +870,7 @@ __global__ void __launch_bounds__(kThreads) linattn_state_kernel(LinAttnArgs a) 
     using G = Tile<T, DK>;
     using O = Op<T>;
     constexpr int Q = G::kQ, NT = DK / 32;
-    __shared__ __align__(16) char sk[2][Q * G::kRow], sv[2][Q * G::kVRow];
+    __shared__ __align__(16) char tk[2][Q * G::kRow], tv[2][Q * G::kVRow];
     __shared__ __align__(16) float w_up[2][Q], w_age[AGE ? 2 * Q : 4];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), w = wv & 3, hf = wv >> 2;
@@ -769,11 +880,14 @@ __global__ void __launch_bounds__(kThreads) linattn_state_kernel(LinAttnArgs a) 
     if (p.first + p.seg_len >= p.Lb) return;   // no later segment starts from this one's state
     const float la = a.log_decay[p.h];
     if (tid < 2 * Q) fill_update_weights<Q, AGE>(w_up, w_age, tid, la, a.s_wr, a.reverse ? 1 : 0, 0);
-    int koff[O::kColOffs], voff[O::kOneCol];
+    const Lds sk = lds_of(tk), sv = lds_of(tv);
+    constexpr Lds KB = sizeof(tk[0]), VB = sizeof(tv[0]);
+    Lds koff[O::kColOffs], voff[O::kOneCol];
 #pragma unroll
-    for (int i = 0; i < O::kColOffs; ++i) koff[i] = O::col_off(i, lr, lg, G::kRow);
+    for (int i = 0; i < O::kColOffs; ++i) koff[i] = opaque(sk + O::col_off(i, lr, lg, G::kRow));
 #pragma unroll
-    for (int i = 0; i < O::kOneCol; ++i) voff[i] = O::one_off(i, w, lr, lg, G::kVRow);
+    for (int i = 0; i < O::kOneCol; ++i) voff[i] = opaque(sv + O::one_off(i, w, lr, lg, G::kVRow));
+    const Lds wup = opaque(lds_of(w_up) + 16 * lg), wage = AGE ? opaque(lds_of(w_age) + 16 * lg) : 0;
     f4 S[NT], R[AGE ? NT : 1];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -782,11 +896,11 @@ __global__ void __launch_bounds__(kThreads) linattn_state_kernel(LinAttnArgs a) 
     }
     const Decay full = decay_of(la, static_cast<float>(Q));
     using Loader = Rows<T, DK, kThreads, false, VEC>;
-    const Loader rows(a, p, tid);
+    const Loader rows(a, p, tid, sk, sk, sv, KB, VB);
     typename Loader::Set set[2];
     rows.load(p.first, set[0]);
     rows.load(p.first + Q, set[1]);
-    rows.stage(p.first, set[0], nullptr, sk[0], sv[0]);
+    rows.stage(p.first, set[0], 0);
     rows.load(p.first + 2 * Q, set[0]);
     __syncthreads();
     // (these segments are whole: seg_len is a multiple of Q)
@@ -794,9 +908,9 @@ __global__ void __launch_bounds__(kThreads) linattn_state_kernel(LinAttnArgs a) 
         constexpr int buf = decltype(which)::value;
         typename O::V4 vp[Q / 16];
 #pragma unroll
-        for (int j = 0; j < Q / 16; ++j) vp[j] = O::one(&sv[buf][16 * j * G::kVRow], voff);
-        update_state<T, Q, G::kRow, NT, AGE>(S, R, hf * NT, sk[buf], koff, vp, w_up[0], w_age, full, Q, lg);
-        rows.stage(t0 + Q, set[buf ^ 1], nullptr, sk[buf ^ 1], sv[buf ^ 1]);
+        for (int j = 0; j < Q / 16; ++j) vp[j] = O::one(buf * VB + 16 * j * G::kVRow, voff);
+        update_state<T, Q, G::kRow, NT, AGE, G::kAhead>(S, R, hf * NT, buf * KB, koff, vp, wup, wage, full, Q);
+        rows.stage(t0 + Q, set[buf ^ 1], buf ^ 1);
         if constexpr (decltype(further)::value) rows.load(t0 + 3 * Q, set[buf ^ 1]);
         __syncthreads();
     };
