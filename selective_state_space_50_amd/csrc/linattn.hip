@@ -105,6 +105,7 @@ struct Op<uint16_t> {
     static constexpr int kOneCol = 1;
     static __device__ __forceinline__ int one_off(int, int t, int lr, int lg, int row_bytes) { return col_off(t, lr, lg, row_bytes); }
     static __device__ __forceinline__ V4 one(Lds block, const Lds (&off)[1]) { return col1(off[0] + block); }
+    static __device__ __forceinline__ Frag pair(Lds a) { return lds_get<s8>(a); }
     static __device__ __forceinline__ f4 widen4(V4 v) {
         const u2 r = __builtin_bit_cast(u2, v);
         return f4{bf_lo(r.x), bf_hi(r.x), bf_lo(r.y), bf_hi(r.y)};
@@ -185,6 +186,7 @@ struct Op<float> {
         for (int j = 0; j < 4; ++j) v[j] = lds_get<float>(off[j] + block);
         return v;
     }
+    static __device__ __forceinline__ Frag pair(Lds a) { return Frag{lds_get<f4>(a), lds_get<f4>(a + 16)}; }
     static __device__ __forceinline__ f4 widen4(V4 v) { return v; }
     static __device__ __forceinline__ float element(V4 v, int j) { return v[j]; }
     static __device__ __forceinline__ bool finite1(float v) { return (__float_as_uint(v) & 0x7f800000u) != 0x7f800000u; }
@@ -218,12 +220,15 @@ struct Tile {
     static constexpr int kBufs = (sizeof(T) == 2 && DK <= 128) ? 2 : 1;
     static constexpr int kRow = DK * sizeof(T), kVRow = kN * sizeof(T);   // bytes
     static constexpr int kBlocks = kQ / 16;
-    static constexpr int kTiles = kBlocks * (kBlocks + 1) / 2;   // 16x16 tiles on and below the diagonal
+    // tiles of q k^T on and below the diagonal, two of a row side by side (an operand over K = 32; the
+    // second of the last pair of an even row is zero)
+    static constexpr int kPairs = kBlocks == 4 ? 6 : 2;
     // operands are read one step ahead of their products where the registers allow it
     static constexpr bool kAhead = sizeof(T) == 2 ? DK <= 128 : DK <= 64;
 };
 
-__host__ __device__ constexpr int tile_of(int k, int i) { return i * (i + 1) / 2 + k; }
+// pair of row block i that holds column block k
+__host__ __device__ constexpr int pair_of(int k, int i) { return (i < 2 ? i : 2 * i - 2) + k / 2; }
 
 // What one workgroup works on: value columns n0 .. n0 + ncols of one (b, h), rows [first, end) of
 // the sequence.  Rows are counted in the sweep's direction (row t is token t, or token Lb - 1 - t),
@@ -468,8 +473,8 @@ struct __align__(16) Smem {
     char q[G::kBufs][G::kQ * G::kRow];
     char k[G::kBufs][G::kQ * G::kRow];
     char v[G::kBufs][G::kQ * G::kVRow];
-    V4 p[Op<T>::kNarrow][G::kTiles][64];                        // decayed (q k^T)^T, operand-ready
-    V4 pa[AGE ? Op<T>::kWide : 1][AGE ? G::kTiles : 1][64];     // the same times i - j (AGE)
+    V4 p[Op<T>::kNarrow][G::kPairs][64][2];                          // decayed (q k^T)^T, operand-ready
+    V4 pa[AGE ? Op<T>::kWide : 1][AGE ? G::kPairs : 1][64][2];       // the same times i - j (AGE)
     f4 y[4][G::kBlocks][64];                                    // the carried state's share of y^T
     float w_up[2][G::kQ], w_age[AGE ? 2 * G::kQ : 4];           // row weights of the update (AGE: and its derivative)
     uint32_t odd[2][8];                                         // waves that staged an infinity or NaN of v
@@ -694,18 +699,26 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
 #pragma unroll
         for (int i = 0; i < O::kRowOffs; ++i) k0off[i] = opaque(qoff[i] + (sk - sq) + 16 * k0 * G::kRow);
         const Lds k1_from_k0 = 16 * (k1 - k0) * G::kRow;   // (negative as it may be: addresses wrap)
-        const Lds pp = opaque(lds_of(sm.p) + lane * sizeof(V4)), ppa = AGE ? opaque(lds_of(sm.pa) + lane * sizeof(V4)) : 0;
-        constexpr Lds TB = 64 * sizeof(V4), PB = G::kTiles * TB;   // bytes of a tile, of a part
-        auto product = [&](f4 (&g)[3], int buf) __attribute__((always_inline)) {
+        const Lds pp = opaque(lds_of(sm.p) + lane * sizeof(Frag)), ppa = AGE ? opaque(lds_of(sm.pa) + lane * sizeof(Frag)) : 0;
+        constexpr Lds TB = 64 * sizeof(Frag), PB = G::kPairs * TB;   // bytes of a pair, of a part
+        if (w == 0) {   // the pairs' empty halves
+            const V4 zero = {};
+            for (int i = 0; i < NB; i += 2) {
+                for (int n = 0; n < O::kNarrow; ++n) lds_put(pp + pair_of(i, i) * TB + n * PB + Lds(sizeof(V4)), zero);
+                if constexpr (AGE)
+                    for (int n = 0; n < O::kWide; ++n) lds_put(ppa + pair_of(i, i) * TB + n * PB + Lds(sizeof(V4)), zero);
+            }
+        }
+        auto product = [&](f4 (&g)[3], int buf, auto own) __attribute__((always_inline)) {
+            constexpr bool OWN = decltype(own)::value;   // the second tile is of column block k0, too
             constexpr bool AHEAD = G::kAhead;
             Frag f[AHEAD ? 2 : 1][5];
             auto read = [&](int c, Frag (&x)[5]) __attribute__((always_inline)) {
-                if (NB == 2 && w == 3) return;
                 x[0] = O::row(buf * KB, k0off, c);
-                x[1] = O::row(buf * KB + k1_from_k0, k0off, c);
                 x[2] = O::row(buf * KB + 16 * (NB - 1) * G::kRow, qoff, c);
+                if (!OWN) x[1] = O::row(buf * KB + k1_from_k0, k0off, c);
                 x[3] = O::row(buf * KB + 16 * i1 * G::kRow, qoff, c);
-                if (NB == 4) x[4] = O::row(buf * KB + 16 * G::kRow, qoff, c);
+                if (OWN && NB == 4) x[4] = O::row(buf * KB + 16 * G::kRow, qoff, c);
             };
 #pragma unroll
             for (int x = 0; x < 3; ++x) g[x] = f4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -716,14 +729,15 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
                 if constexpr (!AHEAD) read(c, f[0]);
                 else if (c + 1 < NC) read(c + 1, f[at ^ 1]);   // the next rows' read meanwhile
                 g[0] = O::mma(f[at][0], f[at][2], g[0]);   // (a wave without a tile: not used)
-                g[1] = O::mma(f[at][1], f[at][3], g[1]);
-                if (NB == 4) g[2] = O::mma(f[at][0], f[at][4], g[2]);
+                g[1] = O::mma(f[at][OWN ? 0 : 1], f[at][3], g[1]);
+                if (OWN && NB == 4) g[2] = O::mma(f[at][0], f[at][4], g[2]);
                 __builtin_amdgcn_sched_barrier(0);   // (no further ahead: the registers are full)
             }
         };
         auto put_tile = [&](const f4 &g, const f4 &wt, int i, int k) __attribute__((always_inline)) {
             // lane: s = 16 k + 4 lg + j, t = 16 i + lr
-            const int idx = tile_of(k, i), d0 = 16 * (i - k) + lr - 4 * lg;
+            const Lds at = pair_of(k, i) * TB + (k & 1) * sizeof(V4);
+            const int d0 = 16 * (i - k) + lr - 4 * lg;
             f4 x = g * wt;
             if (i == k)   // rows after the output's: zero whatever q and k hold
 #pragma unroll
@@ -731,7 +745,7 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
             V4 part[O::kNarrow];
             O::template split<O::kNarrow>(x, part);
 #pragma unroll
-            for (int n = 0; n < O::kNarrow; ++n) lds_put(pp + idx * TB + n * PB, part[n]);
+            for (int n = 0; n < O::kNarrow; ++n) lds_put(pp + at + n * PB, part[n]);
             if constexpr (AGE) {
                 f4 xa;
 #pragma unroll
@@ -739,7 +753,7 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
                 V4 wide[O::kWide];
                 O::template split<O::kWide>(xa, wide);
 #pragma unroll
-                for (int n = 0; n < O::kWide; ++n) lds_put(ppa + idx * TB + n * PB, wide[n]);
+                for (int n = 0; n < O::kWide; ++n) lds_put(ppa + at + n * PB, wide[n]);
             }
         };
         const int col = 16 * w + 4 * lg;
@@ -753,7 +767,8 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
             // ---- tiles of (q k^T)^T with their decay
             {
                 f4 g[3];
-                product(g, buf);
+                if (NB == 4 && w < 3) product(g, buf, std::true_type{});
+                else if (NB == 4 || w < 3) product(g, buf, std::false_type{});
                 if (has0) put_tile(g[0], wt[0], NB - 1, k0);
                 if (has1) put_tile(g[1], wt[1], i1, k1);
                 if (has2) put_tile(g[2], wt[2], 1, k0);
@@ -770,9 +785,10 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
                     f4 y = lds_get<f4>(py + i * 1024), ya = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
                     for (int r = 0; r <= lr; ++r) {
-                        const Lds from = ((r >> 2) * 16 + lr - lane) * sizeof(V4);   // the lane that holds row r, column lr of the tile
+                        // the lane that holds row r, column lr of the tile
+                        const Lds from = ((r >> 2) * 16 + lr - lane) * sizeof(Frag) + pair_of(i, i) * TB + (i & 1) * sizeof(V4);
                         float pr = 0.0f;
-                        for (int n = 0; n < O::kNarrow; ++n) pr += O::element(lds_get<V4>(pp + tile_of(i, i) * TB + n * PB + from), r & 3);
+                        for (int n = 0; n < O::kNarrow; ++n) pr += O::element(lds_get<V4>(pp + n * PB + from), r & 3);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const int at = 16 * i + r, c = col + j, piece = c / (16 / static_cast<int>(sizeof(T)));
@@ -802,22 +818,23 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
 #pragma unroll
                 for (int i = 0; i < NB; ++i) vd[i] = O::only_finite4(vp[i]);
             }
+            // (all pairs of a part read before the products: read one by one, each product waited for its own)
+            auto times_v = [&](f4 (&to)[NB], Lds from) __attribute__((always_inline)) {
+                Frag f[G::kPairs];
 #pragma unroll
-            for (int k = 0; k < NB; k += 2)
+                for (int x = 0; x < G::kPairs; ++x) f[x] = O::pair(from + x * TB);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int i = k; i < NB; ++i) {
-                    const bool two = k + 1 <= i;
-                    const V4 zero = {};
-                    const Frag vf = O::cat(k == i ? vd[k] : vp[k], two ? (k + 1 == i ? vd[k + 1] : vp[k + 1]) : zero);
+                for (int k = 0; k < NB; k += 2)
 #pragma unroll
-                    for (int n = 0; n < O::kNarrow; ++n)
-                        acc[i] = O::mma(vf, O::cat(lds_get<V4>(pp + tile_of(k, i) * TB + n * PB), two ? lds_get<V4>(pp + tile_of(k + 1, i) * TB + n * PB) : zero), acc[i]);
-                    if constexpr (AGE) {
+                    for (int i = k; i < NB; ++i)
+                        to[i] = O::mma(O::cat(k == i ? vd[k] : vp[k], i <= k + 1 ? vd[k + 1] : vp[k + 1]), f[pair_of(k, i)], to[i]);
+            };
 #pragma unroll
-                        for (int n = 0; n < O::kWide; ++n)
-                            acca[i] = O::mma(vf, O::cat(lds_get<V4>(ppa + tile_of(k, i) * TB + n * PB), two ? lds_get<V4>(ppa + tile_of(k + 1, i) * TB + n * PB) : zero), acca[i]);
-                    }
-                }
+            for (int n = 0; n < O::kNarrow; ++n) times_v(acc, pp + n * PB);
+            if constexpr (AGE)
+#pragma unroll
+                for (int n = 0; n < O::kWide; ++n) times_v(acca, ppa + n * PB);
             const int64_t yt = y0 + (t0 + lr) * ystep;
             if (sizeof(T) == 2 && !a.out_f32 && full_cols) {
 #pragma unroll
