@@ -476,6 +476,7 @@ struct __align__(16) Smem {
     V4 p[Op<T>::kNarrow][G::kPairs][64][2];                          // decayed (q k^T)^T, operand-ready
     V4 pa[AGE ? Op<T>::kWide : 1][AGE ? G::kPairs : 1][64][2];       // the same times i - j (AGE)
     f4 y[4][G::kBlocks][64];                                    // the carried state's share of y^T
+    f4 ya[AGE ? 4 : 1][AGE ? G::kBlocks : 1][64];               // and of its derivative
     float w_up[2][G::kQ], w_age[AGE ? 2 * G::kQ : 4];           // row weights of the update (AGE: and its derivative)
     uint32_t odd[2][8];                                         // waves that staged an infinity or NaN of v
     float red[kThreads];
@@ -517,13 +518,20 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
     if (tid < 2 * Q) fill_update_weights<Q, AGE>(sm.w_up, sm.w_age, tid, la, a.s_wr, sh, tail);
     float age = 0.0f;
     // factor of the age products: row t of the sequence, value columns 16 w + 4 lg .. + 3 of this tile
-    auto age_dot = [&](int t, const f4 &x) __attribute__((always_inline)) {
-        const T *g = static_cast<const T *>(a.age_w) + (p.b * a.L + t) * a.age_row + (p.h / (a.H / a.age_heads)) * a.dn + p.n0;
+    // (0 past the columns and the rows; VEC: one load, always of the operand)
+    const T *age_w = AGE ? static_cast<const T *>(a.age_w) + p.b * a.L * a.age_row + (p.h / (a.H / a.age_heads)) * a.dn + p.n0 : nullptr;
+    auto age_factor = [&](int t) __attribute__((always_inline)) {
+        const int n = 16 * w + 4 * lg;
+        V4 g;
+        if constexpr (VEC) {
+            const V4 u = *reinterpret_cast<const V4 *>(age_w + min(t, p.Lb - 1) * a.age_row + (n < p.ncols ? n : 0));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int n = 16 * w + 4 * lg + j;
-            if (n < p.ncols) age = __builtin_fmaf(x[j], widen_v(g[n]), age);
+            for (int j = 0; j < 4; ++j) g[j] = n < p.ncols && t < end ? u[j] : 0;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) g[j] = n + j < p.ncols && t < end ? age_w[t * a.age_row + n + j] : T(0);
         }
+        return g;
     };
     const Lds sq = lds_of(sm.q), sk = lds_of(sm.k), sv = lds_of(sm.v);
     constexpr Lds KB = G::kQ * G::kRow, VB = G::kQ * G::kVRow;   // bytes of one buffer
@@ -533,9 +541,12 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
 #pragma unroll
     for (int i = 0; i < O::kOneCol; ++i) voff[i] = opaque(sv + O::one_off(i, w, lr, lg, G::kVRow));
     const Lds py = opaque(lds_of(sm.y) + w * sizeof(sm.y[0]) + lane * 16);
+    using SmemT = Smem<T, DK, AGE>;
+    constexpr Lds YA = offsetof(SmemT, ya) - offsetof(SmemT, y);   // from a share of y to its derivative's
 
-    // every wave loads and stages an eighth of the rows, PF chunks ahead
-    constexpr int PF = kB;
+    // every wave loads and stages an eighth of the rows, PF chunks ahead (AGE: one, as R takes the registers of
+    // a second set, and spills cost more than the shorter lead)
+    constexpr int PF = AGE ? 1 : kB;
     using Loader = Rows<T, DK, kThreads, true, VEC>;
     const Loader rows(a, p, tid, sq, sk, sv, KB, VB);
     typename Loader::Set set[PF];
@@ -550,17 +561,17 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
         stage(first, 0, set[0]);
         rows.load(first + PF * Q, set[0]);
     }
-    // chunk by chunk: whole turns of PF chunks, then the rest (a way out in the middle of a turn would
+    // chunk by chunk: whole turns of kB chunks, then the rest (a way out in the middle of a turn would
     // make the compiler's waits at the top of the loop cover all loads).  The chunk at row t0 is in
     // LDS buffer `which`, its successor's rows in set (which + 1) % PF; further: rows are loaded ahead
     auto walk = [&](auto chunk) __attribute__((always_inline)) {
         __syncthreads();   // chunk 0 staged
         int t0 = first;
-        for (; t0 + (PF - 1) * Q < end; t0 += PF * Q) {
+        for (; t0 + (kB - 1) * Q < end; t0 += kB * Q) {
             chunk(t0, std::integral_constant<int, 0>{}, std::true_type{});
-            if constexpr (PF > 1) chunk(t0 + Q, std::integral_constant<int, 1 % PF>{}, std::true_type{});
+            if constexpr (kB > 1) chunk(t0 + Q, std::integral_constant<int, 1 % kB>{}, std::true_type{});
         }
-        if constexpr (PF > 1)
+        if constexpr (kB > 1)
             if (t0 < end) chunk(t0, std::integral_constant<int, 0>{}, std::false_type{});
     };
     auto next_rows = [&](int t0, auto which, auto further) __attribute__((always_inline)) {
@@ -644,10 +655,7 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
 #pragma unroll
             for (int i = 0; i < NB; ++i) {
                 lds_put(py + i * 1024, acc[i] * w_rd[i]);
-                if constexpr (AGE) {
-                    const int t = 16 * i + lr;
-                    if (t < m) age_dot(t0 + t, acca[i] * w_rd[i] + acc[i] * (w_rd[i] * static_cast<float>(t + 1)));
-                }
+                if constexpr (AGE) lds_put(py + YA + i * 1024, acca[i] * w_rd[i] + acc[i] * (w_rd[i] * static_cast<float>(16 * i + lr + 1)));
             }
             __syncthreads();   // tiles built, shares written
             V4 vp[Q / 16];
@@ -764,6 +772,10 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
         walk([&](int t0, auto which, auto further) __attribute__((always_inline)) {
             constexpr int buf = decltype(which)::value;
             const int m = min(Q, end - t0);
+            V4 age_g[AGE ? NB : 1];
+            if constexpr (AGE)
+#pragma unroll
+                for (int i = 0; i < NB; ++i) age_g[i] = age_factor(t0 + 16 * i + lr);
             // ---- tiles of (q k^T)^T with their decay
             {
                 f4 g[3];
@@ -782,7 +794,7 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
             if (odd) {
 #pragma unroll 1
                 for (int i = 0; i < NB; ++i) {
-                    f4 y = lds_get<f4>(py + i * 1024), ya = {0.0f, 0.0f, 0.0f, 0.0f};
+                    f4 y = lds_get<f4>(py + i * 1024), ya = lds_get<f4>(py + (AGE ? YA + i * 1024 : 0));
 #pragma unroll 1
                     for (int r = 0; r <= lr; ++r) {
                         // the lane that holds row r, column lr of the tile
@@ -800,8 +812,7 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
                         }
                     }
                     lds_put(py + i * 1024, y);
-                    if constexpr (AGE)
-                        if (16 * i + lr < m) age_dot(t0 + 16 * i + lr, ya);
+                    if constexpr (AGE) lds_put(py + YA + i * 1024, ya);
                 }
             }
             // ---- the tiles times v, on top of the carried state's share
@@ -811,7 +822,7 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
             for (int i = 0; i < NB; ++i) {
                 vp[i] = vd[i] = O::one(buf * VB + 16 * i * G::kVRow, voff);
                 acc[i] = lds_get<f4>(py + i * 1024);
-                if constexpr (AGE) acca[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+                if constexpr (AGE) acca[i] = lds_get<f4>(py + YA + i * 1024);
             }
             if (odd) {
                 asm volatile("");   // (a branch, not selects)
@@ -862,8 +873,11 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
             }
             if constexpr (AGE)
 #pragma unroll
-                for (int i = 0; i < NB; ++i)
-                    if (16 * i + lr < m) age_dot(t0 + 16 * i + lr, acca[i]);
+                for (int i = 0; i < NB; ++i) {
+                    const f4 g = O::widen4(age_g[i]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) age = __builtin_fmaf(acca[i][j], g[j], age);
+                }
             next_rows(t0, which, further);
             __syncthreads();   // the next chunk staged
         });
@@ -1097,6 +1111,7 @@ hipError_t launch_linattn(const LinAttnArgs &a0, bool bf16, hipStream_t s) {
     const int64_t ve = bf16 ? 8 : 4;
     // 16-byte loads where every row and head starts on 16 bytes (the pointers do)
     a.vec = a.q_row % ve == 0 && a.k_row % ve == 0 && a.v_row % ve == 0 && a.dk % ve == 0 && a.dn % ve == 0;
+    if (a.age_part) a.vec = a.vec && a.age_row % ve == 0;
     a.y_vec = a.dn % 4 == 0;
     return bf16 ? launch_typed<uint16_t>(a, s) : launch_typed<float>(a, s);
 }

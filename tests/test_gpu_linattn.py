@@ -323,3 +323,22 @@ def test_deterministic_and_empty(ssm):
     assert torch.equal(g["dh0"], dh) and not g["dlog_decay"].any()
     g = ssm.linattn_bwd(q[:0], k[:0], v[:0], a, s0[:0], dy[:0])
     assert not g["dlog_decay"].any() and g["dq"].shape == (0, 1500, 4, 64)
+
+
+@pytest.mark.parametrize("dt,extra", [("bf16", 1), ("bf16", 4), ("f32", 1), ("f32", 2)])
+@pytest.mark.parametrize("which", ["q", "k", "v"])
+def test_rows_that_miss_16_bytes(ssm, dt, extra, which):
+    """One operand whose tokens do not all start on 16 bytes, the others' do."""
+    import torch
+    c = make(2, 150, 2, 2, 2, 2, 64, 72, dt, seed=extra)
+    args = dict(zip("q k v a h0 dy".split(), dev(c, "q", "k", "v", "a", "h0", "dy")))
+    whole = ssm.linattn_bwd(args["q"], args["k"], args["v"], args["a"], args["h0"], args["dy"])
+    y = ssm.linattn_fwd(args["q"], args["k"], args["v"], args["a"], args["h0"])
+    t = args[which]
+    wide = torch.zeros(*t.shape[:2], t[0, 0].numel() + extra, dtype=t.dtype, device="cuda")
+    wide[..., :-extra] = t.flatten(2)
+    args[which] = wide[..., :-extra].unflatten(-1, t.shape[2:])
+    g = ssm.linattn_bwd(args["q"], args["k"], args["v"], args["a"], args["h0"], args["dy"])
+    for n in whole:
+        assert torch.equal(g[n], whole[n]), n
+    assert torch.equal(ssm.linattn_fwd(args["q"], args["k"], args["v"], args["a"], args["h0"]), y)
