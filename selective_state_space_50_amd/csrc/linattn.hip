@@ -257,8 +257,6 @@ struct Part {
         const int L = static_cast<int>(a.L);
         Lb = a.lengths ? __builtin_amdgcn_readfirstlane(min(max(a.lengths[b], 0), L)) : L;
         seg_len = static_cast<int>(a.seg_len);
-        first = static_cast<int>(seg) * seg_len;
-        end = min(first + seg_len, Lb);
         origin = a.reverse ? Lb - 1 : 0;
         dir = a.reverse ? -1 : 1;
         q = static_cast<const T *>(a.q) + (b * a.L + origin) * a.q_row + (h / (a.H / a.q_heads)) * a.dk;
@@ -496,7 +494,7 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
     const int lr = lane & 15, lg = lane >> 4;
     Part<T> p;
     if (!p.set(a, a.nseg)) return;
-    const int first = p.first, end = p.end;
+    const int first = p.first = static_cast<int>(p.seg) * p.seg_len, end = p.end = min(first + p.seg_len, p.Lb);
 
     // rows past the sequence's end: zeros (a padded batch)
     if (p.Lb < static_cast<int>(a.L)) {
@@ -597,7 +595,8 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
                 float s0 = 0.0f, r0 = 0.0f;
                 if (kk < a.dk && n < a.dn) {
                     if (p.seg > 0) {
-                        const int64_t at = (((p.b * a.H + p.h) * (a.nseg - 1) + p.seg - 1) * a.dk + kk) * a.dn + n;
+                        const int64_t at = ((p.b * a.H + p.h) * (a.nseg - 1) + p.seg) * a.nsub * a.dk * a.dn -
+                                           a.dk * a.dn + kk * a.ws_sr + n * a.ws_sc;   // the slot before its own first
                         s0 = a.ws_S[at];
                         if constexpr (AGE) r0 = a.ws_R[at];
                     } else if (a.h0) {
@@ -894,8 +893,9 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
     }
 }
 
-// ---- the segments' own contributions to the state (from zero), into the workspace: eight waves,
-// wave w value columns 16 (w % 4) .. + 15 and half w / 4 of the contraction columns
+// ---- the segments' own contributions to the state (from zero), into the workspace, in nsub parts of a
+// segment that run side by side: eight waves, wave w value columns 16 (w % 4) .. + 15 and half w / 4 of
+// the contraction columns
 template <class T, int DK, bool AGE, bool VEC>
 __global__ void __launch_bounds__(kThreads) linattn_state_kernel(LinAttnArgs a) {
     using G = Tile<T, DK>;
@@ -907,8 +907,12 @@ __global__ void __launch_bounds__(kThreads) linattn_state_kernel(LinAttnArgs a) 
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), w = wv & 3, hf = wv >> 2;
     const int lr = lane & 15, lg = lane >> 4;
     Part<T> p;
-    if (!p.set(a, a.nseg - 1)) return;
-    if (p.first + p.seg_len >= p.Lb) return;   // no later segment starts from this one's state
+    if (!p.set(a, (a.nseg - 1) * a.nsub)) return;
+    const int of = static_cast<int>(p.seg / a.nsub), sub = static_cast<int>(p.seg % a.nsub), sub_len = static_cast<int>(a.sub_len);
+    const int seg_end = (of + 1) * p.seg_len;
+    if (seg_end >= p.Lb) return;   // no later segment starts from this one's state
+    p.first = of * p.seg_len + sub * sub_len;
+    p.end = min(p.first + sub_len, seg_end);
     const float la = a.log_decay[p.h];
     if (tid < 2 * Q) fill_update_weights<Q, AGE>(w_up, w_age, tid, la, a.s_wr, a.reverse ? 1 : 0, 0);
     const Lds sk = lds_of(tk), sv = lds_of(tv);
@@ -934,7 +938,7 @@ __global__ void __launch_bounds__(kThreads) linattn_state_kernel(LinAttnArgs a) 
     rows.stage(p.first, set[0], 0);
     rows.load(p.first + 2 * Q, set[0]);
     __syncthreads();
-    // (these segments are whole: seg_len is a multiple of Q)
+    // (whole chunks: seg_len and sub_len are multiples of Q)
     auto chunk = [&](int t0, auto which, auto further) __attribute__((always_inline)) {
         constexpr int buf = decltype(which)::value;
         typename O::V4 vp[Q / 16];
@@ -951,7 +955,7 @@ __global__ void __launch_bounds__(kThreads) linattn_state_kernel(LinAttnArgs a) 
         chunk(t0 + Q, std::integral_constant<int, 1>{}, std::true_type{});
     }
     if (t0 < p.end) chunk(t0, std::integral_constant<int, 0>{}, std::false_type{});
-    const int64_t at0 = ((p.b * a.H + p.h) * (a.nseg - 1) + p.seg) * a.dk * a.dn;
+    const int64_t at0 = ((p.b * a.H + p.h) * (a.nseg - 1) * a.nsub + p.seg) * a.dk * a.dn;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -964,27 +968,61 @@ __global__ void __launch_bounds__(kThreads) linattn_state_kernel(LinAttnArgs a) 
         }
 }
 
-// Own contributions of the segments -> the states that segments 1, 2, ... start from, one
-// thread per state element: H_{s+1} = lambda^T H_s + own_s (T rows to a segment), and with R
-// its derivative by log_decay.
+// Own contributions of the segments' parts -> the states that segments 1, 2, ... start from, each in the
+// slot of its predecessor's last part: H <- lambda^T H + own over the parts (T rows to a part), and with
+// R its derivative by log_decay.  Bound by latency: a thread takes four elements of one state, and reads
+// eight parts of them ahead of the chain.
+template <bool AGE>
 __global__ void __launch_bounds__(256) linattn_combine_kernel(LinAttnArgs a) {
-    const int64_t gid = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    const int64_t sz = a.dk * a.dn;
-    if (gid >= a.B * a.H * sz) return;
-    const int64_t bh = gid / sz, e = gid % sz, kk = e / a.dn, n = e % a.dn;
+    constexpr int E = 4, P = AGE ? 4 : 8;
+    __shared__ float decay[2];
+    const int64_t sz = a.dk * a.dn, per = (sz + 256 * E - 1) / (256 * E);
+    const int64_t bh = blockIdx.x / per, e0 = blockIdx.x % per * (256 * E) + threadIdx.x;
     int64_t Lb = a.L;
     if (a.lengths) Lb = min(max(static_cast<int64_t>(a.lengths[bh / a.H]), int64_t(0)), a.L);
-    const double x = static_cast<double>(a.log_decay[bh % a.H]) * static_cast<double>(a.seg_len);
-    const float d = static_cast<float>(exp(x)), T = static_cast<float>(a.seg_len);
-    float S = a.h0 ? a.h0[bh * sz + kk * a.h_sr + n * a.h_sc] : 0.0f, R = 0.0f;
-    for (int64_t s = 0; s + 1 < a.nseg && (s + 1) * a.seg_len < Lb; ++s) {
-        const int64_t at = (bh * (a.nseg - 1) + s) * sz + e;
-        if (a.ws_R) {
-            R = __builtin_fmaf(d, __builtin_fmaf(T, S, R), a.ws_R[at]);
-            a.ws_R[at] = R;
+    const int starts = static_cast<int>(min(a.nseg - 1, (Lb - 1) / a.seg_len)), nsub = static_cast<int>(a.nsub), parts = starts * nsub;
+    if (parts <= 0) return;
+    // (the last part of a segment is what the others leave)
+    const int64_t last_len = a.seg_len - (a.nsub - 1) * a.sub_len;
+    if (threadIdx.x < 2)
+        decay[threadIdx.x] = static_cast<float>(exp(static_cast<double>(a.log_decay[bh % a.H]) *
+                                                    static_cast<double>(threadIdx.x ? last_len : a.sub_len)));
+    __syncthreads();
+    const float d = decay[0], d1 = decay[1], T = static_cast<float>(a.sub_len), T1 = static_cast<float>(last_len);
+    const int64_t at0 = bh * (a.nseg - 1) * nsub * sz;
+    float S[E], R[E];
+#pragma unroll
+    for (int x = 0; x < E; ++x) {
+        const int64_t e = min(e0 + x * 256, sz - 1);
+        S[x] = a.h0 ? a.h0[bh * sz + e / a.dn * a.h_sr + e % a.dn * a.h_sc] : 0.0f;
+        R[x] = 0.0f;
+    }
+    for (int s0 = 0; s0 < parts; s0 += P) {
+        float own[P][E], own_R[AGE ? P : 1][E];
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            if (s0 + i < parts)
+#pragma unroll
+                for (int x = 0; x < E; ++x) {
+                    const int64_t at = at0 + (s0 + i) * sz + min(e0 + x * 256, sz - 1);
+                    own[i][x] = a.ws_S[at];
+                    if constexpr (AGE) own_R[i][x] = a.ws_R[at];
+                }
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            if (s0 + i >= parts) continue;
+            const bool last = (s0 + i + 1) % nsub == 0;
+#pragma unroll
+            for (int x = 0; x < E; ++x) {
+                if constexpr (AGE) R[x] = __builtin_fmaf(last ? d1 : d, __builtin_fmaf(last ? T1 : T, S[x], R[x]), own_R[i][x]);
+                S[x] = __builtin_fmaf(last ? d1 : d, S[x], own[i][x]);
+                if (last && e0 + x * 256 < sz) {
+                    const int64_t at = at0 + (s0 + i) * sz + e0 + x * 256;
+                    a.ws_S[at] = S[x];
+                    if constexpr (AGE) a.ws_R[at] = R[x];
+                }
+            }
         }
-        S = __builtin_fmaf(d, S, a.ws_S[at]);
-        a.ws_S[at] = S;
     }
 }
 
@@ -1079,14 +1117,14 @@ hipError_t launch_sweep(const LinAttnArgs &a0, hipStream_t s) {
         a.work = a.B * a.H * segs * a.ntiles;
         return dim3(static_cast<unsigned>((a.work + 7) / 8 * 8));
     };
-    if (a.nseg > 1) {
-        const dim3 g = grid(a.nseg - 1);
+    if (a.nseg > 1 && !a.have_states) {
+        const dim3 g = grid((a.nseg - 1) * a.nsub);
         if (a.vec) hipLaunchKernelGGL((linattn_state_kernel<T, DK, AGE, true>), g, dim3(kThreads), 0, s, a);
         else hipLaunchKernelGGL((linattn_state_kernel<T, DK, AGE, false>), g, dim3(kThreads), 0, s, a);
         hipError_t e = launch_status(s);
         if (e != hipSuccess) return e;
-        const int64_t n = a.B * a.H * a.dk * a.dn;
-        hipLaunchKernelGGL(linattn_combine_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, s, a);
+        const dim3 blocks(static_cast<unsigned>(a.B * a.H * ((a.dk * a.dn + 1023) / 1024)));
+        hipLaunchKernelGGL((linattn_combine_kernel<AGE>), blocks, dim3(256), 0, s, a);
         e = launch_status(s);
         if (e != hipSuccess) return e;
     }

@@ -1179,7 +1179,9 @@ LinAttnArgs linattn_args(const ssm_linattn_shape &s, const LinAttnPlan &p, const
 
 void linattn_split(LinAttnArgs &a, const LinAttnPlan::Sweep &w, void *workspace) {
     a.nseg = w.nseg; a.seg_len = w.seg_len; a.ntiles = w.ntiles;
+    a.nsub = w.nsub; a.sub_len = w.sub_len;
     a.ws_S = w.nseg > 1 ? static_cast<float *>(workspace) : nullptr;
+    a.ws_sr = a.dn; a.ws_sc = 1;
 }
 
 int fill_floats(float *out, const float *from, int64_t n, hipStream_t s) {
@@ -1286,6 +1288,12 @@ extern "C" int ssm_linattn_bwd(const ssm_linattn_shape *shape, const void *q, co
         a.h0 = dh_last; a.h_last = dh0;
         a.reverse = 1; a.s_in = scale; a.s_wr = scale;
         linattn_split(a, p.fwd, workspace);
+        // cut into the same parts as dk's sweep, it starts from the same states, transposed
+        if (p.fwd.nseg == p.bwd.nseg && p.fwd.seg_len == p.bwd.seg_len) {
+            a.nsub = p.bwd.nsub;
+            a.have_states = 1;
+            a.ws_sr = 1; a.ws_sc = sh.dk;
+        }
         e = sweep(a, dv, sh.v_heads);
     }
     return e == hipSuccess ? SSM_OK : hip_fail("linattn backward launch", e);

@@ -118,8 +118,11 @@ struct LinAttnArgs {
     int reverse = 0;                    // from the last token to the first, the state read before it decays
     float s_in = 1.0f, s_rd = 1.0f, s_wr = 1.0f;   // factors of the in-chunk product, the readout, the update
     int64_t nseg = 1, seg_len = 0;      // segments of the sequence that run side by side
+    int64_t nsub = 1, sub_len = 0;      // parts of a segment in the pass for the segments' own states
     int64_t ntiles = 1;                 // column tiles of v
-    float *ws_S = nullptr, *ws_R = nullptr;   // [B, H, nseg - 1, dk, dn]
+    float *ws_S = nullptr, *ws_R = nullptr;   // [B, H, nseg - 1, nsub, dk, dn]
+    int have_states = 0;                // ws_S holds the start states already, element (k, n) at k ws_sr + n ws_sc
+    int64_t ws_sr = 0, ws_sc = 1;
     // the gradient of log_decay (a sweep of dq): its other factor, q, and the workgroups' shares
     const void *age_w = nullptr;
     int64_t age_row = 0, age_heads = 1;

@@ -163,6 +163,7 @@ struct LinAttnPlan {
     // a sweep with contraction size c and n value columns: segments and their length
     struct Sweep {
         int64_t nseg = 1, seg_len = 0, ntiles = 1;
+        int64_t nsub = 1, sub_len = 0;   // parts of a segment in the pass for the segments' own states
         size_t state_bytes = 0;   // one array of the segments' states
     };
     Sweep fwd;                  // y: contraction over dk, dv columns (dv's sweep, too)
