@@ -112,7 +112,7 @@ template <class T, int VE, int MAXV, bool WG>
 __global__ void __launch_bounds__(kWG) gn_team_kernel(GroupNormArgs a) {
     __shared__ float lds[4];
     const int P = WG ? kWG : a.team, tl = threadIdx.x % P;
-    const uint32_t team = blockIdx.x * (kWG / P) + threadIdx.x / P;
+    const uint32_t team = (blockIdx.y * gridDim.x + blockIdx.x) * (kWG / P) + threadIdx.x / P;
     const bool on = team < static_cast<uint32_t>(a.N * a.G);
     const uint32_t G = static_cast<uint32_t>(a.G), n = (on ? team : 0) / G, g = (on ? team : 0) % G;
     const uint32_t nvec = static_cast<uint32_t>(a.nvec), lpg = static_cast<uint32_t>(a.S / VE);
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kWG) gn_stats_kernel(GroupNormArgs a) {
 
 // slabs' statistics -> mean and rstd of every (n, g); one wave each
 __global__ void __launch_bounds__(64) gn_finalize_kernel(GroupNormArgs a) {
-    const int64_t n = blockIdx.x / a.G, g = blockIdx.x % a.G;
+    const int64_t n = blockIdx.y, g = blockIdx.x, ng = n * a.G + g;
     Stat s = {0.0f, 0.0f, 0.0f};
     for (int64_t i = threadIdx.x; i < a.nslab; i += 64) {
         const float *p = a.part + ((n * a.nslab + i) * a.G + g) * 2;
@@ -238,8 +238,8 @@ __global__ void __launch_bounds__(64) gn_finalize_kernel(GroupNormArgs a) {
         s = (threadIdx.x & o) ? merge(q, s) : merge(s, q);
     }
     if (threadIdx.x == 0) {
-        a.mean[blockIdx.x] = s.mean;
-        a.rstd[blockIdx.x] = 1.0f / sqrtf(s.m2 / (static_cast<float>(a.L) * static_cast<float>(a.S)) + a.eps);
+        a.mean[ng] = s.mean;
+        a.rstd[ng] = 1.0f / sqrtf(s.m2 / (static_cast<float>(a.L) * static_cast<float>(a.S)) + a.eps);
     }
 }
 
@@ -269,14 +269,14 @@ __global__ void __launch_bounds__(kWG) gn_apply_kernel(GroupNormArgs a) {
 }
 
 // ---- backward, L = 1, groups that fit a team's registers.  A workgroup keeps its groups and
-// walks rows, so each lane sums dw and db of its own channels: blockIdx = (rows, groups)
+// walks rows, so each lane sums dw and db of its own channels: blockIdx = (groups, rows)
 template <class T, int VE, int MAXV, bool WG>
 __global__ void __launch_bounds__(kWG) gn_bwd_team_kernel(GroupNormArgs a) {
     __shared__ float lds[4];
     const int P = WG ? kWG : a.team, tl = threadIdx.x % P, teams = kWG / P;
     const int gb = static_cast<int>(min(static_cast<int64_t>(teams), a.G)), side = teams / gb;   // groups, rows side by side
     const int team = threadIdx.x / P;
-    const int64_t g = static_cast<int64_t>(blockIdx.y) * gb + team % gb, rl = team / gb;
+    const int64_t g = static_cast<int64_t>(blockIdx.x) * gb + team % gb, rl = team / gb;
     const bool on = g < a.G && rl < side;
     const int nvec = static_cast<int>(a.nvec);
     float w[MAXV][VE], b[MAXV][VE], dw[MAXV][VE], db[MAXV][VE];
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kWG) gn_bwd_team_kernel(GroupNormArgs a) {
     }
     const float inv_m = 1.0f / static_cast<float>(a.S);
     // (every lane of a workgroup makes the same number of turns: the team sums are collective)
-    for (int64_t n0 = static_cast<int64_t>(blockIdx.x) * side; n0 < a.N; n0 += static_cast<int64_t>(gridDim.x) * side) {
+    for (int64_t n0 = static_cast<int64_t>(blockIdx.y) * side; n0 < a.N; n0 += static_cast<int64_t>(gridDim.y) * side) {
         const int64_t n = n0 + rl;
         const bool row = on && n < a.N;
         const int64_t base = n * a.C + g * a.S;
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kWG) gn_bwd_team_kernel(GroupNormArgs a) {
             }
     }
     if (!a.part || !on) return;
-    float *p = a.part + (static_cast<int64_t>(blockIdx.x) * side + rl) * 2 * a.C + g * a.S;
+    float *p = a.part + (static_cast<int64_t>(blockIdx.y) * side + rl) * 2 * a.C + g * a.S;
 #pragma unroll
     for (int i = 0; i < MAXV; ++i) {
         const int e = tl + i * P;
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(1024) gn_column_sum_kernel(const float *part, 
 
 // sums [N][2 C] of g xh and g -> per (n, g) the two sums of dx, over M; one wave each
 __global__ void __launch_bounds__(64) gn_bwd_group_kernel(GroupNormArgs a) {
-    const int64_t n = blockIdx.x / a.G, g = blockIdx.x % a.G;
+    const int64_t n = blockIdx.y, g = blockIdx.x, ng = n * a.G + g;
     const float *p = a.sums + n * 2 * a.C + g * a.S;
     float s1 = 0.0f, s2 = 0.0f;
     for (int64_t c = threadIdx.x; c < a.S; c += 64) {
@@ -453,8 +453,8 @@ __global__ void __launch_bounds__(64) gn_bwd_group_kernel(GroupNormArgs a) {
     }
     if (threadIdx.x == 0) {
         const float m = static_cast<float>(a.L) * static_cast<float>(a.S);
-        a.gsum[2 * blockIdx.x] = s1 / m;
-        a.gsum[2 * blockIdx.x + 1] = s2 / m;
+        a.gsum[2 * ng] = s1 / m;
+        a.gsum[2 * ng + 1] = s2 / m;
     }
 }
 
@@ -497,8 +497,9 @@ dim3 blocks(const GroupNormArgs &a, int64_t columns) {
 template <class T, int VE>
 hipError_t fwd_typed(const GroupNormArgs &a, hipStream_t s) {
     if (a.team > 0) {
-        const int64_t teams = a.N * a.G;
-        const dim3 grid(static_cast<unsigned>((teams * a.team + kWG - 1) / kWG));
+        // (a launch's threads along one axis are counted in 32 bits)
+        const int64_t n = (a.N * a.G * a.team + kWG - 1) / kWG, across = n < (1 << 20) ? n : 1 << 20;
+        const dim3 grid(static_cast<unsigned>(across), static_cast<unsigned>((n + across - 1) / across));
         if (a.team == kWG) hipLaunchKernelGGL((gn_team_kernel<T, VE, 8, true>), grid, dim3(kWG), 0, s, a);
         else if (a.nvec <= a.team) hipLaunchKernelGGL((gn_team_kernel<T, VE, 1, false>), grid, dim3(kWG), 0, s, a);
         else hipLaunchKernelGGL((gn_team_kernel<T, VE, 4, false>), grid, dim3(kWG), 0, s, a);
@@ -508,7 +509,7 @@ hipError_t fwd_typed(const GroupNormArgs &a, hipStream_t s) {
     hipLaunchKernelGGL((gn_stats_kernel<T, VE>), blocks(a, (a.G + gpb - 1) / gpb), dim3(kWG), 0, s, a);
     hipError_t e = launch_status(s);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(gn_finalize_kernel, dim3(static_cast<unsigned>(a.N * a.G)), dim3(64), 0, s, a);
+    hipLaunchKernelGGL(gn_finalize_kernel, dim3(static_cast<unsigned>(a.G), static_cast<unsigned>(a.N)), dim3(64), 0, s, a);
     e = launch_status(s);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((gn_apply_kernel<T, VE>), blocks(a, (a.C / VE + kWG - 1) / kWG), dim3(kWG), 0, s, a);
@@ -519,7 +520,7 @@ template <class T, int VE>
 hipError_t bwd_typed(const GroupNormArgs &a, hipStream_t s) {
     if (a.team > 0) {
         const int64_t teams = kWG / a.team, gb = teams < a.G ? teams : a.G;
-        const dim3 grid(static_cast<unsigned>(a.nslab), static_cast<unsigned>((a.G + gb - 1) / gb));
+        const dim3 grid(static_cast<unsigned>((a.G + gb - 1) / gb), static_cast<unsigned>(a.nslab));
         if (a.team < kWG) hipLaunchKernelGGL((gn_bwd_team_kernel<T, VE, 1, false>), grid, dim3(kWG), 0, s, a);
         else if (a.nvec <= kWG) hipLaunchKernelGGL((gn_bwd_team_kernel<T, VE, 1, true>), grid, dim3(kWG), 0, s, a);
         else hipLaunchKernelGGL((gn_bwd_team_kernel<T, VE, 2, true>), grid, dim3(kWG), 0, s, a);
@@ -542,7 +543,7 @@ hipError_t bwd_typed(const GroupNormArgs &a, hipStream_t s) {
         e = launch_status(s);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(gn_bwd_group_kernel, dim3(static_cast<unsigned>(a.N * a.G)), dim3(64), 0, s, a);
+    hipLaunchKernelGGL(gn_bwd_group_kernel, dim3(static_cast<unsigned>(a.G), static_cast<unsigned>(a.N)), dim3(64), 0, s, a);
     e = launch_status(s);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((gn_bwd_apply_kernel<T, VE>), grid, dim3(kWG), 0, s, a);

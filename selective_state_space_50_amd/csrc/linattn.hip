@@ -1038,13 +1038,13 @@ __global__ void __launch_bounds__(64) linattn_age_sum_kernel(const float *part, 
 // per-head gradients [rows][H][D] fp32 -> [rows][G][D], summed over the heads of a group in order
 template <class T>
 __global__ void __launch_bounds__(256) linattn_share_kernel(const float *part, T *out, int64_t n, int64_t G, int64_t D, int64_t per) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= n) return;
-    const int64_t d = i % D, g = i / D % G, row = i / (D * G);
-    const float *p = part + (row * G + g) * per * D + d;
-    float s = 0.0f;
-    for (int64_t j = 0; j < per; ++j) s += p[j * D];
-    put(out, i, s);
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t d = i % D, g = i / D % G, row = i / (D * G);
+        const float *p = part + (row * G + g) * per * D + d;
+        float s = 0.0f;
+        for (int64_t j = 0; j < per; ++j) s += p[j * D];
+        put(out, i, s);
+    }
 }
 
 // One token: every state element is read and written once, so the launch is bound by the
@@ -1162,7 +1162,7 @@ hipError_t launch_linattn_age_sum(const LinAttnArgs &a, float *dlog_decay, hipSt
 
 hipError_t launch_linattn_share(const float *part, void *out, int64_t rows, int64_t H, int64_t G, int64_t D, bool bf16, hipStream_t s) {
     const int64_t n = rows * G * D;
-    const dim3 grid(static_cast<unsigned>((n + 255) / 256));
+    const dim3 grid(static_cast<unsigned>(n < (int64_t(1) << 30) ? (n + 255) / 256 : int64_t(1) << 22));
     if (bf16) hipLaunchKernelGGL((linattn_share_kernel<uint16_t>), grid, dim3(256), 0, s, part, static_cast<uint16_t *>(out), n, G, D, H / G);
     else hipLaunchKernelGGL((linattn_share_kernel<float>), grid, dim3(256), 0, s, part, static_cast<float *>(out), n, G, D, H / G);
     return launch_status(s);

@@ -1185,10 +1185,16 @@ void linattn_split(LinAttnArgs &a, const LinAttnPlan::Sweep &w, void *workspace)
 }
 
 int fill_floats(float *out, const float *from, int64_t n, hipStream_t s) {
-    if (!out || n <= 0) return SSM_OK;
-    hipLaunchKernelGGL(fill_state_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, s, out, from, n);
-    const hipError_t e = launch_status(s);
-    return e == hipSuccess ? SSM_OK : hip_fail("fill launch", e);
+    // (a launch's threads are counted in 32 bits)
+    constexpr int64_t most = int64_t(1) << 30;
+    for (int64_t at = 0; out && at < n; at += most) {
+        const int64_t m = n - at < most ? n - at : most;
+        hipLaunchKernelGGL(fill_state_kernel, dim3(static_cast<unsigned>((m + 255) / 256)), dim3(256), 0, s, out + at,
+                           from ? from + at : nullptr, m);
+        const hipError_t e = launch_status(s);
+        if (e != hipSuccess) return hip_fail("fill launch", e);
+    }
+    return SSM_OK;
 }
 }  // namespace
 }  // namespace ssm

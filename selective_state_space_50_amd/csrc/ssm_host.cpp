@@ -862,9 +862,9 @@ int plan_linattn(const ssm_linattn_shape *s, bool decay_grad, LinAttnPlan *plan)
         set_error("dk=%lld, dv=%lld: at most %d is supported", (long long)s->dk, (long long)s->dv, SSM_LINATTN_MAX_DIM);
         return SSM_EUNSUPPORTED;
     }
-    // sizes: one launch's workgroups and every index within 64 bits with room to spare
+    // sizes: a launch's threads (counted in 32 bits), and every index within 64 bits with room to spare
     if (s->batch > (int64_t(1) << 31) || s->seqlen > (int64_t(1) << 30) || s->nheads > (int64_t(1) << 16) ||
-        (s->nheads > 0 && s->batch > (int64_t(1) << 22) / s->nheads) ||
+        (s->nheads > 0 && s->batch > (int64_t(1) << 20) / s->nheads) ||
         (s->batch > 0 && s->nheads > 0 && s->seqlen > kMaxElems / (s->batch * s->nheads * SSM_LINATTN_MAX_DIM))) {
         set_error("shape too large for one launch (batch=%lld, seqlen=%lld, nheads=%lld)", (long long)s->batch,
                   (long long)s->seqlen, (long long)s->nheads);
@@ -1043,7 +1043,8 @@ int plan_groupnorm(int64_t batch, int64_t seqlen, int64_t dim, int64_t groups, i
         plan->ws_bytes = static_cast<size_t>(plan->nslab * side * 2 * dim) * sizeof(float);
         return SSM_OK;
     }
-    if (batch > 65535 || ceil_div(dim, ve) / wg > 65535) {
+    const int64_t lpg = s / ve, gpb = lpg >= wg ? 1 : wg / lpg;   // groups of one workgroup's statistics
+    if (batch > 65535 || ceil_div(ceil_div(dim, ve), wg) > 65535 || ceil_div(groups, gpb) > 65535) {
         set_error("batch=%lld rows of large groups, or dim=%lld: too many for one launch", (long long)batch, (long long)dim);
         return SSM_EUNSUPPORTED;
     }

@@ -227,3 +227,16 @@ def test_captured_and_other_stream(ssm):
         torch.cuda.synchronize()
         for j, (t, r) in enumerate(zip(held, ref)):
             assert torch.equal(t, r), (i, j)
+
+
+def test_more_threads_than_32_bits_count(ssm):
+    """2^26 + 64 groups of 33 channels, a wave each: the last rows are those of a small call."""
+    import torch
+    rows, G = (1 << 20) + 1, 64
+    x = torch.empty(rows, 33 * G, device="cuda", dtype=torch.bfloat16)
+    x.view(-1)[-20 * 33 * G:] = torch.randn(20 * 33 * G, device="cuda").bfloat16()
+    x[:-20] = x[-1]
+    y, mean, rstd = ssm.groupnorm_fwd(x, G, return_stats=True)
+    ref = ssm.groupnorm_fwd(x[-20:].clone(), G, return_stats=True)
+    for a, b in zip((y, mean, rstd), ref):
+        assert torch.equal(a[-20:], b) and torch.equal(a[:1000], b[-1:].expand(1000, -1))

@@ -342,3 +342,22 @@ def test_rows_that_miss_16_bytes(ssm, dt, extra, which):
     for n in whole:
         assert torch.equal(g[n], whole[n]), n
     assert torch.equal(ssm.linattn_fwd(args["q"], args["k"], args["v"], args["a"], args["h0"]), y)
+
+
+def test_shared_gradients_past_2_to_30(ssm):
+    """dq of 131073 tokens, 32 heads of 256, each shared by two: the last token's is that of a call of its own, as
+    nothing is carried from token to token."""
+    import torch
+    L, H, hq = 131073, 64, 32
+    q = torch.ones(1, L, hq, 256, device="cuda", dtype=torch.bfloat16)
+    k = torch.randn(1, 1, 1, 256, device="cuda").bfloat16().expand(1, L, 1, 256).contiguous()
+    v = torch.randn(1, 1, 1, 8, device="cuda").bfloat16().expand(1, L, 1, 8).contiguous()
+    dy = torch.ones(1, L, H, 8, device="cuda", dtype=torch.bfloat16)
+    dy[:, -1] = torch.randn(H, 8, device="cuda").bfloat16()
+    a = torch.full((H,), -float("inf"), device="cuda")
+    g = ssm.linattn_bwd(q, k, v, a, dy=dy, need_dlog_decay=False)["dq"]
+    tail = [t[:, -2:].contiguous() for t in (q, k, v, dy)]
+    ref = ssm.linattn_bwd(*tail[:3], a, dy=tail[3], need_dlog_decay=False)["dq"]
+    # (both round the same value, in different orders of sums: one step of bf16)
+    assert torch.allclose(g[:, -2:].float(), ref.float(), rtol=2.0 ** -7, atol=1e-5)
+    assert torch.equal(g[:, :1], g[:, 70000:70001])

@@ -82,3 +82,9 @@ def test_binding_refuses(lib):
         ssm.groupnorm_fwd(x, 2, activation="relu")
     with pytest.raises(ValueError, match="x must be"):
         ssm.groupnorm_fwd(x[None], 2)
+
+
+def test_blocks_of_one_launch(lib):
+    """Groups just wider than half a workgroup take one each, and a launch has 65535 of them across."""
+    assert fwd(lib, N=1, L=100, C=129 * 100000, G=100000) == 2 and b"too many" in lib.ssm_last_error()
+    assert fwd(lib, N=1, L=100, C=129 * 65000, G=65000, x=None) == 1 and b"x is NULL" in lib.ssm_last_error()

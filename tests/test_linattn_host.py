@@ -142,3 +142,11 @@ def test_strided_rows():
             rows(bad, 2, 5)
     with pytest.raises(ValueError, match="shape"):
         rows(s, 2, 4)
+
+
+def test_rows_of_one_launch(lib):
+    """Batch rows times heads: a launch's threads are counted in 32 bits."""
+    s = shape(batch=1 << 18, seqlen=1, nheads=8, q_heads=8, k_heads=8, v_heads=8, dk=1, dv=1)
+    assert fwd(lib, s) == 2 and b"too large" in lib.ssm_last_error()
+    s.batch = 1 << 17
+    assert fwd(lib, s, q=None) == 1 and b"q is NULL" in lib.ssm_last_error()
