@@ -1246,7 +1246,7 @@ extern "C" int ssm_linattn_bwd(const ssm_linattn_shape *shape, const void *q, co
     const int64_t rows = sh.batch * sh.seqlen, dy_row = sh.nheads * sh.dv;
     log_call("linattn backward B=%lld L=%lld H=%lld dk=%lld dv=%lld dtype=%d: %lld and %lld segments", (long long)sh.batch,
              (long long)sh.seqlen, (long long)sh.nheads, (long long)sh.dk, (long long)sh.dv, sh.dtype,
-             (long long)p.bwd.nseg, (long long)p.fwd.nseg);
+             (long long)p.bwd.nseg, (long long)p.dv.nseg);
     // one sweep, its output summed over the heads that share a row
     auto sweep = [&](LinAttnArgs &a, void *out, int64_t heads) {
         a.out_f32 = heads != sh.nheads;
@@ -1293,10 +1293,8 @@ extern "C" int ssm_linattn_bwd(const ssm_linattn_shape *shape, const void *q, co
         a.v = dy; a.v_heads = sh.nheads; a.v_row = dy_row;
         a.h0 = dh_last; a.h_last = dh0;
         a.reverse = 1; a.s_in = scale; a.s_wr = scale;
-        linattn_split(a, p.fwd, workspace);
-        // cut into the same parts as dk's sweep, it starts from the same states, transposed
-        if (p.fwd.nseg == p.bwd.nseg && p.fwd.seg_len == p.bwd.seg_len) {
-            a.nsub = p.bwd.nsub;
+        linattn_split(a, p.dv, workspace);
+        if (p.dv.given) {   // dk's states, transposed
             a.have_states = 1;
             a.ws_sr = 1; a.ws_sc = sh.dk;
         }

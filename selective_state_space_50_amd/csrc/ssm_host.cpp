@@ -797,36 +797,57 @@ namespace {
 // Segments of one sweep.  A workgroup holds one CU (its LDS tiles), and walks its segment's
 // chunks in order, so a launch takes ceil(workgroups / CUs) rounds of a segment's chunks; more
 // than one segment costs a first pass over k and v for the segments' own states, whose chunk
-// takes about 0.4 of the sweep's.  The least of that sum is taken.  That pass cuts a segment
-// further, until it has a workgroup for every CU (B2 L4096 H32 128x128 bf16, two segments: one part
-// each 46 us, two 25 us; four, two workgroups to a CU: 28 us), but not under eight chunks, as
-// every part writes a state.
+// takes about 0.4 of the sweep's, and their joining.  The least of the estimated time is taken,
+// in microseconds as measured: a chunk 2, 3.2 or 6.5 (contraction over 64, 128, 256 columns; three
+// times that in fp32), 4 before the first chunk of a sweep and 3 of a first pass, 9 for two more
+// launches.  (B2 L777 H8 48x72 fp32: two chunks or one to a segment 31 us forward and 123 us
+// backward, four 42 and 196 us.)  The first pass cuts a segment further, until it has a workgroup for every CU (B2 L4096
+// H32 128x128 bf16, two segments: one part each 46 us, two 25 us; four, two workgroups to a CU:
+// 28 us), but not under eight chunks, as every part writes a state.
 void plan_sweep(int64_t batch, int64_t seqlen, int64_t nheads, int64_t contraction, int64_t columns, int dtype,
-                LinAttnPlan::Sweep *p) {
-    const int64_t rows = dtype == SSM_DTYPE_F32 && contraction > 128 ? 32 : 64;
+                const LinAttnPlan::Sweep *given, LinAttnPlan::Sweep *p) {
+    const bool f32 = dtype == SSM_DTYPE_F32;
+    const int64_t rows = f32 && contraction > 128 ? 32 : 64;
     const int64_t chunks = ceil_div(seqlen, rows);
+    const double chunk = (f32 ? 3.0 : 1.0) * (contraction <= 64 ? 2.0 : contraction <= 128 ? 3.2 : 6.5);
     p->ntiles = ceil_div(columns, 64);
     const int64_t w = batch * nheads * p->ntiles;
+    auto sweep = [&](int64_t n, int64_t len) {
+        return static_cast<double>(ceil_div(w * n, kCUs)) * (static_cast<double>(len) * chunk + 4.0);
+    };
+    auto parts = [&](int64_t n, int64_t len) {   // of a segment in the first pass
+        const int64_t fill = ceil_div(kCUs, w * (n - 1)), most = ceil_div(len, int64_t(8));
+        return ceil_div(len, ceil_div(len, fill < most ? fill : most));
+    };
     int64_t best = 1;
     double least = 0.0;
     for (int64_t n = 1; n <= 256 && n <= chunks; ++n) {
         const int64_t len = ceil_div(chunks, n);
-        if (n > 1 && (len < 4 || ceil_div(chunks, len) != n)) continue;
-        const double cost = static_cast<double>(ceil_div(w * n, kCUs) * len) + 0.4 * static_cast<double>(w * (n - 1) * len) / kCUs;
+        if (ceil_div(chunks, len) != n) continue;
+        double cost = sweep(n, len);
+        if (n > 1) {
+            const int64_t sub = parts(n, len);
+            cost += 9.0 + static_cast<double>(ceil_div((n - 1) * sub, int64_t(8))) +
+                    static_cast<double>(ceil_div(w * (n - 1) * sub, kCUs)) * (static_cast<double>(ceil_div(len, sub)) * 0.4 * chunk + 3.0);
+        }
         if (n == 1 || cost < 0.95 * least) {
             least = cost;
             best = n;
         }
         if (w * n >= 4 * kCUs) break;
     }
+    const int64_t len = ceil_div(chunks, best);
+    // (given: another sweep's segments, whose start states serve this one, too, transposed)
+    p->given = given && given->nseg > 1 && given->seg_len % rows == 0 && sweep(given->nseg, given->seg_len / rows) < least;
+    if (p->given) {
+        p->nseg = given->nseg; p->seg_len = given->seg_len; p->nsub = given->nsub; p->sub_len = given->sub_len;
+        return;
+    }
     p->nseg = best;
-    p->seg_len = ceil_div(chunks, best) * rows;
+    p->seg_len = len * rows;
     if (best > 1) {
-        const int64_t seg = p->seg_len / rows, most = ceil_div(seg, int64_t(8));
-        int64_t sub = ceil_div(kCUs, w * (best - 1));
-        sub = sub < most ? sub : most;
-        p->sub_len = ceil_div(seg, sub) * rows;
-        p->nsub = ceil_div(p->seg_len, p->sub_len);
+        p->nsub = parts(best, len);
+        p->sub_len = ceil_div(len, p->nsub) * rows;
     }
     p->state_bytes = static_cast<size_t>(batch * nheads * (best - 1) * p->nsub * contraction * columns) * sizeof(float);
 }
@@ -885,10 +906,11 @@ int plan_linattn(const ssm_linattn_shape *s, bool decay_grad, LinAttnPlan *plan)
         }
     }
     if (s->batch == 0 || s->nheads == 0 || s->seqlen == 0) return SSM_OK;
-    plan_sweep(s->batch, s->seqlen, s->nheads, s->dk, s->dv, s->dtype, &plan->fwd);
-    plan_sweep(s->batch, s->seqlen, s->nheads, s->dv, s->dk, s->dtype, &plan->bwd);
+    plan_sweep(s->batch, s->seqlen, s->nheads, s->dk, s->dv, s->dtype, nullptr, &plan->fwd);
+    plan_sweep(s->batch, s->seqlen, s->nheads, s->dv, s->dk, s->dtype, nullptr, &plan->bwd);
+    plan_sweep(s->batch, s->seqlen, s->nheads, s->dk, s->dv, s->dtype, &plan->bwd, &plan->dv);
     plan->ws_bytes = plan->fwd.state_bytes;
-    size_t at = align_up(plan->fwd.state_bytes > plan->bwd.state_bytes ? plan->fwd.state_bytes : plan->bwd.state_bytes, kWsAlign);
+    size_t at = align_up(plan->dv.state_bytes > plan->bwd.state_bytes ? plan->dv.state_bytes : plan->bwd.state_bytes, kWsAlign);
     plan->ws_R_off = at;
     if (decay_grad) at = align_up(at + plan->bwd.state_bytes, kWsAlign);
     plan->age_off = at;

@@ -164,10 +164,12 @@ struct LinAttnPlan {
     struct Sweep {
         int64_t nseg = 1, seg_len = 0, ntiles = 1;
         int64_t nsub = 1, sub_len = 0;   // parts of a segment in the pass for the segments' own states
-        size_t state_bytes = 0;   // one array of the segments' states
+        bool given = false;              // starts from the states of another sweep
+        size_t state_bytes = 0;          // one array of the segments' states (its own)
     };
-    Sweep fwd;                  // y: contraction over dk, dv columns (dv's sweep, too)
+    Sweep fwd;                  // y: contraction over dk, dv columns
     Sweep bwd;                  // dq and dk: contraction over dv, dk columns
+    Sweep dv;                   // as fwd; where it gains, from dk's states
     size_t ws_bytes = 0;        // of the forward
     // backward: states (and their derivatives by log_decay), the shares of dlog_decay, per-head
     // fp32 gradients of rows that several heads share
