@@ -1,0 +1,105 @@
+"""Linear attention, the group norm and the state update as a layer uses them: a training step through autograd
+from slices of one projection to the gated norm of every head, and the same layer token by token, eager and as a graph.
+
+Every stage is checked with the tolerances of its own operator (test_gpu_linattn, test_gpu_groupnorm) against the
+fp64 oracle on the stage's actual inputs, so no tolerance spans two roundings.
+"""
+import numpy as np
+import pytest
+
+import synth
+from oracle.linattn_oracle import linattn, linattn_bwd
+from oracle.norm_oracle import groupnorm, groupnorm_bwd
+from tests import test_gpu_groupnorm as tn
+from tests import test_gpu_linattn as ta
+from tests.gpu_util import to_dev, to_host
+from tests.test_gpu_linattn import ssm  # noqa: F401  (the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def norm_case(y, z, w, b, do=None):
+    """fp64 rows of the norm's inputs."""
+    r = lambda t: None if t is None else to_host(t).astype(np.float64).reshape(-1, 1, w.numel())  # noqa: E731
+    return r(y), to_host(w).astype(np.float64), to_host(b).astype(np.float64), r(z), r(do)
+
+
+@pytest.mark.parametrize("B,L,H,G,dk,dv,dt,lengths", [
+    (2, 200, 4, 4, 32, 64, "bf16", None), (1, 1, 2, 1, 16, 16, "f32", None), (3, 77, 6, 2, 40, 24, "f32", [77, 0, 30]),
+    (1, 900, 2, 2, 128, 128, "bf16", None)])
+def test_training_step(ssm, B, L, H, G, dk, dv, dt, lengths):  # noqa: F811
+    import torch
+    c = ta.make(B, L, H, G, G, H, dk, dv, dt, seed=L)
+    r = np.random.default_rng(1)
+    tdt = torch.bfloat16 if dt == "bf16" else torch.float32
+    x = torch.cat([to_dev(c[n], dt).flatten(2) for n in ("q", "k", "v")], -1).requires_grad_()
+    a = torch.from_numpy(c["a"]).cuda().requires_grad_()
+    w, b = (torch.from_numpy(r.standard_normal(H * dv).astype(np.float32)).cuda().requires_grad_() for _ in range(2))
+    z, do = (torch.from_numpy(r.standard_normal((B, L, H * dv)).astype(np.float32)).cuda().to(tdt) for _ in range(2))
+    z.requires_grad_()
+    n = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    q, k, v = (t.unflatten(-1, (-1, d)) for t, d in zip(x.split([G * dk, G * dk, H * dv], -1), (dk, dk, dv)))
+    y = ssm.linear_attention(q, k, v, a, scale=0.3, lengths=n)
+    y.retain_grad()
+    o = ssm.group_norm(y.flatten(2), H, w, b, z)
+    o.backward(do)
+    torch.cuda.synchronize()
+    (yr, _), (ya, _) = ta.both(linattn, c, ("q", "k", "v", "a", 0.3, None), lengths=lengths)
+    ta.check(y.detach(), yr, ya, dt, c, "y")
+    ys, ws, bs, zs, dos = norm_case(y.detach(), z.detach(), w.detach(), b.detach(), do)
+    lim = tn.bounds(ys, H, ws, bs, zs, dos, False)
+    tn.check(o.detach(), groupnorm(ys, H, ws, bs, zs, 1e-5, False), lim["y"], dt, "o")
+    ref = groupnorm_bwd(ys, H, ws, bs, zs, dos, 1e-5, False)
+    for name, t in (("dx", y.grad), ("dz", z.grad), ("dw", w.grad), ("dbias", b.grad)):
+        tn.check(t, ref[name], lim[name], dt if name in ("dx", "dz") else "f32", name)
+    c["dy"] = synth.store(to_host(y.grad).astype(np.float32), dt)   # (exact: its own type's values)
+    ref, big = ta.both(linattn_bwd, c, ("q", "k", "v", "a", 0.3, None, "dy", None), lengths=lengths)
+    got = dict(zip(("dq", "dk", "dv"), (t.unflatten(-1, (-1, d)) for t, d in
+                                        zip(x.grad.split([G * dk, G * dk, H * dv], -1), (dk, dk, dv)))))
+    for name in got:
+        ta.check(got[name].contiguous(), ref[name], big[name], dt, c, name)
+    ta.check(a.grad, ref["dlog_decay"], big["dlog_decay"], "f32", c, "dlog_decay")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_prompt_then_tokens(ssm, dt):  # noqa: F811
+    """A prompt, then tokens one at a time: linear attention of the whole sequence, and its norm."""
+    import torch
+    B, L, P, H, dk, dv = 2, 70, 65, 4, 64, 32
+    c = ta.make(B, L, H, H, 2, 2, dk, dv, dt, seed=9)
+    q, k, v, a = ta.dev(c, "q", "k", "v", "a")
+    w, b = (torch.randn(H * dv, device="cuda") for _ in range(2))
+    z = torch.randn(B, L, H * dv, device="cuda").to(q.dtype)
+    y, h = ssm.linattn_fwd(*(t[:, :P].contiguous() for t in (q, k, v)), a, return_last_state=True)
+    h0 = h.clone()
+    # the token's work, eager and as a graph over fixed buffers
+    t1 = [t[:, P].contiguous() for t in (q, k, v, z)]
+
+    def token():
+        s = ssm.linattn_update(h, *t1[:3], a)
+        return s, ssm.groupnorm_fwd(s.flatten(1), H, w, b, t1[3])
+
+    eager = []
+    for t in range(P, L):
+        for buf, full in zip(t1, (q, k, v, z)):
+            buf.copy_(full[:, t])
+        eager.append([r.clone() for r in token()])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = token()
+    h.copy_(h0)
+    for t in range(P, L):
+        for buf, full in zip(t1, (q, k, v, z)):
+            buf.copy_(full[:, t])
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, ref in zip(held, eager[t - P]):
+            assert torch.equal(got, ref), t
+    (yr, hr), (ya, ha) = ta.both(linattn, c, ("q", "k", "v", "a", dk ** -0.5, None))
+    ta.check(torch.cat([y, torch.stack([e[0] for e in eager], 1)], 1), yr, ya, dt, c, "y")
+    ta.check(h, hr, ha, "f32", c, "h")
+    for t in range(P, L):
+        ys, ws, bs, zs, _ = norm_case(eager[t - P][0], z[:, t].contiguous(), w, b)
+        tn.check(eager[t - P][1], groupnorm(ys, H, ws, bs, zs, 1e-5, False), tn.bounds(ys, H, ws, bs, zs, np.zeros(1), False)["y"],
+                 dt, "o")
