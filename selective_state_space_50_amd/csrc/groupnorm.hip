@@ -16,6 +16,8 @@
 // which gives dw and db and, weighted with w, both sums of dx.
 #include "ssm_device.h"
 
+#include <type_traits>
+
 namespace ssm {
 namespace {
 
@@ -108,11 +110,12 @@ __device__ __forceinline__ float team_sum(float v, int P, float *lds) {
 }
 
 // ---- groups that fit a team's registers: lane t of the team holds the vectors t, t + P, ...
-template <class T, int VE, int MAXV, bool WG>
+// (ONE: L = 1, no division for the place of a vector)
+template <class T, int VE, int MAXV, bool WG, bool ONE>
 __global__ void __launch_bounds__(kWG) gn_team_kernel(GroupNormArgs a) {
     __shared__ float lds[4];
-    const int P = WG ? kWG : a.team, tl = threadIdx.x % P;
-    const uint32_t team = (blockIdx.y * gridDim.x + blockIdx.x) * (kWG / P) + threadIdx.x / P;
+    const int P = WG ? kWG : a.team, sh = __builtin_ctz(P), tl = threadIdx.x & (P - 1);   // (a power of two)
+    const uint32_t team = (blockIdx.y * gridDim.x + blockIdx.x) * (kWG >> sh) + (threadIdx.x >> sh);
     const bool on = team < static_cast<uint32_t>(a.N * a.G);
     const uint32_t G = static_cast<uint32_t>(a.G), n = (on ? team : 0) / G, g = (on ? team : 0) % G;
     const uint32_t nvec = static_cast<uint32_t>(a.nvec), lpg = static_cast<uint32_t>(a.S / VE);
@@ -123,7 +126,7 @@ __global__ void __launch_bounds__(kWG) gn_team_kernel(GroupNormArgs a) {
     bool in[MAXV];
 #pragma unroll
     for (int i = 0; i < MAXV; ++i) {
-        const uint32_t e = tl + i * P, l = a.L == 1 ? 0 : e / lpg, j = a.L == 1 ? e : e % lpg;
+        const uint32_t e = tl + i * P, l = ONE ? 0 : e / lpg, j = ONE ? e : e % lpg;
         in[i] = on && e < nvec;
         ch[i] = j * VE;
         off[i] = in[i] ? l * static_cast<uint32_t>(a.C) + ch[i] : 0;
@@ -139,7 +142,7 @@ __global__ void __launch_bounds__(kWG) gn_team_kernel(GroupNormArgs a) {
     for (int i = 0; i < MAXV; ++i)
 #pragma unroll
         for (int k = 0; k < VE; ++k) s += v[i].v[k];
-    const float inv_m = 1.0f / static_cast<float>(a.L * a.S);
+    const float inv_m = a.inv_m;
     const float mean = team_sum<WG>(s, P, lds) * inv_m;
     s = 0.0f;
 #pragma unroll
@@ -273,9 +276,9 @@ __global__ void __launch_bounds__(kWG) gn_apply_kernel(GroupNormArgs a) {
 template <class T, int VE, int MAXV, bool WG>
 __global__ void __launch_bounds__(kWG) gn_bwd_team_kernel(GroupNormArgs a) {
     __shared__ float lds[4];
-    const int P = WG ? kWG : a.team, tl = threadIdx.x % P, teams = kWG / P;
+    const int P = WG ? kWG : a.team, sh = __builtin_ctz(P), tl = threadIdx.x & (P - 1), teams = kWG >> sh;
     const int gb = static_cast<int>(min(static_cast<int64_t>(teams), a.G)), side = teams / gb;   // groups, rows side by side
-    const int team = threadIdx.x / P;
+    const int team = threadIdx.x >> sh;
     const int64_t g = static_cast<int64_t>(blockIdx.x) * gb + team % gb, rl = team / gb;
     const bool on = g < a.G && rl < side;
     const int nvec = static_cast<int>(a.nvec);
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(kWG) gn_bwd_team_kernel(GroupNormArgs a) {
             channels<VE>(a.b, g * a.S + e * VE, 0.0f, b[i]);
         }
     }
-    const float inv_m = 1.0f / static_cast<float>(a.S);
+    const float inv_m = a.inv_m;
     // (every lane of a workgroup makes the same number of turns: the team sums are collective)
     for (int64_t n0 = static_cast<int64_t>(blockIdx.y) * side; n0 < a.N; n0 += static_cast<int64_t>(gridDim.y) * side) {
         const int64_t n = n0 + rl;
@@ -500,9 +503,14 @@ hipError_t fwd_typed(const GroupNormArgs &a, hipStream_t s) {
         // (a launch's threads along one axis are counted in 32 bits)
         const int64_t n = (a.N * a.G * a.team + kWG - 1) / kWG, across = n < (1 << 20) ? n : 1 << 20;
         const dim3 grid(static_cast<unsigned>(across), static_cast<unsigned>((n + across - 1) / across));
-        if (a.team == kWG) hipLaunchKernelGGL((gn_team_kernel<T, VE, 8, true>), grid, dim3(kWG), 0, s, a);
-        else if (a.nvec <= a.team) hipLaunchKernelGGL((gn_team_kernel<T, VE, 1, false>), grid, dim3(kWG), 0, s, a);
-        else hipLaunchKernelGGL((gn_team_kernel<T, VE, 4, false>), grid, dim3(kWG), 0, s, a);
+        auto launch = [&](auto one) {
+            constexpr bool ONE = decltype(one)::value;
+            if (a.team == kWG) hipLaunchKernelGGL((gn_team_kernel<T, VE, 8, true, ONE>), grid, dim3(kWG), 0, s, a);
+            else if (a.nvec <= a.team) hipLaunchKernelGGL((gn_team_kernel<T, VE, 1, false, ONE>), grid, dim3(kWG), 0, s, a);
+            else hipLaunchKernelGGL((gn_team_kernel<T, VE, 4, false, ONE>), grid, dim3(kWG), 0, s, a);
+        };
+        if (a.L == 1) launch(std::true_type{});
+        else launch(std::false_type{});
         return launch_status(s);
     }
     const int64_t lpg = a.S / VE, gpb = lpg >= kWG ? 1 : kWG / lpg;
@@ -552,12 +560,16 @@ hipError_t bwd_typed(const GroupNormArgs &a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_groupnorm_fwd(const GroupNormArgs &a, bool bf16, bool vec, hipStream_t s) {
+hipError_t launch_groupnorm_fwd(const GroupNormArgs &a0, bool bf16, bool vec, hipStream_t s) {
+    GroupNormArgs a = a0;
+    a.inv_m = 1.0f / (static_cast<float>(a.L) * static_cast<float>(a.S));
     if (bf16) return vec ? fwd_typed<uint16_t, 8>(a, s) : fwd_typed<uint16_t, 1>(a, s);
     return vec ? fwd_typed<float, 4>(a, s) : fwd_typed<float, 1>(a, s);
 }
 
-hipError_t launch_groupnorm_bwd(const GroupNormArgs &a, bool bf16, bool vec, hipStream_t s) {
+hipError_t launch_groupnorm_bwd(const GroupNormArgs &a0, bool bf16, bool vec, hipStream_t s) {
+    GroupNormArgs a = a0;
+    a.inv_m = 1.0f / (static_cast<float>(a.L) * static_cast<float>(a.S));
     if (bf16) return vec ? bwd_typed<uint16_t, 8>(a, s) : bwd_typed<uint16_t, 1>(a, s);
     return vec ? bwd_typed<float, 4>(a, s) : bwd_typed<float, 1>(a, s);
 }

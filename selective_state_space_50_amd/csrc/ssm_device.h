@@ -142,6 +142,7 @@ struct GroupNormArgs {
     void *y, *dx, *dz;
     float *mean, *rstd;              // [N, G]: written by the forward (null: not stored), read by the backward
     float *dw, *db;                  // [C] or null
+    float inv_m = 0.0f;              // 1 / (L S), set by the launcher
     int team = 0;                    // lanes that hold one group (256: a workgroup); 0: slabs of rows
     int64_t nvec = 0;                // vectors of one group
     int64_t nslab = 1, slab_rows = 0;   // slabs (the backward with teams: workgroups along the rows)
