@@ -464,6 +464,12 @@ __device__ __forceinline__ void fill_update_weights(float (&up)[2][Q], float *ag
 // ahead.  Two barriers a chunk.  A state's rows are never read twice and nothing is computed twice: with
 // all eight waves in one role (half a state each) the weights of v and the sum of two output
 // shares cost a third more VALU instructions and LDS traffic.
+//
+// Measured: B4 L4096 H64 128x64 bf16 (one segment, 256 workgroups) 184 us, 4.4 TB/s; a copy reaches 5.2.
+// Chunks of 64 take 2.9 us (128 columns): per SIMD 1.1 us of VALU and 0.7 us of matrix instructions,
+// in two roles that meet at two barriers; without any product the same loads and stores take 168 us.
+// Smaller chunks would cost more state updates, larger ones more in-chunk products and LDS (115 KB now).
+// AGE doubles the readout and the update (dq of B2 L4096 H32 128x128: 176 us against 105).
 template <class T, int DK, bool AGE>
 struct __align__(16) Smem {
     using G = Tile<T, DK>;
@@ -572,6 +578,10 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
         if constexpr (kB > 1)
             if (t0 < end) chunk(t0, std::integral_constant<int, 0>{}, std::false_type{});
     };
+    // With two buffers the next chunk is staged first thing (its buffer's last readers passed the barrier
+    // before), beside the products instead of after them: B2 L4096 H32 128x128 bf16, forward and
+    // backward, 533 -> 525 us.  (Single elements: at the end, else their addresses spill.)
+    constexpr bool kEarly = kB == 2 && VEC;
     auto next_rows = [&](int t0, auto which, auto further) __attribute__((always_inline)) {
         constexpr int nbuf = (decltype(which)::value + 1) % kB, next = (decltype(which)::value + 1) % PF;
         if constexpr (kB == 1) __syncthreads();   // this chunk's rows read
@@ -617,6 +627,7 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
         walk([&](int t0, auto which, auto further) __attribute__((always_inline)) {
             constexpr int buf = decltype(which)::value;
             const int m = min(Q, end - t0);
+            if constexpr (kEarly) next_rows(t0, which, further);
             // ---- the carried state's readout, y^T: lane column n = 4 lg + j, row t = lr
             f4 acc[NB], acca[AGE ? NB : 1];
 #pragma unroll
@@ -662,7 +673,7 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
             for (int j = 0; j < Q / 16; ++j) vp[j] = O::one(buf * VB + 16 * j * G::kVRow, voff);
             const Lds last = m == Q ? 0 : 4 * Q;
             update_state<T, Q, G::kRow, NT, AGE, G::kAhead && !AGE>(S, R, 0, buf * KB, koff, vp, wup + last, wage + last, m == Q ? full : part, m);
-            next_rows(t0, which, further);
+            if constexpr (!kEarly) next_rows(t0, which, further);
             __syncthreads();   // the next chunk staged
         });
 
@@ -775,6 +786,7 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
             if constexpr (AGE)
 #pragma unroll
                 for (int i = 0; i < NB; ++i) age_g[i] = age_factor(t0 + 16 * i + lr);
+            if constexpr (kEarly) next_rows(t0, which, further);
             // ---- tiles of (q k^T)^T with their decay
             {
                 f4 g[3];
@@ -877,7 +889,7 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) age = __builtin_fmaf(acca[i][j], g[j], age);
                 }
-            next_rows(t0, which, further);
+            if constexpr (!kEarly) next_rows(t0, which, further);
             __syncthreads();   // the next chunk staged
         });
     }
@@ -895,7 +907,8 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
 
 // ---- the segments' own contributions to the state (from zero), into the workspace, in nsub parts of a
 // segment that run side by side: eight waves, wave w value columns 16 (w % 4) .. + 15 and half w / 4 of
-// the contraction columns
+// the contraction columns.  B1 L32768 H16 128x128 bf16 (7 of 8 segments, two parts each): 77 us, 3.1 TB/s,
+// bound by the loads' latency at one or two workgroups a CU.
 template <class T, int DK, bool AGE, bool VEC>
 __global__ void __launch_bounds__(kThreads) linattn_state_kernel(LinAttnArgs a) {
     using G = Tile<T, DK>;
@@ -1048,11 +1061,13 @@ __global__ void __launch_bounds__(256) linattn_share_kernel(const float *part, T
 }
 
 // One token: every state element is read and written once, so the launch is bound by the
-// state's traffic.  A workgroup takes CW value columns of one (b, h); thread: four columns
-// (16 bytes) of every (1024 / CW)-th contraction row.
-template <class T, int CW>
+// state's traffic.  A workgroup takes 64 value columns of one (b, h); thread: four columns (16
+// bytes) of every sixteenth contraction row.  (B256 H32 128x64 bf16: 85 us, 6.3 TB/s of state, some of it
+// from the Infinity Cache; 16 columns to a workgroup 138 us, and where that fills more CUs 6.7 against
+// 5.2 us (B4), 5.3 against 4.9 us (B1, 128x128), 4.0 against 4.2 us (B1 H16 64x64).)
+template <class T>
 __global__ void __launch_bounds__(256) linattn_update_kernel(LinAttnArgs a) {
-    constexpr int C4 = CW / 4, RG = 256 / C4;
+    constexpr int CW = kN, C4 = CW / 4, RG = 256 / C4;
     __shared__ float red[4][CW];
     __shared__ float qs[256], ks[256];
     const int tid = threadIdx.x, c4 = tid % C4, rg = tid / C4;
@@ -1171,17 +1186,9 @@ hipError_t launch_linattn_share(const float *part, void *out, int64_t rows, int6
 hipError_t launch_linattn_update(const LinAttnArgs &a0, bool bf16, hipStream_t s) {
     LinAttnArgs a = a0;
     a.y_vec = a.dn % 4 == 0;
-    // 16 columns to a workgroup while that leaves CUs without one at 64
-    const bool narrow = a.B * a.H * ((a.dn + 63) / 64) < kCUs;
-    const int64_t cw = narrow ? 16 : 64;
-    const dim3 grid(static_cast<unsigned>(a.B * a.H * ((a.dn + cw - 1) / cw)));
-    if (narrow) {
-        if (bf16) hipLaunchKernelGGL((linattn_update_kernel<uint16_t, 16>), grid, dim3(256), 0, s, a);
-        else hipLaunchKernelGGL((linattn_update_kernel<float, 16>), grid, dim3(256), 0, s, a);
-    } else {
-        if (bf16) hipLaunchKernelGGL((linattn_update_kernel<uint16_t, 64>), grid, dim3(256), 0, s, a);
-        else hipLaunchKernelGGL((linattn_update_kernel<float, 64>), grid, dim3(256), 0, s, a);
-    }
+    const dim3 grid(static_cast<unsigned>(a.B * a.H * ((a.dn + kN - 1) / kN)));
+    if (bf16) hipLaunchKernelGGL((linattn_update_kernel<uint16_t>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((linattn_update_kernel<float>), grid, dim3(256), 0, s, a);
     return launch_status(s);
 }
 
