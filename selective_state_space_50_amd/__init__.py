@@ -971,7 +971,11 @@ def _linattn_function():
 def linear_attention(q, k, v, log_decay, h0=None, *, scale=None, lengths=None, return_last_state=False):
     """Differentiable linear attention with one decay per head: linattn_fwd with a torch autograd
     backward through linattn_bwd (gradients for q, k, v, log_decay and h0).  Arguments as
-    linattn_fwd; with return_last_state both outputs can be differentiated."""
+    linattn_fwd; with return_last_state both outputs can be differentiated.
+
+    In a captured graph, capture the forward and its backward together, and let no eager autograd
+    graph of the same leaves live meanwhile: torch runs a leaf's accumulation on the stream that
+    first used the leaf, which a capture cannot join."""
     return _linattn_function().apply(q, k, v, log_decay, h0, scale, lengths, bool(return_last_state))
 
 
@@ -1102,5 +1106,6 @@ def _groupnorm_function():
 
 def group_norm(x, groups, w=None, bias=None, z=None, *, span="token", activation="none", eps=1e-5):
     """Differentiable group norm, channels last: groupnorm_fwd with a torch autograd backward
-    through groupnorm_bwd (gradients for x, w, bias and z).  Arguments as groupnorm_fwd."""
+    through groupnorm_bwd (gradients for x, w, bias and z).  Arguments as groupnorm_fwd; captured
+    graphs as linear_attention."""
     return _groupnorm_function().apply(x, groups, w, bias, z, span, activation, eps)

@@ -103,3 +103,41 @@ def test_prompt_then_tokens(ssm, dt):  # noqa: F811
         ys, ws, bs, zs, _ = norm_case(eager[t - P][0], z[:, t].contiguous(), w, b)
         tn.check(eager[t - P][1], groupnorm(ys, H, ws, bs, zs, 1e-5, False), tn.bounds(ys, H, ws, bs, zs, np.zeros(1), False)["y"],
                  dt, "o")
+
+
+def test_captured_training_step(ssm):  # noqa: F811
+    """Forward and backward of the layer through autograd in one graph, replayed over new inputs between eager steps."""
+    import torch
+    B, L, H, d = 2, 300, 4, 64
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    new = lambda *shape: torch.randn(*shape, device="cuda", generator=gen)  # noqa: E731
+    x, z, do = new(B, L, 3 * H * d).bfloat16(), new(B, L, H * d).bfloat16(), new(B, L, H * d).bfloat16()
+    a, w, b = -new(H).abs(), new(H * d), new(H * d)
+
+    def step():
+        leaves = [t.detach().requires_grad_() for t in (x, z, a, w, b)]
+        q, k, v = (t.unflatten(-1, (H, d)) for t in leaves[0].chunk(3, -1))
+        y = ssm.linear_attention(q, k, v, leaves[2])
+        o = ssm.group_norm(y.flatten(2), H, leaves[3], leaves[4], leaves[1])
+        return [o.detach(), *torch.autograd.grad(o, leaves, do)]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for _ in range(4):
+        for t in (x, z, do, w, b):
+            t.copy_(torch.randn(t.shape, device="cuda", generator=gen))
+        ref = [t.clone() for t in step()]
+        torch.cuda.synchronize()
+        for t in held:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, (t, r) in enumerate(zip(held, ref)):
+            assert torch.equal(t, r), i
