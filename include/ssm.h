@@ -516,6 +516,8 @@ size_t ssm_linattn_workspace_bytes(const ssm_linattn_shape *shape);
  * bf16 matrix cores with every fp32 factor split into two or three bf16 parts, fp32 on the fp32
  * matrix cores.  A token's NaN or infinity reaches its own and later outputs only (where an
  * infinity may turn into NaN).  Deterministic.
+ * SSM_EUNSUPPORTED: dk or dv over SSM_LINATTN_MAX_DIM, batch * nheads over 2^20, nheads over 2^16, seqlen
+ * over 2^30, q_row, k_row or v_row over 2^24.
  */
 int ssm_linattn_fwd(const ssm_linattn_shape *shape, const void *q, const void *k, const void *v,
                     const float *log_decay, float scale, const int32_t *lengths, const float *h0,
@@ -575,6 +577,8 @@ size_t ssm_groupnorm_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim,
  *   mean, rstd [batch, groups]       fp32    what the backward reads; NULL = not stored
  *   workspace device memory of ssm_groupnorm_workspace_bytes(.., 0) bytes (NULL if 0)
  * groups must be >= 1 and divide dim, eps >= 0 (else SSM_EINVAL).  batch, seqlen or dim == 0 is a no-op.
+ * SSM_EUNSUPPORTED: dim over 2^24, batch * groups over 2^30, or groups too large for a team's registers with a
+ * batch over 65535 or more than 65535 workgroups across the channels.
  * Statistics in fp32, from deviations (never a difference of squares).  Deterministic.
  */
 int ssm_groupnorm_fwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t groups, int dtype, const void *x,
