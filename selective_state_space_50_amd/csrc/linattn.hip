@@ -886,8 +886,9 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
 #pragma unroll
                 for (int i = 0; i < NB; ++i) {
                     const f4 g = O::widen4(age_g[i]);
+                    const bool in = 16 * i + lr < m;   // (a growing "decay" may overflow in the rows behind the last)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) age = __builtin_fmaf(acca[i][j], g[j], age);
+                    for (int j = 0; j < 4; ++j) age = __builtin_fmaf(in ? acca[i][j] : 0.0f, g[j], age);
                 }
             if constexpr (!kEarly) next_rows(t0, which, further);
             __syncthreads();   // the next chunk staged

@@ -361,3 +361,48 @@ def test_shared_gradients_past_2_to_30(ssm):
     # (both round the same value, in different orders of sums: one step of bf16)
     assert torch.allclose(g[:, -2:].float(), ref.float(), rtol=2.0 ** -7, atol=1e-5)
     assert torch.equal(g[:, :1], g[:, 70000:70001])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("L,decay", [(20, 2.0), (64, 1.0), (70, 1.0)])
+def test_growth_past_the_last_row(ssm, dt, L, decay):
+    """A "decay" whose powers overflow within a chunk, but behind the sequence's end only."""
+    c = make(2, L, 2, 2, 2, 2, 64, 48, dt, seed=L, decay=decay)
+    q, k, v, a, s0, dy = dev(c, "q", "k", "v", "a", "h0", "dy")
+    y, h = ssm.linattn_fwd(q, k, v, a, s0, return_last_state=True)
+    (yr, hr), (ya, ha) = both(linattn, c, ("q", "k", "v", "a", 0.125, "h0"))
+    check(y, yr, ya, dt, c, "y")
+    check(h, hr, ha, "f32", c, "h_last")
+    g = ssm.linattn_bwd(q, k, v, a, s0, dy)
+    r, big = both(linattn_bwd, c, ("q", "k", "v", "a", 0.125, "h0", "dy", None))
+    for name in ("dq", "dk", "dv", "dlog_decay", "dh0"):
+        check(g[name], r[name], big[name], dt if name in ("dq", "dk", "dv") else "f32", c, name)
+
+
+def test_lengths_out_of_range_and_one_tensor_thrice(ssm):
+    """Lengths are cut to 0 .. L; q, k and v may be one tensor."""
+    import torch
+    x = torch.randn(3, 100, 2, 64, device="cuda").bfloat16()
+    a = -torch.rand(2, device="cuda")
+    cut = torch.tensor([100, 0, 40], dtype=torch.int32, device="cuda")
+    far = torch.tensor([1 << 30, -5, 40], dtype=torch.int32, device="cuda")
+    for f in (lambda n: ssm.linattn_fwd(x, x, x, a, lengths=n, return_last_state=True),
+              lambda n: list(ssm.linattn_bwd(x, x, x, a, dy=x, lengths=n).values())[:4]):
+        for one, two in zip(f(cut), f(far)):
+            assert torch.equal(one, two)
+
+
+def test_two_streams_at_once(ssm):
+    """Calls on two streams, each with its own workspace, as one after the other."""
+    import torch
+    c = [make(1, 3000, 2, 2, 2, 2, 64, 64, "bf16", seed=s) for s in (1, 2)]
+    t = [dev(x, "q", "k", "v", "a", "h0", "dy") for x in c]
+    ref = [ssm.linattn_bwd(*x) for x in t]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in t]
+    for _ in range(5):
+        got = [ssm.linattn_bwd(*x, stream=s) for x, s in zip(t, streams)]
+        torch.cuda.synchronize()
+        for g, r in zip(got, ref):
+            for n in r:
+                assert torch.equal(g[n], r[n]), n
