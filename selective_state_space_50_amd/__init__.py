@@ -772,6 +772,7 @@ class _Sizes:
         self.scale = shape.dk ** -0.5
         self.state = (shape.batch, shape.nheads, shape.dk, shape.dv)
         self.out = (shape.batch, shape.seqlen, shape.nheads, shape.dv)
+        self.token = (shape.batch, shape.nheads, shape.dv)
 
     @functools.cached_property
     def fwd_bytes(self):
@@ -878,9 +879,9 @@ def linattn_fwd(q, k, v, log_decay, h0=None, *, scale=None, lengths=None, return
     _need(out, "out", s.out, dt, dev)
     _need(h_last, "h_last", s.state, torch.float32, dev)
     if out is None:
-        out = torch.empty(s.out, dtype=dt, device=dev)
+        out = q.new_empty(s.out)   # (half the time of torch.empty)
     if return_last_state and h_last is None:
-        h_last = torch.empty(s.state, dtype=torch.float32, device=dev)
+        h_last = log_decay.new_empty(s.state)
     need = s.fwd_bytes
     workspace = _workspace(workspace, need, dev)
     _check(lib().ssm_linattn_fwd(s.ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
@@ -910,10 +911,9 @@ def linattn_bwd(q, k, v, log_decay, h0=None, dy=None, dh_last=None, *, scale=Non
     for t, n, shape, d in ((h0, "h0", s.state, torch.float32), (lengths, "lengths", s.state[:1], torch.int32),
                            (dy, "dy", s.out, dt), (dh_last, "dh_last", s.state, torch.float32)):
         _need(t, n, shape, d, dev)
-    new = lambda shape, d: torch.empty(shape, dtype=d, device=dev)  # noqa: E731
-    out = {"dq": new(q.shape, dt), "dk": new(k.shape, dt), "dv": new(v.shape, dt),
-           "dlog_decay": new(log_decay.shape, torch.float32) if need_dlog_decay else None,
-           "dh0": new(s.state, torch.float32) if need_dh0 else None}
+    out = {"dq": q.new_empty(q.shape), "dk": k.new_empty(k.shape), "dv": v.new_empty(v.shape),
+           "dlog_decay": log_decay.new_empty(log_decay.shape) if need_dlog_decay else None,
+           "dh0": log_decay.new_empty(s.state) if need_dh0 else None}
     need = s.bwd_bytes[bool(need_dlog_decay)]
     workspace = _workspace(workspace, need, dev)
     _check(lib().ssm_linattn_bwd(s.ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
@@ -935,9 +935,9 @@ def linattn_update(h, q, k, v, log_decay, *, scale=None, out=None, stream=None):
             return linattn_update(h, q, k, v, log_decay, scale=scale, out=out)
     _need(h, "h", s.state, torch.float32, dev)
     if out is None:
-        out = torch.empty((s.c.batch, s.c.nheads, s.c.dv), dtype=dt, device=dev)
+        out = q.new_empty(s.token)
     else:
-        _need(out, "out", (s.c.batch, s.c.nheads, s.c.dv), dt, dev)
+        _need(out, "out", s.token, dt, dev)
     _check(lib().ssm_linattn_update(s.ref, h.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
                                     s.scale if scale is None else scale, out.data_ptr(), _stream(dev)), "ssm_linattn_update")
     return out
@@ -1033,7 +1033,7 @@ def groupnorm_fwd(x, groups, w=None, bias=None, z=None, *, span="token", activat
     _need(bias, "bias", shape[-1:], torch.float32, dev)
     _need(out, "out", shape, dt, dev)
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=dev)
+        out = x.new_empty(shape)
     mean, rstd = (torch.empty(stats, dtype=torch.float32, device=dev) for _ in range(2)) if return_stats else (None, None)
     need = _groupnorm_bytes(size, groups, code, 0)
     workspace = _workspace(workspace, need, dev)
@@ -1067,10 +1067,9 @@ def groupnorm_bwd(x, groups, w=None, bias=None, z=None, dy=None, mean=None, rstd
                        (bias, "bias", shape[-1:], torch.float32), (mean, "mean", stats, torch.float32),
                        (rstd, "rstd", stats, torch.float32)):
         _need(t, n, s, d, dev)
-    new = lambda s, d: torch.empty(s, dtype=d, device=dev)  # noqa: E731
-    out = {"dx": new(shape, dt), "dz": new(shape, dt) if z is not None else None,
-           "dw": new(shape[-1:], torch.float32) if w is not None and need_dw else None,
-           "dbias": new(shape[-1:], torch.float32) if bias is not None and need_dw else None}
+    out = {"dx": x.new_empty(shape), "dz": x.new_empty(shape) if z is not None else None,
+           "dw": w.new_empty(shape[-1:]) if w is not None and need_dw else None,
+           "dbias": bias.new_empty(shape[-1:]) if bias is not None and need_dw else None}
     need = _groupnorm_bytes(size, groups, code, 1)
     workspace = _workspace(workspace, need, dev)
     _check(lib().ssm_groupnorm_bwd(*size, groups, code, x.data_ptr(), _addr(w), _addr(bias), _addr(z), silu, dy.data_ptr(),
