@@ -513,7 +513,7 @@ size_t ssm_linattn_workspace_bytes(const ssm_linattn_shape *shape);
  *   y         [batch, seqlen, nheads, dv]   dtype   output, contiguous; must not overlap an input
  *   workspace device memory of ssm_linattn_workspace_bytes() bytes (NULL if 0)
  * batch or nheads == 0 is a no-op; seqlen == 0 stores h0 (or zeros) in h_last.  bf16 runs on the
- * bf16 matrix cores with every fp32 factor split into two or three bf16 parts, fp32 on the fp32
+ * bf16 matrix cores with every fp32 factor split into three bf16 parts (all its bits), fp32 on the fp32
  * matrix cores.  A token's NaN or infinity reaches its own and later outputs only (where an
  * infinity may turn into NaN).  Deterministic.
  * SSM_EUNSUPPORTED: dk or dv over SSM_LINATTN_MAX_DIM, batch * nheads over 2^20, nheads over 2^16, seqlen

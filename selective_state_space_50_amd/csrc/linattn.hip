@@ -61,8 +61,10 @@ template <>
 struct Op<uint16_t> {
     using V4 = s4;
     using Frag = s8;
-    static constexpr int kWide = 3;   // bf16 parts that carry an fp32 value whole
-    static constexpr int kNarrow = 2; // and to about 16 bits
+    // bf16 parts that carry an fp32 factor (states, decayed scores, weighted rows) whole.  (Two, 16 bits, in the
+    // scores and the state's readout take B4 L4096 H64 128x64 from 228 to 209 us, B1 L32768 H16 128x128 from 273 to
+    // 257, and leave 0.25% of bf16 outputs one step off those of 32-bit factors, against 0.04%.)
+    static constexpr int kParts = 3;
     static constexpr int kRowOffs = 4, kColOffs = 4;
     static __device__ __forceinline__ Frag cat(V4 a, V4 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
     static __device__ __forceinline__ f4 mma(Frag a, Frag b, f4 c) {
@@ -138,8 +140,7 @@ template <>
 struct Op<float> {
     using V4 = f4;
     struct Frag { f4 a, b; };
-    static constexpr int kWide = 1;
-    static constexpr int kNarrow = 1;
+    static constexpr int kParts = 1;
     static constexpr int kRowOffs = 2, kColOffs = 8;
     static __device__ __forceinline__ Frag cat(V4 a, V4 b) { return Frag{a, b}; }
     // K = 32 as eight products over K = 4 (v_mfma_f32_16x16x4_f32): product e takes element e of
@@ -395,12 +396,12 @@ __device__ __forceinline__ void update_state(f4 (&S)[NT], f4 (&R)[NR], int TB, L
                                              Decay d, int m) {
     using O = Op<T>;
     constexpr int NJ = Q / 32;
-    typename O::V4 wp[2 * NJ][O::kWide], ap[AGE ? 2 * NJ : 1][O::kWide];
+    typename O::V4 wp[2 * NJ][O::kParts], ap[AGE ? 2 * NJ : 1][O::kParts];
 #pragma unroll
     for (int j = 0; j < 2 * NJ; ++j) {
         const f4 x = O::widen4(vp[j]);
-        O::template split<O::kWide>(x * lds_get<f4>(w_up + 64 * j), wp[j]);
-        if constexpr (AGE) O::template split<O::kWide>(x * lds_get<f4>(w_age + 64 * j), ap[j]);
+        O::template split<O::kParts>(x * lds_get<f4>(w_up + 64 * j), wp[j]);
+        if constexpr (AGE) O::template split<O::kParts>(x * lds_get<f4>(w_age + 64 * j), ap[j]);
     }
     // AHEAD: two tiles at a time (their products are chains of accumulations), the next two tiles'
     // columns of k read meanwhile
@@ -433,7 +434,7 @@ __device__ __forceinline__ void update_state(f4 (&S)[NT], f4 (&R)[NR], int TB, L
 #pragma unroll
         for (int c = 0; c < NJ; ++c)
 #pragma unroll
-            for (int n = 0; n < O::kWide; ++n)
+            for (int n = 0; n < O::kParts; ++n)
 #pragma unroll
                 for (int u = 0; u < STEP; ++u) {
                     S[t + u] = O::mma(kf[at][u][c], O::cat(wp[2 * c][n], wp[2 * c + 1][n]), S[t + u]);
@@ -468,7 +469,7 @@ __device__ __forceinline__ void fill_update_weights(float (&up)[2][Q], float *ag
 // Measured: B4 L4096 H64 128x64 bf16 (one segment, 256 workgroups) 184 us, 4.4 TB/s; a copy reaches 5.2.
 // Chunks of 64 take 2.9 us (128 columns): per SIMD 1.1 us of VALU and 0.7 us of matrix instructions,
 // in two roles that meet at two barriers; without any product the same loads and stores take 168 us.
-// Smaller chunks would cost more state updates, larger ones more in-chunk products and LDS (115 KB now).
+// Smaller chunks would cost more state updates, larger ones more in-chunk products and LDS (121 KB now).
 // AGE doubles the readout and the update (dq of B2 L4096 H32 128x128: 176 us against 105).
 template <class T, int DK, bool AGE>
 struct __align__(16) Smem {
@@ -477,8 +478,8 @@ struct __align__(16) Smem {
     char q[G::kBufs][G::kQ * G::kRow];
     char k[G::kBufs][G::kQ * G::kRow];
     char v[G::kBufs][G::kQ * G::kVRow];
-    V4 p[Op<T>::kNarrow][G::kPairs][64][2];                          // decayed (q k^T)^T, operand-ready
-    V4 pa[AGE ? Op<T>::kWide : 1][AGE ? G::kPairs : 1][64][2];       // the same times i - j (AGE)
+    V4 p[Op<T>::kParts][G::kPairs][64][2];                          // decayed (q k^T)^T, operand-ready
+    V4 pa[AGE ? Op<T>::kParts : 1][AGE ? G::kPairs : 1][64][2];       // the same times i - j (AGE)
     f4 y[4][G::kBlocks][64];                                    // the carried state's share of y^T
     f4 ya[AGE ? 4 : 1][AGE ? G::kBlocks : 1][64];               // and of its derivative
     float w_up[2][G::kQ], w_age[AGE ? 2 * G::kQ : 4];           // row weights of the update (AGE: and its derivative)
@@ -493,7 +494,7 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
     using V4 = typename O::V4;
     using Frag = typename O::Frag;
     constexpr int Q = G::kQ, NT = DK / 16, NC = DK / 32, NB = G::kBlocks, kB = G::kBufs;
-    constexpr int NS = AGE ? O::kWide : O::kNarrow;   // parts of the state in its readout
+    constexpr int NS = O::kParts;
     __shared__ Smem<T, DK, AGE> sm;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), w = wv & 3;
@@ -722,9 +723,9 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
         if (w == 0) {   // the pairs' empty halves
             const V4 zero = {};
             for (int i = 0; i < NB; i += 2) {
-                for (int n = 0; n < O::kNarrow; ++n) lds_put(pp + pair_of(i, i) * TB + n * PB + Lds(sizeof(V4)), zero);
+                for (int n = 0; n < O::kParts; ++n) lds_put(pp + pair_of(i, i) * TB + n * PB + Lds(sizeof(V4)), zero);
                 if constexpr (AGE)
-                    for (int n = 0; n < O::kWide; ++n) lds_put(ppa + pair_of(i, i) * TB + n * PB + Lds(sizeof(V4)), zero);
+                    for (int n = 0; n < O::kParts; ++n) lds_put(ppa + pair_of(i, i) * TB + n * PB + Lds(sizeof(V4)), zero);
             }
         }
         auto product = [&](f4 (&g)[3], int buf, auto own) __attribute__((always_inline)) {
@@ -760,18 +761,18 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
             if (i == k)   // rows after the output's: zero whatever q and k hold
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[j] = d0 - j >= 0 ? x[j] : 0.0f;
-            V4 part[O::kNarrow];
-            O::template split<O::kNarrow>(x, part);
+            V4 part[O::kParts];
+            O::template split<O::kParts>(x, part);
 #pragma unroll
-            for (int n = 0; n < O::kNarrow; ++n) lds_put(pp + at + n * PB, part[n]);
+            for (int n = 0; n < O::kParts; ++n) lds_put(pp + at + n * PB, part[n]);
             if constexpr (AGE) {
                 f4 xa;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) xa[j] = x[j] * static_cast<float>(max(d0 - j, 0));
-                V4 wide[O::kWide];
-                O::template split<O::kWide>(xa, wide);
+                V4 wide[O::kParts];
+                O::template split<O::kParts>(xa, wide);
 #pragma unroll
-                for (int n = 0; n < O::kWide; ++n) lds_put(ppa + at + n * PB, wide[n]);
+                for (int n = 0; n < O::kParts; ++n) lds_put(ppa + at + n * PB, wide[n]);
             }
         };
         const int col = 16 * w + 4 * lg;
@@ -811,7 +812,7 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
                         // the lane that holds row r, column lr of the tile
                         const Lds from = ((r >> 2) * 16 + lr - lane) * sizeof(Frag) + pair_of(i, i) * TB + (i & 1) * sizeof(V4);
                         float pr = 0.0f;
-                        for (int n = 0; n < O::kNarrow; ++n) pr += O::element(lds_get<V4>(pp + n * PB + from), r & 3);
+                        for (int n = 0; n < O::kParts; ++n) pr += O::element(lds_get<V4>(pp + n * PB + from), r & 3);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const int at = 16 * i + r, c = col + j, piece = c / (16 / static_cast<int>(sizeof(T)));
@@ -853,10 +854,10 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
                         to[i] = O::mma(O::cat(k == i ? vd[k] : vp[k], i <= k + 1 ? vd[k + 1] : vp[k + 1]), f[pair_of(k, i)], to[i]);
             };
 #pragma unroll
-            for (int n = 0; n < O::kNarrow; ++n) times_v(acc, pp + n * PB);
+            for (int n = 0; n < O::kParts; ++n) times_v(acc, pp + n * PB);
             if constexpr (AGE)
 #pragma unroll
-                for (int n = 0; n < O::kWide; ++n) times_v(acca, ppa + n * PB);
+                for (int n = 0; n < O::kParts; ++n) times_v(acca, ppa + n * PB);
             const int64_t yt = y0 + (t0 + lr) * ystep;
             if (sizeof(T) == 2 && !a.out_f32 && full_cols) {
 #pragma unroll

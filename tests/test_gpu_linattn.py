@@ -406,3 +406,24 @@ def test_two_streams_at_once(ssm):
         for g, r in zip(got, ref):
             for n in r:
                 assert torch.equal(g[n], r[n]), n
+
+
+@pytest.mark.parametrize("which", ["state", "scores", "later scores"])
+def test_bf16_outputs_round_the_whole_factor(ssm, which):
+    """1 + 2^-8 + 2^-20 lies just above the middle of two bf16 values: y is the upper one only if no bit of the fp32
+    factor it comes from (a state's element, a score) was dropped before the product."""
+    import torch
+    x = 1.0 + 2.0 ** -8 + 2.0 ** -20
+    L = 40 if which == "later scores" else 1
+    q, k, v = (torch.zeros(1, L, 1, 16, device="cuda", dtype=torch.bfloat16) for _ in range(3))
+    h0 = torch.zeros(1, 1, 16, 16, device="cuda")
+    if which == "state":
+        q[:, 0, 0, 3] = 1.0
+        h0[0, 0, 3, 5] = x
+    else:   # the score of the last token with the first
+        q[0, -1, 0, :3] = 1.0
+        k[0, 0, 0, :3] = torch.tensor([1.0, 2.0 ** -8, 2.0 ** -20])
+        v[0, 0, 0, 5] = 1.0
+    y = ssm.linattn_fwd(q, k, v, torch.zeros(1, device="cuda"), h0, scale=1.0)
+    # every product and sum here is exact in 24 bits: one rounding, to bf16
+    assert float(y[0, -1, 0, 5]) == 1.0 + 2.0 ** -7
