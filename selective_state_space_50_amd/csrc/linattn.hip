@@ -990,7 +990,7 @@ __global__ void __launch_bounds__(kThreads) linattn_state_kernel(LinAttnArgs a) 
 template <bool AGE>
 __global__ void __launch_bounds__(256) linattn_combine_kernel(LinAttnArgs a) {
     constexpr int E = 4, P = AGE ? 4 : 8;
-    __shared__ float decay[2];
+    __shared__ Decay decay[2];
     const int64_t sz = a.dk * a.dn, per = (sz + 256 * E - 1) / (256 * E);
     const int64_t bh = blockIdx.x / per, e0 = blockIdx.x % per * (256 * E) + threadIdx.x;
     int64_t Lb = a.L;
@@ -999,11 +999,15 @@ __global__ void __launch_bounds__(256) linattn_combine_kernel(LinAttnArgs a) {
     if (parts <= 0) return;
     // (the last part of a segment is what the others leave)
     const int64_t last_len = a.seg_len - (a.nsub - 1) * a.sub_len;
-    if (threadIdx.x < 2)
-        decay[threadIdx.x] = static_cast<float>(exp(static_cast<double>(a.log_decay[bh % a.H]) *
-                                                    static_cast<double>(threadIdx.x ? last_len : a.sub_len)));
+    // (hi + lo, as within a part: the parts' decays are all alike, and so is what rounding them would lose)
+    if (threadIdx.x < 2) {
+        const double x = exp(static_cast<double>(a.log_decay[bh % a.H]) * static_cast<double>(threadIdx.x ? last_len : a.sub_len));
+        const float hi = static_cast<float>(x);
+        decay[threadIdx.x] = Decay{hi, hi < INFINITY ? static_cast<float>(x - static_cast<double>(hi)) : 0.0f};
+    }
     __syncthreads();
-    const float d = decay[0], d1 = decay[1], T = static_cast<float>(a.sub_len), T1 = static_cast<float>(last_len);
+    const Decay d = decay[0], d1 = decay[1];
+    const float T = static_cast<float>(a.sub_len), T1 = static_cast<float>(last_len);
     const int64_t at0 = bh * (a.nseg - 1) * nsub * sz;
     float S[E], R[E];
 #pragma unroll
@@ -1027,10 +1031,14 @@ __global__ void __launch_bounds__(256) linattn_combine_kernel(LinAttnArgs a) {
         for (int i = 0; i < P; ++i) {
             if (s0 + i >= parts) continue;
             const bool last = (s0 + i + 1) % nsub == 0;
+            const Decay by = last ? d1 : d;
 #pragma unroll
             for (int x = 0; x < E; ++x) {
-                if constexpr (AGE) R[x] = __builtin_fmaf(last ? d1 : d, __builtin_fmaf(last ? T1 : T, S[x], R[x]), own_R[i][x]);
-                S[x] = __builtin_fmaf(last ? d1 : d, S[x], own[i][x]);
+                if constexpr (AGE) {
+                    const float r = __builtin_fmaf(last ? T1 : T, S[x], R[x]);
+                    R[x] = __builtin_fmaf(by.hi, r, __builtin_fmaf(by.lo, r, own_R[i][x]));
+                }
+                S[x] = __builtin_fmaf(by.hi, S[x], __builtin_fmaf(by.lo, S[x], own[i][x]));
                 if (last && e0 + x * 256 < sz) {
                     const int64_t at = at0 + (s0 + i) * sz + e0 + x * 256;
                     a.ws_S[at] = S[x];

@@ -427,3 +427,23 @@ def test_bf16_outputs_round_the_whole_factor(ssm, which):
     y = ssm.linattn_fwd(q, k, v, torch.zeros(1, device="cuda"), h0, scale=1.0)
     # every product and sum here is exact in 24 bits: one rounding, to bf16
     assert float(y[0, -1, 0, 5]) == 1.0 + 2.0 ** -7
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("decay", [-5e-6, -7e-6, -4e-6])
+def test_joining_many_segments_keeps_the_precision(ssm, dt, decay):
+    """A start state alone, carried over 131072 tokens in hundreds of segments: what joining them does to a state is all
+    there is.  (h_last = exp(a L) h0, dh0 = exp(a L) dh, da = L exp(a L) <h0, dh>.)"""
+    import torch
+    L = 131072
+    c = make(1, 1, 1, 1, 1, 1, 16, 16, dt, seed=1, decay=decay)
+    a, s0 = dev(c, "a", "h0")
+    zero = torch.zeros(1, L, 1, 16, device="cuda", dtype=torch.bfloat16 if dt == "bf16" else torch.float32)
+    _, h = ssm.linattn_fwd(zero, zero, zero, a, s0, return_last_state=True)
+    g = ssm.linattn_bwd(zero, zero, zero, a, s0, zero, s0)
+    f = np.exp(np.float64(c["a"][0]) * L)
+    h0 = f64(c, "h0")
+    # two roundings (each 2^-24 / sqrt(3) at the root mean square, at most) in each of some 300 joins and chunks:
+    # sqrt(600) 2^-24 / sqrt(3) = 8.4e-7; a decay off by 2^-26 in every one of 255 joins is off by 3.8e-6
+    for got, ref in ((h, f * h0), (g["dh0"], f * h0), (g["dlog_decay"], np.array([L * f * (h0 ** 2).sum()]))):
+        assert np.linalg.norm(to_host(got) - ref) <= 2e-6 * np.linalg.norm(ref)
