@@ -595,7 +595,8 @@ int ssm_groupnorm_fwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t groups
  *   dz        [batch, seqlen, dim]   dtype   required when z is given, else ignored
  *   dw, dbias [dim]                  fp32    NULL = not computed
  *   workspace device memory of ssm_groupnorm_workspace_bytes(.., 1) bytes
- * dim == 0 is a no-op; batch or seqlen == 0 sets dw and dbias to zero.  Deterministic.
+ * Takes every shape that the forward takes.  dim == 0 is a no-op; batch or seqlen == 0 sets dw and dbias to zero.
+ * Deterministic.
  */
 int ssm_groupnorm_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t groups, int dtype, const void *x,
                       const float *w, const float *bias, const void *z, int silu, const void *dy, const float *mean,

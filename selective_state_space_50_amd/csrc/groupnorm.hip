@@ -13,7 +13,8 @@
 // workgroup): mean first, then the sum of squared deviations from it.  Larger groups are cut
 // into slabs of rows: a pass for the statistics (deviations from running means, merged in a
 // fixed order), then a pass that reads x again.  Their backward sums g and g xh per channel,
-// which gives dw and db and, weighted with w, both sums of dx.
+// which gives dw and db and, weighted with w, both sums of dx.  Over few positions (or with more rows of
+// statistics than a launch has slabs for) the backward walks every group by a team of lanes instead.
 //
 // Measured, bf16 (a copy reaches 5.2 TB/s): 16384 rows of 4096 channels in 64 groups, gated: forward 91 us
 // (4.4 TB/s), backward 132 us (5.1 TB/s) and 6 us for the sums of dw and db.  8 x 4000 x 512 in 32 groups
@@ -365,26 +366,99 @@ __global__ void __launch_bounds__(kWG) gn_bwd_team_kernel(GroupNormArgs a) {
     }
 }
 
+// ---- dx and dz where there are many groups, of few values each: a team of lanes walks one (n, g) twice, for
+// the two sums of dx and for dx (the second time from the caches), so nothing per row is kept in memory.  dw
+// and db come from gn_bwd_sums_kernel over all rows.
+template <class T, int VE, bool WG>
+__global__ void __launch_bounds__(kWG) gn_bwd_walk_kernel(GroupNormArgs a) {
+    __shared__ float lds[4];
+    const int P = WG ? kWG : a.team, sh = __builtin_ctz(P), tl = threadIdx.x & (P - 1);
+    const uint32_t team = (blockIdx.y * gridDim.x + blockIdx.x) * (kWG >> sh) + (threadIdx.x >> sh);
+    const bool on = team < static_cast<uint32_t>(a.N * a.G);
+    const uint32_t G = static_cast<uint32_t>(a.G), n = (on ? team : 0) / G, g = (on ? team : 0) % G;
+    const int lpg = static_cast<int>(a.S / VE), dl = P / lpg, dj = P % lpg;   // vectors of a row; a lane's step in rows and vectors
+    const int64_t base = static_cast<int64_t>(n) * a.L * a.C + static_cast<int64_t>(g) * a.S, c0 = static_cast<int64_t>(g) * a.S;
+    const T *x = static_cast<const T *>(a.x) + base, *dy = static_cast<const T *>(a.dy) + base, *z = a.z ? static_cast<const T *>(a.z) + base : nullptr;
+    const float mean = on ? a.mean[team] : 0.0f, rstd = on ? a.rstd[team] : 0.0f;
+    // what(offset, xh, e, dz) for each of the lane's vectors
+    auto walk = [&](auto what) __attribute__((always_inline)) {
+        int64_t l = tl / lpg;
+        int j = tl % lpg;
+        const int64_t rows = on ? a.L : 0;
+        while (l < rows) {
+            const int64_t at = l * a.C + static_cast<int64_t>(j) * VE;
+            Vec<T, VE> xh, e, gate;
+            xh.load(x + at);
+            e.load(dy + at);
+            if (a.z) gate.load(z + at);
+            float w[VE], b[VE];
+            channels<VE>(a.w, c0 + static_cast<int64_t>(j) * VE, 1.0f, w);
+            channels<VE>(a.b, c0 + static_cast<int64_t>(j) * VE, 0.0f, b);
+#pragma unroll
+            for (int k = 0; k < VE; ++k) {
+                xh.v[k] = (xh.v[k] - mean) * rstd;
+                float dz = 0.0f;
+                e.v[k] = norm_grad(xh.v[k], w[k], b[k], a.silu, a.z != nullptr, a.z ? gate.v[k] : 0.0f, e.v[k], dz) * w[k];
+                gate.v[k] = dz;
+            }
+            what(at, xh, e, gate);
+            l += dl;
+            j += dj;
+            if (j >= lpg) {
+                j -= lpg;
+                ++l;
+            }
+        }
+    };
+    float s1 = 0.0f, s2 = 0.0f;
+    walk([&](int64_t, const Vec<T, VE> &xh, const Vec<T, VE> &e, const Vec<T, VE> &) __attribute__((always_inline)) {
+        float p1 = 0.0f, p2 = 0.0f;
+#pragma unroll
+        for (int k = 0; k < VE; ++k) {
+            p1 += e.v[k];
+            p2 = __builtin_fmaf(e.v[k], xh.v[k], p2);
+        }
+        s1 += p1;
+        s2 += p2;
+    });
+    s1 = team_sum<WG>(s1, P, lds) * a.inv_m;
+    s2 = team_sum<WG>(s2, P, lds) * a.inv_m;
+    walk([&](int64_t at, const Vec<T, VE> &xh, const Vec<T, VE> &e, const Vec<T, VE> &dz) __attribute__((always_inline)) {
+        Vec<T, VE> dx;
+#pragma unroll
+        for (int k = 0; k < VE; ++k) dx.v[k] = rstd * (e.v[k] - __builtin_fmaf(xh.v[k], s2, s1));
+        dx.store(static_cast<T *>(a.dx) + base + at);
+        if (a.z) dz.store(static_cast<T *>(a.dz) + base + at);
+    });
+}
+
 // ---- backward of larger groups: sums of g xh and g per channel over one slab, blockIdx =
-// (slab, block of columns, n)
-template <class T, int VE>
+// (slab, block of columns, n); ALL: over rows of every n, for dw and db alone, blockIdx = (block of
+// columns, slab)
+template <class T, int VE, bool ALL>
 __global__ void __launch_bounds__(kWG) gn_bwd_sums_kernel(GroupNormArgs a) {
     __shared__ float lds[kWG][2 * VE + 1];
-    const int64_t vecs = a.C / VE, v0 = static_cast<int64_t>(blockIdx.y) * kWG;
+    const int64_t vecs = a.C / VE, v0 = static_cast<int64_t>(ALL ? blockIdx.x : blockIdx.y) * kWG, slab = ALL ? blockIdx.y : blockIdx.x;
     const int cols = static_cast<int>(min(static_cast<int64_t>(kWG), vecs - v0)), R = kWG / cols;
     const int r = threadIdx.x / cols;
-    const int64_t c = (v0 + threadIdx.x % cols) * VE, n = blockIdx.z;
-    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.slab_rows, end = min(row0 + a.slab_rows, a.L);
+    const int64_t c = (v0 + threadIdx.x % cols) * VE, n = ALL ? 0 : blockIdx.z;
+    const int64_t row0 = slab * a.slab_rows, end = min(row0 + a.slab_rows, ALL ? a.N * a.L : a.L);
     float dw[VE], db[VE];
 #pragma unroll
     for (int k = 0; k < VE; ++k) dw[k] = db[k] = 0.0f;
     if (r < R) {
-        const float mean = a.mean[n * a.G + c / a.S], rstd = a.rstd[n * a.G + c / a.S];
+        const int64_t g = c / a.S;
+        float mean = ALL ? 0.0f : a.mean[n * a.G + g], rstd = ALL ? 0.0f : a.rstd[n * a.G + g];
         float w[VE], b[VE];
         channels<VE>(a.w, c, 1.0f, w);
         channels<VE>(a.b, c, 0.0f, b);
         for (int64_t l = row0 + r; l < end; l += R) {
             const int64_t at = (n * a.L + l) * a.C + c;
+            if constexpr (ALL) {
+                const int64_t ng = (a.L == 1 ? l : l / a.L) * a.G + g;
+                mean = a.mean[ng];
+                rstd = a.rstd[ng];
+            }
             Vec<T, VE> x, dy, z;
             x.load(static_cast<const T *>(a.x) + at);
             dy.load(static_cast<const T *>(a.dy) + at);
@@ -414,7 +488,7 @@ __global__ void __launch_bounds__(kWG) gn_bwd_sums_kernel(GroupNormArgs a) {
         __syncthreads();
     }
     if (r == 0) {
-        float *p = a.part + (n * a.nslab + blockIdx.x) * 2 * a.C + c;
+        float *p = a.part + (n * a.nslab + slab) * 2 * a.C + c;
 #pragma unroll
         for (int k = 0; k < VE; ++k) {
             p[k] = lds[threadIdx.x][k];
@@ -504,12 +578,16 @@ dim3 blocks(const GroupNormArgs &a, int64_t columns) {
     return dim3(static_cast<unsigned>(a.nslab), static_cast<unsigned>(columns), static_cast<unsigned>(a.N));
 }
 
+// a team of lanes for every (n, g) (a launch's threads along one axis are counted in 32 bits)
+dim3 team_grid(const GroupNormArgs &a) {
+    const int64_t n = (a.N * a.G * a.team + kWG - 1) / kWG, across = n < (1 << 20) ? n : 1 << 20;
+    return dim3(static_cast<unsigned>(across), static_cast<unsigned>((n + across - 1) / across));
+}
+
 template <class T, int VE>
 hipError_t fwd_typed(const GroupNormArgs &a, hipStream_t s) {
     if (a.team > 0) {
-        // (a launch's threads along one axis are counted in 32 bits)
-        const int64_t n = (a.N * a.G * a.team + kWG - 1) / kWG, across = n < (1 << 20) ? n : 1 << 20;
-        const dim3 grid(static_cast<unsigned>(across), static_cast<unsigned>((n + across - 1) / across));
+        const dim3 grid = team_grid(a);
         auto launch = [&](auto one) {
             constexpr bool ONE = decltype(one)::value;
             if (a.team == kWG) hipLaunchKernelGGL((gn_team_kernel<T, VE, 8, true, ONE>), grid, dim3(kWG), 0, s, a);
@@ -533,6 +611,20 @@ hipError_t fwd_typed(const GroupNormArgs &a, hipStream_t s) {
 
 template <class T, int VE>
 hipError_t bwd_typed(const GroupNormArgs &a, hipStream_t s) {
+    const unsigned cols = static_cast<unsigned>((2 * a.C + 31) / 32);
+    if (a.walk) {
+        const dim3 grid = team_grid(a);
+        if (a.team == kWG) hipLaunchKernelGGL((gn_bwd_walk_kernel<T, VE, true>), grid, dim3(kWG), 0, s, a);
+        else hipLaunchKernelGGL((gn_bwd_walk_kernel<T, VE, false>), grid, dim3(kWG), 0, s, a);
+        hipError_t e = launch_status(s);
+        if (e != hipSuccess || !(a.dw || a.db)) return e;
+        hipLaunchKernelGGL((gn_bwd_sums_kernel<T, VE, true>),
+                           dim3(static_cast<unsigned>((a.C / VE + kWG - 1) / kWG), static_cast<unsigned>(a.nslab)), dim3(kWG), 0, s, a);
+        e = launch_status(s);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(gn_column_sum_kernel, dim3(cols), dim3(1024), 0, s, a.part, a.nslab, 2 * a.C, a.dw, a.db, true);
+        return launch_status(s);
+    }
     if (a.team > 0) {
         const int64_t teams = kWG / a.team, gb = teams < a.G ? teams : a.G;
         const dim3 grid(static_cast<unsigned>((a.G + gb - 1) / gb), static_cast<unsigned>(a.nslab));
@@ -541,18 +633,19 @@ hipError_t bwd_typed(const GroupNormArgs &a, hipStream_t s) {
         else hipLaunchKernelGGL((gn_bwd_team_kernel<T, VE, 2, true>), grid, dim3(kWG), 0, s, a);
         hipError_t e = launch_status(s);
         if (e != hipSuccess || !a.part) return e;
-        hipLaunchKernelGGL(gn_column_sum_kernel, dim3(static_cast<unsigned>((2 * a.C + 31) / 32)), dim3(1024), 0, s, a.part,
+        hipLaunchKernelGGL(gn_column_sum_kernel, dim3(cols), dim3(1024), 0, s, a.part,
                            a.nslab * (teams / gb), 2 * a.C, a.dw, a.db, true);
         return launch_status(s);
     }
     const dim3 grid = blocks(a, (a.C / VE + kWG - 1) / kWG);
-    hipLaunchKernelGGL((gn_bwd_sums_kernel<T, VE>), grid, dim3(kWG), 0, s, a);
+    hipLaunchKernelGGL((gn_bwd_sums_kernel<T, VE, false>), grid, dim3(kWG), 0, s, a);
     hipError_t e = launch_status(s);
     if (e != hipSuccess) return e;
-    const unsigned cols = static_cast<unsigned>((2 * a.C + 31) / 32);
-    hipLaunchKernelGGL(gn_column_sum_kernel, dim3(cols, static_cast<unsigned>(a.N)), dim3(1024), 0, s, a.part, a.nslab, 2 * a.C, a.sums, nullptr, false);
-    e = launch_status(s);
-    if (e != hipSuccess) return e;
+    if (a.nslab > 1) {   // (one slab: its sums are the rows' sums)
+        hipLaunchKernelGGL(gn_column_sum_kernel, dim3(cols, static_cast<unsigned>(a.N)), dim3(1024), 0, s, a.part, a.nslab, 2 * a.C, a.sums, nullptr, false);
+        e = launch_status(s);
+        if (e != hipSuccess) return e;
+    }
     if (a.dw || a.db) {
         hipLaunchKernelGGL(gn_column_sum_kernel, dim3(cols), dim3(1024), 0, s, a.sums, a.N, 2 * a.C, a.dw, a.db, true);
         e = launch_status(s);

@@ -1364,7 +1364,7 @@ extern "C" int ssm_groupnorm_bwd(int64_t batch, int64_t seqlen, int64_t dim, int
     a.N = batch; a.L = seqlen; a.C = dim; a.G = groups; a.S = dim / groups;
     a.x = x; a.z = z; a.dy = dy; a.w = w; a.b = bias; a.silu = silu; a.dx = dx; a.dz = dz; a.dw = dw; a.db = dbias;
     a.mean = const_cast<float *>(mean); a.rstd = const_cast<float *>(rstd);
-    a.team = p.team; a.nvec = p.nvec; a.nslab = p.nslab; a.slab_rows = p.slab_rows;
+    a.team = p.team; a.walk = p.walk; a.nvec = p.nvec; a.nslab = p.nslab; a.slab_rows = p.slab_rows;
     if (!p.team || dw || dbias) a.part = reinterpret_cast<float *>(ws);
     if (!p.team) {
         a.sums = reinterpret_cast<float *>(ws + p.sums_off);

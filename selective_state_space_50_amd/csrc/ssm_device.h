@@ -144,10 +144,11 @@ struct GroupNormArgs {
     float *dw, *db;                  // [C] or null
     float inv_m = 0.0f;              // 1 / (L S), set by the launcher
     int team = 0;                    // lanes that hold one group (256: a workgroup); 0: slabs of rows
+    int walk = 0;                    // backward: teams walk groups, nslab slabs over the rows of all n
     int64_t nvec = 0;                // vectors of one group
     int64_t nslab = 1, slab_rows = 0;   // slabs (the backward with teams: workgroups along the rows)
     float *part = nullptr;           // slabs' statistics [N, nslab, G, 2], or channel sums [.., 2 C]
-    float *sums = nullptr;           // backward, slabs: channel sums [N, 2 C]
+    float *sums = nullptr;           // backward, slabs: channel sums [N, 2 C] (one slab: part itself)
     float *gsum = nullptr;           // and the two sums of dx [N, G, 2]
 };
 

@@ -1046,15 +1046,21 @@ int plan_groupnorm(int64_t batch, int64_t seqlen, int64_t dim, int64_t groups, i
     plan->vec = s % wide == 0;
     const int64_t ve = plan->vec ? wide : 1, wg = 256;
     plan->nvec = seqlen * s / ve;
-    // up to eight vectors a lane; the backward takes single positions (each lane keeps its
-    // channels from row to row) and two vectors a lane (with more its registers spill)
-    if (backward ? seqlen == 1 && plan->nvec <= 2 * wg : plan->nvec <= 8 * wg && seqlen * dim < (int64_t(1) << 31)) {
-        plan->team = static_cast<int>(wg);
-        if (plan->nvec <= (backward ? 64 : 4 * 64)) {
-            plan->team = 1;
-            while (plan->team < 64 && plan->team < plan->nvec) plan->team *= 2;
-        }
-        if (!backward) return SSM_OK;
+    // up to eight vectors a lane (forward); the backward keeps single positions of up to two vectors a lane (with
+    // more its registers spill)
+    const bool held = plan->nvec <= 8 * wg && seqlen * dim < (int64_t(1) << 31);
+    const auto lanes = [&](int64_t wave) {   // of a team: part of a wave up to `wave` vectors, else a workgroup
+        if (plan->nvec > wave) return static_cast<int>(wg);
+        int n = 1;
+        while (n < 64 && n < plan->nvec) n *= 2;
+        return n;
+    };
+    if (!backward && held) {
+        plan->team = lanes(4 * 64);
+        return SSM_OK;
+    }
+    if (backward && seqlen == 1 && plan->nvec <= 2 * wg) {
+        plan->team = lanes(64);
         const int64_t teams = wg / plan->team, gb = teams < groups ? teams : groups, side = teams / gb;
         // four workgroups to a CU, but eight rows at least to each (their sums of dw and db
         // cost 8 bytes a channel)
@@ -1066,18 +1072,31 @@ int plan_groupnorm(int64_t batch, int64_t seqlen, int64_t dim, int64_t groups, i
         return SSM_OK;
     }
     const int64_t lpg = s / ve, gpb = lpg >= wg ? 1 : wg / lpg;   // groups of one workgroup's statistics
-    if (batch > 65535 || ceil_div(ceil_div(dim, ve), wg) > 65535 || ceil_div(groups, gpb) > 65535) {
+    if (!held && (batch > 65535 || ceil_div(ceil_div(dim, ve), wg) > 65535 || ceil_div(groups, gpb) > 65535)) {
         set_error("batch=%lld rows of large groups, or dim=%lld: too many for one launch", (long long)batch, (long long)dim);
         return SSM_EUNSUPPORTED;
     }
     // slabs: eight workgroups to a CU, but four turns of its rows at least to each
     const int64_t cols = dim / ve < wg ? dim / ve : wg, across = ceil_div(dim / ve, wg), side = wg / cols;
-    int64_t n = 8 * kCUs / (batch * across);
-    const int64_t most = ceil_div(seqlen, 4 * side);
-    if (n > most) n = most;
-    if (n < 1) n = 1;
-    plan->slab_rows = ceil_div(seqlen, n);
-    plan->nslab = ceil_div(seqlen, plan->slab_rows);
+    const auto slabs = [&](int64_t rows, int64_t side_by_side) {
+        int64_t n = 8 * kCUs / side_by_side;
+        const int64_t most = ceil_div(rows, 4 * side);
+        if (n > most) n = most;
+        if (n < 1) n = 1;
+        plan->slab_rows = ceil_div(rows, n);
+        plan->nslab = ceil_div(rows, plan->slab_rows);
+    };
+    slabs(seqlen, batch * across);
+    // The backward over few positions: slabs would hold sums (8 bytes a channel) for every n, and more of them than one
+    // launch takes.  (Slabs and walking, bf16, with w, bias and z: 32768x1x8192 in one group 2833 and 1104 us, 40x1x5000 (fp32) 35 and
+    // 24, 8192x4x512 in 32 groups 196 and 92, but 1100x8x4096 in 64 groups 150 and 171, 2048x500x512 in 32 groups 1784 and 4886.)
+    if (backward && (seqlen <= 4 || batch > 65535 || across > 65535)) {
+        plan->walk = true;
+        plan->team = lanes(4 * 64);
+        slabs(batch * seqlen, across);
+        plan->ws_bytes = static_cast<size_t>(plan->nslab * 2 * dim) * sizeof(float);
+        return SSM_OK;
+    }
     size_t at = static_cast<size_t>(batch * plan->nslab * 2 * (backward ? dim : groups)) * sizeof(float);
     auto take = [&](size_t bytes) {
         const size_t off = align_up(at, kWsAlign);
@@ -1086,7 +1105,7 @@ int plan_groupnorm(int64_t batch, int64_t seqlen, int64_t dim, int64_t groups, i
     };
     const size_t per_group = static_cast<size_t>(batch * groups) * sizeof(float);
     if (backward) {
-        plan->sums_off = take(static_cast<size_t>(batch * 2 * dim) * sizeof(float));
+        if (plan->nslab > 1) plan->sums_off = take(static_cast<size_t>(batch * 2 * dim) * sizeof(float));   // (else the slabs' own)
         plan->gsum_off = take(2 * per_group);
     } else {
         plan->mean_off = take(per_group);

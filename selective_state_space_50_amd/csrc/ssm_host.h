@@ -189,7 +189,8 @@ int check_linattn_update(const ssm_linattn_shape *s, const float *h, const void 
 // Group norm: how groups are held (see groupnorm.hip) and what the workspace holds.
 struct GroupNormPlan {
     bool vec = false;        // 16-byte loads
-    int team = 0;            // lanes that hold one group; 0: slabs of rows
+    int team = 0;            // lanes that hold (walk: that walk) one group; 0: slabs of rows
+    bool walk = false;       // backward: dx by teams that walk groups, dw and dbias over slabs of all rows
     int64_t nvec = 0;        // vectors (or elements) of one group
     int64_t nslab = 1, slab_rows = 0;
     size_t mean_off = 0, rstd_off = 0, sums_off = 0, gsum_off = 0;   // (the slabs' sums come first)

@@ -240,3 +240,61 @@ def test_more_threads_than_32_bits_count(ssm):
     ref = ssm.groupnorm_fwd(x[-20:].clone(), G, return_stats=True)
     for a, b in zip((y, mean, rstd), ref):
         assert torch.equal(a[-20:], b) and torch.equal(a[:1000], b[-1:].expand(1000, -1))
+
+
+# Wide tokens and short sequences: the backward walks each group
+WALKED = [
+    (2, 150, 5000, 1, "token", True, True, True, "f32"),
+    (1, 300, 8192, 1, "token", False, True, True, "bf16"),
+    (1, 70, 9001, 1, "token", False, False, True, "f32"),     # single elements
+    (2, 40, 1040, 2, "token", False, True, False, "bf16"),
+    (2, 40, 1030, 2, "token", True, True, True, "bf16"),      # 515 channels: single elements
+    (300, 2, 96, 4, "sequence", True, False, True, "f32"),
+    (33, 4, 330, 10, "sequence", False, True, True, "f32"),
+    (9, 3, 4096, 2, "sequence", True, True, True, "bf16"),
+    (5, 2, 20000, 1, "sequence", False, True, True, "bf16"),
+    (70000, 4, 16, 2, "sequence", True, True, True, "bf16"),  # more rows than a launch has slabs for
+    (66000, 5, 12, 3, "sequence", False, True, True, "f32"),
+    (2, 1, 70000, 1, "token", False, False, True, "bf16"),
+]
+
+
+@pytest.mark.parametrize("B,L,C,G,span,silu,gate,affine,dt", WALKED)
+def test_parity_walked(ssm, B, L, C, G, span, silu, gate, affine, dt):
+    test_parity(ssm, B, L, C, G, span, silu, gate, affine, dt)
+
+
+def test_more_wide_tokens_than_65535(ssm):
+    """66000 tokens of 515 channels (more than a team's registers hold in the backward): the last tokens' dx and dz
+    are those of a small call, dw and dbias those of the formula in 64 bits."""
+    import torch
+    N, C = 66000, 515
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x, z, dy = (torch.randn(N, C, device="cuda", generator=gen).bfloat16() for _ in range(3))
+    w, b = (torch.randn(C, device="cuda", generator=gen) for _ in range(2))
+    _, mean, rstd = ssm.groupnorm_fwd(x, 1, w, b, z, return_stats=True)
+    g = ssm.groupnorm_bwd(x, 1, w, b, z, dy, mean, rstd)
+    tail = [t[-8:].clone() for t in (x, z, dy, mean, rstd)]
+    ref = ssm.groupnorm_bwd(tail[0], 1, w, b, tail[1], tail[2], tail[3], tail[4])
+    for n in ("dx", "dz"):
+        assert torch.equal(g[n][-8:], ref[n]), n
+    xd, zd = x.double(), z.double()
+    xh = (xd - xd.mean(1, keepdim=True)) / (xd.var(1, unbiased=False, keepdim=True) + EPS).sqrt()
+    e = dy.double() * zd * torch.sigmoid(zd)
+    for got, term in ((g["dw"], e * xh), (g["dbias"], e)):
+        # rows in slabs of at most 300 additions in a row and trees: 600 * 2^-24 of the sum of |terms|, as above
+        assert bool(((got.double() - term.sum(0)).abs() <= 600 * 2.0 ** -24 * term.abs().sum(0)).all())
+
+
+def test_wide_tokens_train(ssm):
+    """The layer norm of wide tokens, through autograd."""
+    import torch
+    x = torch.randn(3, 50, 6000, device="cuda", requires_grad=True)
+    w = torch.randn(6000, device="cuda", requires_grad=True)
+    dy = torch.randn(3, 50, 6000, device="cuda")
+    got = torch.autograd.grad(ssm.group_norm(x, 1, w), (x, w), dy)
+    xd, wd = x.detach().double().requires_grad_(), w.detach().double().requires_grad_()
+    ref = torch.autograd.grad(torch.nn.functional.layer_norm(xd, (6000,), wd, None, 1e-5), (xd, wd), dy.double())
+    for g, r in zip(got, ref):
+        # 600 * 2^-24 of terms of size |x| |w| |dy|, at most 6^3, and of 150 such terms' sum in dw (root mean square 20)
+        assert float((g.double() - r).abs().max()) <= 600 * 2.0 ** -24 * 6.0 ** 3

@@ -88,3 +88,23 @@ def test_blocks_of_one_launch(lib):
     """Groups just wider than half a workgroup take one each, and a launch has 65535 of them across."""
     assert fwd(lib, N=1, L=100, C=129 * 100000, G=100000) == 2 and b"too many" in lib.ssm_last_error()
     assert fwd(lib, N=1, L=100, C=129 * 65000, G=65000, x=None) == 1 and b"x is NULL" in lib.ssm_last_error()
+
+
+@pytest.mark.parametrize("N,L,C,G", [(1 << 16, 1, 5120, 1), (70000, 4, 512, 32), (66000, 1, 515, 1), (65535, 1, 1 << 14, 1), (1 << 20, 2, 64, 64),
+                                     (1 << 16, 1, 1 << 15, 1), (70000, 1000, 512, 32), (2, 100, 129 * 100000, 100000), (3, 1, (1 << 24) - 1, 1),
+                                     (2, 2, (1 << 24) - 1, (1 << 24) - 1), (70000, 2, 1025, 1)])
+@pytest.mark.parametrize("dt", [0, 1])
+def test_the_backward_takes_what_the_forward_takes(lib, N, L, C, G, dt):
+    """(x NULL: refused as a pointer where the shape is taken)"""
+    status = fwd(lib, N=N, L=L, C=C, G=G, dt=dt, x=None)
+    assert status in (1, 2)
+    assert bwd(lib, N=N, L=L, C=C, G=G, dt=dt, x=None) == status, lib.ssm_last_error()
+
+
+def test_the_backwards_workspace_does_not_grow_with_the_tokens(lib):
+    for dtype in ("bf16", "f32"):
+        one, two, many = (ssm.groupnorm_workspace_bytes(1, n, 8192, 1, dtype, backward=True) for n in (16384, 32768, 65535))
+        assert one == two == many <= 64 << 20
+    # sequences of a few positions, short of a launch's slabs and beyond
+    assert ssm.groupnorm_workspace_bytes(60000, 2, 4096, 8, span="sequence", backward=True) <= 64 << 20
+    assert 0 < ssm.groupnorm_workspace_bytes(70000, 4, 512, 32, span="sequence", backward=True) <= 64 << 20
