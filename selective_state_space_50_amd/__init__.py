@@ -236,6 +236,17 @@ def _need(t, name, shape, dtype, device):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _aligned(t):
+    """t, or a copy where t does not start on 16 bytes (a part of another tensor may not), as the library needs it."""
+    return t if t is None or t.data_ptr() % 16 == 0 else t.clone()
+
+
+def _gradient(g):
+    """An incoming gradient as the library takes one: contiguous and on 16 bytes (torch's cat, for one, hands out
+    parts of a larger gradient)."""
+    return None if g is None else _aligned(g.contiguous())
+
+
 def scan_fwd(x, delta, A, B, C, D=None, z=None, h0=None, *, delta_softplus=False,
              discretization="mamba", delta_bias=None,
              return_last_state=False, out=None, h_last=None, workspace=None, chunk_len=0,
@@ -526,7 +537,7 @@ def selective_scan(x, delta, A, B, C, D=None, z=None, h0=None, delta_softplus=Fa
         @staticmethod
         def backward(ctx, gy):
             x, delta, A, B, C, D, z, h0, delta_bias, ck = ctx.saved_tensors
-            g = scan_bwd(x, delta, A, B, C, D, z, h0, gy.contiguous(), delta_softplus=delta_softplus,
+            g = scan_bwd(x, delta, A, B, C, D, z, h0, _gradient(gy), delta_softplus=delta_softplus,
                          discretization=discretization, delta_bias=delta_bias, checkpoints=ck, need_dh0=h0 is not None and ctx.needs_input_grad[7])
             return (g["dx"], g["ddelta"], g["dA"], g["dB"], g["dC"], g["dD"], g["dz"], g["dh0"],
                     g["ddelta_bias"])
@@ -617,7 +628,7 @@ def causal_conv1d(x, w, bias=None, state=None, silu=True):
         @staticmethod
         def backward(ctx, gy):
             x, w, bias, state = ctx.saved_tensors
-            g = conv1d_bwd(x, w, bias, state, gy.contiguous(), silu=silu,
+            g = conv1d_bwd(x, w, bias, state, _gradient(gy), silu=silu,
                            need_dstate=state is not None and ctx.needs_input_grad[3])
             return g["dx"], g["dw"], g["dbias"], g["dstate"]
 
@@ -863,9 +874,10 @@ def linattn_fwd(q, k, v, log_decay, h0=None, *, scale=None, lengths=None, return
     q, k: [B, L, heads, dk];  v: [B, L, heads, dv] (all bf16, or all fp32; dk, dv <= 256);
     log_decay: [H] fp32, usually <= 0;  h0: [B, H, dk, dv] fp32.  The head counts of q, k and v
     each divide H: consecutive heads share a row.  q, k, v may be slices of one wider tensor
-    (heads contiguous, tokens evenly spaced).  scale: default dk ** -0.5.  lengths: [B] int32,
-    the tokens of each row, with padding behind them (y is zero there, the last state is the one
-    after lengths[b] tokens).  Returns y [B, L, H, dv], or (y, h_last) when return_last_state.
+    (heads contiguous, tokens evenly spaced).  Every tensor but log_decay and lengths (which are
+    copied where they do not) starts on 16 bytes; clone() a part that does not.  scale: default
+    dk ** -0.5.  lengths: [B] int32, the tokens of each row, with padding behind them (y is zero
+    there, the last state is the one after lengths[b] tokens).  Returns y [B, L, H, dv], or (y, h_last) when return_last_state.
     """
     import torch
     dev, dt, s = _linattn_call(q, k, v, log_decay, 4, "linattn_fwd")
@@ -882,6 +894,7 @@ def linattn_fwd(q, k, v, log_decay, h0=None, *, scale=None, lengths=None, return
         out = q.new_empty(s.out)   # (half the time of torch.empty)
     if return_last_state and h_last is None:
         h_last = log_decay.new_empty(s.state)
+    log_decay, lengths = _aligned(log_decay), _aligned(lengths)
     need = s.fwd_bytes
     workspace = _workspace(workspace, need, dev)
     _check(lib().ssm_linattn_fwd(s.ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
@@ -914,6 +927,7 @@ def linattn_bwd(q, k, v, log_decay, h0=None, dy=None, dh_last=None, *, scale=Non
     out = {"dq": q.new_empty(q.shape), "dk": k.new_empty(k.shape), "dv": v.new_empty(v.shape),
            "dlog_decay": log_decay.new_empty(log_decay.shape) if need_dlog_decay else None,
            "dh0": log_decay.new_empty(s.state) if need_dh0 else None}
+    log_decay, lengths = _aligned(log_decay), _aligned(lengths)
     need = s.bwd_bytes[bool(need_dlog_decay)]
     workspace = _workspace(workspace, need, dev)
     _check(lib().ssm_linattn_bwd(s.ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
@@ -926,7 +940,7 @@ def linattn_bwd(q, k, v, log_decay, h0=None, dy=None, dh_last=None, *, scale=Non
 
 def linattn_update(h, q, k, v, log_decay, *, scale=None, out=None, stream=None):
     """One token of linattn_fwd: h [B, H, dk, dv] fp32 is updated in place; q, k [B, heads, dk],
-    v [B, heads, dv]; returns y [B, H, dv]."""
+    v [B, heads, dv], alignment as there; returns y [B, H, dv]."""
     import torch
     dev, dt, s = _linattn_call(q, k, v, log_decay, 3, "linattn_update")
     there = _elsewhere(dev, stream)
@@ -938,6 +952,7 @@ def linattn_update(h, q, k, v, log_decay, *, scale=None, out=None, stream=None):
         out = q.new_empty(s.token)
     else:
         _need(out, "out", s.token, dt, dev)
+    log_decay = _aligned(log_decay)
     _check(lib().ssm_linattn_update(s.ref, h.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
                                     s.scale if scale is None else scale, out.data_ptr(), _stream(dev)), "ssm_linattn_update")
     return out
@@ -961,7 +976,7 @@ def _linattn_function():
         def backward(ctx, gy, gh=None):
             q, k, v, log_decay, h0, lengths = ctx.saved_tensors
             need = ctx.needs_input_grad
-            g = linattn_bwd(q, k, v, log_decay, h0, gy.contiguous(), None if gh is None else gh.contiguous(),
+            g = linattn_bwd(q, k, v, log_decay, h0, _gradient(gy), _gradient(gh),
                             scale=ctx.scale, lengths=lengths, need_dlog_decay=need[3], need_dh0=h0 is not None and need[4])
             return g["dq"], g["dk"], g["dv"], g["dlog_decay"], g["dh0"], None, None, None
 
@@ -1015,7 +1030,8 @@ def groupnorm_fwd(x, groups, w=None, bias=None, z=None, *, span="token", activat
     x, z: [B, L, D] or [B, D] (bf16 or fp32), the D channels in ``groups`` groups of consecutive
     ones; w, bias: [D] fp32.  span: the values that share a mean and variance, a group's channels
     of one token ("token": the norm after linear attention, a group per head) or of the whole
-    sequence ("sequence").  activation: "none" or "silu".  Returns y, or (y, mean, rstd) when
+    sequence ("sequence").  activation: "none" or "silu".  Tensors are contiguous and start on 16
+    bytes.  Returns y, or (y, mean, rstd) when
     return_stats: [B, L, groups] (or [B, groups]) fp32, what groupnorm_bwd reads.
     """
     import torch
@@ -1096,7 +1112,7 @@ def _groupnorm_function():
         def backward(ctx, gy):
             x, w, bias, z, mean, rstd = ctx.saved_tensors
             groups, span, activation = ctx.how
-            g = groupnorm_bwd(x, groups, w, bias, z, gy.contiguous(), mean, rstd, span=span, activation=activation,
+            g = groupnorm_bwd(x, groups, w, bias, z, _gradient(gy), mean, rstd, span=span, activation=activation,
                               need_dw=ctx.needs_input_grad[2] or ctx.needs_input_grad[3])
             return g["dx"], None, g["dw"], g["dbias"], g["dz"], None, None, None
 

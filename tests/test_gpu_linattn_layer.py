@@ -141,3 +141,49 @@ def test_captured_training_step(ssm):  # noqa: F811
         torch.cuda.synchronize()
         for i, (t, r) in enumerate(zip(held, ref)):
             assert torch.equal(t, r), i
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_outputs_joined_before_the_loss(ssm, dt):  # noqa: F811
+    """Outputs joined along the batch: the second part's gradient is a part of the whole one and need not start on 16 bytes."""
+    import torch
+    tdt = torch.bfloat16 if dt == "bf16" else torch.float32
+    new = lambda *shape: torch.randn(*shape, device="cuda").to(tdt)  # noqa: E731
+    q, k, v = (new(1, 17, 3, 33) for _ in range(3))
+    a = -torch.rand(3, device="cuda")
+    x, w = new(1, 17, 99), torch.randn(99, device="cuda")
+    dt_, al, bl, cl = -torch.rand(99, 4, device="cuda"), new(1, 17, 99).abs(), new(1, 17, 4), torch.randn(99, 3, device="cuda")
+    for f, args in ((lambda q, k, v, a: ssm.linear_attention(q, k, v, a), (q, k, v, a)),
+                    (lambda x, w: ssm.group_norm(x, 3, w), (x, w)),
+                    (lambda x, w: ssm.causal_conv1d(x, w), (x, cl)),
+                    (lambda x, d, A, B: ssm.selective_scan(x, d, A, B, B), (x, al, dt_, bl))):
+        one, two = ([t.clone().requires_grad_() for t in args] for _ in range(2))
+        y1, y2 = f(*one), f(*two)
+        dy = new(2, *y1.shape[1:])
+        assert dy[1].data_ptr() % 16
+        got = torch.autograd.grad(torch.cat([y1, y2]), [*one, *two], dy)
+        ref = [*torch.autograd.grad(f(*one), one, dy[:1].clone()), *torch.autograd.grad(f(*two), two, dy[1:].clone())]
+        for g, r in zip(got, ref):
+            assert torch.equal(g, r)
+
+
+def test_decays_and_lengths_of_a_larger_tensor(ssm):  # noqa: F811
+    """One layer's row of [layers, 6] decays, and a batch's later lengths."""
+    import torch
+    decays = -torch.rand(3, 6, device="cuda")
+    lengths = torch.tensor([3, 40, 17], dtype=torch.int32, device="cuda")
+    q, k, v, dy = (torch.randn(2, 40, 6, 16, device="cuda").bfloat16() for _ in range(4))
+    a, n = decays[1], lengths[1:]
+    assert a.data_ptr() % 16 and n.data_ptr() % 16
+    (y, h), (yr, hr) = (ssm.linattn_fwd(q, k, v, t, lengths=m, return_last_state=True) for t, m in ((a, n), (a.clone(), n.clone())))
+    assert torch.equal(y, yr) and torch.equal(h, hr)
+    g, r = (ssm.linattn_bwd(q, k, v, t, dy=dy, lengths=m) for t, m in ((a, n), (a.clone(), n.clone())))
+    for name in r:
+        assert torch.equal(g[name], r[name]), name
+    h2 = h.clone()
+    one = [t[:, 0].contiguous() for t in (q, k, v)]
+    assert torch.equal(ssm.linattn_update(h, *one, a), ssm.linattn_update(h2, *one, a.clone())) and torch.equal(h, h2)
+    # and through autograd, where the gradient is the whole tensor's
+    whole = decays.clone().requires_grad_()
+    (gw,) = torch.autograd.grad(ssm.linear_attention(q, k, v, whole[1], lengths=n), whole, dy)
+    assert torch.equal(gw[1], r["dlog_decay"]) and not gw[0].any() and not gw[2].any()
