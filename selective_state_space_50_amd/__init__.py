@@ -247,6 +247,15 @@ def _gradient(g):
     return None if g is None else _aligned(g.contiguous())
 
 
+def _written(*tensors):
+    """Tell autograd that the library writes these (its pointers do not): a backward that has saved one of them then
+    raises, as after torch's own in-place operations."""
+    import torch
+    for t in tensors:
+        if t is not None:
+            torch.autograd.graph.increment_version(t)
+
+
 def scan_fwd(x, delta, A, B, C, D=None, z=None, h0=None, *, delta_softplus=False,
              discretization="mamba", delta_bias=None,
              return_last_state=False, out=None, h_last=None, workspace=None, chunk_len=0,
@@ -296,6 +305,7 @@ def scan_fwd(x, delta, A, B, C, D=None, z=None, h0=None, *, delta_softplus=False
                             _ptr(workspace) if ws_bytes else None, ws_bytes,
                             ctypes.c_void_p(s.cuda_stream))
     _check(st, "ssm_scan_fwd")
+    _written(out, h_last)
     return (out, h_last) if return_last_state else out
 
 
@@ -330,6 +340,7 @@ def scan_fwd_noalloc(x, delta, A, B, C, D=None, z=None, h0=None, *, delta_softpl
                                     int(bool(delta_softplus)), ctypes.byref(v) if v else None,
                                     ctypes.byref(o) if o else None, ctypes.c_void_p(s.cuda_stream))
     _check(st, "ssm_scan_fwd_noalloc")
+    _written(out, h_last)
     return (out, h_last) if h_last is not None else out
 
 
@@ -390,6 +401,7 @@ def state_update(h, x, delta, A, B, C, D=None, z=None, *, delta_softplus=False,
                                 _ptr(C), _ptr(D), _ptr(z), _ptr(out), int(bool(delta_softplus)),
                                 ctypes.byref(v) if v else None, ctypes.c_void_p(s.cuda_stream))
     _check(st, "ssm_state_update")
+    _written(h, out)
     return out
 
 
@@ -452,6 +464,7 @@ def scan_fwd_save(x, delta, A, B, C, D=None, z=None, h0=None, *, delta_softplus=
                                  _ptr(checkpoints), _ptr(workspace) if ws_bytes else None, ws_bytes,
                                  ctypes.c_void_p(s.cuda_stream))
     _check(st, "ssm_scan_fwd_save")
+    _written(out, h_last, checkpoints)
     return (out, h_last, checkpoints) if return_last_state else (out, checkpoints)
 
 
@@ -569,6 +582,7 @@ def conv1d_fwd(x, w, bias=None, state=None, *, silu=True, return_state=False, ou
     _check(lib().ssm_conv1d_fwd(Bsz, L, Dm, W, _dtype_code(x), _ptr(x), _ptr(w), _ptr(bias), _ptr(state),
                                 _ptr(out), _ptr(st_out), int(bool(silu)), ctypes.c_void_p(s.cuda_stream)),
            "ssm_conv1d_fwd")
+    _written(out)
     return (out, st_out) if return_state else out
 
 
@@ -656,6 +670,7 @@ def conv1d_update(state, x, w, bias=None, *, silu=True, out=None, stream=None):
     _check(lib().ssm_conv1d_update(Bsz, Dm, W, _dtype_code(x), _ptr(state), _ptr(x), _ptr(w), _ptr(bias),
                                    _ptr(out), int(bool(silu)), ctypes.c_void_p(s.cuda_stream)),
            "ssm_conv1d_update")
+    _written(state, out)
     return out
 
 
@@ -699,6 +714,7 @@ def ssd_fwd(x, delta, A, B, C, D=None, z=None, h0=None, *, delta_softplus=False,
                            _ptr(z), _ptr(delta_bias), _ptr(h0), _ptr(h_last), _ptr(out),
                            int(bool(delta_softplus)), ctypes.c_void_p(s.cuda_stream))
     _check(st, "ssm_ssd_fwd")
+    _written(out, h_last)
     return (out, h_last) if return_last_state else out
 
 
@@ -890,6 +906,8 @@ def linattn_fwd(q, k, v, log_decay, h0=None, *, scale=None, lengths=None, return
     _need(lengths, "lengths", s.state[:1], torch.int32, dev)
     _need(out, "out", s.out, dt, dev)
     _need(h_last, "h_last", s.state, torch.float32, dev)
+    if out is not None or h_last is not None:
+        _written(out, h_last)
     if out is None:
         out = q.new_empty(s.out)   # (half the time of torch.empty)
     if return_last_state and h_last is None:
@@ -953,6 +971,7 @@ def linattn_update(h, q, k, v, log_decay, *, scale=None, out=None, stream=None):
     else:
         _need(out, "out", s.token, dt, dev)
     log_decay = _aligned(log_decay)
+    _written(h, out)
     _check(lib().ssm_linattn_update(s.ref, h.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
                                     s.scale if scale is None else scale, out.data_ptr(), _stream(dev)), "ssm_linattn_update")
     return out
@@ -1050,6 +1069,8 @@ def groupnorm_fwd(x, groups, w=None, bias=None, z=None, *, span="token", activat
     _need(out, "out", shape, dt, dev)
     if out is None:
         out = x.new_empty(shape)
+    else:
+        _written(out)
     mean, rstd = (torch.empty(stats, dtype=torch.float32, device=dev) for _ in range(2)) if return_stats else (None, None)
     need = _groupnorm_bytes(size, groups, code, 0)
     workspace = _workspace(workspace, need, dev)

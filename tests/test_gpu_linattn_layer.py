@@ -187,3 +187,34 @@ def test_decays_and_lengths_of_a_larger_tensor(ssm):  # noqa: F811
     whole = decays.clone().requires_grad_()
     (gw,) = torch.autograd.grad(ssm.linear_attention(q, k, v, whole[1], lengths=n), whole, dy)
     assert torch.equal(gw[1], r["dlog_decay"]) and not gw[0].any() and not gw[2].any()
+
+
+def test_writes_are_seen_by_autograd(ssm):  # noqa: F811
+    """A tensor that a backward has saved and a call then writes (a state advanced in place, a given output): the
+    backward raises, as after torch's own in-place operations, and does not read the new values."""
+    import torch
+    new = lambda *shape: torch.randn(*shape, device="cuda")  # noqa: E731
+    q, k, v, a, h = new(2, 9, 4, 16), new(2, 9, 4, 16), new(2, 9, 4, 16), -torch.rand(4, device="cuda"), new(2, 4, 16, 16)
+    one = [t[:, 0].contiguous() for t in (q, k, v)]
+    x, w, st = new(2, 9, 64), new(64, 4), new(2, 64, 3)
+    d, A, B, hs = new(2, 9, 64).abs(), -torch.rand(64, 16, device="cuda"), new(2, 9, 16), new(2, 64, 16)
+    x3 = new(2, 4, 16)
+    leaf = lambda t: t.clone().requires_grad_()  # noqa: E731
+    for what, forward, saved, write in (
+            ("linattn_update's state", lambda: ssm.linear_attention(leaf(q), k, v, a, h), h, lambda: ssm.linattn_update(h, *one, a)),
+            ("linattn_update's out", lambda: ssm.group_norm(x3, 4, leaf(x3[0, 0])), x3, lambda: ssm.linattn_update(h, *one, a, out=x3)),
+            ("linattn_fwd's h_last", lambda: ssm.linear_attention(leaf(q), k, v, a, h), h,
+             lambda: ssm.linattn_fwd(q, k, v, a, return_last_state=True, h_last=h)),
+            ("linattn_fwd's out", lambda: ssm.linear_attention(leaf(q), k, v, a), v, lambda: ssm.linattn_fwd(q, k, q, a, out=v)),
+            ("groupnorm_fwd's out", lambda: ssm.group_norm(x, 4, leaf(w[:, 0].contiguous())), x, lambda: ssm.groupnorm_fwd(d, 4, out=x)),
+            ("conv1d_update's state", lambda: ssm.causal_conv1d(leaf(x), w, None, st), st, lambda: ssm.conv1d_update(st, x[:, 0].contiguous(), w)),
+            ("conv1d_fwd's out", lambda: ssm.causal_conv1d(x, leaf(w)), x, lambda: ssm.conv1d_fwd(d, w, out=x)),
+            ("state_update's state", lambda: ssm.selective_scan(leaf(x), d, A, B, B, h0=hs), hs,
+             lambda: ssm.state_update(hs, x[:, 0].contiguous(), d[:, 0].contiguous(), A, B[:, 0].contiguous(), B[:, 0].contiguous())),
+            ("scan_fwd's out", lambda: ssm.selective_scan(leaf(x), d, A, B, B), d, lambda: ssm.scan_fwd(x, d.clone(), A, B, B, out=d))):
+        y = forward()
+        before = saved._version
+        write()
+        assert saved._version > before, what
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.sum().backward()
