@@ -517,7 +517,7 @@ size_t ssm_linattn_workspace_bytes(const ssm_linattn_shape *shape);
  * matrix cores.  A token's NaN or infinity reaches its own and later outputs only (where an
  * infinity may turn into NaN).  Deterministic.
  * SSM_EUNSUPPORTED: dk or dv over SSM_LINATTN_MAX_DIM, batch * nheads over 2^20, nheads over 2^16, seqlen
- * over 2^30, q_row, k_row or v_row over 2^24.
+ * over 2^30, q_row, k_row or v_row over 2^24 where seqlen > 1 (2^50 / (batch * seqlen) where it is 1).
  */
 int ssm_linattn_fwd(const ssm_linattn_shape *shape, const void *q, const void *k, const void *v,
                     const float *log_decay, float scale, const int32_t *lengths, const float *h0,

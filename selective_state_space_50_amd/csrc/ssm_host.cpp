@@ -899,9 +899,13 @@ int plan_linattn(const ssm_linattn_shape *s, bool decay_grad, LinAttnPlan *plan)
                       (long long)least);
             return SSM_EINVAL;
         }
-        // (row offsets within a chunk are 32-bit)
-        if (*out[i] > (int64_t(1) << 24)) {
+        // (row offsets within a chunk are 32-bit; one token has no second row, and batch rows' offsets are 64-bit)
+        if (s->seqlen > 1 && *out[i] > (int64_t(1) << 24)) {
             set_error("%c_row=%lld: at most %d elements from token to token are supported", "qkv"[i], (long long)*out[i], 1 << 24);
+            return SSM_EUNSUPPORTED;
+        }
+        if (s->batch > 0 && s->seqlen > 0 && *out[i] > kMaxElems / (s->batch * s->seqlen)) {
+            set_error("%c_row=%lld is too large", "qkv"[i], (long long)*out[i]);
             return SSM_EUNSUPPORTED;
         }
     }

@@ -447,3 +447,30 @@ def test_joining_many_segments_keeps_the_precision(ssm, dt, decay):
     # sqrt(600) 2^-24 / sqrt(3) = 8.4e-7; a decay off by 2^-26 in every one of 255 joins is off by 3.8e-6
     for got, ref in ((h, f * h0), (g["dh0"], f * h0), (g["dlog_decay"], np.array([L * f * (h0 ** 2).sum()]))):
         assert np.linalg.norm(to_host(got) - ref) <= 2e-6 * np.linalg.norm(ref)
+
+
+def test_tokens_of_a_long_wide_prompt(ssm):
+    """One token of every sequence as a part of a prompt's projection, 2^25 elements apart: the update, and a prompt of one."""
+    import torch
+    x = torch.empty(2, 4096, 8192, device="cuda", dtype=torch.bfloat16)
+    x[:, 4095] = torch.randn(2, 8192, device="cuda").bfloat16()
+    heads = x.view(2, 4096, 64, 128)
+    a = -torch.rand(64, device="cuda")
+    parts = [heads[:, 4095, :, 64 * i:64 * i + 64] for i in range(2)]
+    wide = heads[:, 4095]
+    assert wide.stride(0) == 1 << 25
+    h = torch.randn(2, 64, 128, 128, device="cuda")
+    h0 = h.clone()
+    y = ssm.linattn_update(h, wide, wide, wide, a)
+    h2 = h0.clone()
+    c = wide.contiguous()
+    assert torch.equal(y, ssm.linattn_update(h2, c, c, c, a)) and torch.equal(h, h2)
+    with pytest.raises(ValueError, match="contiguous"):
+        ssm.linattn_update(h0.clone(), parts[0], parts[1], parts[0], a)   # (heads that do not stand side by side)
+    one = heads[:, 4095:]
+    dy = torch.randn(2, 1, 64, 128, device="cuda").bfloat16()
+    (y, h), (yr, hr) = (ssm.linattn_fwd(t, t, t, a, h0, return_last_state=True) for t in (one, one.contiguous()))
+    assert torch.equal(y, yr) and torch.equal(h, hr)
+    g, r = (ssm.linattn_bwd(t, t, t, a, h0, dy) for t in (one, one.contiguous()))
+    for n in r:
+        assert torch.equal(g[n], r[n]), n

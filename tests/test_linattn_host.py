@@ -150,3 +150,17 @@ def test_rows_of_one_launch(lib):
     assert fwd(lib, s) == 2 and b"too large" in lib.ssm_last_error()
     s.batch = 1 << 17
     assert fwd(lib, s, q=None) == 1 and b"q is NULL" in lib.ssm_last_error()
+
+
+def test_one_tokens_rows_may_lie_far_apart(lib):
+    """Offsets within a chunk are 32-bit, but one token (of a prompt, or the update) has no second row there."""
+    for far in (dict(q_row=1 << 25), dict(k_row=1 << 40), dict(v_row=(1 << 24) + 1)):
+        s = shape(seqlen=1, **far)
+        assert fwd(lib, s, q=None) == 1 and b"q is NULL" in lib.ssm_last_error()
+        assert lib.ssm_linattn_update(ctypes.byref(s), None, P(0), P(1), P(2), P(3), 1.0, P(5), None) == 1
+        assert b"h is NULL" in lib.ssm_last_error()
+        s.seqlen = 2
+        assert fwd(lib, s, q=None) == 2 and b"_row" in lib.ssm_last_error()
+    # byte offsets stay within 64 bits
+    assert fwd(lib, shape(seqlen=1, k_row=1 << 60), q=None) == 2 and b"k_row" in lib.ssm_last_error()
+    assert fwd(lib, shape(batch=1 << 16, seqlen=1 << 20, nheads=1, q_heads=1, k_heads=1, v_heads=1, q_row=1 << 24), q=None) == 2
