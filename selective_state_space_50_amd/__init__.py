@@ -247,6 +247,19 @@ def _gradient(g):
     return None if g is None else _aligned(g.contiguous())
 
 
+def _workspace(given, need, device):
+    """The caller's workspace where it is large enough, else a new one.  (A kernel writes ``need`` bytes from its
+    address on: it has to lie in one piece on the tensors' device.)"""
+    import torch
+    if given is not None and given.device != device:
+        raise ValueError(f"workspace is on {given.device}, expected {device}")
+    if given is not None and not given.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if need and (given is None or given.numel() * given.element_size() < need):
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    return given
+
+
 def _written(*tensors):
     """Tell autograd that the library writes these (its pointers do not): a backward that has saved one of them then
     raises, as after torch's own in-place operations."""
@@ -295,8 +308,7 @@ def scan_fwd(x, delta, A, B, C, D=None, z=None, h0=None, *, delta_softplus=False
     _need(h_last, "h_last", (Bsz, Dm, N), torch.float32, dev)
     o = _opts(chunk_len, states_per_lane, time_block, one_block_per_cu, general_a)
     ws_bytes = int(lib().ssm_scan_workspace_bytes(Bsz, L, Dm, N, code, ctypes.byref(o) if o else None))
-    if ws_bytes and (workspace is None or workspace.numel() * workspace.element_size() < ws_bytes):
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    workspace = _workspace(workspace, ws_bytes, dev)
     s = stream if stream is not None else torch.cuda.current_stream(dev)
     st = lib().ssm_scan_fwd(Bsz, L, Dm, N, code, _ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C),
                             _ptr(D), _ptr(z), _ptr(h0), _ptr(h_last), _ptr(out),
@@ -455,8 +467,7 @@ def scan_fwd_save(x, delta, A, B, C, D=None, z=None, h0=None, *, delta_softplus=
     _need(checkpoints, "checkpoints", (Bsz, nck, N, Dm), torch.float32, dev)
     if not checkpoints.is_contiguous() or checkpoints.numel() * 4 != ck_bytes:
         raise ValueError(f"checkpoints must be a contiguous fp32 tensor of {ck_bytes} bytes")
-    if ws_bytes and (workspace is None or workspace.numel() * workspace.element_size() < ws_bytes):
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    workspace = _workspace(workspace, ws_bytes, dev)
     s = stream if stream is not None else torch.cuda.current_stream(dev)
     st = lib().ssm_scan_fwd_save(Bsz, L, Dm, N, code, _ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C),
                                  _ptr(D), _ptr(z), _ptr(h0), _ptr(h_last), _ptr(out),
@@ -511,8 +522,7 @@ def scan_bwd(x, delta, A, B, C, D=None, z=None, h0=None, dy=None, dh_last=None, 
            "dh0": torch.empty((Bsz, Dm, N), dtype=torch.float32, device=dev) if need_dh0 else None,
            "ddelta_bias": torch.empty((Dm,), dtype=torch.float32, device=dev) if delta_bias is not None else None}
     ws_bytes = int(lib().ssm_scan_bwd_workspace_bytes(Bsz, L, Dm, N, code, int(checkpoints is not None)))
-    if ws_bytes and (workspace is None or workspace.numel() * workspace.element_size() < ws_bytes):
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    workspace = _workspace(workspace, ws_bytes, dev)
     s = stream if stream is not None else torch.cuda.current_stream(dev)
     st = lib().ssm_scan_bwd(Bsz, L, Dm, N, code, _ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C),
                             _ptr(D), _ptr(z), _ptr(h0), _ptr(dy), _ptr(dh_last), _ptr(out["dx"]),
@@ -617,8 +627,7 @@ def conv1d_bwd(x, w, bias=None, state=None, dy=None, *, silu=True, need_dstate=N
            "dstate": torch.empty((Bsz, Dm, W - 1), dtype=x.dtype, device=dev) if need_dstate else None}
     code = _dtype_code(x)
     ws_bytes = int(lib().ssm_conv1d_bwd_workspace_bytes(Bsz, L, Dm, W, code))
-    if ws_bytes and (workspace is None or workspace.numel() * workspace.element_size() < ws_bytes):
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    workspace = _workspace(workspace, ws_bytes, dev)
     s = stream if stream is not None else torch.cuda.current_stream(dev)
     _check(lib().ssm_conv1d_bwd(Bsz, L, Dm, W, code, _ptr(x), _ptr(w), _ptr(bias), _ptr(state), _ptr(dy),
                                 _ptr(out["dx"]), _ptr(out["dw"]), _ptr(out["dbias"]), _ptr(out["dstate"]),
@@ -761,8 +770,7 @@ def ssd_bwd(x, delta, A, B, C, D=None, z=None, h0=None, dy=None, dh_last=None, *
            "ddelta_bias": torch.empty((H,), dtype=f32, device=dev) if delta_bias is not None else None,
            "dh0": torch.empty((Bsz, H, P, N), dtype=f32, device=dev)}
     ws_bytes = int(lib().ssm_ssd_bwd_workspace_bytes(Bsz, L, H, P, N, code))
-    if ws_bytes and (workspace is None or workspace.numel() * workspace.element_size() < ws_bytes):
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    workspace = _workspace(workspace, ws_bytes, dev)
     s = stream if stream is not None else torch.cuda.current_stream(dev)
     st = lib().ssm_ssd_bwd(Bsz, L, H, P, N, 1, code, _ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
                            _ptr(z), _ptr(delta_bias), _ptr(h0), _ptr(dy), _ptr(dh_last), _ptr(out["dx"]),
@@ -849,13 +857,6 @@ def _stream(device):
     """torch's current HIP stream on the device, as a raw handle."""
     import torch
     return torch._C._cuda_getCurrentRawStream(device.index)
-
-
-def _workspace(given, need, device):
-    import torch
-    if need and (given is None or given.numel() * given.element_size() < need):
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    return given
 
 
 def _elsewhere(device, stream):

@@ -218,3 +218,25 @@ def test_writes_are_seen_by_autograd(ssm):  # noqa: F811
         assert saved._version > before, what
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             y.sum().backward()
+
+
+def test_small_workspaces_are_replaced(ssm):  # noqa: F811
+    """A workspace that is too small is left alone and another used; one on the host is refused."""
+    import torch
+    q, k, v = (torch.randn(1, 2000, 2, 64, device="cuda").bfloat16() for _ in range(3))
+    a = -torch.rand(2, device="cuda")
+    x, w = torch.randn(2, 3000, 64, device="cuda"), torch.randn(64, device="cuda")
+    _, m, r = ssm.groupnorm_fwd(x, 2, w, span="sequence", return_stats=True)
+    for need, call in ((ssm.linattn_workspace_bytes(1, 2000, 2, 64, 64), lambda ws: ssm.linattn_fwd(q, k, v, a, workspace=ws)),
+                       (ssm.linattn_bwd_workspace_bytes(1, 2000, 2, 64, 64), lambda ws: ssm.linattn_bwd(q, k, v, a, dy=v, workspace=ws)["dq"]),
+                       (ssm.groupnorm_workspace_bytes(2, 3000, 64, 2, "f32", "sequence"),
+                        lambda ws: ssm.groupnorm_fwd(x, 2, w, span="sequence", workspace=ws)),
+                       (ssm.groupnorm_workspace_bytes(2, 3000, 64, 2, "f32", "sequence", True),
+                        lambda ws: ssm.groupnorm_bwd(x, 2, w, None, None, x, m, r, span="sequence", workspace=ws)["dx"])):
+        ref = call(None)
+        for size in (need, need - 1, 0):
+            ws = torch.full((size,), 7, dtype=torch.uint8, device="cuda")
+            assert torch.equal(call(ws), ref)
+            assert size == need or bool((ws == 7).all())
+        with pytest.raises(ValueError, match="workspace is on cpu"):
+            call(torch.empty(need, dtype=torch.uint8))

@@ -164,3 +164,17 @@ def test_one_tokens_rows_may_lie_far_apart(lib):
     # byte offsets stay within 64 bits
     assert fwd(lib, shape(seqlen=1, k_row=1 << 60), q=None) == 2 and b"k_row" in lib.ssm_last_error()
     assert fwd(lib, shape(batch=1 << 16, seqlen=1 << 20, nheads=1, q_heads=1, k_heads=1, v_heads=1, q_row=1 << 24), q=None) == 2
+
+
+def test_workspaces_elsewhere_or_in_pieces_are_refused():
+    """(a kernel would write them by their address)"""
+    import torch
+    gpu, cpu = torch.device("cuda", 0), torch.device("cpu")
+    with pytest.raises(ValueError, match="workspace is on cpu"):
+        ssm._workspace(torch.empty(1000, dtype=torch.uint8), 100, gpu)
+    for bad in (torch.empty(1, dtype=torch.uint8).expand(1000), torch.empty(2000, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="contiguous"):
+            ssm._workspace(bad, 100, cpu)
+    enough = torch.empty(30, dtype=torch.float32)
+    assert ssm._workspace(enough, 120, cpu) is enough and ssm._workspace(None, 0, cpu) is None
+    assert ssm._workspace(enough, 121, cpu).numel() == 121
