@@ -863,6 +863,8 @@ def _elsewhere(device, stream):
     """None where a call runs as things are; else the context it has to run in: the tensors'
     device, and the stream given (what the call allocates then belongs to that stream)."""
     import torch
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
     if stream is None and torch.cuda.current_device() == device.index:
         return None
     return torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)

@@ -178,3 +178,12 @@ def test_workspaces_elsewhere_or_in_pieces_are_refused():
     enough = torch.empty(30, dtype=torch.float32)
     assert ssm._workspace(enough, 120, cpu) is enough and ssm._workspace(None, 0, cpu) is None
     assert ssm._workspace(enough, 121, cpu).numel() == 121
+
+
+def test_a_stream_of_another_device_is_refused():
+    """(the call would run on the tensors' device, but not on the stream)"""
+    from types import SimpleNamespace
+
+    import torch
+    with pytest.raises(ValueError, match="stream is on cuda:1, the tensors on cuda:0"):
+        ssm._elsewhere(torch.device("cuda", 0), SimpleNamespace(device=torch.device("cuda", 1), device_type="cuda"))
