@@ -474,3 +474,32 @@ def test_tokens_of_a_long_wide_prompt(ssm):
     g, r = (ssm.linattn_bwd(t, t, t, a, h0, dy) for t in (one, one.contiguous()))
     for n in r:
         assert torch.equal(g[n], r[n]), n
+
+
+# Sequences whose segments are cut into parts for their own states, the last part of another length than the others
+# (tests/test_linattn_host.py asks the planner); as CASES, and the decay
+PARTS = [
+    (1, 2112, 64, 64, 64, 64, 16, 16, "bf16", True, None, None),
+    (1, 2112, 64, 64, 32, 32, 16, 16, "f32", True, None, -1e-3),
+    (1, 2112, 64, 16, 64, 64, 16, 16, "bf16", True, [1300], -2e-3),      # ends in a segment
+    (2, 1700, 40, 40, 8, 8, 24, 16, "f32", True, [1700, 1000], -1e-3),
+    (2, 2112, 32, 32, 32, 32, 16, 40, "bf16", False, [704, 1409], -5e-4),   # at a segment's end, a row past one
+]
+
+
+@pytest.mark.parametrize("B,L,H,hq,hk,hv,dk,dv,dt,h0,lengths,decay", PARTS)
+def test_segments_in_uneven_parts(ssm, B, L, H, hq, hk, hv, dk, dv, dt, h0, lengths, decay):
+    """Every output and gradient where the states between segments are joined from uneven parts."""
+    import torch
+    c = make(B, L, H, hq, hk, hv, dk, dv, dt, seed=L + dv, decay=decay)
+    q, k, v, a, s0, dy, dh = dev(c, "q", "k", "v", "a", "h0", "dy", "dh")
+    n = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    first, last = (s0, dh) if h0 else (None, None)
+    y, h = ssm.linattn_fwd(q, k, v, a, first, scale=0.3, lengths=n, return_last_state=True)
+    g = ssm.linattn_bwd(q, k, v, a, first, dy, last, scale=0.3, lengths=n)
+    (yr, hr), (ya, ha) = both(linattn, c, ("q", "k", "v", "a", 0.3, "h0" if h0 else None), lengths=lengths)
+    check(y, yr, ya, dt, c, "y")
+    check(h, hr, ha, "f32", c, "h_last")
+    r, big = both(linattn_bwd, c, ("q", "k", "v", "a", 0.3, "h0" if h0 else None, "dy", "dh" if h0 else None), lengths=lengths)
+    for name in ("dq", "dk", "dv", "dlog_decay", "dh0"):
+        check(g[name], r[name], big[name], dt if name in ("dq", "dk", "dv") else "f32", c, name)

@@ -187,3 +187,22 @@ def test_a_stream_of_another_device_is_refused():
     import torch
     with pytest.raises(ValueError, match="stream is on cuda:1, the tensors on cuda:0"):
         ssm._elsewhere(torch.device("cuda", 0), SimpleNamespace(device=torch.device("cuda", 1), device_type="cuda"))
+
+
+def test_the_cases_of_uneven_parts_have_them(tmp_path):
+    """The planner cuts the segments of test_gpu_linattn's PARTS into parts, the last one shorter: forward and backward."""
+    import subprocess
+
+    from tests.test_gpu_linattn import PARTS
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    csrc = os.path.join(root, "selective_state_space_50_amd", "csrc")
+    exe = str(tmp_path / "plan")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-I", os.path.join(root, "include"), "-I", csrc,
+                    os.path.join(root, "tests", "host", "linattn_plan.cpp"), os.path.join(csrc, "ssm_host.cpp"), "-o", exe], check=True)
+    lines = "".join(" ".join(map(str, (*p[:8], 1 if p[8] == "bf16" else 0))) + "\n" for p in PARTS)
+    out = subprocess.run([exe], input=lines, capture_output=True, text=True, check=True).stdout.splitlines()
+    assert len(out) == len(PARTS)
+    for line in out:
+        x = list(map(int, line.split()))
+        for nseg, seg_len, nsub, sub_len in (x[:4], x[4:8]):
+            assert nseg > 1 and nsub > 1 and nsub * sub_len > seg_len, line
