@@ -973,9 +973,13 @@ def linattn_update(h, q, k, v, log_decay, *, scale=None, out=None, stream=None):
         out = q.new_empty(s.token)
     else:
         _need(out, "out", s.token, dt, dev)
-    log_decay = _aligned(log_decay)
-    _written(h, out)
-    _check(lib().ssm_linattn_update(s.ref, h.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+        _written(out)
+    torch.autograd.graph.increment_version(h)   # (as _written)
+    decay = log_decay.data_ptr()
+    if decay % 16:
+        log_decay = log_decay.clone()
+        decay = log_decay.data_ptr()
+    _check(lib().ssm_linattn_update(s.ref, h.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), decay,
                                     s.scale if scale is None else scale, out.data_ptr(), _stream(dev)), "ssm_linattn_update")
     return out
 
