@@ -16,6 +16,9 @@
 // which gives dw and db and, weighted with w, both sums of dx.  Over few positions (or with more rows of
 // statistics than a launch has slabs for) the backward walks every group by a team of lanes instead.
 //
+// All sums are in fp32, in lanes of a few hundred terms and trees of them.  (3x1001x330 in 10 groups, fp32, forward and
+// backward: every output within 1.5e-7 of exact in norm; with dw and db summed in 64 bits, in torch, 1.0e-7.)
+//
 // Measured, bf16 (a copy reaches 5.2 TB/s): 16384 rows of 4096 channels in 64 groups, gated: forward 91 us
 // (4.4 TB/s), backward 132 us (5.1 TB/s) and 6 us for the sums of dw and db.  8 x 4000 x 512 in 32 groups
 // over whole sequences: statistics 8 us (4.1 TB/s), 5 us for their merging, y 16 us (4.1 TB/s of
@@ -77,6 +80,8 @@ __device__ __forceinline__ void channels(const float *p, int64_t c, float none, 
     }
 }
 
+// (hardware exp2 and reciprocal, a step of fp32 each: SiLU and its gradient are within a few steps of exact, below the
+// sums' own roundings)
 __device__ __forceinline__ float sigmoid_f(float u) { return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-u * kLog2e)); }
 
 __device__ __forceinline__ float norm_out(float xh, float w, float b, bool silu, bool gate, float z) {

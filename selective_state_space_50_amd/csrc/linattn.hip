@@ -53,7 +53,10 @@ __device__ __forceinline__ Lds opaque(Lds a) {
 //
 // LDS tiles are unpadded rows of a multiple of 128 bytes; the 16-byte piece c of a row is kept
 // at place c ^ swizzle(row) (within its eight pieces), so that neither reads of one piece of
-// 16 rows nor reads of two pieces of four rows (transposed) meet a bank twice.
+// 16 rows nor reads of two pieces of four rows (transposed) meet a bank more often than reads of
+// 512 bytes in a row do.  (SQ_LDS_BANK_CONFLICT counts two cycles for each of the three.  The bf16 writes pay
+// for it, in two halves of 8 bytes: eight cycles for a row's 16 bytes a lane, and four for a tile of q k^T, where
+// writes in a row count none.)
 template <class T>
 struct Op;
 
@@ -466,11 +469,11 @@ __device__ __forceinline__ void fill_update_weights(float (&up)[2][Q], float *ag
 // all eight waves in one role (half a state each) the weights of v and the sum of two output
 // shares cost a third more VALU instructions and LDS traffic.
 //
-// Measured: B4 L4096 H64 128x64 bf16 (one segment, 256 workgroups) 184 us, 4.4 TB/s; a copy reaches 5.2.
-// Chunks of 64 take 2.9 us (128 columns): per SIMD 1.1 us of VALU and 0.7 us of matrix instructions,
-// in two roles that meet at two barriers; without any product the same loads and stores take 168 us.
+// Measured: B4 L4096 H64 128x64 bf16 (one segment, 256 workgroups) 209 us, 3.9 TB/s (228 us on another
+// machine); a copy reaches 5.2.  Chunks of 64 take 3.2 us (128 columns): per SIMD 1.3 us of VALU and 0.8 us of
+// matrix instructions, in two roles that meet at two barriers; without any product the same loads and stores take 168 us.
 // Smaller chunks would cost more state updates, larger ones more in-chunk products and LDS (121 KB now).
-// AGE doubles the readout and the update (dq of B2 L4096 H32 128x128: 176 us against 105).
+// AGE doubles the readout and the update (dq of B2 L4096 H32 128x128: 189 us against 108 for dk or dv).
 template <class T, int DK, bool AGE>
 struct __align__(16) Smem {
     using G = Tile<T, DK>;
@@ -521,7 +524,7 @@ __global__ void __launch_bounds__(kThreads) linattn_kernel(LinAttnArgs a) {
     const int sh = a.reverse ? 1 : 0, tail = max(end - first, 0) % Q;   // tail: rows of the last chunk, if not whole
     const float la = a.log_decay[p.h];
     if (tid < 2 * Q) fill_update_weights<Q, AGE>(sm.w_up, sm.w_age, tid, la, a.s_wr, sh, tail);
-    float age = 0.0f;
+    float age = 0.0f;   // the thread's share of dlog_decay, over its segment (shares are added in 64 bits)
     // factor of the age products: row t of the sequence, value columns 16 w + 4 lg .. + 3 of this tile
     // (0 past the columns and the rows; VEC: one load, always of the operand)
     const T *age_w = AGE ? static_cast<const T *>(a.age_w) + p.b * a.L * a.age_row + (p.h / (a.H / a.age_heads)) * a.dn + p.n0 : nullptr;
