@@ -1078,7 +1078,8 @@ def groupnorm_fwd(x, groups, w=None, bias=None, z=None, *, span="token", activat
         out = x.new_empty(shape)
     else:
         _written(out)
-    mean, rstd = (torch.empty(stats, dtype=torch.float32, device=dev) for _ in range(2)) if return_stats else (None, None)
+    make = torch.empty if x.numel() else torch.zeros   # (the library leaves statistics of no values as they are)
+    mean, rstd = (make(stats, dtype=torch.float32, device=dev) for _ in range(2)) if return_stats else (None, None)
     need = _groupnorm_bytes(size, groups, code, 0)
     workspace = _workspace(workspace, need, dev)
     _check(lib().ssm_groupnorm_fwd(*size, groups, code, x.data_ptr(), _addr(w), _addr(bias), _addr(z), eps, silu,

@@ -298,3 +298,51 @@ def test_wide_tokens_train(ssm):
     for g, r in zip(got, ref):
         # 600 * 2^-24 of terms of size |x| |w| |dy|, at most 6^3, and of 150 such terms' sum in dw (root mean square 20)
         assert float((g.double() - r).abs().max()) <= 600 * 2.0 ** -24 * 6.0 ** 3
+
+
+def test_walked_backward_captured_and_on_two_streams(ssm):
+    """Wide tokens and short sequences in a graph, replayed over new inputs between eager calls; and two calls at once."""
+    import torch
+    x, z, dy = (torch.randn(6, 3, 9000, device="cuda").bfloat16() for _ in range(3))
+    w, b = torch.randn(9000, device="cuda"), torch.randn(9000, device="cuda")
+
+    def work(stream=None):
+        out = []
+        for span in ("token", "sequence"):
+            _, m, r = ssm.groupnorm_fwd(x, 2, w, b, z, span=span, return_stats=True, stream=stream)
+            out += ssm.groupnorm_bwd(x, 2, w, b, z, dy, m, r, span=span, stream=stream).values()
+        return out
+
+    work()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = work()
+    for i in range(4):
+        for t in (x, z, dy):
+            t.copy_(torch.randn(t.shape, device="cuda"))
+        ref = [t.clone() for t in work()]
+        torch.cuda.synchronize()
+        for t in held:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for j, (t, r) in enumerate(zip(held, ref)):
+            assert torch.equal(t, r), (i, j)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [work(s) for s in streams]
+    torch.cuda.synchronize()
+    for g in got:
+        for t, r in zip(g, ref):
+            assert torch.equal(t, r)
+
+
+def test_statistics_of_no_values(ssm):
+    """A sequence of no positions has statistics of no values: zeros, not what the memory held."""
+    import torch
+    torch.full((12,), 7.0, device="cuda")   # (its memory is the allocator's next choice)
+    x = torch.empty(3, 0, 16, device="cuda")
+    y, mean, rstd = ssm.groupnorm_fwd(x, 4, span="sequence", return_stats=True)
+    assert y.shape == (3, 0, 16) and mean.shape == rstd.shape == (3, 4) and not mean.any() and not rstd.any()
+    g = ssm.groupnorm_bwd(x, 4, torch.ones(16, device="cuda"), None, None, x, mean, rstd, span="sequence")
+    assert g["dx"].shape == x.shape and not g["dw"].any()
