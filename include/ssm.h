@@ -603,6 +603,68 @@ int ssm_groupnorm_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t groups
                       const float *rstd, void *dx, float *dw, float *dbias, void *dz, void *workspace,
                       size_t workspace_bytes, void *stream);
 
+/*
+ * Rotary positions of queries and keys, and an RMS norm of every head in front of them: what lies
+ * between a layer's projection and its (linear) attention.  Per token t and head row x [dim], with
+ * the angle th_j = positions[t] * freqs[j] of pair j < rot / 2:
+ *
+ *     u = x                                      (ssm_rotary_fwd)
+ *     u = x / sqrt(mean(x^2) + eps) * w          (ssm_qknorm_fwd; w: wq for q's heads, wk for k's)
+ *     (y_a, y_b) = magnitude * (u_a cos th_j - u_b sin th_j, u_b cos th_j + u_a sin th_j)
+ *     y_c = u_c                                  for columns c >= rot
+ *
+ * with (a, b) = (j, j + rot / 2), or (2j, 2j + 1) when interleaved.  Angles are taken in 64 bits.
+ * Sizes and layouts of a call:
+ */
+typedef struct ssm_rotary_shape {
+    int64_t tokens;             /* of all batch rows together */
+    int64_t period;             /* token t has positions[t % period]; 0: positions[t] */
+    int64_t q_heads, k_heads;   /* heads of a token; 0: no q, no k */
+    int64_t dim, rot;           /* columns of a head (1 .. SSM_ROTARY_MAX_DIM); how many of them turn: even, 0 .. dim */
+    int64_t q_row, k_row;       /* elements from one token's heads to the next token's (e.g. in a joint
+                                   projection's output); 0: q_heads * dim, k_heads * dim (contiguous) */
+    int32_t interleaved;        /* 0 or 1: how columns pair up */
+    int32_t dtype;              /* an ssm_dtype: q, k, their outputs and gradients */
+} ssm_rotary_shape;
+
+#define SSM_ROTARY_MAX_DIM 256
+
+/*
+ *   q, k       [tokens, *_heads, dim]   dtype   required where there are such heads
+ *   positions  [period or tokens]       int32   required when rot > 0; any values
+ *   freqs      [rot / 2]                fp64    required when rot > 0: radians a position
+ *   q_out, k_out as q, k, contiguous    dtype   outputs; must not overlap an input or each other
+ * back: 1 turns by the opposite angles: with the outputs' gradients as q and k, their inputs'
+ * gradients.  Tensors need no more alignment than their elements'; rows, columns and addresses that
+ * are multiples of 16 bytes are the fast ones.  tokens == 0 or no heads is a no-op.  Deterministic.
+ * SSM_EUNSUPPORTED: dim over SSM_ROTARY_MAX_DIM, more than 4096 heads, more than 2^31 tokens.
+ */
+int ssm_rotary_fwd(const ssm_rotary_shape *shape, const void *q, const void *k, const int32_t *positions,
+                   const double *freqs, float magnitude, int back, void *q_out, void *k_out, void *stream);
+
+/* With the norm: wq, wk [dim] fp32 (NULL: ones), eps >= 0; sums and statistics in fp32.  rot 0: the norm
+ * alone.  Otherwise as ssm_rotary_fwd. */
+int ssm_qknorm_fwd(const ssm_rotary_shape *shape, const void *q, const void *k, const float *wq, const float *wk,
+                   const int32_t *positions, const double *freqs, float eps, float magnitude, void *q_out,
+                   void *k_out, void *stream);
+
+/* Host-only: bytes of device workspace of ssm_qknorm_bwd given dwq or dwk. */
+size_t ssm_qknorm_bwd_workspace_bytes(const ssm_rotary_shape *shape);
+
+/*
+ * Backward pass of ssm_qknorm_fwd, from its inputs and dq_out = dLoss/dq_out, dk_out (contiguous): with
+ * g the gradient turned back, xh = x / sqrt(mean(x^2) + eps) and e = g w,
+ *     dx = (e - xh mean(e xh)) / sqrt(mean(x^2) + eps),   dw = sum over tokens and heads of g xh
+ *   dq, dk     as q, k, contiguous   dtype   required where there are such heads, fully overwritten
+ *   dwq, dwk   [dim]                 fp32    NULL = not computed
+ *   workspace  device memory of ssm_qknorm_bwd_workspace_bytes() bytes (unused when dwq and dwk are NULL)
+ * tokens == 0 or no heads sets dwq and dwk to zero.  Deterministic: the sums have a fixed order.
+ */
+int ssm_qknorm_bwd(const ssm_rotary_shape *shape, const void *q, const void *k, const float *wq, const float *wk,
+                   const int32_t *positions, const double *freqs, float eps, float magnitude, const void *dq_out,
+                   const void *dk_out, void *dq, void *dk, float *dwq, float *dwk, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

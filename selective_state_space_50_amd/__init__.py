@@ -17,7 +17,8 @@ import re
 __all__ = ["scan_fwd", "scan_fwd_save", "scan_save_sizes", "scan_bwd", "state_update", "scan_plan", "scan_workspace_bytes",
            "scan_bwd_workspace_bytes", "selective_scan", "conv1d_fwd", "conv1d_update", "linattn_fwd", "linattn_bwd",
            "linattn_update", "linattn_workspace_bytes", "linattn_bwd_workspace_bytes", "linear_attention",
-           "groupnorm_fwd", "groupnorm_bwd", "groupnorm_workspace_bytes", "group_norm", "lib",
+           "groupnorm_fwd", "groupnorm_bwd", "groupnorm_workspace_bytes", "group_norm", "rotary_freqs", "rotary_fwd",
+           "rotary_bwd", "rotary", "qknorm_fwd", "qknorm_bwd", "qknorm_bwd_workspace_bytes", "qk_norm", "lib",
            "SSMError", "LIB_PATH",
            "HEADER_PATH", "exported_api"]
 
@@ -62,6 +63,11 @@ class LinAttnShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("batch", "seqlen", "nheads", "q_heads", "k_heads", "v_heads", "dk", "dv",
                                               "q_row", "k_row", "v_row")] + \
                [("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class RotaryShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("tokens", "period", "q_heads", "k_heads", "dim", "rot", "q_row", "k_row")] + \
+               [("interleaved", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
 _lib = None
@@ -146,6 +152,15 @@ def lib():
     L.ssm_groupnorm_fwd.argtypes = [I64, I64, I64, I64, I32, P, P, P, P, ctypes.c_float, I32, P, P, P, P, SZ, P]
     L.ssm_groupnorm_bwd.restype = I32
     L.ssm_groupnorm_bwd.argtypes = [I64, I64, I64, I64, I32, P, P, P, P, I32] + [P] * 8 + [SZ, P]
+    R, F = ctypes.POINTER(RotaryShape), ctypes.c_float
+    L.ssm_rotary_fwd.restype = I32
+    L.ssm_rotary_fwd.argtypes = [R, P, P, P, P, F, I32, P, P, P]
+    L.ssm_qknorm_fwd.restype = I32
+    L.ssm_qknorm_fwd.argtypes = [R] + [P] * 6 + [F, F, P, P, P]
+    L.ssm_qknorm_bwd_workspace_bytes.restype = SZ
+    L.ssm_qknorm_bwd_workspace_bytes.argtypes = [R]
+    L.ssm_qknorm_bwd.restype = I32
+    L.ssm_qknorm_bwd.argtypes = [R] + [P] * 6 + [F, F] + [P] * 7 + [SZ, P]
     if L.ssm_abi_version() != ABI_VERSION:
         raise ImportError(f"libssm ABI version {L.ssm_abi_version()} != {ABI_VERSION}")
     _lib = L
@@ -1153,3 +1168,242 @@ def group_norm(x, groups, w=None, bias=None, z=None, *, span="token", activation
     through groupnorm_bwd (gradients for x, w, bias and z).  Arguments as groupnorm_fwd; captured
     graphs as linear_attention."""
     return _groupnorm_function().apply(x, groups, w, bias, z, span, activation, eps)
+
+
+def rotary_freqs(rot, base=10000.0, *, scaling="none", factor=1.0, context=4096, fast=32.0, slow=1.0, device="cuda"):
+    """(freqs, magnitude) of rotary_fwd and qknorm_fwd for ``rot`` turning columns: freqs[j] = base ** (-2 j / rot) radians
+    a position, [rot / 2] fp64 on ``device``; to reach contexts ``factor`` times as long as the ``context`` positions of training,
+    scaled: "linear" (every frequency divided by the factor), "base" (a larger base, so that the slowest pair is
+    divided by the factor and the fastest stays), or "bands" (pairs that turn ``fast`` times or more over the context stay,
+    those that turn ``slow`` times or less are divided, in between a linear mix of both; the magnitude is then
+    0.1 log(factor) + 1, else 1)."""
+    import math
+    import torch
+    if rot < 2 or rot % 2:
+        raise ValueError(f"rot={rot} must be even and >= 2")
+    if not (base > 0 and factor >= 1 and context > 0 and fast > slow > 0):
+        raise ValueError("base and context must be positive, factor >= 1 and fast > slow > 0")
+    if scaling not in ("none", "linear", "base", "bands"):
+        raise ValueError(f"scaling {scaling!r} is not one of 'none', 'linear', 'base', 'bands'")
+    j = torch.arange(rot // 2, dtype=torch.float64) / (rot // 2)
+    if scaling == "base" and rot > 2:
+        base *= factor ** (rot / (rot - 2))
+    f, magnitude = torch.pow(torch.tensor(float(base), dtype=torch.float64), -j), 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "bands":
+        stay = ((context * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0.0, 1.0)
+        f, magnitude = f * stay + f / factor * (1.0 - stay), 0.1 * math.log(factor) + 1.0
+    return f.to(device), magnitude
+
+
+class _RotarySizes:
+    """The ssm_rotary_shape of a call, its reference, and the shapes of its outputs and workspace."""
+
+    def __init__(self, shape, q, k):
+        self.c = shape
+        self.ref = ctypes.byref(shape)
+        self.q, self.k = q, k
+        self.w = (shape.dim,)
+
+    @functools.cached_property
+    def bwd_bytes(self):
+        return int(lib().ssm_qknorm_bwd_workspace_bytes(self.ref))
+
+
+@functools.lru_cache(maxsize=1024)
+def _rotary_sizes(q, k, positions, pairs, layout, code):
+    """From (shape, strides) of q and k ([B, L, heads, dim] or [B, heads, dim]; k may be None) and the shape of positions."""
+    if layout not in ("half", "interleaved"):
+        raise ValueError(f"layout {layout!r} is neither 'half' nor 'interleaved'")
+    n = len(q[0])
+    if n not in (3, 4) or (k is not None and len(k[0]) != n):
+        raise ValueError("q and k must be [batch, seqlen, heads, dim] or [batch, heads, dim]")
+    head, d = tuple(q[0][:-2]), q[0][-1]
+    qr = _rows(q, "q", head, q[0][-2], d)
+    kr = _rows(k, "k", head, k[0][-2], d) if k is not None else 0
+    if pairs and positions not in (head, head[-1:]):
+        raise ValueError(f"positions has shape {positions}, expected {head}" + (f" or {head[-1:]}" if n == 4 else ""))
+    if 2 * pairs > d:
+        raise ValueError(f"{pairs} frequencies turn {2 * pairs} columns, but heads have {d}")
+    tokens = head[0] * (head[1] if n == 4 else 1)
+    period = positions[0] if pairs and positions != head else 0
+    return _RotarySizes(RotaryShape(tokens, period, q[0][-2], k[0][-2] if k is not None else 0, d, 2 * pairs, qr, kr,
+                                    int(layout == "interleaved"), code), tuple(q[0]), tuple(k[0]) if k is not None else None)
+
+
+def _rotary_call(q, k, positions, freqs, layout, what):
+    import torch
+    dev, dt = q.device, q.dtype
+    if dev.type != "cuda":
+        raise ValueError(f"{what} runs on the GPU only; tensors must be on a cuda device")
+    code = _dtype_code(q)
+    if k is not None and (k.dtype != dt or k.device != dev):
+        raise (TypeError if k.dtype != dt else ValueError)(f"k is {k.dtype} on {k.device}, q {dt} on {dev}")
+    if (positions is None) != (freqs is None):
+        raise ValueError("positions and freqs go together")
+    shape, pairs = (), 0
+    if freqs is not None:
+        _need(freqs, "freqs", freqs.shape[:1] if freqs.dim() else (1,), torch.float64, dev)
+        shape, pairs = tuple(positions.shape), freqs.shape[0]
+        _need(positions, "positions", shape, torch.int32, dev)
+    return dev, dt, _rotary_sizes((q.shape, q.stride()), None if k is None else (k.shape, k.stride()), shape, pairs, layout, code)
+
+
+def _rotary_outs(out, q, k, s, dt, dev):
+    if out is None:
+        return q.new_empty(s.q), None if k is None else k.new_empty(s.k)
+    if not isinstance(out, (tuple, list)) or len(out) != 2 or out[0] is None or (out[1] is None) != (k is None):
+        raise ValueError("out must be a pair, of q's output and of k's (None without k)")
+    _need(out[0], "out[0]", s.q, dt, dev)
+    _need(out[1], "out[1]", s.k, dt, dev)
+    _written(*out)
+    return tuple(out)
+
+
+def rotary_fwd(q, k=None, positions=None, freqs=None, *, layout="half", magnitude=1.0, out=None, stream=None, _back=0):
+    """Rotary positions: pair j of each head's first 2 len(freqs) columns turned by positions * freqs[j], times
+    magnitude; the columns behind them as they are.
+
+    q, k: [B, L, heads, dim], or [B, heads, dim] for single tokens (bf16, or fp32; dim <= 256; k may
+    be None), which may be slices of a joint projection's output (heads side by side, tokens evenly
+    spaced; rows and addresses in multiples of 16 bytes are the fast ones).  positions: int32, one for
+    every token, or [L] for all rows alike; freqs: [pairs] fp64 (rotary_freqs).  layout: pairs are columns
+    (j, j + len(freqs)) ("half") or (2 j, 2 j + 1) ("interleaved").  Returns (q, k) turned, contiguous, or
+    q alone where k is None.
+    """
+    if freqs is None:
+        raise ValueError("positions and freqs are required")
+    dev, dt, s = _rotary_call(q, k, positions, freqs, layout, "rotary_fwd")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return rotary_fwd(q, k, positions, freqs, layout=layout, magnitude=magnitude, out=out, _back=_back)
+    qo, ko = _rotary_outs(out, q, k, s, dt, dev)
+    _check(lib().ssm_rotary_fwd(s.ref, q.data_ptr(), _addr(k), positions.data_ptr(), freqs.data_ptr(), magnitude, _back,
+                                qo.data_ptr(), _addr(ko), _stream(dev)), "ssm_rotary_fwd")
+    return qo if k is None else (qo, ko)
+
+
+def rotary_bwd(dq, dk=None, positions=None, freqs=None, *, layout="half", magnitude=1.0, out=None, stream=None):
+    """Gradients for rotary_fwd's q and k from those of its outputs: the same turn by the opposite angles."""
+    return rotary_fwd(dq, dk, positions, freqs, layout=layout, magnitude=magnitude, out=out, stream=stream, _back=1)
+
+
+def qknorm_fwd(q, k=None, wq=None, wk=None, positions=None, freqs=None, *, eps=1e-6, layout="half", magnitude=1.0, out=None,
+               stream=None):
+    """An RMS norm of every head, u = x / sqrt(mean(x^2) + eps) * w, and rotary_fwd of the normed rows in
+    the same pass.  wq, wk: [dim] fp32, for the heads of q and of k (None: ones); positions and freqs None: the
+    norm alone.  Other arguments, and what is returned, as rotary_fwd."""
+    import torch
+    dev, dt, s = _rotary_call(q, k, positions, freqs, layout, "qknorm_fwd")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return qknorm_fwd(q, k, wq, wk, positions, freqs, eps=eps, layout=layout, magnitude=magnitude, out=out)
+    _need(wq, "wq", s.w, torch.float32, dev)
+    _need(wk, "wk", s.w, torch.float32, dev)
+    qo, ko = _rotary_outs(out, q, k, s, dt, dev)
+    _check(lib().ssm_qknorm_fwd(s.ref, q.data_ptr(), _addr(k), _addr(wq), _addr(wk), _addr(positions), _addr(freqs), eps,
+                                magnitude, qo.data_ptr(), _addr(ko), _stream(dev)), "ssm_qknorm_fwd")
+    return qo if k is None else (qo, ko)
+
+
+def qknorm_bwd_workspace_bytes(tokens, dim) -> int:
+    """Device workspace bytes of qknorm_bwd (with gradients of weights) for this many tokens of heads of dim columns."""
+    s = RotaryShape(tokens, 0, 1, 0, dim, 0, 0, 0, 0, 0)
+    return int(lib().ssm_qknorm_bwd_workspace_bytes(ctypes.byref(s)))
+
+
+def qknorm_bwd(q, k=None, wq=None, wk=None, positions=None, freqs=None, dq_out=None, dk_out=None, *, eps=1e-6, layout="half",
+               magnitude=1.0, need_dw=True, workspace=None, stream=None):
+    """Gradients of a loss through qknorm_fwd, given its inputs and dq_out, dk_out = the gradients of its outputs
+    (contiguous, their shapes and dtype).
+
+    Returns a dict: dq, dk (None without k) as q and k, contiguous; dwq, dwk [dim] fp32 (None without that weight, or when
+    need_dw is false).
+    """
+    import torch
+    dev, dt, s = _rotary_call(q, k, positions, freqs, layout, "qknorm_bwd")
+    if dq_out is None or (dk_out is None) != (k is None):
+        raise ValueError("dq_out is required, and dk_out where there is a k")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return qknorm_bwd(q, k, wq, wk, positions, freqs, dq_out, dk_out, eps=eps, layout=layout, magnitude=magnitude,
+                              need_dw=need_dw, workspace=workspace)
+    _need(wq, "wq", s.w, torch.float32, dev)
+    _need(wk, "wk", s.w, torch.float32, dev)
+    _need(dq_out, "dq_out", s.q, dt, dev)
+    _need(dk_out, "dk_out", s.k, dt, dev)
+    out = {"dq": q.new_empty(s.q), "dk": None if k is None else k.new_empty(s.k),
+           "dwq": None if wq is None or not need_dw else wq.new_empty(s.w),
+           "dwk": None if wk is None or not need_dw else wk.new_empty(s.w)}
+    need = 0 if out["dwq"] is None and out["dwk"] is None else s.bwd_bytes
+    workspace = _workspace(workspace, need, dev)
+    _check(lib().ssm_qknorm_bwd(s.ref, q.data_ptr(), _addr(k), _addr(wq), _addr(wk), _addr(positions), _addr(freqs), eps,
+                                magnitude, dq_out.data_ptr(), _addr(dk_out), out["dq"].data_ptr(), _addr(out["dk"]),
+                                _addr(out["dwq"]), _addr(out["dwk"]), _addr(workspace) if need else None, need, _stream(dev)),
+           "ssm_qknorm_bwd")
+    return out
+
+
+@functools.lru_cache(maxsize=None)
+def _rotary_functions():
+    import torch
+
+    def whole(g, shape, like):
+        """The gradient of an output that nothing was made of is zero."""
+        return _gradient(g) if g is not None else like.new_zeros(shape)
+
+    class _Rotary(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, positions, freqs, layout, magnitude):
+            ctx.save_for_backward(positions, freqs)
+            ctx.set_materialize_grads(False)
+            ctx.how = {"layout": layout, "magnitude": magnitude}
+            return rotary_fwd(q, k, positions, freqs, **ctx.how)
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, gq, gk=None):
+            positions, freqs = ctx.saved_tensors
+            turned = [None, None]
+            if gq is not None and gk is not None and ctx.needs_input_grad[0] and ctx.needs_input_grad[1]:
+                turned = rotary_bwd(_gradient(gq), _gradient(gk), positions, freqs, **ctx.how)
+            else:
+                for i, g in enumerate((gq, gk)):
+                    if g is not None and ctx.needs_input_grad[i]:
+                        turned[i] = rotary_bwd(_gradient(g), None, positions, freqs, **ctx.how)
+            return turned[0], turned[1], None, None, None, None
+
+    class _QKNorm(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, wq, wk, positions, freqs, eps, layout, magnitude):
+            ctx.save_for_backward(q, k, wq, wk, positions, freqs)
+            ctx.set_materialize_grads(False)
+            ctx.how = {"eps": eps, "layout": layout, "magnitude": magnitude}
+            return qknorm_fwd(q, k, wq, wk, positions, freqs, **ctx.how)
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, gq, gk=None):
+            q, k, wq, wk, positions, freqs = ctx.saved_tensors
+            g = qknorm_bwd(q, k, wq, wk, positions, freqs, whole(gq, q.shape, q), None if k is None else whole(gk, k.shape, k),
+                           need_dw=ctx.needs_input_grad[2] or ctx.needs_input_grad[3], **ctx.how)
+            return g["dq"], g["dk"], g["dwq"], g["dwk"], None, None, None, None, None
+
+    return _Rotary, _QKNorm
+
+
+def rotary(q, k, positions, freqs, *, layout="half", magnitude=1.0):
+    """Differentiable rotary positions: rotary_fwd with a torch autograd backward through rotary_bwd (gradients for q
+    and k).  Arguments as rotary_fwd; captured graphs as linear_attention."""
+    return _rotary_functions()[0].apply(q, k, positions, freqs, layout, magnitude)
+
+
+def qk_norm(q, k, wq=None, wk=None, positions=None, freqs=None, *, eps=1e-6, layout="half", magnitude=1.0):
+    """Differentiable norms of every head of q and k with their rotary positions: qknorm_fwd with a torch autograd
+    backward through qknorm_bwd (gradients for q, k, wq and wk).  Arguments as qknorm_fwd; captured graphs as
+    linear_attention."""
+    return _rotary_functions()[1].apply(q, k, wq, wk, positions, freqs, eps, layout, magnitude)

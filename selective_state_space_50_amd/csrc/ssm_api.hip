@@ -1375,3 +1375,81 @@ extern "C" int ssm_groupnorm_bwd(int64_t batch, int64_t seqlen, int64_t dim, int
     const hipError_t e = launch_groupnorm_bwd(a, dtype == SSM_DTYPE_BF16, p.vec, s);
     return e == hipSuccess ? SSM_OK : hip_fail("groupnorm backward launch", e);
 }
+
+namespace {
+using namespace ssm;
+RotaryArgs rotary_args(const ssm_rotary_shape &s, const RotaryPlan &p, const void *q, const void *k, const int32_t *positions,
+                       const double *freqs, float magnitude) {
+    RotaryArgs a{};
+    a.tokens = s.tokens; a.period = s.period < s.tokens ? s.period : 0;
+    a.q = q; a.k = k; a.q_row = p.q_row; a.k_row = p.k_row;
+    a.positions = positions; a.freqs = freqs; a.magnitude = magnitude;
+    a.inv_dim = 1.0f / static_cast<float>(s.dim);
+    a.dim = static_cast<int>(s.dim); a.dim_even = (a.dim + 3) / 4 * 4; a.pairs = static_cast<int>(s.rot / 2);
+    a.q_heads = static_cast<int>(s.q_heads); a.heads = static_cast<int>(s.q_heads + s.k_heads);
+    a.team = p.team; a.units = p.units; a.tokens_per = p.tokens_per; a.groups = p.groups; a.blocks = p.blocks;
+    const uint64_t one = uint64_t(1) << 32;
+    a.by_pairs = a.pairs ? (one + a.pairs - 1) / a.pairs : 0;
+    a.by_heads = (one + a.heads - 1) / a.heads;
+    return a;
+}
+
+int rotary_forward(const char *what, const ssm_rotary_shape *shape, const void *q, const void *k, bool norm, const float *wq,
+                   const float *wk, const int32_t *positions, const double *freqs, float eps, float magnitude, int back,
+                   void *q_out, void *k_out, void *stream) {
+    clear_error();
+    if (back != 0 && back != 1) {
+        set_error("back=%d is neither 0 nor 1", back);
+        return SSM_EINVAL;
+    }
+    RotaryPlan p;
+    const int st = check_rotary(shape, q, k, wq, wk, positions, freqs, eps, q_out, k_out, nullptr, nullptr, nullptr, nullptr,
+                                false, nullptr, 0, &p);
+    if (st != SSM_OK) return st;
+    if (p.blocks == 0) return SSM_OK;
+    RotaryArgs a = rotary_args(*shape, p, q, k, positions, freqs, magnitude);
+    a.wq = wq; a.wk = wk; a.eps = eps; a.back = back; a.q_out = q_out; a.k_out = k_out;
+    log_call("%s tokens=%lld heads=%d+%d dim=%d rot=%d dtype=%d: %d elements a load, teams of %d, %d tokens a workgroup",
+             what, (long long)a.tokens, a.q_heads, a.heads - a.q_heads, a.dim, 2 * a.pairs, shape->dtype, p.vec, p.team, p.tokens_per);
+    const hipError_t e = launch_rotary(a, shape->dtype == SSM_DTYPE_BF16, p.vec, shape->interleaved != 0, norm, false,
+                                       static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? SSM_OK : hip_fail("rotary launch", e);
+}
+}  // namespace
+
+extern "C" int ssm_rotary_fwd(const ssm_rotary_shape *shape, const void *q, const void *k, const int32_t *positions,
+                              const double *freqs, float magnitude, int back, void *q_out, void *k_out, void *stream) {
+    return rotary_forward("rotary", shape, q, k, false, nullptr, nullptr, positions, freqs, 0.0f, magnitude, back, q_out, k_out,
+                          stream);
+}
+
+extern "C" int ssm_qknorm_fwd(const ssm_rotary_shape *shape, const void *q, const void *k, const float *wq, const float *wk,
+                              const int32_t *positions, const double *freqs, float eps, float magnitude, void *q_out,
+                              void *k_out, void *stream) {
+    return rotary_forward("qknorm", shape, q, k, true, wq, wk, positions, freqs, eps, magnitude, 0, q_out, k_out, stream);
+}
+
+extern "C" int ssm_qknorm_bwd(const ssm_rotary_shape *shape, const void *q, const void *k, const float *wq, const float *wk,
+                              const int32_t *positions, const double *freqs, float eps, float magnitude, const void *dq_out,
+                              const void *dk_out, void *dq, void *dk, float *dwq, float *dwk, void *workspace,
+                              size_t workspace_bytes, void *stream) {
+    using namespace ssm;
+    clear_error();
+    RotaryPlan p;
+    const int st = check_rotary(shape, q, k, wq, wk, positions, freqs, eps, dq, dk, dq_out, dk_out, dwq, dwk, true, workspace,
+                                workspace_bytes, &p);
+    if (st != SSM_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (p.blocks == 0) {
+        const int r = fill_floats(dwq, nullptr, shape->dim, s);
+        return r == SSM_OK ? fill_floats(dwk, nullptr, shape->dim, s) : r;
+    }
+    RotaryArgs a = rotary_args(*shape, p, q, k, positions, freqs, magnitude);
+    a.wq = wq; a.wk = wk; a.eps = eps; a.q_out = dq; a.k_out = dk; a.dq_out = dq_out; a.dk_out = dk_out;
+    a.dwq = dwq; a.dwk = dwk;
+    a.part = dwq || dwk ? static_cast<float *>(workspace) : nullptr;
+    log_call("qknorm backward tokens=%lld heads=%d+%d dim=%d rot=%d dtype=%d: %d elements a load, teams of %d, %lld workgroups",
+             (long long)a.tokens, a.q_heads, a.heads - a.q_heads, a.dim, 2 * a.pairs, shape->dtype, p.vec, p.team, (long long)p.blocks);
+    const hipError_t e = launch_rotary(a, shape->dtype == SSM_DTYPE_BF16, p.vec, shape->interleaved != 0, true, true, s);
+    return e == hipSuccess ? SSM_OK : hip_fail("qknorm backward launch", e);
+}

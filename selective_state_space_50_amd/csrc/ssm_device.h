@@ -152,6 +152,26 @@ struct GroupNormArgs {
     float *gsum = nullptr;           // and the two sums of dx [N, G, 2]
 };
 
+struct RotaryArgs {
+    int64_t tokens, period;          // positions: token t reads t % period (0: t)
+    const void *q, *k;               // tokens q_row, k_row elements apart, heads side by side
+    int64_t q_row, k_row;
+    const float *wq, *wk;            // normed: [dim] each, or null (ones)
+    const int32_t *positions;
+    const double *freqs;             // [pairs] radians a position
+    float eps, inv_dim, magnitude;
+    int back;                        // turn by the opposite angles
+    void *q_out, *k_out;             // contiguous (backward: dq, dk)
+    const void *dq_out, *dk_out;     // backward: incoming gradients, contiguous
+    float *dwq, *dwk;                // [dim] or null
+    float *part;                     // backward: [blocks][2][dim], null: no dw wanted
+    int dim, dim_even, pairs, q_heads, heads;   // columns, rounded up to 4, turning pairs, heads of q, of q and k
+    // set by the plan
+    int team, units, tokens_per;     // lanes of a row, their units of it, tokens of a workgroup's turn
+    int64_t groups, blocks;          // such turns, workgroups
+    uint64_t by_pairs, by_heads;     // ceil(2^32 / .): i / n = i by_n >> 32 for the small i of a turn
+};
+
 struct ConvArgs {
     int64_t B, L, D;
     int W;                   // filter width (1..4)
@@ -358,6 +378,8 @@ hipError_t launch_linattn_update(const LinAttnArgs &a, bool bf16, hipStream_t s)
 // Group norm; vec: 16-byte loads (the groups' channels a multiple of 16 bytes).
 hipError_t launch_groupnorm_fwd(const GroupNormArgs &a, bool bf16, bool vec, hipStream_t s);
 hipError_t launch_groupnorm_bwd(const GroupNormArgs &a, bool bf16, bool vec, hipStream_t s);
+// Rotary positions, and the norm of every head in front of them; vec: elements a load.
+hipError_t launch_rotary(const RotaryArgs &a, bool bf16, int vec, bool inter, bool norm, bool bwd, hipStream_t s);
 // Backward pass (dstate == 16, dim % 64 == 0).
 hipError_t launch_scan_bwd(const BwdArgs &a, int disc, bool bf16, bool has_z, hipStream_t s);
 

@@ -1172,9 +1172,153 @@ int check_groupnorm_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t grou
     return check_ranges(all + 7, 5, all, 12, workspace, workspace_bytes, plan->ws_bytes);
 }
 
+// ---------------------------------------------------------------- rotary positions, head norms
+
+namespace {
+constexpr int64_t kRotBlocks = 1024;   // workgroups of the backward: their sums of dw are 8 dim bytes each
+
+int check_rotary_shape(const ssm_rotary_shape *s, RotaryPlan *plan) {
+    if (!s) {
+        set_error("required pointer shape is NULL");
+        return SSM_EINVAL;
+    }
+    if (s->dtype != SSM_DTYPE_F32 && s->dtype != SSM_DTYPE_BF16) {
+        set_error("dtype=%d is neither SSM_DTYPE_F32 nor SSM_DTYPE_BF16", s->dtype);
+        return SSM_EINVAL;
+    }
+    if (s->interleaved != 0 && s->interleaved != 1) {
+        set_error("interleaved=%d is neither 0 nor 1", s->interleaved);
+        return SSM_EINVAL;
+    }
+    if (s->tokens < 0 || s->q_heads < 0 || s->k_heads < 0 || s->period < 0) {
+        set_error("negative size (tokens=%lld, q_heads=%lld, k_heads=%lld, period=%lld)", (long long)s->tokens,
+                  (long long)s->q_heads, (long long)s->k_heads, (long long)s->period);
+        return SSM_EINVAL;
+    }
+    if (s->dim < 1 || s->rot < 0 || s->rot % 2 != 0 || s->rot > s->dim) {
+        set_error("dim=%lld must be >= 1, and rot=%lld even and between 0 and dim", (long long)s->dim, (long long)s->rot);
+        return SSM_EINVAL;
+    }
+    if (s->dim > SSM_ROTARY_MAX_DIM || s->q_heads > 4096 || s->k_heads > 4096 || s->q_heads + s->k_heads > 4096 ||
+        s->tokens > (int64_t(1) << 31)) {
+        set_error("dim=%lld over %d, more than 4096 heads (%lld and %lld) or more than 2^31 tokens (%lld)", (long long)s->dim,
+                  SSM_ROTARY_MAX_DIM, (long long)s->q_heads, (long long)s->k_heads, (long long)s->tokens);
+        return SSM_EUNSUPPORTED;
+    }
+    plan->q_row = s->q_row ? s->q_row : s->q_heads * s->dim;
+    plan->k_row = s->k_row ? s->k_row : s->k_heads * s->dim;
+    if (plan->q_row < s->q_heads * s->dim || plan->k_row < s->k_heads * s->dim) {
+        set_error("q_row=%lld or k_row=%lld is shorter than a token's heads", (long long)s->q_row, (long long)s->k_row);
+        return SSM_EINVAL;
+    }
+    const int64_t most = plan->q_row > plan->k_row ? plan->q_row : plan->k_row;
+    if (s->tokens > 0 && most > kMaxElems / s->tokens) {
+        set_error("%lld tokens %lld elements apart are too large", (long long)s->tokens, (long long)most);
+        return SSM_EUNSUPPORTED;
+    }
+    return SSM_OK;
+}
+
+int64_t token_bytes(int64_t tokens, int64_t row, int64_t wide, int64_t es) {
+    return tokens > 0 && wide > 0 ? ((tokens - 1) * row + wide) * es : 0;
+}
+
+int check_element(const Range *all, int n, uintptr_t size) {
+    for (int i = 0; i < n; ++i)
+        if (all[i].lo % size != 0) {
+            set_error("pointer %s is not aligned to its elements of %d bytes", all[i].name, static_cast<int>(size));
+            return SSM_EINVAL;
+        }
+    return SSM_OK;
+}
+}  // namespace
+
+size_t qknorm_bwd_ws_bytes(const ssm_rotary_shape *s) {
+    RotaryPlan p;
+    if (check_rotary_shape(s, &p) != SSM_OK) return 0;
+    const int64_t blocks = s->tokens < kRotBlocks ? s->tokens : kRotBlocks;
+    return static_cast<size_t>(blocks * 2 * s->dim) * sizeof(float);
+}
+
+int check_rotary(const ssm_rotary_shape *s, const void *q, const void *k, const float *wq, const float *wk,
+                 const int32_t *positions, const double *freqs, float eps, const void *q_out, const void *k_out,
+                 const void *dq_out, const void *dk_out, const float *dwq, const float *dwk, bool backward,
+                 const void *workspace, size_t workspace_bytes, RotaryPlan *plan) {
+    int st = check_rotary_shape(s, plan);
+    if (st != SSM_OK) return st;
+    if (!(eps >= 0.0f)) {
+        set_error("eps=%g must be >= 0", static_cast<double>(eps));
+        return SSM_EINVAL;
+    }
+    const int64_t heads = s->q_heads + s->k_heads;
+    const bool any = s->tokens > 0 && heads > 0, any_q = any && s->q_heads > 0, any_k = any && s->k_heads > 0;
+    const char *missing = any_q && !q ? "q" : any_k && !k ? "k" : any && s->rot && !positions ? "positions"
+                        : any && s->rot && !freqs ? "freqs" : any_q && !q_out ? (backward ? "dq" : "q_out")
+                        : any_k && !k_out ? (backward ? "dk" : "k_out") : backward && any_q && !dq_out ? "dq_out"
+                        : backward && any_k && !dk_out ? "dk_out" : nullptr;
+    if (missing) {
+        set_error("required pointer %s is NULL", missing);
+        return SSM_EINVAL;
+    }
+    const int64_t es = static_cast<int64_t>(dtype_size(s->dtype));
+    const int64_t qb = s->tokens * s->q_heads * s->dim * es, kb = s->tokens * s->k_heads * s->dim * es;
+    const int64_t np = s->period && s->period < s->tokens ? s->period : s->tokens;
+    const bool sums = backward && (dwq || dwk);
+    plan->ws_bytes = sums ? qknorm_bwd_ws_bytes(s) : 0;
+    Range all[] = {range("q", q, token_bytes(s->tokens, plan->q_row, s->q_heads * s->dim, es)),
+                   range("k", k, token_bytes(s->tokens, plan->k_row, s->k_heads * s->dim, es)),
+                   range("dq_out", dq_out, qb), range("dk_out", dk_out, kb),
+                   range(backward ? "dq" : "q_out", q_out, qb), range(backward ? "dk" : "k_out", k_out, kb),
+                   range("wq", wq, s->dim * 4), range("wk", wk, s->dim * 4), range("positions", positions, np * 4),
+                   range("dwq", dwq, s->dim * 4), range("dwk", dwk, s->dim * 4),
+                   range("workspace", sums ? workspace : nullptr, static_cast<int64_t>(plan->ws_bytes)),
+                   range("freqs", freqs, s->rot / 2 * 8)};
+    st = check_element(all, 6, static_cast<uintptr_t>(es));
+    if (st == SSM_OK) st = check_element(all + 6, 6, 4);
+    if (st == SSM_OK) st = check_element(all + 12, 1, 8);
+    if (st != SSM_OK) return st;
+    const Range outs[] = {all[4], all[5], all[9], all[10], all[11]};
+    st = check_no_overlap(outs, 5, all, 13);
+    if (st != SSM_OK) return st;
+    if (plan->ws_bytes > 0 && (!workspace || workspace_bytes < plan->ws_bytes)) {
+        set_error("workspace of %zu bytes given, %zu needed", workspace ? workspace_bytes : (size_t)0, plan->ws_bytes);
+        return SSM_EWORKSPACE;
+    }
+    if (!any) return SSM_OK;
+    // the widest loads whose units (two of them a lane) fill rows and turning part and lie on their size
+    for (int64_t v = es == 2 ? 8 : 4; v > 1; v = v == 8 ? 4 : 1) {
+        bool ok = s->dim % (2 * v) == 0 && s->rot % (2 * v) == 0 && (!any_q || plan->q_row % v == 0) && (!any_k || plan->k_row % v == 0);
+        for (int i = 0; i < 6; ++i) ok = ok && all[i].lo % static_cast<uintptr_t>(v * es) == 0;
+        if (ok) {
+            plan->vec = static_cast<int>(v);
+            break;
+        }
+        if (es == 4) break;
+    }
+    const int64_t units = ceil_div(s->dim, 2 * plan->vec);
+    plan->units = static_cast<int>(units);
+    while (plan->team < 64 && plan->team < units) plan->team *= 2;
+    // tokens of a workgroup's turn: four rows to each team, but so that 1024 workgroups have one
+    const int64_t teams = 256 / plan->team;
+    int64_t per = 4 * teams / heads;
+    if (per > 16) per = 16;
+    if (per > s->tokens / 1024) per = s->tokens / 1024;
+    if (per < 1) per = 1;
+    plan->tokens_per = static_cast<int>(per);
+    plan->groups = ceil_div(s->tokens, per);
+    const int64_t most = backward ? kRotBlocks : int64_t(1) << 20;
+    plan->blocks = plan->groups < most ? plan->groups : most;
+    return SSM_OK;
+}
+
 }  // namespace ssm
 
 extern "C" {
+
+size_t ssm_qknorm_bwd_workspace_bytes(const ssm_rotary_shape *shape) {
+    ssm::clear_error();
+    return ssm::qknorm_bwd_ws_bytes(shape);
+}
 
 size_t ssm_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim, int64_t dstate, int dtype,
                                     int saved_checkpoints) {

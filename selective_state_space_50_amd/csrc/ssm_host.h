@@ -206,6 +206,21 @@ int check_groupnorm_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t grou
                         const float *rstd, const void *dx, const float *dw, const float *dbias, const void *dz,
                         const void *workspace, size_t workspace_bytes, GroupNormPlan *plan);
 
+// Rotary positions and head norms: how rows are held (see rotary.hip).
+struct RotaryPlan {
+    int64_t q_row = 0, k_row = 0;
+    int vec = 1;                 // elements a load
+    int team = 1, units = 1, tokens_per = 1;
+    int64_t groups = 0, blocks = 0;
+    size_t ws_bytes = 0;         // of the normed form's backward
+};
+// outs: the contiguous tensors of q and k that are written, grads: incoming gradients (backward), or null
+int check_rotary(const ssm_rotary_shape *s, const void *q, const void *k, const float *wq, const float *wk,
+                 const int32_t *positions, const double *freqs, float eps, const void *q_out, const void *k_out,
+                 const void *dq_out, const void *dk_out, const float *dwq, const float *dwk, bool backward,
+                 const void *workspace, size_t workspace_bytes, RotaryPlan *plan);
+size_t qknorm_bwd_ws_bytes(const ssm_rotary_shape *s);
+
 inline size_t dtype_size(int dtype) { return dtype == SSM_DTYPE_BF16 ? 2 : 4; }
 
 }  // namespace ssm
