@@ -665,6 +665,81 @@ int ssm_qknorm_bwd(const ssm_rotary_shape *shape, const void *q, const void *k, 
                    const void *dk_out, void *dq, void *dk, float *dwq, float *dwk, void *workspace,
                    size_t workspace_bytes, void *stream);
 
+/*
+ * A Mamba-2 layer's mixer as it is served: the short causal convolution with SiLU over the channels of x, B and
+ * C (ssm_conv1d_fwd) and the multi-head scan behind it (ssm_ssd_fwd) in one call, over packed sequences of any
+ * lengths whose states lie in a pool.  For every sequence, token by token, with xbc_t its row of channels = nheads *
+ * headdim + 2 * ngroups * dstate values (x [nheads, headdim], B [ngroups, dstate], C [ngroups, dstate]):
+ *
+ *     a_t     = bias + sum_{k < width} w[:, k] * xbc_{t - width + 1 + k}   (before the first token: conv_state)
+ *     x, B, C = silu(a_t),   dt = delta_t (+ delta_bias[h]; log(1 + exp(.)) of it when delta_softplus)
+ *     S[p,n]  = exp(dt * A[h]) * S[p,n] + dt * B[n] * x[p]                 (S from the sequence's slot of h)
+ *     y_t[p]  = sum_n C[n] * S[p,n] + Dskip[h] * x[p],  then * silu(z_t)   if gated
+ *
+ * and afterwards S and the last width - 1 rows of xbc lie in the sequence's slots.  x, B and C behind the
+ * convolution are never rounded to the input type.  Sizes and layouts of a call:
+ */
+typedef struct ssm_ssdconv_shape {
+    int64_t tokens;                     /* rows of xbc, delta, z and y */
+    int64_t sequences;                  /* (at most 65535) */
+    int64_t max_seqlen;                 /* no sequence is longer (what is known of the lengths on the host decides how
+                                           they are split, nothing else); 0: tokens */
+    int64_t nheads, headdim, dstate, ngroups;   /* dstate <= SSM_SSDCONV_MAX_DSTATE; ngroups divides nheads */
+    int64_t width;                      /* of the filter, 1 .. 4 */
+    int64_t nslots;                     /* of the pools h and conv_state */
+    int64_t x_row, z_row, delta_row;    /* elements from one token's row to the next one's (e.g. in a joint projection's
+                                           output); 0: contiguous */
+    int32_t dtype;                      /* an ssm_dtype: xbc, delta, z, conv_state, y */
+    int32_t reserved;                   /* must be 0 */
+} ssm_ssdconv_shape;
+
+#define SSM_SSDCONV_MAX_DSTATE 128
+
+/* Host-only: bytes of device workspace of the two calls (0: none, or the shape is invalid). */
+size_t ssm_ssdconv_workspace_bytes(const ssm_ssdconv_shape *shape);
+size_t ssm_ssdconv_update_workspace_bytes(const ssm_ssdconv_shape *shape);
+
+/*
+ *   xbc        [tokens, channels]                dtype   required (tokens > 0), likewise delta and y
+ *   delta      [tokens, nheads]                  dtype
+ *   z          [tokens, nheads, headdim]         dtype   NULL = no gate
+ *   A, Dskip, delta_bias  [nheads]               fp32    A required; Dskip, delta_bias may be NULL
+ *   w, bias    [channels, width], [channels]     fp32    w required; bias NULL = 0
+ *   offsets    [sequences + 1]                   int32   sequence s has the rows offsets[s] .. offsets[s + 1] - 1;
+ *              ascending from 0 or more to tokens or less (values are cut to that range; a decrease counts as no
+ *              tokens).  Rows of no sequence: y stays as it was there
+ *   slots      [sequences]                       int32   NULL = sequence s has slot s.  A slot outside 0 .. nslots - 1
+ *              (-1, say): the sequence starts from zeros and its states are not kept.  No two sequences of a
+ *              call may share a slot: what it holds afterwards, and y of those two, is then unspecified
+ *   fresh      [sequences]                       bytes   NULL, or not 0 where a sequence starts from zeros: what its slot
+ *              held (NaN, too) is not used.  A sequence without tokens keeps its states (fresh: they become zeros)
+ *   h          [nslots, nheads, headdim, dstate] fp32    read and updated in place
+ *   conv_state [nslots, channels, width - 1]     dtype   likewise, oldest input first; unused when width is 1
+ *   y          [tokens, nheads, headdim]         dtype   output, contiguous
+ *   workspace  device memory of ssm_ssdconv_workspace_bytes() bytes, on 16 bytes
+ * Outputs (y, h, conv_state, workspace) must not overlap inputs or each other.  Other tensors need no more alignment than their
+ * elements'; z, y and h on 16 bytes with rows of such are the fast ones.  sequences or nheads == 0 is a no-op.
+ * Products on the bf16 matrix cores, fp32 factors in bf16 parts: three (all 24 bits) for the state, and for y three
+ * (fp32) or two (bf16).  A NaN or infinity of x becomes NaN in its channel's outputs from its token on and in its
+ * channel's state, one of B, C, z or delta in those that it enters; no other sequence sees it.  Deterministic.
+ * SSM_EUNSUPPORTED: dstate over SSM_SSDCONV_MAX_DSTATE, sequences over 65535, tokens over 2^28, nheads * headdim over
+ * 2^24, too many workgroups.
+ */
+int ssm_ssdconv_fwd(const ssm_ssdconv_shape *shape, const void *xbc, const void *delta, const float *A, const float *w,
+                    const float *bias, const float *Dskip, const void *z, const float *delta_bias, int delta_softplus,
+                    const int32_t *offsets, const int32_t *slots, const uint8_t *fresh, float *h, void *conv_state,
+                    void *y, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One token of every sequence (generation form): shape->tokens must equal shape->sequences; row b of xbc, delta, z
+ * and y belongs to sequence b.  L calls give the same y and states as one ssm_ssdconv_fwd over those tokens, up to
+ * rounding.  workspace: ssm_ssdconv_update_workspace_bytes() bytes.  Otherwise as ssm_ssdconv_fwd.
+ */
+int ssm_ssdconv_update(const ssm_ssdconv_shape *shape, const void *xbc, const void *delta, const float *A, const float *w,
+                       const float *bias, const float *Dskip, const void *z, const float *delta_bias, int delta_softplus,
+                       const int32_t *slots, float *h, void *conv_state, void *y, void *workspace, size_t workspace_bytes,
+                       void *stream);
+
 #ifdef __cplusplus
 }
 #endif

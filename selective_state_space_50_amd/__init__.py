@@ -18,7 +18,8 @@ __all__ = ["scan_fwd", "scan_fwd_save", "scan_save_sizes", "scan_bwd", "state_up
            "scan_bwd_workspace_bytes", "selective_scan", "conv1d_fwd", "conv1d_update", "linattn_fwd", "linattn_bwd",
            "linattn_update", "linattn_workspace_bytes", "linattn_bwd_workspace_bytes", "linear_attention",
            "groupnorm_fwd", "groupnorm_bwd", "groupnorm_workspace_bytes", "group_norm", "rotary_freqs", "rotary_fwd",
-           "rotary_bwd", "rotary", "qknorm_fwd", "qknorm_bwd", "qknorm_bwd_workspace_bytes", "qk_norm", "lib",
+           "rotary_bwd", "rotary", "qknorm_fwd", "qknorm_bwd", "qknorm_bwd_workspace_bytes", "qk_norm",
+           "ssdconv_fwd", "ssdconv_update", "ssdconv_workspace_bytes", "lib",
            "SSMError", "LIB_PATH",
            "HEADER_PATH", "exported_api"]
 
@@ -68,6 +69,12 @@ class LinAttnShape(ctypes.Structure):
 class RotaryShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("tokens", "period", "q_heads", "k_heads", "dim", "rot", "q_row", "k_row")] + \
                [("interleaved", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class SsdConvShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("tokens", "sequences", "max_seqlen", "nheads", "headdim", "dstate", "ngroups",
+                                              "width", "nslots", "x_row", "z_row", "delta_row")] + \
+               [("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -161,6 +168,13 @@ def lib():
     L.ssm_qknorm_bwd_workspace_bytes.argtypes = [R]
     L.ssm_qknorm_bwd.restype = I32
     L.ssm_qknorm_bwd.argtypes = [R] + [P] * 6 + [F, F] + [P] * 7 + [SZ, P]
+    C = ctypes.POINTER(SsdConvShape)
+    for f in (L.ssm_ssdconv_workspace_bytes, L.ssm_ssdconv_update_workspace_bytes):
+        f.restype, f.argtypes = SZ, [C]
+    L.ssm_ssdconv_fwd.restype = I32
+    L.ssm_ssdconv_fwd.argtypes = [C] + [P] * 8 + [I32] + [P] * 7 + [SZ, P]
+    L.ssm_ssdconv_update.restype = I32
+    L.ssm_ssdconv_update.argtypes = [C] + [P] * 8 + [I32] + [P] * 5 + [SZ, P]
     if L.ssm_abi_version() != ABI_VERSION:
         raise ImportError(f"libssm ABI version {L.ssm_abi_version()} != {ABI_VERSION}")
     _lib = L
@@ -1407,3 +1421,159 @@ def qk_norm(q, k, wq=None, wk=None, positions=None, freqs=None, *, eps=1e-6, lay
     backward through qknorm_bwd (gradients for q, k, wq and wk).  Arguments as qknorm_fwd; captured graphs as
     linear_attention."""
     return _rotary_functions()[1].apply(q, k, wq, wk, positions, freqs, eps, layout, magnitude)
+
+
+class _SsdConvSizes:
+    """The ssm_ssdconv_shape of a call, its reference, and the shapes of its tensors and workspace."""
+
+    def __init__(self, c, token):
+        self.c = c
+        self.ref = ctypes.byref(c)
+        self.channels = c.nheads * c.headdim + 2 * c.ngroups * c.dstate
+        self.heads, self.token = (c.nheads,), token
+        self.w, self.bias = (self.channels, c.width), (self.channels,)
+        self.y = (c.tokens, c.nheads, c.headdim)
+        self.conv_state = (c.nslots, self.channels, c.width - 1)
+        self.seqs, self.offsets = (c.sequences,), (c.sequences + 1,)
+
+    @functools.cached_property
+    def bytes(self):
+        L = lib()
+        return int((L.ssm_ssdconv_update_workspace_bytes if self.token else L.ssm_ssdconv_workspace_bytes)(self.ref))
+
+
+def _row(t, name, width):
+    """Elements from one row of t [rows, width] (or [rows, heads, dim], one row of width values) to the next."""
+    shape, st = t
+    if 0 in shape:
+        return width
+    inner = [(n, s) for n, s in zip(shape[1:], st[1:]) if n > 1]
+    at = 1
+    for n, s in reversed(inner):
+        if s != at:
+            raise ValueError(f"{name} must have rows of contiguous values (strides {tuple(st)})")
+        at *= n
+    row = st[0] if shape[0] > 1 else width
+    if row < width:
+        raise ValueError(f"{name}'s rows overlap (strides {tuple(st)})")
+    return row
+
+
+@functools.lru_cache(maxsize=4096)
+def _ssdconv_sizes(xbc, delta, z, h, w, sequences, max_seqlen, token, code):
+    """From (shape, strides) of xbc, delta and z, and the shapes of h and w."""
+    if len(xbc[0]) != 2 or len(h) != 4 or len(w) != 2:
+        raise ValueError("xbc must be [tokens, channels], h [slots, nheads, headdim, dstate] and w [channels, width]")
+    T, C = xbc[0]
+    nslots, H, P, N = h
+    G, rest = divmod(C - H * P, 2 * N) if N else (0, 1)
+    if rest or G < 1:
+        raise ValueError(f"xbc has {C} channels: not nheads * headdim + 2 * ngroups * dstate = {H} * {P} + 2 * ngroups * {N}")
+    if tuple(delta[0]) != (T, H):
+        raise ValueError(f"delta has shape {tuple(delta[0])}, expected {(T, H)}")
+    if z is not None and tuple(z[0]) != (T, H, P):
+        raise ValueError(f"z has shape {tuple(z[0])}, expected {(T, H, P)}")
+    c = SsdConvShape(T, T if token else sequences, max_seqlen, H, P, N, G, w[1], nslots, _row(xbc, "xbc", C),
+                     0 if z is None else _row(z, "z", H * P), _row(delta, "delta", H), code, 0)
+    return _SsdConvSizes(c, token)
+
+
+def ssdconv_workspace_bytes(tokens, sequences, nheads, headdim, dstate, ngroups=1, width=4, dtype="bf16", max_seqlen=0,
+                            update=False) -> int:
+    """Device workspace bytes of ssdconv_fwd (or, with update, ssdconv_update) for this shape (0: none)."""
+    code = DTYPE_BF16 if dtype in ("bf16", "bfloat16") else DTYPE_F32
+    c = SsdConvShape(tokens, sequences, max_seqlen, nheads, headdim, dstate, ngroups, width, sequences, 0, 0, 0, code, 0)
+    L = lib()
+    return int((L.ssm_ssdconv_update_workspace_bytes if update else L.ssm_ssdconv_workspace_bytes)(ctypes.byref(c)))
+
+
+def _ssdconv_call(xbc, delta, A, w, h, conv_state, slots, sequences, bias, D, z, delta_bias, max_seqlen, out, what):
+    import torch
+    dev, dt = xbc.device, xbc.dtype
+    if dev.type != "cuda":
+        raise ValueError(f"{what} runs on the GPU only; tensors must be on a cuda device")
+    code = _dtype_code(xbc)
+    for t, name in ((delta, "delta"), (z, "z")):
+        if t is not None and t.dtype != dt:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected {dt}")
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    s = _ssdconv_sizes((xbc.shape, xbc.stride()), (delta.shape, delta.stride()), None if z is None else (z.shape, z.stride()),
+                       h.shape, w.shape, sequences, max_seqlen, what == "ssdconv_update", code)
+    f32 = torch.float32
+    _need(A, "A", s.heads, f32, dev)
+    _need(w, "w", s.w, f32, dev)
+    _need(bias, "bias", s.bias, f32, dev)
+    _need(D, "D", s.heads, f32, dev)
+    _need(delta_bias, "delta_bias", s.heads, f32, dev)
+    _need(h, "h", h.shape, f32, dev)
+    if conv_state is None and s.c.width > 1:
+        raise ValueError("conv_state is required for a filter of more than one column")
+    _need(conv_state, "conv_state", s.conv_state, dt, dev)
+    _need(slots, "slots", s.seqs, torch.int32, dev)
+    _need(out, "out", s.y, dt, dev)
+    return dev, s
+
+
+def ssdconv_fwd(xbc, delta, A, w, h, conv_state, offsets, slots=None, *, bias=None, D=None, z=None, delta_bias=None,
+                delta_softplus=False, fresh=None, max_seqlen=None, out=None, workspace=None, stream=None):
+    """A Mamba-2 layer's mixer over packed sequences whose states lie in a pool: the causal convolution (+ SiLU) of
+    conv1d_fwd over the channels of x, B and C, and the multi-head scan of ssd_fwd behind it.
+
+    xbc: [T, H P + 2 G N], a row (x [H, P], B [G, N], C [G, N]) for every token;  delta: [T, H];  z: [T, H, P] (all
+    bf16, or all fp32), each possibly a slice of a joint projection's output (contiguous rows, evenly spaced);
+    A, D, delta_bias: [H] fp32;  w: [channels, W] fp32 (W <= 4), bias: [channels] fp32.  h: [slots, H, P, N]
+    fp32 (N <= 128) and conv_state: [slots, channels, W - 1] (xbc's dtype) are read and updated in place.  offsets: [S + 1]
+    int32: sequence s has the rows offsets[s] .. offsets[s + 1] - 1 (other rows of y are not written).
+    slots: [S] int32, no two alike (default: sequence s has slot s); outside the pool (-1): from zeros, and not
+    kept.  fresh: [S] bool, where a sequence starts from zeros whatever its slot holds.  max_seqlen: the longest sequence's
+    tokens, as the host knows them (they decide how sequences are split); default T.  Returns y [T, H, P].
+    """
+    import torch
+    if offsets.dim() != 1 or not offsets.shape[0]:
+        raise ValueError("offsets must be [sequences + 1]")
+    S = offsets.shape[0] - 1
+    dev, s = _ssdconv_call(xbc, delta, A, w, h, conv_state, slots, S, bias, D, z, delta_bias, int(max_seqlen or 0), out, "ssdconv_fwd")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return ssdconv_fwd(xbc, delta, A, w, h, conv_state, offsets, slots, bias=bias, D=D, z=z, delta_bias=delta_bias,
+                               delta_softplus=delta_softplus, fresh=fresh, max_seqlen=max_seqlen, out=out, workspace=workspace)
+    _need(offsets, "offsets", s.offsets, torch.int32, dev)
+    _need(fresh, "fresh", s.seqs, torch.bool, dev)
+    if out is None:
+        out = xbc.new_empty(s.y)
+    else:
+        _written(out)
+    _written(h, conv_state)
+    need = s.bytes
+    workspace = _workspace(workspace, need, dev)
+    _check(lib().ssm_ssdconv_fwd(s.ref, xbc.data_ptr(), delta.data_ptr(), A.data_ptr(), w.data_ptr(), _addr(bias), _addr(D), _addr(z),
+                                 _addr(delta_bias), int(bool(delta_softplus)), offsets.data_ptr(), _addr(slots), _addr(fresh),
+                                 h.data_ptr(), _addr(conv_state), out.data_ptr(), _addr(workspace) if need else None, need,
+                                 _stream(dev)), "ssm_ssdconv_fwd")
+    return out
+
+
+def ssdconv_update(xbc, delta, A, w, h, conv_state, slots=None, *, bias=None, D=None, z=None, delta_bias=None,
+                   delta_softplus=False, out=None, workspace=None, stream=None):
+    """One token of every sequence of ssdconv_fwd: xbc [S, channels], delta [S, H], z [S, H, P]; h and conv_state are
+    updated in place.  Other arguments as there.  Returns y [S, H, P]."""
+    dev, s = _ssdconv_call(xbc, delta, A, w, h, conv_state, slots, 0, bias, D, z, delta_bias, 0, out, "ssdconv_update")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return ssdconv_update(xbc, delta, A, w, h, conv_state, slots, bias=bias, D=D, z=z, delta_bias=delta_bias,
+                                  delta_softplus=delta_softplus, out=out, workspace=workspace)
+    if out is None:
+        out = xbc.new_empty(s.y)
+    else:
+        _written(out)
+    _written(h, conv_state)
+    need = s.bytes
+    workspace = _workspace(workspace, need, dev)
+    _check(lib().ssm_ssdconv_update(s.ref, xbc.data_ptr(), delta.data_ptr(), A.data_ptr(), w.data_ptr(), _addr(bias), _addr(D),
+                                    _addr(z), _addr(delta_bias), int(bool(delta_softplus)), _addr(slots), h.data_ptr(),
+                                    _addr(conv_state), out.data_ptr(), _addr(workspace) if need else None, need, _stream(dev)),
+           "ssm_ssdconv_update")
+    return out

@@ -1,0 +1,837 @@
+// A Mamba-2 layer's mixer as it is served: the short causal convolution (+ SiLU) over the channels of x, B and C and
+// the multi-head scan behind it (the recurrence of ssd.hip), over packed sequences whose states lie in a pool, and for
+// one token of every sequence.
+//
+// Per sequence and token, xbc the row of all channels (x [H, P], B [G, N], C [G, N]):
+//     a_t = bias + sum_{k < W} w[:, k] xbc_{t-W+1+k},   (x, B, C) = silu(a_t)
+//     dt  = delta (+ bias, softplus optional),   S_t = exp(dt A_h) S_{t-1} + dt x_t B_t^T   (S [P, N] per head)
+//     y_t = (S_t C_t + D_h x_t) silu(z_t)
+// and over a chunk of 64 tokens from the state S, cum the running sum of dt A within the chunk:
+//     y_t = sum_{s<=t} (C_t . B_s) e^(cum_t - cum_s) dt_s x_s + e^(cum_t) S C_t + D x_t
+//     S'  = e^(cum_64) S + sum_s e^(cum_64 - cum_s) dt_s x_s B_s^T
+//
+// Three parts:
+//  * prep (a workgroup per chunk and B/C group, and per chunk and eight heads): what all heads of a group share. B and C
+//    behind the convolution, cut into bf16 parts and stored as the lanes' operands of the products to come, C B^T of the
+//    chunk, and per head the decays. A sequence's first chunk starts at its first token, so no chunk holds two sequences.
+//  * sweep (a workgroup per sequence, head and 64 channels): walks the chunks with the state in registers.  x is
+//    convolved on its way to LDS: neither x, B nor C behind the convolution is ever rounded to the input type, and x goes to
+//    memory once less than with a convolution of its own.
+//  * few heads over long sequences: the sequence in segments. A sweep without outputs makes each segment's own end state,
+//    join passes the states on, and the sweep starts every segment from its own.
+//
+// Numbers: a product of two 32-bit factors runs on v_mfma_f32_16x16x32_bf16 in parts: v = hi + mid + lo, bf16 each, holds
+// all 24 bits.  The state's factors are kept in three parts (six products: those whose order of magnitude is above 2^-24),
+// whatever the input type.  The factors of y are kept in three parts for fp32 and two for bf16 (three products; 2^-16
+// relative, a 128th of the half step that y's own rounding takes).  Exponents are sums over at most 32 tokens, forwards
+// for reads and backwards for writes, so that the nearest tokens' decays carry the smallest errors.
+//
+// Why this split (measured at 16384 tokens, H64 P64 N128): see the figures at the kernels.
+#include "ssm_device.h"
+
+#include <type_traits>
+
+namespace ssm {
+namespace {
+
+constexpr int kQ = 64;                 // tokens of a chunk
+constexpr int kThreads = 512;
+constexpr int kPS = 3;                 // parts of the state's factors
+enum { kE, kWr, kC32, kDt, kEin, kWb, kTabs };   // a head's tables of a chunk, 64 values each:
+// kE   e^(cum_t)                    decay of the carried state up to token t
+// kWr  e^(cum_64 - cum_s) dt_s      weight of token s in the state passed on
+// kC32 exponent of the decay from the 32-token half's start to t, to the base 2
+// kDt  dt_s
+// kEin e^(kC32)                     decay of what a later half reads from earlier ones
+// kWb  e^(to the half's end) dt_s
+
+typedef short s4 __attribute__((ext_vector_type(4)));
+typedef short s8 __attribute__((ext_vector_type(8)));
+typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ f4 mfma(s8 a, s8 b, f4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8, a), __builtin_bit_cast(b8, b), c, 0, 0, 0);
+}
+
+// the sum of the parts' products that lie above 2^-(8 N): i + j < N
+template <int N>
+__device__ __forceinline__ f4 product(const s8 (&a)[N], const s8 (&b)[N], f4 c) {
+#pragma unroll
+    for (int i = N - 1; i >= 0; --i)
+#pragma unroll
+        for (int j = N - 1 - i; j >= 0; --j) c = mfma(a[i], b[j], c);
+    return c;
+}
+
+// v[0 .. K - 1] in N bf16 parts, two to a word: part n's words at w[n]
+template <int N, int K>
+__device__ __forceinline__ void split(const float *v, uint32_t (&w)[N][K / 2]) {
+#pragma unroll
+    for (int i = 0; i < K / 2; ++i) {
+        float a = v[2 * i], b = v[2 * i + 1];
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            w[n][i] = pack_bf16(a, b);
+            if (n + 1 < N) {
+                a -= bf_lo(w[n][i]);
+                b -= bf_hi(w[n][i]);
+            }
+        }
+    }
+}
+template <int N>
+__device__ __forceinline__ void split8(const float *v, s8 (&out)[N]) {
+    uint32_t w[N][4];
+    split<N, 8>(v, w);
+#pragma unroll
+    for (int n = 0; n < N; ++n) out[n] = __builtin_bit_cast(s8, u4{w[n][0], w[n][1], w[n][2], w[n][3]});
+}
+
+// which sequence chunk (or segment) v belongs to, sequence s owning the numbers from offset_s / len + s on (as many as
+// its tokens can need: no sums over the sequences before it); -1: none.  Wave-uniform.
+__device__ __forceinline__ int clamped(const SsdConvArgs &a, int s) {
+    const int o = a.offsets[s];
+    return o < 0 ? 0 : o > a.T ? static_cast<int>(a.T) : o;
+}
+__device__ __forceinline__ int find_sequence(const SsdConvArgs &a, int len, int64_t v) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0, n = a.S;
+    while (true) {
+        const int step = (n + 63) >> 6, s = lo + lane * step;
+        const bool in = lane * step < n && static_cast<int64_t>(clamped(a, s) / len + s) <= v;
+        const int c = __popcll(__ballot(in));
+        if (c == 0) return -1;
+        lo += (c - 1) * step;
+        n -= (c - 1) * step;
+        if (step == 1) return __builtin_amdgcn_readfirstlane(lo);
+        if (n > step) n = step;
+    }
+}
+
+struct Sequence {
+    int s, first, len, slot;      // first row, tokens, slot of the states (-1: none)
+    bool old;                     // goes on from the slot's states
+    __device__ Sequence(const SsdConvArgs &a, int s_) : s(s_) {
+        first = clamped(a, s);
+        const int end = clamped(a, s + 1);
+        len = end > first ? end - first : 0;
+        slot = a.slots ? a.slots[s] : s;
+        if (slot < 0 || slot >= a.nslots) slot = -1;
+        old = slot >= 0 && !(a.fresh && a.fresh[s]);
+        first = __builtin_amdgcn_readfirstlane(first);
+        len = __builtin_amdgcn_readfirstlane(len);
+        slot = __builtin_amdgcn_readfirstlane(slot);
+    }
+};
+
+// Rows t0 - 3 .. t0 + K - 1 of one channel of a sequence (t0 counted from its start; what lies before the start comes
+// from the convolution's state, zeros without one; what lies behind the end is not used).
+template <class T, int K>
+struct Window {
+    T x[K + 3];
+    __device__ void load(const SsdConvArgs &a, const Sequence &q, int channel, int t0) {
+        const T *X = static_cast<const T *>(a.xbc) + channel;
+#pragma unroll
+        for (int i = 0; i < K + 3; ++i) {
+            int t = t0 + i - 3;
+            t = t < 0 ? 0 : t >= q.len ? q.len - 1 : t;      // a row that is there
+            x[i] = X[(q.first + static_cast<int64_t>(t)) * a.x_row];
+        }
+        if (t0 < 3) before(a, q, channel, t0);
+    }
+    __device__ void before(const SsdConvArgs &a, const Sequence &q, int channel, int t0) {
+        const int W1 = a.W - 1;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const int t = t0 + i - 3;
+            if (t >= 0) continue;
+            x[i] = T{};
+            if (q.old && t + W1 >= 0)
+                x[i] = static_cast<const T *>(a.conv_state)[(static_cast<int64_t>(q.slot) * a.C + channel) * W1 + t + W1];
+        }
+    }
+};
+
+// silu of the convolution over a window: o[0 .. K - 1] (a filter of W < 4 columns leaves the earliest rows out)
+template <class T, int K>
+__device__ __forceinline__ void convolve(const Window<T, K> &in, const float (&w)[4], float bias, int W, float *o) {
+#pragma unroll
+    for (int i = 0; i < K; ++i) o[i] = bias;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (k >= 4 - W) {
+#pragma unroll
+            for (int i = 0; i < K; ++i) o[i] = __builtin_fmaf(w[k], widen_v(in.x[i + k]), o[i]);
+        }
+#pragma unroll
+    for (int i = 0; i < K; ++i) o[i] = silu_f(o[i]);
+}
+
+__device__ __forceinline__ void filter(const SsdConvArgs &a, int channel, float (&w)[4], float &bias) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = k >= 4 - a.W ? a.w[static_cast<int64_t>(channel) * a.W + k - (4 - a.W)] : 0.0f;
+    bias = a.bias ? a.bias[channel] : 0.0f;
+}
+
+// One channel's last W - 1 inputs into its slot (what a sequence shorter than that leaves of the old ones in front).
+template <class T>
+__device__ __forceinline__ void conv_state_end(const SsdConvArgs &a, const Sequence &q, int channel) {
+    const int W1 = a.W - 1;
+    T *st = static_cast<T *>(a.conv_state) + (static_cast<int64_t>(q.slot) * a.C + channel) * W1;
+    T v[3];
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+        const int k = q.len + j;            // of the old columns and the tokens side by side
+        if (j >= W1) v[j] = T{};
+        else if (k < W1) v[j] = q.old ? st[k] : T{};
+        else v[j] = static_cast<const T *>(a.xbc)[(q.first + static_cast<int64_t>(k - W1)) * a.x_row + channel];
+    }
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+        if (j < W1) st[j] = v[j];
+}
+
+// ---------------------------------------------------------------------------- prep
+
+// NP: the states padded to 64 or 128; PY: parts of y's factors
+template <class T, int NP, int PY>
+__global__ void __launch_bounds__(kThreads) ssdconv_prep_kernel(SsdConvArgs a) {
+    constexpr int kRow = NP + 4;
+    __shared__ __align__(16) float tile[2][kQ][kRow];    // B and C, token by token
+    const int64_t u = blockIdx.x;
+    const int s = find_sequence(a, kQ, u);
+    if (s < 0) return;
+    const Sequence q(a, s);
+    const int t0 = static_cast<int>(u - (q.first / kQ + s)) * kQ;
+    if (t0 >= q.len) return;
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lr = lane & 15, lg = lane >> 4;
+
+    if (static_cast<int>(blockIdx.y) >= a.G) {   // ---- the decays of eight heads, a wave each
+        const int h = (static_cast<int>(blockIdx.y) - a.G) * 8 + wv;
+        if (h >= a.H) return;
+        float dt = 0.0f;
+        if (t0 + lane < q.len) {
+            dt = widen_v(static_cast<const T *>(a.delta)[(q.first + static_cast<int64_t>(t0) + lane) * a.d_row + h]);
+            if (a.dbias) dt += a.dbias[h];
+            if (a.softplus) dt = softplus_f(dt);
+        }
+        const float step = dt * (a.A[h] * kLog2e);
+        float pre = step, suf = step;            // inclusive, within a half of 32
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float p = __shfl_up(pre, o, 32), f = __shfl_down(suf, o, 32);
+            if ((lane & 31) >= o) pre += p;
+            if ((lane & 31) + o < 32) suf += f;
+        }
+        const float behind = __shfl_down(suf, 1, 32);
+        const float ein = __builtin_amdgcn_exp2f(pre);
+        const float wb = __builtin_amdgcn_exp2f((lane & 31) == 31 ? 0.0f : behind) * dt;
+        const float half0 = __shfl(ein, 31, 64), half1 = __shfl(ein, 63, 64);
+        float *t = a.ws_tab + (u * a.H + h) * (kTabs * kQ) + lane;
+        t[kE * kQ] = lane < 32 ? ein : ein * half0;
+        t[kWr * kQ] = lane < 32 ? wb * half1 : wb;
+        t[kC32 * kQ] = pre;
+        t[kDt * kQ] = dt;
+        t[kEin * kQ] = ein;
+        t[kWb * kQ] = wb;
+        return;
+    }
+
+    // ---- B and C of group g behind the convolution: a thread per channel and run of tokens
+    const int g = blockIdx.y;
+    constexpr int kTok = kQ * 2 * NP / kThreads;         // 32 or 16
+    const int ch = threadIdx.x % (2 * NP), n = ch % NP, which = ch / NP, from = threadIdx.x / (2 * NP) * kTok;
+    const int channel = a.H * a.P + (which * a.G + g) * a.N + n;
+    float w[4], bias;
+    if (n < a.N) filter(a, channel, w, bias);
+    s8 *bt = reinterpret_cast<s8 *>(a.ws_bt) + (u * a.G + g) * (NP / 16 * 2 * kPS * 64);
+#pragma unroll
+    for (int r = 0; r < kTok; r += 16) {
+        float o[16];
+        if (n < a.N) {
+            Window<T, 16> in;
+            in.load(a, q, channel, t0 + from + r);
+            convolve(in, w, bias, a.W, o);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (n >= a.N || t0 + from + r + i >= q.len) o[i] = 0.0f;
+            tile[which][from + r + i][n] = o[i];
+        }
+        if (which == 0) {
+            // operands of the state's product: lane (n % 16, s / 8 % 4) of slice n / 16 holds B[s .. s + 7][n]
+#pragma unroll
+            for (int e = 0; e < 16; e += 8) {
+                s8 part[kPS];
+                split8<kPS>(o + e, part);
+                const int t = from + r + e;
+#pragma unroll
+                for (int k = 0; k < kPS; ++k)
+                    bt[((n / 16 * 2 + t / 32) * kPS + k) * 64 + n % 16 + 16 * (t % 32 / 8)] = part[k];
+            }
+        }
+    }
+    __syncthreads();
+    // ---- operands of C, and C B^T below the diagonal: wave (i, half) takes C's tokens 16 i .. and B's blocks half, half + 2
+    const int i = wv & 3, half = wv >> 2;
+    s8 cf[NP / 32][PY];
+    s8 *cs = reinterpret_cast<s8 *>(a.ws_c) + ((u * a.G + g) * 4 + i) * (NP / 32 * PY * 64) + lane;
+#pragma unroll
+    for (int kk = 0; kk < NP / 32; ++kk) {
+        split8<PY>(&tile[1][16 * i + lr][32 * kk + 8 * lg], cf[kk]);
+        if (half == 0) {
+#pragma unroll
+            for (int k = 0; k < PY; ++k) cs[(kk * PY + k) * 64] = cf[kk][k];
+        }
+    }
+    float *cb = a.ws_cb + ((u * a.G + g) * kQ + 16 * i + lr) * kQ;
+    for (int k = half; k <= i; k += 2) {
+        f4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int kk = 0; kk < NP / 32; ++kk) {
+            s8 bf[PY];
+            split8<PY>(&tile[0][16 * k + lr][32 * kk + 8 * lg], bf);
+            acc = product<PY>(bf, cf[kk], acc);
+        }
+        *reinterpret_cast<f4 *>(cb + 16 * k + 4 * lg) = acc;    // lane: token 16 i + lr, s = 16 k + 4 lg + 0 .. 3
+    }
+}
+
+// ---------------------------------------------------------------------------- sweep
+
+// 16-byte units of a row of LDS are swapped by its number, so that lanes that read a column of rows meet all banks
+__device__ __forceinline__ int at_x(int p, int unit) { return p * kQ + ((unit ^ (((p >> 3) & 3) << 1 | ((p >> 1) & 1))) << 3); }
+__device__ __forceinline__ int at_w(int p, int unit) { return p * kQ + ((unit ^ ((p >> 1) & 7)) << 3); }
+template <int NP>
+__device__ __forceinline__ int at_s(int p, int unit) {
+    const int h = NP == 128 ? ((p >> 3) & 3) << 2 | (p & 3) : ((p >> 3) & 3) << 1 | ((p >> 1) & 1);
+    return p * NP + ((unit ^ h) << 3);
+}
+
+template <int NP, int PY>
+struct SweepLds {
+    static constexpr int kStates = PY == 3 && NP == 128 ? 1 : 2;   // (two copies of the state's parts where they fit)
+    uint16_t xt[2][PY][kQ * kQ];        // x behind the convolution: [channel][token]
+    uint16_t xw[2][kPS][kQ * kQ];       // the same, weighted for the state
+    uint16_t st[kStates][PY][kQ * NP];  // the chunk's start state: [channel][state]
+    float tab[2][kTabs][kQ];
+    int bad[3];                         // whether a chunk's x has a NaN or infinity
+    int first_bad[2][8][kQ];            // and where: [wave][channel] the first such token (64: none)
+};
+struct StateLds {
+    uint16_t xw[2][kPS][kQ * kQ];
+};
+
+template <class T, int NP, int PY, bool OWN>   // OWN: the segments' own end states, nothing else
+__global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) {
+    typedef SweepLds<NP, PY> Lds;
+    __shared__ __align__(16) typename std::conditional<OWN, StateLds, Lds>::type sm;
+    constexpr int kPT = NP == 128 ? 4 : 2;           // 16-channel tiles of a wave's states
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lr = lane & 15, lg = lane >> 4;
+
+    // workgroup -> (segment, head, channels), neighbours on one XCD (they are dealt out in turn): the heads of a
+    // sequence read the same operands of B and C from that XCD's L2
+    const int64_t W = a.items * a.H * a.PB, per = (W + 7) / 8;
+    const int64_t id = static_cast<int64_t>(blockIdx.x) % 8 * per + blockIdx.x / 8;
+    if (blockIdx.x / 8 >= per || id >= W) return;
+    const int pb = static_cast<int>(id % a.PB), h = static_cast<int>(id / a.PB % a.H);
+    const int64_t item = id / a.PB / a.H;
+    const int s = find_sequence(a, a.seg_len, item);
+    if (s < 0) return;
+    const Sequence q(a, s);
+    const int64_t seg = item - (q.first / a.seg_len + s);
+    if (seg * a.seg_len >= q.len && seg > 0) return;
+    const int begin = static_cast<int>(seg * a.seg_len);
+    const bool last = q.len - begin <= a.seg_len;
+    if (OWN && last) return;                         // nobody reads its own state
+    const int end = last ? q.len : begin + a.seg_len, nch = (end - begin + kQ - 1) / kQ;
+    const int g = h / (a.H / a.G);
+    const int64_t u0 = q.first / kQ + s + begin / kQ;   // the first chunk's number (seg_len is a multiple of 64)
+    const int p0 = pb * kQ, np = a.P - p0 < kQ ? a.P - p0 : kQ;   // channels p0 .. p0 + np - 1 of the head
+
+    // ---- the state: wave wv has states 16 sl + 4 lg + j and channels 16 (pt0 + i) + lr
+    const int sl = NP == 128 ? wv : wv & 3, pt0 = NP == 128 ? 0 : wv >> 2 << 1;
+    f4 S[kPT];
+    {
+        const float *from = OWN ? nullptr : a.nseg_split ? a.ws_state + (item * a.H + h) * a.P * a.N
+                                : q.old ? a.h + (static_cast<int64_t>(q.slot) * a.H + h) * a.P * a.N : nullptr;
+#pragma unroll
+        for (int i = 0; i < kPT; ++i) {
+            const int p = 16 * (pt0 + i) + lr;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int n = 16 * sl + 4 * lg + j;
+                S[i][j] = from && p < np && n < a.N ? from[static_cast<int64_t>(p0 + p) * a.N + n] : 0.0f;
+            }
+        }
+    }
+    auto put_state = [&](int b) __attribute__((always_inline)) {
+        if constexpr (!OWN) {
+#pragma unroll
+            for (int i = 0; i < kPT; ++i) {
+                uint32_t w[PY][2];
+                const float v[4] = {S[i][0], S[i][1], S[i][2], S[i][3]};
+                split<PY, 4>(v, w);
+                const int at = at_s<NP>(16 * (pt0 + i) + lr, 2 * sl + (lg >> 1)) + 4 * (lg & 1);
+#pragma unroll
+                for (int k = 0; k < PY; ++k) *reinterpret_cast<u2 *>(&sm.st[b][k][at]) = u2{w[k][0], w[k][1]};
+            }
+        }
+    };
+
+    // ---- staging: thread (channel lane, tokens 8 wv .. 8 wv + 7)
+    const bool mine = lane < np;
+    const int channel = h * a.P + p0 + (mine ? lane : 0);
+    float fw[4], fbias;
+    filter(a, channel, fw, fbias);
+    Window<T, 8> win;
+    auto load_x = [&](int c) __attribute__((always_inline)) { win.load(a, q, channel, begin + c * kQ + 8 * wv); };
+    f4 tq = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto tab_at = [&](int c) { return a.ws_tab + ((u0 + c) * a.H + h) * (kTabs * kQ); };
+    auto load_tab = [&](int c) __attribute__((always_inline)) {
+        if constexpr (!OWN)
+            if (threadIdx.x < kTabs * kQ / 4) tq = *reinterpret_cast<const f4 *>(tab_at(c) + 4 * threadIdx.x);
+    };
+    auto stage = [&](int c) __attribute__((always_inline)) {
+        const int b = c & 1, t0 = begin + c * kQ + 8 * wv;
+        float o[8];
+        convolve(win, fw, fbias, a.W, o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (!mine || t0 + i >= end) o[i] = 0.0f;
+        const float *wr = tab_at(c) + kWr * kQ + 8 * wv;     // (wave-uniform: scalar loads)
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = o[i] * wr[i];
+        s8 part[kPS];
+        split8<kPS>(v, part);
+#pragma unroll
+        for (int k = 0; k < kPS; ++k) *reinterpret_cast<s8 *>(&sm.xw[b][k][at_w(lane, wv)]) = part[k];
+        if constexpr (!OWN) {
+            // A NaN or infinity of x must not meet the zeros above the diagonal: it is taken out here, and y gets
+            // NaN from its token on (through the state, from the next chunk on, all by itself).
+            int first = kQ;
+#pragma unroll
+            for (int i = 7; i >= 0; --i)
+                if (!(__builtin_fabsf(o[i]) <= 3.4028234663852886e38f)) {
+                    first = 8 * wv + i;
+                    o[i] = 0.0f;
+                }
+            sm.first_bad[b][wv][lane] = first;
+            if (first < kQ) sm.bad[c % 3] = 1;
+            s8 y[PY];
+            split8<PY>(o, y);
+#pragma unroll
+            for (int k = 0; k < PY; ++k) *reinterpret_cast<s8 *>(&sm.xt[b][k][at_x(lane, wv)]) = y[k];
+            if (threadIdx.x < kTabs * kQ / 4) *reinterpret_cast<f4 *>(&sm.tab[b][0][0] + 4 * threadIdx.x) = tq;
+        }
+    };
+
+    // ---- operands of B (the wave's 16 states)
+    s8 bf[2][kPS];
+    auto load_b = [&](int c) __attribute__((always_inline)) {
+        const s8 *p = reinterpret_cast<const s8 *>(a.ws_bt) + (((u0 + c) * a.G + g) * (NP / 16) + sl) * (2 * kPS * 64) + lane;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int k = 0; k < kPS; ++k) bf[ks][k] = p[(ks * kPS + k) * 64];
+    };
+
+    // ---- outputs: wave (i, ph) has tokens 16 i + lr and, of the channels 32 ph .., 8 lg .. 8 lg + 7
+    const int i = wv < 4 ? wv : 7 - wv, ph = wv >> 2;      // (a SIMD's two waves: token blocks of 0 and 3, or of 1 and 2)
+    const int t_l = 16 * i + lr, out_p = 32 * ph + 8 * lg;
+    const float dsk = a.Dskip ? a.Dskip[h] : 0.0f;
+    s8 cf[NP / 32][PY];
+    auto load_c = [&](int c) __attribute__((always_inline)) {
+        const s8 *p = reinterpret_cast<const s8 *>(a.ws_c) + (((u0 + c) * a.G + g) * 4 + i) * (NP / 32 * PY * 64) + lane;
+#pragma unroll
+        for (int kk = 0; kk < NP / 32; ++kk)
+#pragma unroll
+            for (int k = 0; k < PY; ++k) cf[kk][k] = p[(kk * PY + k) * 64];
+    };
+    f4 cb[2][2];
+    auto load_cb = [&](int c) __attribute__((always_inline)) {
+        const float *p = a.ws_cb + (((u0 + c) * a.G + g) * kQ + t_l) * kQ + 8 * lg;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+            if (ks <= i >> 1) {
+                cb[ks][0] = *reinterpret_cast<const f4 *>(p + 32 * ks);
+                cb[ks][1] = *reinterpret_cast<const f4 *>(p + 32 * ks + 4);
+            }
+    };
+    T zq[8];
+    auto load_z = [&](int c) __attribute__((always_inline)) {
+        const int t = begin + c * kQ + t_l;
+        if (!a.z || t >= end || out_p >= np) return;
+        const T *p = static_cast<const T *>(a.z) + (q.first + static_cast<int64_t>(t)) * a.z_row + h * a.P + p0 + out_p;
+        if (a.z_vec) {
+#pragma unroll
+            for (int k = 0; k < 8; k += 16 / static_cast<int>(sizeof(T)))
+                *reinterpret_cast<u4 *>(zq + k) = *reinterpret_cast<const u4 *>(p + k);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (out_p + k < np) zq[k] = p[k];
+        }
+    };
+
+    if (nch > 0) {
+        load_x(0);
+        load_tab(0);
+        load_b(0);
+        if constexpr (!OWN) {
+            if (threadIdx.x < 3) sm.bad[threadIdx.x] = 0;
+            load_c(0);
+            load_cb(0);
+            load_z(0);
+            put_state(0);
+            __syncthreads();
+        }
+        stage(0);
+        if (nch > 1) {
+            load_x(1);
+            load_tab(1);
+        }
+        __syncthreads();
+    }
+    float whole = 1.0f;      // decay over the segment
+    for (int c = 0; c < nch; ++c) {
+        const int b = c & 1;
+        const bool more = c + 1 < nch;
+        float dec;
+        if constexpr (OWN) {
+            dec = tab_at(c)[kE * kQ + kQ - 1];
+            whole *= dec;
+        } else {
+            dec = sm.tab[b][kE][kQ - 1];
+            if (threadIdx.x == 0) sm.bad[(c + 2) % 3] = 0;
+            const int sb = Lds::kStates == 2 ? b : 0;
+            const bool on = 32 * ph < np;
+            f4 acc[2] = {};
+            if (on) {
+                // the carried state's share.  Row r of tile k is channel 32 ph + 8 (r / 4) + 4 k + r % 4, so that a lane
+                // gets eight channels side by side
+#pragma unroll
+                for (int kk = 0; kk < NP / 32; ++kk)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        s8 sf[PY];
+                        const int p = 32 * ph + 8 * (lr >> 2) + 4 * k + (lr & 3);
+#pragma unroll
+                        for (int e = 0; e < PY; ++e) sf[e] = *reinterpret_cast<const s8 *>(&sm.st[sb][e][at_s<NP>(p, 4 * kk + lg)]);
+                        acc[k] = product<PY>(sf, cf[kk], acc[k]);
+                    }
+                const float e = sm.tab[b][kE][t_l];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) acc[k] *= e;
+            }
+            if (more) load_c(c + 1);
+            if (on) {
+                // the chunk's own share: (C_t . B_s) decayed, D on the diagonal, times x
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    if (ks > i >> 1) continue;
+                    float v[8];
+                    const int s0 = 32 * ks + 8 * lg;
+                    const f4 d0 = *reinterpret_cast<const f4 *>(&sm.tab[b][ks == i >> 1 ? kDt : kWb][s0]);
+                    const f4 d1 = *reinterpret_cast<const f4 *>(&sm.tab[b][ks == i >> 1 ? kDt : kWb][s0 + 4]);
+                    if (ks == i >> 1) {
+                        const f4 c0 = *reinterpret_cast<const f4 *>(&sm.tab[b][kC32][s0]);
+                        const f4 c1 = *reinterpret_cast<const f4 *>(&sm.tab[b][kC32][s0 + 4]);
+                        const float ct = sm.tab[b][kC32][t_l];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float f = __builtin_amdgcn_exp2f(ct - (e < 4 ? c0[e & 3] : c1[e & 3])) * (e < 4 ? d0[e & 3] : d1[e & 3]);
+                            v[e] = s0 + e <= t_l ? cb[ks][e >> 2][e & 3] * f : 0.0f;
+                            if (s0 + e == t_l) v[e] += dsk;
+                        }
+                    } else {
+                        const float et = sm.tab[b][kEin][t_l];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = cb[ks][e >> 2][e & 3] * (et * (e < 4 ? d0[e & 3] : d1[e & 3]));
+                    }
+                    s8 m[PY];
+                    split8<PY>(v, m);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        s8 xf[PY];
+                        const int p = 32 * ph + 8 * (lr >> 2) + 4 * k + (lr & 3);
+#pragma unroll
+                        for (int e = 0; e < PY; ++e) xf[e] = *reinterpret_cast<const s8 *>(&sm.xt[b][e][at_x(p, 4 * ks + lg)]);
+                        acc[k] = product<PY>(xf, m, acc[k]);
+                    }
+                }
+            }
+            if (more) load_cb(c + 1);
+            const int t = begin + c * kQ + t_l;
+            if (on && t < end && out_p < np) {
+                float y[8] = {acc[0][0], acc[0][1], acc[0][2], acc[0][3], acc[1][0], acc[1][1], acc[1][2], acc[1][3]};
+                if (sm.bad[c % 3]) {
+                    for (int k = 0; k < 8; ++k)
+                        for (int o = 0; o < 8; ++o)
+                            if (sm.first_bad[b][o][out_p + k] <= t_l) y[k] = __builtin_nanf("");
+                }
+                if (a.z) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) y[k] *= silu_f(widen_v(zq[k]));
+                }
+                T *out = static_cast<T *>(a.y) + ((q.first + static_cast<int64_t>(t)) * a.H + h) * a.P + p0 + out_p;
+                if (a.y_vec) {
+                    if constexpr (sizeof(T) == 2)
+                        *reinterpret_cast<u4 *>(out) = u4{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])};
+                    else
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) *reinterpret_cast<f4 *>(out + 4 * k) = f4{y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]};
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (out_p + k < np) put(out, k, y[k]);
+                }
+            }
+            if (more) load_z(c + 1);
+            if constexpr (Lds::kStates == 1) __syncthreads();   // the old state's parts are read
+        }
+        // ---- the state passed on
+#pragma unroll
+        for (int j = 0; j < kPT; ++j) {
+            if (16 * (pt0 + j) >= np) continue;
+            f4 acc = S[j] * dec;
+            const int p = 16 * (pt0 + j) + lr;
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                s8 xf[kPS];
+#pragma unroll
+                for (int k = 0; k < kPS; ++k) xf[k] = *reinterpret_cast<const s8 *>(&sm.xw[b][k][at_w(p, 4 * ks + lg)]);
+                acc = product<kPS>(bf[ks], xf, acc);
+            }
+            S[j] = acc;
+        }
+        if (more) {
+            load_b(c + 1);
+            if constexpr (!OWN) put_state(Lds::kStates == 2 ? b ^ 1 : 0);
+            stage(c + 1);
+            if (c + 2 < nch) {
+                load_x(c + 2);
+                load_tab(c + 2);
+            }
+            __syncthreads();
+        }
+    }
+
+    // ---- end states
+    float *to = OWN ? a.ws_state + (item * a.H + h) * a.P * a.N
+              : last && q.slot >= 0 ? a.h + (static_cast<int64_t>(q.slot) * a.H + h) * a.P * a.N : nullptr;
+    if (to) {
+#pragma unroll
+        for (int k = 0; k < kPT; ++k) {
+            const int p = 16 * (pt0 + k) + lr;
+            if (p >= np) continue;
+            float *row = to + static_cast<int64_t>(p0 + p) * a.N + 16 * sl + 4 * lg;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (16 * sl + 4 * lg + j < a.N) row[j] = S[k][j];
+        }
+    }
+    if constexpr (OWN) {
+        if (pb == 0 && threadIdx.x == 0) a.ws_dec[item * a.H + h] = whole;
+    } else if (!a.nseg_split && q.slot >= 0 && a.W > 1) {
+        // the convolution's state: this workgroup's own channels of x (it alone has read them), and, one workgroup for each
+        // group, those of B and C (read by prep)
+        __syncthreads();
+        const int extra = pb == 0 && h % (a.H / a.G) == 0 ? 2 * a.N : 0;
+        for (int k = threadIdx.x; k < np + extra; k += kThreads) {
+            const int e = k - np;
+            conv_state_end<T>(a, q, k < np ? h * a.P + p0 + k : a.H * a.P + (e < a.N ? g * a.N + e : (a.G + g) * a.N + e - a.N));
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------- segments
+
+// The segments' own end states become their start states: per sequence and head, an element a thread.
+__global__ void __launch_bounds__(256) ssdconv_join_kernel(SsdConvArgs a) {
+    const int64_t hp = static_cast<int64_t>(a.P) * a.N, e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int h = blockIdx.y, s = blockIdx.z;
+    if (e >= hp) return;
+    const Sequence q(a, s);
+    const int64_t item = q.first / a.seg_len + s, n = q.len > 0 ? (q.len + a.seg_len - 1) / a.seg_len : 1;
+    float v = q.old ? a.h[(static_cast<int64_t>(q.slot) * a.H + h) * hp + e] : 0.0f;
+    for (int64_t k = 0; k < n; ++k) {
+        float *p = a.ws_state + ((item + k) * a.H + h) * hp + e;
+        const float own = k + 1 < n ? *p : 0.0f;
+        *p = v;
+        if (k + 1 < n) v = __builtin_fmaf(a.ws_dec[(item + k) * a.H + h], v, own);
+    }
+}
+
+template <class T>
+__global__ void __launch_bounds__(256) ssdconv_conv_state_kernel(SsdConvArgs a) {
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const Sequence q(a, blockIdx.y);
+    if (c < a.C && q.slot >= 0) conv_state_end<T>(a, q, static_cast<int>(c));
+}
+
+// ---------------------------------------------------------------------------- one token
+
+// The convolution of one token, all channels, into 32 bits; its state moves on.
+template <class T>
+__global__ void __launch_bounds__(256) ssdconv_token_conv_kernel(SsdConvArgs a) {
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, b = blockIdx.y;
+    if (c >= a.C) return;
+    int slot = a.slots ? a.slots[b] : static_cast<int>(b);
+    if (slot < 0 || slot >= a.nslots) slot = -1;
+    const int W1 = a.W - 1;
+    T *st = static_cast<T *>(a.conv_state) + (static_cast<int64_t>(slot) * a.C + c) * W1;
+    const T x = static_cast<const T *>(a.xbc)[b * a.x_row + c];
+    T old[3];
+    float v = a.bias ? a.bias[c] : 0.0f;
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+        if (k < W1) {
+            old[k] = slot >= 0 ? st[k] : T{};
+            v = __builtin_fmaf(a.w[c * a.W + k], widen_v(old[k]), v);
+        }
+    v = __builtin_fmaf(a.w[c * a.W + W1], widen_v(x), v);
+    a.ws_x[b * a.C + c] = silu_f(v);
+    if (slot >= 0) {
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+            if (k < W1) st[k] = k + 1 < W1 ? old[k + 1 < 3 ? k + 1 : 2] : x;
+    }
+}
+
+// One token of the scan: a workgroup per sequence and head (gridDim.z: shares of its channels).  Rows of N states are read
+// by teams of lanes, V states a lane and turn (16 bytes where N and the addresses allow it), four rows at a time: memory bound,
+// 8 bytes for every state.
+template <class T, int V>
+__global__ void __launch_bounds__(256) ssdconv_token_kernel(SsdConvArgs a) {
+    const int64_t id = blockIdx.x;
+    const int h = static_cast<int>(id % a.H);
+    const int64_t b = id / a.H;
+    int slot = a.slots ? a.slots[b] : static_cast<int>(b);
+    if (slot < 0 || slot >= a.nslots) slot = -1;
+    const int team = a.team, lane = threadIdx.x & (team - 1), me = threadIdx.x / team, teams = 256 / team;
+    constexpr int kU = V == 4 ? 1 : 2;               // 128 states: 32 lanes of four, or 64 lanes of two single ones
+    constexpr int kR = 4;
+    float dt = widen_v(static_cast<const T *>(a.delta)[b * a.d_row + h]);
+    if (a.dbias) dt += a.dbias[h];
+    if (a.softplus) dt = softplus_f(dt);
+    const float dec = __builtin_amdgcn_exp2f(dt * (a.A[h] * kLog2e)), dsk = a.Dskip ? a.Dskip[h] : 0.0f;
+    const float *xs = a.ws_x + b * a.C, *X = xs + static_cast<int64_t>(h) * a.P;
+    const int g = h / (a.H / a.G);
+    const float *Bv = xs + static_cast<int64_t>(a.H) * a.P + g * a.N, *Cv = Bv + a.G * a.N;
+    float bv[kU][V], cv[kU][V];
+#pragma unroll
+    for (int k = 0; k < kU; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int n = (lane + k * team) * V + j;
+            bv[k][j] = n < a.N ? dt * Bv[n] : 0.0f;
+            cv[k][j] = n < a.N ? Cv[n] : 0.0f;
+        }
+    float *hs = a.h + (static_cast<int64_t>(slot < 0 ? 0 : slot) * a.H + h) * a.P * a.N;
+    const int share = (a.P + static_cast<int>(gridDim.y) - 1) / static_cast<int>(gridDim.y);
+    const int pa = static_cast<int>(blockIdx.y) * share, pe = pa + share < a.P ? pa + share : a.P;
+    for (int p0 = pa + me; p0 < pe; p0 += kR * teams) {
+        float st[kR][kU][V];
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            const int p = p0 + r * teams;
+            const float *row = hs + static_cast<int64_t>(p) * a.N;
+#pragma unroll
+            for (int k = 0; k < kU; ++k) {
+                const int n = (lane + k * team) * V;
+                const bool in = slot >= 0 && p < pe && n < a.N;
+                if constexpr (V == 4) {
+                    const f4 v = in ? __builtin_nontemporal_load(reinterpret_cast<const f4 *>(row + n)) : f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) st[r][k][j] = v[j];
+                } else st[r][k][0] = in ? row[n] : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            const int p = p0 + r * teams;
+            const float x = X[p < pe ? p : pe - 1];
+            float y = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kU; ++k)
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    st[r][k][j] = __builtin_fmaf(dec, st[r][k][j], bv[k][j] * x);
+                    y = __builtin_fmaf(cv[k][j], st[r][k][j], y);
+                }
+            for (int o = team >> 1; o > 0; o >>= 1) y += __shfl_xor(y, o, 64);
+            if (p >= pe) continue;
+            float *row = hs + static_cast<int64_t>(p) * a.N;
+#pragma unroll
+            for (int k = 0; k < kU; ++k) {
+                const int n = (lane + k * team) * V;
+                if (slot < 0 || n >= a.N) continue;
+                if constexpr (V == 4)
+                    __builtin_nontemporal_store(f4{st[r][k][0], st[r][k][1], st[r][k][2], st[r][k][3]}, reinterpret_cast<f4 *>(row + n));
+                else row[n] = st[r][k][0];
+            }
+            if (lane == 0) {
+                float v = __builtin_fmaf(dsk, x, y);
+                if (a.z) v *= silu_f(widen(static_cast<const T *>(a.z), b * a.z_row + static_cast<int64_t>(h) * a.P + p));
+                put(static_cast<T *>(a.y), (b * a.H + h) * a.P + p, v);
+            }
+        }
+    }
+}
+
+template <class T, int NP, int PY>
+hipError_t prompts(const SsdConvArgs &a, hipStream_t s) {
+    const unsigned heads = static_cast<unsigned>((a.H + 7) / 8);
+    hipLaunchKernelGGL((ssdconv_prep_kernel<T, NP, PY>), dim3(static_cast<unsigned>(a.chunks), static_cast<unsigned>(a.G) + heads),
+                       dim3(kThreads), 0, s, a);
+    hipError_t e = launch_status(s);
+    if (e != hipSuccess) return e;
+    const dim3 grid(static_cast<unsigned>((a.items * a.H * a.PB + 7) / 8 * 8));
+    if (a.nseg_split) {
+        hipLaunchKernelGGL((ssdconv_sweep_kernel<T, NP, PY, true>), grid, dim3(kThreads), 0, s, a);
+        e = launch_status(s);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL(ssdconv_join_kernel, dim3(static_cast<unsigned>((a.P * a.N + 255) / 256), static_cast<unsigned>(a.H),
+                                                     static_cast<unsigned>(a.S)), dim3(256), 0, s, a);
+        e = launch_status(s);
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((ssdconv_sweep_kernel<T, NP, PY, false>), grid, dim3(kThreads), 0, s, a);
+    e = launch_status(s);
+    if (e != hipSuccess || !a.nseg_split || a.W == 1) return e;
+    hipLaunchKernelGGL((ssdconv_conv_state_kernel<T>), dim3(static_cast<unsigned>((a.C + 255) / 256), static_cast<unsigned>(a.S)),
+                       dim3(256), 0, s, a);
+    return launch_status(s);
+}
+
+template <class T>
+hipError_t token(const SsdConvArgs &a, hipStream_t s) {
+    hipLaunchKernelGGL((ssdconv_token_conv_kernel<T>), dim3(static_cast<unsigned>((a.C + 255) / 256), static_cast<unsigned>(a.S)),
+                       dim3(256), 0, s, a);
+    hipError_t e = launch_status(s);
+    if (e != hipSuccess) return e;
+    const dim3 grid(static_cast<unsigned>(a.S * a.H), static_cast<unsigned>(a.shares));
+    if (a.h_vec) hipLaunchKernelGGL((ssdconv_token_kernel<T, 4>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((ssdconv_token_kernel<T, 1>), grid, dim3(256), 0, s, a);
+    return launch_status(s);
+}
+
+}  // namespace
+
+hipError_t launch_ssdconv(const SsdConvArgs &a, bool bf16, hipStream_t s) {
+    if (bf16) return a.N > 64 ? prompts<uint16_t, 128, 2>(a, s) : prompts<uint16_t, 64, 2>(a, s);
+    return a.N > 64 ? prompts<float, 128, 3>(a, s) : prompts<float, 64, 3>(a, s);
+}
+
+hipError_t launch_ssdconv_token(const SsdConvArgs &a, bool bf16, hipStream_t s) {
+    return bf16 ? token<uint16_t>(a, s) : token<float>(a, s);
+}
+
+}  // namespace ssm

@@ -1453,3 +1453,66 @@ extern "C" int ssm_qknorm_bwd(const ssm_rotary_shape *shape, const void *q, cons
     const hipError_t e = launch_rotary(a, shape->dtype == SSM_DTYPE_BF16, p.vec, shape->interleaved != 0, true, true, s);
     return e == hipSuccess ? SSM_OK : hip_fail("qknorm backward launch", e);
 }
+
+namespace {
+SsdConvArgs ssdconv_args(const ssm_ssdconv_shape &s, const SsdConvPlan &p, const void *xbc, const void *delta, const float *A,
+                         const float *w, const float *bias, const float *Dskip, const void *z, const float *delta_bias,
+                         int delta_softplus, const int32_t *slots, float *h, void *conv_state, void *y) {
+    SsdConvArgs a{};
+    a.T = s.tokens; a.S = static_cast<int>(s.sequences); a.H = static_cast<int>(s.nheads); a.P = static_cast<int>(s.headdim);
+    a.N = static_cast<int>(s.dstate); a.G = static_cast<int>(s.ngroups); a.W = static_cast<int>(s.width); a.C = p.channels;
+    a.xbc = xbc; a.z = z; a.delta = delta; a.x_row = p.x_row; a.z_row = p.z_row; a.d_row = p.d_row;
+    a.w = w; a.bias = bias; a.A = A; a.Dskip = Dskip; a.dbias = delta_bias; a.softplus = delta_softplus;
+    a.slots = slots; a.nslots = s.nslots; a.h = h; a.conv_state = conv_state; a.y = y;
+    a.PB = static_cast<int>(p.blocks64); a.seg_len = static_cast<int>(p.seg_len); a.nseg_split = p.split;
+    a.chunks = p.chunks; a.items = p.items; a.z_vec = p.z_vec; a.y_vec = p.y_vec; a.h_vec = p.h_vec;
+    a.team = p.team; a.shares = p.shares;
+    return a;
+}
+}  // namespace
+
+extern "C" int ssm_ssdconv_fwd(const ssm_ssdconv_shape *shape, const void *xbc, const void *delta, const float *A,
+                               const float *w, const float *bias, const float *Dskip, const void *z, const float *delta_bias,
+                               int delta_softplus, const int32_t *offsets, const int32_t *slots, const uint8_t *fresh, float *h,
+                               void *conv_state, void *y, void *workspace, size_t workspace_bytes, void *stream) {
+    using namespace ssm;
+    clear_error();
+    SsdConvPlan p;
+    const int st = check_ssdconv(shape, false, xbc, delta, A, w, bias, Dskip, z, delta_bias, delta_softplus, offsets, slots,
+                                 fresh, h, conv_state, y, workspace, workspace_bytes, &p);
+    if (st != SSM_OK) return st;
+    if (shape->sequences == 0 || shape->nheads == 0) return SSM_OK;
+    SsdConvArgs a = ssdconv_args(*shape, p, xbc, delta, A, w, bias, Dskip, z, delta_bias, delta_softplus, slots, h, conv_state, y);
+    a.offsets = offsets; a.fresh = fresh;
+    char *ws = static_cast<char *>(workspace);
+    a.ws_bt = reinterpret_cast<uint16_t *>(ws);
+    a.ws_c = reinterpret_cast<uint16_t *>(ws + p.c_off);
+    a.ws_cb = reinterpret_cast<float *>(ws + p.cb_off);
+    a.ws_tab = reinterpret_cast<float *>(ws + p.tab_off);
+    a.ws_state = reinterpret_cast<float *>(ws + p.state_off);
+    a.ws_dec = reinterpret_cast<float *>(ws + p.dec_off);
+    log_call("ssdconv tokens=%lld sequences=%d H=%d P=%d N=%d G=%d W=%d dtype=%d: %s of %lld tokens, workspace %zu",
+             (long long)a.T, a.S, a.H, a.P, a.N, a.G, a.W, shape->dtype, p.split ? "segments" : "whole sequences",
+             (long long)p.seg_len, p.ws_bytes);
+    const hipError_t e = launch_ssdconv(a, shape->dtype == SSM_DTYPE_BF16, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? SSM_OK : hip_fail("ssdconv launch", e);
+}
+
+extern "C" int ssm_ssdconv_update(const ssm_ssdconv_shape *shape, const void *xbc, const void *delta, const float *A,
+                                  const float *w, const float *bias, const float *Dskip, const void *z, const float *delta_bias,
+                                  int delta_softplus, const int32_t *slots, float *h, void *conv_state, void *y, void *workspace,
+                                  size_t workspace_bytes, void *stream) {
+    using namespace ssm;
+    clear_error();
+    SsdConvPlan p;
+    const int st = check_ssdconv(shape, true, xbc, delta, A, w, bias, Dskip, z, delta_bias, delta_softplus, nullptr, slots,
+                                 nullptr, h, conv_state, y, workspace, workspace_bytes, &p);
+    if (st != SSM_OK) return st;
+    if (shape->sequences == 0 || shape->nheads == 0) return SSM_OK;
+    SsdConvArgs a = ssdconv_args(*shape, p, xbc, delta, A, w, bias, Dskip, z, delta_bias, delta_softplus, slots, h, conv_state, y);
+    a.ws_x = static_cast<float *>(workspace);
+    log_call("ssdconv update sequences=%d H=%d P=%d N=%d G=%d W=%d dtype=%d: teams of %d lanes, %d workgroups a head", a.S, a.H,
+             a.P, a.N, a.G, a.W, shape->dtype, a.team, a.shares);
+    const hipError_t e = launch_ssdconv_token(a, shape->dtype == SSM_DTYPE_BF16, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? SSM_OK : hip_fail("ssdconv update launch", e);
+}

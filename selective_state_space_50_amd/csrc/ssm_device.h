@@ -172,6 +172,30 @@ struct RotaryArgs {
     uint64_t by_pairs, by_heads;     // ceil(2^32 / .): i / n = i by_n >> 32 for the small i of a turn
 };
 
+struct SsdConvArgs {
+    int64_t T;                       // rows of xbc (one token: sequences)
+    int S, H, P, N, G, W;            // sequences, heads, head dim, states, B/C groups, filter width (1..4)
+    int64_t C;                       // channels: H P + 2 G N
+    const void *xbc, *z, *delta;     // rows x_row, z_row, d_row elements apart
+    int64_t x_row, z_row, d_row;
+    const float *w, *bias, *A, *Dskip, *dbias;
+    const int32_t *offsets, *slots;  // [S + 1]; [S] or null (sequence s: slot s)
+    const uint8_t *fresh;            // [S] or null
+    int64_t nslots;
+    float *h;                        // [nslots, H, P, N]
+    void *conv_state;                // [nslots, C, W - 1]
+    void *y;                         // [T, H, P]
+    int softplus;
+    // set by the plan
+    int PB = 1, seg_len = 0;         // blocks of 64 channels; tokens of a segment (a multiple of 64)
+    int nseg_split = 0;              // sequences in segments, their states in ws_state
+    int64_t chunks = 0, items = 0;   // numbers of chunks and segments
+    int z_vec = 0, y_vec = 0, h_vec = 0;
+    int team = 1, shares = 1;        // one token: lanes of a row of states, workgroups of a head
+    uint16_t *ws_bt = nullptr, *ws_c = nullptr;   // operands of B and C in parts
+    float *ws_cb = nullptr, *ws_tab = nullptr, *ws_state = nullptr, *ws_dec = nullptr, *ws_x = nullptr;
+};
+
 struct ConvArgs {
     int64_t B, L, D;
     int W;                   // filter width (1..4)
@@ -378,6 +402,9 @@ hipError_t launch_linattn_update(const LinAttnArgs &a, bool bf16, hipStream_t s)
 // Group norm; vec: 16-byte loads (the groups' channels a multiple of 16 bytes).
 hipError_t launch_groupnorm_fwd(const GroupNormArgs &a, bool bf16, bool vec, hipStream_t s);
 hipError_t launch_groupnorm_bwd(const GroupNormArgs &a, bool bf16, bool vec, hipStream_t s);
+// The served Mamba-2 mixer: packed sequences, and one token of every sequence.
+hipError_t launch_ssdconv(const SsdConvArgs &a, bool bf16, hipStream_t s);
+hipError_t launch_ssdconv_token(const SsdConvArgs &a, bool bf16, hipStream_t s);
 // Rotary positions, and the norm of every head in front of them; vec: elements a load.
 hipError_t launch_rotary(const RotaryArgs &a, bool bf16, int vec, bool inter, bool norm, bool bwd, hipStream_t s);
 // Backward pass (dstate == 16, dim % 64 == 0).

@@ -1311,9 +1311,191 @@ int check_rotary(const ssm_rotary_shape *s, const void *q, const void *k, const 
     return SSM_OK;
 }
 
+// ---------------------------------------------------------------- the served Mamba-2 mixer
+
+int plan_ssdconv(const ssm_ssdconv_shape *s, bool token, SsdConvPlan *plan) {
+    if (!s) {
+        set_error("required pointer shape is NULL");
+        return SSM_EINVAL;
+    }
+    if (s->dtype != SSM_DTYPE_F32 && s->dtype != SSM_DTYPE_BF16) {
+        set_error("dtype=%d is neither SSM_DTYPE_F32 nor SSM_DTYPE_BF16", s->dtype);
+        return SSM_EINVAL;
+    }
+    if (s->tokens < 0 || s->sequences < 0 || s->nheads < 0 || s->nslots < 0 || s->max_seqlen < 0 || s->reserved != 0) {
+        set_error("negative size (tokens=%lld, sequences=%lld, nheads=%lld, nslots=%lld, max_seqlen=%lld) or reserved != 0",
+                  (long long)s->tokens, (long long)s->sequences, (long long)s->nheads, (long long)s->nslots,
+                  (long long)s->max_seqlen);
+        return SSM_EINVAL;
+    }
+    if (s->headdim < 1 || s->dstate < 1 || s->ngroups < 1 || s->nheads % s->ngroups != 0) {
+        set_error("headdim=%lld and dstate=%lld must be >= 1, ngroups=%lld >= 1 and divide nheads=%lld", (long long)s->headdim,
+                  (long long)s->dstate, (long long)s->ngroups, (long long)s->nheads);
+        return SSM_EINVAL;
+    }
+    if (s->width < 1 || s->width > 4) {
+        set_error("width=%lld is not between 1 and 4", (long long)s->width);
+        return SSM_EINVAL;
+    }
+    if (token && s->tokens != s->sequences) {
+        set_error("tokens=%lld must be sequences=%lld for one token each", (long long)s->tokens, (long long)s->sequences);
+        return SSM_EINVAL;
+    }
+    if (s->dstate > SSM_SSDCONV_MAX_DSTATE) {
+        set_error("dstate=%lld exceeds the supported maximum %d", (long long)s->dstate, SSM_SSDCONV_MAX_DSTATE);
+        return SSM_EUNSUPPORTED;
+    }
+    if (s->nheads > 65536 || s->headdim > 65536 || s->sequences > 65535 || s->tokens > (int64_t(1) << 28) ||
+        s->nslots > (int64_t(1) << 30) || s->nheads * s->headdim > (int64_t(1) << 24) || s->ngroups * s->dstate > (int64_t(1) << 22)) {
+        set_error("shape too large (tokens=%lld, sequences=%lld, nslots=%lld, nheads=%lld, headdim=%lld, ngroups=%lld)",
+                  (long long)s->tokens, (long long)s->sequences, (long long)s->nslots, (long long)s->nheads,
+                  (long long)s->headdim, (long long)s->ngroups);
+        return SSM_EUNSUPPORTED;
+    }
+    const int64_t inner = s->nheads * s->headdim;
+    plan->channels = inner + 2 * s->ngroups * s->dstate;
+    plan->x_row = s->x_row ? s->x_row : plan->channels;
+    plan->z_row = s->z_row ? s->z_row : inner;
+    plan->d_row = s->delta_row ? s->delta_row : s->nheads;
+    if (plan->x_row < plan->channels || plan->z_row < inner || plan->d_row < s->nheads) {
+        set_error("x_row=%lld, z_row=%lld or delta_row=%lld is shorter than a token's %lld, %lld and %lld values",
+                  (long long)s->x_row, (long long)s->z_row, (long long)s->delta_row, (long long)plan->channels,
+                  (long long)inner, (long long)s->nheads);
+        return SSM_EINVAL;
+    }
+    int64_t row = plan->x_row > plan->z_row ? plan->x_row : plan->z_row;
+    if (plan->d_row > row) row = plan->d_row;
+    if (s->tokens > 0 && row > kMaxElems / s->tokens) {
+        set_error("%lld tokens %lld elements apart are too large", (long long)s->tokens, (long long)row);
+        return SSM_EUNSUPPORTED;
+    }
+    if (s->sequences == 0 || s->nheads == 0) return SSM_OK;
+    const auto too_many = [&] {
+        set_error("%lld sequences of %lld heads of %lld channels over %lld tokens: too many workgroups for one launch",
+                  (long long)s->sequences, (long long)s->nheads, (long long)s->headdim, (long long)s->tokens);
+        return SSM_EUNSUPPORTED;
+    };
+    if (token) {
+        if (s->sequences * s->nheads > (int64_t(1) << 23)) return too_many();
+        plan->ws_bytes = static_cast<size_t>(s->sequences * plan->channels) * sizeof(float);
+        return SSM_OK;
+    }
+    plan->blocks64 = ceil_div(s->headdim, 64);
+    plan->chunks = s->tokens / 64 + s->sequences;
+    // Whole sequences, or segments of them: a sweep walks its chunks one after another, a workgroup to a CU at once.  A
+    // segment costs a second read of x for its own state (0.6 of a chunk's time, measured) and about three chunks' time
+    // for its start, and the pass between them about eight.
+    const int64_t across = s->nheads * plan->blocks64, all = ceil_div(s->tokens, 64);
+    int64_t longest = s->max_seqlen > 0 && s->max_seqlen < s->tokens ? s->max_seqlen : s->tokens;
+    longest = ceil_div(longest, 64);
+    const int64_t even = ceil_div(all * across, kCUs);
+    double best = static_cast<double>(longest > even ? longest : even);
+    plan->seg_len = kSsdConvWhole;
+    for (int64_t k = 2; k <= 64 && k <= longest; ++k) {
+        const int64_t len = ceil_div(longest, k);
+        if (len < 4) break;
+        const int64_t n = ceil_div(all, len) + (s->sequences - 1) / 2;    // (half a segment is lost to each further sequence)
+        const int64_t rounds = ceil_div(n * across, kCUs);
+        const double cost = static_cast<double>(rounds) * (1.6 * static_cast<double>(len) + 3.0) + 8.0;
+        if (cost < best) {
+            best = cost;
+            plan->seg_len = 64 * len;
+        }
+    }
+    plan->split = plan->seg_len != kSsdConvWhole;
+    plan->items = s->tokens / plan->seg_len + s->sequences;
+    if (plan->items > (int64_t(1) << 23) / across || plan->chunks > (int64_t(1) << 23)) return too_many();
+    const int64_t np = s->dstate > 64 ? 128 : 64, py = s->dtype == SSM_DTYPE_BF16 ? 2 : 3;
+    const int64_t cg = plan->chunks * s->ngroups;
+    if (plan->chunks * s->nheads > (int64_t(1) << 36) || cg > (int64_t(1) << 30)) return too_many();
+    size_t at = static_cast<size_t>(cg * 64 * np * 2 * 3);
+    auto take = [&](int64_t bytes) {
+        const size_t off = align_up(at, kWsAlign);
+        at = off + static_cast<size_t>(bytes);
+        return off;
+    };
+    plan->c_off = take(cg * 64 * np * 2 * py);
+    plan->cb_off = take(cg * 64 * 64 * 4);
+    plan->tab_off = take(plan->chunks * s->nheads * 6 * 64 * 4);
+    if (plan->split) {
+        plan->state_off = take(plan->items * inner * s->dstate * 4);
+        plan->dec_off = take(plan->items * s->nheads * 4);
+    }
+    plan->ws_bytes = at;
+    return SSM_OK;
+}
+
+int check_ssdconv(const ssm_ssdconv_shape *s, bool token, const void *xbc, const void *delta, const float *A, const float *w,
+                  const float *bias, const float *Dskip, const void *z, const float *delta_bias, int delta_softplus,
+                  const int32_t *offsets, const int32_t *slots, const uint8_t *fresh, const float *h, const void *conv_state,
+                  const void *y, const void *workspace, size_t workspace_bytes, SsdConvPlan *plan) {
+    int st = plan_ssdconv(s, token, plan);
+    if (st != SSM_OK) return st;
+    if (delta_softplus != 0 && delta_softplus != 1) {
+        set_error("delta_softplus=%d is neither 0 nor 1", delta_softplus);
+        return SSM_EINVAL;
+    }
+    if (s->sequences == 0 || s->nheads == 0) return SSM_OK;
+    const bool rows = s->tokens > 0, pool = s->nslots > 0;
+    const char *missing = rows && !xbc ? "xbc" : rows && !delta ? "delta" : !A ? "A" : !w ? "w" : !token && !offsets ? "offsets"
+                        : pool && !h ? "h" : pool && s->width > 1 && !conv_state ? "conv_state" : rows && !y ? "y" : nullptr;
+    if (missing) {
+        set_error("required pointer %s is NULL", missing);
+        return SSM_EINVAL;
+    }
+    const int64_t es = static_cast<int64_t>(dtype_size(s->dtype)), inner = s->nheads * s->headdim, H4 = s->nheads * 4;
+    const Range all[] = {range("xbc", xbc, token_bytes(s->tokens, plan->x_row, plan->channels, es)),
+                         range("delta", delta, token_bytes(s->tokens, plan->d_row, s->nheads, es)),
+                         range("z", z, token_bytes(s->tokens, plan->z_row, inner, es)),
+                         range("conv_state", conv_state, s->nslots * plan->channels * (s->width - 1) * es),
+                         range("y", y, s->tokens * inner * es),
+                         range("A", A, H4), range("w", w, plan->channels * s->width * 4),
+                         range("bias", bias, plan->channels * 4), range("Dskip", Dskip, H4),
+                         range("delta_bias", delta_bias, H4), range("offsets", offsets, (s->sequences + 1) * 4),
+                         range("slots", slots, s->sequences * 4), range("h", h, s->nslots * inner * s->dstate * 4),
+                         range("workspace", workspace, static_cast<int64_t>(plan->ws_bytes)),
+                         range("fresh", fresh, s->sequences)};
+    st = check_element(all, 5, static_cast<uintptr_t>(es));
+    if (st == SSM_OK) st = check_element(all + 5, 8, 4);
+    if (st == SSM_OK) st = check_element(all + 13, 1, 16);
+    if (st != SSM_OK) return st;
+    const Range outs[] = {all[3], all[4], all[12], all[13]};
+    st = check_no_overlap(outs, 4, all, 15);
+    if (st != SSM_OK) return st;
+    if (plan->ws_bytes > 0 && (!workspace || workspace_bytes < plan->ws_bytes)) {
+        set_error("workspace of %zu bytes given, %zu needed", workspace ? workspace_bytes : (size_t)0, plan->ws_bytes);
+        return SSM_EWORKSPACE;
+    }
+    const auto on16 = [](const Range &r) { return r.lo % 16 == 0; };
+    plan->z_vec = s->headdim % 8 == 0 && on16(all[2]) && plan->z_row * es % 16 == 0;
+    plan->y_vec = s->headdim % 8 == 0 && on16(all[4]);
+    plan->h_vec = s->dstate % 4 == 0 && on16(all[12]);
+    if (token) {
+        // lanes of a row of states: four states each, or two single ones; and so many workgroups to a head that two are
+        // there for every CU
+        const int64_t lanes = ceil_div(s->dstate, plan->h_vec ? 4 : 2);
+        while (plan->team < lanes) plan->team *= 2;
+        const int64_t most = ceil_div(s->headdim, 256 / plan->team), want = ceil_div(2 * kCUs, s->sequences * s->nheads);
+        plan->shares = static_cast<int>(want < most ? want : most);
+    }
+    return SSM_OK;
+}
+
 }  // namespace ssm
 
 extern "C" {
+
+size_t ssm_ssdconv_workspace_bytes(const ssm_ssdconv_shape *shape) {
+    ssm::clear_error();
+    ssm::SsdConvPlan p;
+    return ssm::plan_ssdconv(shape, false, &p) == SSM_OK ? p.ws_bytes : 0;
+}
+
+size_t ssm_ssdconv_update_workspace_bytes(const ssm_ssdconv_shape *shape) {
+    ssm::clear_error();
+    ssm::SsdConvPlan p;
+    return ssm::plan_ssdconv(shape, true, &p) == SSM_OK ? p.ws_bytes : 0;
+}
 
 size_t ssm_qknorm_bwd_workspace_bytes(const ssm_rotary_shape *shape) {
     ssm::clear_error();

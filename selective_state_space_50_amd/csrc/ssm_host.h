@@ -206,6 +206,24 @@ int check_groupnorm_bwd(int64_t batch, int64_t seqlen, int64_t dim, int64_t grou
                         const float *rstd, const void *dx, const float *dw, const float *dbias, const void *dz,
                         const void *workspace, size_t workspace_bytes, GroupNormPlan *plan);
 
+// The served Mamba-2 mixer: how sequences are split and what the workspace holds (see ssdconv.hip).
+struct SsdConvPlan {
+    int64_t x_row = 0, z_row = 0, d_row = 0, channels = 0;
+    int64_t blocks64 = 1;             // blocks of 64 channels of a head
+    int64_t chunks = 0, items = 0;    // numbers of chunks and segments
+    int64_t seg_len = 0;
+    bool split = false;
+    bool z_vec = false, y_vec = false, h_vec = false;
+    int team = 1, shares = 1;
+    size_t c_off = 0, cb_off = 0, tab_off = 0, state_off = 0, dec_off = 0, ws_bytes = 0;
+};
+constexpr int64_t kSsdConvWhole = int64_t(1) << 30;   // seg_len of sequences that are not split
+int plan_ssdconv(const ssm_ssdconv_shape *s, bool token, SsdConvPlan *plan);
+int check_ssdconv(const ssm_ssdconv_shape *s, bool token, const void *xbc, const void *delta, const float *A, const float *w,
+                  const float *bias, const float *Dskip, const void *z, const float *delta_bias, int delta_softplus,
+                  const int32_t *offsets, const int32_t *slots, const uint8_t *fresh, const float *h, const void *conv_state,
+                  const void *y, const void *workspace, size_t workspace_bytes, SsdConvPlan *plan);
+
 // Rotary positions and head norms: how rows are held (see rotary.hip).
 struct RotaryPlan {
     int64_t q_row = 0, k_row = 0;
