@@ -132,6 +132,16 @@ struct Sequence {
 template <class T, int K>
 struct Window {
     T x[K + 3];
+    // (t0 >= 3: rows one after another, the last one again behind the end)
+    __device__ __forceinline__ void load_on(const SsdConvArgs &a, const Sequence &q, int channel, int t0) {
+        int t = t0 - 3 < q.len - 1 ? t0 - 3 : q.len - 1;
+        const T *X = static_cast<const T *>(a.xbc) + (q.first + static_cast<int64_t>(t)) * a.x_row;
+#pragma unroll
+        for (int i = 0; i < K + 3; ++i, ++t) {
+            x[i] = X[channel];
+            X += t < q.len - 1 ? a.x_row : 0;
+        }
+    }
     __device__ void load(const SsdConvArgs &a, const Sequence &q, int channel, int t0) {
         const T *X = static_cast<const T *>(a.xbc) + channel;
 #pragma unroll
@@ -303,7 +313,8 @@ __global__ void __launch_bounds__(kThreads) ssdconv_prep_kernel(SsdConvArgs a) {
 
 // ---------------------------------------------------------------------------- sweep
 
-// 16-byte units of a row of LDS are swapped by its number, so that lanes that read a column of rows meet all banks
+// 16-byte units of a row of LDS are swapped by its number, so that lanes that read a column of rows meet all banks.
+// (unit ^ number: where unit is 4 kk + lg, the place for kk is that for 0 with the bits of 4 kk turned over.)
 __device__ __forceinline__ int at_x(int p, int unit) { return p * kQ + ((unit ^ (((p >> 3) & 3) << 1 | ((p >> 1) & 1))) << 3); }
 __device__ __forceinline__ int at_w(int p, int unit) { return p * kQ + ((unit ^ ((p >> 1) & 7)) << 3); }
 template <int NP>
@@ -315,18 +326,21 @@ __device__ __forceinline__ int at_s(int p, int unit) {
 template <int NP, int PY>
 struct SweepLds {
     static constexpr int kStates = PY == 3 && NP == 128 ? 1 : 2;   // (two copies of the state's parts where they fit)
-    uint16_t xt[2][PY][kQ * kQ];        // x behind the convolution: [channel][token]
-    uint16_t xw[2][kPS][kQ * kQ];       // the same, weighted for the state
+    uint16_t xw[2][kPS][kQ * kQ];       // x behind the convolution, weighted for the state: [channel][token]
+    float tab[3][kTabs][kQ];
+    uint16_t xt[2][PY][kQ * kQ];        // x behind the convolution
     uint16_t st[kStates][PY][kQ * NP];  // the chunk's start state: [channel][state]
-    float tab[2][kTabs][kQ];
     int bad[3];                         // whether a chunk's x has a NaN or infinity
     int first_bad[2][8][kQ];            // and where: [wave][channel] the first such token (64: none)
 };
 struct StateLds {
     uint16_t xw[2][kPS][kQ * kQ];
+    float tab[3][kTabs][kQ];
 };
 
-template <class T, int NP, int PY, bool OWN>   // OWN: the segments' own end states, nothing else
+// OWN: the segments' own end states, nothing else.  VEC: z and y in 16-byte pieces (headdim a multiple of 8, and so their
+// addresses; the masks of single elements, 64 lanes' worth in a register pair each, spilled the scalar registers)
+template <class T, int NP, int PY, bool OWN, bool VEC>
 __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) {
     typedef SweepLds<NP, PY> Lds;
     __shared__ __align__(16) typename std::conditional<OWN, StateLds, Lds>::type sm;
@@ -384,62 +398,81 @@ __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) 
         }
     };
 
+    // Every operand's pointer is a lane's own and moves by a chunk (scalar bases for all of them spilled).
     // ---- staging: thread (channel lane, tokens 8 wv .. 8 wv + 7)
     const bool mine = lane < np;
     const int channel = h * a.P + p0 + (mine ? lane : 0);
     float fw[4], fbias;
     filter(a, channel, fw, fbias);
     Window<T, 8> win;
-    auto load_x = [&](int c) __attribute__((always_inline)) { win.load(a, q, channel, begin + c * kQ + 8 * wv); };
-    f4 tq = {0.0f, 0.0f, 0.0f, 0.0f};
-    auto tab_at = [&](int c) { return a.ws_tab + ((u0 + c) * a.H + h) * (kTabs * kQ); };
-    auto load_tab = [&](int c) __attribute__((always_inline)) {
-        if constexpr (!OWN)
-            if (threadIdx.x < kTabs * kQ / 4) tq = *reinterpret_cast<const f4 *>(tab_at(c) + 4 * threadIdx.x);
+    int t_x = begin + 8 * wv;                        // first token of the next chunk to load
+    auto load_x = [&]() __attribute__((always_inline)) {
+        win.load_on(a, q, channel, t_x);
+        t_x += kQ;
+    };
+    const float *tab_p = a.ws_tab + (u0 * a.H + h) * (kTabs * kQ) + 4 * (threadIdx.x < kTabs * kQ / 4 ? threadIdx.x : 0);
+    f4 tq;
+    int tabs = nch;                                  // tables still to load
+    auto load_tab = [&]() __attribute__((always_inline)) {
+        tq = *reinterpret_cast<const f4 *>(tab_p);
+        tab_p += --tabs > 0 ? static_cast<int64_t>(a.H) * (kTabs * kQ) : 0;
+    };
+    auto put_tab = [&](int c) __attribute__((always_inline)) {
+        if (threadIdx.x < kTabs * kQ / 4) *reinterpret_cast<f4 *>(&sm.tab[c % 3][0][0] + 4 * threadIdx.x) = tq;
     };
     auto stage = [&](int c) __attribute__((always_inline)) {
-        const int b = c & 1, t0 = begin + c * kQ + 8 * wv;
+        const int b = c & 1, left = end - begin - c * kQ - 8 * wv;     // tokens there are
         float o[8];
         convolve(win, fw, fbias, a.W, o);
+        if (left < 8 || np < kQ) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (!mine || t0 + i >= end) o[i] = 0.0f;
-        const float *wr = tab_at(c) + kWr * kQ + 8 * wv;     // (wave-uniform: scalar loads)
+            for (int i = 0; i < 8; ++i)
+                if (!mine || i >= left) o[i] = 0.0f;
+        }
+        const f4 w0 = *reinterpret_cast<const f4 *>(&sm.tab[c % 3][kWr][8 * wv]);
+        const f4 w1 = *reinterpret_cast<const f4 *>(&sm.tab[c % 3][kWr][8 * wv + 4]);
         float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = o[i] * wr[i];
+        for (int i = 0; i < 8; ++i) v[i] = o[i] * (i < 4 ? w0[i & 3] : w1[i & 3]);
         s8 part[kPS];
         split8<kPS>(v, part);
 #pragma unroll
         for (int k = 0; k < kPS; ++k) *reinterpret_cast<s8 *>(&sm.xw[b][k][at_w(lane, wv)]) = part[k];
         if constexpr (!OWN) {
             // A NaN or infinity of x must not meet the zeros above the diagonal: it is taken out here, and y gets
-            // NaN from its token on (through the state, from the next chunk on, all by itself).
-            int first = kQ;
+            // NaN from its token on (through the state, from the next chunk on, all by itself).  (The sum of eight
+            // times zero is not zero where one of them is such a value.)
+            float z = 0.0f;
 #pragma unroll
-            for (int i = 7; i >= 0; --i)
-                if (!(__builtin_fabsf(o[i]) <= 3.4028234663852886e38f)) {
-                    first = 8 * wv + i;
-                    o[i] = 0.0f;
-                }
+            for (int i = 0; i < 8; ++i) z = __builtin_fmaf(o[i], 0.0f, z);
+            int first = kQ;
+            if (__any(z != 0.0f)) {
+#pragma unroll
+                for (int i = 7; i >= 0; --i)
+                    if (!(__builtin_fabsf(o[i]) <= 3.4028234663852886e38f)) {
+                        first = 8 * wv + i;
+                        o[i] = 0.0f;
+                    }
+                if (first < kQ) sm.bad[c % 3] = 1;
+            }
             sm.first_bad[b][wv][lane] = first;
-            if (first < kQ) sm.bad[c % 3] = 1;
             s8 y[PY];
             split8<PY>(o, y);
 #pragma unroll
             for (int k = 0; k < PY; ++k) *reinterpret_cast<s8 *>(&sm.xt[b][k][at_x(lane, wv)]) = y[k];
-            if (threadIdx.x < kTabs * kQ / 4) *reinterpret_cast<f4 *>(&sm.tab[b][0][0] + 4 * threadIdx.x) = tq;
         }
     };
 
     // ---- operands of B (the wave's 16 states)
     s8 bf[2][kPS];
-    auto load_b = [&](int c) __attribute__((always_inline)) {
-        const s8 *p = reinterpret_cast<const s8 *>(a.ws_bt) + (((u0 + c) * a.G + g) * (NP / 16) + sl) * (2 * kPS * 64) + lane;
+    const s8 *b_p = reinterpret_cast<const s8 *>(a.ws_bt) + ((u0 * a.G + g) * (NP / 16) + sl) * (2 * kPS * 64) + lane;
+    const int64_t b_step = static_cast<int64_t>(a.G) * (NP / 16 * 2 * kPS * 64);
+    auto load_b = [&](bool more) __attribute__((always_inline)) {
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-            for (int k = 0; k < kPS; ++k) bf[ks][k] = p[(ks * kPS + k) * 64];
+            for (int k = 0; k < kPS; ++k) bf[ks][k] = b_p[(ks * kPS + k) * 64];
+        b_p += more ? b_step : 0;
     };
 
     // ---- outputs: wave (i, ph) has tokens 16 i + lr and, of the channels 32 ph .., 8 lg .. 8 lg + 7
@@ -447,73 +480,70 @@ __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) 
     const int t_l = 16 * i + lr, out_p = 32 * ph + 8 * lg;
     const float dsk = a.Dskip ? a.Dskip[h] : 0.0f;
     s8 cf[NP / 32][PY];
-    auto load_c = [&](int c) __attribute__((always_inline)) {
-        const s8 *p = reinterpret_cast<const s8 *>(a.ws_c) + (((u0 + c) * a.G + g) * 4 + i) * (NP / 32 * PY * 64) + lane;
+    const s8 *c_p = reinterpret_cast<const s8 *>(a.ws_c) + ((u0 * a.G + g) * 4 + i) * (NP / 32 * PY * 64) + lane;
+    const int64_t c_step = static_cast<int64_t>(a.G) * (4 * NP / 32 * PY * 64);
+    auto load_c = [&](bool more) __attribute__((always_inline)) {
 #pragma unroll
         for (int kk = 0; kk < NP / 32; ++kk)
 #pragma unroll
-            for (int k = 0; k < PY; ++k) cf[kk][k] = p[(kk * PY + k) * 64];
+            for (int k = 0; k < PY; ++k) cf[kk][k] = c_p[(kk * PY + k) * 64];
+        c_p += more ? c_step : 0;
     };
-    f4 cb[2][2];
-    auto load_cb = [&](int c) __attribute__((always_inline)) {
-        const float *p = a.ws_cb + (((u0 + c) * a.G + g) * kQ + t_l) * kQ + 8 * lg;
+    // s <= t of the block on the diagonal as all bits or none, and D where s = t, for the lane's eight s
+    uint32_t below[8];
+    float diag[8];
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
-            if (ks <= i >> 1) {
-                cb[ks][0] = *reinterpret_cast<const f4 *>(p + 32 * ks);
-                cb[ks][1] = *reinterpret_cast<const f4 *>(p + 32 * ks + 4);
-            }
+    for (int e = 0; e < 8; ++e) {
+        const int d = t_l - (32 * (i >> 1) + 8 * lg + e);
+        below[e] = static_cast<uint32_t>(~(d >> 31));
+        diag[e] = d == 0 ? dsk : 0.0f;
+    }
+    f4 cb[2][2];
+    const float *cb_p = a.ws_cb + ((u0 * a.G + g) * kQ + t_l) * kQ + 8 * lg;
+    auto load_cb = [&](bool more) __attribute__((always_inline)) {
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {     // (what lies above the diagonal is not used)
+            cb[ks][0] = *reinterpret_cast<const f4 *>(cb_p + 32 * ks);
+            cb[ks][1] = *reinterpret_cast<const f4 *>(cb_p + 32 * ks + 4);
+        }
+        cb_p += more ? static_cast<int64_t>(a.G) * (kQ * kQ) : 0;
     };
     T zq[8];
-    auto load_z = [&](int c) __attribute__((always_inline)) {
-        const int t = begin + c * kQ + t_l;
-        if (!a.z || t >= end || out_p >= np) return;
-        const T *p = static_cast<const T *>(a.z) + (q.first + static_cast<int64_t>(t)) * a.z_row + h * a.P + p0 + out_p;
-        if (a.z_vec) {
+    const T *z_p = a.z ? static_cast<const T *>(a.z) + h * a.P + p0 + (out_p < np ? out_p : 0) : nullptr;
+    int t_z = begin + t_l;
+    auto load_z = [&]() __attribute__((always_inline)) {
+        if (!z_p) return;
+        const T *z = z_p + (q.first + static_cast<int64_t>(t_z < end ? t_z : end - 1)) * a.z_row;   // (a row that is there)
+        t_z += kQ;
+        if constexpr (VEC) {
 #pragma unroll
             for (int k = 0; k < 8; k += 16 / static_cast<int>(sizeof(T)))
-                *reinterpret_cast<u4 *>(zq + k) = *reinterpret_cast<const u4 *>(p + k);
+                *reinterpret_cast<u4 *>(zq + k) = *reinterpret_cast<const u4 *>(z + k);
         } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (out_p + k < np) zq[k] = p[k];
+            for (int k = 0; k < 8; ++k) zq[k] = z[out_p + k < np ? k : 0];
         }
     };
+    // Places of this lane's operands in LDS; within the loop they are made new for each chunk (kept, as the compiler would
+    // have it, each of the twenty takes a register, and the registers spill)
+    int st_at = at_s<NP>(32 * ph + 8 * (lr >> 2) + (lr & 3), lg), xt_at = at_x(32 * ph + 8 * (lr >> 2) + (lr & 3), lg);
+    int xw_at = at_w(16 * pt0 + lr, lg);
+    auto fresh = [](int v) __attribute__((always_inline)) {
+        asm volatile("" : "+v"(v));
+        return v;
+    };
+    T *y_p = static_cast<T *>(a.y) + ((q.first + static_cast<int64_t>(begin) + t_l) * a.H + h) * a.P + p0 + out_p;
+    const int64_t y_step = static_cast<int64_t>(kQ) * a.H * a.P;
 
-    if (nch > 0) {
-        load_x(0);
-        load_tab(0);
-        load_b(0);
+    // the outputs of chunk c
+    auto outputs = [&](int c, bool more) __attribute__((always_inline)) {
         if constexpr (!OWN) {
-            if (threadIdx.x < 3) sm.bad[threadIdx.x] = 0;
-            load_c(0);
-            load_cb(0);
-            load_z(0);
-            put_state(0);
-            __syncthreads();
-        }
-        stage(0);
-        if (nch > 1) {
-            load_x(1);
-            load_tab(1);
-        }
-        __syncthreads();
-    }
-    float whole = 1.0f;      // decay over the segment
-    for (int c = 0; c < nch; ++c) {
-        const int b = c & 1;
-        const bool more = c + 1 < nch;
-        float dec;
-        if constexpr (OWN) {
-            dec = tab_at(c)[kE * kQ + kQ - 1];
-            whole *= dec;
-        } else {
-            dec = sm.tab[b][kE][kQ - 1];
-            if (threadIdx.x == 0) sm.bad[(c + 2) % 3] = 0;
-            const int sb = Lds::kStates == 2 ? b : 0;
+            const int b = c & 1, sb = Lds::kStates == 2 ? b : 0;
+            const float(&tab)[kTabs][kQ] = sm.tab[c % 3];
             const bool on = 32 * ph < np;
             f4 acc[2] = {};
             if (on) {
+                const int at = fresh(st_at + sb * (PY * kQ * NP));
                 // the carried state's share.  Row r of tile k is channel 32 ph + 8 (r / 4) + 4 k + r % 4, so that a lane
                 // gets eight channels side by side
 #pragma unroll
@@ -521,37 +551,36 @@ __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) 
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         s8 sf[PY];
-                        const int p = 32 * ph + 8 * (lr >> 2) + 4 * k + (lr & 3);
 #pragma unroll
-                        for (int e = 0; e < PY; ++e) sf[e] = *reinterpret_cast<const s8 *>(&sm.st[sb][e][at_s<NP>(p, 4 * kk + lg)]);
+                        for (int e = 0; e < PY; ++e) sf[e] = *reinterpret_cast<const s8 *>(&sm.st[0][e][0] + ((at ^ 32 * kk) + 4 * NP * k));
                         acc[k] = product<PY>(sf, cf[kk], acc[k]);
                     }
-                const float e = sm.tab[b][kE][t_l];
+                const float e = tab[kE][t_l];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) acc[k] *= e;
             }
-            if (more) load_c(c + 1);
+            load_c(more);
             if (on) {
                 // the chunk's own share: (C_t . B_s) decayed, D on the diagonal, times x
+                const int at = fresh(xt_at + b * (PY * kQ * kQ));
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks) {
                     if (ks > i >> 1) continue;
                     float v[8];
                     const int s0 = 32 * ks + 8 * lg;
-                    const f4 d0 = *reinterpret_cast<const f4 *>(&sm.tab[b][ks == i >> 1 ? kDt : kWb][s0]);
-                    const f4 d1 = *reinterpret_cast<const f4 *>(&sm.tab[b][ks == i >> 1 ? kDt : kWb][s0 + 4]);
+                    const f4 d0 = *reinterpret_cast<const f4 *>(&tab[ks == i >> 1 ? kDt : kWb][s0]);
+                    const f4 d1 = *reinterpret_cast<const f4 *>(&tab[ks == i >> 1 ? kDt : kWb][s0 + 4]);
                     if (ks == i >> 1) {
-                        const f4 c0 = *reinterpret_cast<const f4 *>(&sm.tab[b][kC32][s0]);
-                        const f4 c1 = *reinterpret_cast<const f4 *>(&sm.tab[b][kC32][s0 + 4]);
-                        const float ct = sm.tab[b][kC32][t_l];
+                        const f4 c0 = *reinterpret_cast<const f4 *>(&tab[kC32][s0]);
+                        const f4 c1 = *reinterpret_cast<const f4 *>(&tab[kC32][s0 + 4]);
+                        const float ct = tab[kC32][t_l];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             const float f = __builtin_amdgcn_exp2f(ct - (e < 4 ? c0[e & 3] : c1[e & 3])) * (e < 4 ? d0[e & 3] : d1[e & 3]);
-                            v[e] = s0 + e <= t_l ? cb[ks][e >> 2][e & 3] * f : 0.0f;
-                            if (s0 + e == t_l) v[e] += dsk;
+                            v[e] = __uint_as_float(__float_as_uint(cb[ks][e >> 2][e & 3] * f) & below[e]) + diag[e];
                         }
                     } else {
-                        const float et = sm.tab[b][kEin][t_l];
+                        const float et = tab[kEin][t_l];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) v[e] = cb[ks][e >> 2][e & 3] * (et * (e < 4 ? d0[e & 3] : d1[e & 3]));
                     }
@@ -560,68 +589,112 @@ __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) 
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         s8 xf[PY];
-                        const int p = 32 * ph + 8 * (lr >> 2) + 4 * k + (lr & 3);
 #pragma unroll
-                        for (int e = 0; e < PY; ++e) xf[e] = *reinterpret_cast<const s8 *>(&sm.xt[b][e][at_x(p, 4 * ks + lg)]);
+                        for (int e = 0; e < PY; ++e) xf[e] = *reinterpret_cast<const s8 *>(&sm.xt[0][e][0] + ((at ^ 32 * ks) + 4 * kQ * k));
                         acc[k] = product<PY>(xf, m, acc[k]);
                     }
                 }
             }
-            if (more) load_cb(c + 1);
-            const int t = begin + c * kQ + t_l;
-            if (on && t < end && out_p < np) {
+            load_cb(more);
+            if (on && begin + c * kQ + t_l < end && out_p < np) {
                 float y[8] = {acc[0][0], acc[0][1], acc[0][2], acc[0][3], acc[1][0], acc[1][1], acc[1][2], acc[1][3]};
                 if (sm.bad[c % 3]) {
                     for (int k = 0; k < 8; ++k)
                         for (int o = 0; o < 8; ++o)
                             if (sm.first_bad[b][o][out_p + k] <= t_l) y[k] = __builtin_nanf("");
                 }
-                if (a.z) {
+                if (z_p) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) y[k] *= silu_f(widen_v(zq[k]));
                 }
-                T *out = static_cast<T *>(a.y) + ((q.first + static_cast<int64_t>(t)) * a.H + h) * a.P + p0 + out_p;
-                if (a.y_vec) {
+                if constexpr (VEC) {
                     if constexpr (sizeof(T) == 2)
-                        *reinterpret_cast<u4 *>(out) = u4{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])};
+                        *reinterpret_cast<u4 *>(y_p) = u4{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])};
                     else
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) *reinterpret_cast<f4 *>(out + 4 * k) = f4{y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]};
+                        for (int k = 0; k < 2; ++k) *reinterpret_cast<f4 *>(y_p + 4 * k) = f4{y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]};
                 } else {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        if (out_p + k < np) put(out, k, y[k]);
+                        if (out_p + k < np) put(y_p, k, y[k]);
                 }
             }
-            if (more) load_z(c + 1);
-            if constexpr (Lds::kStates == 1) __syncthreads();   // the old state's parts are read
+            y_p += y_step;
+            load_z();
         }
-        // ---- the state passed on
+    };
+    float whole = 1.0f;      // decay over the segment
+    // the state behind chunk c
+    auto advance = [&](int c, bool more) __attribute__((always_inline)) {
+        const float dec = sm.tab[c % 3][kE][kQ - 1];
+        if constexpr (OWN) whole *= dec;
+        const int at = fresh(xw_at + (c & 1) * (kPS * kQ * kQ));
 #pragma unroll
         for (int j = 0; j < kPT; ++j) {
             if (16 * (pt0 + j) >= np) continue;
             f4 acc = S[j] * dec;
-            const int p = 16 * (pt0 + j) + lr;
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
                 s8 xf[kPS];
 #pragma unroll
-                for (int k = 0; k < kPS; ++k) xf[k] = *reinterpret_cast<const s8 *>(&sm.xw[b][k][at_w(p, 4 * ks + lg)]);
+                for (int k = 0; k < kPS; ++k) xf[k] = *reinterpret_cast<const s8 *>(&sm.xw[0][k][0] + ((at ^ 32 * ks) + 16 * kQ * j));
                 acc = product<kPS>(bf[ks], xf, acc);
             }
             S[j] = acc;
         }
+        load_b(more);
+    };
+    // chunk c + 1 into LDS, chunk c + 2 on its way
+    auto next = [&](int c, bool more) __attribute__((always_inline)) {
         if (more) {
-            load_b(c + 1);
-            if constexpr (!OWN) put_state(Lds::kStates == 2 ? b ^ 1 : 0);
             stage(c + 1);
-            if (c + 2 < nch) {
-                load_x(c + 2);
-                load_tab(c + 2);
-            }
+            put_tab(c + 2);
+        }
+        load_x();
+        load_tab();
+    };
+
+    // Every chunk issues the same loads in the same order, the last ones again where there are no more: a wait for one of
+    // them then leaves the later ones in flight.  (Loads in branches were waited for all together, at the top of each chunk.)
+    if (nch > 0) {
+        win.load(a, q, channel, t_x);
+        t_x += kQ;
+        load_tab();
+        put_tab(0);
+        load_tab();
+        load_b(nch > 1);
+        if constexpr (!OWN) {
+            if (threadIdx.x < 3) sm.bad[threadIdx.x] = 0;
+            load_c(nch > 1);
+            load_cb(nch > 1);
+            load_z();
+            put_state(0);
+        }
+        put_tab(1);
+        __syncthreads();
+        stage(0);
+        load_x();
+        load_tab();
+        __syncthreads();
+    }
+    // A SIMD's two waves take the chunk's work in opposite order: one stages (VALU) while the other multiplies.
+    constexpr bool kOne = !OWN && Lds::kStates == 1;
+    auto chunks = [&](auto first) __attribute__((always_inline)) {
+        constexpr bool kStageFirst = decltype(first)::value;
+        for (int c = 0; c < nch; ++c) {
+            const bool more = c + 1 < nch, more2 = c + 2 < nch;
+            if constexpr (!OWN)
+                if (threadIdx.x == 0) sm.bad[(c + 2) % 3] = 0;
+            if constexpr (kStageFirst) next(c, more);
+            outputs(c, more2);
+            if constexpr (kOne) __syncthreads();   // the old state's parts are read
+            advance(c, more2);
+            if (more) put_state(kOne ? 0 : (c & 1) ^ 1);
+            if constexpr (!kStageFirst) next(c, more);
             __syncthreads();
         }
-    }
+    };
+    chunks(std::false_type{});
 
     // ---- end states
     float *to = OWN ? a.ws_state + (item * a.H + h) * a.P * a.N
@@ -795,7 +868,7 @@ hipError_t prompts(const SsdConvArgs &a, hipStream_t s) {
     if (e != hipSuccess) return e;
     const dim3 grid(static_cast<unsigned>((a.items * a.H * a.PB + 7) / 8 * 8));
     if (a.nseg_split) {
-        hipLaunchKernelGGL((ssdconv_sweep_kernel<T, NP, PY, true>), grid, dim3(kThreads), 0, s, a);
+        hipLaunchKernelGGL((ssdconv_sweep_kernel<T, NP, PY, true, false>), grid, dim3(kThreads), 0, s, a);
         e = launch_status(s);
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL(ssdconv_join_kernel, dim3(static_cast<unsigned>((a.P * a.N + 255) / 256), static_cast<unsigned>(a.H),
@@ -803,7 +876,8 @@ hipError_t prompts(const SsdConvArgs &a, hipStream_t s) {
         e = launch_status(s);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((ssdconv_sweep_kernel<T, NP, PY, false>), grid, dim3(kThreads), 0, s, a);
+    if (a.y_vec && (a.z_vec || !a.z)) hipLaunchKernelGGL((ssdconv_sweep_kernel<T, NP, PY, false, true>), grid, dim3(kThreads), 0, s, a);
+    else hipLaunchKernelGGL((ssdconv_sweep_kernel<T, NP, PY, false, false>), grid, dim3(kThreads), 0, s, a);
     e = launch_status(s);
     if (e != hipSuccess || !a.nseg_split || a.W == 1) return e;
     hipLaunchKernelGGL((ssdconv_conv_state_kernel<T>), dim3(static_cast<unsigned>((a.C + 255) / 256), static_cast<unsigned>(a.S)),
