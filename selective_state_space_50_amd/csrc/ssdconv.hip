@@ -69,6 +69,7 @@ __device__ __forceinline__ f4 product(const s8 (&a)[N], const s8 (&b)[N], f4 c) 
 // v[0 .. K - 1] in N bf16 parts, two to a word: part n's words at w[n]
 template <int N, int K>
 __device__ __forceinline__ void split(const float *v, uint32_t (&w)[N][K / 2]) {
+#pragma clang fp contract(off)   // (the parts of v as it was rounded, wherever it comes from)
 #pragma unroll
     for (int i = 0; i < K / 2; ++i) {
         float a = v[2 * i], b = v[2 * i + 1];
@@ -165,14 +166,14 @@ struct Window {
     }
 };
 
-// silu of the convolution over a window: o[0 .. K - 1] (a filter of W < 4 columns leaves the earliest rows out)
-template <class T, int K>
+// silu of the convolution over a window: o[0 .. K - 1] (a filter of W < 4 columns leaves the earliest rows out; FULL: W is 4)
+template <bool FULL, class T, int K>
 __device__ __forceinline__ void convolve(const Window<T, K> &in, const float (&w)[4], float bias, int W, float *o) {
 #pragma unroll
     for (int i = 0; i < K; ++i) o[i] = bias;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-        if (k >= 4 - W) {
+        if (FULL || k >= 4 - W) {
 #pragma unroll
             for (int i = 0; i < K; ++i) o[i] = __builtin_fmaf(w[k], widen_v(in.x[i + k]), o[i]);
         }
@@ -265,7 +266,7 @@ __global__ void __launch_bounds__(kThreads) ssdconv_prep_kernel(SsdConvArgs a) {
         if (n < a.N) {
             Window<T, 16> in;
             in.load(a, q, channel, t0 + from + r);
-            convolve(in, w, bias, a.W, o);
+            convolve<false>(in, w, bias, a.W, o);
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -338,9 +339,12 @@ struct StateLds {
     float tab[3][kTabs][kQ];
 };
 
-// OWN: the segments' own end states, nothing else.  VEC: z and y in 16-byte pieces (headdim a multiple of 8, and so their
-// addresses; the masks of single elements, 64 lanes' worth in a register pair each, spilled the scalar registers)
-template <class T, int NP, int PY, bool OWN, bool VEC>
+// OWN: the segments' own end states, nothing else.  FAST: z and y in 16-byte pieces (headdim a multiple of 8, and so their
+// addresses; the masks of single elements, 64 lanes' worth in a register pair each, spill the scalar registers) and a
+// filter of four columns.  The chunk's work is one block of code, so that products, LDS and VALU overlap within a wave;
+// what would branch is done for nothing instead (channels behind the head's last, tokens behind the sequence's: their
+// weights are zero and their outputs are not stored).
+template <class T, int NP, int PY, bool OWN, bool FAST>
 __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) {
     typedef SweepLds<NP, PY> Lds;
     __shared__ __align__(16) typename std::conditional<OWN, StateLds, Lds>::type sm;
@@ -421,14 +425,9 @@ __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) 
         if (threadIdx.x < kTabs * kQ / 4) *reinterpret_cast<f4 *>(&sm.tab[c % 3][0][0] + 4 * threadIdx.x) = tq;
     };
     auto stage = [&](int c) __attribute__((always_inline)) {
-        const int b = c & 1, left = end - begin - c * kQ - 8 * wv;     // tokens there are
+        const int b = c & 1;
         float o[8];
-        convolve(win, fw, fbias, a.W, o);
-        if (left < 8 || np < kQ) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (!mine || i >= left) o[i] = 0.0f;
-        }
+        convolve<FAST>(win, fw, fbias, a.W, o);
         const f4 w0 = *reinterpret_cast<const f4 *>(&sm.tab[c % 3][kWr][8 * wv]);
         const f4 w1 = *reinterpret_cast<const f4 *>(&sm.tab[c % 3][kWr][8 * wv + 4]);
         float v[8];
@@ -439,6 +438,10 @@ __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) 
 #pragma unroll
         for (int k = 0; k < kPS; ++k) *reinterpret_cast<s8 *>(&sm.xw[b][k][at_w(lane, wv)]) = part[k];
         if constexpr (!OWN) {
+            s8 y[PY];
+            split8<PY>(o, y);
+#pragma unroll
+            for (int k = 0; k < PY; ++k) *reinterpret_cast<s8 *>(&sm.xt[b][k][at_x(lane, wv)]) = y[k];
             // A NaN or infinity of x must not meet the zeros above the diagonal: it is taken out here, and y gets
             // NaN from its token on (through the state, from the next chunk on, all by itself).  (The sum of eight
             // times zero is not zero where one of them is such a value.)
@@ -453,13 +456,12 @@ __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) 
                         first = 8 * wv + i;
                         o[i] = 0.0f;
                     }
+                split8<PY>(o, y);
+#pragma unroll
+                for (int k = 0; k < PY; ++k) *reinterpret_cast<s8 *>(&sm.xt[b][k][at_x(lane, wv)]) = y[k];
                 if (first < kQ) sm.bad[c % 3] = 1;
             }
             sm.first_bad[b][wv][lane] = first;
-            s8 y[PY];
-            split8<PY>(o, y);
-#pragma unroll
-            for (int k = 0; k < PY; ++k) *reinterpret_cast<s8 *>(&sm.xt[b][k][at_x(lane, wv)]) = y[k];
         }
     };
 
@@ -500,12 +502,13 @@ __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) 
     }
     f4 cb[2][2];
     const float *cb_p = a.ws_cb + ((u0 * a.G + g) * kQ + t_l) * kQ + 8 * lg;
+    // cb[0]: C_t . B_s for the token's own half of the chunk (what lies above the diagonal is not used), cb[1]: for the
+    // first half
     auto load_cb = [&](bool more) __attribute__((always_inline)) {
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {     // (what lies above the diagonal is not used)
-            cb[ks][0] = *reinterpret_cast<const f4 *>(cb_p + 32 * ks);
-            cb[ks][1] = *reinterpret_cast<const f4 *>(cb_p + 32 * ks + 4);
-        }
+        cb[0][0] = *reinterpret_cast<const f4 *>(cb_p + 32 * (i >> 1));
+        cb[0][1] = *reinterpret_cast<const f4 *>(cb_p + 32 * (i >> 1) + 4);
+        cb[1][0] = *reinterpret_cast<const f4 *>(cb_p);
+        cb[1][1] = *reinterpret_cast<const f4 *>(cb_p + 4);
         cb_p += more ? static_cast<int64_t>(a.G) * (kQ * kQ) : 0;
     };
     T zq[8];
@@ -515,7 +518,7 @@ __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) 
         if (!z_p) return;
         const T *z = z_p + (q.first + static_cast<int64_t>(t_z < end ? t_z : end - 1)) * a.z_row;   // (a row that is there)
         t_z += kQ;
-        if constexpr (VEC) {
+        if constexpr (FAST) {
 #pragma unroll
             for (int k = 0; k < 8; k += 16 / static_cast<int>(sizeof(T)))
                 *reinterpret_cast<u4 *>(zq + k) = *reinterpret_cast<const u4 *>(z + k);
@@ -535,79 +538,86 @@ __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) 
     T *y_p = static_cast<T *>(a.y) + ((q.first + static_cast<int64_t>(begin) + t_l) * a.H + h) * a.P + p0 + out_p;
     const int64_t y_step = static_cast<int64_t>(kQ) * a.H * a.P;
 
-    // the outputs of chunk c
-    auto outputs = [&](int c, bool more) __attribute__((always_inline)) {
+    f4 acc[2];      // outputs of the chunk: the wave's tokens, 4 lg + j of both tiles
+    // the carried state's share.  Row r of tile k is channel 32 ph + 8 (r / 4) + 4 k + r % 4, so that a lane gets eight
+    // channels side by side
+    auto carried = [&](int c) __attribute__((always_inline)) {
         if constexpr (!OWN) {
-            const int b = c & 1, sb = Lds::kStates == 2 ? b : 0;
+            const int at = fresh(st_at + (Lds::kStates == 2 ? c & 1 : 0) * (PY * kQ * NP));
+            acc[0] = acc[1] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int kk = 0; kk < NP / 32; ++kk)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    s8 sf[PY];
+#pragma unroll
+                    for (int e = 0; e < PY; ++e) sf[e] = *reinterpret_cast<const s8 *>(&sm.st[0][e][0] + ((at ^ 32 * kk) + 4 * NP * k));
+                    acc[k] = product<PY>(sf, cf[kk], acc[k]);
+                }
+            const float e = sm.tab[c % 3][kE][t_l];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) acc[k] *= e;
+        }
+    };
+    // the chunk's own share from tokens 32 ks ..: (C_t . B_s) decayed, times x
+    auto within = [&](int c, int ks, const float (&v)[8]) __attribute__((always_inline)) {
+        if constexpr (!OWN) {
+            const int at = fresh(xt_at + (c & 1) * (PY * kQ * kQ));
+            s8 m[PY];
+            split8<PY>(v, m);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                s8 xf[PY];
+#pragma unroll
+                for (int e = 0; e < PY; ++e) xf[e] = *reinterpret_cast<const s8 *>(&sm.xt[0][e][0] + ((at ^ 32 * ks) + 4 * kQ * k));
+                acc[k] = product<PY>(xf, m, acc[k]);
+            }
+        }
+    };
+    // of its own half of the chunk, D on the diagonal
+    auto near = [&](int c) __attribute__((always_inline)) {
+        if constexpr (!OWN) {
             const float(&tab)[kTabs][kQ] = sm.tab[c % 3];
-            const bool on = 32 * ph < np;
-            f4 acc[2] = {};
-            if (on) {
-                const int at = fresh(st_at + sb * (PY * kQ * NP));
-                // the carried state's share.  Row r of tile k is channel 32 ph + 8 (r / 4) + 4 k + r % 4, so that a lane
-                // gets eight channels side by side
+            const int ks = i >> 1, s0 = 32 * ks + 8 * lg;
+            const f4 d0 = *reinterpret_cast<const f4 *>(&tab[kDt][s0]), d1 = *reinterpret_cast<const f4 *>(&tab[kDt][s0 + 4]);
+            const f4 c0 = *reinterpret_cast<const f4 *>(&tab[kC32][s0]), c1 = *reinterpret_cast<const f4 *>(&tab[kC32][s0 + 4]);
+            const float ct = tab[kC32][t_l];
+            float v[8];
 #pragma unroll
-                for (int kk = 0; kk < NP / 32; ++kk)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        s8 sf[PY];
-#pragma unroll
-                        for (int e = 0; e < PY; ++e) sf[e] = *reinterpret_cast<const s8 *>(&sm.st[0][e][0] + ((at ^ 32 * kk) + 4 * NP * k));
-                        acc[k] = product<PY>(sf, cf[kk], acc[k]);
-                    }
-                const float e = tab[kE][t_l];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) acc[k] *= e;
+            for (int e = 0; e < 8; ++e) {
+                const float f = __builtin_amdgcn_exp2f(ct - (e < 4 ? c0[e & 3] : c1[e & 3])) * (e < 4 ? d0[e & 3] : d1[e & 3]);
+                v[e] = __uint_as_float(__float_as_uint(cb[0][e >> 2][e & 3] * f) & below[e]) + diag[e];
             }
-            load_c(more);
-            if (on) {
-                // the chunk's own share: (C_t . B_s) decayed, D on the diagonal, times x
-                const int at = fresh(xt_at + b * (PY * kQ * kQ));
+            within(c, ks, v);
+        }
+    };
+    // the second half's tokens: of the first half
+    auto far = [&](int c) __attribute__((always_inline)) {
+        if constexpr (!OWN) {
+            if (i < 2) return;
+            const float(&tab)[kTabs][kQ] = sm.tab[c % 3];
+            const f4 d0 = *reinterpret_cast<const f4 *>(&tab[kWb][8 * lg]), d1 = *reinterpret_cast<const f4 *>(&tab[kWb][8 * lg + 4]);
+            const float et = tab[kEin][t_l];
+            float v[8];
 #pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    if (ks > i >> 1) continue;
-                    float v[8];
-                    const int s0 = 32 * ks + 8 * lg;
-                    const f4 d0 = *reinterpret_cast<const f4 *>(&tab[ks == i >> 1 ? kDt : kWb][s0]);
-                    const f4 d1 = *reinterpret_cast<const f4 *>(&tab[ks == i >> 1 ? kDt : kWb][s0 + 4]);
-                    if (ks == i >> 1) {
-                        const f4 c0 = *reinterpret_cast<const f4 *>(&tab[kC32][s0]);
-                        const f4 c1 = *reinterpret_cast<const f4 *>(&tab[kC32][s0 + 4]);
-                        const float ct = tab[kC32][t_l];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float f = __builtin_amdgcn_exp2f(ct - (e < 4 ? c0[e & 3] : c1[e & 3])) * (e < 4 ? d0[e & 3] : d1[e & 3]);
-                            v[e] = __uint_as_float(__float_as_uint(cb[ks][e >> 2][e & 3] * f) & below[e]) + diag[e];
-                        }
-                    } else {
-                        const float et = tab[kEin][t_l];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = cb[ks][e >> 2][e & 3] * (et * (e < 4 ? d0[e & 3] : d1[e & 3]));
-                    }
-                    s8 m[PY];
-                    split8<PY>(v, m);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        s8 xf[PY];
-#pragma unroll
-                        for (int e = 0; e < PY; ++e) xf[e] = *reinterpret_cast<const s8 *>(&sm.xt[0][e][0] + ((at ^ 32 * ks) + 4 * kQ * k));
-                        acc[k] = product<PY>(xf, m, acc[k]);
-                    }
-                }
+            for (int e = 0; e < 8; ++e) v[e] = cb[1][e >> 2][e & 3] * (et * (e < 4 ? d0[e & 3] : d1[e & 3]));
+            within(c, 0, v);
+        }
+    };
+    auto store = [&](int c) __attribute__((always_inline)) {
+        if constexpr (!OWN) {
+            float y[8] = {acc[0][0], acc[0][1], acc[0][2], acc[0][3], acc[1][0], acc[1][1], acc[1][2], acc[1][3]};
+            if (sm.bad[c % 3]) {
+                for (int k = 0; k < 8; ++k)
+                    for (int o = 0; o < 8; ++o)
+                        if (sm.first_bad[c & 1][o][out_p + k] <= t_l) y[k] = __builtin_nanf("");
             }
-            load_cb(more);
-            if (on && begin + c * kQ + t_l < end && out_p < np) {
-                float y[8] = {acc[0][0], acc[0][1], acc[0][2], acc[0][3], acc[1][0], acc[1][1], acc[1][2], acc[1][3]};
-                if (sm.bad[c % 3]) {
-                    for (int k = 0; k < 8; ++k)
-                        for (int o = 0; o < 8; ++o)
-                            if (sm.first_bad[b][o][out_p + k] <= t_l) y[k] = __builtin_nanf("");
-                }
-                if (z_p) {
+            if (z_p) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) y[k] *= silu_f(widen_v(zq[k]));
-                }
-                if constexpr (VEC) {
+                for (int k = 0; k < 8; ++k) y[k] *= silu_f(widen_v(zq[k]));
+            }
+            if (begin + c * kQ + t_l < end && out_p < np) {
+                if constexpr (FAST) {
                     if constexpr (sizeof(T) == 2)
                         *reinterpret_cast<u4 *>(y_p) = u4{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])};
                     else
@@ -620,42 +630,38 @@ __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) 
                 }
             }
             y_p += y_step;
-            load_z();
         }
     };
     float whole = 1.0f;      // decay over the segment
     // the state behind chunk c
-    auto advance = [&](int c, bool more) __attribute__((always_inline)) {
+    auto advance = [&](int c) __attribute__((always_inline)) {
         const float dec = sm.tab[c % 3][kE][kQ - 1];
         if constexpr (OWN) whole *= dec;
         const int at = fresh(xw_at + (c & 1) * (kPS * kQ * kQ));
 #pragma unroll
         for (int j = 0; j < kPT; ++j) {
-            if (16 * (pt0 + j) >= np) continue;
-            f4 acc = S[j] * dec;
+            f4 v = S[j] * dec;
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
                 s8 xf[kPS];
 #pragma unroll
                 for (int k = 0; k < kPS; ++k) xf[k] = *reinterpret_cast<const s8 *>(&sm.xw[0][k][0] + ((at ^ 32 * ks) + 16 * kQ * j));
-                acc = product<kPS>(bf[ks], xf, acc);
+                v = product<kPS>(bf[ks], xf, v);
             }
-            S[j] = acc;
+            S[j] = v;
         }
-        load_b(more);
-    };
-    // chunk c + 1 into LDS, chunk c + 2 on its way
-    auto next = [&](int c, bool more) __attribute__((always_inline)) {
-        if (more) {
-            stage(c + 1);
-            put_tab(c + 2);
-        }
-        load_x();
-        load_tab();
     };
 
     // Every chunk issues the same loads in the same order, the last ones again where there are no more: a wait for one of
     // them then leaves the later ones in flight.  (Loads in branches were waited for all together, at the top of each chunk.)
+    // Of a SIMD's two waves, one stages before a chunk's products, the other behind them, so that VALU and matrix
+    // instructions meet: waves 4 to 7 pass the barrier first and stage the chunk after next then, which comes to the same
+    // order with one loop.
+    const int early = wv >> 2;
+    auto next = [&](int c) __attribute__((always_inline)) {
+        stage(c);
+        load_x();
+    };
     if (nch > 0) {
         win.load(a, q, channel, t_x);
         t_x += kQ;
@@ -671,30 +677,36 @@ __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) 
             put_state(0);
         }
         put_tab(1);
-        __syncthreads();
-        stage(0);
-        load_x();
         load_tab();
         __syncthreads();
+        next(0);
+        if (early) next(1);
+        __syncthreads();
     }
-    // A SIMD's two waves take the chunk's work in opposite order: one stages (VALU) while the other multiplies.
-    constexpr bool kOne = !OWN && Lds::kStates == 1;
-    auto chunks = [&](auto first) __attribute__((always_inline)) {
-        constexpr bool kStageFirst = decltype(first)::value;
-        for (int c = 0; c < nch; ++c) {
-            const bool more = c + 1 < nch, more2 = c + 2 < nch;
-            if constexpr (!OWN)
-                if (threadIdx.x == 0) sm.bad[(c + 2) % 3] = 0;
-            if constexpr (kStageFirst) next(c, more);
-            outputs(c, more2);
-            if constexpr (kOne) __syncthreads();   // the old state's parts are read
-            advance(c, more2);
-            if (more) put_state(kOne ? 0 : (c & 1) ^ 1);
-            if constexpr (!kStageFirst) next(c, more);
-            __syncthreads();
+    for (int c = 0; c < nch; ++c) {
+        const bool more2 = c + 2 < nch;
+        if constexpr (!OWN) {
+            if (threadIdx.x == 0) sm.bad[(c + 2) % 3] = 0;
+            carried(c);
+            load_c(more2);
+            near(c);
+            if constexpr (Lds::kStates == 1) __syncthreads();   // the old state's parts are read
         }
-    };
-    chunks(std::false_type{});
+        advance(c);
+        load_b(more2);
+        put_state(!OWN && Lds::kStates == 2 ? (c & 1) ^ 1 : 0);
+        if constexpr (!OWN) {
+            far(c);
+            load_cb(more2);
+            store(c);
+            load_z();
+        }
+        put_tab(c + 2);
+        load_tab();
+        if (early) __syncthreads();
+        next(c + 1 + early);
+        if (!early) __syncthreads();
+    }
 
     // ---- end states
     float *to = OWN ? a.ws_state + (item * a.H + h) * a.P * a.N
@@ -868,7 +880,8 @@ hipError_t prompts(const SsdConvArgs &a, hipStream_t s) {
     if (e != hipSuccess) return e;
     const dim3 grid(static_cast<unsigned>((a.items * a.H * a.PB + 7) / 8 * 8));
     if (a.nseg_split) {
-        hipLaunchKernelGGL((ssdconv_sweep_kernel<T, NP, PY, true, false>), grid, dim3(kThreads), 0, s, a);
+        if (a.W == 4) hipLaunchKernelGGL((ssdconv_sweep_kernel<T, NP, PY, true, true>), grid, dim3(kThreads), 0, s, a);
+        else hipLaunchKernelGGL((ssdconv_sweep_kernel<T, NP, PY, true, false>), grid, dim3(kThreads), 0, s, a);
         e = launch_status(s);
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL(ssdconv_join_kernel, dim3(static_cast<unsigned>((a.P * a.N + 255) / 256), static_cast<unsigned>(a.H),
@@ -876,7 +889,7 @@ hipError_t prompts(const SsdConvArgs &a, hipStream_t s) {
         e = launch_status(s);
         if (e != hipSuccess) return e;
     }
-    if (a.y_vec && (a.z_vec || !a.z)) hipLaunchKernelGGL((ssdconv_sweep_kernel<T, NP, PY, false, true>), grid, dim3(kThreads), 0, s, a);
+    if (a.W == 4 && a.y_vec && (a.z_vec || !a.z)) hipLaunchKernelGGL((ssdconv_sweep_kernel<T, NP, PY, false, true>), grid, dim3(kThreads), 0, s, a);
     else hipLaunchKernelGGL((ssdconv_sweep_kernel<T, NP, PY, false, false>), grid, dim3(kThreads), 0, s, a);
     e = launch_status(s);
     if (e != hipSuccess || !a.nseg_split || a.W == 1) return e;
