@@ -11,7 +11,7 @@
 //     S'  = e^(cum_64) S + sum_s e^(cum_64 - cum_s) dt_s x_s B_s^T
 //
 // Three parts:
-//  * prep (a workgroup per chunk and B/C group, and per chunk and eight heads): what all heads of a group share. B and C
+//  * prep (a workgroup per chunk and B/C group, and per chunk and 64 heads): what all heads of a group share. B and C
 //    behind the convolution, cut into bf16 parts and stored as the lanes' operands of the products to come, C B^T of the
 //    chunk, and per head the decays. A sequence's first chunk starts at its first token, so no chunk holds two sequences.
 //  * sweep (a workgroup per sequence, head and 64 channels): walks the chunks with the state in registers.  x is
@@ -221,34 +221,40 @@ __global__ void __launch_bounds__(kThreads) ssdconv_prep_kernel(SsdConvArgs a) {
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, lg = lane >> 4;
 
-    if (static_cast<int>(blockIdx.y) >= a.G) {   // ---- the decays of eight heads, a wave each
-        const int h = (static_cast<int>(blockIdx.y) - a.G) * 8 + wv;
-        if (h >= a.H) return;
-        float dt = 0.0f;
-        if (t0 + lane < q.len) {
-            dt = widen_v(static_cast<const T *>(a.delta)[(q.first + static_cast<int64_t>(t0) + lane) * a.d_row + h]);
+    if (static_cast<int>(blockIdx.y) >= a.G) {   // ---- the decays of 64 heads, eight to a wave
+        const int h0 = (static_cast<int>(blockIdx.y) - a.G) * 64 + wv * 8;
+        const T *D = static_cast<const T *>(a.delta) + (q.first + static_cast<int64_t>(t0 + lane < q.len ? t0 + lane : q.len - 1)) * a.d_row;
+        T raw[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) raw[k] = D[h0 + k < a.H ? h0 + k : a.H - 1];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int h = h0 + k;
+            if (h >= a.H) break;
+            float dt = widen_v(raw[k]);
             if (a.dbias) dt += a.dbias[h];
             if (a.softplus) dt = softplus_f(dt);
-        }
-        const float step = dt * (a.A[h] * kLog2e);
-        float pre = step, suf = step;            // inclusive, within a half of 32
+            if (t0 + lane >= q.len) dt = 0.0f;
+            const float step = dt * (a.A[h] * kLog2e);
+            float pre = step, suf = step;            // inclusive, within a half of 32
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const float p = __shfl_up(pre, o, 32), f = __shfl_down(suf, o, 32);
-            if ((lane & 31) >= o) pre += p;
-            if ((lane & 31) + o < 32) suf += f;
+            for (int o = 1; o < 32; o <<= 1) {
+                const float p = __shfl_up(pre, o, 32), f = __shfl_down(suf, o, 32);
+                if ((lane & 31) >= o) pre += p;
+                if ((lane & 31) + o < 32) suf += f;
+            }
+            const float behind = __shfl_down(suf, 1, 32);
+            const float ein = __builtin_amdgcn_exp2f(pre);
+            const float wb = __builtin_amdgcn_exp2f((lane & 31) == 31 ? 0.0f : behind) * dt;
+            const float half0 = __shfl(ein, 31, 64), half1 = __shfl(ein, 63, 64);
+            float *t = a.ws_tab + (u * a.H + h) * (kTabs * kQ) + lane;
+            t[kE * kQ] = lane < 32 ? ein : ein * half0;
+            t[kWr * kQ] = lane < 32 ? wb * half1 : wb;
+            t[kC32 * kQ] = pre;
+            t[kDt * kQ] = dt;
+            t[kEin * kQ] = ein;
+            t[kWb * kQ] = wb;
         }
-        const float behind = __shfl_down(suf, 1, 32);
-        const float ein = __builtin_amdgcn_exp2f(pre);
-        const float wb = __builtin_amdgcn_exp2f((lane & 31) == 31 ? 0.0f : behind) * dt;
-        const float half0 = __shfl(ein, 31, 64), half1 = __shfl(ein, 63, 64);
-        float *t = a.ws_tab + (u * a.H + h) * (kTabs * kQ) + lane;
-        t[kE * kQ] = lane < 32 ? ein : ein * half0;
-        t[kWr * kQ] = lane < 32 ? wb * half1 : wb;
-        t[kC32 * kQ] = pre;
-        t[kDt * kQ] = dt;
-        t[kEin * kQ] = ein;
-        t[kWb * kQ] = wb;
         return;
     }
 
@@ -352,11 +358,12 @@ __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) 
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, lg = lane >> 4;
 
-    // workgroup -> (segment, head, channels), neighbours on one XCD (they are dealt out in turn): the heads of a
-    // sequence read the same operands of B and C from that XCD's L2
-    const int64_t W = a.items * a.H * a.PB, per = (W + 7) / 8;
-    const int64_t id = static_cast<int64_t>(blockIdx.x) % 8 * per + blockIdx.x / 8;
-    if (blockIdx.x / 8 >= per || id >= W) return;
+    // workgroup -> (segment, head, channels).  The hardware deals workgroups to the 8 XCDs in turn: runs of heads_run heads,
+    // which read the same operands of B and C, get one XCD (its L2), and the runs go round, so that each has its share
+    // whichever segments are empty
+    const int64_t run = blockIdx.x / 8 / a.heads_run * 8 + blockIdx.x % 8;
+    const int64_t id = run * a.heads_run + blockIdx.x / 8 % a.heads_run;
+    if (id >= a.items * a.H * a.PB) return;
     const int pb = static_cast<int>(id % a.PB), h = static_cast<int>(id / a.PB % a.H);
     const int64_t item = id / a.PB / a.H;
     const int s = find_sequence(a, a.seg_len, item);
@@ -380,12 +387,15 @@ __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) 
                                 : q.old ? a.h + (static_cast<int64_t>(q.slot) * a.H + h) * a.P * a.N : nullptr;
 #pragma unroll
         for (int i = 0; i < kPT; ++i) {
-            const int p = 16 * (pt0 + i) + lr;
+            const int p = 16 * (pt0 + i) + lr, n = 16 * sl + 4 * lg;
+            const float *row = from + static_cast<int64_t>(p0 + p) * a.N + n;
+            S[i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (!from || p >= np || n >= a.N) continue;
+            if (a.h_vec) S[i] = *reinterpret_cast<const f4 *>(row);
+            else
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int n = 16 * sl + 4 * lg + j;
-                S[i][j] = from && p < np && n < a.N ? from[static_cast<int64_t>(p0 + p) * a.N + n] : 0.0f;
-            }
+                for (int j = 0; j < 4; ++j)
+                    if (n + j < a.N) S[i][j] = row[j];
         }
     }
     auto put_state = [&](int b) __attribute__((always_inline)) {
@@ -728,11 +738,14 @@ __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) 
 #pragma unroll
         for (int k = 0; k < kPT; ++k) {
             const int p = 16 * (pt0 + k) + lr;
-            if (p >= np) continue;
-            float *row = to + static_cast<int64_t>(p0 + p) * a.N + 16 * sl + 4 * lg;
+            const int n = 16 * sl + 4 * lg;
+            if (p >= np || n >= a.N) continue;
+            float *row = to + static_cast<int64_t>(p0 + p) * a.N + n;
+            if (a.h_vec) *reinterpret_cast<f4 *>(row) = S[k];
+            else
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (16 * sl + 4 * lg + j < a.N) row[j] = S[k][j];
+                for (int j = 0; j < 4; ++j)
+                    if (n + j < a.N) row[j] = S[k][j];
         }
     }
     if constexpr (OWN) {
@@ -759,11 +772,25 @@ __global__ void __launch_bounds__(256) ssdconv_join_kernel(SsdConvArgs a) {
     const Sequence q(a, s);
     const int64_t item = q.first / a.seg_len + s, n = q.len > 0 ? (q.len + a.seg_len - 1) / a.seg_len : 1;
     float v = q.old ? a.h[(static_cast<int64_t>(q.slot) * a.H + h) * hp + e] : 0.0f;
-    for (int64_t k = 0; k < n; ++k) {
-        float *p = a.ws_state + ((item + k) * a.H + h) * hp + e;
-        const float own = k + 1 < n ? *p : 0.0f;
-        *p = v;
-        if (k + 1 < n) v = __builtin_fmaf(a.ws_dec[(item + k) * a.H + h], v, own);
+    float *p = a.ws_state + (item * a.H + h) * hp + e;
+    const float *d = a.ws_dec + item * a.H + h;
+    constexpr int kAtOnce = 8;
+    const int64_t step = a.H * hp;
+    for (int64_t k = 0; k < n; k += kAtOnce) {
+        float own[kAtOnce], dec[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {        // (of the last segment nothing is asked)
+            own[j] = k + j + 1 < n ? p[j * step] : 0.0f;
+            dec[j] = k + j + 1 < n ? d[static_cast<int64_t>(j) * a.H] : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j)
+            if (k + j < n) {
+                p[j * step] = v;
+                v = __builtin_fmaf(dec[j], v, own[j]);
+            }
+        p += kAtOnce * step;
+        d += kAtOnce * a.H;
     }
 }
 
@@ -886,12 +913,12 @@ __global__ void __launch_bounds__(256) ssdconv_token_kernel(SsdConvArgs a) {
 
 template <class T, int NP, int PY>
 hipError_t prompts(const SsdConvArgs &a, hipStream_t s) {
-    const unsigned heads = static_cast<unsigned>((a.H + 7) / 8);
+    const unsigned heads = static_cast<unsigned>((a.H + 63) / 64);
     hipLaunchKernelGGL((ssdconv_prep_kernel<T, NP, PY>), dim3(static_cast<unsigned>(a.chunks), static_cast<unsigned>(a.G) + heads),
                        dim3(kThreads), 0, s, a);
     hipError_t e = launch_status(s);
     if (e != hipSuccess) return e;
-    const dim3 grid(static_cast<unsigned>((a.items * a.H * a.PB + 7) / 8 * 8));
+    const dim3 grid(static_cast<unsigned>((a.items * a.H * a.PB / a.heads_run + 7) / 8 * 8 * a.heads_run));
     if (a.nseg_split) {
         if (a.W == 4) hipLaunchKernelGGL((ssdconv_sweep_kernel<T, NP, PY, true, true>), grid, dim3(kThreads), 0, s, a);
         else hipLaunchKernelGGL((ssdconv_sweep_kernel<T, NP, PY, true, false>), grid, dim3(kThreads), 0, s, a);

@@ -188,6 +188,7 @@ struct SsdConvArgs {
     int softplus;
     // set by the plan
     int PB = 1, seg_len = 0;         // blocks of 64 channels; tokens of a segment (a multiple of 64)
+    int heads_run = 1;               // workgroups of a segment that share an XCD
     int nseg_split = 0;              // sequences in segments, their states in ws_state
     int64_t chunks = 0, items = 0;   // numbers of chunks and segments
     int z_vec = 0, y_vec = 0, h_vec = 0;

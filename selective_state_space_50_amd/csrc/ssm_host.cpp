@@ -1382,21 +1382,28 @@ int plan_ssdconv(const ssm_ssdconv_shape *s, bool token, SsdConvPlan *plan) {
     }
     plan->blocks64 = ceil_div(s->headdim, 64);
     plan->chunks = s->tokens / 64 + s->sequences;
-    // Whole sequences, or segments of them: a sweep walks its chunks one after another, a workgroup to a CU at once.  A
-    // segment costs a second read of x for its own state (0.6 of a chunk's time, measured) and about three chunks' time
-    // for its start, and the pass between them about eight.
+    // Whole sequences, or segments of them.  A sweep's workgroup walks its chunks one after another, one workgroup to a CU;
+    // runs of heads_run of them are dealt out to the 8 XCDs in turn.  In units of a chunk's time (3.4 to 4.2 us),
+    // measured on 8 to 64 heads over 8192 and 32768 tokens in segments of 8 to 128 chunks: a segment costs 1.5 for each
+    // of its chunks (x is read twice) and 3 for its start, the passes in between 6.  (B1 L32768 H24: segments of 52 chunks 354
+    // us, of 26 359, of 32 398, of 16 444, whole 1714; H8: of 20 158, of 16 221, of 52 298, whole 1632; B1 L8192 H64: of 40
+    // 256, of 64 355, whole 431.)
     const int64_t across = s->nheads * plan->blocks64, all = ceil_div(s->tokens, 64);
     int64_t longest = s->max_seqlen > 0 && s->max_seqlen < s->tokens ? s->max_seqlen : s->tokens;
     longest = ceil_div(longest, 64);
-    const int64_t even = ceil_div(all * across, kCUs);
-    double best = static_cast<double>(longest > even ? longest : even);
+    plan->heads_run = across % 4 == 0 ? 4 : across % 2 == 0 ? 2 : 1;
+    const auto rounds = [&](int64_t n) { return ceil_div(ceil_div(n * across / plan->heads_run, 8) * plan->heads_run, kCUs / 8); };
+    double best = static_cast<double>(longest);
+    if (rounds(s->sequences) > 1) {     // (lengths are not known here: several rounds of sequences as if half of one were lost)
+        const double even = 1.15 * static_cast<double>(all * across) / static_cast<double>(kCUs) + 0.5 * static_cast<double>(longest);
+        if (even > best) best = even;
+    }
     plan->seg_len = kSsdConvWhole;
     for (int64_t k = 2; k <= 64 && k <= longest; ++k) {
         const int64_t len = ceil_div(longest, k);
         if (len < 4) break;
-        const int64_t n = ceil_div(all, len) + (s->sequences - 1) / 2;    // (half a segment is lost to each further sequence)
-        const int64_t rounds = ceil_div(n * across, kCUs);
-        const double cost = static_cast<double>(rounds) * (1.6 * static_cast<double>(len) + 3.0) + 8.0;
+        const int64_t n = all / len + ceil_div(s->sequences + 1, 2);      // (each sequence ends inside a segment)
+        const double cost = static_cast<double>(rounds(n)) * (1.5 * static_cast<double>(len) + 3.0) + 6.0;
         if (cost < best) {
             best = cost;
             plan->seg_len = 64 * len;

@@ -211,6 +211,7 @@ struct SsdConvPlan {
     int64_t x_row = 0, z_row = 0, d_row = 0, channels = 0;
     int64_t blocks64 = 1;             // blocks of 64 channels of a head
     int64_t chunks = 0, items = 0;    // numbers of chunks and segments
+    int64_t heads_run = 1;            // workgroups of a segment that share an XCD: divides the segment's
     int64_t seg_len = 0;
     bool split = false;
     bool z_vec = false, y_vec = false, h_vec = false;
