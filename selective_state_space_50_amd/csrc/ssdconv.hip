@@ -143,7 +143,7 @@ struct Window {
             X += t < q.len - 1 ? a.x_row : 0;
         }
     }
-    __device__ void load(const SsdConvArgs &a, const Sequence &q, int channel, int t0) {
+    __device__ __forceinline__ void load(const SsdConvArgs &a, const Sequence &q, int channel, int t0) {
         const T *X = static_cast<const T *>(a.xbc) + channel;
 #pragma unroll
         for (int i = 0; i < K + 3; ++i) {
@@ -166,19 +166,20 @@ struct Window {
     }
 };
 
-// silu of the convolution over a window: o[0 .. K - 1] (a filter of W < 4 columns leaves the earliest rows out; FULL: W is 4)
+// silu of the convolution over eight tokens of a window, from its token r on (a filter of W < 4 columns leaves the earliest
+// rows out; FULL: W is 4)
 template <bool FULL, class T, int K>
-__device__ __forceinline__ void convolve(const Window<T, K> &in, const float (&w)[4], float bias, int W, float *o) {
+__device__ __forceinline__ void convolve(const Window<T, K> &in, int r, const float (&w)[4], float bias, int W, float *o) {
 #pragma unroll
-    for (int i = 0; i < K; ++i) o[i] = bias;
+    for (int i = 0; i < 8; ++i) o[i] = bias;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         if (FULL || k >= 4 - W) {
 #pragma unroll
-            for (int i = 0; i < K; ++i) o[i] = __builtin_fmaf(w[k], widen_v(in.x[i + k]), o[i]);
+            for (int i = 0; i < 8; ++i) o[i] = __builtin_fmaf(w[k], widen_v(in.x[r + i + k]), o[i]);
         }
 #pragma unroll
-    for (int i = 0; i < K; ++i) o[i] = silu_f(o[i]);
+    for (int i = 0; i < 8; ++i) o[i] = silu_f(o[i]);
 }
 
 __device__ __forceinline__ void filter(const SsdConvArgs &a, int channel, float (&w)[4], float &bias) {
@@ -224,14 +225,12 @@ __global__ void __launch_bounds__(kThreads) ssdconv_prep_kernel(SsdConvArgs a) {
     if (static_cast<int>(blockIdx.y) >= a.G) {   // ---- the decays of 64 heads, eight to a wave
         const int h0 = (static_cast<int>(blockIdx.y) - a.G) * 64 + wv * 8;
         const T *D = static_cast<const T *>(a.delta) + (q.first + static_cast<int64_t>(t0 + lane < q.len ? t0 + lane : q.len - 1)) * a.d_row;
-        T raw[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) raw[k] = D[h0 + k < a.H ? h0 + k : a.H - 1];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int h = h0 + k;
-            if (h >= a.H) break;
-            float dt = widen_v(raw[k]);
+        // (loops that are not unrolled: a wave runs this once, and every line of code is a cold one)
+        T raw = D[h0 < a.H ? h0 : a.H - 1];
+#pragma unroll 1
+        for (int h = h0; h < h0 + 8 && h < a.H; ++h) {
+            float dt = widen_v(raw);
+            raw = D[h + 1 < a.H ? h + 1 : a.H - 1];
             if (a.dbias) dt += a.dbias[h];
             if (a.softplus) dt = softplus_f(dt);
             if (t0 + lane >= q.len) dt = 0.0f;
@@ -263,33 +262,33 @@ __global__ void __launch_bounds__(kThreads) ssdconv_prep_kernel(SsdConvArgs a) {
     constexpr int kTok = kQ * 2 * NP / kThreads;         // 32 or 16
     const int ch = threadIdx.x % (2 * NP), n = ch % NP, which = ch / NP, from = threadIdx.x / (2 * NP) * kTok;
     const int channel = a.H * a.P + (which * a.G + g) * a.N + n;
-    float w[4], bias;
-    if (n < a.N) filter(a, channel, w, bias);
     s8 *bt = reinterpret_cast<s8 *>(a.ws_bt) + (u * a.G + g) * (NP / 16 * 2 * kPS * 64);
-#pragma unroll
-    for (int r = 0; r < kTok; r += 16) {
-        float o[16];
+    Window<T, 8> in;
+    float w[4], bias = 0.0f;
+    if (n < a.N) {
+        in.load(a, q, channel, t0 + from);
+        filter(a, channel, w, bias);
+    }
+#pragma unroll 1
+    for (int t = from; t < from + kTok; t += 8) {
+        float o[8];
         if (n < a.N) {
-            Window<T, 16> in;
-            in.load(a, q, channel, t0 + from + r);
-            convolve<false>(in, w, bias, a.W, o);
+            const Window<T, 8> now = in;
+            in.load_on(a, q, channel, t0 + t + 8);
+            convolve<false>(now, 0, w, bias, a.W, o);
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            if (n >= a.N || t0 + from + r + i >= q.len) o[i] = 0.0f;
-            tile[which][from + r + i][n] = o[i];
+        for (int i = 0; i < 8; ++i) {
+            if (n >= a.N || t0 + t + i >= q.len) o[i] = 0.0f;
+            tile[which][t + i][n] = o[i];
         }
         if (which == 0) {
             // operands of the state's product: lane (n % 16, s / 8 % 4) of slice n / 16 holds B[s .. s + 7][n]
+            s8 part[kPS];
+            split8<kPS>(o, part);
 #pragma unroll
-            for (int e = 0; e < 16; e += 8) {
-                s8 part[kPS];
-                split8<kPS>(o + e, part);
-                const int t = from + r + e;
-#pragma unroll
-                for (int k = 0; k < kPS; ++k)
-                    bt[((n / 16 * 2 + t / 32) * kPS + k) * 64 + n % 16 + 16 * (t % 32 / 8)] = part[k];
-            }
+            for (int k = 0; k < kPS; ++k)
+                bt[((n / 16 * 2 + t / 32) * kPS + k) * 64 + n % 16 + 16 * (t % 32 / 8)] = part[k];
         }
     }
     __syncthreads();
@@ -306,6 +305,7 @@ __global__ void __launch_bounds__(kThreads) ssdconv_prep_kernel(SsdConvArgs a) {
         }
     }
     float *cb = a.ws_cb + ((u * a.G + g) * kQ + 16 * i + lr) * kQ;
+#pragma unroll 1
     for (int k = half; k <= i; k += 2) {
         f4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) 
     auto stage = [&](int c) __attribute__((always_inline)) {
         const int b = c & 1;
         float o[8];
-        convolve<FAST>(win, fw, fbias, a.W, o);
+        convolve<FAST>(win, 0, fw, fbias, a.W, o);
         const f4 w0 = *reinterpret_cast<const f4 *>(&sm.tab[c % 3][kWr][8 * wv]);
         const f4 w1 = *reinterpret_cast<const f4 *>(&sm.tab[c % 3][kWr][8 * wv + 4]);
         float v[8];
@@ -714,8 +714,8 @@ __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) 
         put_tab(1);
         load_tab();
         __syncthreads();
-        next(0);
-        if (early) next(1);
+#pragma unroll 1
+        for (int c = 0; c <= early; ++c) next(c);
         __syncthreads();
     }
     for (int c = 0; c < nch; ++c) {
