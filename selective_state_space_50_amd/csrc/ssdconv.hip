@@ -35,7 +35,8 @@ namespace ssm {
 namespace {
 
 constexpr int kQ = 64;                 // tokens of a chunk
-constexpr int kThreads = 512;
+constexpr int kThreads = 512;          // of a sweep
+constexpr int kPrepThreads = 1024;
 constexpr int kPS = 3;                 // parts of the state's factors
 enum { kE, kWr, kC32, kDt, kEin, kWb, kTabs };   // a head's tables of a chunk, 64 values each:
 // kE   e^(cum_t)                    decay of the carried state up to token t
@@ -208,9 +209,27 @@ __device__ __forceinline__ void conv_state_end(const SsdConvArgs &a, const Seque
 
 // ---------------------------------------------------------------------------- prep
 
-// NP: the states padded to 64 or 128; PY: parts of y's factors
+// Sums over the lanes up to (BACK: from) a lane, within each half of 32: four row shifts, then the first (second) row's whole.
+template <bool BACK>
+__device__ __forceinline__ float half_scan(float v, int lane) {
+    const auto add = [&](auto ctrl) __attribute__((always_inline)) {
+        v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), decltype(ctrl)::value, 0xf, 0xf, true));
+    };
+    constexpr int kShift = BACK ? 0x100 : 0x110;     // row_shl, row_shr: what would come from another row is zero
+    add(std::integral_constant<int, kShift + 1>{});
+    add(std::integral_constant<int, kShift + 2>{});
+    add(std::integral_constant<int, kShift + 4>{});
+    add(std::integral_constant<int, kShift + 8>{});
+    const auto whole = [&](int l) { return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l)); };
+    const float lo = whole(BACK ? 16 : 15), hi = whole(BACK ? 48 : 47);
+    if ((lane & 16) == (BACK ? 0 : 16)) v += lane < 32 ? lo : hi;
+    return v;
+}
+
+// NP: the states padded to 64 or 128; PY: parts of y's factors.  Sixteen waves: each has little to do, and what takes the time
+// is one thing waiting for the other (B4 L4096 H64: 20 us with eight).
 template <class T, int NP, int PY>
-__global__ void __launch_bounds__(kThreads) ssdconv_prep_kernel(SsdConvArgs a) {
+__global__ void __launch_bounds__(kPrepThreads) ssdconv_prep_kernel(SsdConvArgs a) {
     constexpr int kRow = NP + 4;
     __shared__ __align__(16) float tile[2][kQ][kRow];    // B and C, token by token
     const int64_t u = blockIdx.x;
@@ -223,25 +242,21 @@ __global__ void __launch_bounds__(kThreads) ssdconv_prep_kernel(SsdConvArgs a) {
     const int lr = lane & 15, lg = lane >> 4;
 
     if (static_cast<int>(blockIdx.y) >= a.G) {   // ---- the decays of 64 heads, eight to a wave
-        const int h0 = (static_cast<int>(blockIdx.y) - a.G) * 64 + wv * 8;
+        const int h0 = (static_cast<int>(blockIdx.y) - a.G) * 64 + wv * 4;
         const T *D = static_cast<const T *>(a.delta) + (q.first + static_cast<int64_t>(t0 + lane < q.len ? t0 + lane : q.len - 1)) * a.d_row;
-        // (loops that are not unrolled: a wave runs this once, and every line of code is a cold one)
-        T raw = D[h0 < a.H ? h0 : a.H - 1];
-#pragma unroll 1
-        for (int h = h0; h < h0 + 8 && h < a.H; ++h) {
-            float dt = widen_v(raw);
-            raw = D[h + 1 < a.H ? h + 1 : a.H - 1];
+        T raw[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) raw[k] = D[h0 + k < a.H ? h0 + k : a.H - 1];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int h = h0 + k;
+            if (h >= a.H) break;
+            float dt = widen_v(raw[k]);
             if (a.dbias) dt += a.dbias[h];
             if (a.softplus) dt = softplus_f(dt);
             if (t0 + lane >= q.len) dt = 0.0f;
             const float step = dt * (a.A[h] * kLog2e);
-            float pre = step, suf = step;            // inclusive, within a half of 32
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float p = __shfl_up(pre, o, 32), f = __shfl_down(suf, o, 32);
-                if ((lane & 31) >= o) pre += p;
-                if ((lane & 31) + o < 32) suf += f;
-            }
+            const float pre = half_scan<false>(step, lane), suf = half_scan<true>(step, lane);   // inclusive
             const float behind = __shfl_down(suf, 1, 32);
             const float ein = __builtin_amdgcn_exp2f(pre);
             const float wb = __builtin_amdgcn_exp2f((lane & 31) == 31 ? 0.0f : behind) * dt;
@@ -259,7 +274,7 @@ __global__ void __launch_bounds__(kThreads) ssdconv_prep_kernel(SsdConvArgs a) {
 
     // ---- B and C of group g behind the convolution: a thread per channel and run of tokens
     const int g = blockIdx.y;
-    constexpr int kTok = kQ * 2 * NP / kThreads;         // 32 or 16
+    constexpr int kTok = kQ * 2 * NP / kPrepThreads;     // 16 or 8
     const int ch = threadIdx.x % (2 * NP), n = ch % NP, which = ch / NP, from = threadIdx.x / (2 * NP) * kTok;
     const int channel = a.H * a.P + (which * a.G + g) * a.N + n;
     s8 *bt = reinterpret_cast<s8 *>(a.ws_bt) + (u * a.G + g) * (NP / 16 * 2 * kPS * 64);
@@ -292,30 +307,26 @@ __global__ void __launch_bounds__(kThreads) ssdconv_prep_kernel(SsdConvArgs a) {
         }
     }
     __syncthreads();
-    // ---- operands of C, and C B^T below the diagonal: wave (i, half) takes C's tokens 16 i .. and B's blocks half, half + 2
-    const int i = wv & 3, half = wv >> 2;
-    s8 cf[NP / 32][PY];
+    // ---- operands of C, and C B^T below the diagonal: wave (i, k) takes C's tokens 16 i .. and B's 16 k .., and of the
+    // operands every fourth
+    const int i = wv & 3, k = wv >> 2;
     s8 *cs = reinterpret_cast<s8 *>(a.ws_c) + ((u * a.G + g) * 4 + i) * (NP / 32 * PY * 64) + lane;
+    f4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int kk = 0; kk < NP / 32; ++kk) {
-        split8<PY>(&tile[1][16 * i + lr][32 * kk + 8 * lg], cf[kk]);
-        if (half == 0) {
+        if (k > i && kk != k) continue;
+        s8 cf[PY], bf[PY];
+        split8<PY>(&tile[1][16 * i + lr][32 * kk + 8 * lg], cf);
+        if (kk == k) {
 #pragma unroll
-            for (int k = 0; k < PY; ++k) cs[(kk * PY + k) * 64] = cf[kk][k];
+            for (int e = 0; e < PY; ++e) cs[(kk * PY + e) * 64] = cf[e];
         }
+        if (k > i) continue;
+        split8<PY>(&tile[0][16 * k + lr][32 * kk + 8 * lg], bf);
+        acc = product<PY>(bf, cf, acc);
     }
-    float *cb = a.ws_cb + ((u * a.G + g) * kQ + 16 * i + lr) * kQ;
-#pragma unroll 1
-    for (int k = half; k <= i; k += 2) {
-        f4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int kk = 0; kk < NP / 32; ++kk) {
-            s8 bf[PY];
-            split8<PY>(&tile[0][16 * k + lr][32 * kk + 8 * lg], bf);
-            acc = product<PY>(bf, cf[kk], acc);
-        }
-        *reinterpret_cast<f4 *>(cb + 16 * k + 4 * lg) = acc;    // lane: token 16 i + lr, s = 16 k + 4 lg + 0 .. 3
-    }
+    // lane: token 16 i + lr, s = 16 k + 4 lg + 0 .. 3
+    if (k <= i) *reinterpret_cast<f4 *>(a.ws_cb + ((u * a.G + g) * kQ + 16 * i + lr) * kQ + 16 * k + 4 * lg) = acc;
 }
 
 // ---------------------------------------------------------------------------- sweep
@@ -915,7 +926,7 @@ template <class T, int NP, int PY>
 hipError_t prompts(const SsdConvArgs &a, hipStream_t s) {
     const unsigned heads = static_cast<unsigned>((a.H + 63) / 64);
     hipLaunchKernelGGL((ssdconv_prep_kernel<T, NP, PY>), dim3(static_cast<unsigned>(a.chunks), static_cast<unsigned>(a.G) + heads),
-                       dim3(kThreads), 0, s, a);
+                       dim3(kPrepThreads), 0, s, a);
     hipError_t e = launch_status(s);
     if (e != hipSuccess) return e;
     const dim3 grid(static_cast<unsigned>((a.items * a.H * a.PB / a.heads_run + 7) / 8 * 8 * a.heads_run));

@@ -1411,7 +1411,7 @@ int plan_ssdconv(const ssm_ssdconv_shape *s, bool token, SsdConvPlan *plan) {
     }
     plan->split = plan->seg_len != kSsdConvWhole;
     plan->items = s->tokens / plan->seg_len + s->sequences;
-    if (plan->items > (int64_t(1) << 23) / across || plan->chunks > (int64_t(1) << 23)) return too_many();
+    if (plan->items > (int64_t(1) << 23) / across || plan->chunks > (int64_t(1) << 22)) return too_many();
     const int64_t np = s->dstate > 64 ? 128 : 64, py = s->dtype == SSM_DTYPE_BF16 ? 2 : 3;
     const int64_t cg = plan->chunks * s->ngroups;
     if (plan->chunks * s->nheads > (int64_t(1) << 36) || cg > (int64_t(1) << 30)) return too_many();
