@@ -38,13 +38,12 @@ constexpr int kQ = 64;                 // tokens of a chunk
 constexpr int kThreads = 512;          // of a sweep
 constexpr int kPrepThreads = 1024;
 constexpr int kPS = 3;                 // parts of the state's factors
-enum { kE, kWr, kC32, kDt, kEin, kWb, kTabs };   // a head's tables of a chunk, 64 values each:
-// kE   e^(cum_t)                    decay of the carried state up to token t
+enum { kWr, kC32, kDt, kWb, kTabs };   // a head's tables of a chunk, 64 values each:
 // kWr  e^(cum_64 - cum_s) dt_s      weight of token s in the state passed on
-// kC32 exponent of the decay from the 32-token half's start to t, to the base 2
+// kC32 exponent of the decay from the 32-token half's start to t, to the base 2 (the carried state's decay up to t
+//      is 2 to it, times the first half's whole in the second half)
 // kDt  dt_s
-// kEin e^(kC32)                     decay of what a later half reads from earlier ones
-// kWb  e^(to the half's end) dt_s
+// kWb  e^(to the half's end) dt_s   weight of the first half's token s in what the second half reads
 
 typedef short s4 __attribute__((ext_vector_type(4)));
 typedef short s8 __attribute__((ext_vector_type(8)));
@@ -258,15 +257,12 @@ __global__ void __launch_bounds__(kPrepThreads) ssdconv_prep_kernel(SsdConvArgs 
             const float step = dt * (a.A[h] * kLog2e);
             const float pre = half_scan<false>(step, lane), suf = half_scan<true>(step, lane);   // inclusive
             const float behind = __shfl_down(suf, 1, 32);
-            const float ein = __builtin_amdgcn_exp2f(pre);
             const float wb = __builtin_amdgcn_exp2f((lane & 31) == 31 ? 0.0f : behind) * dt;
-            const float half0 = __shfl(ein, 31, 64), half1 = __shfl(ein, 63, 64);
+            const float half1 = __shfl(__builtin_amdgcn_exp2f(pre), 63, 64);
             float *t = a.ws_tab + (u * a.H + h) * (kTabs * kQ) + lane;
-            t[kE * kQ] = lane < 32 ? ein : ein * half0;
             t[kWr * kQ] = lane < 32 ? wb * half1 : wb;
             t[kC32 * kQ] = pre;
             t[kDt * kQ] = dt;
-            t[kEin * kQ] = ein;
             t[kWb * kQ] = wb;
         }
         return;
@@ -362,7 +358,7 @@ struct StateLds {
 // what would branch is done for nothing instead (channels behind the head's last, tokens behind the sequence's: their
 // weights are zero and their outputs are not stored).
 template <class T, int NP, int PY, bool OWN, bool FAST>
-__global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) {
+__global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(SsdConvArgs a) {
     typedef SweepLds<NP, PY> Lds;
     __shared__ __align__(16) typename std::conditional<OWN, StateLds, Lds>::type sm;
     constexpr int kPT = NP == 128 ? 4 : 2;           // 16-channel tiles of a wave's states
@@ -430,9 +426,21 @@ __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) 
     float fw[4], fbias;
     filter(a, channel, fw, fbias);
     Window<T, 8> win;
+    const int row_bytes = static_cast<int>(a.x_row) * static_cast<int>(sizeof(T)), x_at = channel * static_cast<int>(sizeof(T));
     int t_x = begin + 8 * wv;                        // first token of the next chunk to load
     auto load_x = [&]() __attribute__((always_inline)) {
-        win.load_on(a, q, channel, t_x);
+        // (chunks behind the first: three rows are in front; rows behind the sequence's end are out of the buffer and read as
+        // zeros, which their weights take out)
+        const int t = t_x - 3 < q.len ? t_x - 3 : q.len;
+        const int64_t bytes = static_cast<int64_t>(q.len - t) * row_bytes;
+        const auto rows = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<T *>(static_cast<const T *>(a.xbc) + (q.first + static_cast<int64_t>(t)) * a.x_row), 0,
+            static_cast<int>(t == q.len ? 0 : bytes < 0x7fffffff ? bytes - row_bytes + a.C * static_cast<int64_t>(sizeof(T)) : 0x7fffffff), 0x00020000);
+#pragma unroll
+        for (int i = 0; i < 11; ++i) {
+            if constexpr (sizeof(T) == 2) win.x[i] = static_cast<T>(__builtin_amdgcn_raw_buffer_load_b16(rows, x_at, i * row_bytes, 0));
+            else win.x[i] = __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(rows, x_at, i * row_bytes, 0));
+        }
         t_x += kQ;
     };
     const float *tab_p = a.ws_tab + (u0 * a.H + h) * (kTabs * kQ) + 4 * (threadIdx.x < kTabs * kQ / 4 ? threadIdx.x : 0);
@@ -442,15 +450,15 @@ __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) 
         tq = *reinterpret_cast<const f4 *>(tab_p);
         tab_p += --tabs > 0 ? static_cast<int64_t>(a.H) * (kTabs * kQ) : 0;
     };
-    auto put_tab = [&](int c) __attribute__((always_inline)) {
-        if (threadIdx.x < kTabs * kQ / 4) *reinterpret_cast<f4 *>(&sm.tab[c % 3][0][0] + 4 * threadIdx.x) = tq;
+    auto put_tab = [&](int k3) __attribute__((always_inline)) {
+        if (threadIdx.x < kTabs * kQ / 4) *reinterpret_cast<f4 *>(&sm.tab[k3][0][0] + 4 * threadIdx.x) = tq;
     };
-    auto stage = [&](int c) __attribute__((always_inline)) {
+    auto stage = [&](int c, int k3) __attribute__((always_inline)) {     // (k3: c % 3)
         const int b = c & 1;
         float o[8];
         convolve<FAST>(win, 0, fw, fbias, a.W, o);
-        const f4 w0 = *reinterpret_cast<const f4 *>(&sm.tab[c % 3][kWr][8 * wv]);
-        const f4 w1 = *reinterpret_cast<const f4 *>(&sm.tab[c % 3][kWr][8 * wv + 4]);
+        const f4 w0 = *reinterpret_cast<const f4 *>(&sm.tab[k3][kWr][8 * wv]);
+        const f4 w1 = *reinterpret_cast<const f4 *>(&sm.tab[k3][kWr][8 * wv + 4]);
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = o[i] * (i < 4 ? w0[i & 3] : w1[i & 3]);
@@ -480,7 +488,7 @@ __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) 
                 split8<PY>(o, y);
 #pragma unroll
                 for (int k = 0; k < PY; ++k) *reinterpret_cast<s8 *>(&sm.xt[b][k][at_x(lane, wv)]) = y[k];
-                if (first < kQ) sm.bad[c % 3] = 1;
+                if (first < kQ) sm.bad[k3] = 1;
             }
             sm.first_bad[b][wv][lane] = first;
         }
@@ -561,7 +569,7 @@ __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) 
 
     // ---- a chunk's products.  Their LDS operands are requested a group ahead of the instructions that take them; the
     // groups' order is held by ahead() (left to itself the compiler reads two operands, waits, multiplies, and reads on:
-    // 281 us against 2xx on B4 L4096 H64 64x128).
+    // 306 us against 294 on B4 L4096 H64 64x128).
     auto ahead = []() __attribute__((always_inline)) { __builtin_amdgcn_sched_barrier(0); };
     constexpr int kKK = NP / 32;
     f4 acc[2];             // outputs: the wave's tokens, 4 lg + j of both tiles
@@ -599,9 +607,9 @@ __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) 
         S[j] = v;
     };
     float whole = 1.0f;      // decay over the segment
-    auto products = [&](int c, bool more2) __attribute__((always_inline)) {
-        const float(&tab)[kTabs][kQ] = sm.tab[c % 3];
-        const float dec = tab[kE][kQ - 1];
+    auto products = [&](int c, int k3, bool more2) __attribute__((always_inline)) {
+        const float(&tab)[kTabs][kQ] = sm.tab[k3];
+        const float first = __builtin_amdgcn_exp2f(tab[kC32][31]), dec = first * __builtin_amdgcn_exp2f(tab[kC32][63]);
         const int w_at = fresh(xw_at + (c & 1) * (kPS * kQ * kQ));
         if constexpr (OWN) {
             whole *= dec;
@@ -610,7 +618,7 @@ __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) 
             // the carried state's share
             const int at = fresh(st_at + (Lds::kStates == 2 ? c & 1 : 0) * (PY * kQ * NP));
             read_state(at, 0);
-            const float e = tab[kE][t_l], ct = tab[kC32][t_l], et = tab[kEin][t_l];
+            const float ct = tab[kC32][t_l];
             const int s0 = 32 * (i >> 1) + 8 * lg;
             f4 d0, d1, c0, c1;
             acc[0] = acc[1] = f4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -631,6 +639,7 @@ __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) 
             load_c(more2);
             read_w(w_at, 0);
             ahead();
+            const float et = __builtin_amdgcn_exp2f(ct), e = i < 2 ? et : et * first;
             // the chunk's own share from the token's half of it: (C_t . B_s) decayed, D on the diagonal, times x
             float v[8];
 #pragma unroll
@@ -663,15 +672,15 @@ __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) 
         for (int j = 0; j < kPT; ++j) {
             if (j + 1 < kPT) read_w(w_at, j + 1);
             ahead();
-            state_tile(j, dec);
+            if (FAST || 16 * (pt0 + j) < np) state_tile(j, dec);
         }
         load_b(more2);
         put_state(!OWN && Lds::kStates == 2 ? (c & 1) ^ 1 : 0);
     };
-    auto store = [&](int c) __attribute__((always_inline)) {
+    auto store = [&](int c, int k3) __attribute__((always_inline)) {
         if constexpr (!OWN) {
             float y[8] = {acc[0][0], acc[0][1], acc[0][2], acc[0][3], acc[1][0], acc[1][1], acc[1][2], acc[1][3]};
-            if (sm.bad[c % 3]) {
+            if (sm.bad[k3]) {
                 for (int k = 0; k < 8; ++k)
                     for (int o = 0; o < 8; ++o)
                         if (sm.first_bad[c & 1][o][out_p + k] <= t_l) y[k] = __builtin_nanf("");
@@ -704,8 +713,8 @@ __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) 
     // instructions meet: waves 4 to 7 pass the barrier first and stage the chunk after next then, which comes to the same
     // order with one loop.
     const int early = wv >> 2;
-    auto next = [&](int c) __attribute__((always_inline)) {
-        stage(c);
+    auto next = [&](int c, int k3) __attribute__((always_inline)) {
+        stage(c, k3);
         load_x();
     };
     if (nch > 0) {
@@ -726,20 +735,24 @@ __global__ void __launch_bounds__(kThreads) ssdconv_sweep_kernel(SsdConvArgs a) 
         load_tab();
         __syncthreads();
 #pragma unroll 1
-        for (int c = 0; c <= early; ++c) next(c);
+        for (int c = 0; c <= early; ++c) next(c, c);
         __syncthreads();
     }
+    const auto follow = [](int k) { return k == 2 ? 0 : k + 1; };
+    int k3 = 0;                                      // c % 3
     for (int c = 0; c < nch; ++c) {
         const bool more2 = c + 2 < nch;
+        const int n3 = follow(k3), m3 = follow(n3);
         if constexpr (!OWN)
-            if (threadIdx.x == 0) sm.bad[(c + 2) % 3] = 0;
-        products(c, more2);
-        store(c);
-        put_tab(c + 2);
+            if (threadIdx.x == 0) sm.bad[m3] = 0;
+        products(c, k3, more2);
+        store(c, k3);
+        put_tab(m3);
         load_tab();
         if (early) __syncthreads();
-        next(c + 1 + early);
+        next(c + 1 + early, early ? m3 : n3);
         if (!early) __syncthreads();
+        k3 = n3;
     }
 
     // ---- end states

@@ -1363,6 +1363,10 @@ int plan_ssdconv(const ssm_ssdconv_shape *s, bool token, SsdConvPlan *plan) {
                   (long long)inner, (long long)s->nheads);
         return SSM_EINVAL;
     }
+    if (!token && plan->x_row > (int64_t(1) << 22)) {
+        set_error("x_row=%lld: rows of xbc more than 2^22 elements apart", (long long)plan->x_row);
+        return SSM_EUNSUPPORTED;
+    }
     int64_t row = plan->x_row > plan->z_row ? plan->x_row : plan->z_row;
     if (plan->d_row > row) row = plan->d_row;
     if (s->tokens > 0 && row > kMaxElems / s->tokens) {
@@ -1411,7 +1415,7 @@ int plan_ssdconv(const ssm_ssdconv_shape *s, bool token, SsdConvPlan *plan) {
     }
     plan->split = plan->seg_len != kSsdConvWhole;
     plan->items = s->tokens / plan->seg_len + s->sequences;
-    if (plan->items > (int64_t(1) << 23) / across || plan->chunks > (int64_t(1) << 22)) return too_many();
+    if (plan->items > (int64_t(1) << 22) / across - 8 || plan->chunks > (int64_t(1) << 22)) return too_many();
     const int64_t np = s->dstate > 64 ? 128 : 64, py = s->dtype == SSM_DTYPE_BF16 ? 2 : 3;
     const int64_t cg = plan->chunks * s->ngroups;
     if (plan->chunks * s->nheads > (int64_t(1) << 36) || cg > (int64_t(1) << 30)) return too_many();
@@ -1423,7 +1427,7 @@ int plan_ssdconv(const ssm_ssdconv_shape *s, bool token, SsdConvPlan *plan) {
     };
     plan->c_off = take(cg * 64 * np * 2 * py);
     plan->cb_off = take(cg * 64 * 64 * 4);
-    plan->tab_off = take(plan->chunks * s->nheads * 6 * 64 * 4);
+    plan->tab_off = take(plan->chunks * s->nheads * 4 * 64 * 4);
     if (plan->split) {
         plan->state_off = take(plan->items * inner * s->dstate * 4);
         plan->dec_off = take(plan->items * s->nheads * 4);
