@@ -127,6 +127,8 @@ struct Units {
             pair[i] = turns ? V * u : -1;
             a_in[i] = oa[i] < a.dim;
             b_in[i] = ob[i] < a.dim;   // (single elements: an odd dim's last unit has one side only)
+            if (!a_in[i]) oa[i] = 0;   // (what is not there counts as zeros, with the first columns' weights)
+            if (!b_in[i]) ob[i] = 0;
         }
     }
 };
@@ -204,8 +206,8 @@ __global__ void __launch_bounds__(kWG) rotary_kernel(RotaryArgs a) {
                     for (int j = 0; j < UL; ++j)
 #pragma unroll
                         for (int e = 0; e < V; ++e) {
-                            xa[j][e] *= rstd * (un.a_in[j] ? wr[un.oa[j] + e] : 0.0f);
-                            xb[j][e] *= rstd * (un.b_in[j] ? wr[un.ob[j] + e] : 0.0f);
+                            xa[j][e] *= rstd * wr[un.oa[j] + e];
+                            xb[j][e] *= rstd * wr[un.ob[j] + e];
                         }
                 }
                 if (i >= rows) continue;
@@ -266,7 +268,7 @@ __global__ void __launch_bounds__(kWG) qknorm_bwd_kernel(RotaryArgs a) {
                 const RowAt at(a, t0, i < rows ? i : rows - 1);
                 float xa[UL][V], xb[UL][V], ga[UL][V], gb[UL][V];
                 const float *wr = w + (at.is_q ? 0 : a.dim_even);
-                float ss = 0.0f, ex = 0.0f;
+                float wa[UL][V], wb[UL][V], ss = 0.0f, ex = 0.0f;
 #pragma unroll
                 for (int j = 0; j < UL; ++j) {
                     open<T, V>(ra[r][j], xa[j]);
@@ -276,9 +278,10 @@ __global__ void __launch_bounds__(kWG) qknorm_bwd_kernel(RotaryArgs a) {
                     if (un.pair[j] >= 0) turn<V, INTER>(ga[j], gb[j], cs + at.token * a.pairs + un.pair[j], true);
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
+                        wa[j][e] = wr[un.oa[j] + e];
+                        wb[j][e] = wr[un.ob[j] + e];
                         ss = __builtin_fmaf(xa[j][e], xa[j][e], __builtin_fmaf(xb[j][e], xb[j][e], ss));
-                        if (un.a_in[j]) ex = __builtin_fmaf(ga[j][e] * wr[un.oa[j] + e], xa[j][e], ex);
-                        if (un.b_in[j]) ex = __builtin_fmaf(gb[j][e] * wr[un.ob[j] + e], xb[j][e], ex);
+                        ex = __builtin_fmaf(ga[j][e] * wa[j][e], xa[j][e], __builtin_fmaf(gb[j][e] * wb[j][e], xb[j][e], ex));
                     }
                 }
                 ss = team_sum(ss, a.team);
@@ -302,8 +305,8 @@ __global__ void __launch_bounds__(kWG) qknorm_bwd_kernel(RotaryArgs a) {
                 for (int j = 0; j < UL; ++j) {
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
-                        ga[j][e] = __builtin_fmaf(ga[j][e] * rstd, un.a_in[j] ? wr[un.oa[j] + e] : 0.0f, -c * xa[j][e]);
-                        gb[j][e] = __builtin_fmaf(gb[j][e] * rstd, un.b_in[j] ? wr[un.ob[j] + e] : 0.0f, -c * xb[j][e]);
+                        ga[j][e] = __builtin_fmaf(ga[j][e] * rstd, wa[j][e], -c * xa[j][e]);
+                        gb[j][e] = __builtin_fmaf(gb[j][e] * rstd, wb[j][e], -c * xb[j][e]);
                     }
                     if (un.a_in[j]) keep<T, V>(dx + un.oa[j], ga[j]);
                     if (un.b_in[j]) keep<T, V>(dx + un.ob[j], gb[j]);
@@ -332,19 +335,31 @@ __global__ void __launch_bounds__(kWG) qknorm_bwd_kernel(RotaryArgs a) {
     }
 }
 
-// dw[c] = the sum of part[row][c] over the rows, 32 columns a workgroup: 32 sums of every 32nd row, then those in
-// their order
+// dw[c] = the sum of part[row][c] over the rows (1024 at most), eight columns a workgroup: 128 sums of every 128th row, then
+// those in their order, in two steps
 __global__ void __launch_bounds__(1024) column_sum_kernel(const float *part, int rows, int dim, float *dwq, float *dwk) {
-    __shared__ float s[32][33];
-    const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
-    float v = 0.0f;
-    if (c < 2 * dim)
-        for (int r = y; r < rows; r += 32) v += part[static_cast<int64_t>(r) * 2 * dim + c];
-    s[y][x] = v;
+    __shared__ float s[128][9];
+    const int x = threadIdx.x & 7, y = threadIdx.x >> 3, c = blockIdx.x * 8 + x;
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = c < 2 * dim && y + 128 * k < rows ? part[static_cast<int64_t>(y + 128 * k) * 2 * dim + c] : 0.0f;
+    float t = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) t += v[k];
+    s[y][x] = t;
+    __syncthreads();
+    if (y < 8) {
+        t = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) t += s[16 * y + i][x];
+    }
+    __syncthreads();
+    if (y < 8) s[y][x] = t;
     __syncthreads();
     if (y || c >= 2 * dim) return;
-    float t = 0.0f;
-    for (int i = 0; i < 32; ++i) t += s[i][x];
+    t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t += s[i][x];
     if (c < dim) { if (dwq) dwq[c] = t; }
     else if (dwk) dwk[c - dim] = t;
 }
@@ -363,7 +378,7 @@ hipError_t typed(const RotaryArgs &a, bool norm, bool bwd, hipStream_t s) {
     hipLaunchKernelGGL((qknorm_bwd_kernel<T, V, UL, INTER>), grid, dim3(kWG), lds, s, a);
     hipError_t e = launch_status(s);
     if (e != hipSuccess || !a.part) return e;
-    hipLaunchKernelGGL(column_sum_kernel, dim3(static_cast<unsigned>((2 * a.dim + 31) / 32)), dim3(1024), 0, s, a.part,
+    hipLaunchKernelGGL(column_sum_kernel, dim3(static_cast<unsigned>((2 * a.dim + 7) / 8)), dim3(1024), 0, s, a.part,
                        static_cast<int>(a.blocks), a.dim, a.dwq, a.dwk);
     return launch_status(s);
 }
