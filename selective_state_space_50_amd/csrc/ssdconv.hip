@@ -692,10 +692,10 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
             if (begin + c * kQ + t_l < end && out_p < np) {
                 if constexpr (FAST) {
                     if constexpr (sizeof(T) == 2)
-                        *reinterpret_cast<u4 *>(y_p) = u4{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])};
+                        __builtin_nontemporal_store(u4{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])}, reinterpret_cast<u4 *>(y_p));
                     else
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) *reinterpret_cast<f4 *>(y_p + 4 * k) = f4{y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]};
+                        for (int k = 0; k < 2; ++k) __builtin_nontemporal_store(f4{y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]}, reinterpret_cast<f4 *>(y_p + 4 * k));
                 } else {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
