@@ -289,15 +289,22 @@ __global__ void __launch_bounds__(kWG) qknorm_bwd_kernel(RotaryArgs a) {
                 ex = team_sum(ex, a.team);
                 if (i >= rows) continue;
                 const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, a.inv_dim, a.eps));
-                const float c = rstd * rstd * rstd * (ex * a.inv_dim);      // dx = rstd e - c x
+                const float c = rstd * (rstd * (ex * a.inv_dim));           // dx = rstd e - c xh (rstd^3 could be infinite)
                 T *dx = static_cast<T *>(at.is_q ? a.q_out : a.k_out) + at.out;
+#pragma unroll
+                for (int j = 0; j < UL; ++j)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        xa[j][e] *= rstd;
+                        xb[j][e] *= rstd;
+                    }
                 auto sums = [&](float (&d)[UL][2][V]) __attribute__((always_inline)) {
 #pragma unroll
                     for (int j = 0; j < UL; ++j)
 #pragma unroll
                         for (int e = 0; e < V; ++e) {
-                            d[j][0][e] = __builtin_fmaf(ga[j][e], xa[j][e] * rstd, d[j][0][e]);
-                            d[j][1][e] = __builtin_fmaf(gb[j][e], xb[j][e] * rstd, d[j][1][e]);
+                            d[j][0][e] = __builtin_fmaf(ga[j][e], xa[j][e], d[j][0][e]);
+                            d[j][1][e] = __builtin_fmaf(gb[j][e], xb[j][e], d[j][1][e]);
                         }
                 };
                 if (at.is_q) sums(dw[0]);

@@ -208,6 +208,21 @@ def test_nan_and_infinity_stay_in_their_head(ssm):
     assert torch.isnan(turned[1, 3, 2]).sum() == 2 and torch.isfinite(turned[1, 3, :2]).all()
 
 
+@pytest.mark.parametrize("scale", [1e-15, 1e15])
+def test_gradients_of_tiny_and_huge_rows(ssm, scale):
+    """rstd reaches 1e15 without eps: its cube would be infinite."""
+    c = make(2, 11, 4, 2, 64, 32, "f32", 9)
+    q = (c["q"] * scale).contiguous()
+    x = to_host(q).reshape(22, 4, 64)
+    g = ssm.qknorm_bwd(q, None, w_dev(c["wq"]), None, c["pos"], c["freqs"], c["dq"], eps=0.0)
+    _, r = ro.norm(x, c["wq"], 0.0)
+    dx, dw = ro.norm_bwd(x, c["wq"], ro.turn(c["gq"], c["p"], c["f"], back=True), 0.0)
+    ga = ro.turn_size(c["gq"], c["f"])
+    e = ga * np.abs(c["wq"])
+    close(g["dq"], dx, 150 * E * r * (e + np.abs(x) * r * r * (e * np.abs(x)).mean(-1, keepdims=True)), "f32", "dq")
+    close(g["dwq"], dw, 600 * E * (ga * np.abs(x) * r).reshape(-1, 64).sum(0), "f32", "dwq")
+
+
 def test_empty_and_deterministic(ssm):
     import torch
     c = make(2, 1500, 9, 3, 64, 64, "bf16", 8)
