@@ -706,8 +706,9 @@ size_t ssm_ssdconv_update_workspace_bytes(const ssm_ssdconv_shape *shape);
  *   A, Dskip, delta_bias  [nheads]               fp32    A required; Dskip, delta_bias may be NULL
  *   w, bias    [channels, width], [channels]     fp32    w required; bias NULL = 0
  *   offsets    [sequences + 1]                   int32   sequence s has the rows offsets[s] .. offsets[s + 1] - 1;
- *              ascending from 0 or more to tokens or less (values are cut to that range; a decrease counts as no
- *              tokens).  Rows of no sequence: y stays as it was there
+ *              ascending from 0 or more to tokens or less (values are cut to that range; where they decrease, y and the
+ *              states of this call are unspecified, and nothing else is written).  Rows of no sequence: y stays as
+ *              it was there
  *   slots      [sequences]                       int32   NULL = sequence s has slot s.  A slot outside 0 .. nslots - 1
  *              (-1, say): the sequence starts from zeros and its states are not kept.  No two sequences of a
  *              call may share a slot: what it holds afterwards, and y of those two, is then unspecified
@@ -722,8 +723,8 @@ size_t ssm_ssdconv_update_workspace_bytes(const ssm_ssdconv_shape *shape);
  * Products on the bf16 matrix cores, fp32 factors in bf16 parts: three (all 24 bits) for the state, and for y three
  * (fp32) or two (bf16).  A NaN or infinity of x becomes NaN in its channel's outputs from its token on and in its
  * channel's state, one of B, C, z or delta in those that it enters; no other sequence sees it.  Deterministic.
- * SSM_EUNSUPPORTED: dstate over SSM_SSDCONV_MAX_DSTATE, sequences over 65535, tokens over 2^28, nheads * headdim over
- * 2^24, too many workgroups.
+ * SSM_EUNSUPPORTED: dstate over SSM_SSDCONV_MAX_DSTATE, sequences over 65535, tokens over 2^28, nheads over 32768, nheads *
+ * headdim over 2^24, ngroups * dstate or (ssm_ssdconv_fwd) x_row over 2^22, too many workgroups.
  */
 int ssm_ssdconv_fwd(const ssm_ssdconv_shape *shape, const void *xbc, const void *delta, const float *A, const float *w,
                     const float *bias, const float *Dskip, const void *z, const float *delta_bias, int delta_softplus,

@@ -92,7 +92,8 @@ __device__ __forceinline__ void split8(const float *v, s8 (&out)[N]) {
 }
 
 // which sequence chunk (or segment) v belongs to, sequence s owning the numbers from offset_s / len + s on (as many as
-// its tokens can need: no sums over the sequences before it); -1: none.  Wave-uniform.
+// its tokens can need: no sums over the sequences before it); -1: none.  Wave-uniform.  Where offsets decrease it may be
+// another sequence, whose numbers start behind v: callers look for that.
 __device__ __forceinline__ int clamped(const SsdConvArgs &a, int s) {
     const int o = a.offsets[s];
     return o < 0 ? 0 : o > a.T ? static_cast<int>(a.T) : o;
@@ -235,8 +236,9 @@ __global__ void __launch_bounds__(kPrepThreads) ssdconv_prep_kernel(SsdConvArgs 
     const int s = find_sequence(a, kQ, u);
     if (s < 0) return;
     const Sequence q(a, s);
-    const int t0 = static_cast<int>(u - (q.first / kQ + s)) * kQ;
-    if (t0 >= q.len) return;
+    const int64_t own = u - (q.first / kQ + s);           // (below 0 only where offsets decrease)
+    const int t0 = static_cast<int>(own) * kQ;
+    if (own < 0 || t0 >= q.len) return;
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, lg = lane >> 4;
 
@@ -377,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
     if (s < 0) return;
     const Sequence q(a, s);
     const int64_t seg = item - (q.first / a.seg_len + s);
-    if (seg * a.seg_len >= q.len && seg > 0) return;
+    if (seg < 0 || (seg * a.seg_len >= q.len && seg > 0)) return;   // (below 0 only where offsets decrease)
     const int begin = static_cast<int>(seg * a.seg_len);
     const bool last = q.len - begin <= a.seg_len;
     if (OWN && last) return;                         // nobody reads its own state

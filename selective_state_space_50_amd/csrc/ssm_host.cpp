@@ -1345,7 +1345,7 @@ int plan_ssdconv(const ssm_ssdconv_shape *s, bool token, SsdConvPlan *plan) {
         set_error("dstate=%lld exceeds the supported maximum %d", (long long)s->dstate, SSM_SSDCONV_MAX_DSTATE);
         return SSM_EUNSUPPORTED;
     }
-    if (s->nheads > 65536 || s->headdim > 65536 || s->sequences > 65535 || s->tokens > (int64_t(1) << 28) ||
+    if (s->nheads > 32768 || s->headdim > 65536 || s->sequences > 65535 || s->tokens > (int64_t(1) << 28) ||
         s->nslots > (int64_t(1) << 30) || s->nheads * s->headdim > (int64_t(1) << 24) || s->ngroups * s->dstate > (int64_t(1) << 22)) {
         set_error("shape too large (tokens=%lld, sequences=%lld, nslots=%lld, nheads=%lld, headdim=%lld, ngroups=%lld)",
                   (long long)s->tokens, (long long)s->sequences, (long long)s->nslots, (long long)s->nheads,
@@ -1364,13 +1364,17 @@ int plan_ssdconv(const ssm_ssdconv_shape *s, bool token, SsdConvPlan *plan) {
         return SSM_EINVAL;
     }
     if (!token && plan->x_row > (int64_t(1) << 22)) {
-        set_error("x_row=%lld: rows of xbc more than 2^22 elements apart", (long long)plan->x_row);
+        set_error("x_row=%lld is too large: rows of xbc more than 2^22 elements apart", (long long)plan->x_row);
         return SSM_EUNSUPPORTED;
     }
     int64_t row = plan->x_row > plan->z_row ? plan->x_row : plan->z_row;
     if (plan->d_row > row) row = plan->d_row;
     if (s->tokens > 0 && row > kMaxElems / s->tokens) {
         set_error("%lld tokens %lld elements apart are too large", (long long)s->tokens, (long long)row);
+        return SSM_EUNSUPPORTED;
+    }
+    if (s->nslots > 0 && inner * s->dstate > kMaxElems / s->nslots) {
+        set_error("%lld slots of %lld states are too large", (long long)s->nslots, (long long)(inner * s->dstate));
         return SSM_EUNSUPPORTED;
     }
     if (s->sequences == 0 || s->nheads == 0) return SSM_OK;
@@ -1415,7 +1419,7 @@ int plan_ssdconv(const ssm_ssdconv_shape *s, bool token, SsdConvPlan *plan) {
     }
     plan->split = plan->seg_len != kSsdConvWhole;
     plan->items = s->tokens / plan->seg_len + s->sequences;
-    if (plan->items > (int64_t(1) << 22) / across - 8 || plan->chunks > (int64_t(1) << 22)) return too_many();
+    if (plan->items > (int64_t(1) << 22) / across - 8 || plan->chunks >= (int64_t(1) << 22)) return too_many();
     const int64_t np = s->dstate > 64 ? 128 : 64, py = s->dtype == SSM_DTYPE_BF16 ? 2 : 3;
     const int64_t cg = plan->chunks * s->ngroups;
     if (plan->chunks * s->nheads > (int64_t(1) << 36) || cg > (int64_t(1) << 30)) return too_many();

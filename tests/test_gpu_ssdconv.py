@@ -337,6 +337,24 @@ def test_offsets_out_of_range(ssm):
         assert torch.equal(d["h"][3:], dev["h"][3:])
 
 
+@pytest.mark.parametrize("hint", [None, 64])
+def test_decreasing_offsets_stay_inside(ssm, hint):
+    """Offsets that fall by many chunks: what y and the states then are is not said, but nothing else is written."""
+    import torch
+    c, dev = make([500, 700, 400, 400], 2, 32, 16, 1, 4, "bf16", 23)
+    T = 2000
+    for ends in ([0, 1900, 0, 64, 2000], [2000, 1000, 500, 100, 0], [1500, 0, 1999, 0, 2000], [0, 2000, 10, 20, 30]):
+        room = torch.full((6000, 2, 32), 3.0, dtype=torch.bfloat16, device="cuda")
+        pool = torch.full((18, 2, 32, 16), 5.0, device="cuda")
+        conv = torch.full((18, 96, 3), 7.0, dtype=torch.bfloat16, device="cuda")
+        d = dict(dev, h=pool[6:12], conv_state=conv[6:12], offsets=torch.tensor(ends, dtype=torch.int32, device="cuda"))
+        c["longest"] = hint
+        call(ssm, c, d, out=room[2000:4000], hint=hint is not None)
+        assert (room[:2000] == 3.0).all() and (room[4000:] == 3.0).all(), ends
+        assert (pool[:6] == 5.0).all() and (pool[10:] == 5.0).all(), ends
+        assert (conv[:6] == 7.0).all() and (conv[10:] == 7.0).all(), ends
+
+
 def test_refusals(ssm):
     import torch
     c, dev = make([20, 30], 2, 32, 16, 1, 4, "bf16", 18)

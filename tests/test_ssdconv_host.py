@@ -72,6 +72,28 @@ def test_more_refusals(lib):
     assert fwd(lib, fresh=P(14, 5)) == 1 and b"workspace overlaps fresh" in lib.ssm_last_error()
 
 
+@pytest.mark.parametrize("bad,text", [
+    (dict(H=32769), "too large"), (dict(H=32768, P_=64, N=128, nslots=1 << 30), "slots of"),
+    (dict(H=2048, P_=16, N=64, G=2048, W=4, nslots=3), None),
+])
+def test_size_limits(lib, bad, text):
+    """As many heads as a launch's grid takes; a pool of more states than can be counted in bytes; in between, calls that are fine."""
+    for call in (fwd, upd):
+        if text is None:
+            assert call(lib, n=100, **bad) == 3
+        else:
+            assert call(lib, **bad) == 2 and text in lib.ssm_last_error().decode()
+
+
+def test_wide_rows(lib):
+    """A prompt's rows reach 2^22 elements, single tokens' any distance."""
+    assert fwd(lib, x_row=(1 << 22) + 1) == 2 and b"too large" in lib.ssm_last_error()
+    assert fwd(lib, x_row=1 << 22, n=100) == 3
+    assert upd(lib, x_row=(1 << 22) + 1, n=100) == 3
+    # one chunk more than a launch has threads for
+    assert ssm.ssdconv_workspace_bytes((1 << 28) - 64, 1, 1, 1, 1, max_seqlen=64) == 0
+
+
 def test_nothing_to_do(lib):
     none = dict.fromkeys(("xbc", "delta", "A", "w", "bias", "D", "z", "db", "slots", "h", "cs", "y", "ws"))
     assert fwd(lib, sequences=0, tokens=0, off=None, fresh=None, n=0, **none) == 0
