@@ -8,7 +8,8 @@
 // g = R^T dy (dx of the plain form); normed, with xh = x rstd and e = g w,
 //     dw = sum over tokens and heads of g xh,   dx = rstd (e - xh mean(e xh)).
 //
-// Memory bound: q and k are read and written once (backward: two reads, one write).  A workgroup takes a few
+// Memory bound: q and k are read and written once (backward: two reads, one write): 336 MB of B4 L4096 32+8 heads of 128
+// bf16 in 50 us, the training pass of B2 L4096 32+32 heads, 671 MB, in 44 + 81 + 4.  A workgroup takes a few
 // tokens: its threads make their cosines and sines once, in LDS, for all heads of q and k (an angle is
 // position * frequency in 64 bits, cut to a part of a turn there, and only then 32 bits: at position 10^6 a
 // 32-bit product would be off by 0.06 rad).  Then teams of lanes take the tokens' heads row by row.  A lane
@@ -344,7 +345,7 @@ __global__ void __launch_bounds__(kWG) qknorm_bwd_kernel(RotaryArgs a) {
 }
 
 // dw[c] = the sum of part[row][c] over the rows (1024 at most), eight columns a workgroup: 128 sums of every 128th row, then
-// those in their order, in two steps
+// those in their order, in two steps (4 us, most of it waiting)
 __global__ void __launch_bounds__(1024) column_sum_kernel(const float *part, int rows, int dim, float *dwq, float *dwk) {
     __shared__ float s[128][9];
     const int x = threadIdx.x & 7, y = threadIdx.x >> 3, c = blockIdx.x * 8 + x;

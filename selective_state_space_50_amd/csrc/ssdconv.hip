@@ -26,7 +26,12 @@
 // relative, a 128th of the half step that y's own rounding takes).  Exponents are sums over at most 32 tokens, forwards
 // for reads and backwards for writes, so that the nearest tokens' decays carry the smallest errors.
 //
-// Why this split (measured at 16384 tokens, H64 P64 N128): see the figures at the kernels.
+// What bounds it (B4 L4096 H64 P64 N128, gated, bf16; 274 us, whose 416 MB would take 83 at a copy's rate): the sweep, 250,
+// by its arithmetic.  Per chunk and head 10.6 MFLOP of products in parts (128 us at a large library product's rate) run beside
+// about 500 vector instructions a wave (convolution, decays, cutting into parts) and 70 KB through LDS; the vector units are
+// busy 56% of the time, the matrix cores 30%, at a clock that the load itself holds near 2.0 GHz.  The prep's 20 us are
+// the 40 MB of operands and decays that it writes (all heads read them from the L2s; written past the caches: 2 us slower).
+// B1 L32768 H24: 312 us in segments, 1714 whole.
 #include "ssm_device.h"
 
 #include <type_traits>
@@ -227,8 +232,8 @@ __device__ __forceinline__ float half_scan(float v, int lane) {
     return v;
 }
 
-// NP: the states padded to 64 or 128; PY: parts of y's factors.  Sixteen waves: each has little to do, and what takes the time
-// is one thing waiting for the other (B4 L4096 H64: 20 us with eight).
+// NP: the states padded to 64 or 128; PY: parts of y's factors.  Sixteen waves (eight: the same 20 us on B4 L4096 H64: about 5
+// of one thing waiting for the other, then 40 MB of operands and tables written).
 template <class T, int NP, int PY>
 __global__ void __launch_bounds__(kPrepThreads) ssdconv_prep_kernel(SsdConvArgs a) {
     constexpr int kRow = NP + 4;
@@ -243,7 +248,7 @@ __global__ void __launch_bounds__(kPrepThreads) ssdconv_prep_kernel(SsdConvArgs 
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, lg = lane >> 4;
 
-    if (static_cast<int>(blockIdx.y) >= a.G) {   // ---- the decays of 64 heads, eight to a wave
+    if (static_cast<int>(blockIdx.y) >= a.G) {   // ---- the decays of 64 heads, four to a wave
         const int h0 = (static_cast<int>(blockIdx.y) - a.G) * 64 + wv * 4;
         const T *D = static_cast<const T *>(a.delta) + (q.first + static_cast<int64_t>(t0 + lane < q.len ? t0 + lane : q.len - 1)) * a.d_row;
         T raw[4];
@@ -577,8 +582,8 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
     auto ahead = []() __attribute__((always_inline)) { __builtin_amdgcn_sched_barrier(0); };
     constexpr int kKK = NP / 32;
     f4 acc[2];             // outputs: the wave's tokens, 4 lg + j of both tiles
-    s8 sf[2][2][PY];       // operands of the carried state, 32 states of them and the next 32.  Row r of tile k is channel 32 ph + 8 (r / 4) + 4 k + r % 4, so that a
-                           // lane gets eight channels side by side
+    s8 sf[2][2][PY];       // operands of the carried state, 32 states of them and the next 32.  Row r of tile k is channel
+                           // 32 ph + 8 (r / 4) + 4 k + r % 4, so that a lane gets eight channels side by side
     s8 xf[2][PY];          // of x
     s8 xw[2][2][kPS];      // of x weighted, for a tile of the state and the next one
     auto read_state = [&](int at, int kk) __attribute__((always_inline)) {
@@ -793,7 +798,8 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
 // ---------------------------------------------------------------------------- segments
 
 // The segments' own end states become their start states: per sequence and head, four elements a thread (V; single ones where
-// the number of states or the pool's address does not allow it).
+// the number of states or the pool's address does not allow it: 11 us instead of 6 on 13 sequences of H12 48x96), eight
+// segments' states requested at once.
 template <int V>
 __global__ void __launch_bounds__(256) ssdconv_join_kernel(SsdConvArgs a) {
     typedef float vec __attribute__((ext_vector_type(V)));
@@ -834,7 +840,8 @@ __global__ void __launch_bounds__(256) ssdconv_join_kernel(SsdConvArgs a) {
 
 // ---------------------------------------------------------------------------- one token
 
-// The convolution of one token, all channels, into 32 bits; its state moves on.
+// The convolution of one token, all channels, into 32 bits; its state moves on.  (A launch of its own, 3 us for one sequence and 7
+// for 128: every head of a group needs its B and C, and no head may read a state that another one has moved on.)
 template <class T>
 __global__ void __launch_bounds__(256) ssdconv_token_conv_kernel(SsdConvArgs a) {
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, b = blockIdx.y;
@@ -862,8 +869,8 @@ __global__ void __launch_bounds__(256) ssdconv_token_conv_kernel(SsdConvArgs a) 
 }
 
 // One token of the scan: a workgroup per sequence and head (gridDim.z: shares of its channels).  Rows of N states are read
-// by teams of lanes, V states a lane and turn (16 bytes where N and the addresses allow it), four rows at a time: memory bound,
-// 8 bytes for every state.
+// by teams of lanes, V states a lane and turn (16 bytes where N and the addresses allow it), four rows at a time, past the caches.
+// Memory bound: 8 bytes for every state (B128 H64 64x128: 106 us for 537 MB, 5.1 TB/s, the rate of a large copy).
 template <class T, int V>
 __global__ void __launch_bounds__(256) ssdconv_token_kernel(SsdConvArgs a) {
     const int64_t id = blockIdx.x;

@@ -33,12 +33,12 @@ def test_mixer_registers(tmp_path):
         assert r["group_segment_fixed_size"] <= (80 if own else 160) * 1024, (name, r)
         if own or m.group(1) == "t":
             assert r.get("vgpr_spill_count", 0) == 0, (name, r)
-    assert seen == 16
+    assert seen == 12
 
 
 def test_mixer_without_spills_in_the_chunk_loop(tmp_path):
     loops = {n: k for n, k in _scratch_in_chunk_loops("ssdconv.hip", tmp_path / "ssdconv.s").items() if "sweep" in n}
-    assert len(loops) == 16
+    assert len(loops) == 12
     for name, n in loops.items():
         m = re.search(r"sweep_kernelI([tf])Li(\d+)ELi(\d)ELb([01])ELb([01])E", name)
         if m.group(1) == "t" or m.group(4) == "1":
