@@ -223,6 +223,24 @@ def test_gradients_of_tiny_and_huge_rows(ssm, scale):
     close(g["dwq"], dw, 600 * E * (ga * np.abs(x) * r).reshape(-1, 64).sum(0), "f32", "dwq")
 
 
+def test_as_many_heads_as_there_can_be(ssm):
+    """4096 heads of a token, of which a turn of a workgroup takes one; and one head over many tokens."""
+    for B, L, hq, hk, d in ((1, 3, 4000, 96, 16), (1, 70001, 1, 1, 16)):
+        c = make(B, L, hq, hk, d, d, "bf16", 11)
+        w = [w_dev(c["wq"]), w_dev(c["wk"])]
+        q, k = ssm.qknorm_fwd(c["q"], c["k"], *w, c["pos"], c["freqs"])
+        g = ssm.qknorm_bwd(c["q"], c["k"], *w, c["pos"], c["freqs"], c["dq"], c["dk"])
+        for n, got in (("q", q), ("k", k)):
+            u, r = ro.norm(c["x" + n], c["w" + n])
+            close(got, ro.turn(u, c["p"], c["f"]), 40 * E * ro.turn_size(u, c["f"]), "bf16", n)
+            dx, dw = ro.norm_bwd(c["x" + n], c["w" + n], ro.turn(c["g" + n], c["p"], c["f"], back=True))
+            ga = ro.turn_size(c["g" + n], c["f"])
+            e = ga * np.abs(c["w" + n])
+            x = np.abs(c["x" + n])
+            close(g["d" + n], dx, 150 * E * r * (e + x * r * r * (e * x).mean(-1, keepdims=True)), "bf16", "d" + n)
+            close(g["dw" + n], dw, 600 * E * (ga * x * r).reshape(-1, d).sum(0), "f32", "dw" + n)
+
+
 def test_empty_and_deterministic(ssm):
     import torch
     c = make(2, 1500, 9, 3, 64, 64, "bf16", 8)

@@ -355,6 +355,59 @@ def test_decreasing_offsets_stay_inside(ssm, hint):
         assert (conv[:6] == 7.0).all() and (conv[10:] == 7.0).all(), ends
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_slots_past_32_bits(ssm, dt):
+    """A pool of more than 2^31 states: the last slots give what a small pool's give, to the bit."""
+    import torch
+    lens, H, P, N = [70, 1, 200], 64, 64, 128
+    c, dev = make(lens, H, P, N, 1, 4, dt, 24, slots=[2, 0, 1], pool=3)
+    many = (1 << 31) // (H * P * N) + 8
+    h = torch.zeros(many, H, P, N, device="cuda")
+    conv = torch.zeros(many, *dev["conv_state"].shape[1:], dtype=dev["conv_state"].dtype, device="cuda")
+    h[-3:], conv[-3:] = dev["h"], dev["conv_state"]
+    big = dict(dev, h=h, conv_state=conv, slots=dev["slots"] + (many - 3))
+    y, yb = call(ssm, c, dev), call(ssm, c, big)
+    t, tb = step(ssm, c, dev, slice(0, 3)), step(ssm, c, big, slice(0, 3))
+    assert torch.equal(y, yb) and torch.equal(t, tb)
+    assert torch.equal(h[-3:], dev["h"]) and torch.equal(conv[-3:], dev["conv_state"])
+    assert not h[:-3].any() and not conv[:-3].any()
+
+
+def test_rows_past_32_bits(ssm):
+    """Rows of a very wide projection: 2^21 elements apart, the last ones behind 2^31."""
+    import torch
+    c, dev = make([1000, 80], 2, 32, 16, 1, 4, "bf16", 25, joint=False)
+    T, C = dev["xbc"].shape
+    wide = torch.empty(T, 1 << 21, dtype=torch.bfloat16, device="cuda")
+    wide[:, 5:5 + C], wide[:, 200:264], wide[:, 300:302] = dev["xbc"], dev["z"].flatten(1), dev["delta"]
+    far = dict(dev, xbc=wide[:, 5:5 + C], z=wide[:, 200:264].unflatten(1, (2, 32)), delta=wide[:, 300:302],
+               h=dev["h"].clone(), conv_state=dev["conv_state"].clone())
+    assert torch.equal(call(ssm, c, dev), call(ssm, c, far))
+    assert torch.equal(dev["h"], far["h"]) and torch.equal(dev["conv_state"], far["conv_state"])
+
+
+def test_as_many_sequences_as_there_can_be(ssm):
+    """65535 sequences of one token; some of them against the oracle, which the single-token call meets too."""
+    import torch
+    S = 65535
+    c, dev = make([1] * S, 1, 8, 4, 1, 4, "f32", 26, pool=S)
+    pick = np.concatenate([np.arange(5), np.random.default_rng(1).integers(5, S, 40), [S - 2, S - 1]])
+    sub = dict(c, offsets=np.arange(len(pick) + 1), slots=np.arange(len(pick)), fresh=np.zeros(len(pick), bool),
+               **{n: c[n][pick] for n in ("xbc", "delta", "z", "h", "conv_state")})
+    ref = mixer(sub)
+    at = torch.from_numpy(pick).cuda()
+    tok = dict(dev, h=dev["h"].clone(), conv_state=dev["conv_state"].clone())
+    for d, y, n in ((dev, call(ssm, c, dev), 1), (tok, step(ssm, c, tok, slice(None)), 0)):
+        got = dict(d, h=d["h"][at], conv_state=d["conv_state"][at])
+        check(c, got, y[at], ref, (90 + 50 * n) * E, (240 + 50 * n) * E)
+
+
+def test_wide_heads_and_many_groups(ssm):
+    """A head of many blocks of channels, and a group for every head."""
+    prompt(ssm, [70, 9], 1, 1000, 40, 1, 4, "bf16", 27)
+    prompt(ssm, [70, 9], 40, 8, 8, 40, 4, "bf16", 28)
+
+
 def test_refusals(ssm):
     import torch
     c, dev = make([20, 30], 2, 32, 16, 1, 4, "bf16", 18)
