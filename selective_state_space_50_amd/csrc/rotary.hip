@@ -338,39 +338,48 @@ __global__ void __launch_bounds__(kWG) qknorm_bwd_kernel(RotaryArgs a) {
             }
     __syncthreads();
     for (int c = threadIdx.x; c < 2 * a.dim; c += kWG) {
-        float s = 0.0f;
-        for (int t = 0; t < teams; ++t) s += lds[2 * t * a.dim + c];
-        a.part[static_cast<int64_t>(blockIdx.x) * 2 * a.dim + c] = s;
+        float s[4] = {};         // (at least four teams; chains a quarter as long)
+        for (int t = 0; t < teams; t += 4)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[i] += lds[2 * (t + i) * a.dim + c];
+        a.part[static_cast<int64_t>(blockIdx.x) * 2 * a.dim + c] = (s[0] + s[1]) + (s[2] + s[3]);
     }
 }
 
+// v[0] = the sum of v[0 .. N - 1], by halves
+template <int N>
+__device__ __forceinline__ void by_halves(float *v) {
+#pragma unroll
+    for (int o = N / 2; o > 0; o /= 2)
+#pragma unroll
+        for (int i = 0; i < o; ++i) v[i] += v[i + o];
+}
+
 // dw[c] = the sum of part[row][c] over the rows (1024 at most), eight columns a workgroup: 128 sums of every 128th row, then
-// those in their order, in two steps (4 us, most of it waiting)
+// those, in two steps, all by halves (4 us, most of it waiting)
 __global__ void __launch_bounds__(1024) column_sum_kernel(const float *part, int rows, int dim, float *dwq, float *dwk) {
     __shared__ float s[128][9];
     const int x = threadIdx.x & 7, y = threadIdx.x >> 3, c = blockIdx.x * 8 + x;
-    float v[8];
+    float v[16];
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = c < 2 * dim && y + 128 * k < rows ? part[static_cast<int64_t>(y + 128 * k) * 2 * dim + c] : 0.0f;
-    float t = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) t += v[k];
-    s[y][x] = t;
+    by_halves<8>(v);
+    s[y][x] = v[0];
     __syncthreads();
     if (y < 8) {
-        t = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) t += s[16 * y + i][x];
+        for (int i = 0; i < 16; ++i) v[i] = s[16 * y + i][x];
+        by_halves<16>(v);
     }
     __syncthreads();
-    if (y < 8) s[y][x] = t;
+    if (y < 8) s[y][x] = v[0];
     __syncthreads();
     if (y || c >= 2 * dim) return;
-    t = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t += s[i][x];
-    if (c < dim) { if (dwq) dwq[c] = t; }
-    else if (dwk) dwk[c - dim] = t;
+    for (int i = 0; i < 8; ++i) v[i] = s[i][x];
+    by_halves<8>(v);
+    if (c < dim) { if (dwq) dwq[c] = v[0]; }
+    else if (dwk) dwk[c - dim] = v[0];
 }
 
 template <class T, int V, int UL, bool INTER>
