@@ -335,15 +335,21 @@ __global__ void __launch_bounds__(kPrepThreads) ssdconv_prep_kernel(SsdConvArgs 
 
 // ---------------------------------------------------------------------------- sweep
 
-// 16-byte units of a row of LDS are swapped by its number, so that lanes that read a column of rows meet all banks.
-// (unit ^ number: where unit is 4 kk + lg, the place for kk is that for 0 with the bits of 4 kk turned over.)
-__device__ __forceinline__ int at_x(int p, int unit) { return p * kQ + ((unit ^ (((p >> 3) & 3) << 1 | ((p >> 1) & 1))) << 3); }
+// 16-byte units of a row of LDS are swapped by its number, so that lanes that read a column of rows meet all banks, and
+// those that write one do: readers go by bits 0, 1, 3 and 4 of the row, writers by bits 0 to 3.
+// (unit ^ number: where unit is 4 kk + lg, the place for kk is that for 0 with the bits of 4 kk turned over; four rows on, bit 2
+// is another, and the place is that of kk with its higher bit turned over.)
 __device__ __forceinline__ int at_w(int p, int unit) { return p * kQ + ((unit ^ ((p >> 1) & 7)) << 3); }
 template <int NP>
 __device__ __forceinline__ int at_s(int p, int unit) {
-    const int h = NP == 128 ? ((p >> 3) & 3) << 2 | (p & 3) : ((p >> 3) & 3) << 1 | ((p >> 1) & 1);
+    const int top = (p >> 2 ^ p >> 4) & 1;
+    const int h = NP == 128 ? top << 3 | (p >> 3 & 1) << 2 | (p & 3) : top << 2 | (p >> 3 & 1) << 1 | (p >> 1 & 1);
     return p * NP + ((unit ^ h) << 3);
 }
+__device__ __forceinline__ int at_x(int p, int unit) { return at_s<kQ>(p, unit); }
+// kk and k of the place in a row four on from a reader's own
+template <int NP>
+__device__ __forceinline__ constexpr int turned(int kk, int k) { return 32 * (kk ^ (NP == 128 ? 2 * k : k)); }
 
 template <int NP, int PY>
 struct SweepLds {
@@ -591,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int e = 0; e < PY; ++e) sf[kk & 1][k][e] = *reinterpret_cast<const s8 *>(&sm.st[0][e][0] + ((at ^ 32 * kk) + 4 * NP * k));
+                for (int e = 0; e < PY; ++e) sf[kk & 1][k][e] = *reinterpret_cast<const s8 *>(&sm.st[0][e][0] + ((at ^ turned<NP>(kk, k)) + 4 * NP * k));
         }
     };
     auto read_x = [&](int c, int ks) __attribute__((always_inline)) {
@@ -600,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int e = 0; e < PY; ++e) xf[k][e] = *reinterpret_cast<const s8 *>(&sm.xt[0][e][0] + ((at ^ 32 * ks) + 4 * kQ * k));
+                for (int e = 0; e < PY; ++e) xf[k][e] = *reinterpret_cast<const s8 *>(&sm.xt[0][e][0] + ((at ^ turned<kQ>(ks, k)) + 4 * kQ * k));
         }
     };
     auto read_w = [&](int at, int j) __attribute__((always_inline)) {
@@ -674,6 +680,10 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
                 for (int k = 0; k < 2; ++k) acc[k] = product<PY>(xf[k], m, acc[k]);
             }
             load_cb(more2);
+            // x, z and tables of the chunks to come are waited for here, between the products, and not where they are used: 277
+            // us against 283 with waits as late as can be (B4 L4096 H64 64x128)
+            constexpr int kNewer = kKK * PY + 4;                                       // the loads of C and C B^T above
+            __builtin_amdgcn_s_waitcnt(0x0f70 | (kNewer & 15) | (kNewer >> 4) << 14);   // vmcnt
             if constexpr (Lds::kStates == 1) __syncthreads();   // the old state's parts are read
         }
         // the state behind the chunk
@@ -701,10 +711,10 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
             if (begin + c * kQ + t_l < end && out_p < np) {
                 if constexpr (FAST) {
                     if constexpr (sizeof(T) == 2)
-                        __builtin_nontemporal_store(u4{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])}, reinterpret_cast<u4 *>(y_p));
+                        *reinterpret_cast<u4 *>(y_p) = u4{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])};
                     else
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) __builtin_nontemporal_store(f4{y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]}, reinterpret_cast<f4 *>(y_p + 4 * k));
+                        for (int k = 0; k < 2; ++k) *reinterpret_cast<f4 *>(y_p + 4 * k) = f4{y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]};
                 } else {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
@@ -742,26 +752,29 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
         }
         put_tab(1);
         load_tab();
+        // (all that is loaded so far is there: else the waits of the loop, which hold for its first round as well, would be for
+        // the order of the loads above)
+        __builtin_amdgcn_s_waitcnt(0x0f70);     // vmcnt(0)
         __syncthreads();
 #pragma unroll 1
         for (int c = 0; c <= early; ++c) next(c, c);
         __syncthreads();
-    }
-    const auto follow = [](int k) { return k == 2 ? 0 : k + 1; };
-    int k3 = 0;                                      // c % 3
-    for (int c = 0; c < nch; ++c) {
-        const bool more2 = c + 2 < nch;
-        const int n3 = follow(k3), m3 = follow(n3);
-        if constexpr (!OWN)
-            if (threadIdx.x == 0) sm.bad[m3] = 0;
-        products(c, k3, more2);
-        store(c, k3);
-        put_tab(m3);
-        load_tab();
-        if (early) __syncthreads();
-        next(c + 1 + early, early ? m3 : n3);
-        if (!early) __syncthreads();
-        k3 = n3;
+        const auto follow = [](int k) { return k == 2 ? 0 : k + 1; };
+        int k3 = 0, c = 0;                           // c % 3, c
+        do {
+            const bool more2 = c + 2 < nch;
+            const int n3 = follow(k3), m3 = follow(n3);
+            if constexpr (!OWN)
+                if (threadIdx.x == 0) sm.bad[m3] = 0;
+            products(c, k3, more2);
+            store(c, k3);
+            put_tab(m3);
+            load_tab();
+            if (early) __syncthreads();
+            next(c + 1 + early, early ? m3 : n3);
+            if (!early) __syncthreads();
+            k3 = n3;
+        } while (++c < nch);
     }
 
     // ---- end states
