@@ -1518,7 +1518,8 @@ def _ssdconv_call(xbc, delta, A, w, h, conv_state, slots, sequences, bias, D, z,
 def ssdconv_fwd(xbc, delta, A, w, h, conv_state, offsets, slots=None, *, bias=None, D=None, z=None, delta_bias=None,
                 delta_softplus=False, fresh=None, max_seqlen=None, out=None, workspace=None, stream=None):
     """A Mamba-2 layer's mixer over packed sequences whose states lie in a pool: the causal convolution (+ SiLU) of
-    conv1d_fwd over the channels of x, B and C, and the multi-head scan of ssd_fwd behind it.
+    conv1d_fwd over the channels of x, B and C, and the multi-head scan of ssd_fwd behind it.  (For serving: no gradients;
+    those two have them.)
 
     xbc: [T, H P + 2 G N], a row (x [H, P], B [G, N], C [G, N]) for every token;  delta: [T, H];  z: [T, H, P] (all
     bf16, or all fp32), each possibly a slice of a joint projection's output (contiguous rows, evenly spaced);
