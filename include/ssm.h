@@ -718,8 +718,9 @@ size_t ssm_ssdconv_update_workspace_bytes(const ssm_ssdconv_shape *shape);
  *   conv_state [nslots, channels, width - 1]     dtype   likewise, oldest input first; unused when width is 1
  *   y          [tokens, nheads, headdim]         dtype   output, contiguous
  *   workspace  device memory of ssm_ssdconv_workspace_bytes() bytes, on 16 bytes
- * Outputs (y, h, conv_state, workspace) must not overlap inputs or each other.  Other tensors need no more alignment than their
- * elements'; z, y and h on 16 bytes with rows of such are the fast ones.  sequences or nheads == 0 is a no-op.
+ * Outputs (y, h, conv_state, workspace) must not overlap inputs or each other.  Other tensors need no more alignment than
+ * their elements'; a headdim that is a multiple of 8, and h on 16 bytes with a dstate that is one of 4, are the fast ones.
+ * sequences or nheads == 0 is a no-op.
  * Products on the bf16 matrix cores, fp32 factors in bf16 parts: three (all 24 bits) for the state, and for y three
  * (fp32) or two (bf16).  A NaN or infinity of x becomes NaN in its channel's outputs from its token on and in its
  * channel's state, one of B, C, z or delta in those that it enters; no other sequence sees it.  Deterministic.

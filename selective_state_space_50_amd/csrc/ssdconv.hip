@@ -56,6 +56,11 @@ typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+// 16 bytes at the address of an element: z may be a part of a wider row, whose length is no multiple of 16 bytes
+template <class T>
+struct Piece;
+template <> struct Piece<uint16_t> { typedef uint32_t type __attribute__((ext_vector_type(4), aligned(2))); };
+template <> struct Piece<float> { typedef uint32_t type __attribute__((ext_vector_type(4), aligned(4))); };
 
 __device__ __forceinline__ f4 mfma(s8 a, s8 b, f4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8, a), __builtin_bit_cast(b8, b), c, 0, 0, 0);
@@ -366,9 +371,8 @@ struct StateLds {
     float tab[3][kTabs][kQ];
 };
 
-// OWN: the segments' own end states, nothing else.  FAST: z and y in 16-byte pieces (headdim a multiple of 8, and so their
-// addresses; the masks of single elements, 64 lanes' worth in a register pair each, spill the scalar registers).
-// The chunk's work is one block of code, so that products, LDS and VALU overlap within a wave; what would branch is
+// OWN: the segments' own end states, nothing else.  FAST: z and y in 16-byte pieces (headdim a multiple of 8; the masks of
+// single elements, 64 lanes' worth in a register pair each, spill the scalar registers).  The chunk's work is one block of code, so that products, LDS and VALU overlap within a wave; what would branch is
 // done for nothing instead (channels behind the head's last, tokens behind the sequence's: their weights are zero and
 // their outputs are not stored; columns that the filter lacks: branches over them took 147 us instead of 122 on 13
 // sequences of 9001 tokens, H12 48x96, fp32, three columns).
@@ -565,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
         if constexpr (FAST) {
 #pragma unroll
             for (int k = 0; k < 8; k += 16 / static_cast<int>(sizeof(T)))
-                *reinterpret_cast<u4 *>(zq + k) = *reinterpret_cast<const u4 *>(z + k);
+                *reinterpret_cast<u4 *>(zq + k) = *reinterpret_cast<const typename Piece<T>::type *>(z + k);
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k) zq[k] = z[out_p + k < np ? k : 0];
@@ -711,10 +715,11 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
             if (begin + c * kQ + t_l < end && out_p < np) {
                 if constexpr (FAST) {
                     if constexpr (sizeof(T) == 2)
-                        *reinterpret_cast<u4 *>(y_p) = u4{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])};
+                        *reinterpret_cast<typename Piece<T>::type *>(y_p) = u4{pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7])};
                     else
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) *reinterpret_cast<f4 *>(y_p + 4 * k) = f4{y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]};
+                        for (int k = 0; k < 2; ++k)
+                            *reinterpret_cast<typename Piece<T>::type *>(y_p + 4 * k) = __builtin_bit_cast(u4, f4{y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]});
                 } else {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
@@ -981,7 +986,7 @@ hipError_t prompts(const SsdConvArgs &a, hipStream_t s) {
         e = launch_status(s);
         if (e != hipSuccess) return e;
     }
-    if (a.y_vec && (a.z_vec || !a.z)) hipLaunchKernelGGL((ssdconv_sweep_kernel<T, NP, PY, false, true>), grid, dim3(kThreads), 0, s, a);
+    if (a.P % 8 == 0) hipLaunchKernelGGL((ssdconv_sweep_kernel<T, NP, PY, false, true>), grid, dim3(kThreads), 0, s, a);
     else hipLaunchKernelGGL((ssdconv_sweep_kernel<T, NP, PY, false, false>), grid, dim3(kThreads), 0, s, a);
     return launch_status(s);
 }

@@ -1466,7 +1466,7 @@ SsdConvArgs ssdconv_args(const ssm_ssdconv_shape &s, const SsdConvPlan &p, const
     a.slots = slots; a.nslots = s.nslots; a.h = h; a.conv_state = conv_state; a.y = y;
     a.PB = static_cast<int>(p.blocks64); a.seg_len = static_cast<int>(p.seg_len); a.nseg_split = p.split;
     a.heads_run = static_cast<int>(p.heads_run);
-    a.chunks = p.chunks; a.items = p.items; a.z_vec = p.z_vec; a.y_vec = p.y_vec; a.h_vec = p.h_vec;
+    a.chunks = p.chunks; a.items = p.items; a.h_vec = p.h_vec;
     a.team = p.team; a.shares = p.shares;
     return a;
 }

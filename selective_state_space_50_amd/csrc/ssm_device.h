@@ -191,7 +191,7 @@ struct SsdConvArgs {
     int heads_run = 1;               // workgroups of a segment that share an XCD
     int nseg_split = 0;              // sequences in segments, their states in ws_state
     int64_t chunks = 0, items = 0;   // numbers of chunks and segments
-    int z_vec = 0, y_vec = 0, h_vec = 0;
+    int h_vec = 0;                   // states in 16-byte pieces
     int team = 1, shares = 1;        // one token: lanes of a row of states, workgroups of a head
     uint16_t *ws_bt = nullptr, *ws_c = nullptr;   // operands of B and C in parts
     float *ws_cb = nullptr, *ws_tab = nullptr, *ws_state = nullptr, *ws_dec = nullptr, *ws_x = nullptr;

@@ -1486,8 +1486,6 @@ int check_ssdconv(const ssm_ssdconv_shape *s, bool token, const void *xbc, const
         return SSM_EWORKSPACE;
     }
     const auto on16 = [](const Range &r) { return r.lo % 16 == 0; };
-    plan->z_vec = s->headdim % 8 == 0 && on16(all[2]) && plan->z_row * es % 16 == 0;
-    plan->y_vec = s->headdim % 8 == 0 && on16(all[4]);
     plan->h_vec = s->dstate % 4 == 0 && on16(all[12]);
     if (token) {
         // lanes of a row of states: four states each, or two single ones; and so many workgroups to a head that two are

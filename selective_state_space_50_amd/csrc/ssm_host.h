@@ -214,7 +214,7 @@ struct SsdConvPlan {
     int64_t heads_run = 1;            // workgroups of a segment that share an XCD: divides the segment's
     int64_t seg_len = 0;
     bool split = false;
-    bool z_vec = false, y_vec = false, h_vec = false;
+    bool h_vec = false;
     int team = 1, shares = 1;
     size_t c_off = 0, cb_off = 0, tab_off = 0, state_off = 0, dec_off = 0, ws_bytes = 0;
 };

@@ -408,6 +408,26 @@ def test_wide_heads_and_many_groups(ssm):
     prompt(ssm, [70, 9], 40, 8, 8, 40, 4, "bf16", 28)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("off", [1, 2, 4])
+def test_gate_and_outputs_off_16_bytes(ssm, dt, off):
+    """z and y at any element, whole pieces of 16 bytes or not: the same values to the bit, and nothing beside them."""
+    import torch
+    for P in (64, 48, 36):
+        c, dev = make([100, 31], 2, P, 64, 1, 4, dt, 29, joint=False)
+        T = 131
+        start = {n: dev[n].clone() for n in ("h", "conv_state")}
+        y = call(ssm, c, dev)
+        wide = torch.zeros(T, 2 * P + 9, dtype=y.dtype, device="cuda")
+        wide[:, off:off + 2 * P] = dev["z"].flatten(1)
+        room = torch.full((T * 2 * P + 16,), 3.0, dtype=y.dtype, device="cuda")
+        out = room[off:off + T * 2 * P].view(T, 2, P)
+        far = dict(dev, z=wide[:, off:off + 2 * P].unflatten(1, (2, P)), **start)
+        call(ssm, c, far, out=out)
+        assert torch.equal(out, y) and torch.equal(far["h"], dev["h"])
+        assert (room[:off] == 3.0).all() and (room[off + T * 2 * P:] == 3.0).all()
+
+
 def test_refusals(ssm):
     import torch
     c, dev = make([20, 30], 2, 32, 16, 1, 4, "bf16", 18)
