@@ -200,12 +200,11 @@ __device__ __forceinline__ void filter(const SsdConvArgs &a, int channel, float 
     bias = a.bias ? a.bias[channel] : 0.0f;
 }
 
-// One channel's last W - 1 inputs into its slot (what a sequence shorter than that leaves of the old ones in front).
+// One channel's last W - 1 inputs (what a sequence shorter than that leaves of the old ones in front), and into its slot.
 template <class T>
-__device__ __forceinline__ void conv_state_end(const SsdConvArgs &a, const Sequence &q, int channel) {
+__device__ __forceinline__ void last_inputs(const SsdConvArgs &a, const Sequence &q, int channel, T (&v)[3]) {
     const int W1 = a.W - 1;
-    T *st = static_cast<T *>(a.conv_state) + (static_cast<int64_t>(q.slot) * a.C + channel) * W1;
-    T v[3];
+    const T *st = static_cast<const T *>(a.conv_state) + (static_cast<int64_t>(q.slot) * a.C + channel) * W1;
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
         const int k = q.len + j;            // of the old columns and the tokens side by side
@@ -213,6 +212,11 @@ __device__ __forceinline__ void conv_state_end(const SsdConvArgs &a, const Seque
         else if (k < W1) v[j] = q.old ? st[k] : T{};
         else v[j] = static_cast<const T *>(a.xbc)[(q.first + static_cast<int64_t>(k - W1)) * a.x_row + channel];
     }
+}
+template <class T>
+__device__ __forceinline__ void keep_inputs(const SsdConvArgs &a, const Sequence &q, int channel, const T (&v)[3]) {
+    const int W1 = a.W - 1;
+    T *st = static_cast<T *>(a.conv_state) + (static_cast<int64_t>(q.slot) * a.C + channel) * W1;
 #pragma unroll
     for (int j = 0; j < 3; ++j)
         if (j < W1) st[j] = v[j];
@@ -738,9 +742,17 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
     // order with one loop.
     const int early = wv >> 2;
     auto next = [&](int c, int k3) __attribute__((always_inline)) {
-        stage(c, k3);
+        if (c < nch) stage(c, k3);
         load_x();
     };
+    // The convolution's state, by the sequence's first segment, which alone still reads it: this workgroup's own channels of x,
+    // and, one workgroup for each group, those of B and C (read by prep).  A channel a thread; loaded here, stored when all
+    // have read the old one.
+    const int extra = pb == 0 && h % (a.H / a.G) == 0 ? 2 * a.N : 0, e = static_cast<int>(threadIdx.x) - np;
+    const bool keeps = !OWN && seg == 0 && q.slot >= 0 && a.W > 1 && e < extra;
+    const int kept = e < 0 ? h * a.P + p0 + e + np : a.H * a.P + (e < a.N ? g * a.N + e : (a.G + g) * a.N + e - a.N);
+    T inputs[3];
+    if (keeps) last_inputs<T>(a, q, kept, inputs);
     if (nch > 0) {
         win.load(a, q, channel, t_x);
         t_x += kQ;
@@ -761,6 +773,7 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
         // the order of the loads above)
         __builtin_amdgcn_s_waitcnt(0x0f70);     // vmcnt(0)
         __syncthreads();
+        if (keeps) keep_inputs<T>(a, q, kept, inputs);
 #pragma unroll 1
         for (int c = 0; c <= early; ++c) next(c, c);
         __syncthreads();
@@ -780,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
             if (!early) __syncthreads();
             k3 = n3;
         } while (++c < nch);
-    }
+    } else if (keeps) keep_inputs<T>(a, q, kept, inputs);
 
     // ---- end states
     float *to = OWN ? a.ws_state + (item * a.H + h) * a.P * a.N
@@ -801,15 +814,6 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
     }
     if constexpr (OWN) {
         if (pb == 0 && threadIdx.x == 0) a.ws_dec[item * a.H + h] = whole;
-    } else if (seg == 0 && q.slot >= 0 && a.W > 1) {
-        // the convolution's state, by the sequence's first segment, which alone still reads it: this workgroup's own
-        // channels of x, and, one workgroup for each group, those of B and C (read by prep)
-        __syncthreads();
-        const int extra = pb == 0 && h % (a.H / a.G) == 0 ? 2 * a.N : 0;
-        for (int k = threadIdx.x; k < np + extra; k += kThreads) {
-            const int e = k - np;
-            conv_state_end<T>(a, q, k < np ? h * a.P + p0 + k : a.H * a.P + (e < a.N ? g * a.N + e : (a.G + g) * a.N + e - a.N));
-        }
     }
 }
 
