@@ -26,12 +26,12 @@
 // relative, a 128th of the half step that y's own rounding takes).  Exponents are sums over at most 32 tokens, forwards
 // for reads and backwards for writes, so that the nearest tokens' decays carry the smallest errors.
 //
-// What bounds it (B4 L4096 H64 P64 N128, gated, bf16; 271 us, whose 422 MB would take 84 at a copy's rate): the sweep, 250.
+// What bounds it (B4 L4096 H64 P64 N128, gated, bf16; 277 us, whose 422 MB would take 84 at a copy's rate): the sweep, 250.
 // Per chunk and head 10.6 MFLOP of products in parts (143 us at a large library product's rate) run beside about 500 vector
 // instructions a wave (convolution, decays, cutting into parts), 470 KB through LDS and 165 KB from the L2; the vector units are busy
 // 56% of the time, the matrix cores 30%, LDS about half, at a clock that the load itself holds near 2.0 GHz.  The prep's 20 us
 // are the 40 MB of operands and decays that it writes (all heads read them from the L2s; written past the caches: 2 us slower).
-// Workgroups of four waves and 32 channels, two to a CU: 304 us against 276.  B1 L32768 H24: 319 us in segments, 1714 whole.
+// Workgroups of four waves and 32 channels, two to a CU: 304 us against 276.  B1 L32768 H24: 312 to 327 us in segments, 1714 whole.
 #include "ssm_device.h"
 
 #include <type_traits>
