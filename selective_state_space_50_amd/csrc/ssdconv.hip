@@ -23,8 +23,11 @@
 // Numbers: a product of two 32-bit factors runs on v_mfma_f32_16x16x32_bf16 in parts: v = hi + mid + lo, bf16 each, holds
 // all 24 bits.  The state's factors are kept in three parts (six products: those whose order of magnitude is above 2^-24),
 // whatever the input type.  The factors of y are kept in three parts for fp32 and two for bf16 (three products; 2^-16
-// relative, a 128th of the half step that y's own rounding takes).  Exponents are sums over at most 32 tokens, forwards
-// for reads and backwards for writes, so that the nearest tokens' decays carry the smallest errors.
+// relative, a 128th of the half step that y's own rounding takes).  Exponents are sums over at most 32 tokens, made in 64
+// bits: forwards for reads and backwards for writes, which decays between the halves are products of.  Within a half the decay from
+// s to t is 2 to the difference of two sums from the half's start.  A difference keeps their absolute error, so one large step would
+// spoil every later pair (fp32, a step of dt A = 1600: 2e-4 of a pair's weight): the sums are kept as hi + lo, lo in the input
+// type (32 bits in all for bf16, 48 for fp32), and the difference is as good as its own 24 bits.
 //
 // What bounds it (B4 L4096 H64 P64 N128, gated, bf16; 277 us, whose 422 MB would take 84 at a copy's rate): the sweep, 250.
 // Per chunk and head 10.6 MFLOP of products in parts (143 us at a large library product's rate) run beside about 500 vector
@@ -43,12 +46,17 @@ constexpr int kQ = 64;                 // tokens of a chunk
 constexpr int kThreads = 512;          // of a sweep
 constexpr int kPrepThreads = 1024;
 constexpr int kPS = 3;                 // parts of the state's factors
-enum { kWr, kC32, kDt, kWb, kTabs };   // a head's tables of a chunk, 64 values each:
-// kWr  e^(cum_64 - cum_s) dt_s      weight of token s in the state passed on
-// kC32 exponent of the decay from the 32-token half's start to t, to the base 2 (the carried state's decay up to t
-//      is 2 to it, times the first half's whole in the second half)
-// kDt  dt_s
-// kWb  e^(to the half's end) dt_s   weight of the first half's token s in what the second half reads
+// A head's tables of a chunk, 64 values each but kWb:
+enum {
+    kWr = 0,            // e^(cum_64 - cum_s) dt_s    weight of token s in the state passed on
+    kC32 = kWr + kQ,    // exponent of the decay from the 32-token half's start to t, to the base 2 (the carried state's decay
+                        // up to t is 2 to it, times the first half's whole in the second half)
+    kDt = kC32 + kQ,    // dt_s
+    kWb = kDt + kQ,     // e^(to the half's end) dt_s: weight of the first half's token s in what the second half reads (32 values)
+    kLo = kWb + kQ / 2  // what kC32 was rounded by, in the input type
+};
+template <class T>
+constexpr int kTab = kLo + kQ * static_cast<int>(sizeof(T)) / 4;   // words of a head's tables
 
 typedef short s4 __attribute__((ext_vector_type(4)));
 typedef short s8 __attribute__((ext_vector_type(8)));
@@ -226,17 +234,21 @@ __device__ __forceinline__ void keep_inputs(const SsdConvArgs &a, const Sequence
 
 // Sums over the lanes up to (BACK: from) a lane, within each half of 32: four row shifts, then the first (second) row's whole.
 template <bool BACK>
-__device__ __forceinline__ float half_scan(float v, int lane) {
+__device__ __forceinline__ double half_scan(double v, int lane) {
+    const auto moved = [&](auto how) __attribute__((always_inline)) {
+        const int2 w = __builtin_bit_cast(int2, v);
+        return __builtin_bit_cast(double, int2{how(w.x), how(w.y)});
+    };
     const auto add = [&](auto ctrl) __attribute__((always_inline)) {
-        v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), decltype(ctrl)::value, 0xf, 0xf, true));
+        v += moved([](int w) { return __builtin_amdgcn_update_dpp(0, w, decltype(ctrl)::value, 0xf, 0xf, true); });
     };
     constexpr int kShift = BACK ? 0x100 : 0x110;     // row_shl, row_shr: what would come from another row is zero
     add(std::integral_constant<int, kShift + 1>{});
     add(std::integral_constant<int, kShift + 2>{});
     add(std::integral_constant<int, kShift + 4>{});
     add(std::integral_constant<int, kShift + 8>{});
-    const auto whole = [&](int l) { return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l)); };
-    const float lo = whole(BACK ? 16 : 15), hi = whole(BACK ? 48 : 47);
+    const double lo = moved([](int w) { return __builtin_amdgcn_readlane(w, BACK ? 16 : 15); });
+    const double hi = moved([](int w) { return __builtin_amdgcn_readlane(w, BACK ? 48 : 47); });
     if ((lane & 16) == (BACK ? 0 : 16)) v += lane < 32 ? lo : hi;
     return v;
 }
@@ -271,16 +283,18 @@ __global__ void __launch_bounds__(kPrepThreads) ssdconv_prep_kernel(SsdConvArgs 
             if (a.dbias) dt += a.dbias[h];
             if (a.softplus) dt = softplus_f(dt);
             if (t0 + lane >= q.len) dt = 0.0f;
-            const float step = dt * (a.A[h] * kLog2e);
-            const float pre = half_scan<false>(step, lane), suf = half_scan<true>(step, lane);   // inclusive
+            const double step = static_cast<double>(dt) * (static_cast<double>(a.A[h]) * 1.4426950408889634074);
+            const double pre = half_scan<false>(step, lane);                                             // inclusive
+            const float c32 = static_cast<float>(pre), suf = static_cast<float>(half_scan<true>(step, lane));
             const float behind = __shfl_down(suf, 1, 32);
             const float wb = __builtin_amdgcn_exp2f((lane & 31) == 31 ? 0.0f : behind) * dt;
-            const float half1 = __shfl(__builtin_amdgcn_exp2f(pre), 63, 64);
-            float *t = a.ws_tab + (u * a.H + h) * (kTabs * kQ) + lane;
-            t[kWr * kQ] = lane < 32 ? wb * half1 : wb;
-            t[kC32 * kQ] = pre;
-            t[kDt * kQ] = dt;
-            t[kWb * kQ] = wb;
+            const float half1 = __shfl(__builtin_amdgcn_exp2f(c32), 63, 64);
+            float *t = a.ws_tab + (u * a.H + h) * kTab<T>;
+            t[kWr + lane] = lane < 32 ? wb * half1 : wb;
+            t[kC32 + lane] = c32;
+            t[kDt + lane] = dt;
+            if (lane < 32) t[kWb + lane] = wb;
+            put(reinterpret_cast<T *>(t + kLo), lane, static_cast<float>(pre - static_cast<double>(c32)));
         }
         return;
     }
@@ -360,19 +374,20 @@ __device__ __forceinline__ int at_x(int p, int unit) { return at_s<kQ>(p, unit);
 template <int NP>
 __device__ __forceinline__ constexpr int turned(int kk, int k) { return 32 * (kk ^ (NP == 128 ? 2 * k : k)); }
 
-template <int NP, int PY>
+template <class T, int NP, int PY>
 struct SweepLds {
     static constexpr int kStates = PY == 3 && NP == 128 ? 1 : 2;   // (two copies of the state's parts where they fit)
     uint16_t xw[2][kPS][kQ * kQ];       // x behind the convolution, weighted for the state: [channel][token]
-    float tab[3][kTabs][kQ];
+    float tab[3][kTab<T>];
     uint16_t xt[2][PY][kQ * kQ];        // x behind the convolution
     uint16_t st[kStates][PY][kQ * NP];  // the chunk's start state: [channel][state]
     int bad[3];                         // whether a chunk's x has a NaN or infinity
     int first_bad[2][8][kQ];            // and where: [wave][channel] the first such token (64: none)
 };
+template <class T>
 struct StateLds {
     uint16_t xw[2][kPS][kQ * kQ];
-    float tab[3][kTabs][kQ];
+    float tab[3][kTab<T>];
 };
 
 // OWN: the segments' own end states, nothing else.  FAST: z and y in 16-byte pieces (headdim a multiple of 8; the masks of
@@ -382,8 +397,8 @@ struct StateLds {
 // sequences of 9001 tokens, H12 48x96, fp32, three columns).
 template <class T, int NP, int PY, bool OWN, bool FAST>
 __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(SsdConvArgs a) {
-    typedef SweepLds<NP, PY> Lds;
-    __shared__ __align__(16) typename std::conditional<OWN, StateLds, Lds>::type sm;
+    typedef SweepLds<T, NP, PY> Lds;
+    __shared__ __align__(16) typename std::conditional<OWN, StateLds<T>, Lds>::type sm;
     constexpr int kPT = NP == 128 ? 4 : 2;           // 16-channel tiles of a wave's states
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, lg = lane >> 4;
@@ -443,6 +458,11 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
     };
 
     // Every operand's pointer is a lane's own and moves by a chunk (scalar bases for all of them spilled).
+    // (a value made new where it is used: kept, as the compiler would have it, what follows from it takes registers all loop long)
+    auto fresh = [](int v) __attribute__((always_inline)) {
+        asm volatile("" : "+v"(v));
+        return v;
+    };
     // ---- staging: thread (channel lane, tokens 8 wv .. 8 wv + 7)
     const bool mine = lane < np;
     const int channel = h * a.P + p0 + (mine ? lane : 0);
@@ -466,22 +486,22 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
         }
         t_x += kQ;
     };
-    const float *tab_p = a.ws_tab + (u0 * a.H + h) * (kTabs * kQ) + 4 * (threadIdx.x < kTabs * kQ / 4 ? threadIdx.x : 0);
+    const float *tab_p = a.ws_tab + (u0 * a.H + h) * kTab<T> + 4 * (threadIdx.x < kTab<T> / 4 ? threadIdx.x : 0);
     f4 tq;
     int tabs = nch;                                  // tables still to load
     auto load_tab = [&]() __attribute__((always_inline)) {
         tq = *reinterpret_cast<const f4 *>(tab_p);
-        tab_p += --tabs > 0 ? static_cast<int64_t>(a.H) * (kTabs * kQ) : 0;
+        tab_p += --tabs > 0 ? static_cast<int64_t>(a.H) * kTab<T> : 0;
     };
     auto put_tab = [&](int k3) __attribute__((always_inline)) {
-        if (threadIdx.x < kTabs * kQ / 4) *reinterpret_cast<f4 *>(&sm.tab[k3][0][0] + 4 * threadIdx.x) = tq;
+        if (threadIdx.x < kTab<T> / 4) *reinterpret_cast<f4 *>(&sm.tab[k3][4 * threadIdx.x]) = tq;
     };
     auto stage = [&](int c, int k3) __attribute__((always_inline)) {     // (k3: c % 3)
         const int b = c & 1;
         float o[8];
         convolve<true>(win, 0, fw, fbias, 4, o);    // (a column that the filter lacks has weight 0)
-        const f4 w0 = *reinterpret_cast<const f4 *>(&sm.tab[k3][kWr][8 * wv]);
-        const f4 w1 = *reinterpret_cast<const f4 *>(&sm.tab[k3][kWr][8 * wv + 4]);
+        const f4 w0 = *reinterpret_cast<const f4 *>(&sm.tab[k3][kWr + 8 * wv]);
+        const f4 w1 = *reinterpret_cast<const f4 *>(&sm.tab[k3][kWr + 8 * wv + 4]);
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = o[i] * (i < 4 ? w0[i & 3] : w1[i & 3]);
@@ -575,18 +595,15 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
             for (int k = 0; k < 8; k += 16 / static_cast<int>(sizeof(T)))
                 *reinterpret_cast<u4 *>(zq + k) = *reinterpret_cast<const typename Piece<T>::type *>(z + k);
         } else {
+            const int has = fresh(np - out_p);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) zq[k] = z[out_p + k < np ? k : 0];
+            for (int k = 0; k < 8; ++k) zq[k] = z[k < has ? k : 0];
         }
     };
     // Places of this lane's operands in LDS; within the loop they are made new for each chunk (kept, as the compiler would
     // have it, each of the twenty takes a register, and the registers spill)
     int st_at = at_s<NP>(32 * ph + 8 * (lr >> 2) + (lr & 3), lg), xt_at = at_x(32 * ph + 8 * (lr >> 2) + (lr & 3), lg);
     int xw_at = at_w(16 * pt0 + lr, lg);
-    auto fresh = [](int v) __attribute__((always_inline)) {
-        asm volatile("" : "+v"(v));
-        return v;
-    };
     T *y_p = static_cast<T *>(a.y) + ((q.first + static_cast<int64_t>(begin) + t_l) * a.H + h) * a.P + p0 + out_p;
     const int64_t y_step = static_cast<int64_t>(kQ) * a.H * a.P;
 
@@ -596,16 +613,14 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
     auto ahead = []() __attribute__((always_inline)) { __builtin_amdgcn_sched_barrier(0); };
     constexpr int kKK = NP / 32;
     f4 acc[2];             // outputs: the wave's tokens, 4 lg + j of both tiles
-    s8 sf[2][2][PY];       // operands of the carried state, 32 states of them and the next 32.  Row r of tile k is channel
+    s8 sf[2][PY];          // operands of the carried state, 32 states of a tile and the next ones'.  Row r of tile k is channel
                            // 32 ph + 8 (r / 4) + 4 k + r % 4, so that a lane gets eight channels side by side
     s8 xf[2][PY];          // of x
-    s8 xw[2][2][kPS];      // of x weighted, for a tile of the state and the next one
-    auto read_state = [&](int at, int kk) __attribute__((always_inline)) {
+    s8 xw[2][kPS];         // of x weighted, of 32 tokens for a tile of the state, and the next ones'
+    auto read_state = [&](int at, int kk, int k) __attribute__((always_inline)) {
         if constexpr (!OWN) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int e = 0; e < PY; ++e) sf[kk & 1][k][e] = *reinterpret_cast<const s8 *>(&sm.st[0][e][0] + ((at ^ turned<NP>(kk, k)) + 4 * NP * k));
+            for (int e = 0; e < PY; ++e) sf[k][e] = *reinterpret_cast<const s8 *>(&sm.st[0][e][0] + ((at ^ turned<NP>(kk, k)) + 4 * NP * k));
         }
     };
     auto read_x = [&](int c, int ks) __attribute__((always_inline)) {
@@ -617,57 +632,56 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
                 for (int e = 0; e < PY; ++e) xf[k][e] = *reinterpret_cast<const s8 *>(&sm.xt[0][e][0] + ((at ^ turned<kQ>(ks, k)) + 4 * kQ * k));
         }
     };
-    auto read_w = [&](int at, int j) __attribute__((always_inline)) {
+    auto read_w = [&](int at, int j, int ks) __attribute__((always_inline)) {
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-            for (int k = 0; k < kPS; ++k) xw[j & 1][ks][k] = *reinterpret_cast<const s8 *>(&sm.xw[0][k][0] + ((at ^ 32 * ks) + 16 * kQ * j));
-    };
-    auto state_tile = [&](int j, float dec) __attribute__((always_inline)) {
-        f4 v = S[j] * dec;
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) v = product<kPS>(bf[ks], xw[j & 1][ks], v);
-        S[j] = v;
+        for (int k = 0; k < kPS; ++k) xw[ks][k] = *reinterpret_cast<const s8 *>(&sm.xw[0][k][0] + ((at ^ 32 * ks) + 16 * kQ * j));
     };
     float whole = 1.0f;      // decay over the segment
     auto products = [&](int c, int k3, bool more2) __attribute__((always_inline)) {
-        const float(&tab)[kTabs][kQ] = sm.tab[k3];
-        const float first = __builtin_amdgcn_exp2f(tab[kC32][31]), dec = first * __builtin_amdgcn_exp2f(tab[kC32][63]);
+        const float(&tab)[kTab<T>] = sm.tab[k3];
+        const T *lows = reinterpret_cast<const T *>(&tab[kLo]);
+        const float first = __builtin_amdgcn_exp2f(tab[kC32 + 31]), dec = first * __builtin_amdgcn_exp2f(tab[kC32 + 63]);
         const int w_at = fresh(xw_at + (c & 1) * (kPS * kQ * kQ));
         if constexpr (OWN) {
             whole *= dec;
-            read_w(w_at, 0);
+            read_w(w_at, 0, 0);
         } else {
             // the carried state's share
             const int at = fresh(st_at + (Lds::kStates == 2 ? c & 1 : 0) * (PY * kQ * NP));
-            read_state(at, 0);
-            const float ct = tab[kC32][t_l];
+            read_state(at, 0, 0);
+            const float ct = tab[kC32 + t_l], ct_lo = widen_v(lows[t_l]);
             const int s0 = 32 * (i >> 1) + 8 * lg;
             f4 d0, d1, c0, c1;
+            T lo[8];
             acc[0] = acc[1] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int kk = 0; kk < kKK; ++kk) {
-                if (kk + 1 < kKK) read_state(at, kk + 1);
+                read_state(at, kk, 1);
+                ahead();
+                acc[0] = product<PY>(sf[0], cf[kk], acc[0]);
+                if (kk + 1 < kKK) read_state(at, kk + 1, 0);
                 else {
-                    d0 = *reinterpret_cast<const f4 *>(&tab[kDt][s0]);
-                    d1 = *reinterpret_cast<const f4 *>(&tab[kDt][s0 + 4]);
-                    c0 = *reinterpret_cast<const f4 *>(&tab[kC32][s0]);
-                    c1 = *reinterpret_cast<const f4 *>(&tab[kC32][s0 + 4]);
+                    c0 = *reinterpret_cast<const f4 *>(&tab[kC32 + s0]);
+                    c1 = *reinterpret_cast<const f4 *>(&tab[kC32 + s0 + 4]);
+#pragma unroll
+                    for (int q = 0; q < 8; q += 16 / static_cast<int>(sizeof(T)))
+                        *reinterpret_cast<u4 *>(lo + q) = *reinterpret_cast<const u4 *>(lows + s0 + q);
                     read_x(c, i >> 1);
                 }
                 ahead();
-#pragma unroll
-                for (int k = 0; k < 2; ++k) acc[k] = product<PY>(sf[kk & 1][k], cf[kk], acc[k]);
+                acc[1] = product<PY>(sf[1], cf[kk], acc[1]);
             }
-            load_c(more2);
-            read_w(w_at, 0);
+            d0 = *reinterpret_cast<const f4 *>(&tab[kDt + s0]);
+            d1 = *reinterpret_cast<const f4 *>(&tab[kDt + s0 + 4]);
+            read_w(w_at, 0, 0);
             ahead();
             const float et = __builtin_amdgcn_exp2f(ct), e = i < 2 ? et : et * first;
             // the chunk's own share from the token's half of it: (C_t . B_s) decayed, D on the diagonal, times x
             float v[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-                const float f = __builtin_amdgcn_exp2f(ct - (q < 4 ? c0[q & 3] : c1[q & 3])) * (q < 4 ? d0[q & 3] : d1[q & 3]);
+                const float x = (ct - (q < 4 ? c0[q & 3] : c1[q & 3])) + (ct_lo - widen_v(lo[q]));
+                const float f = __builtin_amdgcn_exp2f(x) * (q < 4 ? d0[q & 3] : d1[q & 3]);
                 v[q] = __uint_as_float(__float_as_uint(cb[0][q >> 2][q & 3] * f) & below[q]) + diag[q];
             }
             s8 m[PY];
@@ -679,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
             }
             if (i >= 2) {   // and from the first half, of the second half's tokens
                 read_x(c, 0);
-                const f4 w0 = *reinterpret_cast<const f4 *>(&tab[kWb][8 * lg]), w1 = *reinterpret_cast<const f4 *>(&tab[kWb][8 * lg + 4]);
+                const f4 w0 = *reinterpret_cast<const f4 *>(&tab[kWb + 8 * lg]), w1 = *reinterpret_cast<const f4 *>(&tab[kWb + 8 * lg + 4]);
                 ahead();
 #pragma unroll
                 for (int q = 0; q < 8; ++q) v[q] = cb[1][q >> 2][q & 3] * (et * (q < 4 ? w0[q & 3] : w1[q & 3]));
@@ -687,6 +701,7 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
 #pragma unroll
                 for (int k = 0; k < 2; ++k) acc[k] = product<PY>(xf[k], m, acc[k]);
             }
+            load_c(more2);
             load_cb(more2);
             // x, z and tables of the chunks to come are waited for here, between the products, and not where they are used: 277
             // us against 283 with waits as late as can be (B4 L4096 H64 64x128)
@@ -697,9 +712,14 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
         // the state behind the chunk
 #pragma unroll
         for (int j = 0; j < kPT; ++j) {
-            if (j + 1 < kPT) read_w(w_at, j + 1);
+            const bool there = FAST || 16 * (pt0 + j) < np;
+            read_w(w_at, j, 1);
             ahead();
-            if (FAST || 16 * (pt0 + j) < np) state_tile(j, dec);
+            f4 v = S[j] * dec;
+            if (there) v = product<kPS>(bf[0], xw[0], v);
+            if (j + 1 < kPT) read_w(w_at, j + 1, 0);
+            ahead();
+            if (there) S[j] = product<kPS>(bf[1], xw[1], v);
         }
         load_b(more2);
         put_state(!OWN && Lds::kStates == 2 ? (c & 1) ^ 1 : 0);
@@ -725,9 +745,10 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
                         for (int k = 0; k < 2; ++k)
                             *reinterpret_cast<typename Piece<T>::type *>(y_p + 4 * k) = __builtin_bit_cast(u4, f4{y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]});
                 } else {
+                    const int has = fresh(np - out_p);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        if (out_p + k < np) put(y_p, k, y[k]);
+                        if (k < has) put(y_p, k, y[k]);
                 }
             }
             y_p += y_step;

@@ -1435,7 +1435,7 @@ int plan_ssdconv(const ssm_ssdconv_shape *s, bool token, SsdConvPlan *plan) {
     };
     plan->c_off = take(cg * 64 * np * 2 * py);
     plan->cb_off = take(cg * 64 * 64 * 4);
-    plan->tab_off = take(plan->chunks * s->nheads * 4 * 64 * 4);
+    plan->tab_off = take(plan->chunks * s->nheads * (3 * 64 * 4 + 32 * 4 + 64 * static_cast<int64_t>(dtype_size(s->dtype))));
     if (plan->split) {
         plan->state_off = take(plan->items * inner * s->dstate * 4);
         plan->dec_off = take(plan->items * s->nheads * 4);

@@ -1,0 +1,65 @@
+"""Where the served Mamba-2 mixer's numbers could lose digits, against the fp64 oracle."""
+import numpy as np
+import pytest
+
+from oracle.ssdconv_oracle import mixer
+from tests.gpu_util import to_host
+from tests.test_gpu_ssdconv import E, call, make, ssm, step  # noqa: F401  (ssm: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def pulse(dt, reset, at, L=130):
+    """Three heads whose tokens' outputs are single products: a large step at token `at`, then small ones; x is zero but at
+    token at + 1, B and C are 1.5 all along, one state, the filter a single column of one."""
+    import torch
+    P = 8
+    c, dev = make([L], 3, P, 1, 1, 1, dt, 30, gate=False, softplus=False, D=False, bias=False, joint=False, fresh=[1],
+                  A=np.array([-16.0, -4.0, -1.0]))
+    r = np.random.default_rng(31)
+    xbc, delta = np.zeros((L, 3 * P + 2), np.float32), (0.005 + 0.01 * r.random((L, 3))).astype(np.float32)
+    xbc[at + 1, :3 * P] = 1.0 + r.random(3 * P)
+    xbc[:, 3 * P:] = 1.5
+    delta[at] = reset
+    for n, a in (("xbc", xbc), ("delta", delta)):
+        dev[n] = torch.from_numpy(a).cuda().to(dev[n].dtype)
+        c[n] = dev[n].double().cpu().numpy()
+    c["w"], dev["w"] = np.ones_like(c["w"]), torch.ones_like(dev["w"])
+    return c, dev
+
+
+@pytest.mark.parametrize("at", [0, 5, 30, 31, 40, 62, 63])
+@pytest.mark.parametrize("dt,reset", [("f32", 20.0), ("f32", 100.0), ("f32", 4000.0), ("bf16", 4000.0), ("bf16", 30000.0)])
+def test_decays_behind_a_large_step(ssm, dt, reset, at):  # noqa: F811
+    """A step that leaves nothing of what was before must not touch the decays between the tokens behind it.
+
+    One product a token, so the error is relative to the value: silu of x, B and C 6 * 2^-24 each; a product of three-part
+    factors leaves out 3 * 2^-24 and rounds 3 times, C B and then with x (or the state): 12 and 3; the decay's up to
+    three factors and the step in front 2 each: 8; a sum over 32 tokens or a chunk's chain 10: 51, taken as 60; and the exponent X
+    from the pulse on, relative to itself a half step for each of the difference (or the sum) and the exponential's argument, twice
+    behind a half or a chunk: 4 X.  bf16: half a step of the output; the two parts of a factor 2^-17, twice in each of two products
+    and lo * lo 2^-18: 6 * 2^-17; lo of the sums is half a bf16 step off, at a sum of 16 * 30000 * 1.4427 < 2^20 that is
+    2^(20 - 24 - 1 - 8) twice, times log 2: less than 2^-12."""
+    c, dev = pulse(dt, reset, at)
+    ref = mixer(c)["y"]
+    y = call(ssm, c, dev)
+    X = -np.cumsum(np.where(np.arange(130)[:, None] > at + 1, c["delta"] * c["A"], 0.0), 0)[:, :, None]
+    tol = (60 + 4 * X) * E
+    if dt == "bf16":
+        tol = tol + 2.0 ** -8 + 6 * 2.0 ** -17 + 2.0 ** -12
+    worst = (np.abs(to_host(y).reshape(ref.shape) - ref) / (tol * np.abs(ref) + 1e-30)).max()
+    assert worst <= 1.0, f"{worst:.3g} of the tolerance"
+
+
+@pytest.mark.parametrize("reset", [20.0, 400.0])
+def test_prompt_and_tokens_behind_a_large_step(ssm, reset):  # noqa: F811
+    """The same tokens one by one: both forms lie within the tolerance above of the oracle, so they are twice it apart at most."""
+    import torch
+    c, dev = pulse("f32", reset, 3, L=64)
+    y = call(ssm, c, dict(dev, h=dev["h"].clone(), conv_state=dev["conv_state"].clone()))
+    dev["h"].zero_()
+    t = torch.cat([step(ssm, c, dev, slice(i, i + 1)) for i in range(64)])
+    X = -np.cumsum(np.where(np.arange(64)[:, None] > 4, c["delta"] * c["A"], 0.0), 0)[:, :, None]
+    a, b = to_host(y).reshape(64, 3, -1), to_host(t).reshape(64, 3, -1)
+    # (the token form multiplies a decay and rounds the state once a token: 3 * 2^-24 more for each of 60)
+    assert (np.abs(a - b) <= (2 * (60 + 4 * X) + 180) * E * np.abs(b) + 1e-30).all()
