@@ -721,8 +721,7 @@ size_t ssm_ssdconv_update_workspace_bytes(const ssm_ssdconv_shape *shape);
  * Outputs (y, h, conv_state, workspace) must not overlap inputs or each other.  Other tensors need no more alignment than
  * their elements'; a headdim that is a multiple of 8, and h on 16 bytes with a dstate that is one of 4, are the fast ones.
  * sequences or nheads == 0 is a no-op.
- * Products on the bf16 matrix cores, fp32 factors in bf16 parts: three (all 24 bits) for the state, and for y three
- * (fp32) or two (bf16).  A NaN or infinity of x becomes NaN in its channel's outputs from its token on and in its
+ * Products on the bf16 matrix cores, fp32 factors in three bf16 parts (all 24 bits).  A NaN or infinity of x becomes NaN in its channel's outputs from its token on and in its
  * channel's state, one of B, C, z or delta in those that it enters; no other sequence sees it.  Deterministic.
  * SSM_EUNSUPPORTED: dstate over SSM_SSDCONV_MAX_DSTATE, sequences over 65535, tokens over 2^28, nheads over 32768, nheads *
  * headdim over 2^24, ngroups * dstate or (ssm_ssdconv_fwd) x_row over 2^22, too many workgroups.

@@ -21,13 +21,13 @@
 //    join passes the states on, and the sweep starts every segment from its own.
 //
 // Numbers: a product of two 32-bit factors runs on v_mfma_f32_16x16x32_bf16 in parts: v = hi + mid + lo, bf16 each, holds
-// all 24 bits.  The state's factors are kept in three parts (six products: those whose order of magnitude is above 2^-24),
-// whatever the input type.  The factors of y are kept in three parts for fp32 and two for bf16 (three products; 2^-16
-// relative, a 128th of the half step that y's own rounding takes).  Exponents are sums over at most 32 tokens, made in 64
-// bits: forwards for reads and backwards for writes, which decays between the halves are products of.  Within a half the decay from
-// s to t is 2 to the difference of two sums from the half's start.  A difference keeps their absolute error, so one large step would
-// spoil every later pair (fp32, a step of dt A = 1600: 2e-4 of a pair's weight): the sums are kept as hi + lo, lo in the input
-// type (32 bits in all for bf16, 48 for fp32), and the difference is as good as its own 24 bits.
+// all 24 bits, and six products of parts those whose order of magnitude is above 2^-24.  That holds for the state and for y,
+// whatever the input type: two parts of y's factors left 0.23% of bf16 outputs a step off, three 0.010% (a 32-bit form 0.011%).
+// Exponents are sums over at most 32 tokens, made in 64 bits: forwards for reads and backwards for writes, which decays between
+// the halves are products of.  Within a half the decay from s to t is 2 to the difference of two sums from the half's start.  A
+// difference keeps their absolute error, so one large step would spoil every later pair (fp32, a step of dt A = 1600: 2e-4 of a
+// pair's weight): the sums are kept as hi + lo, lo in the input type (32 bits in all for bf16, 48 for fp32), and the
+// difference is as good as its own 24 bits.
 //
 // What bounds it (B4 L4096 H64 P64 N128, gated, bf16; 277 us, whose 422 MB would take 84 at a copy's rate): the sweep, 250.
 // Per chunk and head 10.6 MFLOP of products in parts (143 us at a large library product's rate) run beside about 500 vector
@@ -45,7 +45,7 @@ namespace {
 constexpr int kQ = 64;                 // tokens of a chunk
 constexpr int kThreads = 512;          // of a sweep
 constexpr int kPrepThreads = 1024;
-constexpr int kPS = 3;                 // parts of the state's factors
+constexpr int kParts = 3;              // bf16 parts of a product's factors
 // A head's tables of a chunk, 64 values each but kWb:
 enum {
     kWr = 0,            // e^(cum_64 - cum_s) dt_s    weight of token s in the state passed on
@@ -253,9 +253,9 @@ __device__ __forceinline__ double half_scan(double v, int lane) {
     return v;
 }
 
-// NP: the states padded to 64 or 128; PY: parts of y's factors.  Sixteen waves (eight: the same 20 us on B4 L4096 H64: about 5
+// NP: the states padded to 64 or 128.  Sixteen waves (eight: the same 20 us on B4 L4096 H64: about 5
 // of one thing waiting for the other, then 40 MB of operands and tables written).
-template <class T, int NP, int PY>
+template <class T, int NP>
 __global__ void __launch_bounds__(kPrepThreads) ssdconv_prep_kernel(SsdConvArgs a) {
     constexpr int kRow = NP + 4;
     __shared__ __align__(16) float tile[2][kQ][kRow];    // B and C, token by token
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kPrepThreads) ssdconv_prep_kernel(SsdConvArgs 
     constexpr int kTok = kQ * 2 * NP / kPrepThreads;     // 16 or 8
     const int ch = threadIdx.x % (2 * NP), n = ch % NP, which = ch / NP, from = threadIdx.x / (2 * NP) * kTok;
     const int channel = a.H * a.P + (which * a.G + g) * a.N + n;
-    s8 *bt = reinterpret_cast<s8 *>(a.ws_bt) + (u * a.G + g) * (NP / 16 * 2 * kPS * 64);
+    s8 *bt = reinterpret_cast<s8 *>(a.ws_bt) + (u * a.G + g) * (NP / 16 * 2 * kParts * 64);
     Window<T, 8> in;
     float w[4], bias = 0.0f;
     if (n < a.N) {
@@ -326,31 +326,31 @@ __global__ void __launch_bounds__(kPrepThreads) ssdconv_prep_kernel(SsdConvArgs 
         }
         if (which == 0) {
             // operands of the state's product: lane (n % 16, s / 8 % 4) of slice n / 16 holds B[s .. s + 7][n]
-            s8 part[kPS];
-            split8<kPS>(o, part);
+            s8 part[kParts];
+            split8<kParts>(o, part);
 #pragma unroll
-            for (int k = 0; k < kPS; ++k)
-                bt[((n / 16 * 2 + t / 32) * kPS + k) * 64 + n % 16 + 16 * (t % 32 / 8)] = part[k];
+            for (int k = 0; k < kParts; ++k)
+                bt[((n / 16 * 2 + t / 32) * kParts + k) * 64 + n % 16 + 16 * (t % 32 / 8)] = part[k];
         }
     }
     __syncthreads();
     // ---- operands of C, and C B^T below the diagonal: wave (i, k) takes C's tokens 16 i .. and B's 16 k .., and of the
     // operands every fourth
     const int i = wv & 3, k = wv >> 2;
-    s8 *cs = reinterpret_cast<s8 *>(a.ws_c) + ((u * a.G + g) * 4 + i) * (NP / 32 * PY * 64) + lane;
+    s8 *cs = reinterpret_cast<s8 *>(a.ws_c) + ((u * a.G + g) * 4 + i) * (NP / 32 * kParts * 64) + lane;
     f4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int kk = 0; kk < NP / 32; ++kk) {
         if (k > i && kk != k) continue;
-        s8 cf[PY], bf[PY];
-        split8<PY>(&tile[1][16 * i + lr][32 * kk + 8 * lg], cf);
+        s8 cf[kParts], bf[kParts];
+        split8<kParts>(&tile[1][16 * i + lr][32 * kk + 8 * lg], cf);
         if (kk == k) {
 #pragma unroll
-            for (int e = 0; e < PY; ++e) cs[(kk * PY + e) * 64] = cf[e];
+            for (int e = 0; e < kParts; ++e) cs[(kk * kParts + e) * 64] = cf[e];
         }
         if (k > i) continue;
-        split8<PY>(&tile[0][16 * k + lr][32 * kk + 8 * lg], bf);
-        acc = product<PY>(bf, cf, acc);
+        split8<kParts>(&tile[0][16 * k + lr][32 * kk + 8 * lg], bf);
+        acc = product<kParts>(bf, cf, acc);
     }
     // lane: token 16 i + lr, s = 16 k + 4 lg + 0 .. 3
     if (k <= i) *reinterpret_cast<f4 *>(a.ws_cb + ((u * a.G + g) * kQ + 16 * i + lr) * kQ + 16 * k + 4 * lg) = acc;
@@ -374,30 +374,30 @@ __device__ __forceinline__ int at_x(int p, int unit) { return at_s<kQ>(p, unit);
 template <int NP>
 __device__ __forceinline__ constexpr int turned(int kk, int k) { return 32 * (kk ^ (NP == 128 ? 2 * k : k)); }
 
-template <class T, int NP, int PY>
+template <class T, int NP>
 struct SweepLds {
-    static constexpr int kStates = PY == 3 && NP == 128 ? 1 : 2;   // (two copies of the state's parts where they fit)
-    uint16_t xw[2][kPS][kQ * kQ];       // x behind the convolution, weighted for the state: [channel][token]
+    static constexpr int kStates = NP == 128 ? 1 : 2;       // (two copies of the state's parts where they fit)
+    uint16_t xw[2][kParts][kQ * kQ];       // x behind the convolution, weighted for the state: [channel][token]
     float tab[3][kTab<T>];
-    uint16_t xt[2][PY][kQ * kQ];        // x behind the convolution
-    uint16_t st[kStates][PY][kQ * NP];  // the chunk's start state: [channel][state]
+    uint16_t xt[2][kParts][kQ * kQ];        // x behind the convolution
+    uint16_t st[kStates][kParts][kQ * NP];  // the chunk's start state: [channel][state]
     int bad[3];                         // whether a chunk's x has a NaN or infinity
     int first_bad[2][8][kQ];            // and where: [wave][channel] the first such token (64: none)
 };
 template <class T>
 struct StateLds {
-    uint16_t xw[2][kPS][kQ * kQ];
+    uint16_t xw[2][kParts][kQ * kQ];
     float tab[3][kTab<T>];
 };
 
-// OWN: the segments' own end states, nothing else.  FAST: z and y in 16-byte pieces (headdim a multiple of 8; the masks of
-// single elements, 64 lanes' worth in a register pair each, spill the scalar registers).  The chunk's work is one block of code, so that products, LDS and VALU overlap within a wave; what would branch is
+// PARTS: kParts.  OWN: the segments' own end states, nothing else.  FAST: z and y in 16-byte pieces (headdim a multiple of
+// 8).  The chunk's work is one block of code, so that products, LDS and VALU overlap within a wave; what would branch is
 // done for nothing instead (channels behind the head's last, tokens behind the sequence's: their weights are zero and
 // their outputs are not stored; columns that the filter lacks: branches over them took 147 us instead of 122 on 13
 // sequences of 9001 tokens, H12 48x96, fp32, three columns).
-template <class T, int NP, int PY, bool OWN, bool FAST>
+template <class T, int NP, int PARTS, bool OWN, bool FAST>
 __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(SsdConvArgs a) {
-    typedef SweepLds<T, NP, PY> Lds;
+    typedef SweepLds<T, NP> Lds;
     __shared__ __align__(16) typename std::conditional<OWN, StateLds<T>, Lds>::type sm;
     constexpr int kPT = NP == 128 ? 4 : 2;           // 16-channel tiles of a wave's states
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -447,12 +447,12 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
         if constexpr (!OWN) {
 #pragma unroll
             for (int i = 0; i < kPT; ++i) {
-                uint32_t w[PY][2];
+                uint32_t w[PARTS][2];
                 const float v[4] = {S[i][0], S[i][1], S[i][2], S[i][3]};
-                split<PY, 4>(v, w);
+                split<PARTS, 4>(v, w);
                 const int at = at_s<NP>(16 * (pt0 + i) + lr, 2 * sl + (lg >> 1)) + 4 * (lg & 1);
 #pragma unroll
-                for (int k = 0; k < PY; ++k) *reinterpret_cast<u2 *>(&sm.st[b][k][at]) = u2{w[k][0], w[k][1]};
+                for (int k = 0; k < PARTS; ++k) *reinterpret_cast<u2 *>(&sm.st[b][k][at]) = u2{w[k][0], w[k][1]};
             }
         }
     };
@@ -505,15 +505,15 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = o[i] * (i < 4 ? w0[i & 3] : w1[i & 3]);
-        s8 part[kPS];
-        split8<kPS>(v, part);
+        s8 part[PARTS];
+        split8<PARTS>(v, part);
 #pragma unroll
-        for (int k = 0; k < kPS; ++k) *reinterpret_cast<s8 *>(&sm.xw[b][k][at_w(lane, wv)]) = part[k];
+        for (int k = 0; k < PARTS; ++k) *reinterpret_cast<s8 *>(&sm.xw[b][k][at_w(lane, wv)]) = part[k];
         if constexpr (!OWN) {
-            s8 y[PY];
-            split8<PY>(o, y);
+            s8 y[PARTS];
+            split8<PARTS>(o, y);
 #pragma unroll
-            for (int k = 0; k < PY; ++k) *reinterpret_cast<s8 *>(&sm.xt[b][k][at_x(lane, wv)]) = y[k];
+            for (int k = 0; k < PARTS; ++k) *reinterpret_cast<s8 *>(&sm.xt[b][k][at_x(lane, wv)]) = y[k];
             // A NaN or infinity of x must not meet the zeros above the diagonal: it is taken out here, and y gets
             // NaN from its token on (through the state, from the next chunk on, all by itself).  (The sum of eight
             // times zero is not zero where one of them is such a value.)
@@ -528,9 +528,9 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
                         first = 8 * wv + i;
                         o[i] = 0.0f;
                     }
-                split8<PY>(o, y);
+                split8<PARTS>(o, y);
 #pragma unroll
-                for (int k = 0; k < PY; ++k) *reinterpret_cast<s8 *>(&sm.xt[b][k][at_x(lane, wv)]) = y[k];
+                for (int k = 0; k < PARTS; ++k) *reinterpret_cast<s8 *>(&sm.xt[b][k][at_x(lane, wv)]) = y[k];
                 if (first < kQ) sm.bad[k3] = 1;
             }
             sm.first_bad[b][wv][lane] = first;
@@ -538,14 +538,14 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
     };
 
     // ---- operands of B (the wave's 16 states)
-    s8 bf[2][kPS];
-    const s8 *b_p = reinterpret_cast<const s8 *>(a.ws_bt) + ((u0 * a.G + g) * (NP / 16) + sl) * (2 * kPS * 64) + lane;
-    const int64_t b_step = static_cast<int64_t>(a.G) * (NP / 16 * 2 * kPS * 64);
+    s8 bf[2][PARTS];
+    const s8 *b_p = reinterpret_cast<const s8 *>(a.ws_bt) + ((u0 * a.G + g) * (NP / 16) + sl) * (2 * PARTS * 64) + lane;
+    const int64_t b_step = static_cast<int64_t>(a.G) * (NP / 16 * 2 * PARTS * 64);
     auto load_b = [&](bool more) __attribute__((always_inline)) {
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-            for (int k = 0; k < kPS; ++k) bf[ks][k] = b_p[(ks * kPS + k) * 64];
+            for (int k = 0; k < PARTS; ++k) bf[ks][k] = b_p[(ks * PARTS + k) * 64];
         b_p += more ? b_step : 0;
     };
 
@@ -553,14 +553,14 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
     const int i = wv < 4 ? wv : 7 - wv, ph = wv >> 2;      // (a SIMD's two waves: token blocks of 0 and 3, or of 1 and 2)
     const int t_l = 16 * i + lr, out_p = 32 * ph + 8 * lg;
     const float dsk = a.Dskip ? a.Dskip[h] : 0.0f;
-    s8 cf[NP / 32][PY];
-    const s8 *c_p = reinterpret_cast<const s8 *>(a.ws_c) + ((u0 * a.G + g) * 4 + i) * (NP / 32 * PY * 64) + lane;
-    const int64_t c_step = static_cast<int64_t>(a.G) * (4 * NP / 32 * PY * 64);
+    s8 cf[NP / 32][PARTS];
+    const s8 *c_p = reinterpret_cast<const s8 *>(a.ws_c) + ((u0 * a.G + g) * 4 + i) * (NP / 32 * PARTS * 64) + lane;
+    const int64_t c_step = static_cast<int64_t>(a.G) * (4 * NP / 32 * PARTS * 64);
     auto load_c = [&](bool more) __attribute__((always_inline)) {
 #pragma unroll
         for (int kk = 0; kk < NP / 32; ++kk)
 #pragma unroll
-            for (int k = 0; k < PY; ++k) cf[kk][k] = c_p[(kk * PY + k) * 64];
+            for (int k = 0; k < PARTS; ++k) cf[kk][k] = c_p[(kk * PARTS + k) * 64];
         c_p += more ? c_step : 0;
     };
     // s <= t of the block on the diagonal as all bits or none, and D where s = t, for the lane's eight s
@@ -613,41 +613,41 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
     auto ahead = []() __attribute__((always_inline)) { __builtin_amdgcn_sched_barrier(0); };
     constexpr int kKK = NP / 32;
     f4 acc[2];             // outputs: the wave's tokens, 4 lg + j of both tiles
-    s8 sf[2][PY];          // operands of the carried state, 32 states of a tile and the next ones'.  Row r of tile k is channel
+    s8 sf[2][PARTS];       // operands of the carried state, 32 states of a tile and the next ones'.  Row r of tile k is channel
                            // 32 ph + 8 (r / 4) + 4 k + r % 4, so that a lane gets eight channels side by side
-    s8 xf[2][PY];          // of x
-    s8 xw[2][kPS];         // of x weighted, of 32 tokens for a tile of the state, and the next ones'
+    s8 xf[2][PARTS];       // of x
+    s8 xw[2][PARTS];       // of x weighted, of 32 tokens for a tile of the state, and the next ones'
     auto read_state = [&](int at, int kk, int k) __attribute__((always_inline)) {
         if constexpr (!OWN) {
 #pragma unroll
-            for (int e = 0; e < PY; ++e) sf[k][e] = *reinterpret_cast<const s8 *>(&sm.st[0][e][0] + ((at ^ turned<NP>(kk, k)) + 4 * NP * k));
+            for (int e = 0; e < PARTS; ++e) sf[k][e] = *reinterpret_cast<const s8 *>(&sm.st[0][e][0] + ((at ^ turned<NP>(kk, k)) + 4 * NP * k));
         }
     };
     auto read_x = [&](int c, int ks) __attribute__((always_inline)) {
         if constexpr (!OWN) {
-            const int at = fresh(xt_at + (c & 1) * (PY * kQ * kQ));
+            const int at = fresh(xt_at + (c & 1) * (PARTS * kQ * kQ));
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int e = 0; e < PY; ++e) xf[k][e] = *reinterpret_cast<const s8 *>(&sm.xt[0][e][0] + ((at ^ turned<kQ>(ks, k)) + 4 * kQ * k));
+                for (int e = 0; e < PARTS; ++e) xf[k][e] = *reinterpret_cast<const s8 *>(&sm.xt[0][e][0] + ((at ^ turned<kQ>(ks, k)) + 4 * kQ * k));
         }
     };
     auto read_w = [&](int at, int j, int ks) __attribute__((always_inline)) {
 #pragma unroll
-        for (int k = 0; k < kPS; ++k) xw[ks][k] = *reinterpret_cast<const s8 *>(&sm.xw[0][k][0] + ((at ^ 32 * ks) + 16 * kQ * j));
+        for (int k = 0; k < PARTS; ++k) xw[ks][k] = *reinterpret_cast<const s8 *>(&sm.xw[0][k][0] + ((at ^ 32 * ks) + 16 * kQ * j));
     };
     float whole = 1.0f;      // decay over the segment
     auto products = [&](int c, int k3, bool more2) __attribute__((always_inline)) {
         const float(&tab)[kTab<T>] = sm.tab[k3];
         const T *lows = reinterpret_cast<const T *>(&tab[kLo]);
         const float first = __builtin_amdgcn_exp2f(tab[kC32 + 31]), dec = first * __builtin_amdgcn_exp2f(tab[kC32 + 63]);
-        const int w_at = fresh(xw_at + (c & 1) * (kPS * kQ * kQ));
+        const int w_at = fresh(xw_at + (c & 1) * (PARTS * kQ * kQ));
         if constexpr (OWN) {
             whole *= dec;
             read_w(w_at, 0, 0);
         } else {
             // the carried state's share
-            const int at = fresh(st_at + (Lds::kStates == 2 ? c & 1 : 0) * (PY * kQ * NP));
+            const int at = fresh(st_at + (Lds::kStates == 2 ? c & 1 : 0) * (PARTS * kQ * NP));
             read_state(at, 0, 0);
             const float ct = tab[kC32 + t_l], ct_lo = widen_v(lows[t_l]);
             const int s0 = 32 * (i >> 1) + 8 * lg;
@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
             for (int kk = 0; kk < kKK; ++kk) {
                 read_state(at, kk, 1);
                 ahead();
-                acc[0] = product<PY>(sf[0], cf[kk], acc[0]);
+                acc[0] = product<PARTS>(sf[0], cf[kk], acc[0]);
                 if (kk + 1 < kKK) read_state(at, kk + 1, 0);
                 else {
                     c0 = *reinterpret_cast<const f4 *>(&tab[kC32 + s0]);
@@ -669,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
                     read_x(c, i >> 1);
                 }
                 ahead();
-                acc[1] = product<PY>(sf[1], cf[kk], acc[1]);
+                acc[1] = product<PARTS>(sf[1], cf[kk], acc[1]);
             }
             d0 = *reinterpret_cast<const f4 *>(&tab[kDt + s0]);
             d1 = *reinterpret_cast<const f4 *>(&tab[kDt + s0 + 4]);
@@ -684,12 +684,12 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
                 const float f = __builtin_amdgcn_exp2f(x) * (q < 4 ? d0[q & 3] : d1[q & 3]);
                 v[q] = __uint_as_float(__float_as_uint(cb[0][q >> 2][q & 3] * f) & below[q]) + diag[q];
             }
-            s8 m[PY];
-            split8<PY>(v, m);
+            s8 m[PARTS];
+            split8<PARTS>(v, m);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 acc[k] *= e;
-                acc[k] = product<PY>(xf[k], m, acc[k]);
+                acc[k] = product<PARTS>(xf[k], m, acc[k]);
             }
             if (i >= 2) {   // and from the first half, of the second half's tokens
                 read_x(c, 0);
@@ -697,15 +697,15 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
                 ahead();
 #pragma unroll
                 for (int q = 0; q < 8; ++q) v[q] = cb[1][q >> 2][q & 3] * (et * (q < 4 ? w0[q & 3] : w1[q & 3]));
-                split8<PY>(v, m);
+                split8<PARTS>(v, m);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) acc[k] = product<PY>(xf[k], m, acc[k]);
+                for (int k = 0; k < 2; ++k) acc[k] = product<PARTS>(xf[k], m, acc[k]);
             }
             load_c(more2);
             load_cb(more2);
             // x, z and tables of the chunks to come are waited for here, between the products, and not where they are used: 277
             // us against 283 with waits as late as can be (B4 L4096 H64 64x128)
-            constexpr int kNewer = kKK * PY + 4;                                       // the loads of C and C B^T above
+            constexpr int kNewer = kKK * PARTS + 4;                                    // the loads of C and C B^T above
             __builtin_amdgcn_s_waitcnt(0x0f70 | (kNewer & 15) | (kNewer >> 4) << 14);   // vmcnt
             if constexpr (Lds::kStates == 1) __syncthreads();   // the old state's parts are read
         }
@@ -716,10 +716,10 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
             read_w(w_at, j, 1);
             ahead();
             f4 v = S[j] * dec;
-            if (there) v = product<kPS>(bf[0], xw[0], v);
+            if (there) v = product<PARTS>(bf[0], xw[0], v);
             if (j + 1 < kPT) read_w(w_at, j + 1, 0);
             ahead();
-            if (there) S[j] = product<kPS>(bf[1], xw[1], v);
+            if (there) S[j] = product<PARTS>(bf[1], xw[1], v);
         }
         load_b(more2);
         put_state(!OWN && Lds::kStates == 2 ? (c & 1) ^ 1 : 0);
@@ -992,16 +992,16 @@ __global__ void __launch_bounds__(256) ssdconv_token_kernel(SsdConvArgs a) {
     }
 }
 
-template <class T, int NP, int PY>
+template <class T, int NP>
 hipError_t prompts(const SsdConvArgs &a, hipStream_t s) {
     const unsigned heads = static_cast<unsigned>((a.H + 63) / 64);
-    hipLaunchKernelGGL((ssdconv_prep_kernel<T, NP, PY>), dim3(static_cast<unsigned>(a.chunks), static_cast<unsigned>(a.G) + heads),
+    hipLaunchKernelGGL((ssdconv_prep_kernel<T, NP>), dim3(static_cast<unsigned>(a.chunks), static_cast<unsigned>(a.G) + heads),
                        dim3(kPrepThreads), 0, s, a);
     hipError_t e = launch_status(s);
     if (e != hipSuccess) return e;
     const dim3 grid(static_cast<unsigned>((a.items * a.H * a.PB / a.heads_run + 7) / 8 * 8 * a.heads_run));
     if (a.nseg_split) {
-        hipLaunchKernelGGL((ssdconv_sweep_kernel<T, NP, PY, true, true>), grid, dim3(kThreads), 0, s, a);
+        hipLaunchKernelGGL((ssdconv_sweep_kernel<T, NP, kParts, true, true>), grid, dim3(kThreads), 0, s, a);
         e = launch_status(s);
         if (e != hipSuccess) return e;
         const int wide = a.h_vec ? 4 : 1;
@@ -1011,8 +1011,8 @@ hipError_t prompts(const SsdConvArgs &a, hipStream_t s) {
         e = launch_status(s);
         if (e != hipSuccess) return e;
     }
-    if (a.P % 8 == 0) hipLaunchKernelGGL((ssdconv_sweep_kernel<T, NP, PY, false, true>), grid, dim3(kThreads), 0, s, a);
-    else hipLaunchKernelGGL((ssdconv_sweep_kernel<T, NP, PY, false, false>), grid, dim3(kThreads), 0, s, a);
+    if (a.P % 8 == 0) hipLaunchKernelGGL((ssdconv_sweep_kernel<T, NP, kParts, false, true>), grid, dim3(kThreads), 0, s, a);
+    else hipLaunchKernelGGL((ssdconv_sweep_kernel<T, NP, kParts, false, false>), grid, dim3(kThreads), 0, s, a);
     return launch_status(s);
 }
 
@@ -1031,8 +1031,8 @@ hipError_t token(const SsdConvArgs &a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_ssdconv(const SsdConvArgs &a, bool bf16, hipStream_t s) {
-    if (bf16) return a.N > 64 ? prompts<uint16_t, 128, 2>(a, s) : prompts<uint16_t, 64, 2>(a, s);
-    return a.N > 64 ? prompts<float, 128, 3>(a, s) : prompts<float, 64, 3>(a, s);
+    if (bf16) return a.N > 64 ? prompts<uint16_t, 128>(a, s) : prompts<uint16_t, 64>(a, s);
+    return a.N > 64 ? prompts<float, 128>(a, s) : prompts<float, 64>(a, s);
 }
 
 hipError_t launch_ssdconv_token(const SsdConvArgs &a, bool bf16, hipStream_t s) {

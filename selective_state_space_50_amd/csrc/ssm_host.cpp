@@ -1424,16 +1424,16 @@ int plan_ssdconv(const ssm_ssdconv_shape *s, bool token, SsdConvPlan *plan) {
     for (int64_t run = 2 * plan->heads_run; run <= kCUs / 8; ++run)
         if (across % run == 0 && ceil_div(plan->items * across / run, 8) * run <= kCUs / 8) plan->heads_run = run;
     if (plan->items > (int64_t(1) << 22) / across - 8 || plan->chunks >= (int64_t(1) << 22)) return too_many();
-    const int64_t np = s->dstate > 64 ? 128 : 64, py = s->dtype == SSM_DTYPE_BF16 ? 2 : 3;
+    const int64_t np = s->dstate > 64 ? 128 : 64, parts = 3;
     const int64_t cg = plan->chunks * s->ngroups;
     if (plan->chunks * s->nheads > (int64_t(1) << 36) || cg > (int64_t(1) << 30)) return too_many();
-    size_t at = static_cast<size_t>(cg * 64 * np * 2 * 3);
+    size_t at = static_cast<size_t>(cg * 64 * np * 2 * parts);
     auto take = [&](int64_t bytes) {
         const size_t off = align_up(at, kWsAlign);
         at = off + static_cast<size_t>(bytes);
         return off;
     };
-    plan->c_off = take(cg * 64 * np * 2 * py);
+    plan->c_off = take(cg * 64 * np * 2 * parts);
     plan->cb_off = take(cg * 64 * 64 * 4);
     plan->tab_off = take(plan->chunks * s->nheads * (3 * 64 * 4 + 32 * 4 + 64 * static_cast<int64_t>(dtype_size(s->dtype))));
     if (plan->split) {

@@ -37,16 +37,15 @@ def test_decays_behind_a_large_step(ssm, dt, reset, at):  # noqa: F811
     factors leaves out 3 * 2^-24 and rounds 3 times, C B and then with x (or the state): 12 and 3; the decay's up to
     three factors and the step in front 2 each: 8; a sum over 32 tokens or a chunk's chain 10: 51, taken as 60; and the exponent X
     from the pulse on, relative to itself a half step for each of the difference (or the sum) and the exponential's argument, twice
-    behind a half or a chunk: 4 X.  bf16: half a step of the output; the two parts of a factor 2^-17, twice in each of two products
-    and lo * lo 2^-18: 6 * 2^-17; lo of the sums is half a bf16 step off, at a sum of 16 * 30000 * 1.4427 < 2^20 that is
-    2^(20 - 24 - 1 - 8) twice, times log 2: less than 2^-12."""
+    behind a half or a chunk: 4 X.  bf16: half a step of the output; lo of the sums is half a bf16 step off, at a sum of 16 *
+    30000 * 1.4427 < 2^20 that is 2^(20 - 24 - 1 - 8) twice, times log 2: less than 2^-12."""
     c, dev = pulse(dt, reset, at)
     ref = mixer(c)["y"]
     y = call(ssm, c, dev)
     X = -np.cumsum(np.where(np.arange(130)[:, None] > at + 1, c["delta"] * c["A"], 0.0), 0)[:, :, None]
     tol = (60 + 4 * X) * E
     if dt == "bf16":
-        tol = tol + 2.0 ** -8 + 6 * 2.0 ** -17 + 2.0 ** -12
+        tol = tol + 2.0 ** -8 + 2.0 ** -12
     worst = (np.abs(to_host(y).reshape(ref.shape) - ref) / (tol * np.abs(ref) + 1e-30)).max()
     assert worst <= 1.0, f"{worst:.3g} of the tolerance"
 
@@ -63,3 +62,28 @@ def test_prompt_and_tokens_behind_a_large_step(ssm, reset):  # noqa: F811
     a, b = to_host(y).reshape(64, 3, -1), to_host(t).reshape(64, 3, -1)
     # (the token form multiplies a decay and rounds the state once a token: 3 * 2^-24 more for each of 60)
     assert (np.abs(a - b) <= (2 * (60 + 4 * X) + 180) * E * np.abs(b) + 1e-30).all()
+
+
+@pytest.mark.parametrize("at", [0, 20, 40, 70])
+@pytest.mark.parametrize("which", ["x", "B", "C", "state"])
+def test_bf16_outputs_round_the_whole_factor(ssm, which, at):  # noqa: F811
+    """1 + 2^-8 + 2^-20 lies just above the middle of two bf16 values: y is the upper one only if no bit of the fp32 factor it comes
+    from was dropped before a product.  Token 0's x and B reach the output of token `at` in its own half, from the first
+    half, and through the state; without decay, and by values of 64, which silu leaves as they are (1 + e^-64 is 1)."""
+    import torch
+    f = 1.0 + 2.0 ** -8 + 2.0 ** -20
+    H, P, N, L = 1, 16, 16, 80
+    C = H * P + 2 * N
+    dev = {"xbc": torch.zeros(L, C, dtype=torch.bfloat16), "delta": torch.zeros(L, H, dtype=torch.bfloat16), "A": torch.zeros(H),
+           "w": torch.ones(C, 1), "h": torch.zeros(1, H, P, N), "conv_state": torch.zeros(1, C, 0, dtype=torch.bfloat16),
+           "offsets": torch.tensor([0, L], dtype=torch.int32)}
+    dev["xbc"][at, P + N + 3] = 64.0            # C
+    if which == "state":
+        dev["h"][0, 0, 5, 3] = f
+    else:
+        dev["xbc"][0, 5] = dev["xbc"][0, P + 3] = 64.0
+        dev["delta"][0] = 1.0
+        dev["w"][{"x": 5, "B": P + 3, "C": P + N + 3}[which]] = f
+    y = ssm.ssdconv_fwd(**{n: t.cuda() for n, t in dev.items()}).float()
+    # every product and sum here is exact in 24 bits: one rounding, to bf16
+    assert float(y[at, 0, 5]) == (64.0 if which == "state" else 64.0 ** 3) * (1.0 + 2.0 ** -7)
