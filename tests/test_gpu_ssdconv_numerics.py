@@ -87,3 +87,30 @@ def test_bf16_outputs_round_the_whole_factor(ssm, which, at):  # noqa: F811
     y = ssm.ssdconv_fwd(**{n: t.cuda() for n, t in dev.items()}).float()
     # every product and sum here is exact in 24 bits: one rounding, to bf16
     assert float(y[at, 0, 5]) == (64.0 if which == "state" else 64.0 ** 3) * (1.0 + 2.0 ** -7)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("seq", [[200, 90], [1300, 90]])
+def test_nan_from_its_own_token_on(ssm, dt, seq):  # noqa: F811
+    """A NaN or infinity of x at the first and last token of chunks and halves, in every wave's share of a chunk, at a segment's border
+    and at the sequence's last token: its channel's outputs are NaN from that very token on, every other output keeps its bits."""
+    import torch
+    c, dev = make(seq, 4, 64, 64, 2, 4, dt, 14)
+    start = {n: dev[n].clone() for n in ("h", "conv_state")}
+    again = lambda **kw: dict(dev, **{n: t.clone() for n, t in start.items()}, **kw)  # noqa: E731
+    clean_dev = again()
+    clean = call(ssm, c, clean_dev)
+    for k, row in enumerate([0, 9, 18, 27, 31, 32, 45, 54, 63, 64, 70, 127, 128, seq[0] - 2, seq[0] - 1]):
+        head, p = k % 4, (5 + 19 * k) % 64
+        for value in (float("nan"), float("inf"), -float("inf")):
+            xbc = dev["xbc"].clone()
+            xbc[row, 64 * head + p] = value
+            bad = again(xbc=xbc)
+            y = call(ssm, c, bad)
+            hit = torch.zeros(y.shape, dtype=torch.bool, device="cuda")
+            hit[row:seq[0], head, p] = True
+            assert torch.equal(torch.isnan(y.float()), hit), (row, value)
+            assert torch.equal(y[~hit], clean[~hit]), (row, value)
+            gone = torch.zeros(bad["h"].shape, dtype=torch.bool, device="cuda")
+            gone[0, head, p] = True
+            assert torch.equal(torch.isnan(bad["h"]), gone) and torch.equal(bad["h"][~gone], clean_dev["h"][~gone]), (row, value)
