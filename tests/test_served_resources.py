@@ -43,3 +43,13 @@ def test_mixer_without_spills_in_the_chunk_loop(tmp_path):
         m = re.search(r"sweep_kernelI([tf])Li(\d+)ELi(\d)ELb([01])ELb([01])E", name)
         if m.group(1) == "t" or m.group(4) == "1":
             assert n == 0, (name, n)
+
+
+def test_no_sweep_of_the_mixer_spills(tmp_path):
+    """fp32 and bf16, whole pieces or single elements: all 24 bits of every factor in registers, and no scratch memory."""
+    sweeps = {n: r for n, r in _kernels("ssdconv.hip", tmp_path).items() if "ssdconv_sweep_kernel" in n}
+    assert len(sweeps) == 12
+    for name, r in sweeps.items():
+        assert r.get("vgpr_spill_count", 0) == 0, (name, r)
+    for name, n in _scratch_in_chunk_loops("ssdconv.hip", tmp_path / "ssdconv.s").items():
+        assert n == 0, (name, n)
