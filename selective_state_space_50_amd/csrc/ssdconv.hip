@@ -500,6 +500,12 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
         const int b = c & 1;
         float o[8];
         convolve<true>(win, 0, fw, fbias, 4, o);    // (a column that the filter lacks has weight 0)
+        // (the convolution of rows behind the end may be an infinity where no token's is: a weight of zero would not do)
+        const int left = q.len - (begin + c * kQ + 8 * wv);
+        if (left < 8) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = i < left ? o[i] : 0.0f;
+        }
         const f4 w0 = *reinterpret_cast<const f4 *>(&sm.tab[k3][kWr + 8 * wv]);
         const f4 w1 = *reinterpret_cast<const f4 *>(&sm.tab[k3][kWr + 8 * wv + 4]);
         float v[8];

@@ -4,7 +4,7 @@ import pytest
 
 from oracle.ssdconv_oracle import mixer
 from tests.gpu_util import to_host
-from tests.test_gpu_ssdconv import E, call, make, ssm, step  # noqa: F401  (ssm: the fixture)
+from tests.test_gpu_ssdconv import E, call, check, make, ssm, step  # noqa: F401  (ssm: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -114,3 +114,20 @@ def test_nan_from_its_own_token_on(ssm, dt, seq):  # noqa: F811
             gone = torch.zeros(bad["h"].shape, dtype=torch.bool, device="cuda")
             gone[0, head, p] = True
             assert torch.equal(torch.isnan(bad["h"]), gone) and torch.equal(bad["h"][~gone], clean_dev["h"][~gone]), (row, value)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("L", [4, 68, 1284])
+def test_rows_behind_the_end_are_not_convolved(ssm, dt, L):  # noqa: F811
+    """Large finite values of x whose convolutions are finite at every token, but not at the rows behind the last one that its chunk
+    has room for: 2e38, 2e38 with -2e38 in front of them, or the last row once more.  Outputs and states as the oracle's."""
+    import torch
+    c, dev = make([L], 2, 64, 64, 1, 4, dt, 32, gate=False, softplus=False, D=False, bias=False, joint=False, fresh=[1])
+    c["w"][64 + 7], dev["w"][64 + 7] = 1.0, 1.0
+    v = torch.tensor([-2e38, 0.0, 2e38, 2e38], dtype=dev["xbc"].dtype)
+    dev["xbc"][-4:, 64 + 7], c["xbc"][-4:, 64 + 7] = v.cuda(), v.double().numpy()
+    if L > 4:
+        dev["xbc"][-8:-4, 64 + 7], c["xbc"][-8:-4, 64 + 7] = 0.0, 0.0
+    ref = mixer(c)
+    n = (L + 63) // 64
+    check(c, dev, call(ssm, c, dev), ref, (90 + 50 * n) * E, (240 + 50 * n) * E)
