@@ -108,9 +108,12 @@ __device__ __forceinline__ void angles(const RotaryArgs &a, int64_t t0, int n, f
         const int64_t t = t0 + k;
         const int p = a.positions[a.period ? t % a.period : t];
         const double turns = static_cast<double>(p) * (a.freqs[j] * 0.15915494309189533577);   // 1 / (2 pi)
+        // (what rounding the part of a turn to 32 bits takes, up to 2^-26 of one, turns cosine and sine once more: 1 and d)
+        const double part = turns - rint(turns);
+        const float near = static_cast<float>(part), d = 6.2831853f * static_cast<float>(part - static_cast<double>(near));
         float sn, cn;
-        sincospif(2.0f * static_cast<float>(turns - rint(turns)), &sn, &cn);
-        cs[i] = make_float2(a.magnitude * cn, a.magnitude * sn);
+        sincospif(2.0f * near, &sn, &cn);
+        cs[i] = make_float2(a.magnitude * __builtin_fmaf(-d, sn, cn), a.magnitude * __builtin_fmaf(d, cn, sn));
     }
 }
 

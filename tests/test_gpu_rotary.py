@@ -343,3 +343,28 @@ def test_strides_past_32_bits(ssm):
     assert torch.equal(ssm.rotary_fwd(q, None, p, f), ssm.rotary_fwd(q.contiguous(), None, p, f))
     del big, q
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("norm", [False, True])
+def test_angles_next_to_a_quarter_turn(ssm, norm):
+    """A part of a turn is not cut to 32 bits: next to the zeros of cosine and sine, by less than half a 32-bit step of the part, they
+    are as good as their own digits.  Relative to such a value of size t <= 2 pi 2^-27: the 32-bit remainder and its product
+    with 2 pi 3 * 2^-24, the fused product with a sine or cosine of 2 ulp 4 * 2^-24, t^2 / 6 nothing; the norm 7 more: 14."""
+    import torch
+    near = np.repeat([0.25, 0.5, 0.75, 1.0], 4) + np.tile([2.0 ** -27, -2.0 ** -28, 2.0 ** -31, -2.0 ** -33], 4)
+    f = 2 * np.pi * near
+    q = torch.zeros(1, 1, 1, 32, device="cuda")
+    q[..., :16] = 1.0
+    pos, freqs = torch.ones(1, 1, dtype=torch.int32, device="cuda"), torch.from_numpy(f).cuda()
+    if norm:
+        y = ssm.qknorm_fwd(q, None, None, None, pos, freqs, eps=0.0)
+    else:
+        y = ssm.rotary_fwd(q, None, pos, freqs)
+    y = to_host(y).reshape(2, 16) / (np.sqrt(2.0) if norm else 1.0)
+    # (the frequency's own rounding to 64 bits is 2^-53 of it, 2^-18 of the smallest distance: what the 64-bit formula gives for it)
+    ref = np.stack([np.cos(f), np.sin(f)])
+    small = np.abs(ref) < 1e-6
+    assert small.sum() == 16
+    # (the kernel's product with 1 / (2 pi) rounds once more in 64 bits: 2^-53 of a turn, 2 pi 2^-53 rad, against 2 pi 2^-33)
+    assert (np.abs(y - ref)[small] <= (14 * E + 2.0 ** -18) * np.abs(ref)[small]).all()
+    assert (np.abs(y - ref)[~small] <= 14 * E).all()
