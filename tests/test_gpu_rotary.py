@@ -368,3 +368,17 @@ def test_angles_next_to_a_quarter_turn(ssm, norm):
     # (the kernel's product with 1 / (2 pi) rounds once more in 64 bits: 2^-53 of a turn, 2 pi 2^-53 rad, against 2 pi 2^-33)
     assert (np.abs(y - ref)[small] <= (14 * E + 2.0 ** -18) * np.abs(ref)[small]).all()
     assert (np.abs(y - ref)[~small] <= 14 * E).all()
+
+
+@pytest.mark.parametrize("where", ["tokens", "heads"])
+def test_sums_of_dw_are_joined_in_64_bits(ssm, where):
+    """2^25 + 1 - 2^25, each term of another workgroup (one token each) or another team (a head each), whichever two are added first."""
+    import itertools
+    import torch
+    n, d = 3, 16
+    for order in itertools.permutations([2.0 ** 25, 1.0, -2.0 ** 25]):
+        q = torch.ones(1, n if where == "tokens" else 1, 1 if where == "tokens" else n, d, device="cuda")
+        dq = torch.tensor(order, device="cuda").view(q.shape[:-1])[..., None].expand(q.shape).contiguous()
+        w = torch.ones(d, device="cuda")
+        g = ssm.qknorm_bwd(q, None, w, None, dq_out=dq, eps=0.0)     # (xh is x: its mean square is one)
+        assert torch.equal(g["dwq"], w), order
