@@ -9,10 +9,10 @@
 //     dw = sum over tokens and heads of g xh,   dx = rstd (e - xh mean(e xh)).
 //
 // Memory bound: q and k are read and written once (backward: two reads, one write): 336 MB of B4 L4096 32+8 heads of 128
-// bf16 in 50 us, the training pass of B2 L4096 32+32 heads, 671 MB, in 44 + 81 + 4.  A workgroup takes a few
-// tokens: its threads make their cosines and sines once, in LDS, for all heads of q and k (an angle is
-// position * frequency in 64 bits, cut to a part of a turn there, and only then 32 bits: at position 10^6 a
-// 32-bit product would be off by 0.06 rad).  Then teams of lanes take the tokens' heads row by row.  A lane
+// bf16 in 50 us, the training pass of B2 L4096 32+32 heads, 671 MB, in 43 + 81 + 4; fp32, B4 L2048 32+8 heads, 336 MB, in
+// 50, normed 57.  A workgroup takes a few tokens: its threads make their cosines and sines once, in LDS, for all heads of q
+// and k (an angle is position * frequency in 64 bits, cut to a part of a turn there, and only then 32 bits, with the rest kept: at
+// position 10^6 a 32-bit product would be off by 0.06 rad).  Then teams of lanes take the tokens' heads row by row.  A lane
 // holds a unit of 2 V columns: the V of one side of V pairs and the V of their other side (half layout), or 2 V side
 // by side (interleaved, and columns that do not turn), so that pairs never cross lanes and loads stay vectors.
 // 16-byte loads where the sizes and addresses allow them (V = 8 bf16, 4 fp32), else 8-byte ones (bf16), else

@@ -29,12 +29,13 @@
 // pair's weight): the sums are kept as hi + lo, lo in the input type (32 bits in all for bf16, 48 for fp32), and the
 // difference is as good as its own 24 bits.
 //
-// What bounds it (B4 L4096 H64 P64 N128, gated, bf16; 277 us, whose 422 MB would take 84 at a copy's rate): the sweep, 250.
-// Per chunk and head 10.6 MFLOP of products in parts (143 us at a large library product's rate) run beside about 500 vector
-// instructions a wave (convolution, decays, cutting into parts), 470 KB through LDS and 165 KB from the L2; the vector units are busy
-// 56% of the time, the matrix cores 30%, LDS about half, at a clock that the load itself holds near 2.0 GHz.  The prep's 20 us
-// are the 40 MB of operands and decays that it writes (all heads read them from the L2s; written past the caches: 2 us slower).
-// Workgroups of four waves and 32 channels, two to a CU: 304 us against 276.  B1 L32768 H24: 312 to 327 us in segments, 1714 whole.
+// What bounds it (B4 L4096 H64 P64 N128, gated, bf16; 347 us, whose 422 MB would take 84 at a copy's rate): the sweep, 94% of
+// the time.  Per chunk and head 14.9 MFLOP of products in parts (201 us at a large library product's rate) run beside about 580
+// vector instructions a wave (convolution, decays, cutting into parts), 600 KB through LDS and 200 KB from the L2; the vector units
+// are busy 52% of the time, the matrix cores 32%, LDS about half, at a clock that the load itself holds near 1.95 GHz.  The prep's
+// 22 us are the 45 MB of operands and decays that it writes (all heads read them from the L2s; written past the caches: 2 us
+// slower).  B1 L32768 H24: 384 us in segments, 2477 whole.  With y's factors in two parts, workgroups of four waves and 32 channels,
+// two to a CU, took 304 us against 276.
 #include "ssm_device.h"
 
 #include <type_traits>
@@ -253,8 +254,8 @@ __device__ __forceinline__ double half_scan(double v, int lane) {
     return v;
 }
 
-// NP: the states padded to 64 or 128.  Sixteen waves (eight: the same 20 us on B4 L4096 H64: about 5
-// of one thing waiting for the other, then 40 MB of operands and tables written).
+// NP: the states padded to 64 or 128.  Sixteen waves: 22 us on B4 L4096 H64, about 5 of one thing
+// waiting for the other, then 45 MB of operands and tables written (eight took as long as sixteen).
 template <class T, int NP>
 __global__ void __launch_bounds__(kPrepThreads) ssdconv_prep_kernel(SsdConvArgs a) {
     constexpr int kRow = NP + 4;
@@ -615,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
 
     // ---- a chunk's products.  Their LDS operands are requested a group ahead of the instructions that take them; the
     // groups' order is held by ahead() (left to itself the compiler reads two operands, waits, multiplies, and reads on:
-    // 306 us against 294 on B4 L4096 H64 64x128).
+    // 306 us against 294 on B4 L4096 H64 64x128, with two parts of y's factors).
     auto ahead = []() __attribute__((always_inline)) { __builtin_amdgcn_sched_barrier(0); };
     constexpr int kKK = NP / 32;
     f4 acc[2];             // outputs: the wave's tokens, 4 lg + j of both tiles
@@ -710,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, OWN ? 4 : 2) ssdconv_sweep_kernel(Ss
             load_c(more2);
             load_cb(more2);
             // x, z and tables of the chunks to come are waited for here, between the products, and not where they are used: 277
-            // us against 283 with waits as late as can be (B4 L4096 H64 64x128)
+            // us against 283 with waits as late as can be (B4 L4096 H64 64x128, two parts of y's factors)
             constexpr int kNewer = kKK * PARTS + 4;                                    // the loads of C and C B^T above
             __builtin_amdgcn_s_waitcnt(0x0f70 | (kNewer & 15) | (kNewer >> 4) << 14);   // vmcnt
             if constexpr (Lds::kStates == 1) __syncthreads();   // the old state's parts are read
@@ -917,7 +918,7 @@ __global__ void __launch_bounds__(256) ssdconv_token_conv_kernel(SsdConvArgs a) 
     }
 }
 
-// One token of the scan: a workgroup per sequence and head (gridDim.z: shares of its channels).  Rows of N states are read
+// One token of the scan: a workgroup per sequence and head (gridDim.y: shares of its channels).  Rows of N states are read
 // by teams of lanes, V states a lane and turn (16 bytes where N and the addresses allow it), four rows at a time, past the caches.
 // Memory bound: 8 bytes for every state (B128 H64 64x128: 106 us for 537 MB, 5.1 TB/s, the rate of a large copy).
 template <class T, int V>

@@ -1391,11 +1391,14 @@ int plan_ssdconv(const ssm_ssdconv_shape *s, bool token, SsdConvPlan *plan) {
     plan->blocks64 = ceil_div(s->headdim, 64);
     plan->chunks = s->tokens / 64 + s->sequences;
     // Whole sequences, or segments of them.  A sweep's workgroup walks its chunks one after another, one workgroup to a CU;
-    // runs of heads_run of them are dealt out to the 8 XCDs in turn.  In units of a chunk's time (3.4 to 4.2 us),
-    // measured on 8 to 64 heads over 8192 and 32768 tokens in segments of 8 to 128 chunks: a segment costs 1.5 for each
-    // of its chunks (x is read twice) and 3 for its start, the passes in between 6.  (B1 L32768 H24: segments of 52 chunks 354
-    // us, of 26 359, of 32 398, of 16 444, whole 1714; H8: of 20 158, of 16 221, of 52 298, whole 1632; B1 L8192 H64: of 40
-    // 256, of 64 355, whole 431.)
+    // runs of heads_run of them are dealt out to the 8 XCDs in turn.  In units of a chunk's time (4.6 to 4.9 us
+    // at 128 states, 3.5 to 3.8 at 64, bf16 or fp32): a segment costs 1.5 for each of its chunks (x is read twice) and 3 for its
+    // start, the passes in between 6.  Measured at every length, bf16 and fp32, on 11 shapes of 8 to 64 heads, 64 to 128 states and
+    // 2048 to 32768 tokens: the same lengths are good for both types and for both numbers of states, and the rule's choice is at
+    // most 12% above the best one.  (64x128 bf16: B1 L32768 H24 segments of 52 chunks, the rule's, 405 us, of 25 395, of 32 448, of 8
+    // 470, whole 2477; H8 of 17, the rule's, 161, of 16 155, of 52 355, whole 2350; B1 L8192 H64 of 11, the rule's, 269, of 32 243, of
+    // 64 431, whole 609.  64x128 fp32, the same three: 446, 440, 503, 496, 2577; 171, 168, 368, 2447; 293, 273, 457, 646.  64x64 bf16,
+    // B1 L32768 H24: 305, 292, 343, 346, 1874.)
     const int64_t across = s->nheads * plan->blocks64, all = ceil_div(s->tokens, 64);
     int64_t longest = s->max_seqlen > 0 && s->max_seqlen < s->tokens ? s->max_seqlen : s->tokens;
     longest = ceil_div(longest, 64);
@@ -1420,7 +1423,7 @@ int plan_ssdconv(const ssm_ssdconv_shape *s, bool token, SsdConvPlan *plan) {
     plan->split = plan->seg_len != kSsdConvWhole;
     plan->items = s->tokens / plan->seg_len + s->sequences;
     // (longer runs where every workgroup has a CU of its own at once, whichever segments are empty: 277.6 us against 280.3 on B4
-    // L4096 H64, 308 against 311.5 on B1 L32768 H24)
+    // L4096 H64, 308 against 311.5 on B1 L32768 H24, with y's factors in two parts)
     for (int64_t run = 2 * plan->heads_run; run <= kCUs / 8; ++run)
         if (across % run == 0 && ceil_div(plan->items * across / run, 8) * run <= kCUs / 8) plan->heads_run = run;
     if (plan->items > (int64_t(1) << 22) / across - 8 || plan->chunks >= (int64_t(1) << 22)) return too_many();
